@@ -442,6 +442,162 @@ ZERO_API int zero_step_noalloc(uint64_t psi, int n_ranks, int stage, int dtype, 
                       float loss_scale, int64_t steps_applied, zero_result_t* result,
                       void* stream);
 
+/*
+ * Orthogonalised momentum (the Muon optimiser) for the matrices of a
+ * partitioned model.  None of the ZeRO pages has a counterpart: the step
+ * keeps their structure (the ranks' gradients averaged into fp32 state, the
+ * new values rounded into every rank's replica) with another update rule.
+ * A step over matrices that lie back to back in flat buffers of `count`
+ * elements is three calls on one stream:
+ *   1. zero_muon_momentum   gradients of all ranks -> momentum, update
+ *   2. zero_orthogonalize   once for each shape among the matrices
+ *   3. zero_muon_apply      orthogonalised update -> master, all replicas
+ * They take no handle, allocate nothing, can be captured into a CUDA graph
+ * (after one call of each outside a capture, which loads the kernels) and
+ * keep what a step carries to the next in a device struct of the caller's.
+ * Errors: read zero_last_error(NULL).
+ */
+typedef struct {
+    float lr, momentum, weight_decay;
+    int32_t nesterov;      /* 1: update = g + momentum * m', 0: m' */
+} zero_muon_hyper_t;
+
+/* DEVICE memory of the caller's, 8-byte aligned; set by zero_muon_set_state. */
+typedef struct {
+    float loss_scale;      /* halved (floor 1.0) after a step whose gradients overflowed */
+    int32_t slot;          /* live slot (0/1) of the momentum */
+    int32_t pending;       /* zero_muon_momentum saw a non-finite averaged gradient */
+    int32_t overflow;      /* last finished step was skipped */
+    int32_t applied;       /* last finished step updated the state */
+    uint32_t ticket;       /* 0 between calls */
+    int64_t steps_applied, steps_skipped;
+    int64_t reserved[3];
+} zero_muon_state_t;
+
+/* Set the state: before the first step, or to resume.  Stream-ordered.  The
+ * loss scale must be finite and > 0.  Errors: EINVAL, ECUDA. */
+ZERO_API int zero_muon_set_state(zero_muon_state_t* state, float loss_scale, int64_t steps_applied, int32_t slot,
+                                 void* stream);
+
+/* Copy the state to the host struct *out.  Synchronises the stream. */
+ZERO_API int zero_muon_get_state(const zero_muon_state_t* state, void* stream, zero_muon_state_t* out);
+
+/*
+ * zero_muon_momentum -- average, unscale, momentum, update:
+ *   g = (sum over ranks, in rank order from +0, of f32(g_r)) / (N * loss_scale)
+ *   m' = momentum * m + g;   update = nesterov ? g + momentum * m' : m'
+ * each fp32 operation rounded once, the update rounded to bf16 for both
+ * gradient types (an unscaled gradient can lie below fp16's range).
+ *   dtype     zero_dtype_t of the gradients
+ *   grads     host array of n_ranks device pointers, count elements each
+ *   momentum  fp32, two slots of ceil(count/8)*8 floats: read from the live
+ *             slot, written to the other
+ *   update    count bf16 values
+ * A non-finite averaged gradient is noted in the state; the step is then
+ * skipped by zero_muon_apply, with the momentum as it was.
+ * Pointers 16-byte aligned.  count 0 is an empty call.  Errors: EINVAL, ECUDA.
+ */
+ZERO_API int zero_muon_momentum(int dtype, int n_ranks, uint64_t count, const void* const* grads, float* momentum,
+                                void* update, const zero_muon_hyper_t* hyper, zero_muon_state_t* state, void* stream);
+
+/*
+ * zero_muon_apply -- master = (1 - lr * weight_decay) * master - lr * ortho,
+ * every replica = the 16-bit rounding of it; then the step is finished in
+ * the state (the momentum's new slot becomes live).  After an overflow
+ * master and replicas keep their values, the loss scale halves and the
+ * momentum's live slot stays.
+ *   dtype   zero_dtype_t of the replicas
+ *   ortho   count bf16 values;  master: count floats
+ *   params  host array of n_ranks device pointers, count elements each
+ * Pointers 16-byte aligned.  count 0 only finishes the step.  Errors: EINVAL, ECUDA.
+ */
+ZERO_API int zero_muon_apply(int dtype, int n_ranks, uint64_t count, const void* ortho, float* master,
+                             void* const* params, const zero_muon_hyper_t* hyper, zero_muon_state_t* state,
+                             void* stream);
+
+/*
+ * zero_orthogonalize -- a batch of rows x cols matrices of 16-bit values by
+ * `steps` Newton-Schulz steps, rounded to bf16:
+ *   X = G / ||G||_F;   X <- (a I + b A + c A^2) X with A = X X^T;
+ *   dst = scale * X
+ * (A is formed over the shorter side; the result is the same.)  A zero
+ * matrix gives zeros; one that holds an infinity or a NaN gives NaN.
+ *   dtype   zero_dtype_t of src; dst is bf16 for both
+ *   batch   0..ZERO_MAX_MATRICES; sides 0..ZERO_MAX_SIDE
+ *   src, dst  host arrays of `batch` device pointers (2-byte aligned; rows
+ *           that start on 16 bytes are read and written faster), with
+ *           ld_src and ld_dst elements between rows.  dst[i] may be src[i]
+ *           when the leading dimensions agree; matrices may not overlap
+ *           otherwise.
+ *   coeffs  host array of 3 * steps floats, {a, b, c} of each step, or NULL
+ *           for {3.4445, -4.7750, 2.0315} throughout
+ *   steps   1..ZERO_MAX_NS_STEPS
+ *   workspace  device memory, 256-byte aligned, at least
+ *           zero_orthogonalize_workspace_bytes(batch, rows, cols) bytes; its
+ *           contents need not be kept between calls
+ * Intermediate matrices are held in fp16 with fixed scales, products
+ * accumulate in fp32; coefficients must keep the singular values of every
+ * X below 2 and those of a I + b A + c A^2 below 64 (two of them multiplied:
+ * below 512), or the fp16 values overflow and the result is not finite.
+ * Errors: EINVAL, ECUDA; see zero_matrix_status for a wait that gave up.
+ */
+#define ZERO_MAX_MATRICES 128
+#define ZERO_MAX_SIDE (1ull << 18)
+#define ZERO_MAX_NS_STEPS 32
+ZERO_API int zero_orthogonalize(int dtype, int batch, uint64_t rows, uint64_t cols, const void* const* src,
+                                uint64_t ld_src, void* const* dst, uint64_t ld_dst, int steps, const float* coeffs,
+                                float scale, void* workspace, uint64_t workspace_bytes, void* stream);
+
+/* Bytes of zero_orthogonalize's workspace (a host query); 0 for sizes that it refuses or that are empty. */
+ZERO_API uint64_t zero_orthogonalize_workspace_bytes(int batch, uint64_t rows, uint64_t cols);
+
+/*
+ * Microscaled 4-bit floats (the OCP MX format with e2m1 elements): an
+ * exchange in a quarter of 16 bits whose codes the tensor cores multiply as
+ * they are, next to the zero-point formats of zero_quantize_blocks, which
+ * must be dequantized first.
+ * A block is ZERO_MX_BLOCK consecutive values of a row.  Its scale is
+ * 2^(floor(log2(largest magnitude)) - 2), not below 2^-127, one byte with a
+ * bias of 127; a value's code is x / scale rounded to the nearest of +-{0,
+ * 0.5, 1, 1.5, 2, 3, 4, 6}, ties to the even code, larger ones to 6.  A block
+ * with an infinity or a NaN has the scale byte 255 and stands for NaN.
+ * Layout of a rows x cols matrix:
+ *   codes   rows of ceil(cols/32)*16 bytes, two codes a byte, the even one
+ *           low, zeros after cols
+ *   scales  tiles of 128 rows x 4 blocks, 512 bytes each, row-major over
+ *           the matrix; byte 16 (r mod 32) + 4 (r div 32) + b of a tile;
+ *           0 where the matrix has no row or block
+ * Both 16-byte aligned.  16-bit matrices are row-major with `ld` elements
+ * between rows, 2-byte aligned (faster when rows start on 16 bytes).
+ * Errors of these calls: EINVAL, ECUDA (zero_last_error(NULL)).
+ */
+#define ZERO_MX_BLOCK 32
+ZERO_API uint64_t zero_mx4_codes_bytes(uint64_t rows, uint64_t cols);
+ZERO_API uint64_t zero_mx4_scales_bytes(uint64_t rows, uint64_t cols);
+
+/* Quantize src16 (rows x cols) along its rows, or with transpose != 0 along
+ * its columns: then codes and scales are those of the cols x rows transpose,
+ * as the products of a backward pass take them. */
+ZERO_API int zero_mx4_quantize(int dtype, uint64_t rows, uint64_t cols, const void* src16, uint64_t ld, int transpose,
+                               void* codes, void* scales, void* stream);
+
+/* The values of a rows x cols matrix of codes, rounded to 16 bits. */
+ZERO_API int zero_mx4_dequantize(int dtype, uint64_t rows, uint64_t cols, const void* codes, const void* scales,
+                                 void* out16, uint64_t ld, void* stream);
+
+/* out16[m][n] = sum over k of A[m][k] * B[n][k], both quantized along k, fp32
+ * accumulation, rounded to 16 bits.  Y = X W^T of a linear layer whose weight
+ * is W [n][k]; its backward pass is the same call on transposed operands
+ * (dX: dY and W along their shared outer dimension; dW: dY and X along the
+ * tokens).  k = 0 gives zeros.  See zero_matrix_status. */
+ZERO_API int zero_mx4_matmul(int dtype, uint64_t m, uint64_t n, uint64_t k, const void* a_codes, const void* a_scales,
+                             const void* b_codes, const void* b_scales, void* out16, uint64_t ld, void* stream);
+
+/* Whether a bounded wait inside a kernel of zero_orthogonalize or
+ * zero_mx4_matmul has given up on this device since the last call: ZERO_OK or
+ * ZERO_ETIMEOUT (that kernel's output is incomplete).  Synchronises the stream. */
+ZERO_API int zero_matrix_status(void* stream);
+
 /* Last error message of this handle (or of the last failed init when h is
  * NULL).  The string is owned by the library and valid until the next call. */
 ZERO_API const char* zero_last_error(zero_handle_t h);

@@ -1,0 +1,68 @@
+"""Host-only checks of the matrix operators (no GPU): sizes, refusals before
+any CUDA call, and the references themselves against small cases by hand."""
+
+import numpy as np
+import pytest
+import torch
+
+from _matrix_ref import mx4_decode, mx4_encode, mx4_pack, mx4_tile, newton_schulz
+
+
+@pytest.fixture(scope="module")
+def Z():
+    from zero_partitioned_mixed_gb300.build import build_library
+    build_library()
+    import zero_partitioned_mixed_gb300 as Z
+    return Z
+
+
+def test_sizes(Z):
+    assert Z.zero_mx4_codes_bytes(3, 33) == 3 * 32
+    assert Z.zero_mx4_scales_bytes(129, 129) == 4 * 512
+    assert Z.zero_mx4_scales_bytes(0, 10) == 0 and Z.zero_mx4_codes_bytes(10, 0) == 0
+    assert Z.zero_mx4_codes_bytes((1 << 30) + 1, 1) == 0
+    # two copies of X, three square matrices, and the norms
+    need = Z.zero_orthogonalize_workspace_bytes(2, 100, 200)
+    assert need >= 2 * (2 * 100 * 200 * 2 + 3 * 100 * 104 * 2)
+    assert Z.zero_orthogonalize_workspace_bytes(0, 4, 4) == 0 and Z.zero_orthogonalize_workspace_bytes(1, 0, 4) == 0
+
+
+def test_refusals_come_before_any_cuda_call(Z):
+    for call in (lambda: Z.zero_orthogonalize(7, 4, 4, [], [], None, stream=0),
+                 lambda: Z.zero_orthogonalize(0, 4, 4, [16], [16], None, steps=0, stream=0),
+                 lambda: Z.zero_mx4_quantize(1, 4, 32, 16, None, 16, stream=0),
+                 lambda: Z.zero_mx4_matmul(9, 4, 4, 32, 16, 16, 16, 16, 16, stream=0),
+                 lambda: Z.zero_muon_momentum(0, 8, [16] * 65, 32, 32, Z.muon_hyper(), 16, stream=0),
+                 lambda: Z.zero_muon_apply(0, 8, 16, 16, [8], Z.muon_hyper(), 16, stream=0)):
+        with pytest.raises(Z.ZeroError) as e:
+            call()
+        assert e.value.code == 1
+
+
+def test_muon_state_has_the_header_s_size(Z):
+    import ctypes
+    assert ctypes.sizeof(Z._binding.MuonState) == 64 and ctypes.sizeof(Z._binding.MuonHyper) == 16
+
+
+def test_newton_schulz_reference_on_a_diagonal():
+    # on a diagonal matrix the iteration acts on each value by itself
+    d = torch.tensor([3.0, 1.0, 0.5, 0.0], dtype=torch.float64)
+    x = d / torch.linalg.vector_norm(d)
+    for _ in range(5):
+        x = 3.4445 * x - 4.7750 * x ** 3 + 2.0315 * x ** 5
+    assert torch.allclose(newton_schulz(torch.diag(d)), torch.diag(x), atol=1e-14)
+    tall = torch.randn(9, 4, dtype=torch.float64)
+    assert torch.allclose(newton_schulz(tall), newton_schulz(tall.t()).t(), atol=1e-12)
+
+
+def test_mx4_reference_by_hand():
+    x = np.zeros((1, 33))
+    x[0, :6] = [7.0, -5.0, 3.5, 2.5, 0.25, -0.75]      # largest exponent 2: scale 1
+    x[0, 32] = 0.375                                   # 1.5 * 2^-2: scale 2^-4, code of 6
+    codes, scales = mx4_encode(x)
+    assert scales.tolist() == [[127, 123]]
+    assert codes[0, :7].tolist() == [7, 14, 6, 4, 0, 10, 0] and codes[0, 32] == 7
+    assert mx4_decode(codes, scales, 33)[0, [0, 1, 2, 3, 4, 5, 32]].tolist() == [6.0, -4.0, 4.0, 2.0, 0.0, -1.0, 0.375]
+    assert mx4_pack(codes)[0, :3].tolist() == [7 | 14 << 4, 6 | 4 << 4, 0 | 10 << 4]
+    t = mx4_tile(np.arange(1, 131, dtype=np.uint8)[:, None])
+    assert t.size == 1024 and t[0] == 1 and t[16] == 2 and t[4] == 33 and t[512] == 129

@@ -18,4 +18,7 @@ from ._binding import (  # noqa: F401
     zero_step_noalloc, zero_noalloc_scratch_bytes, zero_quantize_blocks, zero_dequantize_blocks, zero_gather_bucket_q8,
     zero_reduce_scatter_bucket_q, ZERO_Q_BLOCK, zero_reduce_scatter_gather_bucket, zero_set_persistent,
     result_from_device, pointer_array,
+    muon_hyper, zero_muon_set_state, zero_muon_get_state, zero_muon_momentum, zero_muon_apply, zero_orthogonalize,
+    zero_orthogonalize_workspace_bytes, zero_mx4_codes_bytes, zero_mx4_scales_bytes, zero_mx4_quantize,
+    zero_mx4_dequantize, zero_mx4_matmul, zero_matrix_status, ZERO_MX_BLOCK, ZERO_MAX_MATRICES,
 )

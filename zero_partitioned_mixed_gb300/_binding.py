@@ -25,8 +25,13 @@ EXPORTS = (
     "zero_reduce_scatter_bucket_replicas", "zero_quantize_blocks", "zero_dequantize_blocks",
     "zero_gather_bucket_q8", "zero_reduce_scatter_bucket_q", "zero_debug_hold_staged",
     "zero_noalloc_scratch_bytes", "zero_set_persistent", "zero_reduce_scatter_gather_bucket",
+    "zero_muon_set_state", "zero_muon_get_state", "zero_muon_momentum", "zero_muon_apply",
+    "zero_orthogonalize", "zero_orthogonalize_workspace_bytes", "zero_mx4_codes_bytes", "zero_mx4_scales_bytes",
+    "zero_mx4_quantize", "zero_mx4_dequantize", "zero_mx4_matmul", "zero_matrix_status",
 )
 ZERO_Q_BLOCK = 256
+ZERO_MX_BLOCK = 32
+ZERO_MAX_MATRICES = 128
 
 
 class ZeroError(RuntimeError):
@@ -53,6 +58,16 @@ class Bytes(C.Structure):
         "psi", "psi_pad", "shard", "n_ranks", "stage", "model_state_bytes_per_rank",
         "comm_elems_paper", "comm_elems_ring", "hbm_read_bytes", "hbm_write_bytes",
         "hbm_read_total", "hbm_write_total")]
+
+
+class MuonHyper(C.Structure):
+    _fields_ = [("lr", C.c_float), ("momentum", C.c_float), ("weight_decay", C.c_float), ("nesterov", C.c_int32)]
+
+
+class MuonState(C.Structure):
+    _fields_ = [("loss_scale", C.c_float), ("slot", C.c_int32), ("pending", C.c_int32), ("overflow", C.c_int32),
+                ("applied", C.c_int32), ("ticket", C.c_uint32), ("steps_applied", C.c_int64),
+                ("steps_skipped", C.c_int64), ("reserved", C.c_int64 * 3)]
 
 
 _lib = None
@@ -105,8 +120,23 @@ def load_library():
     lib.zero_destroy.restype = None
     lib.zero_noalloc_scratch_bytes.argtypes = []
     lib.zero_noalloc_scratch_bytes.restype = U64
+    lib.zero_muon_set_state.argtypes = [P, C.c_float, C.c_int64, C.c_int32, P]
+    lib.zero_muon_get_state.argtypes = [P, P, C.POINTER(MuonState)]
+    lib.zero_muon_momentum.argtypes = [I32, I32, U64, C.POINTER(P), P, P, C.POINTER(MuonHyper), P, P]
+    lib.zero_muon_apply.argtypes = [I32, I32, U64, P, P, C.POINTER(P), C.POINTER(MuonHyper), P, P]
+    lib.zero_orthogonalize.argtypes = [I32, I32, U64, U64, C.POINTER(P), U64, C.POINTER(P), U64, I32,
+                                       C.POINTER(C.c_float), C.c_float, P, U64, P]
+    lib.zero_mx4_quantize.argtypes = [I32, U64, U64, P, U64, I32, P, P, P]
+    lib.zero_mx4_dequantize.argtypes = [I32, U64, U64, P, P, P, U64, P]
+    lib.zero_mx4_matmul.argtypes = [I32, U64, U64, U64, P, P, P, P, P, U64, P]
+    lib.zero_matrix_status.argtypes = [P]
+    lib.zero_orthogonalize_workspace_bytes.argtypes = [I32, U64, U64]
+    lib.zero_mx4_codes_bytes.argtypes = lib.zero_mx4_scales_bytes.argtypes = [U64, U64]
+    sizes = ("zero_orthogonalize_workspace_bytes", "zero_mx4_codes_bytes", "zero_mx4_scales_bytes")
+    for name in sizes:
+        getattr(lib, name).restype = U64
     for name in EXPORTS:
-        if name not in ("zero_last_error", "zero_destroy", "zero_noalloc_scratch_bytes"):
+        if name not in ("zero_last_error", "zero_destroy", "zero_noalloc_scratch_bytes") + sizes:
             getattr(lib, name).restype = C.c_int
     _lib = lib
     return lib
@@ -305,6 +335,94 @@ def result_from_device(t) -> dict:
     raw = bytes(t.view(-1)[:C.sizeof(Result)].cpu().numpy().tobytes())
     r = Result.from_buffer_copy(raw)
     return {f: getattr(r, f) for f, _ in Result._fields_ if f != "reserved"}
+
+
+# ------------------------------------------------- orthogonalised momentum
+def muon_hyper(lr=0.02, momentum=0.95, weight_decay=0.0, nesterov=True) -> MuonHyper:
+    return MuonHyper(lr, momentum, weight_decay, 1 if nesterov else 0)
+
+
+def zero_muon_set_state(state, loss_scale: float = 1.0, steps_applied: int = 0, slot: int = 0, stream=None):
+    """state: device tensor of at least 64 bytes, 8-byte aligned."""
+    _check(load_library().zero_muon_set_state(_ptr(state), loss_scale, steps_applied, slot, _stream(stream)), None)
+
+
+def zero_muon_get_state(state, stream=None) -> dict:
+    out = MuonState()
+    _check(load_library().zero_muon_get_state(_ptr(state), _stream(stream), C.byref(out)), None)
+    return {f: getattr(out, f) for f, _ in MuonState._fields_ if f not in ("reserved", "ticket")}
+
+
+def zero_muon_momentum(dtype: int, count: int, grads, momentum, update, hyp: MuonHyper, state, stream=None):
+    """grads: one row per rank (a list of tensors, or their pointer_array)."""
+    rc = load_library().zero_muon_momentum(dtype, len(grads), count, _ptr_array(grads), _ptr(momentum), _ptr(update),
+                                           C.byref(hyp), _ptr(state), _stream(stream))
+    _check(rc, None)
+
+
+def zero_muon_apply(dtype: int, count: int, ortho, master, params, hyp: MuonHyper, state, stream=None):
+    """params: one row per rank (a list of tensors, or their pointer_array)."""
+    rc = load_library().zero_muon_apply(dtype, len(params), count, _ptr(ortho), _ptr(master), _ptr_array(params),
+                                        C.byref(hyp), _ptr(state), _stream(stream))
+    _check(rc, None)
+
+
+def zero_orthogonalize_workspace_bytes(batch: int, rows: int, cols: int) -> int:
+    return int(load_library().zero_orthogonalize_workspace_bytes(batch, rows, cols))
+
+
+def zero_orthogonalize(dtype: int, rows: int, cols: int, src, dst, workspace, ld_src: Optional[int] = None,
+                       ld_dst: Optional[int] = None, steps: int = 5, coeffs=None, scale: float = 1.0, stream=None):
+    """src, dst: one matrix each per entry (lists of tensors, or their
+    pointer_array); workspace: a device tensor.  coeffs: one (a, b, c) for
+    every step, or `steps` of them; None takes the library's."""
+    if len(src) != len(dst):
+        raise ZeroError(1, "src and dst must have the same length")
+    arr = None
+    if coeffs is not None:
+        flat = [float(x) for c in coeffs for x in (c if hasattr(c, "__len__") else (c,))]
+        if len(flat) == 3:
+            flat = flat * max(steps, 0)
+        if len(flat) != 3 * steps:
+            raise ZeroError(1, "coeffs must be one (a, b, c), or one for each step")
+        arr = (C.c_float * max(1, len(flat)))(*flat)
+    rc = load_library().zero_orthogonalize(dtype, len(src), rows, cols, _ptr_array(src),
+                                           cols if ld_src is None else ld_src, _ptr_array(dst),
+                                           cols if ld_dst is None else ld_dst, steps, arr, scale, _ptr(workspace),
+                                           workspace.numel() * workspace.element_size() if workspace is not None else 0,
+                                           _stream(stream))
+    _check(rc, None)
+
+
+# ---------------------------------------------- microscaled 4-bit floats
+def zero_mx4_codes_bytes(rows: int, cols: int) -> int:
+    return int(load_library().zero_mx4_codes_bytes(rows, cols))
+
+
+def zero_mx4_scales_bytes(rows: int, cols: int) -> int:
+    return int(load_library().zero_mx4_scales_bytes(rows, cols))
+
+
+def zero_mx4_quantize(dtype: int, rows: int, cols: int, src16, codes, scales, ld: Optional[int] = None,
+                      transpose: bool = False, stream=None):
+    _check(load_library().zero_mx4_quantize(dtype, rows, cols, _ptr(src16), cols if ld is None else ld,
+                                            1 if transpose else 0, _ptr(codes), _ptr(scales), _stream(stream)), None)
+
+
+def zero_mx4_dequantize(dtype: int, rows: int, cols: int, codes, scales, out16, ld: Optional[int] = None, stream=None):
+    _check(load_library().zero_mx4_dequantize(dtype, rows, cols, _ptr(codes), _ptr(scales), _ptr(out16),
+                                              cols if ld is None else ld, _stream(stream)), None)
+
+
+def zero_mx4_matmul(dtype: int, m: int, n: int, k: int, a_codes, a_scales, b_codes, b_scales, out16,
+                    ld: Optional[int] = None, stream=None):
+    _check(load_library().zero_mx4_matmul(dtype, m, n, k, _ptr(a_codes), _ptr(a_scales), _ptr(b_codes), _ptr(b_scales),
+                                          _ptr(out16), n if ld is None else ld, _stream(stream)), None)
+
+
+def zero_matrix_status(stream=None) -> None:
+    """Raises ZeroError (ZERO_ETIMEOUT) when a matrix kernel's bounded wait gave up since the last call."""
+    _check(load_library().zero_matrix_status(_stream(stream)), None)
 
 
 def zero_last_error(h) -> str:

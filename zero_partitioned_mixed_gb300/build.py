@@ -25,9 +25,10 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB_NAME = "libzero_gb300.so"
 LIB_PATH = os.path.join(BUILD_DIR, LIB_NAME)
 
-SOURCES = ["zero_kernels.cu", "zero_quant.cu", "zero_tma.cu", "zero_api.cpp", "zero_noalloc.cu"]
+SOURCES = ["zero_kernels.cu", "zero_quant.cu", "zero_tma.cu", "zero_api.cpp", "zero_noalloc.cu",
+           "zero_muon.cu", "zero_ortho.cu", "zero_mx4.cu"]
 HEADERS = [os.path.join(INCLUDE, "zero_gb300.h"), os.path.join(CSRC, "zero_internal.h"),
-           os.path.join(CSRC, "zero_device.cuh")]
+           os.path.join(CSRC, "zero_device.cuh"), os.path.join(CSRC, "zero_host.h"), os.path.join(CSRC, "zero_tc.cuh")]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 
@@ -48,7 +49,7 @@ def nvcc_command(out: str = LIB_PATH, extra=None) -> list:
         nvcc, ARCH, "-O3", "-lineinfo", "-std=c++17",
         "-fmad=false", "-prec-div=true", "-prec-sqrt=true", "-ftz=false",
         "-Xcompiler", "-fPIC,-O2,-ffp-contract=off,-fvisibility=hidden",
-        "-Xptxas", "-v",
+        "-Xptxas", "-v", "--threads", "0",   # one compilation per core
         "-shared", "-cudart", "shared",
         "-Xlinker", "-rpath," + _cuda_lib_dir(nvcc),
         "-I" + INCLUDE, "-I" + CSRC,

@@ -9,6 +9,7 @@
 #include <cuda_fp16.h>
 
 #include <mutex>
+#include <utility>
 
 #include "zero_internal.h"
 
@@ -577,6 +578,34 @@ cudaError_t resident_ctas(KernelT kernel, int dev, int per_sm_cap, uint64_t* out
     if (per_sm_cap > 0 && per_sm > per_sm_cap) per_sm = per_sm_cap;
     *out = static_cast<uint64_t>(sms) * static_cast<uint64_t>(per_sm);
     return cudaSuccess;
+}
+
+// Launch with programmatic stream serialisation (see pdl_enter) on a given
+// grid, with `smem` bytes of dynamic shared memory and, when cluster > 1,
+// clusters of that many CTAs.  The kernel must call pdl_enter(), or
+// griddepcontrol.wait in every thread that touches global memory, before its
+// first access to memory that another kernel of the stream writes or reads.
+template <typename... P, typename... A>
+cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, unsigned cluster, cudaStream_t s,
+                       A&&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 1;
+    if (cluster > 1) {
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = cluster;
+        attr[1].val.clusterDim.y = 1;
+        attr[1].val.clusterDim.z = 1;
+        cfg.numAttrs = 2;
+    }
+    cfg.attrs = attr;
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
 }
 
 // Launch on a persistent grid: as many CTAs as fit on the SMs at once (from

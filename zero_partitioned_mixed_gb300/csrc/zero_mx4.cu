@@ -1,0 +1,540 @@
+// Microscaled 4-bit floats (the OCP MX format with e2m1 elements): quantising
+// a matrix along its rows or its columns, reading it back, and the product of
+// two such matrices on the block-scaled tensor cores.
+//
+// A block is 32 consecutive values of a row.  With E the exponent of the
+// block's largest magnitude, its scale is 2^(E - 2) (2 is e2m1's largest
+// exponent), stored as a byte with a bias of 127 and never below 2^-127; a
+// value's code is x / scale rounded to the nearest of 0, 0.5, 1, 1.5, 2, 3,
+// 4, 6 (ties to the even code), larger ones becoming 6.  The division is a
+// multiplication by a power of two and exact.  A block that holds an
+// infinity or a NaN gets the scale 255, which stands for NaN, and codes of 0.
+//
+// Layout.  Codes: row by row, two a byte, the even one low, every row filled
+// with zeros to whole blocks.  Scales: tiles of 128 rows x 4 blocks, 512
+// bytes each, row-major over the matrix; in a tile, byte 16 (r mod 32) +
+// 4 (r / 32) + b.  That is what the tensor cores take: a tile is copied into
+// tensor memory as it stands.  The tiles' unused bytes are 0.
+
+#include <cstdint>
+#include <string>
+
+#include <nvtx3/nvToolsExt.h>
+
+#include "zero_gb300.h"
+#include "zero_tc.cuh"
+
+namespace zg {
+namespace {
+
+constexpr int kMxBlock = ZERO_MX_BLOCK;
+
+struct MxArgs {
+    const void* src;
+    void* dst;
+    uint8_t* codes;
+    uint8_t* scales;
+    uint64_t rows, cols, ld;   // of the 16-bit matrix
+    uint64_t pitch;            // bytes of a row of codes
+    uint64_t tiles_k;          // scale tiles along a row of codes
+    int vec;                   // rows of the 16-bit matrix start on 16 bytes
+};
+
+__device__ __forceinline__ uint64_t scale_at(uint64_t row, uint64_t block, uint64_t tiles_k) {
+    return ((row >> 7) * tiles_k + (block >> 2)) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4 + (block & 3);
+}
+
+// The scale byte of a block from the bits of its largest magnitude.
+__device__ __forceinline__ uint32_t scale_byte(float top) {
+    const uint32_t e = __float_as_uint(top) >> 23;   // 255: infinity or NaN
+    return e == 255u ? 255u : e > 2u ? e - 2u : 0u;
+}
+// 1 / scale; 0 for a NaN block, whose codes are 0.
+__device__ __forceinline__ float scale_inverse(uint32_t byte) {
+    return byte == 255u ? 0.0f : __uint_as_float((254u - byte) << 23);
+}
+// 8 values as codes, the first in the lowest 4 bits.  A NaN block's values
+// must be given as zeros.
+__device__ __forceinline__ uint32_t codes8(const float (&x)[8]) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(r)
+        : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+    return r;
+}
+// Largest magnitude, by its bits: NaN above infinity above every number.
+__device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+
+// Along the rows.  A warp takes 256 columns of a row, a lane 8 of them, so
+// four lanes share a block; rows and columns that only fill the last scale
+// tiles are walked too, for their zeros.
+template <int DT>
+__global__ void __launch_bounds__(kThreads) k_mx4_rows(const __grid_constant__ MxArgs a) {
+    pdl_enter();
+    const int lane = threadIdx.x & 31;
+    const uint64_t segments = (a.tiles_k * 128 + 255) / 256;
+    const uint64_t units = (a.rows + 127) / 128 * 128 * segments;
+    for (uint64_t u = static_cast<uint64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); u < units;
+         u += static_cast<uint64_t>(gridDim.x) * (kThreads / 32)) {
+        const uint64_t row = u / segments, c = (u - row * segments) * 256 + 8 * lane;
+        float v[8] = {};
+        if (row < a.rows) {
+            const unsigned short* src = static_cast<const unsigned short*>(a.src) + row * a.ld;
+            if (a.vec && c + 8 <= a.cols) {
+                const uint4 x = __ldcs(reinterpret_cast<const uint4*>(src + c));
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = widen<DT>((w[e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (c + e < a.cols) v[e] = widen<DT>(__ldcs(src + c + e));
+            }
+        }
+        uint32_t top = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = max(top, magnitude(v[e]));
+        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+        const uint32_t byte = scale_byte(__uint_as_float(top));
+        const float inv = scale_inverse(byte);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = byte == 255u ? 0.0f : __fmul_rn(v[e], inv);
+        const uint32_t q = codes8(v);
+        if (row < a.rows && (c >> 1) < a.pitch) *reinterpret_cast<uint32_t*>(a.codes + row * a.pitch + (c >> 1)) = q;
+        // the four blocks of a scale tile's row in one word
+        uint32_t word = byte;
+        word |= __shfl_down_sync(0xFFFFFFFFu, byte, 4) << 8;
+        word |= __shfl_down_sync(0xFFFFFFFFu, byte, 8) << 16;
+        word |= __shfl_down_sync(0xFFFFFFFFu, byte, 12) << 24;
+        if ((lane & 15) == 0 && (c >> 7) < a.tiles_k)
+            *reinterpret_cast<uint32_t*>(a.scales + scale_at(row, c >> 5, a.tiles_k)) = word;
+    }
+}
+
+// Along the columns: the codes are those of the transpose.  A thread takes
+// 128 values of one column, so it holds whole blocks and writes 64 bytes of
+// one row of codes; a warp's loads are 32 neighbouring columns.
+template <int DT>
+__global__ void __launch_bounds__(kThreads) k_mx4_columns(const __grid_constant__ MxArgs a) {
+    pdl_enter();
+    const uint64_t col = static_cast<uint64_t>(blockIdx.x) * kThreads + threadIdx.x;
+    const uint64_t tile = blockIdx.y, row0 = tile * 128;
+    if (col >= (a.cols + 127) / 128 * 128) return;
+    const unsigned short* src = static_cast<const unsigned short*>(a.src) + col;
+    uint32_t word = 0;
+#pragma unroll 1
+    for (int b = 0; b < 4; ++b) {
+        float v[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+            const uint64_t r = row0 + 32 * b + e;
+            v[e] = r < a.rows && col < a.cols ? widen<DT>(__ldcs(src + r * a.ld)) : 0.0f;
+        }
+        uint32_t top = 0;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) top = max(top, magnitude(v[e]));
+        const uint32_t byte = scale_byte(__uint_as_float(top));
+        const float inv = scale_inverse(byte);
+        uint32_t q[4];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = byte == 255u ? 0.0f : __fmul_rn(v[8 * g + e], inv);
+            q[g] = codes8(x);
+        }
+        const uint64_t at = (row0 + 32 * b) / 2;
+        if (col < a.cols && at < a.pitch)
+            *reinterpret_cast<uint4*>(a.codes + col * a.pitch + at) = make_uint4(q[0], q[1], q[2], q[3]);
+        word |= byte << (8 * b);
+    }
+    *reinterpret_cast<uint32_t*>(a.scales + scale_at(col, 4 * tile, a.tiles_k)) = word;
+}
+
+// Codes and scales back to 16 bits, 8 values a thread.
+template <int DT>
+__global__ void __launch_bounds__(kThreads) k_mx4_values(const __grid_constant__ MxArgs a) {
+    pdl_enter();
+    const uint64_t groups = (a.cols + 7) / 8, total = a.rows * groups;
+    for (uint64_t i = thread_id(); i < total; i += grid_threads()) {
+        const uint64_t row = i / groups, c = (i - row * groups) * 8;
+        const uint32_t q = __ldcs(reinterpret_cast<const uint32_t*>(a.codes + row * a.pitch + (c >> 1)));
+        const uint32_t byte = a.scales[scale_at(row, c >> 5, a.tiles_k)];
+        // 2^(byte - 127): the smallest is a subnormal number
+        const float scale = byte == 255u ? NAN : __uint_as_float(byte == 0u ? 0x00400000u : byte << 23);
+        uint32_t out[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            uint32_t h;
+            asm("{\n\t.reg .b8 b, x, y, z;\n\tmov.b32 {b, x, y, z}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}"
+                : "=r"(h)
+                : "r"(q >> (8 * e)));
+            out[2 * e] = narrow<DT>(__fmul_rn(widen<kFp16>(h & 0xFFFFu), scale));
+            out[2 * e + 1] = narrow<DT>(__fmul_rn(widen<kFp16>(h >> 16), scale));
+        }
+        unsigned short* dst = static_cast<unsigned short*>(a.dst) + row * a.ld + c;
+        if (a.vec && c + 8 <= a.cols) {
+            __stcs(reinterpret_cast<uint4*>(dst), make_uint4(out[0] | out[1] << 16, out[2] | out[3] << 16,
+                                                             out[4] | out[5] << 16, out[6] | out[7] << 16));
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (c + e < a.cols) __stcs(dst + e, static_cast<unsigned short>(out[e]));
+        }
+    }
+}
+
+// ----------------------------------------------------------------- product
+// out[m][n] = sum over k of A[m][k] B[n][k], fp32 accumulation.
+struct MxProductArgs {
+    uint32_t m, n, k;
+    uint32_t tiles_n, total;
+    uint32_t tiles_k;        // scale tiles along k
+    const uint8_t* a_scales;
+    const uint8_t* b_scales;
+    void* out;
+    uint64_t ld;
+    int vec;
+};
+
+constexpr int kMxM = 128, kMxN = 128;
+constexpr int kMxK = 256;                          // values a stage: 128 bytes a row
+constexpr uint32_t kMxOperand = kMxM * kMxK / 2;   // bytes of one operand's tile
+constexpr uint32_t kMxScales = 1024;               // two scale tiles an operand
+constexpr uint32_t kMxStage = 2 * kMxOperand + 2 * kMxScales;
+constexpr int kMxStages = 6;
+constexpr size_t kMxSmem = 1024 + static_cast<size_t>(kMxStages) * kMxStage;
+constexpr int kMxThreads = 192;
+
+// A scale tile (32 lines of 16 bytes in shared memory) into 4 columns of
+// tensor memory, repeated in each quarter of the lanes.
+__device__ __forceinline__ void tc_copy_scales(uint32_t tmem, uint32_t smem) {
+    uint64_t d = static_cast<uint64_t>((smem & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(128u >> 4) << 32;   // 8 lines of 16 bytes
+    d |= static_cast<uint64_t>(1) << 46;
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(d) : "memory");
+}
+__device__ __forceinline__ void mma_mx4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
+                                        bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(static_cast<uint32_t>(accumulate))
+        : "memory");
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kMxThreads)
+k_mx4_product(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+              const __grid_constant__ MxProductArgs p) {
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ __align__(8) uint64_t bars[2 * kMxStages + 4];
+    __shared__ __align__(8) uint64_t s_last;
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_quit;
+    volatile int* quit = &s_quit;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const uint32_t full = smem_u32(bars), empty = full + 8 * kMxStages, done = empty + 8 * kMxStages, freed = done + 16;
+    if (threadIdx.x == 0) {
+        s_quit = 0;
+        for (int i = 0; i < kMxStages; ++i) {
+            bar_init(full + 8 * i, 1);
+            bar_init(empty + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            bar_init(done + 8 * i, 1);
+            bar_init(freed + 8 * i, 128);
+        }
+        bar_init(smem_u32(&s_last), 1);
+        bar_init_fence();
+        prefetch_map(&map_a);
+        prefetch_map(&map_b);
+    }
+    if (warp == 1) tmem_alloc(smem_u32(&s_tmem), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    pdl_enter();
+    const uint32_t nk = (p.k + kMxK - 1) / kMxK;
+
+    if (warp == 0 && lane == 0) {
+        uint32_t it = 0;
+        bool ok = true;
+        for (uint32_t t = blockIdx.x; t < p.total && ok; t += gridDim.x) {
+            const uint32_t tm = t / p.tiles_n, tn = t - tm * p.tiles_n;
+            for (uint32_t kb = 0; kb < nk; ++kb, ++it) {
+                const uint32_t s = it % kMxStages;
+                if (it >= kMxStages && !bar_wait(empty + 8 * s, (it / kMxStages - 1) & 1, quit)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t bar = full + 8 * s, st = ring + s * kMxStage;
+                const uint32_t scales = 2 * kb + 2 <= p.tiles_k ? 1024u : 512u;
+                bar_expect(bar, 2 * kMxOperand + 2 * scales);
+                copy_box(st, &map_a, static_cast<int>(kb * 128), static_cast<int>(tm * kMxM), 0, bar);
+                copy_box(st + kMxOperand, &map_b, static_cast<int>(kb * 128), static_cast<int>(tn * kMxN), 0, bar);
+                copy_bytes(st + 2 * kMxOperand, p.a_scales + (static_cast<uint64_t>(tm) * p.tiles_k + 2 * kb) * 512,
+                           scales, bar);
+                copy_bytes(st + 2 * kMxOperand + kMxScales,
+                           p.b_scales + (static_cast<uint64_t>(tn) * p.tiles_k + 2 * kb) * 512, scales, bar);
+            }
+        }
+        if (!ok)
+            for (uint32_t i = it > kMxStages ? it - kMxStages : 0; i < it; ++i)
+                bar_drain(full + 8 * (i % kMxStages), (i / kMxStages) & 1);
+    } else if (warp == 1 && lane == 0) {
+        // e2m1 operands, power-of-two scales, 128 x 128
+        constexpr uint32_t idesc = (1u << 7) | (1u << 10) | (static_cast<uint32_t>(kMxN >> 3) << 17) | (1u << 23) |
+                                   (static_cast<uint32_t>(kMxM >> 4) << 24);
+        uint32_t it = 0, n = 0;
+        bool ok = true;
+        for (uint32_t t = blockIdx.x; t < p.total && ok; t += gridDim.x, ++n) {
+            const uint32_t acc = n & 1, d = tmem + acc * kMxN;
+            if (n >= 2 && !bar_wait(freed + 8 * acc, (n / 2 - 1) & 1, quit)) break;
+            tc_fence_after();
+            for (uint32_t kb = 0; kb < nk; ++kb, ++it) {
+                const uint32_t s = it % kMxStages;
+                if (!bar_wait(full + 8 * s, (it / kMxStages) & 1, quit)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t st = ring + s * kMxStage, ss = st + 2 * kMxOperand;
+                const uint64_t da = operand_desc(st, 0), db = operand_desc(st + kMxOperand, 0);
+                const uint32_t sf = tmem + 2 * kMxN + (it & 1) * 16;
+#pragma unroll
+                for (uint32_t h = 0; h < 2; ++h) {   // 128 values: one scale tile of each operand, two products
+                    if (2 * kb + h >= p.tiles_k) break;
+                    tc_copy_scales(sf + 4 * h, ss + 512 * h);
+                    tc_copy_scales(sf + 8 + 4 * h, ss + kMxScales + 512 * h);
+#pragma unroll
+                    for (uint32_t j = 0; j < 2; ++j)
+                        mma_mx4(d, da + (2 * h + j) * 2, db + (2 * h + j) * 2, idesc | (2 * j << 4) | (2 * j << 29),
+                                sf + 4 * h, sf + 8 + 4 * h, kb > 0 || h > 0 || j > 0);
+                }
+                tc_commit(empty + 8 * s);
+            }
+            if (ok) tc_commit(done + 8 * acc);
+        }
+        if (*quit) {
+            tc_commit(smem_u32(&s_last));
+            bar_drain(smem_u32(&s_last), 0);
+        }
+    } else if (warp >= 2) {
+        const uint32_t quarter = warp & 3;
+        uint32_t n = 0;
+        for (uint32_t t = blockIdx.x; t < p.total; t += gridDim.x, ++n) {
+            const uint32_t acc = n & 1, tm = t / p.tiles_n, tn = t - tm * p.tiles_n;
+            const bool ok = bar_wait(done + 8 * acc, (n / 2) & 1, quit);
+            if (__any_sync(0xFFFFFFFFu, !ok)) break;
+            tc_fence_after();
+            const uint32_t row = tm * kMxM + quarter * 32 + lane;
+            unsigned short* out = static_cast<unsigned short*>(p.out) + static_cast<uint64_t>(row) * p.ld;
+#pragma unroll 1
+            for (int cc = 0; cc < kMxN / 32; ++cc) {
+                const uint32_t col = tn * kMxN + cc * 32;
+                if (col >= p.n) break;
+                float v[32];
+                tmem_load32(tmem + acc * kMxN + cc * 32 + (quarter << 21), v);
+                if (row < p.m) {
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        uint32_t q[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            q[e] = DT == kFp16 ? pack_half2(v[8 * g + 2 * e], v[8 * g + 2 * e + 1])
+                                               : pack_bf2(v[8 * g + 2 * e], v[8 * g + 2 * e + 1]);
+                        const uint32_t c = col + 8 * g;
+                        if (p.vec && c + 8 <= p.n) {
+                            *reinterpret_cast<uint4*>(out + c) = make_uint4(q[0], q[1], q[2], q[3]);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                if (c + e < p.n) out[c + e] = static_cast<unsigned short>(q[e >> 1] >> (16 * (e & 1)));
+                        }
+                    }
+                }
+            }
+            tc_fence_before();
+            bar_arrive(freed + 8 * acc);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_free(tmem, 512);
+    }
+}
+
+// -------------------------------------------------------------------- host
+constexpr uint64_t kMaxSide = 1ull << 30;
+
+uint64_t mx_pitch(uint64_t cols) { return up(cols, kMxBlock) / 2; }
+
+// Checks shared by the calls on one matrix; (rows, cols) are those of the codes.
+int mx_check(int dtype, uint64_t rows, uint64_t cols, const void* codes, const void* scales) {
+    if (dtype != ZERO_FP16 && dtype != ZERO_BF16) return refuse(ZERO_EINVAL, "dtype must be fp16 or bf16");
+    if (rows > kMaxSide || cols > kMaxSide) return refuse(ZERO_EINVAL, "a side is longer than 2^30");
+    if (rows == 0 || cols == 0) return ZERO_OK;
+    if (!codes || !aligned(codes, 16)) return refuse(ZERO_EINVAL, "codes is NULL or not 16-byte aligned");
+    if (!scales || !aligned(scales, 16)) return refuse(ZERO_EINVAL, "scales is NULL or not 16-byte aligned");
+    return ZERO_OK;
+}
+
+unsigned grid_of(uint64_t blocks, int sms, int per_sm) {
+    const uint64_t cap = static_cast<uint64_t>(sms) * per_sm;
+    return static_cast<unsigned>(blocks < 1 ? 1 : blocks < cap ? blocks : cap);
+}
+
+}  // namespace
+
+cudaError_t mx4_gave_up(cudaStream_t s, int32_t* out) { return read_gave_up(s, out); }
+cudaError_t ortho_gave_up(cudaStream_t s, int32_t* out);   // zero_ortho.cu
+
+}  // namespace zg
+
+using namespace zg;
+
+extern "C" {
+
+uint64_t zero_mx4_codes_bytes(uint64_t rows, uint64_t cols) {
+    return rows > kMaxSide || cols > kMaxSide ? 0 : rows * mx_pitch(cols);
+}
+
+uint64_t zero_mx4_scales_bytes(uint64_t rows, uint64_t cols) {
+    return rows > kMaxSide || cols > kMaxSide ? 0 : up(rows, 128) / 128 * (up(cols, 128) / 128) * 512;
+}
+
+int zero_mx4_quantize(int dtype, uint64_t rows, uint64_t cols, const void* src16, uint64_t ld, int transpose,
+                      void* codes, void* scales, void* stream) {
+    nvtxRangePushA("zero_mx4_quantize");
+    struct Pop { ~Pop() { nvtxRangePop(); } } pop;
+    if (const int rc = mx_check(dtype, rows, cols, codes, scales)) return rc;
+    if (rows == 0 || cols == 0) return ZERO_OK;
+    if (!src16 || !aligned(src16, 2)) return refuse(ZERO_EINVAL, "src16 is NULL or not 2-byte aligned");
+    if (ld < cols || ld > (1ull << 40)) return refuse(ZERO_EINVAL, "ld must be at least cols (and at most 2^40)");
+    MxArgs a = {};
+    a.src = src16;
+    a.codes = static_cast<uint8_t*>(codes);
+    a.scales = static_cast<uint8_t*>(scales);
+    a.rows = rows;
+    a.cols = cols;
+    a.ld = ld;
+    a.vec = aligned(src16, 16) && ld % 8 == 0;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (transpose) {
+        a.pitch = mx_pitch(rows);
+        a.tiles_k = up(rows, 128) / 128;
+        if (a.tiles_k > 65535) return refuse(ZERO_EINVAL, "a transposed matrix has at most 65535 * 128 rows");
+        const dim3 grid(static_cast<unsigned>(up(cols, kThreads) / kThreads), static_cast<unsigned>(a.tiles_k));
+        e = dtype == ZERO_FP16 ? launch_pdl(k_mx4_columns<kFp16>, grid, kThreads, 0, 1, s, a)
+                               : launch_pdl(k_mx4_columns<kBf16>, grid, kThreads, 0, 1, s, a);
+    } else {
+        a.pitch = mx_pitch(cols);
+        a.tiles_k = up(cols, 128) / 128;
+        int sms = 0;
+        if ((e = sm_count(&sms)) != cudaSuccess) return cuda_refuse(e, "zero_mx4_quantize");
+        const uint64_t units = up(rows, 128) * (up(cols, 256) / 256);
+        const dim3 grid(grid_of((units + 7) / 8, sms, 32));
+        e = dtype == ZERO_FP16 ? launch_pdl(k_mx4_rows<kFp16>, grid, kThreads, 0, 1, s, a)
+                               : launch_pdl(k_mx4_rows<kBf16>, grid, kThreads, 0, 1, s, a);
+    }
+    return e == cudaSuccess ? ZERO_OK : cuda_refuse(e, "zero_mx4_quantize");
+}
+
+int zero_mx4_dequantize(int dtype, uint64_t rows, uint64_t cols, const void* codes, const void* scales, void* out16,
+                        uint64_t ld, void* stream) {
+    nvtxRangePushA("zero_mx4_dequantize");
+    struct Pop { ~Pop() { nvtxRangePop(); } } pop;
+    if (const int rc = mx_check(dtype, rows, cols, codes, scales)) return rc;
+    if (rows == 0 || cols == 0) return ZERO_OK;
+    if (!out16 || !aligned(out16, 2)) return refuse(ZERO_EINVAL, "out16 is NULL or not 2-byte aligned");
+    if (ld < cols || ld > (1ull << 40)) return refuse(ZERO_EINVAL, "ld must be at least cols (and at most 2^40)");
+    MxArgs a = {};
+    a.dst = out16;
+    a.codes = static_cast<uint8_t*>(const_cast<void*>(codes));
+    a.scales = static_cast<uint8_t*>(const_cast<void*>(scales));
+    a.rows = rows;
+    a.cols = cols;
+    a.ld = ld;
+    a.pitch = mx_pitch(cols);
+    a.tiles_k = up(cols, 128) / 128;
+    a.vec = aligned(out16, 16) && ld % 8 == 0;
+    int sms = 0;
+    cudaError_t e = sm_count(&sms);
+    if (e != cudaSuccess) return cuda_refuse(e, "zero_mx4_dequantize");
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const dim3 grid(grid_of((rows * ((cols + 7) / 8) + kThreads - 1) / kThreads, sms, 32));
+    e = dtype == ZERO_FP16 ? launch_pdl(k_mx4_values<kFp16>, grid, kThreads, 0, 1, s, a)
+                           : launch_pdl(k_mx4_values<kBf16>, grid, kThreads, 0, 1, s, a);
+    return e == cudaSuccess ? ZERO_OK : cuda_refuse(e, "zero_mx4_dequantize");
+}
+
+int zero_mx4_matmul(int dtype, uint64_t m, uint64_t n, uint64_t k, const void* a_codes, const void* a_scales,
+                    const void* b_codes, const void* b_scales, void* out16, uint64_t ld, void* stream) {
+    nvtxRangePushA("zero_mx4_matmul");
+    struct Pop { ~Pop() { nvtxRangePop(); } } pop;
+    if (const int rc = mx_check(dtype, m, k, a_codes, a_scales)) return rc;
+    if (const int rc = mx_check(dtype, n, k, b_codes, b_scales)) return rc;
+    if (m == 0 || n == 0) return ZERO_OK;
+    if (!out16 || !aligned(out16, 2)) return refuse(ZERO_EINVAL, "out16 is NULL or not 2-byte aligned");
+    if (ld < n || ld > (1ull << 40)) return refuse(ZERO_EINVAL, "ld must be at least n (and at most 2^40)");
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (k == 0) {   // an empty sum
+        e = cudaMemset2DAsync(out16, ld * 2, 0, n * 2, m, s);
+        return e == cudaSuccess ? ZERO_OK : cuda_refuse(e, "zero_mx4_matmul");
+    }
+    const uint64_t tiles = up(m, kMxM) / kMxM * (up(n, kMxN) / kMxN);
+    if (tiles > 0x7FFFFFFFull) return refuse(ZERO_EINVAL, "m and n are too large together");
+    int sms = 0;
+    if ((e = sm_count(&sms)) != cudaSuccess) return cuda_refuse(e, "zero_mx4_matmul");
+    MxProductArgs p = {};
+    p.m = static_cast<uint32_t>(m);
+    p.n = static_cast<uint32_t>(n);
+    p.k = static_cast<uint32_t>(k);
+    p.tiles_n = static_cast<uint32_t>(up(n, kMxN) / kMxN);
+    p.total = static_cast<uint32_t>(tiles);
+    p.tiles_k = static_cast<uint32_t>(up(k, 128) / 128);
+    p.a_scales = static_cast<const uint8_t*>(a_scales);
+    p.b_scales = static_cast<const uint8_t*>(b_scales);
+    p.out = out16;
+    p.ld = ld;
+    p.vec = aligned(out16, 16) && ld % 8 == 0;
+    CUtensorMap ma, mb;
+    const uint64_t pitch = mx_pitch(k);
+    if ((e = make_map(&ma, 1, a_codes, pitch, m, 1, pitch, m * pitch, 128, 128)) != cudaSuccess ||
+        (e = make_map(&mb, 1, b_codes, pitch, n, 1, pitch, n * pitch, 128, 128)) != cudaSuccess)
+        return cuda_refuse(e, "tensor map");
+    const unsigned grid = grid_of(tiles, sms, 1);
+    if (dtype == ZERO_FP16) {
+        if ((e = allow_smem<k_mx4_product<kFp16>>(kMxSmem)) == cudaSuccess)
+            e = launch_pdl(k_mx4_product<kFp16>, dim3(grid), kMxThreads, kMxSmem, 1, s, ma, mb, p);
+    } else {
+        if ((e = allow_smem<k_mx4_product<kBf16>>(kMxSmem)) == cudaSuccess)
+            e = launch_pdl(k_mx4_product<kBf16>, dim3(grid), kMxThreads, kMxSmem, 1, s, ma, mb, p);
+    }
+    return e == cudaSuccess ? ZERO_OK : cuda_refuse(e, "zero_mx4_matmul");
+}
+
+int zero_matrix_status(void* stream) {
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int32_t a = 0, b = 0;
+    cudaError_t e = ortho_gave_up(s, &a);
+    if (e == cudaSuccess) e = mx4_gave_up(s, &b);
+    if (e != cudaSuccess) return cuda_refuse(e, "zero_matrix_status");
+    if (a | b) return refuse(ZERO_ETIMEOUT, "a bounded wait inside a matrix kernel gave up: its output is incomplete");
+    return ZERO_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,255 @@
+// Tensor-core plumbing shared by the matrix kernels (zero_ortho.cu,
+// zero_mx4.cu): tensor maps on the host; mbarriers with bounded waits, bulk
+// tensor copies, and the tcgen05 instructions on the device.  Each
+// translation unit gets its own copy (anonymous namespace).
+//
+// Operand tiles live in shared memory in the 128-byte swizzle, which both
+// the bulk tensor copy and the matrix instructions apply by themselves:
+//   * "K-major": a row of the tile is 128 bytes along the contraction, rows
+//     follow each other, groups of 8 rows every 1024 bytes;
+//   * "MN-major": a row is 64 16-bit values along the tile's own M or N, one
+//     row per step of the contraction, groups of 8 steps every 1024 bytes,
+//     the next 64 values of M or N a whole block further on.
+#pragma once
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "zero_host.h"
+#include "zero_device.cuh"
+
+namespace zg {
+namespace {
+
+// ------------------------------------------------------------ tensor maps
+// cuTensorMapEncodeTiled, found through the runtime so that the library does
+// not link against the driver.
+inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult found = cudaDriverEntryPointSymbolNotFound;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) !=
+                cudaSuccess ||
+            found != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            p = nullptr;
+        }
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }();
+    return fn;
+}
+
+// A [batch][rows][cols] array of `elem`-byte values (1: bytes, 2: 16 bits)
+// with `pitch` values between rows, read in boxes of box_cols x box_rows in
+// the 128-byte swizzle; what lies outside the array reads as zero.
+inline cudaError_t make_map(CUtensorMap* map, int elem, const void* base, uint64_t cols, uint64_t rows, uint64_t batch,
+                            uint64_t pitch, uint64_t matrix_stride, uint32_t box_cols, uint32_t box_rows) {
+    const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+    if (!encode) return cudaErrorNotSupported;
+    const cuuint64_t dims[3] = {cols, rows, batch};
+    const cuuint64_t strides[2] = {pitch * static_cast<uint64_t>(elem), matrix_stride * static_cast<uint64_t>(elem)};
+    const cuuint32_t box[3] = {box_cols, box_rows, 1};
+    const cuuint32_t step[3] = {1, 1, 1};
+    const CUresult r = encode(map, elem == 2 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3,
+                              const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// ---------------------------------------------------------------- barriers
+constexpr uint64_t kGiveUpNs = 2000000000ull;   // every wait ends within about 2 s
+
+// 1 + the kernel role whose bounded wait gave up; read and cleared by the
+// host's status call.
+__device__ int32_t g_gave_up;
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) {
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ uint64_t now_ns() {
+    uint64_t t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
+}
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_init_fence() {
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// Waits for the phase of parity `parity`; false when the wait gave up or
+// another role of the block had (`*quit`).  The time is looked at only after
+// a few hundred failed tries, each of which may itself suspend the thread.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* quit) {
+    if (bar_test(bar, parity)) return true;
+    uint64_t t0 = 0;
+    for (uint32_t i = 1;; ++i) {
+        if (bar_test(bar, parity)) return true;
+        if ((i & 127u) == 0u) {
+            if (*quit) return false;
+            const uint64_t t = now_ns();
+            if (t0 == 0) t0 = t;
+            if (t - t0 > kGiveUpNs) {
+                *quit = 1;
+                atomicExch(&g_gave_up, 1);
+                return false;
+            }
+        }
+    }
+}
+// The same without regard to `quit`: for the copies and products that a
+// block still has in flight when it gives up.
+__device__ __forceinline__ void bar_drain(uint32_t bar, uint32_t parity) {
+    const uint64_t t0 = now_ns();
+    while (!bar_test(bar, parity) && now_ns() - t0 < kGiveUpNs) {}
+}
+
+// ------------------------------------------------------------------ copies
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void copy_bytes(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(dst), "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+// ----------------------------------------------------------------- tcgen05
+__device__ __forceinline__ void tmem_alloc(uint32_t smem_slot, uint32_t cols) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_slot), "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// The barrier gets one arrival once every product issued so far has finished.
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+// D (fp32, tensor memory) = A B + (accumulate ? D : 0), 16-bit operands.
+__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+        : "memory");
+}
+// 32 lanes x 32 columns of fp32: thread t gets lane (its warp's quarter) + t.
+__device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32]) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// Shared-memory operand descriptor in the 128-byte swizzle.  `lead` is the
+// distance in bytes between 64-value blocks of an MN-major tile (unused for
+// K-major); groups of 8 rows are 1024 bytes apart in both.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, uint32_t lead) {
+    uint64_t d = static_cast<uint64_t>((addr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>((lead >> 4) & 0x3FFFu) << 16;
+    d |= static_cast<uint64_t>(1024u >> 4) << 32;
+    d |= static_cast<uint64_t>(1) << 46;   // descriptor version of sm_100
+    d |= static_cast<uint64_t>(2) << 61;   // 128-byte swizzle
+    return d;
+}
+
+// Two fp32 values as packed 16-bit ones, the first in the low half.
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_bf2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Lower-triangular tile t of a square grid of tiles: row i >= column j.
+__device__ __forceinline__ void triangle(uint32_t t, uint32_t& i, uint32_t& j) {
+    uint32_t r = static_cast<uint32_t>((__fsqrt_rn(8.0f * static_cast<float>(t) + 1.0f) - 1.0f) * 0.5f);
+    while (r * (r + 1) / 2 > t) --r;
+    while ((r + 1) * (r + 2) / 2 <= t) ++r;
+    i = r;
+    j = t - r * (r + 1) / 2;
+}
+
+// -------------------------------------------------------------------- host
+inline cudaError_t sm_count(int* out) {
+    static std::mutex mu;
+    static int sms[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lock(mu);
+    if (!sms[dev] && (e = cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
+        return e;
+    *out = sms[dev];
+    return cudaSuccess;
+}
+
+// Raises a kernel's shared-memory limit, once per kernel and device.
+template <auto Kernel>
+cudaError_t allow_smem(size_t bytes) {
+    static std::mutex mu;
+    static uint64_t seen = 0;   // one bit a device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lock(mu);
+    if ((seen >> dev) & 1) return cudaSuccess;
+    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    if (e == cudaSuccess) seen |= 1ull << dev;
+    return e;
+}
+
+// Reads this file's give-up word and, when it is set, clears it.
+// Synchronises the stream.
+inline cudaError_t read_gave_up(cudaStream_t s, int32_t* out) {
+    static const int32_t zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbolAsync(out, g_gave_up, sizeof(zero), 0, cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e == cudaSuccess && *out)
+        e = cudaMemcpyToSymbolAsync(g_gave_up, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s);
+    return e;
+}
+
+}  // namespace
+}  // namespace zg
