@@ -608,6 +608,28 @@ cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, unsigned threads, size_t
     return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
 }
 
+// A cooperative launch (all CTAs resident at once, so they may wait for one
+// another) in clusters of `cluster` CTAs, in plain stream order.
+template <typename... P, typename... A>
+cudaError_t launch_together(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, unsigned cluster,
+                            cudaStream_t s, A&&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+    cfg.attrs = attr;
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+}
+
 // Launch on a persistent grid: as many CTAs as fit on the SMs at once (from
 // the occupancy API, or per_sm CTAs per SM when per_sm > 0 caps it lower),
 // or fewer when `nvec` vectors need fewer, capped at the per-block partial

@@ -25,6 +25,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <cstring>
 #include <string>
 
 #include <nvtx3/nvToolsExt.h>
@@ -36,6 +37,7 @@ namespace zg {
 namespace {
 
 constexpr int kMaxMatrices = ZERO_MAX_MATRICES;
+constexpr int kMaxPhases = 3 * ZERO_MAX_NS_STEPS + 3;
 
 // Storage scales (all powers of two): entries of X and A are at most a
 // little over 1, those of p(A) and Q at most a^2 or so.
@@ -56,6 +58,7 @@ struct PackArgs {
     int partials;
     double* partial;            // [batch][kPartials]
     float* g0;                  // [batch]
+    uint32_t* done;             // [batch][kMaxPhases], cleared for the products
     __half* x0;                 // [batch][rows][pitch]
 };
 
@@ -88,6 +91,8 @@ template <int DT>
 __global__ void __launch_bounds__(kThreads) k_ortho_norm(const __grid_constant__ PackArgs a) {
     pdl_enter();
     const int b = blockIdx.y;
+    if (blockIdx.x == 0)
+        for (int i = threadIdx.x; i < kMaxPhases; i += kThreads) a.done[static_cast<uint64_t>(b) * kMaxPhases + i] = 0u;
     double acc = 0.0;
     for (uint64_t u = static_cast<uint64_t>(blockIdx.x) * kPackWarps + (threadIdx.x >> 5); u < a.units;
          u += static_cast<uint64_t>(gridDim.x) * kPackWarps) {
@@ -102,7 +107,7 @@ __global__ void __launch_bounds__(kThreads) k_ortho_norm(const __grid_constant__
         }
         if (!(s < INFINITY) || !(top < 0x1p60f) || (top > 0.0f && top < 0x1p-50f)) {
             double d = 0.0;
-#pragma unroll 8
+#pragma unroll
             for (int i = 0; i < 64; ++i) d = fma(static_cast<double>(v[i]), static_cast<double>(v[i]), d);
             acc += d;
         } else {
@@ -163,55 +168,171 @@ __global__ void __launch_bounds__(kThreads) k_ortho_pack(const __grid_constant__
 }
 
 // ---------------------------------------------------------------- products
-// One product of every matrix of the batch, out = epilogue(A B^T): A has the
-// output's rows, B its columns, both over `depth`.
-enum Epi : int {
+// All products of a call run in one kernel.  Each is a phase: for every
+// matrix of the batch, out = epilogue(A B^T), A having the output's rows and
+// B its columns, both over `depth`.  A tile of a phase waits until the
+// matrix's previous phase is complete (a counter per matrix and phase), so
+// the matrices of a batch run through the phases independently, without a
+// launch or a grid-wide barrier between them.  Tiles are handed out in
+// order of phase, matrix, tile, round robin over the CTA pairs, so every
+// tile depends on earlier ones only, and the launch is cooperative: every
+// wait ends.
+enum Epi : int32_t {
     kScale,   // out = f acc
     kPoly,    // out = f acc + f_lin lin + f_diag I
     kFinal,   // bf16, into the caller's matrices: out = f acc
 };
 
-struct ProductArgs {
+struct Phase {
+    int32_t a, b;              // tensor maps of the operands
+    int32_t a_mn, b_mn;        // their order in memory: 0 K-major, 1 MN-major
+    int32_t out, mirror, lin;  // tensor maps: output, its mirror image (-1: not symmetric), the linear term
+    Epi epi;
     uint32_t rows, cols, depth;
-    uint32_t tiles_n, tiles, total;   // tiles a row, a matrix, all
-    __half* out;
-    const __half* lin;
-    uint32_t pitch;          // of out and lin
-    uint64_t stride;         // between matrices of out and lin
+    uint32_t tiles_n, tiles;   // tiles a row, a matrix
     float f_acc, f_lin, f_diag;
-    const float* g0;         // further factor g0[b]^g_power, or null
-    int g_power;
-    void* dst[kMaxMatrices]; // kFinal
-    uint64_t dst_ld;
-    int dst_vec;             // every row of dst starts on 16 bytes
+    int32_t g_power;           // further factor g0[b]^g_power
 };
 
-constexpr int kBlockM = 128, kBlockK = 64;
-constexpr int kProductThreads = 192;   // copies, products, 4 warps of epilogue
+enum Map : int { kXRows0, kXRows1, kXCols0, kXCols1, kSquare0, kSquare1, kSquare2,   // operands
+                 kXOut0, kXOut1, kSquareOut0, kSquareOut1, kSquareOut2,             // outputs (and linear terms)
+                 kMirror0, kMirror1, kMirror2, kMaps };
 
-__host__ __device__ constexpr int stages_of(int bn) { return bn == 256 ? 4 : 6; }
-__host__ __device__ constexpr uint32_t stage_bytes(int bn) { return (kBlockM + bn) * kBlockK * 2u; }
-__host__ __device__ constexpr size_t product_smem(int bn) { return 1024 + static_cast<size_t>(stages_of(bn)) * stage_bytes(bn); }
+struct ProductArgs {
+    CUtensorMap maps[kMaps];
+    Phase phases[kMaxPhases];
+    void* dst[kMaxMatrices];   // kFinal
+    uint64_t dst_ld;
+    const float* g0;           // [batch]
+    uint32_t* done;            // [batch][kMaxPhases] finished epilogues, zero at the start
+    int32_t dst_vec;           // every row of dst starts on 16 bytes
+    uint32_t n_phases, batch;
+};
 
-// Warp 0 copies operand tiles into a ring of stages, warp 1 issues the
-// products, warps 2 to 5 read finished accumulators; two accumulators in
-// tensor memory, so that the epilogue of one tile runs under the products of
-// the next.
-template <int BN, bool A_MN, bool B_MN, int EPI, bool SYM>
-__global__ void __launch_bounds__(kProductThreads)
-k_ortho_product(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                const __grid_constant__ ProductArgs p) {
-    constexpr int kStages = stages_of(BN);
-    constexpr uint32_t kStageBytes = stage_bytes(BN), kABytes = kBlockM * kBlockK * 2;
+// A pair of CTAs computes 256 x 256 tiles: a stage of 64 steps of the
+// contraction is 32 KiB a CTA for 512 cycles of products, which is about
+// what an SM gets from L2 (128 x 128 tiles of one CTA need twice that, and
+// ran at 0.9 PFLOP/s).  Warp 0 copies operands into a ring of stages, warp 1
+// of the leader issues the products, warps 2 to 5 turn finished accumulators
+// into output; two accumulators in tensor memory, so that one tile's
+// epilogue runs under the next one's products.
+constexpr int kTile = 256, kHalf = 128, kBlockK = 64;
+constexpr int kProductThreads = 192;
+constexpr int kStages = 5;
+constexpr uint32_t kOperandBytes = kHalf * kBlockK * 2, kStageBytes = 2 * kOperandBytes;
+// A warp's output buffers: 32 rows x 64 columns twice, and the mirror image
+// (64 x 32) twice.
+constexpr uint32_t kOutBytes = 32 * 64 * 2, kWarpBytes = 4 * kOutBytes;
+constexpr size_t kProductSmem = 1024 + kStages * kStageBytes + 4 * kWarpBytes;
+constexpr uint32_t kDonePerTile = 8;   // 4 warps of 2 CTAs
+
+// The tiles of one CTA pair, in order.
+struct Walk {
+    const ProductArgs& p;
+    uint32_t phase, at;   // `at`: index within the phase
+    uint32_t b, tm, tn;
+    __device__ explicit Walk(const ProductArgs& args) : p(args), phase(0), at(blockIdx.x >> 1), b(0), tm(0), tn(0) {}
+    __device__ bool find() {
+        while (phase < p.n_phases) {
+            const Phase& f = p.phases[phase];
+            const uint32_t total = f.tiles * p.batch;
+            if (at < total) {
+                b = at / f.tiles;
+                const uint32_t t = at - b * f.tiles;
+                if (f.mirror >= 0) {
+                    triangle(t, tm, tn);
+                } else {
+                    tm = t / f.tiles_n;
+                    tn = t - tm * f.tiles_n;
+                }
+                return true;
+            }
+            at -= total;
+            ++phase;
+        }
+        return false;
+    }
+    __device__ bool next() {
+        at += gridDim.x >> 1;
+        return find();
+    }
+    // Waits for the matrix's previous phase.
+    __device__ bool inputs_ready(volatile int* quit) const {
+        if (phase == 0) return true;
+        return count_wait(p.done + static_cast<uint64_t>(b) * kMaxPhases + phase - 1,
+                          p.phases[phase - 1].tiles * kDonePerTile, quit);
+    }
+};
+
+// Byte offset of 16-byte piece j of row r in a buffer of 128-byte or 64-byte
+// rows, as the bulk copy's swizzle of that width places it.
+__device__ __forceinline__ uint32_t piece128(uint32_t r, uint32_t j) { return r * 128 + ((j ^ (r & 7)) << 4); }
+__device__ __forceinline__ uint32_t piece64(uint32_t r, uint32_t j) { return r * 64 + ((j ^ ((r >> 1) & 3)) << 4); }
+__device__ __forceinline__ void st_shared(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+__device__ __forceinline__ void st_shared(uint32_t addr, uint32_t x) {
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared(uint32_t addr) {
+    uint4 x;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                 : "r"(addr)
+                 : "memory");
+    return x;
+}
+__device__ __forceinline__ uint16_t ld_shared16(uint32_t addr) {
+    uint16_t x;
+    asm volatile("ld.shared.b16 %0, [%1];" : "=h"(x) : "r"(addr) : "memory");
+    return x;
+}
+
+// 32 rows x 64 columns of bf16 in a warp's buffer into the caller's matrix:
+// whole 128-byte rows where they are aligned, element by element elsewhere.
+__device__ __forceinline__ void write_rows(const ProductArgs& p, const Phase& f, uint32_t b, uint32_t row0, uint32_t col0,
+                                           uint32_t buf) {
+    const uint32_t lane = threadIdx.x & 31;
+    unsigned short* dst = static_cast<unsigned short*>(p.dst[b]);
+    if (p.dst_vec) {
+#pragma unroll 4
+        for (uint32_t i = lane; i < 256; i += 32) {
+            const uint32_t r = i >> 3, j = i & 7, col = col0 + 8 * j;
+            if (row0 + r >= f.rows || col >= f.cols) continue;
+            unsigned short* out = dst + static_cast<uint64_t>(row0 + r) * p.dst_ld + col;
+            const uint4 x = ld_shared(buf + piece128(r, j));
+            if (col + 8 <= f.cols) {
+                *reinterpret_cast<uint4*>(out) = x;
+            } else {
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (uint32_t e = 0; e < 8; ++e)
+                    if (col + e < f.cols) out[e] = static_cast<unsigned short>(w[e >> 1] >> (16 * (e & 1)));
+            }
+        }
+    } else {
+#pragma unroll 4
+        for (uint32_t i = lane; i < 32 * 64; i += 32) {
+            const uint32_t r = i >> 6, e = i & 63;
+            if (row0 + r < f.rows && col0 + e < f.cols)
+                dst[static_cast<uint64_t>(row0 + r) * p.dst_ld + col0 + e] =
+                    ld_shared16(buf + piece128(r, e >> 3) + 2 * (e & 7));
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kProductThreads) k_ortho_products(const __grid_constant__ ProductArgs p) {
     extern __shared__ unsigned char smem_raw[];
-    __shared__ __align__(8) uint64_t bars[2 * kStages + 4];
+    __shared__ __align__(8) uint64_t bars[2 * kStages + 4 + 8];
+    __shared__ __align__(8) uint64_t s_last;
     __shared__ uint32_t s_tmem;
     __shared__ int s_quit;
     volatile int* quit = &s_quit;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
     const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    const uint32_t full = smem_u32(bars), empty = full + 8 * kStages, done = empty + 8 * kStages, freed = done + 16;
-
+    const uint32_t full = smem_u32(bars), empty = full + 8 * kStages, done = empty + 8 * kStages, freed = done + 16,
+                   lin0 = freed + 16;
     if (threadIdx.x == 0) {
         s_quit = 0;
         for (int i = 0; i < kStages; ++i) {
@@ -220,78 +341,70 @@ k_ortho_product(const __grid_constant__ CUtensorMap map_a, const __grid_constant
         }
         for (int i = 0; i < 2; ++i) {
             bar_init(done + 8 * i, 1);
-            bar_init(freed + 8 * i, 128);
+            bar_init(freed + 8 * i, 8);
         }
+        for (int i = 0; i < 8; ++i) bar_init(lin0 + 8 * i, 1);
+        bar_init(smem_u32(&s_last), 1);
         bar_init_fence();
-        prefetch_map(&map_a);
-        prefetch_map(&map_b);
     }
-    if (warp == 1) tmem_alloc(smem_u32(&s_tmem), 2 * BN);
+    if (warp == 1) tmem_alloc_pair(smem_u32(&s_tmem), 2 * kTile);
     tc_fence_before();
     __syncthreads();
+    cluster_sync();
     tc_fence_after();
     const uint32_t tmem = s_tmem;
-    pdl_enter();
-
-    const uint32_t nk = (p.depth + kBlockK - 1) / kBlockK;
-    auto place = [&](uint32_t t, uint32_t& b, uint32_t& tm, uint32_t& tn) {
-        b = t / p.tiles;
-        t -= b * p.tiles;
-        if (SYM) {
-            triangle(t, tm, tn);
-        } else {
-            tm = t / p.tiles_n;
-            tn = t - tm * p.tiles_n;
-        }
-    };
 
     if (warp == 0 && lane == 0) {
+        const uint32_t leader_full = cluster_addr(full, 0);
         uint32_t it = 0;   // fills so far
         bool ok = true;
-        for (uint32_t t = blockIdx.x; t < p.total && ok; t += gridDim.x) {
-            uint32_t b, tm, tn;
-            place(t, b, tm, tn);
+        Walk w(p);
+        for (bool more = w.find(); more && ok; more = w.next()) {
+            const Phase& f = p.phases[w.phase];
+            if (!w.inputs_ready(quit)) break;
+            proxy_fence();
+            const uint32_t nk = (f.depth + kBlockK - 1) / kBlockK;
+            const CUtensorMap *ma = &p.maps[f.a], *mb = &p.maps[f.b];
+            const int ra = static_cast<int>(w.tm * kTile + rank * kHalf);
+            const int rb = static_cast<int>(w.tn * kTile + rank * kHalf), z = static_cast<int>(w.b);
+            const bool a_mn = f.a_mn, b_mn = f.b_mn;
             for (uint32_t kb = 0; kb < nk; ++kb, ++it) {
                 const uint32_t s = it % kStages;
                 if (it >= kStages && !bar_wait(empty + 8 * s, (it / kStages - 1) & 1, quit)) {
                     ok = false;
                     break;
                 }
-                const uint32_t bar = full + 8 * s, sa = ring + s * kStageBytes, sb = sa + kABytes;
+                const uint32_t bar = leader_full + 8 * s, sa = ring + s * kStageBytes, sb = sa + kOperandBytes;
                 const int k0 = static_cast<int>(kb * kBlockK);
-                bar_expect(bar, kStageBytes);
-                if (A_MN) {
-#pragma unroll
-                    for (int i = 0; i < kBlockM / 64; ++i)
-                        copy_box(sa + i * 8192, &map_a, static_cast<int>(tm * kBlockM) + 64 * i, k0, static_cast<int>(b), bar);
+                if (rank == 0) bar_expect(full + 8 * s, 2 * kStageBytes);   // the bytes of both CTAs
+                if (a_mn) {
+                    copy_box_pair(sa, ma, ra, k0, z, bar);
+                    copy_box_pair(sa + 8192, ma, ra + 64, k0, z, bar);
                 } else {
-                    copy_box(sa, &map_a, k0, static_cast<int>(tm * kBlockM), static_cast<int>(b), bar);
+                    copy_box_pair(sa, ma, k0, ra, z, bar);
                 }
-                if (B_MN) {
-#pragma unroll
-                    for (int i = 0; i < BN / 64; ++i)
-                        copy_box(sb + i * 8192, &map_b, static_cast<int>(tn * BN) + 64 * i, k0, static_cast<int>(b), bar);
+                if (b_mn) {
+                    copy_box_pair(sb, mb, rb, k0, z, bar);
+                    copy_box_pair(sb + 8192, mb, rb + 64, k0, z, bar);
                 } else {
-#pragma unroll
-                    for (int i = 0; i < BN / 128; ++i)
-                        copy_box(sb + i * 16384, &map_b, k0, static_cast<int>(tn * BN) + 128 * i, static_cast<int>(b), bar);
+                    copy_box_pair(sb, mb, k0, rb, z, bar);
                 }
             }
         }
-        if (!ok)   // the block must not leave with copies in flight
-            for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i)
-                bar_drain(full + 8 * (i % kStages), (i / kStages) & 1);
-    } else if (warp == 1 && lane == 0) {
-        // fp32 accumulation, fp16 operands, 128 x BN
-        constexpr uint32_t idesc = (1u << 4) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u) |
-                                   (static_cast<uint32_t>(BN >> 3) << 17) | (static_cast<uint32_t>(kBlockM >> 4) << 24);
-        constexpr uint32_t step_a = (A_MN ? 2048u : 32u) >> 4, step_b = (B_MN ? 2048u : 32u) >> 4;
+    } else if (warp == 1 && lane == 0 && rank == 0) {
         uint32_t it = 0, n = 0;
         bool ok = true;
-        for (uint32_t t = blockIdx.x; t < p.total && ok; t += gridDim.x, ++n) {
-            const uint32_t acc = n & 1, d = tmem + acc * BN;
+        Walk w(p);
+        for (bool more = w.find(); more && ok; more = w.next(), ++n) {
+            const Phase& f = p.phases[w.phase];
+            // fp32 accumulation, fp16 operands, 256 x 256
+            const uint32_t idesc = (1u << 4) | (f.a_mn ? 1u << 15 : 0u) | (f.b_mn ? 1u << 16 : 0u) |
+                                   (static_cast<uint32_t>(kTile >> 3) << 17) | (static_cast<uint32_t>(kTile >> 4) << 24);
+            const uint32_t step_a = (f.a_mn ? 2048u : 32u) >> 4, step_b = (f.b_mn ? 2048u : 32u) >> 4;
+            const uint32_t acc = n & 1, d = tmem + acc * kTile;
             if (n >= 2 && !bar_wait(freed + 8 * acc, (n / 2 - 1) & 1, quit)) break;
             tc_fence_after();
+            const uint32_t nk = (f.depth + kBlockK - 1) / kBlockK;
             for (uint32_t kb = 0; kb < nk; ++kb, ++it) {
                 const uint32_t s = it % kStages;
                 if (!bar_wait(full + 8 * s, (it / kStages) & 1, quit)) {
@@ -300,114 +413,159 @@ k_ortho_product(const __grid_constant__ CUtensorMap map_a, const __grid_constant
                 }
                 tc_fence_after();
                 const uint32_t sa = ring + s * kStageBytes;
-                const uint64_t da = operand_desc(sa, 8192), db = operand_desc(sa + kABytes, 8192);
+                const uint64_t da = operand_desc(sa, 8192), db = operand_desc(sa + kOperandBytes, 8192);
 #pragma unroll
                 for (int k = 0; k < kBlockK / 16; ++k)
-                    mma_f16(d, da + k * step_a, db + k * step_b, idesc, kb > 0 || k > 0);
-                tc_commit(empty + 8 * s);
+                    mma_f16_pair(d, da + k * step_a, db + k * step_b, idesc, kb > 0 || k > 0);
+                tc_commit_pair(empty + 8 * s);
             }
-            if (ok) tc_commit(done + 8 * acc);
+            if (ok) tc_commit_pair(done + 8 * acc);
         }
-        if (*quit) {   // nor free tensor memory under a product
-            // a ring slot's barrier may be mid-phase, so finish on one of its own
-            __shared__ __align__(8) uint64_t s_last;
-            bar_init(smem_u32(&s_last), 1);
-            bar_init_fence();
-            tc_commit(smem_u32(&s_last));
+        if (*quit) {   // tensor memory must not be freed under a product
+            tc_commit_pair(smem_u32(&s_last));
             bar_drain(smem_u32(&s_last), 0);
         }
     } else if (warp >= 2) {
-        const uint32_t quarter = warp & 3;
-        uint32_t n = 0;
-        for (uint32_t t = blockIdx.x; t < p.total; t += gridDim.x, ++n) {
+        const uint32_t quarter = warp & 3;   // the lanes of tensor memory that this warp can read
+        const uint32_t mine = ring + kStages * kStageBytes + quarter * kWarpBytes;
+        const uint32_t leader_freed = cluster_addr(freed, 0), lin_bar = lin0 + 16 * quarter;
+        uint32_t n = 0, lin_parity = 0;   // bit i: parity of the next fill of buffer i
+        Walk w(p);
+        for (bool more = w.find(); more; more = w.next(), ++n) {
+            const Phase& f = p.phases[w.phase];
             const uint32_t acc = n & 1;
-            uint32_t b, tm, tn;
-            place(t, b, tm, tn);
-            const bool ok = bar_wait(done + 8 * acc, (n / 2) & 1, quit);
+            const uint32_t row0 = w.tm * kTile + rank * kHalf + quarter * 32, col0 = w.tn * kTile;
+            const int z = static_cast<int>(w.b);
+            // chunks of 64 columns that hold output
+            const uint32_t left = (f.cols - col0 + 63u) / 64u, chunks = row0 >= f.rows ? 0u : left < 4u ? left : 4u;
+            const bool poly = f.epi == kPoly, final = f.epi == kFinal, mirror = f.mirror >= 0 && w.tm != w.tn;
+            auto fetch_lin = [&](uint32_t c) {   // one lane: the buffer's last store has been read, then fill it
+                store_wait_read<0>();
+                proxy_fence();
+                bar_expect(lin_bar + 8 * (c & 1), kOutBytes);
+                copy_box(mine + (c & 1) * kOutBytes, &p.maps[f.lin], static_cast<int>(col0 + 64 * c),
+                         static_cast<int>(row0), z, lin_bar + 8 * (c & 1));
+            };
+            bool ok = true;
+            if (poly && chunks && lane == 0) {   // the linear term's first chunks arrive under the products
+                ok = w.inputs_ready(quit);
+                if (ok) {
+                    fetch_lin(0);
+                    if (chunks > 1) fetch_lin(1);
+                }
+            }
+            ok = ok && bar_wait(done + 8 * acc, (n / 2) & 1, quit);
             if (__any_sync(0xFFFFFFFFu, !ok)) break;
             tc_fence_after();
-            const uint32_t row = tm * kBlockM + quarter * 32 + lane;
-            float f = p.f_acc;
-            if (p.g0) {
-                const float g = __ldg(p.g0 + b);
-                f *= p.g_power == 2 ? g * g : g;
+            float scale = f.f_acc;
+            if (f.g_power) {
+                const float g = __ldg(p.g0 + w.b);
+                scale *= f.g_power == 2 ? g * g : g;
             }
-            const uint64_t at = b * p.stride + static_cast<uint64_t>(row) * p.pitch;
+            const float f_lin = f.f_lin, f_diag = f.f_diag;
 #pragma unroll 1
-            for (int cc = 0; cc < BN / 32; ++cc) {
-                const uint32_t col = tn * BN + cc * 32;
-                if (col >= p.cols) break;   // uniform over the warp
-                float v[32];
-                tmem_load32(tmem + acc * BN + cc * 32 + (quarter << 21), v);
-                if (EPI == kPoly) {
-#pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        uint4 x = make_uint4(0, 0, 0, 0);
-                        if (row < p.rows && col + 8 * g < p.cols)
-                            x = *reinterpret_cast<const uint4*>(p.lin + at + col + 8 * g);
-                        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float l = widen<kFp16>((w[e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
-                            float y = __fmaf_rn(v[8 * g + e], f, l * p.f_lin);
-                            if (row == col + 8 * g + e) y += p.f_diag;
-                            v[8 * g + e] = y;
-                        }
+            for (uint32_t c = 0; c < chunks; ++c) {
+                const uint32_t buf = mine + (c & 1) * kOutBytes, flip = mine + (2 + (c & 1)) * kOutBytes;
+                if (lane == 0) {
+                    if (poly) {
+                        if (c >= 1 && c + 1 < chunks) fetch_lin(c + 1);
+                        ok = bar_wait(lin_bar + 8 * (c & 1), (lin_parity >> (c & 1)) & 1, quit);
+                        lin_parity ^= 1u << (c & 1);
                     }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) v[e] *= f;
+                    store_wait_read<1>();   // the stores of chunk c - 2 have left its buffers
                 }
-                if (EPI == kFinal) {
-                    if (row < p.rows) {
-                        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.dst[b]) + static_cast<uint64_t>(row) * p.dst_ld;
+                if (__any_sync(0xFFFFFFFFu, !ok)) break;
 #pragma unroll
-                        for (int g = 0; g < 4; ++g) {
-                            const uint32_t c = col + 8 * g;
-                            if (p.dst_vec && c + 8 <= p.cols) {
-                                *reinterpret_cast<uint4*>(out + c) =
-                                    make_uint4(pack_bf2(v[8 * g], v[8 * g + 1]), pack_bf2(v[8 * g + 2], v[8 * g + 3]),
-                                               pack_bf2(v[8 * g + 4], v[8 * g + 5]), pack_bf2(v[8 * g + 6], v[8 * g + 7]));
-                            } else {
+                for (uint32_t h = 0; h < 2; ++h) {
+                    float v[32];
+                    tmem_load32(tmem + acc * kTile + c * 64 + h * 32 + (quarter << 21), v);
+                    if (poly) {
+                        const uint32_t diag = row0 + lane - (col0 + 64 * c + 32 * h);   // index of the diagonal, if < 32
 #pragma unroll
-                                for (int e = 0; e < 8; ++e)
-                                    if (c + e < p.cols) out[c + e] = __float2bfloat16_rn(v[8 * g + e]);
+                        for (uint32_t j = 0; j < 4; ++j) {
+                            const uint4 x = ld_shared(buf + piece128(lane, 4 * h + j));
+                            const uint32_t q[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                            for (uint32_t e = 0; e < 8; ++e) {
+                                const float l = widen<kFp16>((q[e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
+                                float y = __fmaf_rn(v[8 * j + e], scale, l * f_lin);
+                                if (diag == 8 * j + e) y += f_diag;
+                                v[8 * j + e] = y;
                             }
                         }
+                    } else {
+#pragma unroll
+                        for (uint32_t e = 0; e < 32; ++e) v[e] *= scale;
                     }
+                    uint32_t q[16];
+#pragma unroll
+                    for (uint32_t e = 0; e < 16; ++e)
+                        q[e] = final ? pack_bf2(v[2 * e], v[2 * e + 1]) : pack_half2(v[2 * e], v[2 * e + 1]);
+#pragma unroll
+                    for (uint32_t j = 0; j < 4; ++j)
+                        st_shared(buf + piece128(lane, 4 * h + j), q[4 * j], q[4 * j + 1], q[4 * j + 2], q[4 * j + 3]);
+                    if (mirror) {
+                        // columns become rows: two lanes trade halves, the even one then holds column 2e of
+                        // its own and the next row, the odd one column 2e + 1 of the previous and its own
+#pragma unroll
+                        for (uint32_t e = 0; e < 16; ++e) {
+                            const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, q[e], 1);
+                            const uint32_t word = lane & 1 ? __byte_perm(other, q[e], 0x7632) : __byte_perm(q[e], other, 0x5410);
+                            const uint32_t r = 32 * h + 2 * e + (lane & 1);
+                            st_shared(flip + piece64(r, lane >> 3) + 4 * ((lane >> 1) & 3), word);
+                        }
+                    }
+                }
+                if (final) {
+                    __syncwarp();
+                    write_rows(p, f, w.b, row0, col0 + 64 * c, buf);
+                    __syncwarp();
                 } else {
-                    if (row < p.rows) {
-#pragma unroll
-                        for (int g = 0; g < 4; ++g)
-                            if (col + 8 * g < p.cols)   // whole vectors: the pitch is a multiple of 8
-                                *reinterpret_cast<uint4*>(p.out + at + col + 8 * g) = make_uint4(
-                                    pack_half2(v[8 * g], v[8 * g + 1]), pack_half2(v[8 * g + 2], v[8 * g + 3]),
-                                    pack_half2(v[8 * g + 4], v[8 * g + 5]), pack_half2(v[8 * g + 6], v[8 * g + 7]));
-                    }
-                    if (SYM && tm != tn && row < p.rows) {
-                        __half* mirror = p.out + b * p.stride + static_cast<uint64_t>(col) * p.pitch + row;
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (col + e < p.cols) mirror[static_cast<uint64_t>(e) * p.pitch] = __float2half_rn(v[e]);
+                    proxy_fence();
+                    __syncwarp();
+                    if (lane == 0) {
+                        store_box(&p.maps[f.out], static_cast<int>(col0 + 64 * c), static_cast<int>(row0), z, buf);
+                        if (mirror)
+                            store_box(&p.maps[f.mirror], static_cast<int>(row0), static_cast<int>(col0 + 64 * c), z, flip);
+                        store_commit();
                     }
                 }
             }
             tc_fence_before();
-            bar_arrive(freed + 8 * acc);
+            if (__any_sync(0xFFFFFFFFu, !ok)) break;
+            if (lane == 0) {
+                bar_arrive_cluster(leader_freed + 8 * acc);
+                if (!final) {   // the tile's output is in memory before it counts
+                    store_wait<0>();
+                    proxy_fence();
+                    count_done(p.done + static_cast<uint64_t>(w.b) * kMaxPhases + w.phase);
+                }
+            }
+            __syncwarp();
         }
+        if (lane == 0) store_wait<0>();
     }
+    __syncwarp();
+    if (*quit && threadIdx.x == 0) {   // copies in flight land within microseconds: leave them a millisecond
+        const uint64_t t0 = now_ns();
+        while (now_ns() - t0 < 1000000ull) {}
+    }
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
+    cluster_sync();
     if (warp == 1) {
         tc_fence_after();
-        tmem_free(tmem, 2 * BN);
+        tmem_free_pair(tmem, 2 * kTile);
     }
+    __syncwarp();
+    cluster_sync();
 }
 
 // -------------------------------------------------------------------- host
 // The scratch of a call, as offsets from its start.
 struct Scratch {
-    uint64_t partial, g0, x[2], s[3], bytes;
+    uint64_t partial, g0, done, x[2], s[3], bytes;
 };
 Scratch scratch_of(uint64_t batch, uint64_t rows, uint64_t cols) {
     const uint64_t side = rows < cols ? rows : cols;
@@ -420,33 +578,41 @@ Scratch scratch_of(uint64_t batch, uint64_t rows, uint64_t cols) {
     };
     z.partial = take(batch * kPartials * sizeof(double));
     z.g0 = take(batch * sizeof(float));
+    z.done = take(batch * kMaxPhases * sizeof(uint32_t));
     for (uint64_t& x : z.x) x = take(batch * rows * up(cols, 8) * 2);
     for (uint64_t& s : z.s) s = take(batch * side * up(side, 8) * 2);
     z.bytes = at;
     return z;
 }
 
-template <int BN, bool A_MN, bool B_MN, int EPI, bool SYM>
-cudaError_t product(int sms, const CUtensorMap& ma, const CUtensorMap& mb, ProductArgs& p, uint32_t batch,
-                    cudaStream_t s) {
-    const uint32_t tm = (p.rows + kBlockM - 1) / kBlockM;
-    p.tiles_n = (p.cols + BN - 1) / BN;
-    p.tiles = SYM ? tm * (tm + 1) / 2 : tm * p.tiles_n;
-    p.total = p.tiles * batch;
-    static_assert(!SYM || BN == kBlockM, "symmetric products take square tiles");
-    constexpr auto kernel = k_ortho_product<BN, A_MN, B_MN, EPI, SYM>;
-    const cudaError_t e = allow_smem<kernel>(product_smem(BN));
+// CTA pairs that can be resident at once on the current device.
+cudaError_t pairs(int* out) {
+    static std::mutex mu;
+    static int known[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    const unsigned grid = p.total < static_cast<uint32_t>(sms) ? p.total : static_cast<unsigned>(sms);
-    return launch_pdl(kernel, dim3(grid), kProductThreads, product_smem(BN), 1, s, ma, mb, p);
-}
-
-// The update X <- p X (wide) or X p (tall), into scratch or the caller's matrices.
-template <int EPI>
-cudaError_t update(int sms, bool tall, const CUtensorMap& poly, const CUtensorMap& x_rows, const CUtensorMap& x_cols,
-                   ProductArgs& p, uint32_t batch, cudaStream_t s) {
-    return tall ? product<128, false, false, EPI, false>(sms, x_rows, poly, p, batch, s)
-                : product<128, false, true, EPI, false>(sms, poly, x_cols, p, batch, s);
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lock(mu);
+    if (!known[dev]) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2);
+        cfg.blockDim = dim3(kProductThreads);
+        cfg.dynamicSmemBytes = kProductSmem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if ((e = cudaOccupancyMaxActiveClusters(&n, k_ortho_products, &cfg)) != cudaSuccess) return e;
+        if (n < 1) return cudaErrorLaunchOutOfResources;
+        known[dev] = n;
+    }
+    *out = known[dev];
+    return cudaSuccess;
 }
 
 constexpr float kDefaultCoeffs[3] = {3.4445f, -4.7750f, 2.0315f};
@@ -496,23 +662,21 @@ int zero_orthogonalize(int dtype, int batch, uint64_t rows, uint64_t cols, const
     const uint32_t nb = static_cast<uint32_t>(batch);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
 
-    int sms = 0;
-    cudaError_t e = sm_count(&sms);
-    if (e != cudaSuccess) return cuda_refuse(e, "zero_orthogonalize");
-
+    cudaError_t e;
     PackArgs q = {};
-    ProductArgs last = {};
+    ProductArgs p;   // its maps and phases are filled below
+    std::memset(&p, 0, sizeof(p));
     q.vec = ld_src % 8 == 0;
-    last.dst_vec = ld_dst % 8 == 0;
+    p.dst_vec = ld_dst % 8 == 0;
     for (int i = 0; i < batch; ++i) {
         if (!src[i] || !aligned(src[i], 2)) return refuse(ZERO_EINVAL, "src[i] is NULL or not 2-byte aligned");
         if (!dst[i] || !aligned(dst[i], 2)) return refuse(ZERO_EINVAL, "dst[i] is NULL or not 2-byte aligned");
         q.src[i] = src[i];
-        last.dst[i] = dst[i];
+        p.dst[i] = dst[i];
         q.vec &= aligned(src[i], 16);
-        last.dst_vec &= aligned(dst[i], 16);
+        p.dst_vec &= aligned(dst[i], 16);
     }
-    last.dst_ld = ld_dst;
+    p.dst_ld = ld_dst;
     q.rows = rows;
     q.cols = cols;
     q.ld = ld_src;
@@ -521,6 +685,7 @@ int zero_orthogonalize(int dtype, int batch, uint64_t rows, uint64_t cols, const
     q.units = rows * q.segments;
     q.partial = reinterpret_cast<double*>(ws + z.partial);
     q.g0 = reinterpret_cast<float*>(ws + z.g0);
+    q.done = reinterpret_cast<uint32_t*>(ws + z.done);
     q.x0 = reinterpret_cast<__half*>(ws + z.x[0]);
     const uint64_t want = (q.units + kPackWarps - 1) / kPackWarps;
     q.partials = static_cast<int>(want < kPartials ? want : kPartials);
@@ -535,88 +700,109 @@ int zero_orthogonalize(int dtype, int batch, uint64_t rows, uint64_t cols, const
         if (e != cudaSuccess) return cuda_refuse(e, "pack");
     }
 
-    // tensor maps: X by rows (K-major over columns, or MN-major blocks), the square ones by rows
-    CUtensorMap x_k[2], x_mn[2], sq[3];
+    const uint64_t xs = rows * xp, ss = side * sp;
     for (int i = 0; i < 2; ++i) {
         const void* base = ws + z.x[i];
-        if ((e = make_map(&x_k[i], 2, base, cols, rows, nb, xp, rows * xp, 64, 128)) != cudaSuccess ||
-            (e = make_map(&x_mn[i], 2, base, cols, rows, nb, xp, rows * xp, 64, 64)) != cudaSuccess)
+        if ((e = make_map(&p.maps[kXRows0 + i], 2, base, cols, rows, nb, xp, xs, kBlockK, kHalf)) != cudaSuccess ||
+            (e = make_map(&p.maps[kXCols0 + i], 2, base, cols, rows, nb, xp, xs, 64, kBlockK)) != cudaSuccess ||
+            (e = make_map(&p.maps[kXOut0 + i], 2, base, cols, rows, nb, xp, xs, 64, 32)) != cudaSuccess)
             return cuda_refuse(e, "tensor map");
     }
-    for (int i = 0; i < 3; ++i)
-        if ((e = make_map(&sq[i], 2, ws + z.s[i], side, side, nb, sp, side * sp, 64, 128)) != cudaSuccess)
+    for (int i = 0; i < 3; ++i) {
+        const void* base = ws + z.s[i];
+        if ((e = make_map(&p.maps[kSquare0 + i], 2, base, side, side, nb, sp, ss, kBlockK, kHalf)) != cudaSuccess ||
+            (e = make_map(&p.maps[kSquareOut0 + i], 2, base, side, side, nb, sp, ss, 64, 32)) != cudaSuccess ||
+            (e = make_map(&p.maps[kMirror0 + i], 2, base, side, side, nb, sp, ss, 32, 64, CU_TENSOR_MAP_SWIZZLE_64B)) !=
+                cudaSuccess)
             return cuda_refuse(e, "tensor map");
+    }
+    p.g0 = q.g0;
+    p.done = q.done;
+    p.batch = nb;
+    uint32_t most = 0;   // tiles of the largest phase
 
-    auto square = [&](int to, uint64_t depth) {   // a symmetric product into square matrix `to`
-        ProductArgs p = {};
-        p.rows = p.cols = static_cast<uint32_t>(side);
-        p.depth = static_cast<uint32_t>(depth);
-        p.out = reinterpret_cast<__half*>(ws + z.s[to]);
-        p.pitch = static_cast<uint32_t>(sp);
-        p.stride = side * sp;
-        return p;
+    auto square = [&](int to, int a, int b, uint64_t depth) -> Phase& {   // a symmetric product into square matrix `to`
+        Phase& f = p.phases[p.n_phases++];
+        const uint32_t t = static_cast<uint32_t>((side + kTile - 1) / kTile);
+        f.a = a;
+        f.b = b;
+        f.out = kSquareOut0 + to;
+        f.mirror = kMirror0 + to;
+        f.lin = -1;
+        f.epi = kScale;
+        f.rows = f.cols = static_cast<uint32_t>(side);
+        f.depth = static_cast<uint32_t>(depth);
+        f.tiles_n = t;
+        f.tiles = t * (t + 1) / 2;
+        most = f.tiles > most ? f.tiles : most;
+        return f;
     };
     // A = X X^T or X^T X of X buffer `x` into `to`; `raw`: that buffer still holds X0
     auto gram = [&](int to, int x, bool raw) {
-        ProductArgs p = square(to, span);
-        p.f_acc = raw ? kScaleA : kScaleA / (kScaleX * kScaleX);
-        p.g0 = raw ? q.g0 : nullptr;
-        p.g_power = 2;
-        return tall ? product<128, true, true, kScale, true>(sms, x_mn[x], x_mn[x], p, nb, s)
-                    : product<128, false, false, kScale, true>(sms, x_k[x], x_k[x], p, nb, s);
+        const int map = (tall ? kXCols0 : kXRows0) + x;
+        Phase& f = square(to, map, map, span);
+        f.a_mn = f.b_mn = tall;
+        f.f_acc = raw ? kScaleA : kScaleA / (kScaleX * kScaleX);
+        f.g_power = raw ? 2 : 0;
     };
     // to = a I + b A + c A^2
     auto poly = [&](int to, int a, const float* c) {
-        ProductArgs p = square(to, side);
-        p.lin = reinterpret_cast<const __half*>(ws + z.s[a]);
-        p.f_diag = c[0] * kScaleB;
-        p.f_lin = c[1] * (kScaleB / kScaleA);
-        p.f_acc = c[2] * (kScaleB / (kScaleA * kScaleA));
-        return product<128, false, false, kPoly, true>(sms, sq[a], sq[a], p, nb, s);
+        Phase& f = square(to, kSquare0 + a, kSquare0 + a, side);
+        f.epi = kPoly;
+        f.lin = kSquareOut0 + a;
+        f.f_diag = c[0] * kScaleB;
+        f.f_lin = c[1] * (kScaleB / kScaleA);
+        f.f_acc = c[2] * (kScaleB / (kScaleA * kScaleA));
     };
-    // to = B M, two commuting symmetric matrices, one of them of scale kScaleB
+    // to = B M, two commuting symmetric matrices, B of scale kScaleB
     auto commuting = [&](int to, int b, int m) {
-        ProductArgs p = square(to, side);
-        p.f_acc = 1.0f / kScaleB;
-        return product<128, false, false, kScale, true>(sms, sq[b], sq[m], p, nb, s);
+        square(to, kSquare0 + b, kSquare0 + m, side).f_acc = 1.0f / kScaleB;
     };
+    // the other X buffer (or dst) = B X, or X B of a tall matrix
     auto apply = [&](int x, int b, bool raw, bool to_dst) {
-        ProductArgs p = last;
-        p.rows = static_cast<uint32_t>(rows);
-        p.cols = static_cast<uint32_t>(cols);
-        p.depth = static_cast<uint32_t>(side);
-        p.out = reinterpret_cast<__half*>(ws + z.x[x ^ 1]);
-        p.pitch = static_cast<uint32_t>(xp);
-        p.stride = rows * xp;
-        p.g0 = raw ? q.g0 : nullptr;
-        p.g_power = 1;
-        if (to_dst) {
-            p.f_acc = raw ? scale / kScaleB : scale / (kScaleB * kScaleX);
-            return update<kFinal>(sms, tall, sq[b], x_k[x], x_mn[x], p, nb, s);
-        }
-        p.f_acc = raw ? kScaleX / kScaleB : 1.0f / kScaleB;
-        return update<kScale>(sms, tall, sq[b], x_k[x], x_mn[x], p, nb, s);
+        Phase& f = p.phases[p.n_phases++];
+        f.a = tall ? kXRows0 + x : kSquare0 + b;
+        f.b = tall ? kSquare0 + b : kXCols0 + x;
+        f.b_mn = !tall;
+        f.out = kXOut0 + (x ^ 1);
+        f.mirror = f.lin = -1;
+        f.epi = to_dst ? kFinal : kScale;
+        f.rows = static_cast<uint32_t>(rows);
+        f.cols = static_cast<uint32_t>(cols);
+        f.depth = static_cast<uint32_t>(side);
+        f.tiles_n = (f.cols + kTile - 1) / kTile;
+        f.tiles = f.tiles_n * ((f.rows + kTile - 1) / kTile);
+        most = f.tiles > most ? f.tiles : most;
+        f.g_power = raw ? 1 : 0;
+        f.f_acc = (to_dst ? scale : kScaleX) / (raw ? kScaleB : kScaleB * kScaleX);
     };
 
     int x = 0;
     for (int k = 0; k < steps;) {
         const float* c = coeffs ? coeffs + 3 * k : kDefaultCoeffs;
         const bool raw = k == 0, pair = raw && steps >= 2;
-        if ((e = gram(0, x, raw)) != cudaSuccess || (e = poly(1, 0, c)) != cudaSuccess) return cuda_refuse(e, "product");
+        gram(0, x, raw);
+        poly(1, 0, c);
         int b = 1;
         if (pair) {
-            const float* c1 = coeffs ? coeffs + 3 : kDefaultCoeffs;
-            if ((e = commuting(2, 1, 0)) != cudaSuccess ||       // B A
-                (e = commuting(0, 1, 2)) != cudaSuccess ||       // A_1 = B (B A)
-                (e = poly(2, 0, c1)) != cudaSuccess ||           // B_1
-                (e = commuting(0, 2, 1)) != cudaSuccess)         // Q = B_1 B
-                return cuda_refuse(e, "product");
+            commuting(2, 1, 0);                             // B A
+            commuting(0, 1, 2);                             // A_1 = B (B A)
+            poly(2, 0, coeffs ? coeffs + 3 : kDefaultCoeffs);
+            commuting(0, 2, 1);                             // Q = B_1 B
             b = 0;
         }
         k += pair ? 2 : 1;
-        if ((e = apply(x, b, raw, k >= steps)) != cudaSuccess) return cuda_refuse(e, "product");
+        apply(x, b, raw, k >= steps);
         x ^= 1;
     }
+
+    int resident = 0;
+    if ((e = allow_smem<k_ortho_products>(kProductSmem)) != cudaSuccess || (e = pairs(&resident)) != cudaSuccess)
+        return cuda_refuse(e, "zero_orthogonalize");
+    const uint64_t tiles = static_cast<uint64_t>(most) * nb;
+    const unsigned grid = 2u * static_cast<unsigned>(tiles < static_cast<uint64_t>(resident) ? tiles : resident);
+    e = launch_together(k_ortho_products, dim3(grid), kProductThreads, kProductSmem, 2, s, p);
+    if (e != cudaSuccess) return cuda_refuse(e, "products");
     return ZERO_OK;
 }
 
