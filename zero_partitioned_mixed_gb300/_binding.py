@@ -157,11 +157,9 @@ def exported_symbols() -> list:
 
 # ---------------------------------------------------------------- marshalling
 def _ptr(x) -> Optional[int]:
-    if x is None:
-        return None
-    if isinstance(x, int):
+    if x is None or isinstance(x, int):
         return x
-    return int(x.data_ptr())
+    return x.data_ptr()
 
 
 def _ptr_array(xs: Optional[Sequence]):
@@ -170,10 +168,7 @@ def _ptr_array(xs: Optional[Sequence]):
         return None
     if isinstance(xs, C.Array):
         return xs
-    arr = (C.c_void_p * max(1, len(xs)))()
-    for i, x in enumerate(xs):
-        arr[i] = _ptr(x)
-    return arr
+    return (C.c_void_p * max(1, len(xs)))(*[_ptr(x) for x in xs])
 
 
 def pointer_array(tensors: Sequence):
@@ -184,10 +179,18 @@ def pointer_array(tensors: Sequence):
     return _ptr_array(list(tensors))
 
 
+_raw_stream = None   # device index -> the current stream's handle
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
+        global _raw_stream
         import torch
-        return int(torch.cuda.current_stream().cuda_stream)
+        if _raw_stream is None:
+            # a few tenths of a microsecond; torch.cuda.current_stream() builds a Stream object (several)
+            _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+                lambda device: int(torch.cuda.current_stream(device).cuda_stream))
+        return _raw_stream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return int(stream.cuda_stream)

@@ -28,7 +28,8 @@ LIB_PATH = os.path.join(BUILD_DIR, LIB_NAME)
 SOURCES = ["zero_kernels.cu", "zero_quant.cu", "zero_tma.cu", "zero_api.cpp", "zero_noalloc.cu",
            "zero_muon.cu", "zero_ortho.cu", "zero_mx4.cu"]
 HEADERS = [os.path.join(INCLUDE, "zero_gb300.h"), os.path.join(CSRC, "zero_internal.h"),
-           os.path.join(CSRC, "zero_device.cuh"), os.path.join(CSRC, "zero_host.h"), os.path.join(CSRC, "zero_tc.cuh")]
+           os.path.join(CSRC, "zero_device.cuh"), os.path.join(CSRC, "zero_host.h"), os.path.join(CSRC, "zero_tc.cuh"),
+           os.path.join(CSRC, "zero_rows.cuh")]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 

@@ -22,6 +22,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "zero_gb300.h"
+#include "zero_rows.cuh"
 #include "zero_tc.cuh"
 
 namespace zg {
@@ -37,7 +38,6 @@ struct MxArgs {
     uint64_t rows, cols, ld;   // of the 16-bit matrix
     uint64_t pitch;            // bytes of a row of codes
     uint64_t tiles_k;          // scale tiles along a row of codes
-    int vec;                   // rows of the 16-bit matrix start on 16 bytes
 };
 
 __device__ __forceinline__ uint64_t scale_at(uint64_t row, uint64_t block, uint64_t tiles_k) {
@@ -70,122 +70,147 @@ __device__ __forceinline__ uint32_t codes8(const float (&x)[8]) {
 // Largest magnitude, by its bits: NaN above infinity above every number.
 __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 
-// Along the rows.  A warp takes 256 columns of a row, a lane 8 of them, so
-// four lanes share a block; rows and columns that only fill the last scale
-// tiles are walked too, for their zeros.
+// A warp's work in the two row kernels: kMxRows rows by 256 columns, 8 a
+// lane, all rows' loads in flight together.
+constexpr int kMxRows = 4;
+
+__device__ __forceinline__ int row_values(uint64_t cols, uint64_t c) {   // left of the row from column c on, within +-8
+    const int64_t left = static_cast<int64_t>(cols) - static_cast<int64_t>(c);
+    return left > 8 ? 8 : left < -8 ? -8 : static_cast<int>(left);
+}
+
+// Along the rows.  Four lanes share a block; rows and columns that only fill
+// the last scale tiles are walked too, for their zeros.
 template <int DT>
 __global__ void __launch_bounds__(kThreads) k_mx4_rows(const __grid_constant__ MxArgs a) {
     pdl_enter();
     const int lane = threadIdx.x & 31;
-    const uint64_t segments = (a.tiles_k * 128 + 255) / 256;
-    const uint64_t units = (a.rows + 127) / 128 * 128 * segments;
+    const uint64_t segments = (a.tiles_k + 1) / 2;
+    const uint64_t units = (a.rows + 127) / 128 * (128 / kMxRows) * segments;
+    const unsigned short* src = static_cast<const unsigned short*>(a.src);
+    const int64_t total = static_cast<int64_t>((a.rows - 1) * a.ld + a.cols);
     for (uint64_t u = static_cast<uint64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); u < units;
          u += static_cast<uint64_t>(gridDim.x) * (kThreads / 32)) {
-        const uint64_t row = u / segments, c = (u - row * segments) * 256 + 8 * lane;
-        float v[8] = {};
-        if (row < a.rows) {
-            const unsigned short* src = static_cast<const unsigned short*>(a.src) + row * a.ld;
-            if (a.vec && c + 8 <= a.cols) {
-                const uint4 x = __ldcs(reinterpret_cast<const uint4*>(src + c));
-                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        const uint64_t group = u / segments, row0 = group * kMxRows, c = (u - group * segments) * 256 + 8 * lane;
+        const int valid = row_values(a.cols, c);
+        uint32_t raw[kMxRows][4];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = widen<DT>((w[e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
+        for (int r = 0; r < kMxRows; ++r) {
+            if (row0 + r < a.rows) {
+                load8(src, static_cast<int64_t>((row0 + r) * a.ld + c), total, raw[r]);
             } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (c + e < a.cols) v[e] = widen<DT>(__ldcs(src + c + e));
+                raw[r][0] = raw[r][1] = raw[r][2] = raw[r][3] = 0;
             }
         }
-        uint32_t top = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) top = max(top, magnitude(v[e]));
-        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-        const uint32_t byte = scale_byte(__uint_as_float(top));
-        const float inv = scale_inverse(byte);
+        for (int r = 0; r < kMxRows; ++r) {
+            float v[8];
+            uint32_t top = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = byte == 255u ? 0.0f : __fmul_rn(v[e], inv);
-        const uint32_t q = codes8(v);
-        if (row < a.rows && (c >> 1) < a.pitch) *reinterpret_cast<uint32_t*>(a.codes + row * a.pitch + (c >> 1)) = q;
-        // the four blocks of a scale tile's row in one word
-        uint32_t word = byte;
-        word |= __shfl_down_sync(0xFFFFFFFFu, byte, 4) << 8;
-        word |= __shfl_down_sync(0xFFFFFFFFu, byte, 8) << 16;
-        word |= __shfl_down_sync(0xFFFFFFFFu, byte, 12) << 24;
-        if ((lane & 15) == 0 && (c >> 7) < a.tiles_k)
-            *reinterpret_cast<uint32_t*>(a.scales + scale_at(row, c >> 5, a.tiles_k)) = word;
+            for (int e = 0; e < 8; ++e) {
+                v[e] = e < valid ? widen<DT>((raw[r][e >> 1] >> (16 * (e & 1))) & 0xFFFFu) : 0.0f;
+                top = max(top, magnitude(v[e]));
+            }
+            top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+            top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+            const uint32_t byte = scale_byte(__uint_as_float(top));
+            const float inv = scale_inverse(byte);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = byte == 255u ? 0.0f : __fmul_rn(v[e], inv);
+            const uint32_t q = codes8(v);
+            const uint64_t row = row0 + r;
+            if (row < a.rows && (c >> 1) < a.pitch) __stcs(reinterpret_cast<uint32_t*>(a.codes + row * a.pitch + (c >> 1)), q);
+            // the four blocks of a scale tile's row in one word
+            uint32_t word = byte;
+            word |= __shfl_down_sync(0xFFFFFFFFu, byte, 4) << 8;
+            word |= __shfl_down_sync(0xFFFFFFFFu, byte, 8) << 16;
+            word |= __shfl_down_sync(0xFFFFFFFFu, byte, 12) << 24;
+            if ((lane & 15) == 0 && (c >> 7) < a.tiles_k)
+                *reinterpret_cast<uint32_t*>(a.scales + scale_at(row, c >> 5, a.tiles_k)) = word;
+        }
     }
 }
 
-// Along the columns: the codes are those of the transpose.  A thread takes
-// 128 values of one column, so it holds whole blocks and writes 64 bytes of
-// one row of codes; a warp's loads are 32 neighbouring columns.
+// Along the columns: the codes are those of the transpose.  A block takes
+// 128 rows (a scale tile's four blocks) of 64 columns, a thread 32 values of
+// one column; the codes go through shared memory so that a row of them
+// leaves as 64 neighbouring bytes.
 template <int DT>
 __global__ void __launch_bounds__(kThreads) k_mx4_columns(const __grid_constant__ MxArgs a) {
     pdl_enter();
-    const uint64_t col = static_cast<uint64_t>(blockIdx.x) * kThreads + threadIdx.x;
-    const uint64_t tile = blockIdx.y, row0 = tile * 128;
-    if (col >= (a.cols + 127) / 128 * 128) return;
+    __shared__ __align__(16) uint4 s_codes[64][5];   // 5: no two columns of a warp in the same banks
+    __shared__ uint8_t s_scale[64][4];
+    const int c = threadIdx.x & 63, b = threadIdx.x >> 6;
+    const uint64_t col = static_cast<uint64_t>(blockIdx.x) * 64 + c, row0 = static_cast<uint64_t>(blockIdx.y) * 128;
     const unsigned short* src = static_cast<const unsigned short*>(a.src) + col;
-    uint32_t word = 0;
-#pragma unroll 1
-    for (int b = 0; b < 4; ++b) {
-        float v[32];
+    uint32_t raw[32];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-            const uint64_t r = row0 + 32 * b + e;
-            v[e] = r < a.rows && col < a.cols ? widen<DT>(__ldcs(src + r * a.ld)) : 0.0f;
-        }
-        uint32_t top = 0;
-#pragma unroll
-        for (int e = 0; e < 32; ++e) top = max(top, magnitude(v[e]));
-        const uint32_t byte = scale_byte(__uint_as_float(top));
-        const float inv = scale_inverse(byte);
-        uint32_t q[4];
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            float x[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = byte == 255u ? 0.0f : __fmul_rn(v[8 * g + e], inv);
-            q[g] = codes8(x);
-        }
-        const uint64_t at = (row0 + 32 * b) / 2;
-        if (col < a.cols && at < a.pitch)
-            *reinterpret_cast<uint4*>(a.codes + col * a.pitch + at) = make_uint4(q[0], q[1], q[2], q[3]);
-        word |= byte << (8 * b);
+    for (int e = 0; e < 32; ++e) {
+        const uint64_t r = row0 + 32 * b + e;
+        raw[e] = r < a.rows && col < a.cols ? __ldg(src + r * a.ld) : 0u;
     }
-    *reinterpret_cast<uint32_t*>(a.scales + scale_at(col, 4 * tile, a.tiles_k)) = word;
+    uint32_t top = 0;
+#pragma unroll
+    for (int e = 0; e < 32; ++e) top = max(top, raw[e] & 0x7FFFu);   // the 16-bit patterns are ordered like the values
+    const uint32_t byte = scale_byte(widen<DT>(top));
+    const float inv = scale_inverse(byte);
+    uint32_t q[4];
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = byte == 255u ? 0.0f : __fmul_rn(widen<DT>(raw[8 * g + e]), inv);
+        q[g] = codes8(x);
+    }
+    s_codes[c][b] = make_uint4(q[0], q[1], q[2], q[3]);
+    s_scale[c][b] = static_cast<uint8_t>(byte);
+    __syncthreads();
+    {
+        const int cc = threadIdx.x >> 2, bb = threadIdx.x & 3;
+        const uint64_t out = static_cast<uint64_t>(blockIdx.x) * 64 + cc, at = (row0 + 32 * bb) / 2;
+        if (out < a.cols && at < a.pitch) *reinterpret_cast<uint4*>(a.codes + out * a.pitch + at) = s_codes[cc][bb];
+    }
+    if (b == 0)   // the grid covers whole tiles of 128 columns
+        *reinterpret_cast<uint32_t*>(a.scales + scale_at(col, 4 * static_cast<uint64_t>(blockIdx.y), a.tiles_k)) =
+            *reinterpret_cast<const uint32_t*>(s_scale[c]);
 }
 
-// Codes and scales back to 16 bits, 8 values a thread.
+// Codes and scales back to 16 bits.
 template <int DT>
 __global__ void __launch_bounds__(kThreads) k_mx4_values(const __grid_constant__ MxArgs a) {
     pdl_enter();
-    const uint64_t groups = (a.cols + 7) / 8, total = a.rows * groups;
-    for (uint64_t i = thread_id(); i < total; i += grid_threads()) {
-        const uint64_t row = i / groups, c = (i - row * groups) * 8;
-        const uint32_t q = __ldcs(reinterpret_cast<const uint32_t*>(a.codes + row * a.pitch + (c >> 1)));
-        const uint32_t byte = a.scales[scale_at(row, c >> 5, a.tiles_k)];
-        // 2^(byte - 127): the smallest is a subnormal number
-        const float scale = byte == 255u ? NAN : __uint_as_float(byte == 0u ? 0x00400000u : byte << 23);
-        uint32_t out[8];
+    const int lane = threadIdx.x & 31;
+    const uint64_t segments = (a.cols + 255) / 256;
+    const uint64_t units = (a.rows + kMxRows - 1) / kMxRows * segments;
+    for (uint64_t u = static_cast<uint64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); u < units;
+         u += static_cast<uint64_t>(gridDim.x) * (kThreads / 32)) {
+        const uint64_t group = u / segments, row0 = group * kMxRows, c = (u - group * segments) * 256 + 8 * lane;
+        const int valid = row_values(a.cols, c);
+        uint32_t q[kMxRows], byte[kMxRows];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            uint32_t h;
-            asm("{\n\t.reg .b8 b, x, y, z;\n\tmov.b32 {b, x, y, z}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}"
-                : "=r"(h)
-                : "r"(q >> (8 * e)));
-            out[2 * e] = narrow<DT>(__fmul_rn(widen<kFp16>(h & 0xFFFFu), scale));
-            out[2 * e + 1] = narrow<DT>(__fmul_rn(widen<kFp16>(h >> 16), scale));
+        for (int r = 0; r < kMxRows; ++r) {
+            q[r] = byte[r] = 0;
+            if (row0 + r < a.rows && valid > 0) {
+                q[r] = __ldg(reinterpret_cast<const uint32_t*>(a.codes + (row0 + r) * a.pitch + (c >> 1)));
+                byte[r] = __ldg(a.scales + scale_at(row0 + r, c >> 5, a.tiles_k));
+            }
         }
-        unsigned short* dst = static_cast<unsigned short*>(a.dst) + row * a.ld + c;
-        if (a.vec && c + 8 <= a.cols) {
-            __stcs(reinterpret_cast<uint4*>(dst), make_uint4(out[0] | out[1] << 16, out[2] | out[3] << 16,
-                                                             out[4] | out[5] << 16, out[6] | out[7] << 16));
-        } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (c + e < a.cols) __stcs(dst + e, static_cast<unsigned short>(out[e]));
+        for (int r = 0; r < kMxRows; ++r) {
+            if (row0 + r >= a.rows) break;
+            // 2^(byte - 127): the smallest is a subnormal number
+            const float scale = byte[r] == 255u ? NAN : __uint_as_float(byte[r] == 0u ? 0x00400000u : byte[r] << 23);
+            uint32_t out[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                uint32_t h;
+                asm("{\n\t.reg .b8 b, x, y, z;\n\tmov.b32 {b, x, y, z}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}"
+                    : "=r"(h)
+                    : "r"(q[r] >> (8 * e)));
+                const float lo = __fmul_rn(widen<kFp16>(h & 0xFFFFu), scale), hi = __fmul_rn(widen<kFp16>(h >> 16), scale);
+                out[e] = narrow<DT>(lo) | narrow<DT>(hi) << 16;
+            }
+            store8(static_cast<unsigned short*>(a.dst), static_cast<int64_t>((row0 + r) * a.ld + c), valid, out);
         }
     }
 }
@@ -429,14 +454,13 @@ int zero_mx4_quantize(int dtype, uint64_t rows, uint64_t cols, const void* src16
     a.rows = rows;
     a.cols = cols;
     a.ld = ld;
-    a.vec = aligned(src16, 16) && ld % 8 == 0;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (transpose) {
         a.pitch = mx_pitch(rows);
         a.tiles_k = up(rows, 128) / 128;
         if (a.tiles_k > 65535) return refuse(ZERO_EINVAL, "a transposed matrix has at most 65535 * 128 rows");
-        const dim3 grid(static_cast<unsigned>(up(cols, kThreads) / kThreads), static_cast<unsigned>(a.tiles_k));
+        const dim3 grid(static_cast<unsigned>(up(cols, 128) / 64), static_cast<unsigned>(a.tiles_k));
         e = dtype == ZERO_FP16 ? launch_pdl(k_mx4_columns<kFp16>, grid, kThreads, 0, 1, s, a)
                                : launch_pdl(k_mx4_columns<kBf16>, grid, kThreads, 0, 1, s, a);
     } else {
@@ -444,8 +468,8 @@ int zero_mx4_quantize(int dtype, uint64_t rows, uint64_t cols, const void* src16
         a.tiles_k = up(cols, 128) / 128;
         int sms = 0;
         if ((e = sm_count(&sms)) != cudaSuccess) return cuda_refuse(e, "zero_mx4_quantize");
-        const uint64_t units = up(rows, 128) * (up(cols, 256) / 256);
-        const dim3 grid(grid_of((units + 7) / 8, sms, 32));
+        const uint64_t units = up(rows, 128) / kMxRows * (up(cols, 256) / 256);
+        const dim3 grid(grid_of((units + 7) / 8, sms, 64));
         e = dtype == ZERO_FP16 ? launch_pdl(k_mx4_rows<kFp16>, grid, kThreads, 0, 1, s, a)
                                : launch_pdl(k_mx4_rows<kBf16>, grid, kThreads, 0, 1, s, a);
     }
@@ -469,12 +493,12 @@ int zero_mx4_dequantize(int dtype, uint64_t rows, uint64_t cols, const void* cod
     a.ld = ld;
     a.pitch = mx_pitch(cols);
     a.tiles_k = up(cols, 128) / 128;
-    a.vec = aligned(out16, 16) && ld % 8 == 0;
     int sms = 0;
     cudaError_t e = sm_count(&sms);
     if (e != cudaSuccess) return cuda_refuse(e, "zero_mx4_dequantize");
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const dim3 grid(grid_of((rows * ((cols + 7) / 8) + kThreads - 1) / kThreads, sms, 32));
+    const uint64_t units = up(rows, kMxRows) / kMxRows * (up(cols, 256) / 256);
+    const dim3 grid(grid_of((units + 7) / 8, sms, 64));
     e = dtype == ZERO_FP16 ? launch_pdl(k_mx4_values<kFp16>, grid, kThreads, 0, 1, s, a)
                            : launch_pdl(k_mx4_values<kBf16>, grid, kThreads, 0, 1, s, a);
     return e == cudaSuccess ? ZERO_OK : cuda_refuse(e, "zero_mx4_dequantize");

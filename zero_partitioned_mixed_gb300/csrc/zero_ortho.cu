@@ -31,6 +31,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "zero_gb300.h"
+#include "zero_rows.cuh"
 #include "zero_tc.cuh"
 
 namespace zg {
@@ -44,17 +45,16 @@ constexpr int kMaxPhases = 3 * ZERO_MAX_NS_STEPS + 3;
 constexpr float kScaleX = 8192.0f, kScaleA = 4096.0f, kScaleB = 128.0f;
 
 // ------------------------------------------------------- norm and packing
-// A matrix is read in units of one row's segment of kSegment columns, one
-// warp a unit: 8 loads of 8 values a lane in flight.
-constexpr int kSegment = 2048;
-constexpr int kPartials = 256;   // partial sums of squares of one matrix, at most
+// A matrix is read in units of kPackRows rows by 256 columns, one warp a
+// unit, 8 values a lane and row, the rows' loads in flight together.
+constexpr int kPackRows = 4;
+constexpr int kPartials = 1024;   // partial sums of squares of one matrix, at most
 constexpr int kPackWarps = kThreads / 32;
 
 struct PackArgs {
     const void* src[kMaxMatrices];
     uint64_t rows, cols, ld, pitch;
-    uint64_t segments, units;   // segments a row; units a matrix
-    int vec;                    // every row starts on 16 bytes
+    uint64_t segments, units;   // 256-column segments a row; units a matrix
     int partials;
     double* partial;            // [batch][kPartials]
     float* g0;                  // [batch]
@@ -62,31 +62,28 @@ struct PackArgs {
     __half* x0;                 // [batch][rows][pitch]
 };
 
-// A lane's values of unit `u`: vals[8 k + e] is column seg + 256 k + 8 lane + e.
+// A lane's values of unit `u`: row0 + r, columns c to c + 7; zeros past the matrix.
 template <int DT>
-__device__ __forceinline__ void load_unit(const PackArgs& a, int b, uint64_t u, uint64_t& row, uint64_t& col0,
-                                          float (&v)[64]) {
-    const int lane = threadIdx.x & 31;
-    row = u / a.segments;
-    col0 = (u - row * a.segments) * kSegment;
-    const unsigned short* src = static_cast<const unsigned short*>(a.src[b]) + row * a.ld;
+__device__ __forceinline__ void load_unit(const PackArgs& a, int b, uint64_t u, uint64_t& row0, uint64_t& c,
+                                          float (&v)[kPackRows][8]) {
+    row0 = u / a.segments;
+    c = (u - row0 * a.segments) * 256 + 8 * (threadIdx.x & 31);
+    row0 *= kPackRows;
+    const unsigned short* src = static_cast<const unsigned short*>(a.src[b]);
+    const int64_t total = static_cast<int64_t>((a.rows - 1) * a.ld + a.cols);
+    uint32_t w[kPackRows][4];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        const uint64_t c = col0 + 256 * k + 8 * lane;
-        if (a.vec && c + 8 <= a.cols) {
-            const uint4 x = __ldg(reinterpret_cast<const uint4*>(src + c));
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    for (int r = 0; r < kPackRows; ++r)
+        if (row0 + r < a.rows) load8(src, static_cast<int64_t>((row0 + r) * a.ld + c), total, w[r]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[8 * k + e] = widen<DT>((w[e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
-        } else {
+    for (int r = 0; r < kPackRows; ++r)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[8 * k + e] = c + e < a.cols ? widen<DT>(__ldg(src + c + e)) : 0.0f;
-        }
-    }
+        for (int e = 0; e < 8; ++e)
+            v[r][e] = row0 + r < a.rows && c + e < a.cols ? widen<DT>((w[r][e >> 1] >> (16 * (e & 1))) & 0xFFFFu) : 0.0f;
 }
 
-// Sum of squares: 64 values in fp32, everything above in fp64.  Values whose
-// squares could leave fp32's range are squared in fp64.
+// Sum of squares: the 32 values of a unit in fp32, everything above in fp64.
+// Values whose squares could leave fp32's range are squared in fp64.
 template <int DT>
 __global__ void __launch_bounds__(kThreads) k_ortho_norm(const __grid_constant__ PackArgs a) {
     pdl_enter();
@@ -96,22 +93,27 @@ __global__ void __launch_bounds__(kThreads) k_ortho_norm(const __grid_constant__
     double acc = 0.0;
     for (uint64_t u = static_cast<uint64_t>(blockIdx.x) * kPackWarps + (threadIdx.x >> 5); u < a.units;
          u += static_cast<uint64_t>(gridDim.x) * kPackWarps) {
-        uint64_t row, col0;
-        float v[64];
-        load_unit<DT>(a, b, u, row, col0, v);
-        float s = 0.0f, top = 0.0f;
+        uint64_t row0, c;
+        float v[kPackRows][8];
+        load_unit<DT>(a, b, u, row0, c, v);
+        float s[kPackRows] = {}, top = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 64; ++i) {
-            s = __fmaf_rn(v[i], v[i], s);
-            top = fmaxf(top, fabsf(v[i]));
-        }
-        if (!(s < INFINITY) || !(top < 0x1p60f) || (top > 0.0f && top < 0x1p-50f)) {
+        for (int r = 0; r < kPackRows; ++r)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                s[r] = __fmaf_rn(v[r][e], v[r][e], s[r]);
+                top = fmaxf(top, fabsf(v[r][e]));
+            }
+        const float sum = (s[0] + s[1]) + (s[2] + s[3]);
+        if (!(sum < INFINITY) || !(top < 0x1p60f) || (top > 0.0f && top < 0x1p-50f)) {
             double d = 0.0;
 #pragma unroll
-            for (int i = 0; i < 64; ++i) d = fma(static_cast<double>(v[i]), static_cast<double>(v[i]), d);
+            for (int r = 0; r < kPackRows; ++r)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) d = fma(static_cast<double>(v[r][e]), static_cast<double>(v[r][e]), d);
             acc += d;
         } else {
-            acc += static_cast<double>(s);
+            acc += static_cast<double>(sum);
         }
     }
     const double t = block_sum(acc);
@@ -126,9 +128,9 @@ __global__ void __launch_bounds__(kThreads) k_ortho_pack(const __grid_constant__
     pdl_enter();
     __shared__ float s_mul[2];
     const int b = blockIdx.y;
-    const double t = block_sum(static_cast<int>(threadIdx.x) < a.partials
-                                   ? a.partial[static_cast<uint64_t>(b) * kPartials + threadIdx.x]
-                                   : 0.0);
+    double part = 0.0;
+    for (int i = threadIdx.x; i < a.partials; i += kThreads) part += a.partial[static_cast<uint64_t>(b) * kPartials + i];
+    const double t = block_sum(part);
     if (threadIdx.x == 0) {
         const double norm = sqrt(t);
         int e = 0;
@@ -149,20 +151,19 @@ __global__ void __launch_bounds__(kThreads) k_ortho_pack(const __grid_constant__
     const float m0 = s_mul[0], m1 = s_mul[1];
     for (uint64_t u = static_cast<uint64_t>(blockIdx.x) * kPackWarps + (threadIdx.x >> 5); u < a.units;
          u += static_cast<uint64_t>(gridDim.x) * kPackWarps) {
-        uint64_t row, col0;
-        float v[64];
-        load_unit<DT>(a, b, u, row, col0, v);
-        __half* out = a.x0 + (static_cast<uint64_t>(b) * a.rows + row) * a.pitch;
+        uint64_t row0, c;
+        float v[kPackRows][8];
+        load_unit<DT>(a, b, u, row0, c, v);
+        if (c >= a.cols) continue;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const uint64_t c = col0 + 256 * k + 8 * (threadIdx.x & 31);
-            if (c < a.cols) {   // the row's padding up to 8 columns is written as zeros
-                uint32_t q[4];
+        for (int r = 0; r < kPackRows; ++r) {
+            if (row0 + r >= a.rows) break;
+            uint32_t q[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    q[e] = pack_half2(v[8 * k + 2 * e] * m0 * m1, v[8 * k + 2 * e + 1] * m0 * m1);
-                *reinterpret_cast<uint4*>(out + c) = make_uint4(q[0], q[1], q[2], q[3]);
-            }
+            for (int e = 0; e < 4; ++e) q[e] = pack_half2(v[r][2 * e] * m0 * m1, v[r][2 * e + 1] * m0 * m1);
+            // whole eights: the pitch is a multiple of 8
+            *reinterpret_cast<uint4*>(a.x0 + (static_cast<uint64_t>(b) * a.rows + row0 + r) * a.pitch + c) =
+                make_uint4(q[0], q[1], q[2], q[3]);
         }
     }
 }
@@ -666,14 +667,12 @@ int zero_orthogonalize(int dtype, int batch, uint64_t rows, uint64_t cols, const
     PackArgs q = {};
     ProductArgs p;   // its maps and phases are filled below
     std::memset(&p, 0, sizeof(p));
-    q.vec = ld_src % 8 == 0;
     p.dst_vec = ld_dst % 8 == 0;
     for (int i = 0; i < batch; ++i) {
         if (!src[i] || !aligned(src[i], 2)) return refuse(ZERO_EINVAL, "src[i] is NULL or not 2-byte aligned");
         if (!dst[i] || !aligned(dst[i], 2)) return refuse(ZERO_EINVAL, "dst[i] is NULL or not 2-byte aligned");
         q.src[i] = src[i];
         p.dst[i] = dst[i];
-        q.vec &= aligned(src[i], 16);
         p.dst_vec &= aligned(dst[i], 16);
     }
     p.dst_ld = ld_dst;
@@ -681,8 +680,8 @@ int zero_orthogonalize(int dtype, int batch, uint64_t rows, uint64_t cols, const
     q.cols = cols;
     q.ld = ld_src;
     q.pitch = xp;
-    q.segments = (cols + kSegment - 1) / kSegment;
-    q.units = rows * q.segments;
+    q.segments = (cols + 255) / 256;
+    q.units = (rows + kPackRows - 1) / kPackRows * q.segments;
     q.partial = reinterpret_cast<double*>(ws + z.partial);
     q.g0 = reinterpret_cast<float*>(ws + z.g0);
     q.done = reinterpret_cast<uint32_t*>(ws + z.done);
