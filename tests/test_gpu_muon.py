@@ -43,7 +43,8 @@ def ortho(src, **kw):
 
 SIZES = [(1, 1), (1, 40), (40, 1), (3, 5), (8, 8), (16, 16), (31, 33), (64, 64), (65, 63), (96, 160), (127, 128),
          (128, 129), (129, 127), (200, 2049), (2049, 200), (256, 256), (255, 511), (384, 640), (700, 300), (513, 1030),
-         (1030, 513), (1024, 1024)]
+         (1030, 513), (1024, 1024), (128, 512), (128, 513), (513, 128), (20, 4096), (4096, 100), (128, 4097), (4100, 77),
+         (1, 3000), (129, 4096), (257, 256)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])

@@ -53,8 +53,7 @@ __device__ __forceinline__ uint32_t scale_byte(float top) {
 __device__ __forceinline__ float scale_inverse(uint32_t byte) {
     return byte == 255u ? 0.0f : __uint_as_float((254u - byte) << 23);
 }
-// 8 values as codes, the first in the lowest 4 bits.  A NaN block's values
-// must be given as zeros.
+// 8 values as codes, the first in the lowest 4 bits.
 __device__ __forceinline__ uint32_t codes8(const float (&x)[8]) {
     uint32_t r;
     asm("{\n\t.reg .b8 a, b, c, d;\n\t"
@@ -67,151 +66,216 @@ __device__ __forceinline__ uint32_t codes8(const float (&x)[8]) {
         : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
     return r;
 }
-// Largest magnitude, by its bits: NaN above infinity above every number.
-__device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 
-// A warp's work in the two row kernels: kMxRows rows by 256 columns, 8 a
-// lane, all rows' loads in flight together.
+// The row kernels: a warp takes kMxRows rows by 256 columns, 8 a lane, all
+// rows' loads in flight together.  They are bound by the instructions they
+// issue as much as by HBM, so a piece that lies inside the matrix and starts
+// on 16 bytes takes a path without any of the edges' cases (`INSIDE`).
 constexpr int kMxRows = 4;
 
-__device__ __forceinline__ int row_values(uint64_t cols, uint64_t c) {   // left of the row from column c on, within +-8
-    const int64_t left = static_cast<int64_t>(cols) - static_cast<int64_t>(c);
-    return left > 8 ? 8 : left < -8 ? -8 : static_cast<int>(left);
+__device__ __forceinline__ bool all_inside(const MxArgs& a, const void* p16, uint64_t row0, uint64_t segment) {
+    return row0 + kMxRows <= a.rows && (segment + 1) * 256 <= a.cols && (a.ld & 7) == 0 &&
+           (reinterpret_cast<uintptr_t>(p16) & 15) == 0;
 }
 
-// Along the rows.  Four lanes share a block; rows and columns that only fill
-// the last scale tiles are walked too, for their zeros.
-template <int DT>
-__global__ void __launch_bounds__(kThreads) k_mx4_rows(const __grid_constant__ MxArgs a) {
-    pdl_enter();
+template <int DT, bool INSIDE>
+__device__ __forceinline__ void rows_piece(const MxArgs& a, uint64_t row0, uint64_t segment) {
     const int lane = threadIdx.x & 31;
-    const uint64_t segments = (a.tiles_k + 1) / 2;
-    const uint64_t units = (a.rows + 127) / 128 * (128 / kMxRows) * segments;
+    const uint64_t c = segment * 256 + 8 * lane;
     const unsigned short* src = static_cast<const unsigned short*>(a.src);
-    const int64_t total = static_cast<int64_t>((a.rows - 1) * a.ld + a.cols);
-    for (uint64_t u = static_cast<uint64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); u < units;
-         u += static_cast<uint64_t>(gridDim.x) * (kThreads / 32)) {
-        const uint64_t group = u / segments, row0 = group * kMxRows, c = (u - group * segments) * 256 + 8 * lane;
-        const int valid = row_values(a.cols, c);
-        uint32_t raw[kMxRows][4];
+    const int valid = INSIDE ? 8 : values_left(a.cols, c);
+    uint32_t raw[kMxRows][4];
+    if (INSIDE) {
+        const unsigned short* at = src + row0 * a.ld + c;
+#pragma unroll
+        for (int r = 0; r < kMxRows; ++r, at += a.ld) {
+            const uint4 x = __ldcs(reinterpret_cast<const uint4*>(at));
+            raw[r][0] = x.x; raw[r][1] = x.y; raw[r][2] = x.z; raw[r][3] = x.w;
+        }
+    } else {
+        const int64_t total = static_cast<int64_t>((a.rows - 1) * a.ld + a.cols);
 #pragma unroll
         for (int r = 0; r < kMxRows; ++r) {
             if (row0 + r < a.rows) {
                 load8(src, static_cast<int64_t>((row0 + r) * a.ld + c), total, raw[r]);
+                clear_from(raw[r], valid);
             } else {
                 raw[r][0] = raw[r][1] = raw[r][2] = raw[r][3] = 0;
             }
         }
+    }
+    uint8_t* codes = a.codes + row0 * a.pitch + (c >> 1);
+    // kMxRows rows of a scale tile follow each other at 16 bytes
+    uint8_t* scales = a.scales + scale_at(row0, c >> 5, a.tiles_k);
 #pragma unroll
-        for (int r = 0; r < kMxRows; ++r) {
-            float v[8];
-            uint32_t top = 0;
+    for (int r = 0; r < kMxRows; ++r, codes += a.pitch) {
+        uint32_t top = top_pattern(raw[r]);
+        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));   // four lanes share a block
+        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+        const uint32_t byte = scale_byte(widen<DT>(top));
+        const float inv = scale_inverse(byte);
+        float v[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                v[e] = e < valid ? widen<DT>((raw[r][e >> 1] >> (16 * (e & 1))) & 0xFFFFu) : 0.0f;
-                top = max(top, magnitude(v[e]));
-            }
-            top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-            top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-            const uint32_t byte = scale_byte(__uint_as_float(top));
-            const float inv = scale_inverse(byte);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = byte == 255u ? 0.0f : __fmul_rn(v[e], inv);
-            const uint32_t q = codes8(v);
-            const uint64_t row = row0 + r;
-            if (row < a.rows && (c >> 1) < a.pitch) __stcs(reinterpret_cast<uint32_t*>(a.codes + row * a.pitch + (c >> 1)), q);
-            // the four blocks of a scale tile's row in one word
-            uint32_t word = byte;
-            word |= __shfl_down_sync(0xFFFFFFFFu, byte, 4) << 8;
-            word |= __shfl_down_sync(0xFFFFFFFFu, byte, 8) << 16;
-            word |= __shfl_down_sync(0xFFFFFFFFu, byte, 12) << 24;
-            if ((lane & 15) == 0 && (c >> 7) < a.tiles_k)
-                *reinterpret_cast<uint32_t*>(a.scales + scale_at(row, c >> 5, a.tiles_k)) = word;
+        for (int e = 0; e < 4; ++e) {
+            widen2<DT>(raw[r][e], v[2 * e], v[2 * e + 1]);
+            mul2(v[2 * e], v[2 * e + 1], inv);
         }
+        const uint32_t q = byte == 255u ? 0u : codes8(v);
+        if (INSIDE || (row0 + r < a.rows && (c >> 1) < a.pitch)) __stcs(reinterpret_cast<uint32_t*>(codes), q);
+        // the four blocks of a scale tile's row in one word
+        uint32_t word = byte | __shfl_down_sync(0xFFFFFFFFu, byte, 4) << 8;
+        word |= __shfl_down_sync(0xFFFFFFFFu, word, 8) << 16;
+        if ((lane & 15) == 0 && (INSIDE || (c >> 7) < a.tiles_k)) *reinterpret_cast<uint32_t*>(scales + 16 * r) = word;
+    }
+}
+
+// Along the rows; those that only fill the last scale tiles are walked too,
+// for their zeros.
+template <int DT>
+__global__ void __launch_bounds__(kThreads) k_mx4_rows(const __grid_constant__ MxArgs a) {
+    pdl_enter();
+    const uint64_t row0 = (static_cast<uint64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5)) * kMxRows;
+    for (uint64_t segment = blockIdx.y; segment < (a.tiles_k + 1) / 2; segment += gridDim.y) {
+        if (all_inside(a, a.src, row0, segment)) rows_piece<DT, true>(a, row0, segment);
+        else rows_piece<DT, false>(a, row0, segment);
     }
 }
 
 // Along the columns: the codes are those of the transpose.  A block takes
-// 128 rows (a scale tile's four blocks) of 64 columns, a thread 32 values of
-// one column; the codes go through shared memory so that a row of them
-// leaves as 64 neighbouring bytes.
+// 128 rows (a scale tile's four blocks) of 128 columns, a thread 32 values
+// of two neighbouring columns; the codes go through shared memory so that a
+// row of them leaves as 64 neighbouring bytes.
 template <int DT>
-__global__ void __launch_bounds__(kThreads) k_mx4_columns(const __grid_constant__ MxArgs a) {
+__global__ void __launch_bounds__(kThreads, 5) k_mx4_columns(const __grid_constant__ MxArgs a) {
     pdl_enter();
-    __shared__ __align__(16) uint4 s_codes[64][5];   // 5: no two columns of a warp in the same banks
-    __shared__ uint8_t s_scale[64][4];
-    const int c = threadIdx.x & 63, b = threadIdx.x >> 6;
-    const uint64_t col = static_cast<uint64_t>(blockIdx.x) * 64 + c, row0 = static_cast<uint64_t>(blockIdx.y) * 128;
-    const unsigned short* src = static_cast<const unsigned short*>(a.src) + col;
-    uint32_t raw[32];
+    __shared__ __align__(16) uint4 s_codes[128][5];   // 5: neighbouring columns start in other banks
+    __shared__ uint8_t s_scale[128][4];
+    const int lane = threadIdx.x & 31, b = (threadIdx.x >> 5) & 3;
+    const int c = (threadIdx.x >> 7) * 64 + 2 * lane;
+    const uint64_t col0 = static_cast<uint64_t>(blockIdx.x) * 128, row0 = static_cast<uint64_t>(blockIdx.y) * 128;
+    const unsigned short* src = static_cast<const unsigned short*>(a.src) + (row0 + 32 * b) * a.ld + col0 + c;
+    const bool inside = row0 + 128 <= a.rows && col0 + 128 <= a.cols;
+    uint32_t raw[32];   // a row's two values each
+    if (inside && (a.ld & 1) == 0 && (reinterpret_cast<uintptr_t>(a.src) & 3) == 0) {
 #pragma unroll
-    for (int e = 0; e < 32; ++e) {
-        const uint64_t r = row0 + 32 * b + e;
-        raw[e] = r < a.rows && col < a.cols ? __ldg(src + r * a.ld) : 0u;
+        for (int e = 0; e < 32; ++e, src += a.ld) raw[e] = __ldg(reinterpret_cast<const uint32_t*>(src));
+    } else if (inside) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e, src += a.ld)
+            raw[e] = static_cast<uint32_t>(__ldg(src)) | static_cast<uint32_t>(__ldg(src + 1)) << 16;
+    } else {
+        const uint64_t r0 = row0 + 32 * b;
+        const int rows = r0 >= a.rows ? 0 : a.rows - r0 < 32 ? static_cast<int>(a.rows - r0) : 32;
+        const int cols = col0 + c >= a.cols ? 0 : a.cols - col0 - c < 2 ? 1 : 2;
+#pragma unroll
+        for (int e = 0; e < 32; ++e, src += a.ld) {
+            raw[e] = 0;
+            if (e < rows && cols > 0) raw[e] = __ldg(src);
+            if (e < rows && cols > 1) raw[e] |= static_cast<uint32_t>(__ldg(src + 1)) << 16;
+        }
     }
-    uint32_t top = 0;
+    uint32_t tops = 0;
 #pragma unroll
-    for (int e = 0; e < 32; ++e) top = max(top, raw[e] & 0x7FFFu);   // the 16-bit patterns are ordered like the values
-    const uint32_t byte = scale_byte(widen<DT>(top));
-    const float inv = scale_inverse(byte);
-    uint32_t q[4];
+    for (int e = 0; e < 32; ++e) tops = __vmaxu2(tops, raw[e] & 0x7FFF7FFFu);
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-        float x[8];
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t byte = scale_byte(widen<DT>((tops >> (16 * h)) & 0xFFFFu));
+        const float inv = scale_inverse(byte);
+        uint32_t q[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = byte == 255u ? 0.0f : __fmul_rn(widen<DT>(raw[8 * g + e]), inv);
-        q[g] = codes8(x);
+        for (int g = 0; g < 4; ++g) {
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+                x[e] = widen<DT>((raw[8 * g + e] >> (16 * h)) & 0xFFFFu);
+                x[e + 1] = widen<DT>((raw[8 * g + e + 1] >> (16 * h)) & 0xFFFFu);
+                mul2(x[e], x[e + 1], inv);
+            }
+            q[g] = byte == 255u ? 0u : codes8(x);
+        }
+        s_codes[c + h][b] = make_uint4(q[0], q[1], q[2], q[3]);
+        s_scale[c + h][b] = static_cast<uint8_t>(byte);
     }
-    s_codes[c][b] = make_uint4(q[0], q[1], q[2], q[3]);
-    s_scale[c][b] = static_cast<uint8_t>(byte);
     __syncthreads();
-    {
-        const int cc = threadIdx.x >> 2, bb = threadIdx.x & 3;
-        const uint64_t out = static_cast<uint64_t>(blockIdx.x) * 64 + cc, at = (row0 + 32 * bb) / 2;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int cc = (threadIdx.x >> 2) + 64 * k, bb = threadIdx.x & 3;
+        const uint64_t out = col0 + cc, at = (row0 + 32 * bb) / 2;
         if (out < a.cols && at < a.pitch) *reinterpret_cast<uint4*>(a.codes + out * a.pitch + at) = s_codes[cc][bb];
     }
-    if (b == 0)   // the grid covers whole tiles of 128 columns
-        *reinterpret_cast<uint32_t*>(a.scales + scale_at(col, 4 * static_cast<uint64_t>(blockIdx.y), a.tiles_k)) =
-            *reinterpret_cast<const uint32_t*>(s_scale[c]);
+    if (threadIdx.x < 128)   // the grid covers whole scale tiles
+        *reinterpret_cast<uint32_t*>(a.scales + scale_at(col0 + threadIdx.x, 4 * static_cast<uint64_t>(blockIdx.y), a.tiles_k)) =
+            *reinterpret_cast<const uint32_t*>(s_scale[threadIdx.x]);
+}
+
+// 8 codes of a block with scale byte `byte` as 16-bit values.
+template <int DT>
+__device__ __forceinline__ void decode8(uint32_t q, uint32_t byte, uint32_t (&out)[4]) {
+    // 2^(byte - 127): the smallest is a subnormal number
+    const float scale = byte == 255u ? NAN : __uint_as_float(byte == 0u ? 0x00400000u : byte << 23);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        uint32_t h;
+        asm("{\n\t.reg .b8 b, x, y, z;\n\tmov.b32 {b, x, y, z}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}"
+            : "=r"(h)
+            : "r"(q >> (8 * e)));
+        float lo, hi;
+        widen2<kFp16>(h, lo, hi);
+        mul2(lo, hi, scale);
+        out[e] = narrow2<DT>(lo, hi);
+    }
+}
+
+template <int DT, bool INSIDE>
+__device__ __forceinline__ void values_piece(const MxArgs& a, uint64_t row0, uint64_t segment) {
+    const uint64_t c = segment * 256 + 8 * (threadIdx.x & 31);
+    const int valid = INSIDE ? 8 : values_left(a.cols, c);
+    const uint8_t* codes = a.codes + row0 * a.pitch + (c >> 1);
+    const uint8_t* scales = a.scales + scale_at(row0, c >> 5, a.tiles_k);
+    uint32_t q[kMxRows], byte[kMxRows];
+#pragma unroll
+    for (int r = 0; r < kMxRows; ++r, codes += a.pitch) {
+        q[r] = byte[r] = 0;
+        if (INSIDE || (row0 + r < a.rows && valid > 0)) {
+            q[r] = __ldcs(reinterpret_cast<const uint32_t*>(codes));
+            byte[r] = __ldg(scales + 16 * r);
+        }
+    }
+    if (INSIDE) {
+        unsigned short* dst = static_cast<unsigned short*>(a.dst) + row0 * a.ld + c;
+#pragma unroll
+        for (int r = 0; r < kMxRows; ++r, dst += a.ld) {
+            uint32_t out[4];
+            decode8<DT>(q[r], byte[r], out);
+            __stcs(reinterpret_cast<uint4*>(dst), make_uint4(out[0], out[1], out[2], out[3]));
+        }
+    } else {
+        // a loop: unrolled, the stores' cases would take a hundred registers
+        int64_t at = static_cast<int64_t>(row0 * a.ld + c);
+#pragma unroll 1
+        for (int r = 0; r < kMxRows; ++r, at += static_cast<int64_t>(a.ld)) {
+            if (row0 + r >= a.rows) break;
+            uint32_t out[4];
+            decode8<DT>(q[0], byte[0], out);
+            store8(static_cast<unsigned short*>(a.dst), at, valid, out);
+#pragma unroll
+            for (int i = 0; i + 1 < kMxRows; ++i) {
+                q[i] = q[i + 1];
+                byte[i] = byte[i + 1];
+            }
+        }
+    }
 }
 
 // Codes and scales back to 16 bits.
 template <int DT>
 __global__ void __launch_bounds__(kThreads) k_mx4_values(const __grid_constant__ MxArgs a) {
     pdl_enter();
-    const int lane = threadIdx.x & 31;
-    const uint64_t segments = (a.cols + 255) / 256;
-    const uint64_t units = (a.rows + kMxRows - 1) / kMxRows * segments;
-    for (uint64_t u = static_cast<uint64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); u < units;
-         u += static_cast<uint64_t>(gridDim.x) * (kThreads / 32)) {
-        const uint64_t group = u / segments, row0 = group * kMxRows, c = (u - group * segments) * 256 + 8 * lane;
-        const int valid = row_values(a.cols, c);
-        uint32_t q[kMxRows], byte[kMxRows];
-#pragma unroll
-        for (int r = 0; r < kMxRows; ++r) {
-            q[r] = byte[r] = 0;
-            if (row0 + r < a.rows && valid > 0) {
-                q[r] = __ldg(reinterpret_cast<const uint32_t*>(a.codes + (row0 + r) * a.pitch + (c >> 1)));
-                byte[r] = __ldg(a.scales + scale_at(row0 + r, c >> 5, a.tiles_k));
-            }
-        }
-#pragma unroll
-        for (int r = 0; r < kMxRows; ++r) {
-            if (row0 + r >= a.rows) break;
-            // 2^(byte - 127): the smallest is a subnormal number
-            const float scale = byte[r] == 255u ? NAN : __uint_as_float(byte[r] == 0u ? 0x00400000u : byte[r] << 23);
-            uint32_t out[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                uint32_t h;
-                asm("{\n\t.reg .b8 b, x, y, z;\n\tmov.b32 {b, x, y, z}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}"
-                    : "=r"(h)
-                    : "r"(q[r] >> (8 * e)));
-                const float lo = __fmul_rn(widen<kFp16>(h & 0xFFFFu), scale), hi = __fmul_rn(widen<kFp16>(h >> 16), scale);
-                out[e] = narrow<DT>(lo) | narrow<DT>(hi) << 16;
-            }
-            store8(static_cast<unsigned short*>(a.dst), static_cast<int64_t>((row0 + r) * a.ld + c), valid, out);
-        }
+    const uint64_t row0 = (static_cast<uint64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5)) * kMxRows;
+    if (row0 >= a.rows) return;
+    for (uint64_t segment = blockIdx.y; segment < (a.cols + 255) / 256; segment += gridDim.y) {
+        if (all_inside(a, a.dst, row0, segment)) values_piece<DT, true>(a, row0, segment);
+        else values_piece<DT, false>(a, row0, segment);
     }
 }
 
@@ -375,8 +439,7 @@ k_mx4_product(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
                         uint32_t q[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            q[e] = DT == kFp16 ? pack_half2(v[8 * g + 2 * e], v[8 * g + 2 * e + 1])
-                                               : pack_bf2(v[8 * g + 2 * e], v[8 * g + 2 * e + 1]);
+                            q[e] = narrow2<DT>(v[8 * g + 2 * e], v[8 * g + 2 * e + 1]);
                         const uint32_t c = col + 8 * g;
                         if (p.vec && c + 8 <= p.n) {
                             *reinterpret_cast<uint4*>(out + c) = make_uint4(q[0], q[1], q[2], q[3]);
@@ -413,6 +476,12 @@ int mx_check(int dtype, uint64_t rows, uint64_t cols, const void* codes, const v
     if (!codes || !aligned(codes, 16)) return refuse(ZERO_EINVAL, "codes is NULL or not 16-byte aligned");
     if (!scales || !aligned(scales, 16)) return refuse(ZERO_EINVAL, "scales is NULL or not 16-byte aligned");
     return ZERO_OK;
+}
+
+// Grid of the row kernels: blocks of 8 warps down the rows, segments across.
+dim3 row_grid(uint64_t rows, uint64_t cols) {
+    const uint64_t per = static_cast<uint64_t>(kThreads / 32) * kMxRows, segments = up(cols, 256) / 256;
+    return dim3(static_cast<unsigned>(up(rows, per) / per), static_cast<unsigned>(segments < 65535 ? segments : 65535));
 }
 
 unsigned grid_of(uint64_t blocks, int sms, int per_sm) {
@@ -460,16 +529,13 @@ int zero_mx4_quantize(int dtype, uint64_t rows, uint64_t cols, const void* src16
         a.pitch = mx_pitch(rows);
         a.tiles_k = up(rows, 128) / 128;
         if (a.tiles_k > 65535) return refuse(ZERO_EINVAL, "a transposed matrix has at most 65535 * 128 rows");
-        const dim3 grid(static_cast<unsigned>(up(cols, 128) / 64), static_cast<unsigned>(a.tiles_k));
+        const dim3 grid(static_cast<unsigned>(up(cols, 128) / 128), static_cast<unsigned>(a.tiles_k));
         e = dtype == ZERO_FP16 ? launch_pdl(k_mx4_columns<kFp16>, grid, kThreads, 0, 1, s, a)
                                : launch_pdl(k_mx4_columns<kBf16>, grid, kThreads, 0, 1, s, a);
     } else {
         a.pitch = mx_pitch(cols);
         a.tiles_k = up(cols, 128) / 128;
-        int sms = 0;
-        if ((e = sm_count(&sms)) != cudaSuccess) return cuda_refuse(e, "zero_mx4_quantize");
-        const uint64_t units = up(rows, 128) / kMxRows * (up(cols, 256) / 256);
-        const dim3 grid(grid_of((units + 7) / 8, sms, 64));
+        const dim3 grid = row_grid(up(rows, 128), cols);
         e = dtype == ZERO_FP16 ? launch_pdl(k_mx4_rows<kFp16>, grid, kThreads, 0, 1, s, a)
                                : launch_pdl(k_mx4_rows<kBf16>, grid, kThreads, 0, 1, s, a);
     }
@@ -493,13 +559,9 @@ int zero_mx4_dequantize(int dtype, uint64_t rows, uint64_t cols, const void* cod
     a.ld = ld;
     a.pitch = mx_pitch(cols);
     a.tiles_k = up(cols, 128) / 128;
-    int sms = 0;
-    cudaError_t e = sm_count(&sms);
-    if (e != cudaSuccess) return cuda_refuse(e, "zero_mx4_dequantize");
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const uint64_t units = up(rows, kMxRows) / kMxRows * (up(cols, 256) / 256);
-    const dim3 grid(grid_of((units + 7) / 8, sms, 64));
-    e = dtype == ZERO_FP16 ? launch_pdl(k_mx4_values<kFp16>, grid, kThreads, 0, 1, s, a)
+    const dim3 grid = row_grid(rows, cols);
+    const cudaError_t e = dtype == ZERO_FP16 ? launch_pdl(k_mx4_values<kFp16>, grid, kThreads, 0, 1, s, a)
                            : launch_pdl(k_mx4_values<kBf16>, grid, kThreads, 0, 1, s, a);
     return e == cudaSuccess ? ZERO_OK : cuda_refuse(e, "zero_mx4_dequantize");
 }

@@ -54,7 +54,7 @@ constexpr int kPackWarps = kThreads / 32;
 struct PackArgs {
     const void* src[kMaxMatrices];
     uint64_t rows, cols, ld, pitch;
-    uint64_t segments, units;   // 256-column segments a row; units a matrix
+    uint32_t segments, units;   // 256-column segments a row; units a matrix
     int partials;
     double* partial;            // [batch][kPartials]
     float* g0;                  // [batch]
@@ -62,24 +62,23 @@ struct PackArgs {
     __half* x0;                 // [batch][rows][pitch]
 };
 
-// A lane's values of unit `u`: row0 + r, columns c to c + 7; zeros past the matrix.
-template <int DT>
-__device__ __forceinline__ void load_unit(const PackArgs& a, int b, uint64_t u, uint64_t& row0, uint64_t& c,
-                                          float (&v)[kPackRows][8]) {
-    row0 = u / a.segments;
-    c = (u - row0 * a.segments) * 256 + 8 * (threadIdx.x & 31);
-    row0 *= kPackRows;
+// A lane's values of unit `u`: row0 + r, columns c to c + 7, packed; zeros
+// past the matrix.
+__device__ __forceinline__ void load_unit(const PackArgs& a, int b, uint32_t u, uint64_t& row0, uint64_t& c,
+                                          uint32_t (&w)[kPackRows][4]) {
+    const uint32_t group = u / a.segments;
+    c = (u - group * a.segments) * 256u + 8 * (threadIdx.x & 31);
+    row0 = static_cast<uint64_t>(group) * kPackRows;
     const unsigned short* src = static_cast<const unsigned short*>(a.src[b]);
     const int64_t total = static_cast<int64_t>((a.rows - 1) * a.ld + a.cols);
-    uint32_t w[kPackRows][4];
 #pragma unroll
-    for (int r = 0; r < kPackRows; ++r)
+    for (int r = 0; r < kPackRows; ++r) {
         if (row0 + r < a.rows) load8(src, static_cast<int64_t>((row0 + r) * a.ld + c), total, w[r]);
+        else w[r][0] = w[r][1] = w[r][2] = w[r][3] = 0;
+    }
+    const int valid = values_left(a.cols, c);
 #pragma unroll
-    for (int r = 0; r < kPackRows; ++r)
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            v[r][e] = row0 + r < a.rows && c + e < a.cols ? widen<DT>((w[r][e >> 1] >> (16 * (e & 1))) & 0xFFFFu) : 0.0f;
+    for (int r = 0; r < kPackRows; ++r) clear_from(w[r], valid);
 }
 
 // Sum of squares: the 32 values of a unit in fp32, everything above in fp64.
@@ -91,26 +90,33 @@ __global__ void __launch_bounds__(kThreads) k_ortho_norm(const __grid_constant__
     if (blockIdx.x == 0)
         for (int i = threadIdx.x; i < kMaxPhases; i += kThreads) a.done[static_cast<uint64_t>(b) * kMaxPhases + i] = 0u;
     double acc = 0.0;
-    for (uint64_t u = static_cast<uint64_t>(blockIdx.x) * kPackWarps + (threadIdx.x >> 5); u < a.units;
-         u += static_cast<uint64_t>(gridDim.x) * kPackWarps) {
+    for (uint32_t u = blockIdx.x * kPackWarps + (threadIdx.x >> 5); u < a.units; u += gridDim.x * kPackWarps) {
         uint64_t row0, c;
-        float v[kPackRows][8];
-        load_unit<DT>(a, b, u, row0, c, v);
-        float s[kPackRows] = {}, top = 0.0f;
+        uint32_t w[kPackRows][4];
+        load_unit(a, b, u, row0, c, w);
+        float sum = 0.0f;
+        uint32_t top = 0;
 #pragma unroll
-        for (int r = 0; r < kPackRows; ++r)
+        for (int r = 0; r < kPackRows; ++r) {
+            float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                s[r] = __fmaf_rn(v[r][e], v[r][e], s[r]);
-                top = fmaxf(top, fabsf(v[r][e]));
+            for (int e = 0; e < 4; ++e) {
+                float lo, hi;
+                widen2<DT>(w[r][e], lo, hi);
+                s0 = __fmaf_rn(lo, lo, s0);
+                s1 = __fmaf_rn(hi, hi, s1);
             }
-        const float sum = (s[0] + s[1]) + (s[2] + s[3]);
-        if (!(sum < INFINITY) || !(top < 0x1p60f) || (top > 0.0f && top < 0x1p-50f)) {
+            sum += s0 + s1;
+            top = max(top, top_pattern(w[r]));
+        }
+        const float most = widen<DT>(top);
+        if (!(most < 0x1p60f) || (most > 0.0f && most < 0x1p-50f)) {
             double d = 0.0;
 #pragma unroll
-            for (int r = 0; r < kPackRows; ++r)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) d = fma(static_cast<double>(v[r][e]), static_cast<double>(v[r][e]), d);
+            for (int i = 0; i < kPackRows * 8; ++i) {
+                const double x = static_cast<double>(widen<DT>((w[i >> 3][(i >> 1) & 3] >> (16 * (i & 1))) & 0xFFFFu));
+                d = fma(x, x, d);
+            }
             acc += d;
         } else {
             acc += static_cast<double>(sum);
@@ -120,51 +126,61 @@ __global__ void __launch_bounds__(kThreads) k_ortho_norm(const __grid_constant__
     if (threadIdx.x == 0) a.partial[static_cast<uint64_t>(b) * kPartials + blockIdx.x] = t;
 }
 
-// X0 = G 2^k in fp16, k such that ||G|| 2^k lies in [2^12, 2^13), and g0 =
-// 1 / (||G|| 2^k), which the products that read X0 take into their scale.
-// A zero matrix gives g0 = 0; infinities and NaN give a NaN g0.
+// From ||G||: 2^k as two factors (each a normal fp32 number), k such that
+// ||G|| 2^k lies in [2^12, 2^13), and g0 = 1 / (||G|| 2^k).  A zero matrix
+// gives g0 = 0; infinities and NaN give a NaN g0.
+__device__ void norm_factors(double norm, float& m0, float& m1, float& g0) {
+    int e = 0;
+    g0 = 0.0f;
+    if (norm > 0.0 && norm < INFINITY) {
+        frexp(norm, &e);   // norm = f 2^e, f in [1/2, 1)
+        e = 13 - e;
+        g0 = static_cast<float>(1.0 / ldexp(norm, e));
+    } else if (!(norm == 0.0)) {
+        g0 = NAN;
+    }
+    m0 = ldexpf(1.0f, e / 2);
+    m1 = ldexpf(1.0f, e - e / 2);
+}
+
+// X0 = G 2^k in fp16, and g0, which the products that read X0 take into
+// their scale.
+// One unit a warp, its loads in flight while the norm is put together.
 template <int DT>
 __global__ void __launch_bounds__(kThreads) k_ortho_pack(const __grid_constant__ PackArgs a) {
     pdl_enter();
     __shared__ float s_mul[2];
     const int b = blockIdx.y;
+    const uint32_t u = blockIdx.x * kPackWarps + (threadIdx.x >> 5);
+    uint64_t row0 = a.rows, c = a.cols;
+    uint32_t w[kPackRows][4] = {};
+    if (u < a.units) load_unit(a, b, u, row0, c, w);
     double part = 0.0;
     for (int i = threadIdx.x; i < a.partials; i += kThreads) part += a.partial[static_cast<uint64_t>(b) * kPartials + i];
     const double t = block_sum(part);
     if (threadIdx.x == 0) {
-        const double norm = sqrt(t);
-        int e = 0;
-        float g = 0.0f;
-        if (norm > 0.0 && norm < INFINITY) {
-            frexp(norm, &e);   // norm = f 2^e, f in [1/2, 1)
-            e = 13 - e;
-            g = static_cast<float>(1.0 / ldexp(norm, e));
-        } else if (!(norm == 0.0)) {
-            g = NAN;
-        }
-        // 2^e as two factors, each a normal fp32 number
-        s_mul[0] = ldexpf(1.0f, e / 2);
-        s_mul[1] = ldexpf(1.0f, e - e / 2);
+        float g;
+        norm_factors(sqrt(t), s_mul[0], s_mul[1], g);
         if (blockIdx.x == 0) a.g0[b] = g;
     }
     __syncthreads();
     const float m0 = s_mul[0], m1 = s_mul[1];
-    for (uint64_t u = static_cast<uint64_t>(blockIdx.x) * kPackWarps + (threadIdx.x >> 5); u < a.units;
-         u += static_cast<uint64_t>(gridDim.x) * kPackWarps) {
-        uint64_t row0, c;
-        float v[kPackRows][8];
-        load_unit<DT>(a, b, u, row0, c, v);
-        if (c >= a.cols) continue;
+    if (c >= a.cols) return;
 #pragma unroll
-        for (int r = 0; r < kPackRows; ++r) {
-            if (row0 + r >= a.rows) break;
-            uint32_t q[4];
+    for (int r = 0; r < kPackRows; ++r) {
+        if (row0 + r >= a.rows) break;
+        uint32_t q[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) q[e] = pack_half2(v[r][2 * e] * m0 * m1, v[r][2 * e + 1] * m0 * m1);
-            // whole eights: the pitch is a multiple of 8
-            *reinterpret_cast<uint4*>(a.x0 + (static_cast<uint64_t>(b) * a.rows + row0 + r) * a.pitch + c) =
-                make_uint4(q[0], q[1], q[2], q[3]);
+        for (int e = 0; e < 4; ++e) {
+            float lo, hi;
+            widen2<DT>(w[r][e], lo, hi);
+            mul2(lo, hi, m0);
+            mul2(lo, hi, m1);
+            q[e] = narrow2<kFp16>(lo, hi);
         }
+        // whole eights: the pitch is a multiple of 8
+        *reinterpret_cast<uint4*>(a.x0 + (static_cast<uint64_t>(b) * a.rows + row0 + r) * a.pitch + c) =
+            make_uint4(q[0], q[1], q[2], q[3]);
     }
 }
 
@@ -501,7 +517,7 @@ __global__ void __launch_bounds__(kProductThreads) k_ortho_products(const __grid
                     uint32_t q[16];
 #pragma unroll
                     for (uint32_t e = 0; e < 16; ++e)
-                        q[e] = final ? pack_bf2(v[2 * e], v[2 * e + 1]) : pack_half2(v[2 * e], v[2 * e + 1]);
+                        q[e] = final ? narrow2<kBf16>(v[2 * e], v[2 * e + 1]) : narrow2<kFp16>(v[2 * e], v[2 * e + 1]);
 #pragma unroll
                     for (uint32_t j = 0; j < 4; ++j)
                         st_shared(buf + piece128(lane, 4 * h + j), q[4 * j], q[4 * j + 1], q[4 * j + 2], q[4 * j + 3]);
@@ -561,6 +577,361 @@ __global__ void __launch_bounds__(kProductThreads) k_ortho_products(const __grid
     }
     __syncwarp();
     cluster_sync();
+}
+
+// ----------------------------------------------------- short sides up to 128
+// A matrix whose shorter side is at most 128 stays on the SM: one CTA holds
+// 512 of the longer side's values (X as 128 rows of 64-column blocks, which
+// are K-major operands of X X^T and MN-major ones of B X alike), a cluster
+// of up to 8 CTAs the whole of it, and the square matrices are computed by
+// each CTA for itself.  Only X X^T is summed over the cluster, through its
+// shared memory.  The sixteen dependent products take about a microsecond
+// each this way; through global memory they took five.
+constexpr uint32_t kSide = 128, kSlabBlocks = 8, kMaxCtas = 8;
+constexpr uint32_t kBlockBytes = kSide * 128;           // 64 columns of X, or half a square
+constexpr uint32_t kSquareBytes = 2 * kBlockBytes;
+constexpr int kSmallThreads = 256;
+
+struct SmallArgs {
+    const void* src[kMaxMatrices];
+    void* dst[kMaxMatrices];
+    uint64_t ld_src, ld_dst;
+    uint32_t side, span;     // the shorter and the longer side
+    uint32_t ctas, per;      // CTAs a matrix, blocks of 64 a CTA
+    int32_t tall, steps;
+    float scale;
+    float coeffs[3 * ZERO_MAX_NS_STEPS];
+};
+
+__device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
+    float4 x;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+                 : "r"(addr)
+                 : "memory");
+    return x;
+}
+__device__ __forceinline__ double ld_cluster_f64(uint32_t addr) {
+    double x;
+    asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(x) : "r"(addr) : "memory");
+    return x;
+}
+__device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t x, uint32_t y) {
+    asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(x), "r"(y) : "memory");
+}
+__device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t x) {
+    asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr), "h"(static_cast<uint16_t>(x)) : "memory");
+}
+
+// 8 values of a row of the caller's matrix from column c on, packed; zeros
+// from `valid` on.
+__device__ __forceinline__ void load_eight(const unsigned short* at, int valid, bool whole, uint32_t (&w)[4]) {
+    if (whole && valid >= 8) {
+        const uint4 x = __ldg(reinterpret_cast<const uint4*>(at));
+        w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t lo = 2 * e < valid ? __ldg(at + 2 * e) : 0u;
+            const uint32_t hi = 2 * e + 1 < valid ? __ldg(at + 2 * e + 1) : 0u;
+            w[e] = lo | hi << 16;
+        }
+    }
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kSmallThreads) k_ortho_small(const __grid_constant__ SmallArgs p) {
+    pdl_enter();
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ __align__(8) uint64_t s_bar;
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_quit;
+    __shared__ double s_sum;
+    __shared__ float s_mul[3];
+    volatile int* quit = &s_quit;
+    const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = p.ctas > 1 ? cluster_rank() : 0, b = blockIdx.x / p.ctas;
+    const uint32_t first = rank * p.per * 64;                              // this CTA's part of the longer side
+    const uint32_t span = min(p.span - first, p.per * 64), blocks = (span + 63) / 64;
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const uint32_t sq[3] = {base, base + kSquareBytes, base + 2 * kSquareBytes}, x = base + 3 * kSquareBytes;
+    const uint32_t bar = smem_u32(&s_bar);
+    if (tid == 0) {
+        s_quit = 0;
+        bar_init(bar, 1);
+        bar_init_fence();
+    }
+    if (warp == 0) tmem_alloc(smem_u32(&s_tmem), 512);
+    for (uint32_t i = tid; i < blocks * (kBlockBytes / 16); i += kSmallThreads) st_shared(x + 16 * i, 0u, 0u, 0u, 0u);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+
+    // G as it is into X (transposed when tall), and its sum of squares
+    const unsigned short* src = static_cast<const unsigned short*>(p.src[b]);
+    const uint32_t in_rows = p.tall ? span : p.side, in_cols = p.tall ? p.side : span;
+    const uint32_t eights = (in_cols + 7) / 8, pieces = in_rows * eights;
+    if (p.tall) src += static_cast<uint64_t>(first) * p.ld_src;
+    else src += first;
+    {
+        const bool whole = (reinterpret_cast<uintptr_t>(src) & 15) == 0 && p.ld_src % 8 == 0;
+        double acc = 0.0;
+        for (uint32_t i0 = tid; i0 < pieces; i0 += 4 * kSmallThreads) {
+            uint32_t w[4][4];
+#pragma unroll
+            for (uint32_t k = 0; k < 4; ++k) {
+                const uint32_t i = i0 + k * kSmallThreads, r = i / eights, c = (i - r * eights) * 8;
+                load_eight(src + static_cast<uint64_t>(r) * p.ld_src + c, i < pieces ? static_cast<int>(in_cols - c) : 0, whole, w[k]);
+            }
+#pragma unroll
+            for (uint32_t k = 0; k < 4; ++k) {
+                const uint32_t i = i0 + k * kSmallThreads, r = i / eights, c = (i - r * eights) * 8;
+                if (i >= pieces) break;
+                float s = 0.0f;
+                double d = 0.0;
+                const float top = widen<DT>(top_pattern(w[k]));
+                const bool far = !(top < 0x1p60f) || (top > 0.0f && top < 0x1p-50f);   // squares leave fp32's range
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float lo, hi;
+                    widen2<DT>(w[k][e], lo, hi);
+                    s = __fmaf_rn(hi, hi, __fmaf_rn(lo, lo, s));
+                    if (far) {
+                        d = fma(static_cast<double>(lo), static_cast<double>(lo), d);
+                        d = fma(static_cast<double>(hi), static_cast<double>(hi), d);
+                    }
+                }
+                acc += far ? d : static_cast<double>(s);
+                if (p.tall) {
+#pragma unroll
+                    for (uint32_t e = 0; e < 8; ++e)
+                        if (c + e < in_cols)
+                            st_shared16(x + (r >> 6) * kBlockBytes + piece128(c + e, (r & 63) >> 3) + 2 * (r & 7),
+                                        (w[k][e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
+                } else {
+                    st_shared(x + (c >> 6) * kBlockBytes + piece128(r, (c & 63) >> 3), w[k][0], w[k][1], w[k][2], w[k][3]);
+                }
+            }
+        }
+        const double t = block_sum(acc);
+        if (tid == 0) s_sum = t;
+    }
+    if (p.ctas > 1) cluster_sync();
+    if (tid == 0) {
+        double t = 0.0;
+        if (p.ctas > 1)
+            for (uint32_t q = 0; q < p.ctas; ++q) t += ld_cluster_f64(cluster_addr(smem_u32(&s_sum), q));
+        else
+            t = s_sum;
+        norm_factors(sqrt(t), s_mul[0], s_mul[1], s_mul[2]);
+    }
+    __syncthreads();
+    const float g0 = s_mul[2];
+    for (uint32_t i = tid; i < blocks * (kBlockBytes / 16); i += kSmallThreads) {   // X0 = G 2^k, in place
+        const uint4 v = ld_shared(x + 16 * i);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint32_t q[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float lo, hi;
+            widen2<DT>(w[e], lo, hi);
+            mul2(lo, hi, s_mul[0]);
+            mul2(lo, hi, s_mul[1]);
+            q[e] = narrow2<kFp16>(lo, hi);
+        }
+        st_shared(x + 16 * i, q[0], q[1], q[2], q[3]);
+    }
+
+    // Products: every thread's writes before it are seen by the tensor cores,
+    // one thread issues, all wait.
+    uint32_t parity = 0;
+    const uint32_t steps_k = (p.side + 15) / 16;
+    auto begin = [&]() {
+        proxy_fence();
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+    };
+    auto finish = [&]() {
+        if (tid == 0) tc_commit(bar);
+        bar_wait(bar, parity, quit);
+        parity ^= 1;
+        tc_fence_after();
+    };
+    constexpr uint32_t kIdesc = (1u << 4) | (static_cast<uint32_t>(kSide >> 4) << 24);
+    // this thread's part of a 128 x 128 result
+    const uint32_t row = (warp & 3) * 32 + lane, half = (warp >> 2) * 64;
+    // squares[to] = f acc (+ f_lin squares[lin] + f_diag I), acc in the first 128 columns
+    auto square_out = [&](uint32_t to, float f, bool poly, uint32_t lin, float f_lin, float f_diag) {
+#pragma unroll 1
+        for (uint32_t h = 0; h < 64; h += 32) {
+            float v[32];
+            tmem_load32(tmem + half + h + ((warp & 3) << 21), v);
+            const uint32_t at = (half >> 6) * kBlockBytes;
+#pragma unroll
+            for (uint32_t j = 0; j < 4; ++j) {
+                uint32_t q[4];
+                const uint32_t piece = at + piece128(row, (h >> 3) + j);
+                uint4 l = make_uint4(0, 0, 0, 0);
+                if (poly) l = ld_shared(lin + piece);
+                const uint32_t lw[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+                for (uint32_t e = 0; e < 4; ++e) {
+                    float lo, hi;
+                    widen2<kFp16>(lw[e], lo, hi);
+                    float y0 = __fmaf_rn(v[8 * j + 2 * e], f, lo * f_lin), y1 = __fmaf_rn(v[8 * j + 2 * e + 1], f, hi * f_lin);
+                    const uint32_t col = half + h + 8 * j + 2 * e;
+                    if (poly && row == col && row < p.side) y0 += f_diag;
+                    if (poly && row == col + 1 && row < p.side) y1 += f_diag;
+                    q[e] = narrow2<kFp16>(y0, y1);
+                }
+                st_shared(to + piece, q[0], q[1], q[2], q[3]);
+            }
+        }
+    };
+    auto square = [&](uint32_t to, uint32_t a, uint32_t c, float f, bool poly, float f_lin, float f_diag) {
+        begin();
+        if (tid == 0)
+            for (uint32_t k = 0; k < steps_k; ++k) {
+                const uint32_t at = (k >> 2) * kBlockBytes + (k & 3) * 32;
+                mma_f16(tmem, operand_desc(a + at, 0), operand_desc(c + at, 0), kIdesc | ((kSide >> 3) << 17), k > 0);
+            }
+        finish();
+        square_out(to, f, poly, a, f_lin, f_diag);
+    };
+    // sq[0] = A = f X X^T, summed over the cluster
+    auto gram = [&](float f) {
+        begin();
+        if (tid == 0)
+            for (uint32_t k = 0; k < blocks * 4; ++k) {
+                const uint64_t d = operand_desc(x + (k >> 2) * kBlockBytes + (k & 3) * 32, 0);
+                mma_f16(tmem, d, d, kIdesc | ((kSide >> 3) << 17), k > 0);
+            }
+        finish();
+        if (p.ctas == 1) {
+            square_out(sq[0], f, false, 0, 0.0f, 0.0f);
+            return;
+        }
+        // the partial sums in fp32 where the other squares are, which are free here
+        const uint32_t part = sq[1];
+#pragma unroll 1
+        for (uint32_t h = 0; h < 64; h += 32) {
+            float v[32];
+            tmem_load32(tmem + half + h + ((warp & 3) << 21), v);
+#pragma unroll
+            for (uint32_t j = 0; j < 8; ++j)   // pieces of 4 columns, rotated by the row against bank conflicts
+                st_shared(part + row * 512 + ((((half + h) / 4 + j) ^ (row & 7)) << 4), __float_as_uint(v[4 * j]),
+                          __float_as_uint(v[4 * j + 1]), __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3]));
+        }
+        cluster_sync();
+        // every CTA adds up some of the rows, in order of rank, and gives the sums to all
+        for (uint32_t i = rank * kSmallThreads + tid; i < kSide * 32; i += p.ctas * kSmallThreads) {
+            const uint32_t r = i >> 5, c4 = i & 31;
+            const uint32_t at = part + r * 512 + ((c4 ^ (r & 7)) << 4);
+            float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (uint32_t q = 0; q < p.ctas; ++q) {
+                const float4 y = ld_cluster(cluster_addr(at, q));
+                s.x += y.x; s.y += y.y; s.z += y.z; s.w += y.w;
+            }
+            const uint32_t lo = narrow2<kFp16>(s.x * f, s.y * f), hi = narrow2<kFp16>(s.z * f, s.w * f);
+            const uint32_t to = sq[0] + (c4 >> 4) * kBlockBytes + piece128(r, (c4 & 15) >> 1) + 8 * (c4 & 1);
+            for (uint32_t q = 0; q < p.ctas; ++q) st_cluster(cluster_addr(to, q), lo, hi);
+        }
+        proxy_fence();
+        cluster_sync();
+    };
+    // X = f B X in place, or as bf16 for the caller
+    auto update = [&](uint32_t m, float f, bool final) {
+        begin();
+        if (tid == 0)
+            for (uint32_t n0 = 0; n0 < blocks; n0 += 4) {
+                const uint32_t n = min(4u, blocks - n0);
+                for (uint32_t k = 0; k < steps_k; ++k)
+                    mma_f16(tmem + n0 * 64, operand_desc(m + (k >> 2) * kBlockBytes + (k & 3) * 32, 0),
+                            operand_desc(x + n0 * kBlockBytes + k * 2048, kBlockBytes),
+                            kIdesc | (1u << 16) | ((n * 8) << 17), k > 0);
+            }
+        finish();
+#pragma unroll 1
+        for (uint32_t n = warp >> 2; n < 2 * blocks; n += 2) {   // 32 columns each
+            float v[32];
+            tmem_load32(tmem + n * 32 + ((warp & 3) << 21), v);
+            const uint32_t to = x + (n >> 1) * kBlockBytes;
+#pragma unroll
+            for (uint32_t j = 0; j < 4; ++j) {
+                uint32_t q[4];
+#pragma unroll
+                for (uint32_t e = 0; e < 4; ++e) {
+                    const float lo = v[8 * j + 2 * e] * f, hi = v[8 * j + 2 * e + 1] * f;
+                    q[e] = final ? narrow2<kBf16>(lo, hi) : narrow2<kFp16>(lo, hi);
+                }
+                st_shared(to + piece128(row, (n & 1) * 4 + j), q[0], q[1], q[2], q[3]);
+            }
+        }
+    };
+
+    for (int k = 0; k < p.steps;) {
+        const float* c = p.coeffs + 3 * k;
+        const bool raw = k == 0, pair = raw && p.steps >= 2;
+        auto poly = [&](uint32_t to, uint32_t a, const float* co) {
+            square(to, a, a, co[2] * (kScaleB / (kScaleA * kScaleA)), true, co[1] * (kScaleB / kScaleA), co[0] * kScaleB);
+        };
+        gram(raw ? kScaleA * g0 * g0 : kScaleA / (kScaleX * kScaleX));
+        poly(sq[1], sq[0], c);
+        uint32_t m = sq[1];
+        if (pair) {
+            square(sq[2], sq[1], sq[0], 1.0f / kScaleB, false, 0.0f, 0.0f);   // B A
+            square(sq[0], sq[1], sq[2], 1.0f / kScaleB, false, 0.0f, 0.0f);   // A_1 = B (B A)
+            poly(sq[2], sq[0], c + 3);                                        // B_1
+            square(sq[0], sq[2], sq[1], 1.0f / kScaleB, false, 0.0f, 0.0f);   // Q = B_1 B
+            m = sq[0];
+        }
+        k += pair ? 2 : 1;
+        const bool final = k >= p.steps;
+        update(m, (final ? p.scale : kScaleX) / (raw ? kScaleB : kScaleB * kScaleX) * (raw ? g0 : 1.0f), final);
+    }
+    __syncthreads();
+
+    // to the caller's matrix, along its rows
+    unsigned short* dst = static_cast<unsigned short*>(p.dst[b]);
+    if (p.tall) dst += static_cast<uint64_t>(first) * p.ld_dst;
+    else dst += first;
+    const bool whole = (reinterpret_cast<uintptr_t>(dst) & 15) == 0 && p.ld_dst % 8 == 0;
+    for (uint32_t i = tid; i < pieces; i += kSmallThreads) {
+        const uint32_t r = i / eights, c = (i - r * eights) * 8;
+        uint32_t w[4];
+        if (p.tall) {
+#pragma unroll
+            for (uint32_t e = 0; e < 8; e += 2) {
+                const uint32_t at = x + (r >> 6) * kBlockBytes + 2 * (r & 7);
+                w[e >> 1] = static_cast<uint32_t>(ld_shared16(at + piece128(c + e, (r & 63) >> 3))) |
+                            static_cast<uint32_t>(ld_shared16(at + piece128(c + e + 1, (r & 63) >> 3))) << 16;
+            }
+        } else {
+            const uint4 v = ld_shared(x + (c >> 6) * kBlockBytes + piece128(r, (c & 63) >> 3));
+            w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+        }
+        unsigned short* out = dst + static_cast<uint64_t>(r) * p.ld_dst + c;
+        if (whole && c + 8 <= in_cols) {
+            *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+#pragma unroll
+            for (uint32_t e = 0; e < 8; ++e)
+                if (c + e < in_cols) out[e] = static_cast<unsigned short>(w[e >> 1] >> (16 * (e & 1)));
+        }
+    }
+    if (*quit && tid == 0) {   // a wait gave up: products may still be running
+        const uint64_t t0 = now_ns();
+        while (now_ns() - t0 < 1000000ull) {}
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (p.ctas > 1) cluster_sync();   // nobody reads this CTA's shared memory any more
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_free(tmem, 512);
+    }
 }
 
 // -------------------------------------------------------------------- host
@@ -664,6 +1035,39 @@ int zero_orthogonalize(int dtype, int batch, uint64_t rows, uint64_t cols, const
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
 
     cudaError_t e;
+    if (side <= kSide && span <= kMaxCtas * kSlabBlocks * 64) {
+        SmallArgs m = {};
+        for (int i = 0; i < batch; ++i) {
+            if (!src[i] || !aligned(src[i], 2)) return refuse(ZERO_EINVAL, "src[i] is NULL or not 2-byte aligned");
+            if (!dst[i] || !aligned(dst[i], 2)) return refuse(ZERO_EINVAL, "dst[i] is NULL or not 2-byte aligned");
+            m.src[i] = src[i];
+            m.dst[i] = dst[i];
+        }
+        m.ld_src = ld_src;
+        m.ld_dst = ld_dst;
+        m.side = static_cast<uint32_t>(side);
+        m.span = static_cast<uint32_t>(span);
+        const uint32_t blocks = (m.span + 63) / 64;
+        m.ctas = (blocks + kSlabBlocks - 1) / kSlabBlocks;
+        m.per = (blocks + m.ctas - 1) / m.ctas;
+        m.ctas = (blocks + m.per - 1) / m.per;   // none without a block
+        m.tall = tall;
+        m.steps = steps;
+        m.scale = scale;
+        for (int i = 0; i < 3 * steps; ++i) m.coeffs[i] = coeffs ? coeffs[i] : kDefaultCoeffs[i % 3];
+        const size_t smem = 1024 + 3 * kSquareBytes + static_cast<size_t>(m.per) * kBlockBytes;
+        constexpr size_t most = 1024 + 3 * kSquareBytes + kSlabBlocks * kBlockBytes;
+        const dim3 grid(m.ctas * nb);
+        if (dtype == ZERO_FP16) {
+            if ((e = allow_smem<k_ortho_small<kFp16>>(most)) == cudaSuccess)
+                e = launch_pdl(k_ortho_small<kFp16>, grid, kSmallThreads, smem, m.ctas, s, m);
+        } else {
+            if ((e = allow_smem<k_ortho_small<kBf16>>(most)) == cudaSuccess)
+                e = launch_pdl(k_ortho_small<kBf16>, grid, kSmallThreads, smem, m.ctas, s, m);
+        }
+        return e == cudaSuccess ? ZERO_OK : cuda_refuse(e, "zero_orthogonalize");
+    }
+
     PackArgs q = {};
     ProductArgs p;   // its maps and phases are filled below
     std::memset(&p, 0, sizeof(p));
@@ -680,8 +1084,8 @@ int zero_orthogonalize(int dtype, int batch, uint64_t rows, uint64_t cols, const
     q.cols = cols;
     q.ld = ld_src;
     q.pitch = xp;
-    q.segments = (cols + 255) / 256;
-    q.units = (rows + kPackRows - 1) / kPackRows * q.segments;
+    q.segments = static_cast<uint32_t>((cols + 255) / 256);
+    q.units = static_cast<uint32_t>((rows + kPackRows - 1) / kPackRows) * q.segments;
     q.partial = reinterpret_cast<double*>(ws + z.partial);
     q.g0 = reinterpret_cast<float*>(ws + z.g0);
     q.done = reinterpret_cast<uint32_t*>(ws + z.done);
@@ -690,7 +1094,7 @@ int zero_orthogonalize(int dtype, int batch, uint64_t rows, uint64_t cols, const
     q.partials = static_cast<int>(want < kPartials ? want : kPartials);
     {
         const dim3 grid(static_cast<unsigned>(q.partials), nb);
-        const dim3 packs(static_cast<unsigned>(want < 4096 ? want : 4096), nb);
+        const dim3 packs(static_cast<unsigned>(want), nb);
         e = dtype == ZERO_FP16 ? launch_pdl(k_ortho_norm<kFp16>, grid, kThreads, 0, 1, s, q)
                                : launch_pdl(k_ortho_norm<kBf16>, grid, kThreads, 0, 1, s, q);
         if (e != cudaSuccess) return cuda_refuse(e, "norm");

@@ -111,5 +111,53 @@ __device__ __forceinline__ void store8(unsigned short* base, int64_t at, int val
     }
 }
 
+// A lane's values left of a row's `cols` from column c on, within +-8.
+__device__ __forceinline__ int values_left(uint64_t cols, uint64_t c) {
+    const int64_t left = static_cast<int64_t>(cols) - static_cast<int64_t>(c);
+    return left > 8 ? 8 : left < -8 ? -8 : static_cast<int>(left);
+}
+// Zeros in place of the values from `valid` on.
+__device__ __forceinline__ void clear_from(uint32_t (&w)[4], int valid) {
+    if (valid >= 8) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        w[i] = valid >= 2 * i + 2 ? w[i] : valid == 2 * i + 1 ? w[i] & 0xFFFFu : 0u;
+}
+// The largest magnitude of 8 values as a 16-bit pattern: patterns are ordered
+// like magnitudes in both formats, infinity and NaN above every number.
+__device__ __forceinline__ uint32_t top_pattern(const uint32_t (&w)[4]) {
+    const uint32_t m = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu),
+                                __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+    return max(m & 0xFFFFu, m >> 16);
+}
+// Both values of a word.
+template <int DT>
+__device__ __forceinline__ void widen2(uint32_t w, float& lo, float& hi) {
+    if (DT == kBf16) {
+        lo = __uint_as_float(w << 16);
+        hi = __uint_as_float(w & 0xFFFF0000u);
+    } else {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+        lo = f.x;
+        hi = f.y;
+    }
+}
+// Two fp32 values as packed 16-bit ones, the first in the low half.
+template <int DT>
+__device__ __forceinline__ uint32_t narrow2(float lo, float hi) {
+    uint32_t r;
+    if (DT == kBf16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// Two products, each rounded once.
+__device__ __forceinline__ void mul2(float& a, float& b, float by) {
+    unsigned long long x, y;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a), "f"(b));
+    asm("mov.b64 %0, {%1, %1};" : "=l"(y) : "f"(by));
+    asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(x) : "l"(y));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+
 }  // namespace
 }  // namespace zg

@@ -170,6 +170,7 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
     return r;
 }
 __device__ __forceinline__ void cluster_sync() {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void bar_arrive_cluster(uint32_t bar) {
@@ -278,18 +279,6 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr, uint32_t lead) {
     d |= static_cast<uint64_t>(1) << 46;   // descriptor version of sm_100
     d |= static_cast<uint64_t>(2) << 61;   // 128-byte swizzle
     return d;
-}
-
-// Two fp32 values as packed 16-bit ones, the first in the low half.
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-__device__ __forceinline__ uint32_t pack_bf2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
 }
 
 // Lower-triangular tile t of a square grid of tiles: row i >= column j.
