@@ -280,40 +280,45 @@ __global__ void __launch_bounds__(kThreads) k_mx4_values(const __grid_constant__
 }
 
 // ----------------------------------------------------------------- product
-// out[m][n] = sum over k of A[m][k] B[n][k], fp32 accumulation.
+// out[m][n] = sum over k of A[m][k] B[n][k], fp32 accumulation.  A pair of
+// CTAs computes 256 x 192: a stage of 256 values of k is 31 KiB a CTA for 384
+// cycles of products, so L2's supply to the SMs is what bounds it, and the
+// tile is as large as leaves room in tensor memory for two accumulators (one
+// tile's output is written under the next one's products) beside the
+// scales.  192 columns begin in the middle of a scale tile of 128 rows half
+// of the time: two scale tiles cover them either way, and the product starts
+// two columns further on in tensor memory.
 struct MxProductArgs {
     uint32_t m, n, k;
     uint32_t tiles_n, total;
     uint32_t tiles_k;        // scale tiles along k
-    const uint8_t* a_scales;
-    const uint8_t* b_scales;
     void* out;
     uint64_t ld;
-    int vec;
+    int vec;                 // rows of out start on 16 bytes
 };
 
-constexpr int kMxM = 128, kMxN = 128;
-constexpr int kMxK = 256;                          // values a stage: 128 bytes a row
-constexpr uint32_t kMxOperand = kMxM * kMxK / 2;   // bytes of one operand's tile
-constexpr uint32_t kMxScales = 1024;               // two scale tiles an operand
-constexpr uint32_t kMxStage = 2 * kMxOperand + 2 * kMxScales;
+constexpr int kMxM = 256, kMxN = 192, kMxK = 256;   // a stage's values of k are 128 bytes of a row
+constexpr uint32_t kMxABytes = kMxM / 2 * kMxK / 2, kMxBBytes = kMxN / 2 * kMxK / 2;   // a CTA's halves
+constexpr uint32_t kMxStage = kMxABytes + kMxBBytes + 1024 + 2048;   // and its rows' scales, and all columns'
 constexpr int kMxStages = 6;
-constexpr size_t kMxSmem = 1024 + static_cast<size_t>(kMxStages) * kMxStage;
+constexpr uint32_t kMxOut = 32 * 64 * 2;            // a warp's output buffer, two each
+constexpr size_t kMxSmem = 1024 + kMxStages * kMxStage + 8 * kMxOut;
 constexpr int kMxThreads = 192;
 
 // A scale tile (32 lines of 16 bytes in shared memory) into 4 columns of
-// tensor memory, repeated in each quarter of the lanes.
+// tensor memory, repeated in each quarter of the lanes, in both CTAs from
+// their own shared memory.
 __device__ __forceinline__ void tc_copy_scales(uint32_t tmem, uint32_t smem) {
     uint64_t d = static_cast<uint64_t>((smem & 0x3FFFFu) >> 4);
     d |= static_cast<uint64_t>(128u >> 4) << 32;   // 8 lines of 16 bytes
     d |= static_cast<uint64_t>(1) << 46;
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(d) : "memory");
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(d) : "memory");
 }
 __device__ __forceinline__ void mma_mx4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
                                         bool accumulate) {
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
         ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(static_cast<uint32_t>(accumulate))
         : "memory");
 }
@@ -321,6 +326,7 @@ __device__ __forceinline__ void mma_mx4(uint32_t d, uint64_t a, uint64_t b, uint
 template <int DT>
 __global__ void __launch_bounds__(kMxThreads)
 k_mx4_product(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+              const __grid_constant__ CUtensorMap map_sa, const __grid_constant__ CUtensorMap map_sb,
               const __grid_constant__ MxProductArgs p) {
     extern __shared__ unsigned char smem_raw[];
     __shared__ __align__(8) uint64_t bars[2 * kMxStages + 4];
@@ -329,6 +335,7 @@ k_mx4_product(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
     __shared__ int s_quit;
     volatile int* quit = &s_quit;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
     const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint32_t full = smem_u32(bars), empty = full + 8 * kMxStages, done = empty + 8 * kMxStages, freed = done + 16;
     if (threadIdx.x == 0) {
@@ -339,54 +346,55 @@ k_mx4_product(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
         }
         for (int i = 0; i < 2; ++i) {
             bar_init(done + 8 * i, 1);
-            bar_init(freed + 8 * i, 128);
+            bar_init(freed + 8 * i, 8);
         }
         bar_init(smem_u32(&s_last), 1);
         bar_init_fence();
         prefetch_map(&map_a);
         prefetch_map(&map_b);
+        prefetch_map(&map_sa);
+        prefetch_map(&map_sb);
     }
-    if (warp == 1) tmem_alloc(smem_u32(&s_tmem), 512);
+    if (warp == 1) tmem_alloc_pair(smem_u32(&s_tmem), 512);
     tc_fence_before();
     __syncthreads();
+    cluster_sync();
     tc_fence_after();
     const uint32_t tmem = s_tmem;
     pdl_enter();
-    const uint32_t nk = (p.k + kMxK - 1) / kMxK;
+    const uint32_t nk = (p.k + kMxK - 1) / kMxK, stride = gridDim.x >> 1;
 
     if (warp == 0 && lane == 0) {
+        const uint32_t leader_full = cluster_addr(full, 0);
         uint32_t it = 0;
         bool ok = true;
-        for (uint32_t t = blockIdx.x; t < p.total && ok; t += gridDim.x) {
+        for (uint32_t t = blockIdx.x >> 1; t < p.total && ok; t += stride) {
             const uint32_t tm = t / p.tiles_n, tn = t - tm * p.tiles_n;
+            const int ra = static_cast<int>(tm * kMxM + rank * (kMxM / 2)), rb = static_cast<int>(tn * kMxN + rank * (kMxN / 2));
             for (uint32_t kb = 0; kb < nk; ++kb, ++it) {
                 const uint32_t s = it % kMxStages;
                 if (it >= kMxStages && !bar_wait(empty + 8 * s, (it / kMxStages - 1) & 1, quit)) {
                     ok = false;
                     break;
                 }
-                const uint32_t bar = full + 8 * s, st = ring + s * kMxStage;
-                const uint32_t scales = 2 * kb + 2 <= p.tiles_k ? 1024u : 512u;
-                bar_expect(bar, 2 * kMxOperand + 2 * scales);
-                copy_box(st, &map_a, static_cast<int>(kb * 128), static_cast<int>(tm * kMxM), 0, bar);
-                copy_box(st + kMxOperand, &map_b, static_cast<int>(kb * 128), static_cast<int>(tn * kMxN), 0, bar);
-                copy_bytes(st + 2 * kMxOperand, p.a_scales + (static_cast<uint64_t>(tm) * p.tiles_k + 2 * kb) * 512,
-                           scales, bar);
-                copy_bytes(st + 2 * kMxOperand + kMxScales,
-                           p.b_scales + (static_cast<uint64_t>(tn) * p.tiles_k + 2 * kb) * 512, scales, bar);
+                const uint32_t bar = leader_full + 8 * s, st = ring + s * kMxStage;
+                const uint32_t ss = st + kMxABytes + kMxBBytes;
+                if (rank == 0) bar_expect(full + 8 * s, 2 * kMxStage);   // the bytes of both CTAs
+                copy_box_pair(st, &map_a, static_cast<int>(kb * 128), ra, 0, bar);
+                copy_box_pair(st + kMxABytes, &map_b, static_cast<int>(kb * 128), rb, 0, bar);
+                copy_box_pair(ss, &map_sa, static_cast<int>(kb * 256), ra >> 7, 0, bar);
+                copy_box_pair(ss + 1024, &map_sb, static_cast<int>(kb * 256), static_cast<int>(tn * kMxN) >> 7, 0, bar);
             }
         }
-        if (!ok)
-            for (uint32_t i = it > kMxStages ? it - kMxStages : 0; i < it; ++i)
-                bar_drain(full + 8 * (i % kMxStages), (i / kMxStages) & 1);
-    } else if (warp == 1 && lane == 0) {
-        // e2m1 operands, power-of-two scales, 128 x 128
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+        // e2m1 operands, power-of-two scales, 256 x 192
         constexpr uint32_t idesc = (1u << 7) | (1u << 10) | (static_cast<uint32_t>(kMxN >> 3) << 17) | (1u << 23) |
                                    (static_cast<uint32_t>(kMxM >> 4) << 24);
         uint32_t it = 0, n = 0;
         bool ok = true;
-        for (uint32_t t = blockIdx.x; t < p.total && ok; t += gridDim.x, ++n) {
+        for (uint32_t t = blockIdx.x >> 1; t < p.total && ok; t += stride, ++n) {
             const uint32_t acc = n & 1, d = tmem + acc * kMxN;
+            const uint32_t odd = (t % p.tiles_n) & 1 ? 2u : 0u;   // columns that begin with a scale tile's row 64
             if (n >= 2 && !bar_wait(freed + 8 * acc, (n / 2 - 1) & 1, quit)) break;
             tc_fence_after();
             for (uint32_t kb = 0; kb < nk; ++kb, ++it) {
@@ -396,71 +404,75 @@ k_mx4_product(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
                     break;
                 }
                 tc_fence_after();
-                const uint32_t st = ring + s * kMxStage, ss = st + 2 * kMxOperand;
-                const uint64_t da = operand_desc(st, 0), db = operand_desc(st + kMxOperand, 0);
-                const uint32_t sf = tmem + 2 * kMxN + (it & 1) * 16;
+                const uint32_t st = ring + s * kMxStage, ss = st + kMxABytes + kMxBBytes;
+                const uint64_t da = operand_desc(st, 0), db = operand_desc(st + kMxABytes, 0);
+                const uint32_t sf = tmem + 2 * kMxN + (it & 1) * 24;
 #pragma unroll
-                for (uint32_t h = 0; h < 2; ++h) {   // 128 values: one scale tile of each operand, two products
+                for (uint32_t h = 0; h < 2; ++h) {   // 128 values: a scale tile of A's rows, two of B's, two products
                     if (2 * kb + h >= p.tiles_k) break;
-                    tc_copy_scales(sf + 4 * h, ss + 512 * h);
-                    tc_copy_scales(sf + 8 + 4 * h, ss + kMxScales + 512 * h);
+                    const uint32_t sa = sf + 4 * h, sb = sf + 8 + 8 * h;
+                    tc_copy_scales(sa, ss + 512 * h);
+                    tc_copy_scales(sb, ss + 1024 + 512 * h);
+                    tc_copy_scales(sb + 4, ss + 2048 + 512 * h);
 #pragma unroll
                     for (uint32_t j = 0; j < 2; ++j)
-                        mma_mx4(d, da + (2 * h + j) * 2, db + (2 * h + j) * 2, idesc | (2 * j << 4) | (2 * j << 29),
-                                sf + 4 * h, sf + 8 + 4 * h, kb > 0 || h > 0 || j > 0);
+                        mma_mx4(d, da + (2 * h + j) * 2, db + (2 * h + j) * 2, idesc | (2 * j << 4) | (2 * j << 29), sa,
+                                sb + odd, kb > 0 || h > 0 || j > 0);
                 }
-                tc_commit(empty + 8 * s);
+                tc_commit_pair(empty + 8 * s);
             }
-            if (ok) tc_commit(done + 8 * acc);
+            if (ok) tc_commit_pair(done + 8 * acc);
         }
-        if (*quit) {
-            tc_commit(smem_u32(&s_last));
+        if (*quit) {   // tensor memory must not be freed under a product
+            tc_commit_pair(smem_u32(&s_last));
             bar_drain(smem_u32(&s_last), 0);
         }
     } else if (warp >= 2) {
-        const uint32_t quarter = warp & 3;
+        const uint32_t quarter = warp & 3, leader_freed = cluster_addr(freed, 0);
+        const uint32_t mine = ring + kMxStages * kMxStage + quarter * 2 * kMxOut;
         uint32_t n = 0;
-        for (uint32_t t = blockIdx.x; t < p.total; t += gridDim.x, ++n) {
+        for (uint32_t t = blockIdx.x >> 1; t < p.total; t += stride, ++n) {
             const uint32_t acc = n & 1, tm = t / p.tiles_n, tn = t - tm * p.tiles_n;
+            const uint32_t row0 = tm * kMxM + rank * (kMxM / 2) + quarter * 32, col0 = tn * kMxN;
             const bool ok = bar_wait(done + 8 * acc, (n / 2) & 1, quit);
             if (__any_sync(0xFFFFFFFFu, !ok)) break;
             tc_fence_after();
-            const uint32_t row = tm * kMxM + quarter * 32 + lane;
-            unsigned short* out = static_cast<unsigned short*>(p.out) + static_cast<uint64_t>(row) * p.ld;
 #pragma unroll 1
-            for (int cc = 0; cc < kMxN / 32; ++cc) {
-                const uint32_t col = tn * kMxN + cc * 32;
-                if (col >= p.n) break;
-                float v[32];
-                tmem_load32(tmem + acc * kMxN + cc * 32 + (quarter << 21), v);
-                if (row < p.m) {
+            for (uint32_t c = 0; c < kMxN / 64; ++c) {
+                if (row0 >= p.m || col0 + 64 * c >= p.n) break;   // uniform over the warp
+                const uint32_t buf = mine + (c & 1) * kMxOut;
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        uint32_t q[4];
+                for (uint32_t h = 0; h < 2; ++h) {
+                    float v[32];
+                    tmem_load32(tmem + acc * kMxN + 64 * c + 32 * h + (quarter << 21), v);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            q[e] = narrow2<DT>(v[8 * g + 2 * e], v[8 * g + 2 * e + 1]);
-                        const uint32_t c = col + 8 * g;
-                        if (p.vec && c + 8 <= p.n) {
-                            *reinterpret_cast<uint4*>(out + c) = make_uint4(q[0], q[1], q[2], q[3]);
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                if (c + e < p.n) out[c + e] = static_cast<unsigned short>(q[e >> 1] >> (16 * (e & 1)));
-                        }
-                    }
+                    for (uint32_t j = 0; j < 4; ++j)
+                        st_shared(buf + piece128(lane, 4 * h + j), narrow2<DT>(v[8 * j], v[8 * j + 1]),
+                                  narrow2<DT>(v[8 * j + 2], v[8 * j + 3]), narrow2<DT>(v[8 * j + 4], v[8 * j + 5]),
+                                  narrow2<DT>(v[8 * j + 6], v[8 * j + 7]));
                 }
+                __syncwarp();
+                write_rows(static_cast<unsigned short*>(p.out), p.ld, p.vec, p.m, p.n, row0, col0 + 64 * c, buf);
             }
             tc_fence_before();
-            bar_arrive(freed + 8 * acc);
+            __syncwarp();
+            if (lane == 0) bar_arrive_cluster(leader_freed + 8 * acc);
         }
     }
+    __syncwarp();
+    if (*quit && threadIdx.x == 0) {   // copies in flight land within microseconds: leave them a millisecond
+        const uint64_t t0 = now_ns();
+        while (now_ns() - t0 < 1000000ull) {}
+    }
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
+    cluster_sync();
     if (warp == 1) {
         tc_fence_after();
-        tmem_free(tmem, 512);
+        tmem_free_pair(tmem, 512);
     }
+    cluster_sync();
 }
 
 // -------------------------------------------------------------------- host
@@ -592,23 +604,24 @@ int zero_mx4_matmul(int dtype, uint64_t m, uint64_t n, uint64_t k, const void* a
     p.tiles_n = static_cast<uint32_t>(up(n, kMxN) / kMxN);
     p.total = static_cast<uint32_t>(tiles);
     p.tiles_k = static_cast<uint32_t>(up(k, 128) / 128);
-    p.a_scales = static_cast<const uint8_t*>(a_scales);
-    p.b_scales = static_cast<const uint8_t*>(b_scales);
     p.out = out16;
     p.ld = ld;
     p.vec = aligned(out16, 16) && ld % 8 == 0;
-    CUtensorMap ma, mb;
-    const uint64_t pitch = mx_pitch(k);
-    if ((e = make_map(&ma, 1, a_codes, pitch, m, 1, pitch, m * pitch, 128, 128)) != cudaSuccess ||
-        (e = make_map(&mb, 1, b_codes, pitch, n, 1, pitch, n * pitch, 128, 128)) != cudaSuccess)
+    CUtensorMap ma, mb, sa, sb;
+    const uint64_t pitch = mx_pitch(k), words = static_cast<uint64_t>(p.tiles_k) * 128;   // of a row of scale tiles
+    const CUtensorMapSwizzle plain = CU_TENSOR_MAP_SWIZZLE_NONE;
+    if ((e = make_map(&ma, 1, a_codes, pitch, m, 1, pitch, m * pitch, 128, kMxM / 2)) != cudaSuccess ||
+        (e = make_map(&mb, 1, b_codes, pitch, n, 1, pitch, n * pitch, 128, kMxN / 2)) != cudaSuccess ||
+        (e = make_map(&sa, 4, a_scales, words, up(m, 128) / 128, 1, words, words * (up(m, 128) / 128), 256, 1, plain)) != cudaSuccess ||
+        (e = make_map(&sb, 4, b_scales, words, up(n, 128) / 128, 1, words, words * (up(n, 128) / 128), 256, 2, plain)) != cudaSuccess)
         return cuda_refuse(e, "tensor map");
-    const unsigned grid = grid_of(tiles, sms, 1);
+    const unsigned grid = 2 * grid_of(tiles, sms / 2, 1);
     if (dtype == ZERO_FP16) {
         if ((e = allow_smem<k_mx4_product<kFp16>>(kMxSmem)) == cudaSuccess)
-            e = launch_pdl(k_mx4_product<kFp16>, dim3(grid), kMxThreads, kMxSmem, 1, s, ma, mb, p);
+            e = launch_pdl(k_mx4_product<kFp16>, dim3(grid), kMxThreads, kMxSmem, 2, s, ma, mb, sa, sb, p);
     } else {
         if ((e = allow_smem<k_mx4_product<kBf16>>(kMxSmem)) == cudaSuccess)
-            e = launch_pdl(k_mx4_product<kBf16>, dim3(grid), kMxThreads, kMxSmem, 1, s, ma, mb, p);
+            e = launch_pdl(k_mx4_product<kBf16>, dim3(grid), kMxThreads, kMxSmem, 2, s, ma, mb, sa, sb, p);
     }
     return e == cudaSuccess ? ZERO_OK : cuda_refuse(e, "zero_mx4_matmul");
 }

@@ -281,63 +281,6 @@ struct Walk {
     }
 };
 
-// Byte offset of 16-byte piece j of row r in a buffer of 128-byte or 64-byte
-// rows, as the bulk copy's swizzle of that width places it.
-__device__ __forceinline__ uint32_t piece128(uint32_t r, uint32_t j) { return r * 128 + ((j ^ (r & 7)) << 4); }
-__device__ __forceinline__ uint32_t piece64(uint32_t r, uint32_t j) { return r * 64 + ((j ^ ((r >> 1) & 3)) << 4); }
-__device__ __forceinline__ void st_shared(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
-}
-__device__ __forceinline__ void st_shared(uint32_t addr, uint32_t x) {
-    asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
-}
-__device__ __forceinline__ uint4 ld_shared(uint32_t addr) {
-    uint4 x;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-                 : "r"(addr)
-                 : "memory");
-    return x;
-}
-__device__ __forceinline__ uint16_t ld_shared16(uint32_t addr) {
-    uint16_t x;
-    asm volatile("ld.shared.b16 %0, [%1];" : "=h"(x) : "r"(addr) : "memory");
-    return x;
-}
-
-// 32 rows x 64 columns of bf16 in a warp's buffer into the caller's matrix:
-// whole 128-byte rows where they are aligned, element by element elsewhere.
-__device__ __forceinline__ void write_rows(const ProductArgs& p, const Phase& f, uint32_t b, uint32_t row0, uint32_t col0,
-                                           uint32_t buf) {
-    const uint32_t lane = threadIdx.x & 31;
-    unsigned short* dst = static_cast<unsigned short*>(p.dst[b]);
-    if (p.dst_vec) {
-#pragma unroll 4
-        for (uint32_t i = lane; i < 256; i += 32) {
-            const uint32_t r = i >> 3, j = i & 7, col = col0 + 8 * j;
-            if (row0 + r >= f.rows || col >= f.cols) continue;
-            unsigned short* out = dst + static_cast<uint64_t>(row0 + r) * p.dst_ld + col;
-            const uint4 x = ld_shared(buf + piece128(r, j));
-            if (col + 8 <= f.cols) {
-                *reinterpret_cast<uint4*>(out) = x;
-            } else {
-                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                for (uint32_t e = 0; e < 8; ++e)
-                    if (col + e < f.cols) out[e] = static_cast<unsigned short>(w[e >> 1] >> (16 * (e & 1)));
-            }
-        }
-    } else {
-#pragma unroll 4
-        for (uint32_t i = lane; i < 32 * 64; i += 32) {
-            const uint32_t r = i >> 6, e = i & 63;
-            if (row0 + r < f.rows && col0 + e < f.cols)
-                dst[static_cast<uint64_t>(row0 + r) * p.dst_ld + col0 + e] =
-                    ld_shared16(buf + piece128(r, e >> 3) + 2 * (e & 7));
-        }
-    }
-}
-
 __global__ void __launch_bounds__(kProductThreads) k_ortho_products(const __grid_constant__ ProductArgs p) {
     extern __shared__ unsigned char smem_raw[];
     __shared__ __align__(8) uint64_t bars[2 * kStages + 4 + 8];
@@ -535,7 +478,7 @@ __global__ void __launch_bounds__(kProductThreads) k_ortho_products(const __grid
                 }
                 if (final) {
                     __syncwarp();
-                    write_rows(p, f, w.b, row0, col0 + 64 * c, buf);
+                    write_rows(static_cast<unsigned short*>(p.dst[w.b]), p.dst_ld, p.dst_vec, f.rows, f.cols, row0, col0 + 64 * c, buf);
                     __syncwarp();
                 } else {
                     proxy_fence();

@@ -39,7 +39,7 @@ inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
     return fn;
 }
 
-// A [batch][rows][cols] array of `elem`-byte values (1: bytes, 2: 16 bits)
+// A [batch][rows][cols] array of `elem`-byte values (1, 2 or 4)
 // with `pitch` values between rows, read in boxes of box_cols x box_rows in
 // the 128-byte swizzle (or another); what lies outside the array reads as zero.
 inline cudaError_t make_map(CUtensorMap* map, int elem, const void* base, uint64_t cols, uint64_t rows, uint64_t batch,
@@ -51,7 +51,9 @@ inline cudaError_t make_map(CUtensorMap* map, int elem, const void* base, uint64
     const cuuint64_t strides[2] = {pitch * static_cast<uint64_t>(elem), matrix_stride * static_cast<uint64_t>(elem)};
     const cuuint32_t box[3] = {box_cols, box_rows, 1};
     const cuuint32_t step[3] = {1, 1, 1};
-    const CUresult r = encode(map, elem == 2 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3,
+    const CUresult r = encode(map, elem == 4   ? CU_TENSOR_MAP_DATA_TYPE_UINT32
+                                   : elem == 2 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                               : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3,
                               const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
                               swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -199,12 +201,6 @@ __device__ __forceinline__ bool count_wait(const uint32_t* counter, uint32_t tar
 __device__ __forceinline__ void count_done(uint32_t* counter) {
     asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(counter) : "memory");
 }
-__device__ __forceinline__ void copy_bytes(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-                 ::"r"(dst), "l"(src), "r"(bytes), "r"(bar)
-                 : "memory");
-}
-
 // ----------------------------------------------------------------- tcgen05
 __device__ __forceinline__ void tmem_alloc(uint32_t smem_slot, uint32_t cols) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_slot), "r"(cols)
@@ -279,6 +275,62 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr, uint32_t lead) {
     d |= static_cast<uint64_t>(1) << 46;   // descriptor version of sm_100
     d |= static_cast<uint64_t>(2) << 61;   // 128-byte swizzle
     return d;
+}
+
+// Byte offset of 16-byte piece j of row r in a buffer of 128-byte or 64-byte
+// rows, as the bulk copy's swizzle of that width places it.
+__device__ __forceinline__ uint32_t piece128(uint32_t r, uint32_t j) { return r * 128 + ((j ^ (r & 7)) << 4); }
+__device__ __forceinline__ uint32_t piece64(uint32_t r, uint32_t j) { return r * 64 + ((j ^ ((r >> 1) & 3)) << 4); }
+__device__ __forceinline__ void st_shared(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+__device__ __forceinline__ void st_shared(uint32_t addr, uint32_t x) {
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared(uint32_t addr) {
+    uint4 x;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                 : "r"(addr)
+                 : "memory");
+    return x;
+}
+__device__ __forceinline__ uint16_t ld_shared16(uint32_t addr) {
+    uint16_t x;
+    asm volatile("ld.shared.b16 %0, [%1];" : "=h"(x) : "r"(addr) : "memory");
+    return x;
+}
+
+// 32 rows x 64 columns of 16-bit values in a warp's buffer into rows row0...
+// and columns col0... of a row-major rows x cols matrix: whole 128-byte rows
+// where every row starts on 16 bytes (`vec`), value by value elsewhere.
+__device__ __forceinline__ void write_rows(unsigned short* dst, uint64_t ld, bool vec, uint32_t rows, uint32_t cols,
+                                           uint32_t row0, uint32_t col0, uint32_t buf) {
+    const uint32_t lane = threadIdx.x & 31;
+    if (vec) {
+#pragma unroll 4
+        for (uint32_t i = lane; i < 256; i += 32) {
+            const uint32_t r = i >> 3, j = i & 7, col = col0 + 8 * j;
+            if (row0 + r >= rows || col >= cols) continue;
+            unsigned short* out = dst + static_cast<uint64_t>(row0 + r) * ld + col;
+            const uint4 x = ld_shared(buf + piece128(r, j));
+            if (col + 8 <= cols) {
+                *reinterpret_cast<uint4*>(out) = x;
+            } else {
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (uint32_t e = 0; e < 8; ++e)
+                    if (col + e < cols) out[e] = static_cast<unsigned short>(w[e >> 1] >> (16 * (e & 1)));
+            }
+        }
+    } else {
+#pragma unroll 4
+        for (uint32_t i = lane; i < 32 * 64; i += 32) {
+            const uint32_t r = i >> 6, e = i & 63;
+            if (row0 + r < rows && col0 + e < cols)
+                dst[static_cast<uint64_t>(row0 + r) * ld + col0 + e] = ld_shared16(buf + piece128(r, e >> 3) + 2 * (e & 7));
+        }
+    }
 }
 
 // Lower-triangular tile t of a square grid of tiles: row i >= column j.
