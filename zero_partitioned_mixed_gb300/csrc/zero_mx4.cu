@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(kThreads) k_mx4_values(const __grid_constant__
 // two columns further on in tensor memory.
 struct MxProductArgs {
     uint32_t m, n, k;
-    uint32_t tiles_n, total;
+    uint32_t tiles_m, tiles_n, total;
     uint32_t tiles_k;        // scale tiles along k
     void* out;
     uint64_t ld;
@@ -308,10 +308,13 @@ constexpr int kMxThreads = 192;
 // A scale tile (32 lines of 16 bytes in shared memory) into 4 columns of
 // tensor memory, repeated in each quarter of the lanes, in both CTAs from
 // their own shared memory.
-__device__ __forceinline__ void tc_copy_scales(uint32_t tmem, uint32_t smem) {
+__device__ __forceinline__ uint64_t scale_desc(uint32_t smem) {
     uint64_t d = static_cast<uint64_t>((smem & 0x3FFFFu) >> 4);
     d |= static_cast<uint64_t>(128u >> 4) << 32;   // 8 lines of 16 bytes
     d |= static_cast<uint64_t>(1) << 46;
+    return d;
+}
+__device__ __forceinline__ void tc_copy_scales(uint32_t tmem, uint64_t d) {
     asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(d) : "memory");
 }
 __device__ __forceinline__ void mma_mx4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
@@ -321,6 +324,16 @@ __device__ __forceinline__ void mma_mx4(uint32_t d, uint64_t a, uint64_t b, uint
         "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
         ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(static_cast<uint32_t>(accumulate))
         : "memory");
+}
+
+// Tile t in bands of kBand tiles down, band after band: the tiles in flight
+// at a time then share their operands in both directions.
+constexpr uint32_t kBand = 8;
+__device__ __forceinline__ void mx_tile(const MxProductArgs& p, uint32_t t, uint32_t& tm, uint32_t& tn) {
+    const uint32_t band = t / (kBand * p.tiles_n), in = t - band * kBand * p.tiles_n;
+    const uint32_t high = min(kBand, p.tiles_m - band * kBand);   // the last band may be lower
+    tn = in / high;
+    tm = band * kBand + in - tn * high;
 }
 
 template <int DT>
@@ -364,62 +377,83 @@ k_mx4_product(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
     pdl_enter();
     const uint32_t nk = (p.k + kMxK - 1) / kMxK, stride = gridDim.x >> 1;
 
-    if (warp == 0 && lane == 0) {
+    if (warp == 0 && elect_one()) {
         const uint32_t leader_full = cluster_addr(full, 0);
-        uint32_t it = 0;
+        Ring<kMxStages> r;
         bool ok = true;
         for (uint32_t t = blockIdx.x >> 1; t < p.total && ok; t += stride) {
-            const uint32_t tm = t / p.tiles_n, tn = t - tm * p.tiles_n;
+            uint32_t tm, tn;
+            mx_tile(p, t, tm, tn);
             const int ra = static_cast<int>(tm * kMxM + rank * (kMxM / 2)), rb = static_cast<int>(tn * kMxN + rank * (kMxN / 2));
-            for (uint32_t kb = 0; kb < nk; ++kb, ++it) {
-                const uint32_t s = it % kMxStages;
-                if (it >= kMxStages && !bar_wait(empty + 8 * s, (it / kMxStages - 1) & 1, quit)) {
+            for (uint32_t kb = 0; kb < nk; ++kb, r.next()) {
+                if (!bar_wait(empty + 8 * r.s, r.parity ^ 1, quit)) {   // passes at once in the first round
                     ok = false;
                     break;
                 }
-                const uint32_t bar = leader_full + 8 * s, st = ring + s * kMxStage;
+                const uint32_t bar = leader_full + 8 * r.s, st = ring + r.s * kMxStage;
                 const uint32_t ss = st + kMxABytes + kMxBBytes;
-                if (rank == 0) bar_expect(full + 8 * s, 2 * kMxStage);   // the bytes of both CTAs
+                if (rank == 0) bar_expect(full + 8 * r.s, 2 * kMxStage);   // the bytes of both CTAs
                 copy_box_pair(st, &map_a, static_cast<int>(kb * 128), ra, 0, bar);
                 copy_box_pair(st + kMxABytes, &map_b, static_cast<int>(kb * 128), rb, 0, bar);
-                copy_box_pair(ss, &map_sa, static_cast<int>(kb * 256), ra >> 7, 0, bar);
-                copy_box_pair(ss + 1024, &map_sb, static_cast<int>(kb * 256), static_cast<int>(tn * kMxN) >> 7, 0, bar);
+                copy_box_pair(ss, &map_sa, 0, static_cast<int>(8 * kb), ra >> 7, bar);
+                copy_box_pair(ss + 1024, &map_sb, 0, static_cast<int>(8 * kb), static_cast<int>(tn * kMxN) >> 7, bar);
             }
         }
-    } else if (warp == 1 && lane == 0 && rank == 0) {
+    } else if (warp == 1 && rank == 0 && elect_one()) {
         // e2m1 operands, power-of-two scales, 256 x 192
         constexpr uint32_t idesc = (1u << 7) | (1u << 10) | (static_cast<uint32_t>(kMxN >> 3) << 17) | (1u << 23) |
                                    (static_cast<uint32_t>(kMxM >> 4) << 24);
-        uint32_t it = 0, n = 0;
+        const uint64_t desc0 = operand_desc(ring, 0), scales0 = scale_desc(ring + kMxABytes + kMxBBytes);
+        Ring<kMxStages> r, c;     // the products' stage, and that whose scales go into tensor memory next
+        uint32_t it = 0, copied = 0, n = 0;   // stages so far, of both
+        const uint32_t mine = blockIdx.x >> 1 < p.total ? (p.total - 1 - (blockIdx.x >> 1)) / stride + 1 : 0;
+        const uint32_t fills = mine * nk;
+        const uint32_t sf0 = tmem + 2 * kMxN;
+        auto copy_scales = [&]() {
+            const uint64_t ss = scales0 + c.s * (kMxStage >> 4);
+            const uint32_t sf = sf0 + (copied & 3) * 24;
+#pragma unroll
+            for (uint32_t h = 0; h < 2; ++h) {   // per 128 values: a scale tile of A's rows, two of B's
+                tc_copy_scales(sf + 4 * h, ss + (512 >> 4) * h);
+                tc_copy_scales(sf + 8 + 8 * h, ss + (1024 >> 4) + (512 >> 4) * h);
+                tc_copy_scales(sf + 12 + 8 * h, ss + (2048 >> 4) + (512 >> 4) * h);
+            }
+            ++copied;
+            c.next();
+        };
         bool ok = true;
         for (uint32_t t = blockIdx.x >> 1; t < p.total && ok; t += stride, ++n) {
             const uint32_t acc = n & 1, d = tmem + acc * kMxN;
-            const uint32_t odd = (t % p.tiles_n) & 1 ? 2u : 0u;   // columns that begin with a scale tile's row 64
+            uint32_t tm, tn;
+            mx_tile(p, t, tm, tn);
+            const uint32_t odd = tn & 1 ? 2u : 0u;   // columns that begin with a scale tile's row 64
             if (n >= 2 && !bar_wait(freed + 8 * acc, (n / 2 - 1) & 1, quit)) break;
             tc_fence_after();
-            for (uint32_t kb = 0; kb < nk; ++kb, ++it) {
-                const uint32_t s = it % kMxStages;
-                if (!bar_wait(full + 8 * s, (it / kMxStages) & 1, quit)) {
-                    ok = false;
-                    break;
+            for (uint32_t kb = 0; kb < nk; ++kb, ++it, r.next()) {
+                if (copied == it) {
+                    if (!bar_wait(full + 8 * c.s, c.parity, quit)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    copy_scales();
                 }
-                tc_fence_after();
-                const uint32_t st = ring + s * kMxStage, ss = st + kMxABytes + kMxBBytes;
-                const uint64_t da = operand_desc(st, 0), db = operand_desc(st + kMxABytes, 0);
-                const uint32_t sf = tmem + 2 * kMxN + (it & 1) * 24;
+                // the next stage's scales go ahead of this stage's products, which hide their way
+                if (copied < fills && bar_peek(full + 8 * c.s, c.parity)) {
+                    tc_fence_after();
+                    copy_scales();
+                }
+                const uint64_t da = desc0 + r.s * (kMxStage >> 4), db = da + (kMxABytes >> 4);
+                const uint32_t sf = sf0 + (it & 3) * 24;
 #pragma unroll
-                for (uint32_t h = 0; h < 2; ++h) {   // 128 values: a scale tile of A's rows, two of B's, two products
+                for (uint32_t h = 0; h < 2; ++h) {
                     if (2 * kb + h >= p.tiles_k) break;
-                    const uint32_t sa = sf + 4 * h, sb = sf + 8 + 8 * h;
-                    tc_copy_scales(sa, ss + 512 * h);
-                    tc_copy_scales(sb, ss + 1024 + 512 * h);
-                    tc_copy_scales(sb + 4, ss + 2048 + 512 * h);
 #pragma unroll
                     for (uint32_t j = 0; j < 2; ++j)
-                        mma_mx4(d, da + (2 * h + j) * 2, db + (2 * h + j) * 2, idesc | (2 * j << 4) | (2 * j << 29), sa,
-                                sb + odd, kb > 0 || h > 0 || j > 0);
+                        mma_mx4(d, da + (2 * h + j) * 2, db + (2 * h + j) * 2, idesc | (2 * j << 4) | (2 * j << 29), sf + 4 * h,
+                                sf + 8 + 8 * h + odd, kb > 0 || h > 0 || j > 0);
                 }
-                tc_commit_pair(empty + 8 * s);
+                tc_commit_pair(empty + 8 * r.s);
             }
             if (ok) tc_commit_pair(done + 8 * acc);
         }
@@ -432,7 +466,9 @@ k_mx4_product(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
         const uint32_t mine = ring + kMxStages * kMxStage + quarter * 2 * kMxOut;
         uint32_t n = 0;
         for (uint32_t t = blockIdx.x >> 1; t < p.total; t += stride, ++n) {
-            const uint32_t acc = n & 1, tm = t / p.tiles_n, tn = t - tm * p.tiles_n;
+            const uint32_t acc = n & 1;
+            uint32_t tm, tn;
+            mx_tile(p, t, tm, tn);
             const uint32_t row0 = tm * kMxM + rank * (kMxM / 2) + quarter * 32, col0 = tn * kMxN;
             const bool ok = bar_wait(done + 8 * acc, (n / 2) & 1, quit);
             if (__any_sync(0xFFFFFFFFu, !ok)) break;
@@ -601,6 +637,7 @@ int zero_mx4_matmul(int dtype, uint64_t m, uint64_t n, uint64_t k, const void* a
     p.m = static_cast<uint32_t>(m);
     p.n = static_cast<uint32_t>(n);
     p.k = static_cast<uint32_t>(k);
+    p.tiles_m = static_cast<uint32_t>(up(m, kMxM) / kMxM);
     p.tiles_n = static_cast<uint32_t>(up(n, kMxN) / kMxN);
     p.total = static_cast<uint32_t>(tiles);
     p.tiles_k = static_cast<uint32_t>(up(k, 128) / 128);
@@ -608,12 +645,12 @@ int zero_mx4_matmul(int dtype, uint64_t m, uint64_t n, uint64_t k, const void* a
     p.ld = ld;
     p.vec = aligned(out16, 16) && ld % 8 == 0;
     CUtensorMap ma, mb, sa, sb;
-    const uint64_t pitch = mx_pitch(k), words = static_cast<uint64_t>(p.tiles_k) * 128;   // of a row of scale tiles
     const CUtensorMapSwizzle plain = CU_TENSOR_MAP_SWIZZLE_NONE;
+    const uint64_t pitch = mx_pitch(k), lines = static_cast<uint64_t>(p.tiles_k) * 4;   // of 128 bytes, in a row of scale tiles
     if ((e = make_map(&ma, 1, a_codes, pitch, m, 1, pitch, m * pitch, 128, kMxM / 2)) != cudaSuccess ||
         (e = make_map(&mb, 1, b_codes, pitch, n, 1, pitch, n * pitch, 128, kMxN / 2)) != cudaSuccess ||
-        (e = make_map(&sa, 4, a_scales, words, up(m, 128) / 128, 1, words, words * (up(m, 128) / 128), 256, 1, plain)) != cudaSuccess ||
-        (e = make_map(&sb, 4, b_scales, words, up(n, 128) / 128, 1, words, words * (up(n, 128) / 128), 256, 2, plain)) != cudaSuccess)
+        (e = make_map(&sa, 1, a_scales, 128, lines, up(m, 128) / 128, 128, lines * 128, 128, 8, plain, 1)) != cudaSuccess ||
+        (e = make_map(&sb, 1, b_scales, 128, lines, up(n, 128) / 128, 128, lines * 128, 128, 8, plain, 2)) != cudaSuccess)
         return cuda_refuse(e, "tensor map");
     const unsigned grid = 2 * grid_of(tiles, sms / 2, 1);
     if (dtype == ZERO_FP16) {

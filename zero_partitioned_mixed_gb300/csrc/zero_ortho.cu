@@ -314,9 +314,9 @@ __global__ void __launch_bounds__(kProductThreads) k_ortho_products(const __grid
     tc_fence_after();
     const uint32_t tmem = s_tmem;
 
-    if (warp == 0 && lane == 0) {
+    if (warp == 0 && elect_one()) {
         const uint32_t leader_full = cluster_addr(full, 0);
-        uint32_t it = 0;   // fills so far
+        Ring<kStages> r;
         bool ok = true;
         Walk w(p);
         for (bool more = w.find(); more && ok; more = w.next()) {
@@ -328,15 +328,14 @@ __global__ void __launch_bounds__(kProductThreads) k_ortho_products(const __grid
             const int ra = static_cast<int>(w.tm * kTile + rank * kHalf);
             const int rb = static_cast<int>(w.tn * kTile + rank * kHalf), z = static_cast<int>(w.b);
             const bool a_mn = f.a_mn, b_mn = f.b_mn;
-            for (uint32_t kb = 0; kb < nk; ++kb, ++it) {
-                const uint32_t s = it % kStages;
-                if (it >= kStages && !bar_wait(empty + 8 * s, (it / kStages - 1) & 1, quit)) {
+            for (uint32_t kb = 0; kb < nk; ++kb, r.next()) {
+                if (!bar_wait(empty + 8 * r.s, r.parity ^ 1, quit)) {   // passes at once in the first round
                     ok = false;
                     break;
                 }
-                const uint32_t bar = leader_full + 8 * s, sa = ring + s * kStageBytes, sb = sa + kOperandBytes;
+                const uint32_t bar = leader_full + 8 * r.s, sa = ring + r.s * kStageBytes, sb = sa + kOperandBytes;
                 const int k0 = static_cast<int>(kb * kBlockK);
-                if (rank == 0) bar_expect(full + 8 * s, 2 * kStageBytes);   // the bytes of both CTAs
+                if (rank == 0) bar_expect(full + 8 * r.s, 2 * kStageBytes);   // the bytes of both CTAs
                 if (a_mn) {
                     copy_box_pair(sa, ma, ra, k0, z, bar);
                     copy_box_pair(sa + 8192, ma, ra + 64, k0, z, bar);
@@ -351,8 +350,10 @@ __global__ void __launch_bounds__(kProductThreads) k_ortho_products(const __grid
                 }
             }
         }
-    } else if (warp == 1 && lane == 0 && rank == 0) {
-        uint32_t it = 0, n = 0;
+    } else if (warp == 1 && rank == 0 && elect_one()) {
+        const uint64_t desc0 = operand_desc(ring, 8192);
+        Ring<kStages> r;
+        uint32_t n = 0;
         bool ok = true;
         Walk w(p);
         for (bool more = w.find(); more && ok; more = w.next(), ++n) {
@@ -365,19 +366,17 @@ __global__ void __launch_bounds__(kProductThreads) k_ortho_products(const __grid
             if (n >= 2 && !bar_wait(freed + 8 * acc, (n / 2 - 1) & 1, quit)) break;
             tc_fence_after();
             const uint32_t nk = (f.depth + kBlockK - 1) / kBlockK;
-            for (uint32_t kb = 0; kb < nk; ++kb, ++it) {
-                const uint32_t s = it % kStages;
-                if (!bar_wait(full + 8 * s, (it / kStages) & 1, quit)) {
+            for (uint32_t kb = 0; kb < nk; ++kb, r.next()) {
+                if (!bar_wait(full + 8 * r.s, r.parity, quit)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t sa = ring + s * kStageBytes;
-                const uint64_t da = operand_desc(sa, 8192), db = operand_desc(sa + kOperandBytes, 8192);
+                const uint64_t da = desc0 + r.s * (kStageBytes >> 4), db = da + (kOperandBytes >> 4);
 #pragma unroll
                 for (int k = 0; k < kBlockK / 16; ++k)
                     mma_f16_pair(d, da + k * step_a, db + k * step_b, idesc, kb > 0 || k > 0);
-                tc_commit_pair(empty + 8 * s);
+                tc_commit_pair(empty + 8 * r.s);
             }
             if (ok) tc_commit_pair(done + 8 * acc);
         }

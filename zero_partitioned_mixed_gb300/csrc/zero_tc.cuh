@@ -44,12 +44,12 @@ inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 // the 128-byte swizzle (or another); what lies outside the array reads as zero.
 inline cudaError_t make_map(CUtensorMap* map, int elem, const void* base, uint64_t cols, uint64_t rows, uint64_t batch,
                             uint64_t pitch, uint64_t matrix_stride, uint32_t box_cols, uint32_t box_rows,
-                            CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
+                            CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B, uint32_t box_batch = 1) {
     const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
     if (!encode) return cudaErrorNotSupported;
     const cuuint64_t dims[3] = {cols, rows, batch};
     const cuuint64_t strides[2] = {pitch * static_cast<uint64_t>(elem), matrix_stride * static_cast<uint64_t>(elem)};
-    const cuuint32_t box[3] = {box_cols, box_rows, 1};
+    const cuuint32_t box[3] = {box_cols, box_rows, box_batch};
     const cuuint32_t step[3] = {1, 1, 1};
     const CUresult r = encode(map, elem == 4   ? CU_TENSOR_MAP_DATA_TYPE_UINT32
                                    : elem == 2 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
@@ -96,6 +96,37 @@ __device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
+// One lane of a converged warp.  The compiler knows that a region under it has
+// one thread, and keeps the operands of the copies and products issued there
+// in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+// Whether the phase is complete, without waiting (bar_test may suspend the
+// thread for a while).
+__device__ __forceinline__ bool bar_peek(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// A place in a ring of N stages: its index, and the parity of its barriers'
+// phase in this round.
+template <uint32_t N>
+struct Ring {
+    uint32_t s = 0, parity = 0;
+    __device__ __forceinline__ void next() {
+        if (++s == N) {
+            s = 0;
+            parity ^= 1;
+        }
+    }
+};
 // Waits for the phase of parity `parity`; false when the wait gave up or
 // another role of the block had (`*quit`).  The time is looked at only after
 // a few hundred failed tries, each of which may itself suspend the thread.
