@@ -168,7 +168,10 @@ def _ptr_array(xs: Optional[Sequence]):
         return None
     if isinstance(xs, C.Array):
         return xs
-    return (C.c_void_p * max(1, len(xs)))(*[_ptr(x) for x in xs])
+    try:   # tensors throughout is the common case
+        return (C.c_void_p * max(1, len(xs)))(*[x.data_ptr() for x in xs])
+    except AttributeError:
+        return (C.c_void_p * max(1, len(xs)))(*[_ptr(x) for x in xs])
 
 
 def pointer_array(tensors: Sequence):

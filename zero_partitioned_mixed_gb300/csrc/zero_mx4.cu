@@ -511,8 +511,172 @@ k_mx4_product(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
     cluster_sync();
 }
 
+// ------------------------------------------------- product with few rows
+// Up to 128 rows of A (a token, a handful, a small batch): bound by reading
+// B once.  B's rows are the tensor cores' 128 rows and A's the columns (NT of
+// them), a CTA takes 128 of B's rows over a share of k, and the CTAs of a
+// cluster add up their shares through shared memory, in order of rank.  The
+// shares are chosen so that about two CTAs an SM have their copies in flight
+// from the start.
+struct MxNarrowArgs {
+    uint32_t m, n;
+    uint32_t tiles_k, stages;   // scale tiles along k; stages of 256 values
+    uint32_t split;             // CTAs a cluster
+    void* out;
+    uint64_t ld;
+};
+
+constexpr int kNarrowThreads = 192, kNarrowStages = 3;
+template <int NT>
+struct Narrow {
+    static constexpr uint32_t kB = 128 * 128, kA = NT * 128, kStage = kB + kA + 2048;   // and 1 KiB of scales each
+    static constexpr size_t kSmem = 1024 + kNarrowStages * kStage;
+    static constexpr uint32_t kTmem = NT <= 64 ? 128 : 256;   // the accumulator and four sets of scales
+    static_assert(kNarrowStages * kStage >= NT * 512, "the partial sums take the ring's place");
+};
+
+__device__ __forceinline__ void tc_copy_scales_one(uint32_t tmem, uint64_t d) {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(d) : "memory");
+}
+__device__ __forceinline__ void mma_mx4_one(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
+                                            bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(static_cast<uint32_t>(accumulate))
+        : "memory");
+}
+template <int DT, int NT>
+__global__ void __launch_bounds__(kNarrowThreads)
+k_mx4_narrow(const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_a,
+             const __grid_constant__ CUtensorMap map_sb, const __grid_constant__ CUtensorMap map_sa,
+             const __grid_constant__ MxNarrowArgs p) {
+    using L = Narrow<NT>;
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ __align__(8) uint64_t bars[2 * kNarrowStages + 1];
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_quit;
+    volatile int* quit = &s_quit;
+    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = p.split > 1 ? cluster_rank() : 0, tile = blockIdx.x / p.split;
+    const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const uint32_t full = smem_u32(bars), empty = full + 8 * kNarrowStages, done = empty + 8 * kNarrowStages;
+    const uint32_t k0 = rank * p.stages / p.split, k1 = (rank + 1) * p.stages / p.split;
+    if (threadIdx.x == 0) {
+        s_quit = 0;
+        for (int i = 0; i < 2 * kNarrowStages + 1; ++i) bar_init(full + 8 * i, 1);
+        bar_init_fence();
+        prefetch_map(&map_b);
+        prefetch_map(&map_a);
+    }
+    if (warp == 1) tmem_alloc(smem_u32(&s_tmem), L::kTmem);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    pdl_enter();
+
+    if (warp == 0 && elect_one()) {
+        Ring<kNarrowStages> r;
+        uint32_t kb = k0;
+        for (; kb < k1; ++kb, r.next()) {
+            if (!bar_wait(empty + 8 * r.s, r.parity ^ 1, quit)) break;
+            const uint32_t bar = full + 8 * r.s, st = ring + r.s * L::kStage;
+            bar_expect(bar, L::kStage);
+            copy_box(st, &map_b, static_cast<int>(kb * 128), static_cast<int>(tile * 128), 0, bar);
+            copy_box(st + L::kB, &map_a, static_cast<int>(kb * 128), 0, 0, bar);
+            copy_box(st + L::kB + L::kA, &map_sb, 0, static_cast<int>(8 * kb), static_cast<int>(tile), bar);
+            copy_box(st + L::kB + L::kA + 1024, &map_sa, 0, static_cast<int>(8 * kb), 0, bar);
+        }
+    } else if (warp == 1 && elect_one()) {
+        constexpr uint32_t idesc = (1u << 7) | (1u << 10) | (static_cast<uint32_t>(NT >> 3) << 17) | (1u << 23) | (8u << 24);
+        const uint64_t desc0 = operand_desc(ring, 0), scales0 = scale_desc(ring + L::kB + L::kA);
+        Ring<kNarrowStages> r;
+        bool ok = true;
+        for (uint32_t kb = k0; kb < k1; ++kb, r.next()) {
+            if (!bar_wait(full + 8 * r.s, r.parity, quit)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const uint64_t db = desc0 + r.s * (L::kStage >> 4), da = db + (L::kB >> 4), ss = scales0 + r.s * (L::kStage >> 4);
+            const uint32_t sf = tmem + NT + ((kb - k0) & 3) * 16;
+#pragma unroll
+            for (uint32_t h = 0; h < 2; ++h) {
+                tc_copy_scales_one(sf + 4 * h, ss + (512 >> 4) * h);
+                tc_copy_scales_one(sf + 8 + 4 * h, ss + (1024 >> 4) + (512 >> 4) * h);
+            }
+#pragma unroll
+            for (uint32_t h = 0; h < 2; ++h) {
+                if (2 * kb + h >= p.tiles_k) break;
+#pragma unroll
+                for (uint32_t j = 0; j < 2; ++j)
+                    mma_mx4_one(tmem, db + (2 * h + j) * 2, da + (2 * h + j) * 2, idesc | (2 * j << 4) | (2 * j << 29),
+                                sf + 4 * h, sf + 8 + 4 * h, kb > k0 || h > 0 || j > 0);
+            }
+            tc_commit(empty + 8 * r.s);
+        }
+        tc_commit(done);
+        if (!ok) bar_drain(done, 0);
+    } else if (warp >= 2) {
+        // partial sums [column][128 rows] where the ring was
+        const bool ok = bar_wait(done, 0, quit);
+        const uint32_t row = (warp & 3) * 32 + lane;
+        if (!__any_sync(0xFFFFFFFFu, !ok)) {
+            tc_fence_after();
+#pragma unroll
+            for (uint32_t c = 0; c < NT; c += 16) {
+                float v[16];
+                tmem_load16(tmem + c + ((warp & 3) << 21), v);
+#pragma unroll
+                for (uint32_t e = 0; e < 16; ++e) st_shared(ring + (c + e) * 512 + row * 4, __float_as_uint(v[e]));
+            }
+        }
+    }
+    __syncwarp();
+    if (*quit && threadIdx.x == 0) {   // copies in flight land within microseconds: leave them a millisecond
+        const uint64_t t0 = now_ns();
+        while (now_ns() - t0 < 1000000ull) {}
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (p.split > 1) cluster_sync();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_free(tmem, L::kTmem);
+    }
+    // this CTA's share of the rows, four at a time, for all columns
+    const uint32_t rows = 128 / p.split, fours = rows / 4;   // split is a power of two, at most 8
+    const uint32_t first = tile * 128 + rank * rows;
+    unsigned short* out = static_cast<unsigned short*>(p.out) + first;
+    const bool whole = (reinterpret_cast<uintptr_t>(out) & 7) == 0 && (p.ld & 3) == 0;
+    for (uint32_t i = threadIdx.x; i < fours * p.m; i += kNarrowThreads) {
+        const uint32_t c = i / fours, r = (i - c * fours) * 4;
+        if (first + r >= p.n) continue;
+        const uint32_t at = ring + c * 512 + (rank * rows + r) * 4;
+        float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+        for (uint32_t q = 0; q < p.split; ++q) {
+            const float4 y = ld_cluster(cluster_addr(at, q));
+            s.x += y.x; s.y += y.y; s.z += y.z; s.w += y.w;
+        }
+        const uint32_t lo = narrow2<DT>(s.x, s.y), hi = narrow2<DT>(s.z, s.w);
+        unsigned short* to = out + c * p.ld + r;
+        if (whole && first + r + 4 <= p.n) {
+            *reinterpret_cast<uint2*>(to) = make_uint2(lo, hi);
+        } else {
+#pragma unroll
+            for (uint32_t e = 0; e < 4; ++e)
+                if (first + r + e < p.n) to[e] = static_cast<unsigned short>((e < 2 ? lo : hi) >> (16 * (e & 1)));
+        }
+    }
+    if (p.split > 1) cluster_sync();   // the others may still be reading here
+}
+
 // -------------------------------------------------------------------- host
 constexpr uint64_t kMaxSide = 1ull << 30;
+constexpr size_t kSmemPerSm = 228 * 1024;   // each CTA takes 1 KiB more than it asks for
 
 uint64_t mx_pitch(uint64_t cols) { return up(cols, kMxBlock) / 2; }
 
@@ -535,6 +699,46 @@ dim3 row_grid(uint64_t rows, uint64_t cols) {
 unsigned grid_of(uint64_t blocks, int sms, int per_sm) {
     const uint64_t cap = static_cast<uint64_t>(sms) * per_sm;
     return static_cast<unsigned>(blocks < 1 ? 1 : blocks < cap ? blocks : cap);
+}
+
+// The map of a matrix of codes in boxes of `box_rows` rows, and of its scale
+// tiles in boxes of 1 KiB (two tiles along k) by `box_tiles`.
+cudaError_t mx_maps(CUtensorMap* codes_map, CUtensorMap* scales_map, const void* codes, const void* scales, uint64_t rows,
+                    uint64_t k, uint32_t box_rows, uint32_t box_tiles) {
+    const uint64_t pitch = mx_pitch(k), lines = up(k, 128) / 128 * 4;   // lines of 128 bytes in a row of scale tiles
+    const cudaError_t e = make_map(codes_map, 1, codes, pitch, rows, 1, pitch, rows * pitch, 128, box_rows);
+    return e != cudaSuccess ? e
+                            : make_map(scales_map, 1, scales, 128, lines, up(rows, 128) / 128, 128, lines * 128, 128, 8,
+                                       CU_TENSOR_MAP_SWIZZLE_NONE, box_tiles);
+}
+
+template <int NT>
+cudaError_t narrow_of(int dtype, uint64_t m, uint64_t n, uint64_t k, const void* a_codes, const void* a_scales,
+                      const void* b_codes, const void* b_scales, void* out, uint64_t ld, cudaStream_t s) {
+    CUtensorMap ma, mb, sa, sb;
+    int sms = 0;
+    cudaError_t e;
+    if ((e = sm_count(&sms)) != cudaSuccess || (e = mx_maps(&ma, &sa, a_codes, a_scales, m, k, NT, 1)) != cudaSuccess ||
+        (e = mx_maps(&mb, &sb, b_codes, b_scales, n, k, 128, 1)) != cudaSuccess)
+        return e;
+    MxNarrowArgs p = {};
+    p.m = static_cast<uint32_t>(m);
+    p.n = static_cast<uint32_t>(n);
+    p.tiles_k = static_cast<uint32_t>(up(k, 128) / 128);
+    p.stages = static_cast<uint32_t>(up(k, kMxK) / kMxK);
+    p.out = out;
+    p.ld = ld;
+    const uint64_t tiles = up(n, 128) / 128;
+    // shares of k: up to 8, as long as all CTAs are resident at once (by their shared memory) and a share keeps two stages
+    const uint64_t resident = static_cast<uint64_t>(sms) * (kSmemPerSm / (Narrow<NT>::kSmem + 1024));
+    for (p.split = 1; p.split < 8 && 2 * tiles * p.split <= resident && p.stages >= 4 * p.split;) p.split *= 2;
+    const dim3 grid(static_cast<unsigned>(tiles * p.split));
+    if (dtype == ZERO_FP16) {
+        if ((e = allow_smem<k_mx4_narrow<kFp16, NT>>(Narrow<NT>::kSmem)) != cudaSuccess) return e;
+        return launch_pdl(k_mx4_narrow<kFp16, NT>, grid, kNarrowThreads, Narrow<NT>::kSmem, p.split, s, mb, ma, sb, sa, p);
+    }
+    if ((e = allow_smem<k_mx4_narrow<kBf16, NT>>(Narrow<NT>::kSmem)) != cudaSuccess) return e;
+    return launch_pdl(k_mx4_narrow<kBf16, NT>, grid, kNarrowThreads, Narrow<NT>::kSmem, p.split, s, mb, ma, sb, sa, p);
 }
 
 }  // namespace
@@ -629,6 +833,13 @@ int zero_mx4_matmul(int dtype, uint64_t m, uint64_t n, uint64_t k, const void* a
         e = cudaMemset2DAsync(out16, ld * 2, 0, n * 2, m, s);
         return e == cudaSuccess ? ZERO_OK : cuda_refuse(e, "zero_mx4_matmul");
     }
+    if (m <= 128) {
+        e = m <= 16 ? narrow_of<16>(dtype, m, n, k, a_codes, a_scales, b_codes, b_scales, out16, ld, s)
+            : m <= 32 ? narrow_of<32>(dtype, m, n, k, a_codes, a_scales, b_codes, b_scales, out16, ld, s)
+            : m <= 64 ? narrow_of<64>(dtype, m, n, k, a_codes, a_scales, b_codes, b_scales, out16, ld, s)
+                      : narrow_of<128>(dtype, m, n, k, a_codes, a_scales, b_codes, b_scales, out16, ld, s);
+        return e == cudaSuccess ? ZERO_OK : cuda_refuse(e, "zero_mx4_matmul");
+    }
     const uint64_t tiles = up(m, kMxM) / kMxM * (up(n, kMxN) / kMxN);
     if (tiles > 0x7FFFFFFFull) return refuse(ZERO_EINVAL, "m and n are too large together");
     int sms = 0;
@@ -645,12 +856,8 @@ int zero_mx4_matmul(int dtype, uint64_t m, uint64_t n, uint64_t k, const void* a
     p.ld = ld;
     p.vec = aligned(out16, 16) && ld % 8 == 0;
     CUtensorMap ma, mb, sa, sb;
-    const CUtensorMapSwizzle plain = CU_TENSOR_MAP_SWIZZLE_NONE;
-    const uint64_t pitch = mx_pitch(k), lines = static_cast<uint64_t>(p.tiles_k) * 4;   // of 128 bytes, in a row of scale tiles
-    if ((e = make_map(&ma, 1, a_codes, pitch, m, 1, pitch, m * pitch, 128, kMxM / 2)) != cudaSuccess ||
-        (e = make_map(&mb, 1, b_codes, pitch, n, 1, pitch, n * pitch, 128, kMxN / 2)) != cudaSuccess ||
-        (e = make_map(&sa, 1, a_scales, 128, lines, up(m, 128) / 128, 128, lines * 128, 128, 8, plain, 1)) != cudaSuccess ||
-        (e = make_map(&sb, 1, b_scales, 128, lines, up(n, 128) / 128, 128, lines * 128, 128, 8, plain, 2)) != cudaSuccess)
+    if ((e = mx_maps(&ma, &sa, a_codes, a_scales, m, k, kMxM / 2, 1)) != cudaSuccess ||
+        (e = mx_maps(&mb, &sb, b_codes, b_scales, n, k, kMxN / 2, 2)) != cudaSuccess)
         return cuda_refuse(e, "tensor map");
     const unsigned grid = 2 * grid_of(tiles, sms / 2, 1);
     if (dtype == ZERO_FP16) {

@@ -44,19 +44,27 @@ constexpr int kMaxPhases = 3 * ZERO_MAX_NS_STEPS + 3;
 // little over 1, those of p(A) and Q at most a^2 or so.
 constexpr float kScaleX = 8192.0f, kScaleA = 4096.0f, kScaleB = 128.0f;
 
-// ------------------------------------------------------- norm and packing
-// A matrix is read in units of kPackRows rows by 256 columns, one warp a
-// unit, 8 values a lane and row, the rows' loads in flight together.
+// ----------------------------------------------------- scaling and packing
+// X0 = G 2^k in fp16, k such that the largest magnitude lies in [2^12, 2^13),
+// and g0 = 1 / ||X0||, which the products that read X0 take into their scale.
+// Scaled like that, squares and their sums stay in fp32's range whatever G's
+// magnitudes are (a value whose square underflows is 2^-70 of the largest).
+// One pass finds the largest magnitude, one packs and sums the squares; both
+// are streams, the second mostly out of L2.  A matrix is read in units of
+// kPackRows rows by 256 columns, one warp a unit, 8 values a lane and row,
+// the rows' loads in flight together.
 constexpr int kPackRows = 4;
-constexpr int kPartials = 1024;   // partial sums of squares of one matrix, at most
 constexpr int kPackWarps = kThreads / 32;
+constexpr uint32_t kTopBlocks = 1024;   // blocks of the first pass for one matrix, at most
 
 struct PackArgs {
     const void* src[kMaxMatrices];
     uint64_t rows, cols, ld, pitch;
     uint32_t segments, units;   // 256-column segments a row; units a matrix
-    int partials;
-    double* partial;            // [batch][kPartials]
+    uint32_t tops, sums;        // blocks a matrix of the two passes
+    uint32_t* top;              // [batch][kTopBlocks] largest magnitudes, as 16-bit patterns
+    float* sum;                 // [batch][sums] sums of squares of X0
+    uint32_t* ticket;           // [batch] finished blocks of the second pass
     float* g0;                  // [batch]
     uint32_t* done;             // [batch][kMaxPhases], cleared for the products
     __half* x0;                 // [batch][rows][pitch]
@@ -81,107 +89,119 @@ __device__ __forceinline__ void load_unit(const PackArgs& a, int b, uint32_t u, 
     for (int r = 0; r < kPackRows; ++r) clear_from(w[r], valid);
 }
 
-// Sum of squares: the 32 values of a unit in fp32, everything above in fp64.
-// Values whose squares could leave fp32's range are squared in fp64.
+// Block-wide results in every thread, in a fixed order.
+__device__ __forceinline__ uint32_t block_top(uint32_t x) {
+    __shared__ uint32_t s[32];
+    x = __reduce_max_sync(0xFFFFFFFFu, x);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = x;
+    __syncthreads();
+    x = 0;
+    for (uint32_t i = 0; i < blockDim.x / 32; ++i) x = max(x, s[i]);
+    return x;
+}
+__device__ __forceinline__ float block_sum32(float x) {
+    __shared__ float s[32];
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, off);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = x;
+    __syncthreads();
+    x = 0.0f;
+    for (uint32_t i = 0; i < blockDim.x / 32; ++i) x += s[i];
+    return x;
+}
+
+// The two factors of 2^k (each a normal fp32 number) from the largest
+// magnitude's pattern; 1 for a zero matrix.  An infinity or a NaN stays one.
 template <int DT>
-__global__ void __launch_bounds__(kThreads) k_ortho_norm(const __grid_constant__ PackArgs a) {
+__device__ __forceinline__ void scale_factors(uint32_t top, float& m0, float& m1) {
+    const float x = widen<DT>(top);
+    const int e = x > 0.0f && x < INFINITY ? 12 - ilogbf(x) : 0;
+    m0 = ldexpf(1.0f, e / 2);
+    m1 = ldexpf(1.0f, e - e / 2);
+}
+// g0 from the sum of squares of X0: 0 for a zero matrix, NaN where G has an
+// infinity or a NaN.
+__device__ __forceinline__ float inverse_norm(float sum, uint32_t top, uint32_t infinite) {
+    return top >= infinite ? NAN : top == 0u ? 0.0f : 1.0f / sqrtf(sum);
+}
+template <int DT>
+__device__ constexpr uint32_t infinity_pattern() { return DT == kBf16 ? 0x7F80u : 0x7C00u; }
+
+// 8 packed values times m0 m1 in fp16; adds their squares to `sum`.
+template <int DT>
+__device__ __forceinline__ void scale8(const uint32_t (&w)[4], float m0, float m1, uint32_t (&q)[4], float& sum) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        float lo, hi;
+        widen2<DT>(w[e], lo, hi);
+        mul2(lo, hi, m0);
+        mul2(lo, hi, m1);
+        sum = __fmaf_rn(hi, hi, __fmaf_rn(lo, lo, sum));
+        q[e] = narrow2<kFp16>(lo, hi);
+    }
+}
+
+__global__ void __launch_bounds__(kThreads) k_ortho_top(const __grid_constant__ PackArgs a) {
     pdl_enter();
     const int b = blockIdx.y;
-    if (blockIdx.x == 0)
+    if (blockIdx.x == 0) {
         for (int i = threadIdx.x; i < kMaxPhases; i += kThreads) a.done[static_cast<uint64_t>(b) * kMaxPhases + i] = 0u;
-    double acc = 0.0;
+        if (threadIdx.x == 0) a.ticket[b] = 0u;
+    }
+    uint32_t top = 0;
     for (uint32_t u = blockIdx.x * kPackWarps + (threadIdx.x >> 5); u < a.units; u += gridDim.x * kPackWarps) {
         uint64_t row0, c;
         uint32_t w[kPackRows][4];
         load_unit(a, b, u, row0, c, w);
-        float sum = 0.0f;
-        uint32_t top = 0;
 #pragma unroll
-        for (int r = 0; r < kPackRows; ++r) {
-            float s0 = 0.0f, s1 = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float lo, hi;
-                widen2<DT>(w[r][e], lo, hi);
-                s0 = __fmaf_rn(lo, lo, s0);
-                s1 = __fmaf_rn(hi, hi, s1);
-            }
-            sum += s0 + s1;
-            top = max(top, top_pattern(w[r]));
-        }
-        const float most = widen<DT>(top);
-        if (!(most < 0x1p60f) || (most > 0.0f && most < 0x1p-50f)) {
-            double d = 0.0;
-#pragma unroll
-            for (int i = 0; i < kPackRows * 8; ++i) {
-                const double x = static_cast<double>(widen<DT>((w[i >> 3][(i >> 1) & 3] >> (16 * (i & 1))) & 0xFFFFu));
-                d = fma(x, x, d);
-            }
-            acc += d;
-        } else {
-            acc += static_cast<double>(sum);
-        }
+        for (int r = 0; r < kPackRows; ++r) top = max(top, top_pattern(w[r]));
     }
-    const double t = block_sum(acc);
-    if (threadIdx.x == 0) a.partial[static_cast<uint64_t>(b) * kPartials + blockIdx.x] = t;
+    top = block_top(top);
+    if (threadIdx.x == 0) a.top[static_cast<uint64_t>(b) * kTopBlocks + blockIdx.x] = top;
 }
 
-// From ||G||: 2^k as two factors (each a normal fp32 number), k such that
-// ||G|| 2^k lies in [2^12, 2^13), and g0 = 1 / (||G|| 2^k).  A zero matrix
-// gives g0 = 0; infinities and NaN give a NaN g0.
-__device__ void norm_factors(double norm, float& m0, float& m1, float& g0) {
-    int e = 0;
-    g0 = 0.0f;
-    if (norm > 0.0 && norm < INFINITY) {
-        frexp(norm, &e);   // norm = f 2^e, f in [1/2, 1)
-        e = 13 - e;
-        g0 = static_cast<float>(1.0 / ldexp(norm, e));
-    } else if (!(norm == 0.0)) {
-        g0 = NAN;
-    }
-    m0 = ldexpf(1.0f, e / 2);
-    m1 = ldexpf(1.0f, e - e / 2);
-}
-
-// X0 = G 2^k in fp16, and g0, which the products that read X0 take into
-// their scale.
-// One unit a warp, its loads in flight while the norm is put together.
+// One unit a warp, its loads in flight while the scale is put together; the
+// last block of a matrix adds up the sums.
 template <int DT>
 __global__ void __launch_bounds__(kThreads) k_ortho_pack(const __grid_constant__ PackArgs a) {
     pdl_enter();
-    __shared__ float s_mul[2];
+    __shared__ int s_last;
     const int b = blockIdx.y;
     const uint32_t u = blockIdx.x * kPackWarps + (threadIdx.x >> 5);
     uint64_t row0 = a.rows, c = a.cols;
     uint32_t w[kPackRows][4] = {};
     if (u < a.units) load_unit(a, b, u, row0, c, w);
-    double part = 0.0;
-    for (int i = threadIdx.x; i < a.partials; i += kThreads) part += a.partial[static_cast<uint64_t>(b) * kPartials + i];
-    const double t = block_sum(part);
+    uint32_t top = 0;
+    for (uint32_t i = threadIdx.x; i < a.tops; i += kThreads) top = max(top, a.top[static_cast<uint64_t>(b) * kTopBlocks + i]);
+    top = block_top(top);
+    float m0, m1, sum = 0.0f;
+    scale_factors<DT>(top, m0, m1);
+    if (c < a.cols) {
+        __half* out = a.x0 + (static_cast<uint64_t>(b) * a.rows + row0) * a.pitch + c;
+#pragma unroll
+        for (int r = 0; r < kPackRows; ++r, out += a.pitch) {
+            if (row0 + r >= a.rows) break;
+            uint32_t q[4];
+            scale8<DT>(w[r], m0, m1, q, sum);
+            // whole eights: the pitch is a multiple of 8
+            *reinterpret_cast<uint4*>(out) = make_uint4(q[0], q[1], q[2], q[3]);
+        }
+    }
+    sum = block_sum32(sum);
     if (threadIdx.x == 0) {
-        float g;
-        norm_factors(sqrt(t), s_mul[0], s_mul[1], g);
-        if (blockIdx.x == 0) a.g0[b] = g;
+        a.sum[static_cast<uint64_t>(b) * a.sums + blockIdx.x] = sum;
+        __threadfence();
+        s_last = atomicAdd(&a.ticket[b], 1u) == gridDim.x - 1;
     }
     __syncthreads();
-    const float m0 = s_mul[0], m1 = s_mul[1];
-    if (c >= a.cols) return;
-#pragma unroll
-    for (int r = 0; r < kPackRows; ++r) {
-        if (row0 + r >= a.rows) break;
-        uint32_t q[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            float lo, hi;
-            widen2<DT>(w[r][e], lo, hi);
-            mul2(lo, hi, m0);
-            mul2(lo, hi, m1);
-            q[e] = narrow2<kFp16>(lo, hi);
-        }
-        // whole eights: the pitch is a multiple of 8
-        *reinterpret_cast<uint4*>(a.x0 + (static_cast<uint64_t>(b) * a.rows + row0 + r) * a.pitch + c) =
-            make_uint4(q[0], q[1], q[2], q[3]);
-    }
+    if (!s_last) return;
+    __threadfence();
+    sum = 0.0f;
+    for (uint32_t i = threadIdx.x; i < a.sums; i += kThreads) sum += __ldcg(a.sum + static_cast<uint64_t>(b) * a.sums + i);
+    sum = block_sum32(sum);
+    if (threadIdx.x == 0) a.g0[b] = inverse_norm(sum, top, infinity_pattern<DT>());
 }
 
 // ---------------------------------------------------------------- products
@@ -545,17 +565,9 @@ struct SmallArgs {
     float coeffs[3 * ZERO_MAX_NS_STEPS];
 };
 
-__device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
-    float4 x;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
-                 : "r"(addr)
-                 : "memory");
-    return x;
-}
-__device__ __forceinline__ double ld_cluster_f64(uint32_t addr) {
-    double x;
-    asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(x) : "r"(addr) : "memory");
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
+    uint32_t x;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(addr) : "memory");
     return x;
 }
 __device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t x, uint32_t y) {
@@ -588,8 +600,8 @@ __global__ void __launch_bounds__(kSmallThreads) k_ortho_small(const __grid_cons
     __shared__ __align__(8) uint64_t s_bar;
     __shared__ uint32_t s_tmem;
     __shared__ int s_quit;
-    __shared__ double s_sum;
-    __shared__ float s_mul[3];
+    __shared__ uint32_t s_top;
+    __shared__ float s_sum;
     volatile int* quit = &s_quit;
     const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = p.ctas > 1 ? cluster_rank() : 0, b = blockIdx.x / p.ctas;
@@ -610,15 +622,15 @@ __global__ void __launch_bounds__(kSmallThreads) k_ortho_small(const __grid_cons
     tc_fence_after();
     const uint32_t tmem = s_tmem;
 
-    // G as it is into X (transposed when tall), and its sum of squares
+    // G as it is into X (transposed when tall), and its largest magnitude
     const unsigned short* src = static_cast<const unsigned short*>(p.src[b]);
     const uint32_t in_rows = p.tall ? span : p.side, in_cols = p.tall ? p.side : span;
     const uint32_t eights = (in_cols + 7) / 8, pieces = in_rows * eights;
     if (p.tall) src += static_cast<uint64_t>(first) * p.ld_src;
     else src += first;
+    uint32_t top = 0;
     {
         const bool whole = (reinterpret_cast<uintptr_t>(src) & 15) == 0 && p.ld_src % 8 == 0;
-        double acc = 0.0;
         for (uint32_t i0 = tid; i0 < pieces; i0 += 4 * kSmallThreads) {
             uint32_t w[4][4];
 #pragma unroll
@@ -630,21 +642,7 @@ __global__ void __launch_bounds__(kSmallThreads) k_ortho_small(const __grid_cons
             for (uint32_t k = 0; k < 4; ++k) {
                 const uint32_t i = i0 + k * kSmallThreads, r = i / eights, c = (i - r * eights) * 8;
                 if (i >= pieces) break;
-                float s = 0.0f;
-                double d = 0.0;
-                const float top = widen<DT>(top_pattern(w[k]));
-                const bool far = !(top < 0x1p60f) || (top > 0.0f && top < 0x1p-50f);   // squares leave fp32's range
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float lo, hi;
-                    widen2<DT>(w[k][e], lo, hi);
-                    s = __fmaf_rn(hi, hi, __fmaf_rn(lo, lo, s));
-                    if (far) {
-                        d = fma(static_cast<double>(lo), static_cast<double>(lo), d);
-                        d = fma(static_cast<double>(hi), static_cast<double>(hi), d);
-                    }
-                }
-                acc += far ? d : static_cast<double>(s);
+                top = max(top, top_pattern(w[k]));
                 if (p.tall) {
 #pragma unroll
                     for (uint32_t e = 0; e < 8; ++e)
@@ -656,100 +654,114 @@ __global__ void __launch_bounds__(kSmallThreads) k_ortho_small(const __grid_cons
                 }
             }
         }
-        const double t = block_sum(acc);
-        if (tid == 0) s_sum = t;
     }
-    if (p.ctas > 1) cluster_sync();
-    if (tid == 0) {
-        double t = 0.0;
-        if (p.ctas > 1)
-            for (uint32_t q = 0; q < p.ctas; ++q) t += ld_cluster_f64(cluster_addr(smem_u32(&s_sum), q));
-        else
-            t = s_sum;
-        norm_factors(sqrt(t), s_mul[0], s_mul[1], s_mul[2]);
+    top = block_top(top);
+    if (p.ctas > 1) {
+        if (tid == 0) s_top = top;
+        cluster_sync();
+        for (uint32_t q = 0; q < p.ctas; ++q) top = max(top, ld_cluster_u32(cluster_addr(smem_u32(&s_top), q)));
     }
-    __syncthreads();
-    const float g0 = s_mul[2];
-    for (uint32_t i = tid; i < blocks * (kBlockBytes / 16); i += kSmallThreads) {   // X0 = G 2^k, in place
+    // X0 = G 2^k in place, and its sum of squares
+    float m0, m1, sum = 0.0f;
+    scale_factors<DT>(top, m0, m1);
+    for (uint32_t i = tid; i < blocks * (kBlockBytes / 16); i += kSmallThreads) {
         const uint4 v = ld_shared(x + 16 * i);
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
         uint32_t q[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            float lo, hi;
-            widen2<DT>(w[e], lo, hi);
-            mul2(lo, hi, s_mul[0]);
-            mul2(lo, hi, s_mul[1]);
-            q[e] = narrow2<kFp16>(lo, hi);
-        }
+        scale8<DT>(w, m0, m1, q, sum);
         st_shared(x + 16 * i, q[0], q[1], q[2], q[3]);
     }
+    sum = block_sum32(sum);
+    if (p.ctas > 1) {
+        if (tid == 0) s_sum = sum;
+        cluster_sync();
+        sum = 0.0f;
+        for (uint32_t q = 0; q < p.ctas; ++q) sum += __uint_as_float(ld_cluster_u32(cluster_addr(smem_u32(&s_sum), q)));
+    }
+    const float g0 = inverse_norm(sum, top, infinity_pattern<DT>());
 
     // Products: every thread's writes before it are seen by the tensor cores,
     // one thread issues, all wait.
     uint32_t parity = 0;
     const uint32_t steps_k = (p.side + 15) / 16;
     auto begin = [&]() {
-        proxy_fence();
+        proxy_fence_shared();
         tc_fence_before();
         __syncthreads();
         tc_fence_after();
     };
     auto finish = [&]() {
-        if (tid == 0) tc_commit(bar);
         bar_wait(bar, parity, quit);
         parity ^= 1;
         tc_fence_after();
     };
     constexpr uint32_t kIdesc = (1u << 4) | (static_cast<uint32_t>(kSide >> 4) << 24);
-    // this thread's part of a 128 x 128 result
-    const uint32_t row = (warp & 3) * 32 + lane, half = (warp >> 2) * 64;
-    // squares[to] = f acc (+ f_lin squares[lin] + f_diag I), acc in the first 128 columns
+    // this thread's part of a 128 x 128 result: 64 columns of a row
+    const uint32_t row = (warp & 3) * 32 + lane, half = warp >> 2;
+    const uint32_t my_tmem = tmem + half * 64 + ((warp & 3) << 21), my_piece = half * kBlockBytes;
+    // to = f acc (+ f_lin lin + f_diag I), acc in the first 128 columns
     auto square_out = [&](uint32_t to, float f, bool poly, uint32_t lin, float f_lin, float f_diag) {
-#pragma unroll 1
-        for (uint32_t h = 0; h < 64; h += 32) {
-            float v[32];
-            tmem_load32(tmem + half + h + ((warp & 3) << 21), v);
-            const uint32_t at = (half >> 6) * kBlockBytes;
+        uint32_t v[2][32];
+        tmem_start32(my_tmem, v[0]);
+        tmem_start32(my_tmem + 32, v[1]);
+        tmem_wait(v[0]);
+        tmem_wait(v[1]);
+        const bool diagonal = poly && row < p.side;
+#pragma unroll
+        for (uint32_t h = 0; h < 2; ++h) {
+            // the diagonal crosses this warp's rows in one group of 32 columns
+            const uint32_t diag = diagonal && 2 * half + h == (warp & 3) ? lane : 64u;
 #pragma unroll
             for (uint32_t j = 0; j < 4; ++j) {
-                uint32_t q[4];
-                const uint32_t piece = at + piece128(row, (h >> 3) + j);
-                uint4 l = make_uint4(0, 0, 0, 0);
-                if (poly) l = ld_shared(lin + piece);
-                const uint32_t lw[4] = {l.x, l.y, l.z, l.w};
+                const uint32_t piece = my_piece + piece128(row, 4 * h + j);
+                float y[8];
 #pragma unroll
-                for (uint32_t e = 0; e < 4; ++e) {
-                    float lo, hi;
-                    widen2<kFp16>(lw[e], lo, hi);
-                    float y0 = __fmaf_rn(v[8 * j + 2 * e], f, lo * f_lin), y1 = __fmaf_rn(v[8 * j + 2 * e + 1], f, hi * f_lin);
-                    const uint32_t col = half + h + 8 * j + 2 * e;
-                    if (poly && row == col && row < p.side) y0 += f_diag;
-                    if (poly && row == col + 1 && row < p.side) y1 += f_diag;
-                    q[e] = narrow2<kFp16>(y0, y1);
+                for (uint32_t e = 0; e < 8; ++e) y[e] = __uint_as_float(v[h][8 * j + e]) * f;
+                if (poly) {
+                    const uint4 l = ld_shared(lin + piece);
+                    const uint32_t lw[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+                    for (uint32_t e = 0; e < 4; ++e) {
+                        float lo, hi;
+                        widen2<kFp16>(lw[e], lo, hi);
+                        y[2 * e] = __fmaf_rn(lo, f_lin, y[2 * e]);
+                        y[2 * e + 1] = __fmaf_rn(hi, f_lin, y[2 * e + 1]);
+                    }
+                    if (diag < 64u) {
+#pragma unroll
+                        for (uint32_t e = 0; e < 8; ++e)
+                            if (diag == 8 * j + e) y[e] += f_diag;
+                    }
                 }
-                st_shared(to + piece, q[0], q[1], q[2], q[3]);
+                st_shared(to + piece, narrow2<kFp16>(y[0], y[1]), narrow2<kFp16>(y[2], y[3]), narrow2<kFp16>(y[4], y[5]),
+                          narrow2<kFp16>(y[6], y[7]));
             }
         }
     };
     auto square = [&](uint32_t to, uint32_t a, uint32_t c, float f, bool poly, float f_lin, float f_diag) {
         begin();
-        if (tid == 0)
-            for (uint32_t k = 0; k < steps_k; ++k) {
-                const uint32_t at = (k >> 2) * kBlockBytes + (k & 3) * 32;
-                mma_f16(tmem, operand_desc(a + at, 0), operand_desc(c + at, 0), kIdesc | ((kSide >> 3) << 17), k > 0);
-            }
+        if (warp == 0 && elect_one()) {
+            const uint64_t da = operand_desc(a, 0), dc = operand_desc(c, 0);
+#pragma unroll
+            for (uint32_t k = 0; k < kSide / 16; ++k)
+                if (k < steps_k)
+                    mma_f16(tmem, da + (k >> 2) * (kBlockBytes >> 4) + (k & 3) * 2,
+                            dc + (k >> 2) * (kBlockBytes >> 4) + (k & 3) * 2, kIdesc | ((kSide >> 3) << 17), k > 0);
+            tc_commit(bar);
+        }
         finish();
         square_out(to, f, poly, a, f_lin, f_diag);
     };
     // sq[0] = A = f X X^T, summed over the cluster
     auto gram = [&](float f) {
         begin();
-        if (tid == 0)
-            for (uint32_t k = 0; k < blocks * 4; ++k) {
-                const uint64_t d = operand_desc(x + (k >> 2) * kBlockBytes + (k & 3) * 32, 0);
-                mma_f16(tmem, d, d, kIdesc | ((kSide >> 3) << 17), k > 0);
-            }
+        if (warp == 0 && elect_one()) {
+            uint64_t d = operand_desc(x, 0);
+            for (uint32_t n = 0; n < blocks; ++n, d += kBlockBytes >> 4)
+#pragma unroll
+                for (uint32_t k = 0; k < 4; ++k) mma_f16(tmem, d + 2 * k, d + 2 * k, kIdesc | ((kSide >> 3) << 17), n > 0 || k > 0);
+            tc_commit(bar);
+        }
         finish();
         if (p.ctas == 1) {
             square_out(sq[0], f, false, 0, 0.0f, 0.0f);
@@ -760,10 +772,10 @@ __global__ void __launch_bounds__(kSmallThreads) k_ortho_small(const __grid_cons
 #pragma unroll 1
         for (uint32_t h = 0; h < 64; h += 32) {
             float v[32];
-            tmem_load32(tmem + half + h + ((warp & 3) << 21), v);
+            tmem_load32(my_tmem + h, v);
 #pragma unroll
             for (uint32_t j = 0; j < 8; ++j)   // pieces of 4 columns, rotated by the row against bank conflicts
-                st_shared(part + row * 512 + ((((half + h) / 4 + j) ^ (row & 7)) << 4), __float_as_uint(v[4 * j]),
+                st_shared(part + row * 512 + (((half * 16 + h / 4 + j) ^ (row & 7)) << 4), __float_as_uint(v[4 * j]),
                           __float_as_uint(v[4 * j + 1]), __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3]));
         }
         cluster_sync();
@@ -786,26 +798,31 @@ __global__ void __launch_bounds__(kSmallThreads) k_ortho_small(const __grid_cons
     // X = f B X in place, or as bf16 for the caller
     auto update = [&](uint32_t m, float f, bool final) {
         begin();
-        if (tid == 0)
+        if (warp == 0 && elect_one()) {
+            const uint64_t dm = operand_desc(m, 0), dx = operand_desc(x, kBlockBytes);
             for (uint32_t n0 = 0; n0 < blocks; n0 += 4) {
-                const uint32_t n = min(4u, blocks - n0);
-                for (uint32_t k = 0; k < steps_k; ++k)
-                    mma_f16(tmem + n0 * 64, operand_desc(m + (k >> 2) * kBlockBytes + (k & 3) * 32, 0),
-                            operand_desc(x + n0 * kBlockBytes + k * 2048, kBlockBytes),
-                            kIdesc | (1u << 16) | ((n * 8) << 17), k > 0);
+                const uint32_t n = min(4u, blocks - n0), idesc = kIdesc | (1u << 16) | ((n * 8) << 17);
+#pragma unroll
+                for (uint32_t k = 0; k < kSide / 16; ++k)
+                    if (k < steps_k)
+                        mma_f16(tmem + n0 * 64, dm + (k >> 2) * (kBlockBytes >> 4) + (k & 3) * 2,
+                                dx + n0 * (kBlockBytes >> 4) + k * (2048 >> 4), idesc, k > 0);
             }
+            tc_commit(bar);
+        }
         finish();
-#pragma unroll 1
-        for (uint32_t n = warp >> 2; n < 2 * blocks; n += 2) {   // 32 columns each
-            float v[32];
-            tmem_load32(tmem + n * 32 + ((warp & 3) << 21), v);
+#pragma unroll 2
+        for (uint32_t n = half; n < 2 * blocks; n += 2) {   // 32 columns each
+            uint32_t v[32];
+            tmem_start32(tmem + n * 32 + ((warp & 3) << 21), v);
+            tmem_wait(v);
             const uint32_t to = x + (n >> 1) * kBlockBytes;
 #pragma unroll
             for (uint32_t j = 0; j < 4; ++j) {
                 uint32_t q[4];
 #pragma unroll
                 for (uint32_t e = 0; e < 4; ++e) {
-                    const float lo = v[8 * j + 2 * e] * f, hi = v[8 * j + 2 * e + 1] * f;
+                    const float lo = __uint_as_float(v[8 * j + 2 * e]) * f, hi = __uint_as_float(v[8 * j + 2 * e + 1]) * f;
                     q[e] = final ? narrow2<kBf16>(lo, hi) : narrow2<kFp16>(lo, hi);
                 }
                 st_shared(to + piece128(row, (n & 1) * 4 + j), q[0], q[1], q[2], q[3]);
@@ -877,9 +894,15 @@ __global__ void __launch_bounds__(kSmallThreads) k_ortho_small(const __grid_cons
 }
 
 // -------------------------------------------------------------------- host
+// Blocks of the packing pass for one matrix: a unit a warp.
+uint64_t pack_blocks(uint64_t rows, uint64_t cols) {
+    const uint64_t units = (rows + kPackRows - 1) / kPackRows * ((cols + 255) / 256);
+    return (units + kPackWarps - 1) / kPackWarps;
+}
+
 // The scratch of a call, as offsets from its start.
 struct Scratch {
-    uint64_t partial, g0, done, x[2], s[3], bytes;
+    uint64_t top, sum, ticket, g0, done, x[2], s[3], bytes;
 };
 Scratch scratch_of(uint64_t batch, uint64_t rows, uint64_t cols) {
     const uint64_t side = rows < cols ? rows : cols;
@@ -890,7 +913,9 @@ Scratch scratch_of(uint64_t batch, uint64_t rows, uint64_t cols) {
         at = up(at + bytes, 1024);
         return here;
     };
-    z.partial = take(batch * kPartials * sizeof(double));
+    z.top = take(batch * kTopBlocks * sizeof(uint32_t));
+    z.sum = take(batch * pack_blocks(rows, cols) * sizeof(float));
+    z.ticket = take(batch * sizeof(uint32_t));
     z.g0 = take(batch * sizeof(float));
     z.done = take(batch * kMaxPhases * sizeof(uint32_t));
     for (uint64_t& x : z.x) x = take(batch * rows * up(cols, 8) * 2);
@@ -1028,23 +1053,18 @@ int zero_orthogonalize(int dtype, int batch, uint64_t rows, uint64_t cols, const
     q.pitch = xp;
     q.segments = static_cast<uint32_t>((cols + 255) / 256);
     q.units = static_cast<uint32_t>((rows + kPackRows - 1) / kPackRows) * q.segments;
-    q.partial = reinterpret_cast<double*>(ws + z.partial);
+    q.top = reinterpret_cast<uint32_t*>(ws + z.top);
+    q.sum = reinterpret_cast<float*>(ws + z.sum);
+    q.ticket = reinterpret_cast<uint32_t*>(ws + z.ticket);
     q.g0 = reinterpret_cast<float*>(ws + z.g0);
     q.done = reinterpret_cast<uint32_t*>(ws + z.done);
     q.x0 = reinterpret_cast<__half*>(ws + z.x[0]);
-    const uint64_t want = (q.units + kPackWarps - 1) / kPackWarps;
-    q.partials = static_cast<int>(want < kPartials ? want : kPartials);
-    {
-        const dim3 grid(static_cast<unsigned>(q.partials), nb);
-        const dim3 packs(static_cast<unsigned>(want), nb);
-        e = dtype == ZERO_FP16 ? launch_pdl(k_ortho_norm<kFp16>, grid, kThreads, 0, 1, s, q)
-                               : launch_pdl(k_ortho_norm<kBf16>, grid, kThreads, 0, 1, s, q);
-        if (e != cudaSuccess) return cuda_refuse(e, "norm");
-        e = dtype == ZERO_FP16 ? launch_pdl(k_ortho_pack<kFp16>, packs, kThreads, 0, 1, s, q)
-                               : launch_pdl(k_ortho_pack<kBf16>, packs, kThreads, 0, 1, s, q);
-        if (e != cudaSuccess) return cuda_refuse(e, "pack");
-    }
-
+    q.sums = static_cast<uint32_t>(pack_blocks(rows, cols));
+    q.tops = q.sums < kTopBlocks ? q.sums : kTopBlocks;
+    if ((e = launch_pdl(k_ortho_top, dim3(q.tops, nb), kThreads, 0, 1, s, q)) != cudaSuccess) return cuda_refuse(e, "scale");
+    e = dtype == ZERO_FP16 ? launch_pdl(k_ortho_pack<kFp16>, dim3(q.sums, nb), kThreads, 0, 1, s, q)
+                           : launch_pdl(k_ortho_pack<kBf16>, dim3(q.sums, nb), kThreads, 0, 1, s, q);
+    if (e != cudaSuccess) return cuda_refuse(e, "pack");
     const uint64_t xs = rows * xp, ss = side * sp;
     for (int i = 0; i < 2; ++i) {
         const void* base = ws + z.x[i];
