@@ -328,6 +328,11 @@ __global__ void __launch_bounds__(kProductThreads) k_ortho_products(const __grid
         bar_init_fence();
     }
     if (warp == 1) tmem_alloc_pair(smem_u32(&s_tmem), 2 * kTile);
+    {   // the phases into the constant cache: a first read there costs microseconds
+        uint32_t touched = 0;
+        for (uint32_t i = 0; i < p.n_phases; ++i) touched |= p.phases[i].tiles;
+        if (touched == 0u) s_quit = 0;   // never; keeps the reads
+    }
     tc_fence_before();
     __syncthreads();
     cluster_sync();
@@ -467,9 +472,8 @@ __global__ void __launch_bounds__(kProductThreads) k_ortho_products(const __grid
 #pragma unroll
                             for (uint32_t e = 0; e < 8; ++e) {
                                 const float l = widen<kFp16>((q[e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
-                                float y = __fmaf_rn(v[8 * j + e], scale, l * f_lin);
-                                if (diag == 8 * j + e) y += f_diag;
-                                v[8 * j + e] = y;
+                                // f_diag is added as a value, zero or not: a test of each turns into a branch a lane
+                                v[8 * j + e] = __fmaf_rn(v[8 * j + e], scale, l * f_lin) + (diag == 8 * j + e ? f_diag : 0.0f);
                             }
                         }
                     } else {
@@ -602,6 +606,7 @@ __global__ void __launch_bounds__(kSmallThreads) k_ortho_small(const __grid_cons
     __shared__ int s_quit;
     __shared__ uint32_t s_top;
     __shared__ float s_sum;
+    __shared__ float s_coeffs[3 * ZERO_MAX_NS_STEPS];   // a first read of a parameter costs microseconds: not in between
     volatile int* quit = &s_quit;
     const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = p.ctas > 1 ? cluster_rank() : 0, b = blockIdx.x / p.ctas;
@@ -616,6 +621,7 @@ __global__ void __launch_bounds__(kSmallThreads) k_ortho_small(const __grid_cons
         bar_init_fence();
     }
     if (warp == 0) tmem_alloc(smem_u32(&s_tmem), 512);
+    for (uint32_t i = tid; i < 3u * p.steps; i += kSmallThreads) s_coeffs[i] = p.coeffs[i];
     for (uint32_t i = tid; i < blocks * (kBlockBytes / 16); i += kSmallThreads) st_shared(x + 16 * i, 0u, 0u, 0u, 0u);
     tc_fence_before();
     __syncthreads();
@@ -727,11 +733,9 @@ __global__ void __launch_bounds__(kSmallThreads) k_ortho_small(const __grid_cons
                         y[2 * e] = __fmaf_rn(lo, f_lin, y[2 * e]);
                         y[2 * e + 1] = __fmaf_rn(hi, f_lin, y[2 * e + 1]);
                     }
-                    if (diag < 64u) {
+                    // added to every value, zero or not: a test of each turns into a branch a lane
 #pragma unroll
-                        for (uint32_t e = 0; e < 8; ++e)
-                            if (diag == 8 * j + e) y[e] += f_diag;
-                    }
+                    for (uint32_t e = 0; e < 8; ++e) y[e] += diag == 8 * j + e ? f_diag : 0.0f;
                 }
                 st_shared(to + piece, narrow2<kFp16>(y[0], y[1]), narrow2<kFp16>(y[2], y[3]), narrow2<kFp16>(y[4], y[5]),
                           narrow2<kFp16>(y[6], y[7]));
@@ -831,7 +835,7 @@ __global__ void __launch_bounds__(kSmallThreads) k_ortho_small(const __grid_cons
     };
 
     for (int k = 0; k < p.steps;) {
-        const float* c = p.coeffs + 3 * k;
+        const float* c = s_coeffs + 3 * k;
         const bool raw = k == 0, pair = raw && p.steps >= 2;
         auto poly = [&](uint32_t to, uint32_t a, const float* co) {
             square(to, a, a, co[2] * (kScaleB / (kScaleA * kScaleA)), true, co[1] * (kScaleB / kScaleA), co[0] * kScaleB);
