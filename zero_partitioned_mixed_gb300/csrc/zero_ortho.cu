@@ -223,7 +223,9 @@ enum Epi : int32_t {
 struct Phase {
     int32_t a, b;              // tensor maps of the operands
     int32_t a_mn, b_mn;        // their order in memory: 0 K-major, 1 MN-major
-    int32_t out, mirror, lin;  // tensor maps: output, its mirror image (-1: not symmetric), the linear term
+    int32_t out;               // tensor map of the output
+    int32_t symmetric;         // tiles on and below the diagonal, each written with its mirror image
+    int32_t lin;               // the linear term: a square matrix's index
     Epi epi;
     uint32_t rows, cols, depth;
     uint32_t tiles_n, tiles;   // tiles a row, a matrix
@@ -232,14 +234,15 @@ struct Phase {
 };
 
 enum Map : int { kXRows0, kXRows1, kXCols0, kXCols1, kSquare0, kSquare1, kSquare2,   // operands
-                 kXOut0, kXOut1, kSquareOut0, kSquareOut1, kSquareOut2,             // outputs (and linear terms)
-                 kMirror0, kMirror1, kMirror2, kMaps };
+                 kXOut0, kXOut1, kSquareOut0, kSquareOut1, kSquareOut2, kMaps };    // outputs
 
 struct ProductArgs {
     CUtensorMap maps[kMaps];
     Phase phases[kMaxPhases];
     void* dst[kMaxMatrices];   // kFinal
     uint64_t dst_ld;
+    const __half* square[3];   // the square matrices, [batch][side][square_pitch]
+    uint64_t square_pitch, square_stride;
     const float* g0;           // [batch]
     uint32_t* done;            // [batch][kMaxPhases] finished epilogues, zero at the start
     int32_t dst_vec;           // every row of dst starts on 16 bytes
@@ -250,18 +253,19 @@ struct ProductArgs {
 // contraction is 32 KiB a CTA for 512 cycles of products, which is about
 // what an SM gets from L2 (128 x 128 tiles of one CTA need twice that, and
 // ran at 0.9 PFLOP/s).  Warp 0 copies operands into a ring of stages, warp 1
-// of the leader issues the products, warps 2 to 5 turn finished accumulators
-// into output; two accumulators in tensor memory, so that one tile's
-// epilogue runs under the next one's products.
+// of the leader issues the products, warps 2 to 9 turn finished accumulators
+// into output (each 32 rows by 128 columns of a tile, by 32 columns at a
+// time); two accumulators in tensor memory, so that one tile's epilogue runs
+// under the next one's products.  Between dependent phases an epilogue is not
+// hidden: eight warps take 2 us where four took 4 (8 with a linear term).
 constexpr int kTile = 256, kHalf = 128, kBlockK = 64;
-constexpr int kProductThreads = 192;
+constexpr int kOutWarps = 8, kProductThreads = 64 + 32 * kOutWarps;
 constexpr int kStages = 5;
 constexpr uint32_t kOperandBytes = kHalf * kBlockK * 2, kStageBytes = 2 * kOperandBytes;
-// A warp's output buffers: 32 rows x 64 columns twice, and the mirror image
-// (64 x 32) twice.
-constexpr uint32_t kOutBytes = 32 * 64 * 2, kWarpBytes = 4 * kOutBytes;
-constexpr size_t kProductSmem = 1024 + kStages * kStageBytes + 4 * kWarpBytes;
-constexpr uint32_t kDonePerTile = 8;   // 4 warps of 2 CTAs
+// A warp's output buffers: 32 x 32 values twice, and twice their mirror image.
+constexpr uint32_t kOutBytes = 32 * 32 * 2, kWarpBytes = 4 * kOutBytes;
+constexpr size_t kProductSmem = 1024 + kStages * kStageBytes + kOutWarps * kWarpBytes;
+constexpr uint32_t kDonePerTile = 2 * kOutWarps;   // the warps of 2 CTAs
 
 // The tiles of one CTA pair, in order.
 struct Walk {
@@ -276,7 +280,7 @@ struct Walk {
             if (at < total) {
                 b = at / f.tiles;
                 const uint32_t t = at - b * f.tiles;
-                if (f.mirror >= 0) {
+                if (f.symmetric) {
                     triangle(t, tm, tn);
                 } else {
                     tm = t / f.tiles_n;
@@ -303,7 +307,7 @@ struct Walk {
 
 __global__ void __launch_bounds__(kProductThreads) k_ortho_products(const __grid_constant__ ProductArgs p) {
     extern __shared__ unsigned char smem_raw[];
-    __shared__ __align__(8) uint64_t bars[2 * kStages + 4 + 8];
+    __shared__ __align__(8) uint64_t bars[2 * kStages + 4];
     __shared__ __align__(8) uint64_t s_last;
     __shared__ uint32_t s_tmem;
     __shared__ int s_quit;
@@ -311,8 +315,7 @@ __global__ void __launch_bounds__(kProductThreads) k_ortho_products(const __grid
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    const uint32_t full = smem_u32(bars), empty = full + 8 * kStages, done = empty + 8 * kStages, freed = done + 16,
-                   lin0 = freed + 16;
+    const uint32_t full = smem_u32(bars), empty = full + 8 * kStages, done = empty + 8 * kStages, freed = done + 16;
     if (threadIdx.x == 0) {
         s_quit = 0;
         for (int i = 0; i < kStages; ++i) {
@@ -321,9 +324,8 @@ __global__ void __launch_bounds__(kProductThreads) k_ortho_products(const __grid
         }
         for (int i = 0; i < 2; ++i) {
             bar_init(done + 8 * i, 1);
-            bar_init(freed + 8 * i, 8);
+            bar_init(freed + 8 * i, 2 * kOutWarps);
         }
-        for (int i = 0; i < 8; ++i) bar_init(lin0 + 8 * i, 1);
         bar_init(smem_u32(&s_last), 1);
         bar_init_fence();
     }
@@ -347,7 +349,7 @@ __global__ void __launch_bounds__(kProductThreads) k_ortho_products(const __grid
         for (bool more = w.find(); more && ok; more = w.next()) {
             const Phase& f = p.phases[w.phase];
             if (!w.inputs_ready(quit)) break;
-            proxy_fence();
+            proxy_fence_global();
             const uint32_t nk = (f.depth + kBlockK - 1) / kBlockK;
             const CUtensorMap *ma = &p.maps[f.a], *mb = &p.maps[f.b];
             const int ra = static_cast<int>(w.tm * kTile + rank * kHalf);
@@ -411,32 +413,33 @@ __global__ void __launch_bounds__(kProductThreads) k_ortho_products(const __grid
         }
     } else if (warp >= 2) {
         const uint32_t quarter = warp & 3;   // the lanes of tensor memory that this warp can read
-        const uint32_t mine = ring + kStages * kStageBytes + quarter * kWarpBytes;
-        const uint32_t leader_freed = cluster_addr(freed, 0), lin_bar = lin0 + 16 * quarter;
-        uint32_t n = 0, lin_parity = 0;   // bit i: parity of the next fill of buffer i
+        const uint32_t part = static_cast<uint32_t>(warp - 2) >> 2;   // its half of the columns
+        const uint32_t mine = ring + kStages * kStageBytes + static_cast<uint32_t>(warp - 2) * kWarpBytes;
+        const uint32_t leader_freed = cluster_addr(freed, 0);
+        uint32_t n = 0;
         Walk w(p);
         for (bool more = w.find(); more; more = w.next(), ++n) {
             const Phase& f = p.phases[w.phase];
             const uint32_t acc = n & 1;
-            const uint32_t row0 = w.tm * kTile + rank * kHalf + quarter * 32, col0 = w.tn * kTile;
+            const uint32_t row0 = w.tm * kTile + rank * kHalf + quarter * 32, row = row0 + lane;
+            const uint32_t col0 = w.tn * kTile + part * 128;
             const int z = static_cast<int>(w.b);
-            // chunks of 64 columns that hold output
-            const uint32_t left = (f.cols - col0 + 63u) / 64u, chunks = row0 >= f.rows ? 0u : left < 4u ? left : 4u;
-            const bool poly = f.epi == kPoly, final = f.epi == kFinal, mirror = f.mirror >= 0 && w.tm != w.tn;
-            auto fetch_lin = [&](uint32_t c) {   // one lane: the buffer's last store has been read, then fill it
-                store_wait_read<0>();
-                proxy_fence();
-                bar_expect(lin_bar + 8 * (c & 1), kOutBytes);
-                copy_box(mine + (c & 1) * kOutBytes, &p.maps[f.lin], static_cast<int>(col0 + 64 * c),
-                         static_cast<int>(row0), z, lin_bar + 8 * (c & 1));
-            };
+            const bool poly = f.epi == kPoly, final = f.epi == kFinal, mirror = f.symmetric && w.tm != w.tn;
+            // chunks of 32 columns that hold output
+            const uint32_t chunks = row0 >= f.rows || col0 >= f.cols ? 0u : min(4u, (f.cols - col0 + 31u) / 32u);
             bool ok = true;
-            if (poly && chunks && lane == 0) {   // the linear term's first chunks arrive under the products
-                ok = w.inputs_ready(quit);
-                if (ok) {
-                    fetch_lin(0);
-                    if (chunks > 1) fetch_lin(1);
-                }
+            uint4 lin[4][4];   // this lane's row of the linear term, read under the products
+            if (poly && chunks) {
+                ok = lane != 0 || w.inputs_ready(quit);
+                __syncwarp();
+                const __half* from = p.square[f.lin] + w.b * p.square_stride + row * p.square_pitch + col0;
+#pragma unroll
+                for (uint32_t c = 0; c < 4; ++c)
+#pragma unroll
+                    for (uint32_t j = 0; j < 4; ++j)
+                        lin[c][j] = row < f.rows && col0 + 32 * c + 8 * j < f.cols
+                                        ? __ldcg(reinterpret_cast<const uint4*>(from + 32 * c + 8 * j))
+                                        : make_uint4(0u, 0u, 0u, 0u);
             }
             ok = ok && bar_wait(done + 8 * acc, (n / 2) & 1, quit);
             if (__any_sync(0xFFFFFFFFu, !ok)) break;
@@ -447,80 +450,82 @@ __global__ void __launch_bounds__(kProductThreads) k_ortho_products(const __grid
                 scale *= f.g_power == 2 ? g * g : g;
             }
             const float f_lin = f.f_lin, f_diag = f.f_diag;
-#pragma unroll 1
-            for (uint32_t c = 0; c < chunks; ++c) {
+            const uint32_t acc0 = tmem + acc * kTile + part * 128 + (quarter << 21);
+            uint32_t v[2][32];
+            if (chunks) tmem_start32(acc0, v[0]);
+#pragma unroll
+            for (uint32_t c = 0; c < 4; ++c) {
+                if (c >= chunks) break;
+                uint32_t (&a)[32] = v[c & 1];
+                tmem_wait(a);
+                if (c + 1 < chunks) tmem_start32(acc0 + 32 * (c + 1), v[(c + 1) & 1]);
                 const uint32_t buf = mine + (c & 1) * kOutBytes, flip = mine + (2 + (c & 1)) * kOutBytes;
-                if (lane == 0) {
-                    if (poly) {
-                        if (c >= 1 && c + 1 < chunks) fetch_lin(c + 1);
-                        ok = bar_wait(lin_bar + 8 * (c & 1), (lin_parity >> (c & 1)) & 1, quit);
-                        lin_parity ^= 1u << (c & 1);
+                uint32_t q[16];
+                if (poly) {
+                    const uint32_t lw[16] = {lin[c][0].x, lin[c][0].y, lin[c][0].z, lin[c][0].w, lin[c][1].x, lin[c][1].y,
+                                             lin[c][1].z, lin[c][1].w, lin[c][2].x, lin[c][2].y, lin[c][2].z, lin[c][2].w,
+                                             lin[c][3].x, lin[c][3].y, lin[c][3].z, lin[c][3].w};
+#pragma unroll
+                    for (uint32_t e = 0; e < 16; ++e) {
+                        float lo, hi;
+                        widen2<kFp16>(lw[e], lo, hi);
+                        a[2 * e] = __float_as_uint(__fmaf_rn(__uint_as_float(a[2 * e]), scale, lo * f_lin));
+                        a[2 * e + 1] = __float_as_uint(__fmaf_rn(__uint_as_float(a[2 * e + 1]), scale, hi * f_lin));
                     }
-                    store_wait_read<1>();   // the stores of chunk c - 2 have left its buffers
+                    if (row0 == col0 + 32 * c) {   // the diagonal's chunk
+                        // f_diag is added as a value, zero or not: a test of each turns into a branch a lane
+#pragma unroll
+                        for (uint32_t e = 0; e < 32; ++e)
+                            a[e] = __float_as_uint(__uint_as_float(a[e]) + (lane == e ? f_diag : 0.0f));
+                    }
+                } else {
+#pragma unroll
+                    for (uint32_t e = 0; e < 32; ++e) a[e] = __float_as_uint(__uint_as_float(a[e]) * scale);
                 }
-                if (__any_sync(0xFFFFFFFFu, !ok)) break;
+                if (final) {
 #pragma unroll
-                for (uint32_t h = 0; h < 2; ++h) {
-                    float v[32];
-                    tmem_load32(tmem + acc * kTile + c * 64 + h * 32 + (quarter << 21), v);
-                    if (poly) {
-                        const uint32_t diag = row0 + lane - (col0 + 64 * c + 32 * h);   // index of the diagonal, if < 32
+                    for (uint32_t e = 0; e < 16; ++e) q[e] = narrow2<kBf16>(__uint_as_float(a[2 * e]), __uint_as_float(a[2 * e + 1]));
+                } else {
 #pragma unroll
-                        for (uint32_t j = 0; j < 4; ++j) {
-                            const uint4 x = ld_shared(buf + piece128(lane, 4 * h + j));
-                            const uint32_t q[4] = {x.x, x.y, x.z, x.w};
+                    for (uint32_t e = 0; e < 16; ++e) q[e] = narrow2<kFp16>(__uint_as_float(a[2 * e]), __uint_as_float(a[2 * e + 1]));
+                }
+                if (lane == 0) store_wait_read<1>();   // the stores of chunk c - 2 have left its buffers
+                __syncwarp();
 #pragma unroll
-                            for (uint32_t e = 0; e < 8; ++e) {
-                                const float l = widen<kFp16>((q[e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
-                                // f_diag is added as a value, zero or not: a test of each turns into a branch a lane
-                                v[8 * j + e] = __fmaf_rn(v[8 * j + e], scale, l * f_lin) + (diag == 8 * j + e ? f_diag : 0.0f);
-                            }
-                        }
-                    } else {
+                for (uint32_t j = 0; j < 4; ++j)
+                    st_shared(buf + piece64(lane, j), q[4 * j], q[4 * j + 1], q[4 * j + 2], q[4 * j + 3]);
+                if (mirror) {
+                    // columns become rows: two lanes trade halves, the even one then holds column 2e of
+                    // its own and the next row, the odd one column 2e + 1 of the previous and its own
 #pragma unroll
-                        for (uint32_t e = 0; e < 32; ++e) v[e] *= scale;
-                    }
-                    uint32_t q[16];
-#pragma unroll
-                    for (uint32_t e = 0; e < 16; ++e)
-                        q[e] = final ? narrow2<kBf16>(v[2 * e], v[2 * e + 1]) : narrow2<kFp16>(v[2 * e], v[2 * e + 1]);
-#pragma unroll
-                    for (uint32_t j = 0; j < 4; ++j)
-                        st_shared(buf + piece128(lane, 4 * h + j), q[4 * j], q[4 * j + 1], q[4 * j + 2], q[4 * j + 3]);
-                    if (mirror) {
-                        // columns become rows: two lanes trade halves, the even one then holds column 2e of
-                        // its own and the next row, the odd one column 2e + 1 of the previous and its own
-#pragma unroll
-                        for (uint32_t e = 0; e < 16; ++e) {
-                            const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, q[e], 1);
-                            const uint32_t word = lane & 1 ? __byte_perm(other, q[e], 0x7632) : __byte_perm(q[e], other, 0x5410);
-                            const uint32_t r = 32 * h + 2 * e + (lane & 1);
-                            st_shared(flip + piece64(r, lane >> 3) + 4 * ((lane >> 1) & 3), word);
-                        }
+                    for (uint32_t e = 0; e < 16; ++e) {
+                        const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, q[e], 1);
+                        const uint32_t word = lane & 1 ? __byte_perm(other, q[e], 0x7632) : __byte_perm(q[e], other, 0x5410);
+                        st_shared(flip + piece64(2 * e + (lane & 1), lane >> 3) + 4 * ((lane >> 1) & 3), word);
                     }
                 }
                 if (final) {
                     __syncwarp();
-                    write_rows(static_cast<unsigned short*>(p.dst[w.b]), p.dst_ld, p.dst_vec, f.rows, f.cols, row0, col0 + 64 * c, buf);
-                    __syncwarp();
+                    write_rows<32>(static_cast<unsigned short*>(p.dst[w.b]), p.dst_ld, p.dst_vec, f.rows, f.cols, row0,
+                                   col0 + 32 * c, buf);
                 } else {
-                    proxy_fence();
+                    proxy_fence_shared();
                     __syncwarp();
                     if (lane == 0) {
-                        store_box(&p.maps[f.out], static_cast<int>(col0 + 64 * c), static_cast<int>(row0), z, buf);
-                        if (mirror)
-                            store_box(&p.maps[f.mirror], static_cast<int>(row0), static_cast<int>(col0 + 64 * c), z, flip);
+                        const int y = static_cast<int>(row0), x = static_cast<int>(col0 + 32 * c);
+                        store_box(&p.maps[f.out], x, y, z, buf);
+                        if (mirror) store_box(&p.maps[f.out], y, x, z, flip);
                         store_commit();
                     }
                 }
             }
             tc_fence_before();
-            if (__any_sync(0xFFFFFFFFu, !ok)) break;
+            __syncwarp();
             if (lane == 0) {
                 bar_arrive_cluster(leader_freed + 8 * acc);
                 if (!final) {   // the tile's output is in memory before it counts
                     store_wait<0>();
-                    proxy_fence();
+                    proxy_fence_global();
                     count_done(p.done + static_cast<uint64_t>(w.b) * kMaxPhases + w.phase);
                 }
             }
@@ -1074,17 +1079,20 @@ int zero_orthogonalize(int dtype, int batch, uint64_t rows, uint64_t cols, const
         const void* base = ws + z.x[i];
         if ((e = make_map(&p.maps[kXRows0 + i], 2, base, cols, rows, nb, xp, xs, kBlockK, kHalf)) != cudaSuccess ||
             (e = make_map(&p.maps[kXCols0 + i], 2, base, cols, rows, nb, xp, xs, 64, kBlockK)) != cudaSuccess ||
-            (e = make_map(&p.maps[kXOut0 + i], 2, base, cols, rows, nb, xp, xs, 64, 32)) != cudaSuccess)
+            (e = make_map(&p.maps[kXOut0 + i], 2, base, cols, rows, nb, xp, xs, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B)) !=
+                cudaSuccess)
             return cuda_refuse(e, "tensor map");
     }
     for (int i = 0; i < 3; ++i) {
         const void* base = ws + z.s[i];
         if ((e = make_map(&p.maps[kSquare0 + i], 2, base, side, side, nb, sp, ss, kBlockK, kHalf)) != cudaSuccess ||
-            (e = make_map(&p.maps[kSquareOut0 + i], 2, base, side, side, nb, sp, ss, 64, 32)) != cudaSuccess ||
-            (e = make_map(&p.maps[kMirror0 + i], 2, base, side, side, nb, sp, ss, 32, 64, CU_TENSOR_MAP_SWIZZLE_64B)) !=
+            (e = make_map(&p.maps[kSquareOut0 + i], 2, base, side, side, nb, sp, ss, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B)) !=
                 cudaSuccess)
             return cuda_refuse(e, "tensor map");
     }
+    for (int i = 0; i < 3; ++i) p.square[i] = reinterpret_cast<const __half*>(ws + z.s[i]);
+    p.square_pitch = sp;
+    p.square_stride = ss;
     p.g0 = q.g0;
     p.done = q.done;
     p.batch = nb;
@@ -1096,8 +1104,7 @@ int zero_orthogonalize(int dtype, int batch, uint64_t rows, uint64_t cols, const
         f.a = a;
         f.b = b;
         f.out = kSquareOut0 + to;
-        f.mirror = kMirror0 + to;
-        f.lin = -1;
+        f.symmetric = 1;
         f.epi = kScale;
         f.rows = f.cols = static_cast<uint32_t>(side);
         f.depth = static_cast<uint32_t>(depth);
@@ -1118,7 +1125,7 @@ int zero_orthogonalize(int dtype, int batch, uint64_t rows, uint64_t cols, const
     auto poly = [&](int to, int a, const float* c) {
         Phase& f = square(to, kSquare0 + a, kSquare0 + a, side);
         f.epi = kPoly;
-        f.lin = kSquareOut0 + a;
+        f.lin = a;
         f.f_diag = c[0] * kScaleB;
         f.f_lin = c[1] * (kScaleB / kScaleA);
         f.f_acc = c[2] * (kScaleB / (kScaleA * kScaleA));
@@ -1134,7 +1141,6 @@ int zero_orthogonalize(int dtype, int batch, uint64_t rows, uint64_t cols, const
         f.b = tall ? kSquare0 + b : kXCols0 + x;
         f.b_mn = !tall;
         f.out = kXOut0 + (x ^ 1);
-        f.mirror = f.lin = -1;
         f.epi = to_dst ? kFinal : kScale;
         f.rows = static_cast<uint32_t>(rows);
         f.cols = static_cast<uint32_t>(cols);

@@ -191,6 +191,7 @@ __device__ __forceinline__ void store_wait() {
 // Ordinary accesses before it and bulk copies after it (or the reverse) are ordered.
 __device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
+__device__ __forceinline__ void proxy_fence_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
 __device__ __forceinline__ void proxy_fence_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -370,19 +371,21 @@ __device__ __forceinline__ uint16_t ld_shared16(uint32_t addr) {
     return x;
 }
 
-// 32 rows x 64 columns of 16-bit values in a warp's buffer into rows row0...
-// and columns col0... of a row-major rows x cols matrix: whole 128-byte rows
-// where every row starts on 16 bytes (`vec`), value by value elsewhere.
+// 32 rows x W columns (64 or 32) of 16-bit values in a warp's buffer, swizzled
+// for rows of that width, into rows row0... and columns col0... of a row-major
+// rows x cols matrix: 16 bytes a lane where every row starts on 16 bytes
+// (`vec`), value by value elsewhere.
+template <uint32_t W>
 __device__ __forceinline__ void write_rows(unsigned short* dst, uint64_t ld, bool vec, uint32_t rows, uint32_t cols,
                                            uint32_t row0, uint32_t col0, uint32_t buf) {
     const uint32_t lane = threadIdx.x & 31;
     if (vec) {
-#pragma unroll 4
-        for (uint32_t i = lane; i < 256; i += 32) {
-            const uint32_t r = i >> 3, j = i & 7, col = col0 + 8 * j;
+#pragma unroll
+        for (uint32_t i = lane; i < 4 * W; i += 32) {
+            const uint32_t r = i / (W / 8), j = i % (W / 8), col = col0 + 8 * j;
             if (row0 + r >= rows || col >= cols) continue;
             unsigned short* out = dst + static_cast<uint64_t>(row0 + r) * ld + col;
-            const uint4 x = ld_shared(buf + piece128(r, j));
+            const uint4 x = ld_shared(buf + (W == 64 ? piece128(r, j) : piece64(r, j)));
             if (col + 8 <= cols) {
                 *reinterpret_cast<uint4*>(out) = x;
             } else {
@@ -394,10 +397,11 @@ __device__ __forceinline__ void write_rows(unsigned short* dst, uint64_t ld, boo
         }
     } else {
 #pragma unroll 4
-        for (uint32_t i = lane; i < 32 * 64; i += 32) {
-            const uint32_t r = i >> 6, e = i & 63;
+        for (uint32_t i = lane; i < 32 * W; i += 32) {
+            const uint32_t r = i / W, e = i % W;
             if (row0 + r < rows && col0 + e < cols)
-                dst[static_cast<uint64_t>(row0 + r) * ld + col0 + e] = ld_shared16(buf + piece128(r, e >> 3) + 2 * (e & 7));
+                dst[static_cast<uint64_t>(row0 + r) * ld + col0 + e] =
+                    ld_shared16(buf + (W == 64 ? piece128(r, e >> 3) : piece64(r, e >> 3)) + 2 * (e & 7));
         }
     }
 }
