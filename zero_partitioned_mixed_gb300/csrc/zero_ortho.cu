@@ -225,7 +225,7 @@ struct Phase {
     int32_t a_mn, b_mn;        // their order in memory: 0 K-major, 1 MN-major
     int32_t out;               // tensor map of the output
     int32_t symmetric;         // tiles on and below the diagonal, each written with its mirror image
-    int32_t lin;               // the linear term: a square matrix's index
+    int32_t lin;               // tensor map of the linear term
     Epi epi;
     uint32_t rows, cols, depth;
     uint32_t tiles_n, tiles;   // tiles a row, a matrix
@@ -234,15 +234,13 @@ struct Phase {
 };
 
 enum Map : int { kXRows0, kXRows1, kXCols0, kXCols1, kSquare0, kSquare1, kSquare2,   // operands
-                 kXOut0, kXOut1, kSquareOut0, kSquareOut1, kSquareOut2, kMaps };    // outputs
+                 kXOut0, kXOut1, kSquareOut0, kSquareOut1, kSquareOut2, kMaps };    // outputs (and linear terms)
 
 struct ProductArgs {
     CUtensorMap maps[kMaps];
     Phase phases[kMaxPhases];
     void* dst[kMaxMatrices];   // kFinal
     uint64_t dst_ld;
-    const __half* square[3];   // the square matrices, [batch][side][square_pitch]
-    uint64_t square_pitch, square_stride;
     const float* g0;           // [batch]
     uint32_t* done;            // [batch][kMaxPhases] finished epilogues, zero at the start
     int32_t dst_vec;           // every row of dst starts on 16 bytes
@@ -307,7 +305,7 @@ struct Walk {
 
 __global__ void __launch_bounds__(kProductThreads) k_ortho_products(const __grid_constant__ ProductArgs p) {
     extern __shared__ unsigned char smem_raw[];
-    __shared__ __align__(8) uint64_t bars[2 * kStages + 4];
+    __shared__ __align__(8) uint64_t bars[2 * kStages + 4 + kOutWarps];
     __shared__ __align__(8) uint64_t s_last;
     __shared__ uint32_t s_tmem;
     __shared__ int s_quit;
@@ -315,7 +313,8 @@ __global__ void __launch_bounds__(kProductThreads) k_ortho_products(const __grid
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    const uint32_t full = smem_u32(bars), empty = full + 8 * kStages, done = empty + 8 * kStages, freed = done + 16;
+    const uint32_t full = smem_u32(bars), empty = full + 8 * kStages, done = empty + 8 * kStages, freed = done + 16,
+                   lin0 = freed + 16;
     if (threadIdx.x == 0) {
         s_quit = 0;
         for (int i = 0; i < kStages; ++i) {
@@ -326,6 +325,7 @@ __global__ void __launch_bounds__(kProductThreads) k_ortho_products(const __grid
             bar_init(done + 8 * i, 1);
             bar_init(freed + 8 * i, 2 * kOutWarps);
         }
+        for (int i = 0; i < kOutWarps; ++i) bar_init(lin0 + 8 * i, 1);
         bar_init(smem_u32(&s_last), 1);
         bar_init_fence();
     }
@@ -415,31 +415,38 @@ __global__ void __launch_bounds__(kProductThreads) k_ortho_products(const __grid
         const uint32_t quarter = warp & 3;   // the lanes of tensor memory that this warp can read
         const uint32_t part = static_cast<uint32_t>(warp - 2) >> 2;   // its half of the columns
         const uint32_t mine = ring + kStages * kStageBytes + static_cast<uint32_t>(warp - 2) * kWarpBytes;
-        const uint32_t leader_freed = cluster_addr(freed, 0);
-        uint32_t n = 0;
+        const uint32_t leader_freed = cluster_addr(freed, 0), lin_bar = lin0 + 8 * static_cast<uint32_t>(warp - 2);
+        uint32_t n = 0, lin_parity = 0;
         Walk w(p);
         for (bool more = w.find(); more; more = w.next(), ++n) {
             const Phase& f = p.phases[w.phase];
             const uint32_t acc = n & 1;
-            const uint32_t row0 = w.tm * kTile + rank * kHalf + quarter * 32, row = row0 + lane;
+            const uint32_t row0 = w.tm * kTile + rank * kHalf + quarter * 32;
             const uint32_t col0 = w.tn * kTile + part * 128;
             const int z = static_cast<int>(w.b);
             const bool poly = f.epi == kPoly, final = f.epi == kFinal, mirror = f.symmetric && w.tm != w.tn;
             // chunks of 32 columns that hold output
             const uint32_t chunks = row0 >= f.rows || col0 >= f.cols ? 0u : min(4u, (f.cols - col0 + 31u) / 32u);
             bool ok = true;
-            uint4 lin[4][4];   // this lane's row of the linear term, read under the products
+            uint4 lin[4][4];   // this lane's row of the linear term, fetched under the products
             if (poly && chunks) {
-                ok = lane != 0 || w.inputs_ready(quit);
-                __syncwarp();
-                const __half* from = p.square[f.lin] + w.b * p.square_stride + row * p.square_pitch + col0;
+                // through the output buffers, which are free: the last tile's stores were waited for
+                if (lane == 0) {
+                    ok = w.inputs_ready(quit);
+                    if (ok) {
+                        proxy_fence();
+                        bar_expect(lin_bar, chunks * kOutBytes);
+                        for (uint32_t c = 0; c < chunks; ++c)
+                            copy_box(mine + c * kOutBytes, &p.maps[f.lin], static_cast<int>(col0 + 32 * c),
+                                     static_cast<int>(row0), z, lin_bar);
+                    }
+                }
+                ok = __all_sync(0xFFFFFFFFu, ok) && bar_wait(lin_bar, lin_parity, quit);
+                lin_parity ^= 1;
 #pragma unroll
                 for (uint32_t c = 0; c < 4; ++c)
 #pragma unroll
-                    for (uint32_t j = 0; j < 4; ++j)
-                        lin[c][j] = row < f.rows && col0 + 32 * c + 8 * j < f.cols
-                                        ? __ldcg(reinterpret_cast<const uint4*>(from + 32 * c + 8 * j))
-                                        : make_uint4(0u, 0u, 0u, 0u);
+                    for (uint32_t j = 0; j < 4; ++j) lin[c][j] = ld_shared(mine + c * kOutBytes + piece64(lane, j));
             }
             ok = ok && bar_wait(done + 8 * acc, (n / 2) & 1, quit);
             if (__any_sync(0xFFFFFFFFu, !ok)) break;
@@ -1090,9 +1097,6 @@ int zero_orthogonalize(int dtype, int batch, uint64_t rows, uint64_t cols, const
                 cudaSuccess)
             return cuda_refuse(e, "tensor map");
     }
-    for (int i = 0; i < 3; ++i) p.square[i] = reinterpret_cast<const __half*>(ws + z.s[i]);
-    p.square_pitch = sp;
-    p.square_stride = ss;
     p.g0 = q.g0;
     p.done = q.done;
     p.batch = nb;
@@ -1125,7 +1129,7 @@ int zero_orthogonalize(int dtype, int batch, uint64_t rows, uint64_t cols, const
     auto poly = [&](int to, int a, const float* c) {
         Phase& f = square(to, kSquare0 + a, kSquare0 + a, side);
         f.epi = kPoly;
-        f.lin = a;
+        f.lin = kSquareOut0 + a;
         f.f_diag = c[0] * kScaleB;
         f.f_lin = c[1] * (kScaleB / kScaleA);
         f.f_acc = c[2] * (kScaleB / (kScaleA * kScaleA));
