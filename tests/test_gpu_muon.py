@@ -321,6 +321,20 @@ def test_a_captured_step_replays_like_calls():
     assert bufs[1].master.any()
 
 
+def test_the_example_trains():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "muon_mx4.py")
+    spec = importlib.util.spec_from_file_location("muon_mx4_example", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    losses = mod.train(steps=25)
+    assert all(np.isfinite(losses))
+    # 25 steps of an update whose size is the learning rate reach well below half of the start
+    assert losses[-1] < 0.5 * losses[0] and min(losses) == min(losses[5:])
+    assert losses == mod.train(steps=25)     # every kernel of the path gives the same bits again
+
+
 # ------------------------------------------------------------------ refusals
 def test_refusals():
     t = torch.zeros(4096, device="cuda")

@@ -37,3 +37,21 @@ def test_run_is_the_only_launch_with_the_attribute():
     src = _sources()
     hits = [n for n, t in src.items() if "cudaLaunchAttributeProgrammaticStreamSerialization" in t]
     assert hits == ["zero_device.cuh"]
+
+
+def test_tensor_memory_is_allocated_before_the_next_kernel_may_start():
+    # a block that let the next kernel's blocks in before its own allocation
+    # could wait for tensor memory that they hold while they wait for it
+    found = 0
+    for name, t in _sources().items():
+        for m in re.finditer(r"__global__ void[^{;]*?\b(k_\w+)\([^{;]*\)\s*\{(.*?)\n\}\n", t, re.S):
+            body = m.group(2)
+            alloc = re.search(r"\btmem_alloc(?:_pair)?\(", body)
+            if not alloc:
+                continue
+            found += 1
+            enter = body.find("pdl_enter();")
+            if enter >= 0:
+                assert alloc.start() < enter, f"{name}: {m.group(1)}"
+                assert "__syncthreads();" in body[alloc.start():enter], f"{name}: {m.group(1)}"
+    assert found >= 3

@@ -70,13 +70,9 @@ __device__ __forceinline__ uint32_t codes8(const float (&x)[8]) {
 // The row kernels: a warp takes kMxRows rows by 256 columns, 8 a lane, all
 // rows' loads in flight together.  They are bound by the instructions they
 // issue as much as by HBM, so a piece that lies inside the matrix and starts
-// on 16 bytes takes a path without any of the edges' cases (`INSIDE`).
+// on 16 bytes takes a path without any of the edges' cases (`INSIDE`): 42 us
+// against 57 for 11008 x 4096 quantised and read back.
 constexpr int kMxRows = 4;
-
-__device__ __forceinline__ bool all_inside(const MxArgs& a, const void* p16, uint64_t row0, uint64_t segment) {
-    return row0 + kMxRows <= a.rows && (segment + 1) * 256 <= a.cols && (a.ld & 7) == 0 &&
-           (reinterpret_cast<uintptr_t>(p16) & 15) == 0;
-}
 
 template <int DT, bool INSIDE>
 __device__ __forceinline__ void rows_piece(const MxArgs& a, uint64_t row0, uint64_t segment) {
@@ -130,13 +126,13 @@ __device__ __forceinline__ void rows_piece(const MxArgs& a, uint64_t row0, uint6
 }
 
 // Along the rows; those that only fill the last scale tiles are walked too,
-// for their zeros.
-template <int DT>
+// for their zeros.  ALIGNED: every row of the matrix starts on 16 bytes.
+template <int DT, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads) k_mx4_rows(const __grid_constant__ MxArgs a) {
     pdl_enter();
     const uint64_t row0 = (static_cast<uint64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5)) * kMxRows;
     for (uint64_t segment = blockIdx.y; segment < (a.tiles_k + 1) / 2; segment += gridDim.y) {
-        if (all_inside(a, a.src, row0, segment)) rows_piece<DT, true>(a, row0, segment);
+        if (ALIGNED && row0 + kMxRows <= a.rows && (segment + 1) * 256 <= a.cols) rows_piece<DT, true>(a, row0, segment);
         else rows_piece<DT, false>(a, row0, segment);
     }
 }
@@ -146,7 +142,7 @@ __global__ void __launch_bounds__(kThreads) k_mx4_rows(const __grid_constant__ M
 // of two neighbouring columns; the codes go through shared memory so that a
 // row of them leaves as 64 neighbouring bytes.
 template <int DT>
-__global__ void __launch_bounds__(kThreads, 5) k_mx4_columns(const __grid_constant__ MxArgs a) {
+__global__ void __launch_bounds__(kThreads) k_mx4_columns(const __grid_constant__ MxArgs a) {
     pdl_enter();
     __shared__ __align__(16) uint4 s_codes[128][5];   // 5: neighbouring columns start in other banks
     __shared__ uint8_t s_scale[128][4];
@@ -208,74 +204,107 @@ __global__ void __launch_bounds__(kThreads, 5) k_mx4_columns(const __grid_consta
             *reinterpret_cast<const uint32_t*>(s_scale[threadIdx.x]);
 }
 
-// 8 codes of a block with scale byte `byte` as 16-bit values.
-template <int DT>
-__device__ __forceinline__ void decode8(uint32_t q, uint32_t byte, uint32_t (&out)[4]) {
-    // 2^(byte - 127): the smallest is a subnormal number
-    const float scale = byte == 255u ? NAN : __uint_as_float(byte == 0u ? 0x00400000u : byte << 23);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        uint32_t h;
-        asm("{\n\t.reg .b8 b, x, y, z;\n\tmov.b32 {b, x, y, z}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}"
-            : "=r"(h)
-            : "r"(q >> (8 * e)));
-        float lo, hi;
-        widen2<kFp16>(h, lo, hi);
-        mul2(lo, hi, scale);
-        out[e] = narrow2<DT>(lo, hi);
-    }
+// What a scale byte stands for: 2^(byte - 127), the smallest a subnormal number.
+__device__ __forceinline__ float scale_value(uint32_t byte) {
+    return byte == 255u ? NAN : __uint_as_float(byte == 0u ? 0x00400000u : byte << 23);
+}
+// Two codes (the low 8 bits of q) as fp32.
+__device__ __forceinline__ void decode2(uint32_t q, float& lo, float& hi) {
+    uint32_t h;
+    asm("{\n\t.reg .b8 b, x, y, z;\n\tmov.b32 {b, x, y, z}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}" : "=r"(h) : "r"(q));
+    widen2<kFp16>(h, lo, hi);
 }
 
-template <int DT, bool INSIDE>
-__device__ __forceinline__ void values_piece(const MxArgs& a, uint64_t row0, uint64_t segment) {
+// Rows that start on 16 bytes, 256 columns of them inside the matrix.
+template <int DT>
+__device__ __forceinline__ void values_inside(const MxArgs& a, uint64_t row0, uint64_t segment) {
     const uint64_t c = segment * 256 + 8 * (threadIdx.x & 31);
-    const int valid = INSIDE ? 8 : values_left(a.cols, c);
     const uint8_t* codes = a.codes + row0 * a.pitch + (c >> 1);
     const uint8_t* scales = a.scales + scale_at(row0, c >> 5, a.tiles_k);
     uint32_t q[kMxRows], byte[kMxRows];
 #pragma unroll
     for (int r = 0; r < kMxRows; ++r, codes += a.pitch) {
-        q[r] = byte[r] = 0;
-        if (INSIDE || (row0 + r < a.rows && valid > 0)) {
-            q[r] = __ldcs(reinterpret_cast<const uint32_t*>(codes));
-            byte[r] = __ldg(scales + 16 * r);
+        q[r] = __ldcs(reinterpret_cast<const uint32_t*>(codes));
+        byte[r] = __ldg(scales + 16 * r);
+    }
+    unsigned short* dst = static_cast<unsigned short*>(a.dst) + row0 * a.ld + c;
+#pragma unroll
+    for (int r = 0; r < kMxRows; ++r, dst += a.ld) {
+        const float scale = scale_value(byte[r]);
+        uint32_t out[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float lo, hi;
+            decode2(q[r] >> (8 * e), lo, hi);
+            mul2(lo, hi, scale);
+            out[e] = narrow2<DT>(lo, hi);
+        }
+        __stcs(reinterpret_cast<uint4*>(dst), make_uint4(out[0], out[1], out[2], out[3]));
+    }
+}
+
+// Any rows and columns.  A lane writes an aligned piece of 16 bytes; where a
+// row starts between two boundaries (not ALIGNED), the piece begins m values
+// before a word of 8 codes does, and its first m values are the last ones of
+// the word before, which may belong to another block.
+template <int DT, bool ALIGNED>
+__device__ __forceinline__ void values_any(const MxArgs& a, uint64_t row0, uint64_t segment) {
+    const int64_t word = static_cast<int64_t>(segment) * 32 + (threadIdx.x & 31);   // along the row of codes
+    const int64_t words = static_cast<int64_t>(a.pitch / 4), cols = static_cast<int64_t>(a.cols);
+    // words past the row's ends stand for nothing that is written: any will do
+    const int64_t here = min(word, words - 1), there = max(min(word - 1, words - 1), static_cast<int64_t>(0));
+    const uint32_t* codes = reinterpret_cast<const uint32_t*>(a.codes + row0 * a.pitch);
+    const uint8_t* scales = a.scales + scale_at(row0, here >> 2, a.tiles_k);
+    const uint8_t* scales_before = a.scales + scale_at(row0, there >> 2, a.tiles_k);
+    uint32_t q[kMxRows], before[kMxRows], byte[kMxRows], byte_before[kMxRows];
+#pragma unroll
+    for (int r = 0; r < kMxRows; ++r, codes += words) {
+        if (row0 + r >= a.rows) break;
+        q[r] = __ldg(codes + here);
+        byte[r] = __ldg(scales + 16 * r);
+        if (!ALIGNED) {
+            before[r] = __ldg(codes + there);
+            byte_before[r] = __ldg(scales_before + 16 * r);
         }
     }
-    if (INSIDE) {
-        unsigned short* dst = static_cast<unsigned short*>(a.dst) + row0 * a.ld + c;
+    unsigned short* row = static_cast<unsigned short*>(a.dst) + row0 * a.ld;
 #pragma unroll
-        for (int r = 0; r < kMxRows; ++r, dst += a.ld) {
-            uint32_t out[4];
-            decode8<DT>(q[r], byte[r], out);
-            __stcs(reinterpret_cast<uint4*>(dst), make_uint4(out[0], out[1], out[2], out[3]));
+    for (int r = 0; r < kMxRows; ++r, row += a.ld) {
+        if (row0 + r >= a.rows) break;
+        const int m = ALIGNED ? 0 : static_cast<int>((reinterpret_cast<uintptr_t>(row) >> 1) & 7);
+        const float scale = scale_value(byte[r]), scale_before = ALIGNED ? 0.0f : scale_value(byte_before[r]);
+        const uint32_t eight = m == 0 ? q[r] : __funnelshift_r(before[r], q[r], 4 * (8 - m));
+        uint32_t out[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float lo, hi;
+            decode2(eight >> (8 * e), lo, hi);
+            lo = __fmul_rn(lo, 2 * e < m ? scale_before : scale);
+            hi = __fmul_rn(hi, 2 * e + 1 < m ? scale_before : scale);
+            out[e] = narrow2<DT>(lo, hi);
         }
-    } else {
-        // a loop: unrolled, the stores' cases would take a hundred registers
-        int64_t at = static_cast<int64_t>(row0 * a.ld + c);
-#pragma unroll 1
-        for (int r = 0; r < kMxRows; ++r, at += static_cast<int64_t>(a.ld)) {
-            if (row0 + r >= a.rows) break;
-            uint32_t out[4];
-            decode8<DT>(q[0], byte[0], out);
-            store8(static_cast<unsigned short*>(a.dst), at, valid, out);
+        const int64_t c = 8 * word - m;
+        if (c >= 0 && c + 8 <= cols) {
+            __stcs(reinterpret_cast<uint4*>(row + c), make_uint4(out[0], out[1], out[2], out[3]));
+        } else if (c < cols) {
 #pragma unroll
-            for (int i = 0; i + 1 < kMxRows; ++i) {
-                q[i] = q[i + 1];
-                byte[i] = byte[i + 1];
-            }
+            for (int e = 0; e < 8; ++e)
+                if (c + e >= 0 && c + e < cols) row[c + e] = static_cast<unsigned short>(out[e >> 1] >> (16 * (e & 1)));
         }
     }
 }
 
-// Codes and scales back to 16 bits.
-template <int DT>
+// Codes and scales back to 16 bits.  ALIGNED: every row of the matrix starts
+// on 16 bytes.
+template <int DT, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads) k_mx4_values(const __grid_constant__ MxArgs a) {
     pdl_enter();
     const uint64_t row0 = (static_cast<uint64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5)) * kMxRows;
     if (row0 >= a.rows) return;
-    for (uint64_t segment = blockIdx.y; segment < (a.cols + 255) / 256; segment += gridDim.y) {
-        if (all_inside(a, a.dst, row0, segment)) values_piece<DT, true>(a, row0, segment);
-        else values_piece<DT, false>(a, row0, segment);
+    // the pieces of a row that starts between boundaries may be one more than its words
+    for (uint64_t segment = blockIdx.y; segment < (a.cols + (ALIGNED ? 0 : 7) + 255) / 256; segment += gridDim.y) {
+        if (ALIGNED && row0 + kMxRows <= a.rows && (segment + 1) * 256 <= a.cols) values_inside<DT>(a, row0, segment);
+        else values_any<DT, ALIGNED>(a, row0, segment);
     }
 }
 
@@ -788,8 +817,10 @@ int zero_mx4_quantize(int dtype, uint64_t rows, uint64_t cols, const void* src16
         a.pitch = mx_pitch(cols);
         a.tiles_k = up(cols, 128) / 128;
         const dim3 grid = row_grid(up(rows, 128), cols);
-        e = dtype == ZERO_FP16 ? launch_pdl(k_mx4_rows<kFp16>, grid, kThreads, 0, 1, s, a)
-                               : launch_pdl(k_mx4_rows<kBf16>, grid, kThreads, 0, 1, s, a);
+        const bool fp16 = dtype == ZERO_FP16;
+        e = launch_pdl(aligned(src16, 16) && ld % 8 == 0 ? (fp16 ? k_mx4_rows<kFp16, true> : k_mx4_rows<kBf16, true>)
+                                                         : (fp16 ? k_mx4_rows<kFp16, false> : k_mx4_rows<kBf16, false>),
+                       grid, kThreads, 0, 1, s, a);
     }
     return e == cudaSuccess ? ZERO_OK : cuda_refuse(e, "zero_mx4_quantize");
 }
@@ -812,9 +843,12 @@ int zero_mx4_dequantize(int dtype, uint64_t rows, uint64_t cols, const void* cod
     a.pitch = mx_pitch(cols);
     a.tiles_k = up(cols, 128) / 128;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const dim3 grid = row_grid(rows, cols);
-    const cudaError_t e = dtype == ZERO_FP16 ? launch_pdl(k_mx4_values<kFp16>, grid, kThreads, 0, 1, s, a)
-                           : launch_pdl(k_mx4_values<kBf16>, grid, kThreads, 0, 1, s, a);
+    const dim3 grid = row_grid(rows, cols + 7);
+    const bool fp16 = dtype == ZERO_FP16;
+    const cudaError_t e =
+        launch_pdl(aligned(out16, 16) && ld % 8 == 0 ? (fp16 ? k_mx4_values<kFp16, true> : k_mx4_values<kBf16, true>)
+                                                     : (fp16 ? k_mx4_values<kFp16, false> : k_mx4_values<kBf16, false>),
+                   grid, kThreads, 0, 1, s, a);
     return e == cudaSuccess ? ZERO_OK : cuda_refuse(e, "zero_mx4_dequantize");
 }
 

@@ -611,7 +611,6 @@ __device__ __forceinline__ void load_eight(const unsigned short* at, int valid, 
 
 template <int DT>
 __global__ void __launch_bounds__(kSmallThreads) k_ortho_small(const __grid_constant__ SmallArgs p) {
-    pdl_enter();
     extern __shared__ unsigned char smem_raw[];
     __shared__ __align__(8) uint64_t s_bar;
     __shared__ uint32_t s_tmem;
@@ -633,6 +632,8 @@ __global__ void __launch_bounds__(kSmallThreads) k_ortho_small(const __grid_cons
         bar_init_fence();
     }
     if (warp == 0) tmem_alloc(smem_u32(&s_tmem), 512);
+    __syncthreads();   // tensor memory is held before the next kernel may come (pdl_enter)
+    pdl_enter();
     for (uint32_t i = tid; i < 3u * p.steps; i += kSmallThreads) s_coeffs[i] = p.coeffs[i];
     for (uint32_t i = tid; i < blocks * (kBlockBytes / 16); i += kSmallThreads) st_shared(x + 16 * i, 0u, 0u, 0u, 0u);
     tc_fence_before();

@@ -1,9 +1,7 @@
-// A warp's access to 256 consecutive 16-bit values of a row-major matrix
-// whose rows may start anywhere: 8 values a lane, moved as aligned 16-byte
-// pieces whatever the row's alignment.  A row that starts m values past a
-// 16-byte boundary is read as the pieces that cover it, each lane joining its
-// own with its neighbour's; only pieces that would leave the matrix are read
-// or written value by value, so nothing outside the matrix is touched.
+// A warp's reads of 256 consecutive 16-bit values of a row-major matrix whose
+// rows may start anywhere: 8 values a lane, as the aligned 16-byte pieces that
+// cover them, whatever the row's alignment.  Only pieces that would leave the
+// matrix are read value by value, so nothing outside of it is touched.
 #pragma once
 
 #include "zero_device.cuh"
@@ -11,8 +9,8 @@
 namespace zg {
 namespace {
 
-// Words [m, m + 8) halves of the 16 halves lo:hi, m in 1..7 and the same in
-// all lanes.
+// Halves m to m + 7 of the 16 halves lo, hi; m in 1..7 and the same in all
+// lanes.
 __device__ __forceinline__ void shift_halves(const uint32_t (&lo)[4], const uint32_t (&hi)[4], uint32_t m,
                                              uint32_t (&out)[4]) {
     uint32_t w[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
@@ -47,68 +45,24 @@ __device__ __forceinline__ void load_piece(const unsigned short* base, int64_t a
 
 // This lane's 8 values (packed pairs) from value `at` of the matrix on; lanes
 // of a warp take consecutive eights.  `total`: values from `base` to the
-// matrix's end.  Values past a row's end are the caller's to ignore.  Every
-// lane of the warp must call it.
+// matrix's end.  Values past a row's end are the caller's to ignore.
 __device__ __forceinline__ void load8(const unsigned short* base, int64_t at, int64_t total, uint32_t (&w)[4]) {
     const uint32_t m = static_cast<uint32_t>((reinterpret_cast<uintptr_t>(base) >> 1) + static_cast<uint64_t>(at)) & 7u;
     if (m == 0) {
         load_piece(base, at, total, w);
         return;
     }
-    uint32_t own[4], next[4];
-    load_piece(base, at - m, total, own);
-    const bool last = (threadIdx.x & 31) == 31;
-    if (last) load_piece(base, at - m + 8, total, next);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t x = __shfl_down_sync(0xFFFFFFFFu, own[i], 1);
-        if (!last) next[i] = x;
+    uint32_t own[4], next[4];   // two pieces, the second one the next lane's first: the cache serves it
+    if (at >= static_cast<int64_t>(m) && at + 16 <= total) {
+        const uint4* from = reinterpret_cast<const uint4*>(base + at - m);
+        const uint4 x = __ldg(from), y = __ldg(from + 1);
+        own[0] = x.x; own[1] = x.y; own[2] = x.z; own[3] = x.w;
+        next[0] = y.x; next[1] = y.y; next[2] = y.z; next[3] = y.w;
+    } else {
+        load_piece(base, at - m, total, own);
+        load_piece(base, at - m + 8, total, next);
     }
     shift_halves(own, next, m, w);
-}
-
-// Writes the first `valid` of this lane's 8 values at value `at`; lanes of a
-// warp hold consecutive eights of one row, `valid` being the row's values
-// from this lane's first one on (any more than 8 are the next lane's; 0 and
-// less past the row's end).  Every lane of the warp must call it.
-__device__ __forceinline__ void store8(unsigned short* base, int64_t at, int valid, const uint32_t (&w)[4]) {
-    const uint32_t m = static_cast<uint32_t>((reinterpret_cast<uintptr_t>(base) >> 1) + static_cast<uint64_t>(at)) & 7u;
-    const int lane = threadIdx.x & 31;
-    if (m == 0) {
-        if (valid >= 8) {
-            __stcs(reinterpret_cast<uint4*>(base + at), make_uint4(w[0], w[1], w[2], w[3]));
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (e < valid) base[at + e] = static_cast<unsigned short>(w[e >> 1] >> (16 * (e & 1)));
-        }
-        return;
-    }
-    // this lane's aligned piece starts m values before `at`: the last m
-    // values of the lane before, then its own first 8 - m
-    uint32_t prev[4], piece[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) prev[i] = __shfl_up_sync(0xFFFFFFFFu, w[i], 1);
-    shift_halves(prev, w, 8 - m, piece);
-    if (lane > 0 && valid >= static_cast<int>(8 - m)) {
-        __stcs(reinterpret_cast<uint4*>(base + at - m), make_uint4(piece[0], piece[1], piece[2], piece[3]));
-    } else {
-        // a partial piece: lane 0 has no values before its own; elsewhere
-        // the row ends inside it
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int mine = e - static_cast<int>(m);   // index among this lane's values
-            if (mine < valid && (mine >= 0 || lane > 0))
-                base[at + mine] = static_cast<unsigned short>(piece[e >> 1] >> (16 * (e & 1)));
-        }
-    }
-    // the last lane's remaining m values have no lane after it
-    if (lane == 31) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (e >= static_cast<int>(8 - m) && e < valid)
-                base[at + e] = static_cast<unsigned short>(w[e >> 1] >> (16 * (e & 1)));
-    }
 }
 
 // A lane's values left of a row's `cols` from column c on, within +-8.

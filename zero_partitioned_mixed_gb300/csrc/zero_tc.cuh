@@ -244,6 +244,10 @@ __device__ __forceinline__ void count_done(uint32_t* counter) {
     asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(counter) : "memory");
 }
 // ----------------------------------------------------------------- tcgen05
+// A block allocates tensor memory before its pdl_enter(), with a block-wide
+// barrier in between: the next kernel's blocks come only after every block of
+// this one has passed pdl_enter(), so they cannot hold tensor memory that a
+// block of this kernel still waits for while they themselves wait for it.
 __device__ __forceinline__ void tmem_alloc(uint32_t smem_slot, uint32_t cols) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_slot), "r"(cols)
                  : "memory");

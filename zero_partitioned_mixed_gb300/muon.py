@@ -16,6 +16,7 @@ from typing import Dict, List, Optional, Sequence, Tuple
 import torch
 
 from . import _binding as B
+from .mx4 import Mx4Matrix
 from .synth import torch_dtype
 
 _ZDT = {"fp16": B.ZERO_FP16, "bf16": B.ZERO_BF16}
@@ -86,6 +87,11 @@ class MuonBuffers:
             B.zero_orthogonalize(B.ZERO_BF16, r, c, src, dst, self.workspace, steps=steps, coeffs=coeffs,
                                  scale=float(scale(r, c)), stream=stream)
         B.zero_muon_apply(dt, self.count, self.ortho, self.master, self._param_rows, hyp, self.state, stream)
+
+    def quantize(self, i: int, transpose: bool = False, rank: int = 0, stream=None) -> Mx4Matrix:
+        """Matrix i of a rank's replica in microscaled 4 bits: what the others receive in a 4-bit gather,
+        ready to multiply with.  transpose: along its columns, as the backward pass takes it."""
+        return Mx4Matrix.of(self.matrix(i, self.params[rank]), transpose, stream)
 
     def status(self, stream=None) -> dict:
         """The state after the last step; raises when a kernel's bounded wait gave up."""
