@@ -100,8 +100,8 @@ def test_code_and_scale_buffers_keep_their_bounds():
 
 
 PRODUCTS = [(1, 1, 1), (1, 300, 64), (1, 129, 1000), (2, 8, 31), (5, 257, 96), (16, 40, 33), (17, 130, 512), (33, 640, 2049),
-            (64, 128, 128), (100, 100, 4100), (127, 129, 257), (128, 256, 256), (130, 515, 1111), (300, 70, 640),
-            (513, 511, 300), (700, 1300, 384)]
+            (64, 128, 128), (100, 100, 4100), (32, 200, 700), (65, 2000, 300), (127, 129, 257), (128, 256, 256), (130, 515, 1111), (300, 70, 640),
+            (513, 511, 300), (700, 1300, 384), (2100, 4000, 520), (257, 193, 64), (3000, 2000, 256)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
@@ -216,6 +216,20 @@ def test_other_stream_graph_and_repeats():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want)
+
+
+def test_many_passes_in_a_row():
+    # quantising and product alternate without a wait for the host, each overlapping the other's start
+    x, w = matrix(1500, 1024, "bf16", 1).cuda(), Mx4Matrix.of(matrix(3000, 1024, "bf16", 2).cuda())
+    few = x[:7]
+    want, want_few = mx4_linear(x, w), mx4_linear(few, w)
+    scratch, scratch_few = Mx4Matrix(1500, 1024), Mx4Matrix(7, 1024)
+    outs, outs_few = [torch.empty_like(want) for _ in range(4)], [torch.empty_like(want_few) for _ in range(4)]
+    for i in range(400):
+        mx4_linear(x, w, outs[i % 4], scratch)
+        mx4_linear(few, w, outs_few[i % 4], scratch_few)
+    Z.zero_matrix_status()
+    assert all(torch.equal(o, want) for o in outs) and all(torch.equal(o, want_few) for o in outs_few)
 
 
 def test_refusals():

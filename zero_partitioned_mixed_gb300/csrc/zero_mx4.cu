@@ -309,14 +309,16 @@ __global__ void __launch_bounds__(kThreads) k_mx4_values(const __grid_constant__
 }
 
 // ----------------------------------------------------------------- product
-// out[m][n] = sum over k of A[m][k] B[n][k], fp32 accumulation.  A pair of
-// CTAs computes 256 x 192: a stage of 256 values of k is 31 KiB a CTA for 384
-// cycles of products, so L2's supply to the SMs is what bounds it, and the
-// tile is as large as leaves room in tensor memory for two accumulators (one
-// tile's output is written under the next one's products) beside the
-// scales.  192 columns begin in the middle of a scale tile of 128 rows half
-// of the time: two scale tiles cover them either way, and the product starts
-// two columns further on in tensor memory.
+// out[m][n] = sum over k of A[m][k] B[n][k], fp32 accumulation.  A CTA
+// computes 256 x 192 as two accumulators of 128 rows that share B's tile (MT
+// 2), or 128 x 192 (MT 1).  A stage of 256 values of k is 60 KiB for 768
+// cycles of products (43 for 384), so what an SM gets from L2 (some 50 bytes
+// a cycle) bounds it and the larger tile is the better one as long as there
+// are tiles for all SMs.  Two accumulators and four sets of scales fill
+// tensor memory: one accumulator is written out while the other one's
+// products run.  192 columns begin in the middle of a scale tile of 128 rows
+// half of the time: two scale tiles cover them either way, and the product
+// starts two columns further on in tensor memory.
 struct MxProductArgs {
     uint32_t m, n, k;
     uint32_t tiles_m, tiles_n, total;
@@ -326,17 +328,21 @@ struct MxProductArgs {
     int vec;                 // rows of out start on 16 bytes
 };
 
-constexpr int kMxM = 256, kMxN = 192, kMxK = 256;   // a stage's values of k are 128 bytes of a row
-constexpr uint32_t kMxABytes = kMxM / 2 * kMxK / 2, kMxBBytes = kMxN / 2 * kMxK / 2;   // a CTA's halves
-constexpr uint32_t kMxStage = kMxABytes + kMxBBytes + 1024 + 2048;   // and its rows' scales, and all columns'
-constexpr int kMxStages = 6;
-constexpr uint32_t kMxOut = 32 * 64 * 2;            // a warp's output buffer, two each
-constexpr size_t kMxSmem = 1024 + kMxStages * kMxStage + 8 * kMxOut;
-constexpr int kMxThreads = 192;
+constexpr int kMxN = 192, kMxK = 256;   // a stage's values of k are 128 bytes of a row
+constexpr int kMxOutWarps = 8, kMxThreads = 64 + 32 * kMxOutWarps;
+constexpr uint32_t kMxOut = 32 * 32 * 2;   // a warp's output buffer, two each
+template <int MT>
+struct MxTile {
+    static constexpr uint32_t kRows = 128 * MT, kA = kRows * 128, kB = kMxN * 128, kScaleA = 1024 * MT, kScaleB = 2048;
+    static constexpr uint32_t kStage = kA + kB + kScaleA + kScaleB;
+    static constexpr int kStages = MT == 2 ? 3 : 4;   // at most the sets of scales: a set is free once its stage is
+    static constexpr uint32_t kSet = 8 * MT + 16;     // columns of a set: 4 for 128 rows and 128 values of k
+    static constexpr size_t kSmem = 1024 + kStages * kStage + kMxOutWarps * 2 * kMxOut;
+    static_assert(2 * kMxN + 4 * kSet <= 512, "tensor memory");
+};
 
 // A scale tile (32 lines of 16 bytes in shared memory) into 4 columns of
-// tensor memory, repeated in each quarter of the lanes, in both CTAs from
-// their own shared memory.
+// tensor memory, repeated in each quarter of the lanes.
 __device__ __forceinline__ uint64_t scale_desc(uint32_t smem) {
     uint64_t d = static_cast<uint64_t>((smem & 0x3FFFFu) >> 4);
     d |= static_cast<uint64_t>(128u >> 4) << 32;   // 8 lines of 16 bytes
@@ -344,13 +350,13 @@ __device__ __forceinline__ uint64_t scale_desc(uint32_t smem) {
     return d;
 }
 __device__ __forceinline__ void tc_copy_scales(uint32_t tmem, uint64_t d) {
-    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(d) : "memory");
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(d) : "memory");
 }
 __device__ __forceinline__ void mma_mx4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
                                         bool accumulate) {
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
         ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(static_cast<uint32_t>(accumulate))
         : "memory");
 }
@@ -365,184 +371,171 @@ __device__ __forceinline__ void mx_tile(const MxProductArgs& p, uint32_t t, uint
     tm = band * kBand + in - tn * high;
 }
 
-template <int DT>
+template <int DT, int MT>
 __global__ void __launch_bounds__(kMxThreads)
 k_mx4_product(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
               const __grid_constant__ CUtensorMap map_sa, const __grid_constant__ CUtensorMap map_sb,
               const __grid_constant__ MxProductArgs p) {
+    using T = MxTile<MT>;
+    constexpr uint32_t kStages = T::kStages;
     extern __shared__ unsigned char smem_raw[];
-    __shared__ __align__(8) uint64_t bars[2 * kMxStages + 4];
-    __shared__ __align__(8) uint64_t s_last;
+    __shared__ __align__(8) uint64_t bars[2 * kStages + 5];
     __shared__ uint32_t s_tmem;
     __shared__ int s_quit;
     volatile int* quit = &s_quit;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_rank();
+    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    const uint32_t full = smem_u32(bars), empty = full + 8 * kMxStages, done = empty + 8 * kMxStages, freed = done + 16;
+    const uint32_t full = smem_u32(bars), empty = full + 8 * kStages, done = empty + 8 * kStages, freed = done + 16,
+                   last = freed + 16;
     if (threadIdx.x == 0) {
         s_quit = 0;
-        for (int i = 0; i < kMxStages; ++i) {
-            bar_init(full + 8 * i, 1);
-            bar_init(empty + 8 * i, 1);
-        }
-        for (int i = 0; i < 2; ++i) {
-            bar_init(done + 8 * i, 1);
-            bar_init(freed + 8 * i, 8);
-        }
-        bar_init(smem_u32(&s_last), 1);
+        for (uint32_t i = 0; i < 2 * kStages + 2; ++i) bar_init(full + 8 * i, 1);
+        for (uint32_t i = 0; i < 2; ++i) bar_init(freed + 8 * i, kMxOutWarps);
+        bar_init(last, 1);
         bar_init_fence();
         prefetch_map(&map_a);
         prefetch_map(&map_b);
         prefetch_map(&map_sa);
         prefetch_map(&map_sb);
     }
-    if (warp == 1) tmem_alloc_pair(smem_u32(&s_tmem), 512);
+    if (warp == 1) tmem_alloc(smem_u32(&s_tmem), 512);
     tc_fence_before();
     __syncthreads();
-    cluster_sync();
     tc_fence_after();
     const uint32_t tmem = s_tmem;
     pdl_enter();
-    const uint32_t nk = (p.k + kMxK - 1) / kMxK, stride = gridDim.x >> 1;
+    const uint32_t nk = (p.k + kMxK - 1) / kMxK;
 
     if (warp == 0 && elect_one()) {
-        const uint32_t leader_full = cluster_addr(full, 0);
-        Ring<kMxStages> r;
+        Ring<kStages> r;
+        uint32_t fills = 0;
         bool ok = true;
-        for (uint32_t t = blockIdx.x >> 1; t < p.total && ok; t += stride) {
+        for (uint32_t t = blockIdx.x; t < p.total && ok; t += gridDim.x) {
             uint32_t tm, tn;
             mx_tile(p, t, tm, tn);
-            const int ra = static_cast<int>(tm * kMxM + rank * (kMxM / 2)), rb = static_cast<int>(tn * kMxN + rank * (kMxN / 2));
-            for (uint32_t kb = 0; kb < nk; ++kb, r.next()) {
-                if (!bar_wait(empty + 8 * r.s, r.parity ^ 1, quit)) {   // passes at once in the first round
+            const int ra = static_cast<int>(tm * T::kRows), rb = static_cast<int>(tn * kMxN);
+            for (uint32_t kb = 0; kb < nk; ++kb, r.next(), ++fills) {
+                if (!bar_wait(empty + 8 * r.s, r.parity ^ 1, quit, kForSpace)) {   // passes at once in the first round
                     ok = false;
                     break;
                 }
-                const uint32_t bar = leader_full + 8 * r.s, st = ring + r.s * kMxStage;
-                const uint32_t ss = st + kMxABytes + kMxBBytes;
-                if (rank == 0) bar_expect(full + 8 * r.s, 2 * kMxStage);   // the bytes of both CTAs
-                copy_box_pair(st, &map_a, static_cast<int>(kb * 128), ra, 0, bar);
-                copy_box_pair(st + kMxABytes, &map_b, static_cast<int>(kb * 128), rb, 0, bar);
-                copy_box_pair(ss, &map_sa, 0, static_cast<int>(8 * kb), ra >> 7, bar);
-                copy_box_pair(ss + 1024, &map_sb, 0, static_cast<int>(8 * kb), static_cast<int>(tn * kMxN) >> 7, bar);
+                const uint32_t bar = full + 8 * r.s, st = ring + r.s * T::kStage;
+                const uint32_t ss = st + T::kA + T::kB;
+                bar_expect(bar, T::kStage);
+                copy_box(st, &map_a, static_cast<int>(kb * 128), ra, 0, bar);
+                copy_box(st + T::kA, &map_b, static_cast<int>(kb * 128), rb, 0, bar);
+                copy_box(ss, &map_sa, 0, static_cast<int>(8 * kb), ra >> 7, bar);
+                copy_box(ss + T::kScaleA, &map_sb, 0, static_cast<int>(8 * kb), rb >> 7, bar);
             }
         }
-    } else if (warp == 1 && rank == 0 && elect_one()) {
-        // e2m1 operands, power-of-two scales, 256 x 192
-        constexpr uint32_t idesc = (1u << 7) | (1u << 10) | (static_cast<uint32_t>(kMxN >> 3) << 17) | (1u << 23) |
-                                   (static_cast<uint32_t>(kMxM >> 4) << 24);
-        const uint64_t desc0 = operand_desc(ring, 0), scales0 = scale_desc(ring + kMxABytes + kMxBBytes);
-        Ring<kMxStages> r, c;     // the products' stage, and that whose scales go into tensor memory next
-        uint32_t it = 0, copied = 0, n = 0;   // stages so far, of both
-        const uint32_t mine = blockIdx.x >> 1 < p.total ? (p.total - 1 - (blockIdx.x >> 1)) / stride + 1 : 0;
-        const uint32_t fills = mine * nk;
-        const uint32_t sf0 = tmem + 2 * kMxN;
-        auto copy_scales = [&]() {
-            const uint64_t ss = scales0 + c.s * (kMxStage >> 4);
-            const uint32_t sf = sf0 + (copied & 3) * 24;
-#pragma unroll
-            for (uint32_t h = 0; h < 2; ++h) {   // per 128 values: a scale tile of A's rows, two of B's
-                tc_copy_scales(sf + 4 * h, ss + (512 >> 4) * h);
-                tc_copy_scales(sf + 8 + 8 * h, ss + (1024 >> 4) + (512 >> 4) * h);
-                tc_copy_scales(sf + 12 + 8 * h, ss + (2048 >> 4) + (512 >> 4) * h);
-            }
-            ++copied;
-            c.next();
-        };
+        if (!ok)   // the block must not leave with copies in flight
+            for (uint32_t i = fills > kStages ? fills - kStages : 0; i < fills; ++i)
+                bar_drain(full + 8 * (i % kStages), (i / kStages) & 1);
+    } else if (warp == 1 && elect_one()) {
+        // e2m1 operands, power-of-two scales, 128 x 192
+        constexpr uint32_t idesc =
+            (1u << 7) | (1u << 10) | (static_cast<uint32_t>(kMxN >> 3) << 17) | (1u << 23) | (8u << 24);
+        const uint64_t desc0 = operand_desc(ring, 0), scales0 = scale_desc(ring + T::kA + T::kB);
+        Ring<kStages> r;
+        uint32_t it = 0, n = 0;   // stages, and accumulators begun
         bool ok = true;
-        for (uint32_t t = blockIdx.x >> 1; t < p.total && ok; t += stride, ++n) {
-            const uint32_t acc = n & 1, d = tmem + acc * kMxN;
+        for (uint32_t t = blockIdx.x; t < p.total && ok; t += gridDim.x, n += MT) {
             uint32_t tm, tn;
             mx_tile(p, t, tm, tn);
             const uint32_t odd = tn & 1 ? 2u : 0u;   // columns that begin with a scale tile's row 64
-            if (n >= 2 && !bar_wait(freed + 8 * acc, (n / 2 - 1) & 1, quit)) break;
-            tc_fence_after();
-            for (uint32_t kb = 0; kb < nk; ++kb, ++it, r.next()) {
-                if (copied == it) {
-                    if (!bar_wait(full + 8 * c.s, c.parity, quit)) {
-                        ok = false;
-                        break;
+            for (uint32_t kb = 0; kb < nk && ok; ++kb, ++it, r.next()) {
+                if (!bar_wait(full + 8 * r.s, r.parity, quit, kForData)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint64_t da = desc0 + r.s * (T::kStage >> 4), db = da + (T::kA >> 4);
+                const uint64_t ss = scales0 + r.s * (T::kStage >> 4);
+                const uint32_t sf = tmem + 2 * kMxN + (it & 3) * T::kSet, sfb = sf + 8 * MT;
+#pragma unroll
+                for (uint32_t h = 0; h < 2; ++h) {   // per 128 values of k
+#pragma unroll
+                    for (uint32_t i = 0; i < MT; ++i) tc_copy_scales(sf + 8 * i + 4 * h, ss + (1024 >> 4) * i + (512 >> 4) * h);
+#pragma unroll
+                    for (uint32_t i = 0; i < 2; ++i)
+                        tc_copy_scales(sfb + 8 * h + 4 * i, ss + (T::kScaleA >> 4) + (1024 >> 4) * i + (512 >> 4) * h);
+                }
+#pragma unroll
+                for (uint32_t i = 0; i < MT; ++i) {
+                    const uint32_t unit = n + i, acc = unit & 1, d = tmem + acc * kMxN;
+                    if (kb == 0 && unit >= 2) {
+                        if (!bar_wait(freed + 8 * acc, (unit / 2 - 1) & 1, quit, kForSpace)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
                     }
-                    tc_fence_after();
-                    copy_scales();
-                }
-                // the next stage's scales go ahead of this stage's products, which hide their way
-                if (copied < fills && bar_peek(full + 8 * c.s, c.parity)) {
-                    tc_fence_after();
-                    copy_scales();
-                }
-                const uint64_t da = desc0 + r.s * (kMxStage >> 4), db = da + (kMxABytes >> 4);
-                const uint32_t sf = sf0 + (it & 3) * 24;
 #pragma unroll
-                for (uint32_t h = 0; h < 2; ++h) {
-                    if (2 * kb + h >= p.tiles_k) break;
+                    for (uint32_t h = 0; h < 2; ++h) {
+                        if (2 * kb + h >= p.tiles_k) break;
 #pragma unroll
-                    for (uint32_t j = 0; j < 2; ++j)
-                        mma_mx4(d, da + (2 * h + j) * 2, db + (2 * h + j) * 2, idesc | (2 * j << 4) | (2 * j << 29), sf + 4 * h,
-                                sf + 8 + 8 * h + odd, kb > 0 || h > 0 || j > 0);
+                        for (uint32_t j = 0; j < 2; ++j)
+                            mma_mx4(d, da + (16384 >> 4) * i + (2 * h + j) * 2, db + (2 * h + j) * 2,
+                                    idesc | (2 * j << 4) | (2 * j << 29), sf + 8 * i + 4 * h, sfb + 8 * h + odd,
+                                    kb > 0 || h > 0 || j > 0);
+                    }
+                    if (kb + 1 == nk) tc_commit(done + 8 * acc);
                 }
-                tc_commit_pair(empty + 8 * r.s);
+                tc_commit(empty + 8 * r.s);
             }
-            if (ok) tc_commit_pair(done + 8 * acc);
         }
         if (*quit) {   // tensor memory must not be freed under a product
-            tc_commit_pair(smem_u32(&s_last));
-            bar_drain(smem_u32(&s_last), 0);
+            tc_commit(last);
+            bar_drain(last, 0);
         }
     } else if (warp >= 2) {
-        const uint32_t quarter = warp & 3, leader_freed = cluster_addr(freed, 0);
-        const uint32_t mine = ring + kMxStages * kMxStage + quarter * 2 * kMxOut;
-        uint32_t n = 0;
-        for (uint32_t t = blockIdx.x >> 1; t < p.total; t += stride, ++n) {
-            const uint32_t acc = n & 1;
+        const uint32_t quarter = warp & 3, part = (warp - 2) >> 2;   // 32 rows, 96 columns
+        const uint32_t mine = ring + kStages * T::kStage + (warp - 2) * 2 * kMxOut;
+        uint32_t n = 0, flip = 0;
+        bool ok = true;
+        for (uint32_t t = blockIdx.x; t < p.total && ok; t += gridDim.x) {
             uint32_t tm, tn;
             mx_tile(p, t, tm, tn);
-            const uint32_t row0 = tm * kMxM + rank * (kMxM / 2) + quarter * 32, col0 = tn * kMxN;
-            const bool ok = bar_wait(done + 8 * acc, (n / 2) & 1, quit);
-            if (__any_sync(0xFFFFFFFFu, !ok)) break;
-            tc_fence_after();
+            for (uint32_t i = 0; i < MT; ++i, ++n) {
+                const uint32_t acc = n & 1;
+                const uint32_t row0 = tm * T::kRows + 128 * i + quarter * 32, col0 = tn * kMxN + part * 96;
+                ok = bar_wait(done + 8 * acc, (n / 2) & 1, quit);
+                ok = !__any_sync(0xFFFFFFFFu, !ok);
+                if (!ok) break;
+                tc_fence_after();
 #pragma unroll 1
-            for (uint32_t c = 0; c < kMxN / 64; ++c) {
-                if (row0 >= p.m || col0 + 64 * c >= p.n) break;   // uniform over the warp
-                const uint32_t buf = mine + (c & 1) * kMxOut;
-#pragma unroll
-                for (uint32_t h = 0; h < 2; ++h) {
+                for (uint32_t c = 0; c < 96 && row0 < p.m && col0 + c < p.n; c += 32) {   // uniform over the warp
+                    const uint32_t buf = mine + flip * kMxOut;
+                    flip ^= 1;
                     float v[32];
-                    tmem_load32(tmem + acc * kMxN + 64 * c + 32 * h + (quarter << 21), v);
+                    tmem_load32(tmem + acc * kMxN + part * 96 + c + (quarter << 21), v);
 #pragma unroll
                     for (uint32_t j = 0; j < 4; ++j)
-                        st_shared(buf + piece128(lane, 4 * h + j), narrow2<DT>(v[8 * j], v[8 * j + 1]),
+                        st_shared(buf + piece64(lane, j), narrow2<DT>(v[8 * j], v[8 * j + 1]),
                                   narrow2<DT>(v[8 * j + 2], v[8 * j + 3]), narrow2<DT>(v[8 * j + 4], v[8 * j + 5]),
                                   narrow2<DT>(v[8 * j + 6], v[8 * j + 7]));
+                    __syncwarp();
+                    write_rows<32>(static_cast<unsigned short*>(p.out), p.ld, p.vec, p.m, p.n, row0, col0 + c, buf);
                 }
+                tc_fence_before();
                 __syncwarp();
-                write_rows<64>(static_cast<unsigned short*>(p.out), p.ld, p.vec, p.m, p.n, row0, col0 + 64 * c, buf);
+                if (lane == 0) bar_arrive(freed + 8 * acc);
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) bar_arrive_cluster(leader_freed + 8 * acc);
         }
-    }
-    __syncwarp();
-    if (*quit && threadIdx.x == 0) {   // copies in flight land within microseconds: leave them a millisecond
-        const uint64_t t0 = now_ns();
-        while (now_ns() - t0 < 1000000ull) {}
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    cluster_sync();
     if (warp == 1) {
         tc_fence_after();
-        tmem_free_pair(tmem, 512);
+        tmem_free(tmem, 512);
     }
-    cluster_sync();
 }
 
 // ------------------------------------------------- product with few rows
-// Up to 128 rows of A (a token, a handful, a small batch): bound by reading
-// B once.  B's rows are the tensor cores' 128 rows and A's the columns (NT of
+// Up to 32 rows of A (a token, a handful): bound by reading B once, 6.4 us for
+// a row against 4096 x 11008 (3.7 TB/s; above 32 rows the tiles of 128 are
+// faster, 8.5 us up to 256 rows).  B's rows are the tensor cores' 128 rows and A's the columns (NT of
 // them), a CTA takes 128 of B's rows over a share of k, and the CTAs of a
 // cluster add up their shares through shared memory, in order of rank.  The
 // shares are chosen so that about two CTAs an SM have their copies in flight
@@ -560,21 +553,11 @@ template <int NT>
 struct Narrow {
     static constexpr uint32_t kB = 128 * 128, kA = NT * 128, kStage = kB + kA + 2048;   // and 1 KiB of scales each
     static constexpr size_t kSmem = 1024 + kNarrowStages * kStage;
-    static constexpr uint32_t kTmem = NT <= 64 ? 128 : 256;   // the accumulator and four sets of scales
+    static constexpr uint32_t kTmem = 128;   // the accumulator and four sets of scales
+    static_assert(NT + 4 * 16 <= kTmem, "tensor memory");
     static_assert(kNarrowStages * kStage >= NT * 512, "the partial sums take the ring's place");
 };
 
-__device__ __forceinline__ void tc_copy_scales_one(uint32_t tmem, uint64_t d) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(d) : "memory");
-}
-__device__ __forceinline__ void mma_mx4_one(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
-                                            bool accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
-        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(static_cast<uint32_t>(accumulate))
-        : "memory");
-}
 template <int DT, int NT>
 __global__ void __launch_bounds__(kNarrowThreads)
 k_mx4_narrow(const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_a,
@@ -609,7 +592,7 @@ k_mx4_narrow(const __grid_constant__ CUtensorMap map_b, const __grid_constant__ 
         Ring<kNarrowStages> r;
         uint32_t kb = k0;
         for (; kb < k1; ++kb, r.next()) {
-            if (!bar_wait(empty + 8 * r.s, r.parity ^ 1, quit)) break;
+            if (!bar_wait(empty + 8 * r.s, r.parity ^ 1, quit, kForSpace)) break;
             const uint32_t bar = full + 8 * r.s, st = ring + r.s * L::kStage;
             bar_expect(bar, L::kStage);
             copy_box(st, &map_b, static_cast<int>(kb * 128), static_cast<int>(tile * 128), 0, bar);
@@ -623,7 +606,7 @@ k_mx4_narrow(const __grid_constant__ CUtensorMap map_b, const __grid_constant__ 
         Ring<kNarrowStages> r;
         bool ok = true;
         for (uint32_t kb = k0; kb < k1; ++kb, r.next()) {
-            if (!bar_wait(full + 8 * r.s, r.parity, quit)) {
+            if (!bar_wait(full + 8 * r.s, r.parity, quit, kForData)) {
                 ok = false;
                 break;
             }
@@ -632,15 +615,15 @@ k_mx4_narrow(const __grid_constant__ CUtensorMap map_b, const __grid_constant__ 
             const uint32_t sf = tmem + NT + ((kb - k0) & 3) * 16;
 #pragma unroll
             for (uint32_t h = 0; h < 2; ++h) {
-                tc_copy_scales_one(sf + 4 * h, ss + (512 >> 4) * h);
-                tc_copy_scales_one(sf + 8 + 4 * h, ss + (1024 >> 4) + (512 >> 4) * h);
+                tc_copy_scales(sf + 4 * h, ss + (512 >> 4) * h);
+                tc_copy_scales(sf + 8 + 4 * h, ss + (1024 >> 4) + (512 >> 4) * h);
             }
 #pragma unroll
             for (uint32_t h = 0; h < 2; ++h) {
                 if (2 * kb + h >= p.tiles_k) break;
 #pragma unroll
                 for (uint32_t j = 0; j < 2; ++j)
-                    mma_mx4_one(tmem, db + (2 * h + j) * 2, da + (2 * h + j) * 2, idesc | (2 * j << 4) | (2 * j << 29),
+                    mma_mx4(tmem, db + (2 * h + j) * 2, da + (2 * h + j) * 2, idesc | (2 * j << 4) | (2 * j << 29),
                                 sf + 4 * h, sf + 8 + 4 * h, kb > k0 || h > 0 || j > 0);
             }
             tc_commit(empty + 8 * r.s);
@@ -723,11 +706,6 @@ int mx_check(int dtype, uint64_t rows, uint64_t cols, const void* codes, const v
 dim3 row_grid(uint64_t rows, uint64_t cols) {
     const uint64_t per = static_cast<uint64_t>(kThreads / 32) * kMxRows, segments = up(cols, 256) / 256;
     return dim3(static_cast<unsigned>(up(rows, per) / per), static_cast<unsigned>(segments < 65535 ? segments : 65535));
-}
-
-unsigned grid_of(uint64_t blocks, int sms, int per_sm) {
-    const uint64_t cap = static_cast<uint64_t>(sms) * per_sm;
-    return static_cast<unsigned>(blocks < 1 ? 1 : blocks < cap ? blocks : cap);
 }
 
 // The map of a matrix of codes in boxes of `box_rows` rows, and of its scale
@@ -867,39 +845,46 @@ int zero_mx4_matmul(int dtype, uint64_t m, uint64_t n, uint64_t k, const void* a
         e = cudaMemset2DAsync(out16, ld * 2, 0, n * 2, m, s);
         return e == cudaSuccess ? ZERO_OK : cuda_refuse(e, "zero_mx4_matmul");
     }
-    if (m <= 128) {
+    if (m <= 32) {
         e = m <= 16 ? narrow_of<16>(dtype, m, n, k, a_codes, a_scales, b_codes, b_scales, out16, ld, s)
-            : m <= 32 ? narrow_of<32>(dtype, m, n, k, a_codes, a_scales, b_codes, b_scales, out16, ld, s)
-            : m <= 64 ? narrow_of<64>(dtype, m, n, k, a_codes, a_scales, b_codes, b_scales, out16, ld, s)
-                      : narrow_of<128>(dtype, m, n, k, a_codes, a_scales, b_codes, b_scales, out16, ld, s);
+                    : narrow_of<32>(dtype, m, n, k, a_codes, a_scales, b_codes, b_scales, out16, ld, s);
         return e == cudaSuccess ? ZERO_OK : cuda_refuse(e, "zero_mx4_matmul");
     }
-    const uint64_t tiles = up(m, kMxM) / kMxM * (up(n, kMxN) / kMxN);
-    if (tiles > 0x7FFFFFFFull) return refuse(ZERO_EINVAL, "m and n are too large together");
     int sms = 0;
     if ((e = sm_count(&sms)) != cudaSuccess) return cuda_refuse(e, "zero_mx4_matmul");
+    // 256 rows a tile are cheaper a row (1224 cycles a stage against 863 for 128) unless they leave SMs idle
+    const uint64_t across = up(n, kMxN) / kMxN;
+    auto rounds = [&](uint64_t rows) { return (up(m, rows) / rows * across + sms - 1) / sms; };
+    const bool tall = rounds(256) * 1224 <= rounds(128) * 863;
+    const uint64_t rows = tall ? 256 : 128, tiles = up(m, rows) / rows * across;
+    if (tiles > 0x7FFFFFFFull) return refuse(ZERO_EINVAL, "m and n are too large together");
     MxProductArgs p = {};
     p.m = static_cast<uint32_t>(m);
     p.n = static_cast<uint32_t>(n);
     p.k = static_cast<uint32_t>(k);
-    p.tiles_m = static_cast<uint32_t>(up(m, kMxM) / kMxM);
-    p.tiles_n = static_cast<uint32_t>(up(n, kMxN) / kMxN);
+    p.tiles_m = static_cast<uint32_t>(up(m, rows) / rows);
+    p.tiles_n = static_cast<uint32_t>(across);
     p.total = static_cast<uint32_t>(tiles);
     p.tiles_k = static_cast<uint32_t>(up(k, 128) / 128);
     p.out = out16;
     p.ld = ld;
     p.vec = aligned(out16, 16) && ld % 8 == 0;
     CUtensorMap ma, mb, sa, sb;
-    if ((e = mx_maps(&ma, &sa, a_codes, a_scales, m, k, kMxM / 2, 1)) != cudaSuccess ||
-        (e = mx_maps(&mb, &sb, b_codes, b_scales, n, k, kMxN / 2, 2)) != cudaSuccess)
+    if ((e = mx_maps(&ma, &sa, a_codes, a_scales, m, k, static_cast<uint32_t>(rows), tall ? 2 : 1)) != cudaSuccess ||
+        (e = mx_maps(&mb, &sb, b_codes, b_scales, n, k, kMxN, 2)) != cudaSuccess)
         return cuda_refuse(e, "tensor map");
-    const unsigned grid = 2 * grid_of(tiles, sms / 2, 1);
-    if (dtype == ZERO_FP16) {
-        if ((e = allow_smem<k_mx4_product<kFp16>>(kMxSmem)) == cudaSuccess)
-            e = launch_pdl(k_mx4_product<kFp16>, dim3(grid), kMxThreads, kMxSmem, 2, s, ma, mb, sa, sb, p);
+    const dim3 grid(static_cast<unsigned>(tiles < static_cast<uint64_t>(sms) ? tiles : sms));
+    const bool fp16 = dtype == ZERO_FP16;
+    if (tall) {
+        constexpr size_t smem = MxTile<2>::kSmem;
+        if ((e = allow_smem<k_mx4_product<kFp16, 2>>(smem)) == cudaSuccess &&
+            (e = allow_smem<k_mx4_product<kBf16, 2>>(smem)) == cudaSuccess)
+            e = launch_pdl(fp16 ? k_mx4_product<kFp16, 2> : k_mx4_product<kBf16, 2>, grid, kMxThreads, smem, 1, s, ma, mb, sa, sb, p);
     } else {
-        if ((e = allow_smem<k_mx4_product<kBf16>>(kMxSmem)) == cudaSuccess)
-            e = launch_pdl(k_mx4_product<kBf16>, dim3(grid), kMxThreads, kMxSmem, 2, s, ma, mb, sa, sb, p);
+        constexpr size_t smem = MxTile<1>::kSmem;
+        if ((e = allow_smem<k_mx4_product<kFp16, 1>>(smem)) == cudaSuccess &&
+            (e = allow_smem<k_mx4_product<kBf16, 1>>(smem)) == cudaSuccess)
+            e = launch_pdl(fp16 ? k_mx4_product<kFp16, 1> : k_mx4_product<kBf16, 1>, grid, kMxThreads, smem, 1, s, ma, mb, sa, sb, p);
     }
     return e == cudaSuccess ? ZERO_OK : cuda_refuse(e, "zero_mx4_matmul");
 }
@@ -910,7 +895,13 @@ int zero_matrix_status(void* stream) {
     cudaError_t e = ortho_gave_up(s, &a);
     if (e == cudaSuccess) e = mx4_gave_up(s, &b);
     if (e != cudaSuccess) return cuda_refuse(e, "zero_matrix_status");
-    if (a | b) return refuse(ZERO_ETIMEOUT, "a bounded wait inside a matrix kernel gave up: its output is incomplete");
+    if (a | b) {
+        const char* what[] = {"", "space", "data", "products", "inputs"};
+        const int32_t w = a ? a : b;
+        return refuse(ZERO_ETIMEOUT, std::string("a bounded wait inside a kernel of ") +
+                                         (a ? "zero_orthogonalize" : "zero_mx4_matmul") + " gave up, for " +
+                                         what[w >= 1 && w <= 4 ? w : 0] + ": its output is incomplete");
+    }
     return ZERO_OK;
 }
 

@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(kProductThreads) k_ortho_products(const __grid
             const int rb = static_cast<int>(w.tn * kTile + rank * kHalf), z = static_cast<int>(w.b);
             const bool a_mn = f.a_mn, b_mn = f.b_mn;
             for (uint32_t kb = 0; kb < nk; ++kb, r.next()) {
-                if (!bar_wait(empty + 8 * r.s, r.parity ^ 1, quit)) {   // passes at once in the first round
+                if (!bar_wait(empty + 8 * r.s, r.parity ^ 1, quit, kForSpace)) {   // passes at once in the first round
                     ok = false;
                     break;
                 }
@@ -390,11 +390,11 @@ __global__ void __launch_bounds__(kProductThreads) k_ortho_products(const __grid
                                    (static_cast<uint32_t>(kTile >> 3) << 17) | (static_cast<uint32_t>(kTile >> 4) << 24);
             const uint32_t step_a = (f.a_mn ? 2048u : 32u) >> 4, step_b = (f.b_mn ? 2048u : 32u) >> 4;
             const uint32_t acc = n & 1, d = tmem + acc * kTile;
-            if (n >= 2 && !bar_wait(freed + 8 * acc, (n / 2 - 1) & 1, quit)) break;
+            if (n >= 2 && !bar_wait(freed + 8 * acc, (n / 2 - 1) & 1, quit, kForSpace)) break;
             tc_fence_after();
             const uint32_t nk = (f.depth + kBlockK - 1) / kBlockK;
             for (uint32_t kb = 0; kb < nk; ++kb, r.next()) {
-                if (!bar_wait(full + 8 * r.s, r.parity, quit)) {
+                if (!bar_wait(full + 8 * r.s, r.parity, quit, kForData)) {
                     ok = false;
                     break;
                 }
@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(kProductThreads) k_ortho_products(const __grid
                                      static_cast<int>(row0), z, lin_bar);
                     }
                 }
-                ok = __all_sync(0xFFFFFFFFu, ok) && bar_wait(lin_bar, lin_parity, quit);
+                ok = __all_sync(0xFFFFFFFFu, ok) && bar_wait(lin_bar, lin_parity, quit, kForData);
                 lin_parity ^= 1;
 #pragma unroll
                 for (uint32_t c = 0; c < 4; ++c)

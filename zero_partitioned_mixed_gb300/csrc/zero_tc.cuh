@@ -63,8 +63,8 @@ inline cudaError_t make_map(CUtensorMap* map, int elem, const void* base, uint64
 // ---------------------------------------------------------------- barriers
 constexpr uint64_t kGiveUpNs = 2000000000ull;   // every wait ends within about 2 s
 
-// 1 + the kernel role whose bounded wait gave up; read and cleared by the
-// host's status call.
+// What the first thread whose bounded wait gave up was waiting for (WaitFor);
+// read and cleared by the host's status call.
 __device__ int32_t g_gave_up;
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -87,12 +87,16 @@ __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
 __device__ __forceinline__ void bar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// Whether the phase of parity `parity` is complete; may suspend the thread
+// for up to kTryNs until it is.
+constexpr uint32_t kTryNs = 20000;
 __device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
-        : "r"(bar), "r"(parity)
+        : "r"(bar), "r"(parity), "r"(kTryNs)
         : "memory");
     return ok != 0;
 }
@@ -127,21 +131,24 @@ struct Ring {
         }
     }
 };
+// What a thread was waiting for when it gave up (g_gave_up).
+enum WaitFor : int32_t { kForSpace = 1, kForData = 2, kForProducts = 3, kForInputs = 4 };
+
+__device__ __noinline__ void give_up(volatile int* quit, int32_t what) {
+    *quit = 1;
+    atomicCAS(&g_gave_up, 0, what);   // the first one is the one to look at
+}
 // Waits for the phase of parity `parity`; false when the wait gave up or
-// another role of the block had (`*quit`).  The time is looked at only after
-// a few hundred failed tries, each of which may itself suspend the thread.
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* quit) {
+// another role of the block had (`*quit`).
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* quit, int32_t what = kForProducts) {
     if (bar_test(bar, parity)) return true;
-    uint64_t t0 = 0;
+    const uint64_t t0 = now_ns();
     for (uint32_t i = 1;; ++i) {
         if (bar_test(bar, parity)) return true;
-        if ((i & 127u) == 0u) {
+        if ((i & 15u) == 0u) {
             if (*quit) return false;
-            const uint64_t t = now_ns();
-            if (t0 == 0) t0 = t;
-            if (t - t0 > kGiveUpNs) {
-                *quit = 1;
-                atomicExch(&g_gave_up, 1);
+            if (now_ns() - t0 > kGiveUpNs) {
+                give_up(quit, what);
                 return false;
             }
         }
@@ -223,18 +230,15 @@ __device__ __forceinline__ void bar_arrive_cluster(uint32_t bar) {
 // Waits until the counter reaches `target` (a count of finished pieces of
 // work of other blocks, released by count_done).
 __device__ __forceinline__ bool count_wait(const uint32_t* counter, uint32_t target, volatile int* quit) {
-    uint64_t t0 = 0;
+    const uint64_t t0 = now_ns();
     for (uint32_t i = 1;; ++i) {
         uint32_t v;
         asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(counter) : "memory");
         if (v >= target) return true;
         if ((i & 63u) == 0u) {
             if (*quit) return false;
-            const uint64_t t = now_ns();
-            if (t0 == 0) t0 = t;
-            if (t - t0 > kGiveUpNs) {
-                *quit = 1;
-                atomicExch(&g_gave_up, 1);
+            if (now_ns() - t0 > kGiveUpNs) {
+                give_up(quit, kForInputs);
                 return false;
             }
         }
