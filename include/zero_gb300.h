@@ -536,9 +536,13 @@ ZERO_API int zero_muon_apply(int dtype, int n_ranks, uint64_t count, const void*
  *           zero_orthogonalize_workspace_bytes(batch, rows, cols) bytes; its
  *           contents need not be kept between calls
  * Intermediate matrices are held in fp16 with fixed scales, products
- * accumulate in fp32; coefficients must keep the singular values of every
- * X below 2 and those of a I + b A + c A^2 below 64 (two of them multiplied:
- * below 512), or the fp16 values overflow and the result is not finite.
+ * accumulate in fp32.  The coefficients must keep the singular values of
+ * every X below 3 and those of a I + b A + c A^2 (and of the first two
+ * steps' product of it) below 500, or fp16 overflows and the result is not
+ * finite.  Against 64 bits the result is off by about 2e-3 of its 2-norm,
+ * most of it the rounding to bf16; more where the shorter side is below 16.
+ * For a shorter side above 128 (or a longer one above 4096) the products run
+ * as one cooperative launch that takes the whole GPU.
  * Errors: EINVAL, ECUDA; see zero_matrix_status for a wait that gave up.
  */
 #define ZERO_MAX_MATRICES 128

@@ -70,8 +70,10 @@ __device__ __forceinline__ uint32_t codes8(const float (&x)[8]) {
 // The row kernels: a warp takes kMxRows rows by 256 columns, 8 a lane, all
 // rows' loads in flight together.  They are bound by the instructions they
 // issue as much as by HBM, so a piece that lies inside the matrix and starts
-// on 16 bytes takes a path without any of the edges' cases (`INSIDE`): 42 us
-// against 57 for 11008 x 4096 quantised and read back.
+// on 16 bytes takes a path without any of the edges' cases (`INSIDE`): for
+// 11008 x 4096 bf16 21 us to quantise (5.4 TB/s) and 23 us to read back (4.9
+// TB/s) against 28 and 28 with one path for all.  Rows at odd strides: 9.8
+// and 9.0 us for 2047 x 5003 against 6.8 and 7.3 for 2048 x 5000.
 constexpr int kMxRows = 4;
 
 template <int DT, bool INSIDE>
@@ -140,7 +142,8 @@ __global__ void __launch_bounds__(kThreads) k_mx4_rows(const __grid_constant__ M
 // Along the columns: the codes are those of the transpose.  A block takes
 // 128 rows (a scale tile's four blocks) of 128 columns, a thread 32 values
 // of two neighbouring columns; the codes go through shared memory so that a
-// row of them leaves as 64 neighbouring bytes.
+// row of them leaves as 64 neighbouring bytes.  11008 x 4096: 19.5 us (5.9
+// TB/s; one column a thread and codes straight from registers took 33).
 template <int DT>
 __global__ void __launch_bounds__(kThreads) k_mx4_columns(const __grid_constant__ MxArgs a) {
     pdl_enter();
@@ -821,10 +824,10 @@ int zero_mx4_dequantize(int dtype, uint64_t rows, uint64_t cols, const void* cod
     a.pitch = mx_pitch(cols);
     a.tiles_k = up(cols, 128) / 128;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const dim3 grid = row_grid(rows, cols + 7);
-    const bool fp16 = dtype == ZERO_FP16;
+    const bool fp16 = dtype == ZERO_FP16, whole = aligned(out16, 16) && ld % 8 == 0;
+    const dim3 grid = row_grid(rows, cols + (whole ? 0 : 7));
     const cudaError_t e =
-        launch_pdl(aligned(out16, 16) && ld % 8 == 0 ? (fp16 ? k_mx4_values<kFp16, true> : k_mx4_values<kBf16, true>)
+        launch_pdl(whole ? (fp16 ? k_mx4_values<kFp16, true> : k_mx4_values<kBf16, true>)
                                                      : (fp16 ? k_mx4_values<kFp16, false> : k_mx4_values<kBf16, false>),
                    grid, kThreads, 0, 1, s, a);
     return e == cudaSuccess ? ZERO_OK : cuda_refuse(e, "zero_mx4_dequantize");

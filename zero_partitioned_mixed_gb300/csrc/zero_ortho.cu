@@ -6,22 +6,30 @@
 //
 // Precision.  Every stored matrix is fp16 times a fixed power of two (11 bits
 // of significand against bf16's 8, at the same tensor rate); the products
-// accumulate in fp32.  G itself is exact in that form up to one power of two.
-// The rounding that costs most is that of X while its small singular values
-// are still small, so the first two steps do not form X_1 at all: with
-// B = p(A) they compose A_1 = (B A) B and Q = p(A_1) B, and X_2 = Q X_0.
-// Against 64 bits the result is off by 1.0e-3 to 1.9e-3 (2-norm, gradients
-// of low rank over noise, 64 x 64 to 768 x 2048), about what its rounding to
-// bf16 costs (1.7e-3); rounding every X gives up to 3.2e-3 and bf16
-// throughout 1e-2 to 2.5e-2.
+// accumulate in fp32.  G itself is exact in that form, but for values 2^26
+// times smaller than its largest.  The rounding that costs most is that of X
+// while its small singular values are still small, so the first two steps do
+// not form X_1 at all: with B = p(A) they compose A_1 = (B A) B and Q =
+// p(A_1) B, and X_2 = Q X_0.  Against 64 bits a result before its rounding to
+// bf16 is off by 1.0e-3 to 1.9e-3 (2-norm; gradients of low rank over noise,
+// 64 x 64 to 768 x 2048), about what that rounding costs (1.7e-3); rounding
+// every X gives up to 3.2e-3, and bf16 throughout 1e-2 to 2.5e-2.
 //
 // Work.  All products but the last of a step are symmetric: only tiles on or
-// below the diagonal are computed and each is written twice.  For the
+// below the diagonal are computed, and each is written twice.  With the
 // shorter side s and the longer l, the first two steps cost s^2 l + 5 s^3 +
-// 2 s^2 l and each further one 3 s^2 l + s^3 multiply-adds (times one; a
-// plain product would be s^2 l times two).  X is never transposed: a tall
-// matrix takes its Gram matrix from MN-major operands and is multiplied from
-// the right, a wide one the other way around.
+// 2 s^2 l floating-point operations and each further one s^2 l + s^3 +
+// 2 s^2 l (an ordinary product of s x l by l x s costs 2 s^2 l).  X is never
+// transposed: a tall matrix takes its Gram matrix from MN-major operands and
+// is multiplied from the right, a wide one the other way around.
+//
+// Two kernels by size.  A shorter side of at most 128 (and a longer one of at
+// most 4096) stays on chip: k_ortho_small, one launch, 21 us for 96 x 160.
+// Anything else goes through global memory (in practice L2): two streams that
+// scale and pack G, then k_ortho_products, all products in one cooperative
+// launch.  Measured with five steps: 12 x 768 x 768 188 us, 6 x 1531 x 1003
+// 252 us, 11008 x 4096 1.92 ms, which is 1.44 PFLOP/s of the operations above
+// (75 % of a plain bf16 product's rate).
 
 #include <cmath>
 #include <cstdint>
@@ -213,7 +221,11 @@ __global__ void __launch_bounds__(kThreads) k_ortho_pack(const __grid_constant__
 // launch or a grid-wide barrier between them.  Tiles are handed out in
 // order of phase, matrix, tile, round robin over the CTA pairs, so every
 // tile depends on earlier ones only, and the launch is cooperative: every
-// wait ends.
+// wait ends.  For small matrices the chain of sixteen phases bounds it, some
+// 10 us each: an input's way from L2 1 us, the products 3 us (768 values),
+// their end 1 us, the epilogue 2 us, its stores and the counter 1.3 us, the
+// next phase's sight of it 1.3 us.  Large ones lose most to whole rounds of
+// tiles (136 tiles of 4096 x 4096 on 76 pairs take two).
 enum Epi : int32_t {
     kScale,   // out = f acc
     kPoly,    // out = f acc + f_lin lin + f_diag I
@@ -250,7 +262,7 @@ struct ProductArgs {
 // A pair of CTAs computes 256 x 256 tiles: a stage of 64 steps of the
 // contraction is 32 KiB a CTA for 512 cycles of products, which is about
 // what an SM gets from L2 (128 x 128 tiles of one CTA need twice that, and
-// ran at 0.9 PFLOP/s).  Warp 0 copies operands into a ring of stages, warp 1
+// ran at 0.9 PFLOP/s, 2.85 ms for 11008 x 4096).  Warp 0 copies operands into a ring of stages, warp 1
 // of the leader issues the products, warps 2 to 9 turn finished accumulators
 // into output (each 32 rows by 128 columns of a tile, by 32 columns at a
 // time); two accumulators in tensor memory, so that one tile's epilogue runs
@@ -563,8 +575,9 @@ __global__ void __launch_bounds__(kProductThreads) k_ortho_products(const __grid
 // are K-major operands of X X^T and MN-major ones of B X alike), a cluster
 // of up to 8 CTAs the whole of it, and the square matrices are computed by
 // each CTA for itself.  Only X X^T is summed over the cluster, through its
-// shared memory.  The sixteen dependent products take about a microsecond
-// each this way; through global memory they took five.
+// shared memory.  The sixteen dependent products of five steps take about a
+// microsecond each this way (21 us in all for 96 x 160); through global
+// memory they took five.
 constexpr uint32_t kSide = 128, kSlabBlocks = 8, kMaxCtas = 8;
 constexpr uint32_t kBlockBytes = kSide * 128;           // 64 columns of X, or half a square
 constexpr uint32_t kSquareBytes = 2 * kBlockBytes;
