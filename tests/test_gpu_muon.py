@@ -335,6 +335,45 @@ def test_the_example_trains():
     assert losses == mod.train(steps=25)     # every kernel of the path gives the same bits again
 
 
+# ------------------------------------------------- offsets past 32 bits
+def test_a_batch_whose_offsets_pass_32_bits():
+    side, batch = 5800, 128          # 4.3e9 elements
+    src = torch.empty((batch, side, side), dtype=torch.bfloat16, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    one = torch.randn((side, side), generator=gen, device="cuda")
+    for i in range(batch):
+        src[i] = one.roll(37 * i, 1) * (1.0 + i)
+    ws = torch.empty(Z.zero_orthogonalize_workspace_bytes(batch, side, side), dtype=torch.uint8, device="cuda")
+    Z.zero_orthogonalize(Z.ZERO_BF16, side, side, list(src.unbind(0)), list(src.unbind(0)), ws, steps=2)   # in place
+    for i in (0, 127):
+        mine = (one.roll(37 * i, 1) * (1.0 + i)).bfloat16()
+        Z.zero_orthogonalize(Z.ZERO_BF16, side, side, [mine], [mine], ws, steps=2)
+        assert torch.equal(mine, src[i])
+    Z.zero_matrix_status()
+
+
+def test_a_flat_region_whose_offsets_pass_32_bits():
+    count, tail = (1 << 32) + 1003, 5000
+    grads = torch.zeros((2, count + 5), dtype=torch.bfloat16, device="cuda")      # rows of whole eights
+    momentum = torch.zeros(2 * (count + 5), device="cuda")
+    update = torch.zeros(count + 5, dtype=torch.bfloat16, device="cuda")
+    master, params = torch.zeros(count + 5, device="cuda"), torch.zeros((1, count + 5), dtype=torch.bfloat16, device="cuda")
+    state = torch.zeros(16, dtype=torch.int32, device="cuda")
+    Z.zero_muon_set_state(state)
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    grads[:, count - tail:count] = torch.randn((2, tail), generator=gen, device="cuda").bfloat16()
+    hyp = Z.muon_hyper(lr=0.5, momentum=0.5)
+    Z.zero_muon_momentum(Z.ZERO_BF16, count, list(grads.unbind(0)), momentum, update, hyp, state)
+    Z.zero_muon_apply(Z.ZERO_BF16, count, update, master, list(params.unbind(0)), hyp, state)
+    g = (grads[0, count - tail:count].float() + grads[1, count - tail:count].float()) * 0.5
+    u = (g + 0.5 * g).bfloat16()
+    assert torch.equal(momentum[2 * (count + 5) - 5 - tail:-5], g)
+    assert torch.equal(update[count - tail:count], u)
+    assert torch.equal(master[count - tail:count], -0.5 * u.float())
+    assert torch.equal(params[0, count - tail:count], (-0.5 * u.float()).bfloat16())
+    assert not update[:count - tail].any() and not master[count:].any()
+
+
 # ------------------------------------------------------------------ refusals
 def test_refusals():
     t = torch.zeros(4096, device="cuda")

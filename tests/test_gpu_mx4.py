@@ -218,6 +218,23 @@ def test_other_stream_graph_and_repeats():
         assert torch.equal(out, want)
 
 
+def test_offsets_past_32_bits():
+    rows, cols, tail = 66016, 66003, 160        # 4.36e9 values, rows at odd offsets; the tail is whole blocks
+    x = torch.zeros((rows, cols), dtype=torch.bfloat16, device="cuda")
+    x[-tail:] = matrix(tail, cols, "bf16", 1).cuda()
+    q, small = Mx4Matrix.of(x), Mx4Matrix.of(x[-tail:])
+    assert torch.equal(q.codes.view(rows, -1)[-tail:], small.codes.view(tail, -1))
+    y = q.values()
+    assert torch.equal(y[-tail:], small.values()) and not y[:-tail].any()
+    y = Mx4Matrix.of(x, transpose=True).values()
+    assert torch.equal(y[:, -tail:], Mx4Matrix.of(x[-tail:], transpose=True).values()) and not y[:, :-tail].any()
+    del y
+    w = Mx4Matrix.of(matrix(70, cols, "bf16", 2).cuda())
+    out = mx4_product(q, w)                     # the last rows' codes lie beyond 2^31 bytes
+    # (two results, each within 2^-9 of the exact one)
+    assert rel(out[-tail:], mx4_product(small, w).double().cpu()) <= 2.0 ** -8 and not out[:-tail].any()
+
+
 def test_many_passes_in_a_row():
     # quantising and product alternate without a wait for the host, each overlapping the other's start
     x, w = matrix(1500, 1024, "bf16", 1).cuda(), Mx4Matrix.of(matrix(3000, 1024, "bf16", 2).cuda())

@@ -2,7 +2,8 @@
 
 A rank that gathers its parameters in 4 bits multiplies with the codes as
 they arrive; the three products of a layer's training step are one call on
-operands quantised along the dimension that is summed over.
+operands quantised along the dimension that is summed over.  Everything here
+runs on torch's current stream, where the tensors it makes belong.
 """
 
 from __future__ import annotations
@@ -38,27 +39,25 @@ class Mx4Matrix:
         self.scales = torch.empty(max(16, B.zero_mx4_scales_bytes(rows, cols)), dtype=torch.uint8, device=device)
 
     @classmethod
-    def of(cls, src: torch.Tensor, transpose: bool = False, stream=None) -> "Mx4Matrix":
+    def of(cls, src: torch.Tensor, transpose: bool = False) -> "Mx4Matrix":
         r, c = src.shape
-        return cls(*((c, r) if transpose else (r, c)), device=src.device).fill(src, transpose, stream)
+        return cls(*((c, r) if transpose else (r, c)), device=src.device).fill(src, transpose)
 
-    def fill(self, src: torch.Tensor, transpose: bool = False, stream=None) -> "Mx4Matrix":
+    def fill(self, src: torch.Tensor, transpose: bool = False) -> "Mx4Matrix":
         """Quantise src along its rows, or along its columns (then self holds its transpose)."""
         r, c = src.shape
         if ((c, r) if transpose else (r, c)) != (self.rows, self.cols):
             raise B.ZeroError(1, f"expected a matrix for {self.rows} x {self.cols}, got {tuple(src.shape)}")
-        B.zero_mx4_quantize(_dtype(src), r, c, src, self.codes, self.scales, ld=_rows(src), transpose=transpose,
-                            stream=stream)
+        B.zero_mx4_quantize(_dtype(src), r, c, src, self.codes, self.scales, ld=_rows(src), transpose=transpose)
         return self
 
-    def values(self, dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+    def values(self, dtype=torch.bfloat16) -> torch.Tensor:
         out = torch.empty((self.rows, self.cols), dtype=dtype, device=self.codes.device)
-        B.zero_mx4_dequantize(_dtype(out), self.rows, self.cols, self.codes, self.scales, out, stream=stream)
+        B.zero_mx4_dequantize(_dtype(out), self.rows, self.cols, self.codes, self.scales, out)
         return out
 
 
-def mx4_product(a: Mx4Matrix, b: Mx4Matrix, dtype=torch.bfloat16, out: Optional[torch.Tensor] = None,
-                stream=None) -> torch.Tensor:
+def mx4_product(a: Mx4Matrix, b: Mx4Matrix, dtype=torch.bfloat16, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """a b^T, both quantised along the dimension that is summed over."""
     if a.cols != b.cols:
         raise B.ZeroError(1, f"the operands have {a.cols} and {b.cols} columns")
@@ -66,24 +65,22 @@ def mx4_product(a: Mx4Matrix, b: Mx4Matrix, dtype=torch.bfloat16, out: Optional[
         out = torch.empty((a.rows, b.rows), dtype=dtype, device=a.codes.device)
     elif tuple(out.shape) != (a.rows, b.rows):
         raise B.ZeroError(1, f"out must be {a.rows} x {b.rows}")
-    B.zero_mx4_matmul(_dtype(out), a.rows, b.rows, a.cols, a.codes, a.scales, b.codes, b.scales, out, ld=_rows(out),
-                      stream=stream)
+    B.zero_mx4_matmul(_dtype(out), a.rows, b.rows, a.cols, a.codes, a.scales, b.codes, b.scales, out, ld=_rows(out))
     return out
 
 
 def mx4_linear(x: torch.Tensor, w: Mx4Matrix, out: Optional[torch.Tensor] = None,
-               scratch: Optional[Mx4Matrix] = None, stream=None) -> torch.Tensor:
+               scratch: Optional[Mx4Matrix] = None) -> torch.Tensor:
     """y = x w^T: x [tokens, inner] in 16 bits is quantised, w [outer, inner] is kept in 4.
     scratch: a Mx4Matrix of x's size to reuse from call to call."""
-    q = scratch.fill(x, stream=stream) if scratch is not None else Mx4Matrix.of(x, stream=stream)
-    return mx4_product(q, w, x.dtype, out, stream)
+    q = scratch.fill(x) if scratch is not None else Mx4Matrix.of(x)
+    return mx4_product(q, w, x.dtype, out)
 
 
-def mx4_linear_backward(dy: torch.Tensor, x: torch.Tensor, w_t: Mx4Matrix,
-                        stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+def mx4_linear_backward(dy: torch.Tensor, x: torch.Tensor, w_t: Mx4Matrix) -> Tuple[torch.Tensor, torch.Tensor]:
     """(dx, dw) of y = x w^T, with the rounding of the operands passed through:
     dx = dy w and dw = dy^T x, each from operands quantised along the summed
     dimension.  w_t: w quantised along its columns (Mx4Matrix.of(w, transpose=True))."""
-    dx = mx4_product(Mx4Matrix.of(dy, stream=stream), w_t, dy.dtype, stream=stream)
-    dw = mx4_product(Mx4Matrix.of(dy, True, stream), Mx4Matrix.of(x, True, stream), dy.dtype, stream=stream)
+    dx = mx4_product(Mx4Matrix.of(dy), w_t, dy.dtype)
+    dw = mx4_product(Mx4Matrix.of(dy, True), Mx4Matrix.of(x, True), dy.dtype)
     return dx, dw
