@@ -570,25 +570,34 @@ __global__ void __launch_bounds__(kProductThreads) k_ortho_products(const __grid
 }
 
 // ----------------------------------------------------- short sides up to 128
-// A matrix whose shorter side is at most 128 stays on the SM: one CTA holds
-// 512 of the longer side's values (X as 128 rows of 64-column blocks, which
-// are K-major operands of X X^T and MN-major ones of B X alike), a cluster
-// of up to 8 CTAs the whole of it, and the square matrices are computed by
-// each CTA for itself.  Only X X^T is summed over the cluster, through its
-// shared memory.  The sixteen dependent products of five steps take about a
-// microsecond each this way (21 us in all for 96 x 160); through global
-// memory they took five.
+// A matrix whose shorter side is at most 128 stays on the SM: one CTA holds up
+// to 512 of the longer side's values (256 while there are SMs for that), a
+// cluster of up to 8 CTAs the whole of it, and the square matrices are
+// computed by each CTA for itself.  Only X X^T is summed over the cluster,
+// through its shared memory.  The sixteen dependent products of five steps
+// take about a microsecond each this way; through global memory they took
+// five.
+//
+// X lies as the caller has it, in blocks of 64 columns whose rows are 128
+// bytes.  That one layout serves both products: of a wide matrix the blocks
+// are K-major operands of X X^T and MN-major ones of B X, of a tall one
+// MN-major operands of X^T X and K-major ones of X B.
+//
+// All of it runs once a launch, mostly out of a cold instruction cache, so the
+// code is kept short: one copy of the products' code for all of them, and
+// loads that need no registers (cp.async).
 constexpr uint32_t kSide = 128, kSlabBlocks = 8, kMaxCtas = 8;
-constexpr uint32_t kBlockBytes = kSide * 128;           // 64 columns of X, or half a square
+constexpr uint32_t kBlockBytes = kSide * 128;   // half a square
 constexpr uint32_t kSquareBytes = 2 * kBlockBytes;
-constexpr int kSmallThreads = 256;
+constexpr uint32_t kSlabUnit = 64 * kSide * 2;  // bytes of X for 64 of the longer side
+constexpr int kSmallThreads = 512;   // 16 warps: an epilogue is latency, and half as long as with 8
 
 struct SmallArgs {
     const void* src[kMaxMatrices];
     void* dst[kMaxMatrices];
     uint64_t ld_src, ld_dst;
     uint32_t side, span;     // the shorter and the longer side
-    uint32_t ctas, per;      // CTAs a matrix, blocks of 64 a CTA
+    uint32_t ctas, per;      // CTAs a matrix, 64s of the longer side a CTA
     int32_t tall, steps;
     float scale;
     float coeffs[3 * ZERO_MAX_NS_STEPS];
@@ -605,21 +614,9 @@ __device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t x, uint32_t y
 __device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t x) {
     asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr), "h"(static_cast<uint16_t>(x)) : "memory");
 }
-
-// 8 values of a row of the caller's matrix from column c on, packed; zeros
-// from `valid` on.
-__device__ __forceinline__ void load_eight(const unsigned short* at, int valid, bool whole, uint32_t (&w)[4]) {
-    if (whole && valid >= 8) {
-        const uint4 x = __ldg(reinterpret_cast<const uint4*>(at));
-        w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
-    } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint32_t lo = 2 * e < valid ? __ldg(at + 2 * e) : 0u;
-            const uint32_t hi = 2 * e + 1 < valid ? __ldg(at + 2 * e + 1) : 0u;
-            w[e] = lo | hi << 16;
-        }
-    }
+// 16 bytes into shared memory, the last 16 - `bytes` of them zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
 template <int DT>
@@ -634,10 +631,14 @@ __global__ void __launch_bounds__(kSmallThreads) k_ortho_small(const __grid_cons
     volatile int* quit = &s_quit;
     const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = p.ctas > 1 ? cluster_rank() : 0, b = blockIdx.x / p.ctas;
-    const uint32_t first = rank * p.per * 64;                              // this CTA's part of the longer side
-    const uint32_t span = min(p.span - first, p.per * 64), blocks = (span + 63) / 64;
+    const uint32_t first = rank * p.per * 64;                       // this CTA's part of the longer side
+    const uint32_t span = min(p.span - first, p.per * 64);
+    const bool tall = p.tall;
+    // 64s of it; an even number of a tall matrix, whose products take 128 rows at a time
+    const uint32_t blocks = tall ? (span + 127) / 128 * 2 : (span + 63) / 64;
+    const uint32_t block_bytes = tall ? blocks * 8192 : kBlockBytes;   // from 64 columns of X to the next
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    const uint32_t sq[3] = {base, base + kSquareBytes, base + 2 * kSquareBytes}, x = base + 3 * kSquareBytes;
+    const uint32_t sq0 = base, x = base + 3 * kSquareBytes;         // three squares, then X
     const uint32_t bar = smem_u32(&s_bar);
     if (tid == 0) {
         s_quit = 0;
@@ -648,44 +649,54 @@ __global__ void __launch_bounds__(kSmallThreads) k_ortho_small(const __grid_cons
     __syncthreads();   // tensor memory is held before the next kernel may come (pdl_enter)
     pdl_enter();
     for (uint32_t i = tid; i < 3u * p.steps; i += kSmallThreads) s_coeffs[i] = p.coeffs[i];
-    for (uint32_t i = tid; i < blocks * (kBlockBytes / 16); i += kSmallThreads) st_shared(x + 16 * i, 0u, 0u, 0u, 0u);
+    for (uint32_t i = tid; i < blocks * (kSlabUnit / 16); i += kSmallThreads) st_shared(x + 16 * i, 0u, 0u, 0u, 0u);
+    if (p.ctas > 1)   // what the cluster's sums leave out
+        for (uint32_t i = tid; i < kSquareBytes / 16; i += kSmallThreads) st_shared(sq0 + 16 * i, 0u, 0u, 0u, 0u);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s_tmem;
 
-    // G as it is into X (transposed when tall), and its largest magnitude
-    const unsigned short* src = static_cast<const unsigned short*>(p.src[b]);
-    const uint32_t in_rows = p.tall ? span : p.side, in_cols = p.tall ? p.side : span;
-    const uint32_t eights = (in_cols + 7) / 8, pieces = in_rows * eights;
-    if (p.tall) src += static_cast<uint64_t>(first) * p.ld_src;
-    else src += first;
-    uint32_t top = 0;
+    // G as it is into X, 16 bytes at a time where its rows start on 16 bytes
+    const uint32_t rows = tall ? span : p.side, cols = tall ? p.side : span;
+    auto place = [&](uint32_t r, uint32_t c) {
+        return x + (c >> 6) * block_bytes + piece128(r, (c & 63) >> 3) + 2 * (c & 7);
+    };
+    const uint32_t eights = (cols + 7) / 8, strips = (cols + 31) / 32;
     {
-        const bool whole = (reinterpret_cast<uintptr_t>(src) & 15) == 0 && p.ld_src % 8 == 0;
-        for (uint32_t i0 = tid; i0 < pieces; i0 += 4 * kSmallThreads) {
-            uint32_t w[4][4];
-#pragma unroll
-            for (uint32_t k = 0; k < 4; ++k) {
-                const uint32_t i = i0 + k * kSmallThreads, r = i / eights, c = (i - r * eights) * 8;
-                load_eight(src + static_cast<uint64_t>(r) * p.ld_src + c, i < pieces ? static_cast<int>(in_cols - c) : 0, whole, w[k]);
+        const unsigned short* src = static_cast<const unsigned short*>(p.src[b]) + (tall ? first * p.ld_src : first);
+        if ((reinterpret_cast<uintptr_t>(src) & 15) == 0 && p.ld_src % 8 == 0) {
+#pragma unroll 1
+            for (uint32_t i = tid; i < rows * eights; i += kSmallThreads) {
+                const uint32_t r = i / eights, c = (i - r * eights) * 8;
+                copy16(place(r, c), src + r * p.ld_src + c, 2 * min(8u, cols - c));
             }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+        } else {   // value by value, a warp's 32 next to one another
+#pragma unroll 1
+            for (uint32_t i0 = warp; i0 < rows * strips; i0 += 8 * (kSmallThreads / 32)) {
+                uint32_t v[8];   // on their way together
 #pragma unroll
-            for (uint32_t k = 0; k < 4; ++k) {
-                const uint32_t i = i0 + k * kSmallThreads, r = i / eights, c = (i - r * eights) * 8;
-                if (i >= pieces) break;
-                top = max(top, top_pattern(w[k]));
-                if (p.tall) {
+                for (uint32_t k = 0; k < 8; ++k) {
+                    const uint32_t i = i0 + k * (kSmallThreads / 32), r = i / strips, c = (i - r * strips) * 32 + lane;
+                    v[k] = r < rows && c < cols ? __ldg(src + r * p.ld_src + c) : 0u;
+                }
 #pragma unroll
-                    for (uint32_t e = 0; e < 8; ++e)
-                        if (c + e < in_cols)
-                            st_shared16(x + (r >> 6) * kBlockBytes + piece128(c + e, (r & 63) >> 3) + 2 * (r & 7),
-                                        (w[k][e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
-                } else {
-                    st_shared(x + (c >> 6) * kBlockBytes + piece128(r, (c & 63) >> 3), w[k][0], w[k][1], w[k][2], w[k][3]);
+                for (uint32_t k = 0; k < 8; ++k) {
+                    const uint32_t i = i0 + k * (kSmallThreads / 32), r = i / strips, c = (i - r * strips) * 32 + lane;
+                    if (r < rows && c < cols) st_shared16(place(r, c), v[k]);
                 }
             }
         }
+    }
+    __syncthreads();
+    // its largest magnitude
+    uint32_t top = 0;
+#pragma unroll 2
+    for (uint32_t i = tid; i < blocks * (kSlabUnit / 16); i += kSmallThreads) {
+        const uint4 v = ld_shared(x + 16 * i);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        top = max(top, top_pattern(w));
     }
     top = block_top(top);
     if (p.ctas > 1) {
@@ -696,7 +707,8 @@ __global__ void __launch_bounds__(kSmallThreads) k_ortho_small(const __grid_cons
     // X0 = G 2^k in place, and its sum of squares
     float m0, m1, sum = 0.0f;
     scale_factors<DT>(top, m0, m1);
-    for (uint32_t i = tid; i < blocks * (kBlockBytes / 16); i += kSmallThreads) {
+#pragma unroll 2
+    for (uint32_t i = tid; i < blocks * (kSlabUnit / 16); i += kSmallThreads) {
         const uint4 v = ld_shared(x + 16 * i);
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
         uint32_t q[4];
@@ -727,126 +739,120 @@ __global__ void __launch_bounds__(kSmallThreads) k_ortho_small(const __grid_cons
         parity ^= 1;
         tc_fence_after();
     };
-    constexpr uint32_t kIdesc = (1u << 4) | (static_cast<uint32_t>(kSide >> 4) << 24);
-    // this thread's part of a 128 x 128 result: 64 columns of a row
-    const uint32_t row = (warp & 3) * 32 + lane, half = warp >> 2;
-    const uint32_t my_tmem = tmem + half * 64 + ((warp & 3) << 21), my_piece = half * kBlockBytes;
-    // to = f acc (+ f_lin lin + f_diag I), acc in the first 128 columns
+    constexpr uint32_t kIdesc = (1u << 4) | (static_cast<uint32_t>(kSide >> 4) << 24);   // fp32 = fp16 fp16, 128 rows
+    constexpr uint32_t kIdesc128 = kIdesc | ((kSide >> 3) << 17), kMnA = 1u << 15, kMnB = 1u << 16;
+    // this thread's part of a 128 x 128 result: 32 columns of a row
+    const uint32_t row = (warp & 3) * 32 + lane, part = warp >> 2;
+    const uint32_t my_tmem = tmem + part * 32 + ((warp & 3) << 21);
+
+    // square `to` = f acc (+ f_lin `lin` + f_diag I), acc in the first 128 columns
     auto square_out = [&](uint32_t to, float f, bool poly, uint32_t lin, float f_lin, float f_diag) {
-        uint32_t v[2][32];
-        tmem_start32(my_tmem, v[0]);
-        tmem_start32(my_tmem + 32, v[1]);
-        tmem_wait(v[0]);
-        tmem_wait(v[1]);
-        const bool diagonal = poly && row < p.side;
+        uint32_t v[32];
+        tmem_start32(my_tmem, v);
+        tmem_wait(v);
+        const bool diagonal = poly && part == (warp & 3);   // it crosses these rows in these columns
+        const float d = row < p.side ? f_diag : 0.0f;
 #pragma unroll
-        for (uint32_t h = 0; h < 2; ++h) {
-            // the diagonal crosses this warp's rows in one group of 32 columns
-            const uint32_t diag = diagonal && 2 * half + h == (warp & 3) ? lane : 64u;
+        for (uint32_t j = 0; j < 4; ++j) {
+            const uint32_t piece = (part >> 1) * kBlockBytes + piece128(row, (part & 1) * 4 + j);
+            float y[8];
 #pragma unroll
-            for (uint32_t j = 0; j < 4; ++j) {
-                const uint32_t piece = my_piece + piece128(row, 4 * h + j);
-                float y[8];
+            for (uint32_t e = 0; e < 8; ++e) y[e] = __uint_as_float(v[8 * j + e]) * f;
+            if (poly) {
+                const uint4 l = ld_shared(lin + piece);
+                const uint32_t lw[4] = {l.x, l.y, l.z, l.w};
 #pragma unroll
-                for (uint32_t e = 0; e < 8; ++e) y[e] = __uint_as_float(v[h][8 * j + e]) * f;
-                if (poly) {
-                    const uint4 l = ld_shared(lin + piece);
-                    const uint32_t lw[4] = {l.x, l.y, l.z, l.w};
-#pragma unroll
-                    for (uint32_t e = 0; e < 4; ++e) {
-                        float lo, hi;
-                        widen2<kFp16>(lw[e], lo, hi);
-                        y[2 * e] = __fmaf_rn(lo, f_lin, y[2 * e]);
-                        y[2 * e + 1] = __fmaf_rn(hi, f_lin, y[2 * e + 1]);
-                    }
-                    // added to every value, zero or not: a test of each turns into a branch a lane
-#pragma unroll
-                    for (uint32_t e = 0; e < 8; ++e) y[e] += diag == 8 * j + e ? f_diag : 0.0f;
+                for (uint32_t e = 0; e < 4; ++e) {
+                    float lo, hi;
+                    widen2<kFp16>(lw[e], lo, hi);
+                    y[2 * e] = __fmaf_rn(lo, f_lin, y[2 * e]);
+                    y[2 * e + 1] = __fmaf_rn(hi, f_lin, y[2 * e + 1]);
                 }
-                st_shared(to + piece, narrow2<kFp16>(y[0], y[1]), narrow2<kFp16>(y[2], y[3]), narrow2<kFp16>(y[4], y[5]),
-                          narrow2<kFp16>(y[6], y[7]));
-            }
-        }
-    };
-    auto square = [&](uint32_t to, uint32_t a, uint32_t c, float f, bool poly, float f_lin, float f_diag) {
-        begin();
-        if (warp == 0 && elect_one()) {
-            const uint64_t da = operand_desc(a, 0), dc = operand_desc(c, 0);
+                if (diagonal) {   // added to every value, zero or not: a test of each turns into a branch a lane
 #pragma unroll
-            for (uint32_t k = 0; k < kSide / 16; ++k)
-                if (k < steps_k)
-                    mma_f16(tmem, da + (k >> 2) * (kBlockBytes >> 4) + (k & 3) * 2,
-                            dc + (k >> 2) * (kBlockBytes >> 4) + (k & 3) * 2, kIdesc | ((kSide >> 3) << 17), k > 0);
-            tc_commit(bar);
+                    for (uint32_t e = 0; e < 8; ++e) y[e] += lane == 8 * j + e ? d : 0.0f;
+                }
+            }
+            st_shared(to + piece, narrow2<kFp16>(y[0], y[1]), narrow2<kFp16>(y[2], y[3]), narrow2<kFp16>(y[4], y[5]),
+                      narrow2<kFp16>(y[6], y[7]));
         }
-        finish();
-        square_out(to, f, poly, a, f_lin, f_diag);
     };
-    // sq[0] = A = f X X^T, summed over the cluster
+    // the first square = f X X^T (or X^T X), summed over the cluster
     auto gram = [&](float f) {
         begin();
         if (warp == 0 && elect_one()) {
-            uint64_t d = operand_desc(x, 0);
-            for (uint32_t n = 0; n < blocks; ++n, d += kBlockBytes >> 4)
-#pragma unroll
-                for (uint32_t k = 0; k < 4; ++k) mma_f16(tmem, d + 2 * k, d + 2 * k, kIdesc | ((kSide >> 3) << 17), n > 0 || k > 0);
+            // 16 of the longer side a product: 32 bytes of a wide block's rows, 16 rows of a tall one's blocks
+            const uint64_t d0 = operand_desc(x, block_bytes);
+            const uint32_t idesc = kIdesc128 | (tall ? kMnA | kMnB : 0u);
+#pragma unroll 4
+            for (uint32_t k = 0; k < blocks * 4; ++k) {
+                const uint64_t d = d0 + (tall ? k * (2048 >> 4) : (k >> 2) * (kBlockBytes >> 4) + (k & 3) * 2);
+                mma_f16(tmem, d, d, idesc, k > 0);
+            }
             tc_commit(bar);
         }
         finish();
-        if (p.ctas == 1) {
-            square_out(sq[0], f, false, 0, 0.0f, 0.0f);
-            return;
-        }
+        if (p.ctas == 1) return;
         // the partial sums in fp32 where the other squares are, which are free here
-        const uint32_t part = sq[1];
-#pragma unroll 1
-        for (uint32_t h = 0; h < 64; h += 32) {
-            float v[32];
-            tmem_load32(my_tmem + h, v);
+        const uint32_t partial = sq0 + kSquareBytes;
+        float v[32];
+        tmem_load32(my_tmem, v);
 #pragma unroll
-            for (uint32_t j = 0; j < 8; ++j)   // pieces of 4 columns, rotated by the row against bank conflicts
-                st_shared(part + row * 512 + (((half * 16 + h / 4 + j) ^ (row & 7)) << 4), __float_as_uint(v[4 * j]),
-                          __float_as_uint(v[4 * j + 1]), __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3]));
-        }
+        for (uint32_t j = 0; j < 8; ++j)   // pieces of 4 columns, rotated by the row against bank conflicts
+            st_shared(partial + row * 512 + (((part * 8 + j) ^ (row & 7)) << 4), __float_as_uint(v[4 * j]),
+                      __float_as_uint(v[4 * j + 1]), __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3]));
         cluster_sync();
-        // every CTA adds up some of the rows, in order of rank, and gives the sums to all
-        for (uint32_t i = rank * kSmallThreads + tid; i < kSide * 32; i += p.ctas * kSmallThreads) {
-            const uint32_t r = i >> 5, c4 = i & 31;
-            const uint32_t at = part + r * 512 + ((c4 ^ (r & 7)) << 4);
-            float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            for (uint32_t q = 0; q < p.ctas; ++q) {
-                const float4 y = ld_cluster(cluster_addr(at, q));
-                s.x += y.x; s.y += y.y; s.z += y.z; s.w += y.w;
+        // every CTA adds up some of the sums, in order of rank, and gives them to all; what is past the matrix's side
+        // stays the zeros that it began with
+        const uint32_t quads = (p.side + 3) / 4, sums = p.side * quads;
+#pragma unroll 1
+        for (uint32_t i = rank * kSmallThreads + tid; i < sums; i += p.ctas * kSmallThreads) {
+            const uint32_t r = i / quads, c4 = i - r * quads;
+            const uint32_t at = partial + r * 512 + ((c4 ^ (r & 7)) << 4);
+            float4 y[kMaxCtas], s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (uint32_t q = 0; q < kMaxCtas; ++q)   // all on their way before the first is added
+                y[q] = q < p.ctas ? ld_cluster(cluster_addr(at, q)) : s;
+#pragma unroll
+            for (uint32_t q = 0; q < kMaxCtas; ++q) {
+                s.x += y[q].x; s.y += y[q].y; s.z += y[q].z; s.w += y[q].w;
             }
             const uint32_t lo = narrow2<kFp16>(s.x * f, s.y * f), hi = narrow2<kFp16>(s.z * f, s.w * f);
-            const uint32_t to = sq[0] + (c4 >> 4) * kBlockBytes + piece128(r, (c4 & 15) >> 1) + 8 * (c4 & 1);
+            const uint32_t to = sq0 + (c4 >> 4) * kBlockBytes + piece128(r, (c4 & 15) >> 1) + 8 * (c4 & 1);
+#pragma unroll 1
             for (uint32_t q = 0; q < p.ctas; ++q) st_cluster(cluster_addr(to, q), lo, hi);
         }
         proxy_fence();
         cluster_sync();
     };
-    // X = f B X in place, or as bf16 for the caller
+    // X = f B X (or X B) in place, or as bf16 for the caller
     auto update = [&](uint32_t m, float f, bool final) {
         begin();
         if (warp == 0 && elect_one()) {
-            const uint64_t dm = operand_desc(m, 0), dx = operand_desc(x, kBlockBytes);
-            for (uint32_t n0 = 0; n0 < blocks; n0 += 4) {
-                const uint32_t n = min(4u, blocks - n0), idesc = kIdesc | (1u << 16) | ((n * 8) << 17);
-#pragma unroll
-                for (uint32_t k = 0; k < kSide / 16; ++k)
-                    if (k < steps_k)
-                        mma_f16(tmem + n0 * 64, dm + (k >> 2) * (kBlockBytes >> 4) + (k & 3) * 2,
-                                dx + n0 * (kBlockBytes >> 4) + k * (2048 >> 4), idesc, k > 0);
+            const uint64_t dm = operand_desc(m, 0), dx = operand_desc(x, block_bytes);
+#pragma unroll 1
+            for (uint32_t n0 = 0; n0 < blocks; n0 += tall ? 2 : 4) {   // 256 columns, or 128 rows, at a time
+                const uint32_t idesc = tall ? kIdesc128 : kIdesc | kMnB | ((min(4u, blocks - n0) * 8) << 17);
+#pragma unroll 2
+                for (uint32_t k = 0; k < steps_k; ++k) {
+                    const uint64_t square = dm + (k >> 2) * (kBlockBytes >> 4) + (k & 3) * 2;
+                    if (tall)
+                        mma_f16(tmem + n0 * 64, dx + n0 * (8192 >> 4) + (k >> 2) * (block_bytes >> 4) + (k & 3) * 2, square,
+                                idesc, k > 0);
+                    else
+                        mma_f16(tmem + n0 * 64, square, dx + n0 * (kBlockBytes >> 4) + k * (2048 >> 4), idesc, k > 0);
+                }
             }
             tc_commit(bar);
         }
         finish();
-#pragma unroll 2
-        for (uint32_t n = half; n < 2 * blocks; n += 2) {   // 32 columns each
+#pragma unroll 1
+        for (uint32_t n = part; n < 2 * blocks; n += 4) {   // 32 columns of tensor memory each
             uint32_t v[32];
             tmem_start32(tmem + n * 32 + ((warp & 3) << 21), v);
             tmem_wait(v);
-            const uint32_t to = x + (n >> 1) * kBlockBytes;
+            const uint32_t to_row = tall ? (n >> 2) * 128 + row : row, to_col = (tall ? n & 3 : n) * 32;
+            const uint32_t to = x + (to_col >> 6) * block_bytes;
 #pragma unroll
             for (uint32_t j = 0; j < 4; ++j) {
                 uint32_t q[4];
@@ -855,59 +861,76 @@ __global__ void __launch_bounds__(kSmallThreads) k_ortho_small(const __grid_cons
                     const float lo = __uint_as_float(v[8 * j + 2 * e]) * f, hi = __uint_as_float(v[8 * j + 2 * e + 1]) * f;
                     q[e] = final ? narrow2<kBf16>(lo, hi) : narrow2<kFp16>(lo, hi);
                 }
-                st_shared(to + piece128(row, (n & 1) * 4 + j), q[0], q[1], q[2], q[3]);
+                st_shared(to + piece128(to_row, ((to_col & 63) >> 3) + j), q[0], q[1], q[2], q[3]);
             }
         }
     };
 
+#pragma unroll 1
     for (int k = 0; k < p.steps;) {
-        const float* c = s_coeffs + 3 * k;
         const bool raw = k == 0, pair = raw && p.steps >= 2;
-        auto poly = [&](uint32_t to, uint32_t a, const float* co) {
-            square(to, a, a, co[2] * (kScaleB / (kScaleA * kScaleA)), true, co[1] * (kScaleB / kScaleA), co[0] * kScaleB);
-        };
-        gram(raw ? kScaleA * g0 * g0 : kScaleA / (kScaleX * kScaleX));
-        poly(sq[1], sq[0], c);
-        uint32_t m = sq[1];
-        if (pair) {
-            square(sq[2], sq[1], sq[0], 1.0f / kScaleB, false, 0.0f, 0.0f);   // B A
-            square(sq[0], sq[1], sq[2], 1.0f / kScaleB, false, 0.0f, 0.0f);   // A_1 = B (B A)
-            poly(sq[2], sq[0], c + 3);                                        // B_1
-            square(sq[0], sq[2], sq[1], 1.0f / kScaleB, false, 0.0f, 0.0f);   // Q = B_1 B
-            m = sq[0];
+        const float f_gram = raw ? kScaleA * g0 * g0 : kScaleA / (kScaleX * kScaleX);
+        gram(f_gram);
+        // The square products that follow: B = p(A) alone, or B, B A, A_1 = B (B A), B_1 = p(A_1), Q = B_1 B.  Each
+        // digit of the three numbers is one of the squares: the result's, and the operands'.  Before them, without
+        // a cluster, the Gram matrix's own rounding.
+        const uint32_t products = pair ? 5 : 1;
+#pragma unroll 1
+        for (uint32_t i = p.ctas == 1 ? 0 : 1; i <= products; ++i) {
+            const uint32_t digit = 4 * (i - 1);
+            const uint32_t to = i == 0 ? 0u : (0x02021u >> digit) & 15u;
+            const uint32_t a = sq0 + (i == 0 ? 0u : (0x20110u >> digit) & 15u) * kSquareBytes;
+            const uint32_t c = sq0 + (i == 0 ? 0u : (0x10200u >> digit) & 15u) * kSquareBytes;
+            const bool poly = i == 1 || i == 4;
+            const float* co = s_coeffs + 3 * (k + (i == 4 ? 1 : 0));
+            if (i > 0) {
+                begin();
+                if (warp == 0 && elect_one()) {
+                    const uint64_t da = operand_desc(a, 0), dc = operand_desc(c, 0);
+#pragma unroll 2
+                    for (uint32_t s = 0; s < steps_k; ++s) {
+                        const uint32_t at = (s >> 2) * (kBlockBytes >> 4) + (s & 3) * 2;
+                        mma_f16(tmem, da + at, dc + at, kIdesc128, s > 0);
+                    }
+                    tc_commit(bar);
+                }
+                finish();
+            }
+            square_out(sq0 + to * kSquareBytes,
+                       i == 0 ? f_gram : poly ? co[2] * (kScaleB / (kScaleA * kScaleA)) : 1.0f / kScaleB, poly, a,
+                       co[1] * (kScaleB / kScaleA), co[0] * kScaleB);
         }
         k += pair ? 2 : 1;
         const bool final = k >= p.steps;
-        update(m, (final ? p.scale : kScaleX) / (raw ? kScaleB : kScaleB * kScaleX) * (raw ? g0 : 1.0f), final);
+        update(sq0 + (pair ? 0u : kSquareBytes),
+               (final ? p.scale : kScaleX) / (raw ? kScaleB : kScaleB * kScaleX) * (raw ? g0 : 1.0f), final);
     }
     __syncthreads();
 
-    // to the caller's matrix, along its rows
-    unsigned short* dst = static_cast<unsigned short*>(p.dst[b]);
-    if (p.tall) dst += static_cast<uint64_t>(first) * p.ld_dst;
-    else dst += first;
-    const bool whole = (reinterpret_cast<uintptr_t>(dst) & 15) == 0 && p.ld_dst % 8 == 0;
-    for (uint32_t i = tid; i < pieces; i += kSmallThreads) {
-        const uint32_t r = i / eights, c = (i - r * eights) * 8;
-        uint32_t w[4];
-        if (p.tall) {
+    // to the caller's matrix
+    {
+        unsigned short* dst = static_cast<unsigned short*>(p.dst[b]) + (tall ? first * p.ld_dst : first);
+        if ((reinterpret_cast<uintptr_t>(dst) & 15) == 0 && p.ld_dst % 8 == 0) {
+#pragma unroll 1
+            for (uint32_t i = tid; i < rows * eights; i += kSmallThreads) {
+                const uint32_t r = i / eights, c = (i - r * eights) * 8;
+                const uint4 v = ld_shared(place(r, c));
+                unsigned short* out = dst + r * p.ld_dst + c;
+                if (c + 8 <= cols) {
+                    *reinterpret_cast<uint4*>(out) = v;
+                } else {
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (uint32_t e = 0; e < 8; e += 2) {
-                const uint32_t at = x + (r >> 6) * kBlockBytes + 2 * (r & 7);
-                w[e >> 1] = static_cast<uint32_t>(ld_shared16(at + piece128(c + e, (r & 63) >> 3))) |
-                            static_cast<uint32_t>(ld_shared16(at + piece128(c + e + 1, (r & 63) >> 3))) << 16;
+                    for (uint32_t e = 0; e < 8; ++e)
+                        if (c + e < cols) out[e] = static_cast<unsigned short>(w[e >> 1] >> (16 * (e & 1)));
+                }
             }
         } else {
-            const uint4 v = ld_shared(x + (c >> 6) * kBlockBytes + piece128(r, (c & 63) >> 3));
-            w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
-        }
-        unsigned short* out = dst + static_cast<uint64_t>(r) * p.ld_dst + c;
-        if (whole && c + 8 <= in_cols) {
-            *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
-        } else {
-#pragma unroll
-            for (uint32_t e = 0; e < 8; ++e)
-                if (c + e < in_cols) out[e] = static_cast<unsigned short>(w[e >> 1] >> (16 * (e & 1)));
+#pragma unroll 4
+            for (uint32_t i = warp; i < rows * strips; i += kSmallThreads / 32) {
+                const uint32_t r = i / strips, c = (i - r * strips) * 32 + lane;
+                if (c < cols) dst[r * p.ld_dst + c] = ld_shared16(place(r, c));
+            }
         }
     }
     if (*quit && tid == 0) {   // a wait gave up: products may still be running
@@ -1045,15 +1068,21 @@ int zero_orthogonalize(int dtype, int batch, uint64_t rows, uint64_t cols, const
         m.side = static_cast<uint32_t>(side);
         m.span = static_cast<uint32_t>(span);
         const uint32_t blocks = (m.span + 63) / 64;
-        m.ctas = (blocks + kSlabBlocks - 1) / kSlabBlocks;
+        // 4 blocks a CTA (256 values) as long as there are SMs for that, else as many as fit
+        int sms = 0;
+        if ((e = sm_count(&sms)) != cudaSuccess) return cuda_refuse(e, "zero_orthogonalize");
+        m.ctas = (blocks + 3) / 4;
+        if (m.ctas > kMaxCtas) m.ctas = kMaxCtas;
+        while (m.ctas > 1 && m.ctas * nb > static_cast<uint32_t>(sms) && (m.ctas - 1) * kSlabBlocks >= blocks) --m.ctas;
         m.per = (blocks + m.ctas - 1) / m.ctas;
+        if (tall) m.per += m.per & 1;            // 128 rows at a time
         m.ctas = (blocks + m.per - 1) / m.per;   // none without a block
         m.tall = tall;
         m.steps = steps;
         m.scale = scale;
         for (int i = 0; i < 3 * steps; ++i) m.coeffs[i] = coeffs ? coeffs[i] : kDefaultCoeffs[i % 3];
-        const size_t smem = 1024 + 3 * kSquareBytes + static_cast<size_t>(m.per) * kBlockBytes;
-        constexpr size_t most = 1024 + 3 * kSquareBytes + kSlabBlocks * kBlockBytes;
+        const size_t smem = 1024 + 3 * kSquareBytes + static_cast<size_t>(m.per) * kSlabUnit;
+        constexpr size_t most = 1024 + 3 * kSquareBytes + kSlabBlocks * kSlabUnit;
         const dim3 grid(m.ctas * nb);
         if (dtype == ZERO_FP16) {
             if ((e = allow_smem<k_ortho_small<kFp16>>(most)) == cudaSuccess)
