@@ -24,11 +24,11 @@
 // is multiplied from the right, a wide one the other way around.
 //
 // Two kernels by size.  A shorter side of at most 128 (and a longer one of at
-// most 4096) stays on chip: k_ortho_small, one launch, 21 us for 96 x 160.
+// most 4096) stays on chip: k_ortho_small, one launch, 23 us for 96 x 160.
 // Anything else goes through global memory (in practice L2): two streams that
 // scale and pack G, then k_ortho_products, all products in one cooperative
-// launch.  Measured with five steps: 12 x 768 x 768 188 us, 6 x 1531 x 1003
-// 252 us, 11008 x 4096 1.92 ms, which is 1.44 PFLOP/s of the operations above
+// launch.  Measured with five steps: 12 x 768 x 768 186 us, 6 x 1531 x 1003
+// 249 us, 11008 x 4096 1.92 ms, which is 1.44 PFLOP/s of the operations above
 // (75 % of a plain bf16 product's rate).
 
 #include <cmath>
@@ -577,6 +577,9 @@ __global__ void __launch_bounds__(kProductThreads) k_ortho_products(const __grid
 // through its shared memory.  The sixteen dependent products of five steps
 // take about a microsecond each this way; through global memory they took
 // five.
+// Bound by that chain and by the copies in and out, on few SMs.  Five steps of
+// bf16: 96 x 160 23 us, 23 x 1519 33, 128 x 4096 55, 4096 x 128 56, 100
+// matrices of 48 x 300 31, 60 of 100 x 2000 97.
 //
 // X lies as the caller has it, in blocks of 64 columns whose rows are 128
 // bytes.  That one layout serves both products: of a wide matrix the blocks
@@ -590,7 +593,9 @@ constexpr uint32_t kSide = 128, kSlabBlocks = 8, kMaxCtas = 8;
 constexpr uint32_t kBlockBytes = kSide * 128;   // half a square
 constexpr uint32_t kSquareBytes = 2 * kBlockBytes;
 constexpr uint32_t kSlabUnit = 64 * kSide * 2;  // bytes of X for 64 of the longer side
-constexpr int kSmallThreads = 512;   // 16 warps: an epilogue is latency, and half as long as with 8
+// 16 warps: a form in which 8 of them take the products' results took 61 us against 55 for 128 x 4096 and 30 against
+// 26 for 128 x 256 (31 against 33 for 23 x 1519, whose results are smaller).
+constexpr int kSmallThreads = 512;
 
 struct SmallArgs {
     const void* src[kMaxMatrices];
