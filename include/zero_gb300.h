@@ -541,7 +541,7 @@ ZERO_API int zero_muon_apply(int dtype, int n_ranks, uint64_t count, const void*
  * steps' product of it) below 500, or fp16 overflows and the result is not
  * finite.  Against 64 bits the result is off by about 2e-3 of its 2-norm,
  * most of it the rounding to bf16; more where the shorter side is below 16.
- * For a shorter side above 128 (or a longer one above 4096) the products run
+ * For a shorter side above 128 (or a longer one above 8192) the products run
  * as one cooperative launch that takes the whole GPU.
  * Errors: EINVAL, ECUDA; see zero_matrix_status for a wait that gave up.
  */

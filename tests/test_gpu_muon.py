@@ -56,6 +56,20 @@ def test_orthogonalize_matches_64_bits(rows, cols, dtype):
         assert rel(got[i], newton_schulz(g[i].double())) <= bound(rows, cols)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("batch,rows,cols", [(1, 5, 4097), (1, 100, 8192), (1, 8191, 128), (20, 37, 5001), (3, 6000, 16),
+                                             (1, 64, 8193), (1, 8193, 33), (40, 128, 2600), (8, 2049, 90), (9, 2176, 128)])
+def test_long_thin_matrices(batch, rows, cols, dtype):
+    """Lengths around what a cluster of 8 and one of 16 blocks holds, more matrices than such clusters fit at once."""
+    g = gradient(rows, cols, rows * 31 + cols, batch=batch).to(TD[dtype])
+    got = ortho(g.cuda())
+    for i in sorted({0, batch // 2, batch - 1}):
+        x = g[i].double()
+        want = newton_schulz(x.t()).t() if rows > cols else newton_schulz(x)   # the shorter side's Gram matrix
+        assert rel(got[i], want) <= bound(rows, cols)
+    assert torch.equal(got, ortho(g.cuda()))
+
+
 @pytest.mark.parametrize("batch", [1, 5, 128])
 def test_batches_are_independent(batch):
     g = gradient(72, 104, batch, batch=batch).bfloat16().cuda()

@@ -24,7 +24,7 @@
 // is multiplied from the right, a wide one the other way around.
 //
 // Two kernels by size.  A shorter side of at most 128 (and a longer one of at
-// most 4096) stays on chip: k_ortho_small, one launch, 23 us for 96 x 160.
+// most 8192) stays on chip: k_ortho_small, one launch, 23 us for 96 x 160.
 // Anything else goes through global memory (in practice L2): two streams that
 // scale and pack G, then k_ortho_products, all products in one cooperative
 // launch.  Measured with five steps: 12 x 768 x 768 186 us, 6 x 1531 x 1003
@@ -571,14 +571,16 @@ __global__ void __launch_bounds__(kProductThreads) k_ortho_products(const __grid
 
 // ----------------------------------------------------- short sides up to 128
 // A matrix whose shorter side is at most 128 stays on the SM: one CTA holds up
-// to 512 of the longer side's values (256 while there are SMs for that), a
-// cluster of up to 8 CTAs the whole of it, and the square matrices are
-// computed by each CTA for itself.  Only X X^T is summed over the cluster,
-// through its shared memory.  The sixteen dependent products of five steps
-// take about a microsecond each this way; through global memory they took
-// five.
+// to 512 of the longer side's values (fewer while there are SMs for that), a
+// cluster of up to 8 CTAs the whole of it (16 for a longer side above 4096,
+// where global memory took 231 us for 100 x 8192, not 59; and above 2048 while
+// such clusters fit side by side: 128 x 4096 took 55 us in 8, 51 in 16), and
+// the square matrices are computed by each CTA for itself.  Only X X^T is
+// summed over the cluster, through its shared memory.  The sixteen dependent
+// products of five steps take about a microsecond each this way; through
+// global memory they took five.
 // Bound by that chain and by the copies in and out, on few SMs.  Five steps of
-// bf16: 96 x 160 23 us, 23 x 1519 33, 128 x 4096 55, 4096 x 128 56, 100
+// bf16: 96 x 160 23 us, 23 x 1519 33, 128 x 4096 51, 100 x 8192 59, 100
 // matrices of 48 x 300 31, 60 of 100 x 2000 97.
 //
 // X lies as the caller has it, in blocks of 64 columns whose rows are 128
@@ -589,7 +591,7 @@ __global__ void __launch_bounds__(kProductThreads) k_ortho_products(const __grid
 // All of it runs once a launch, mostly out of a cold instruction cache, so the
 // code is kept short: one copy of the products' code for all of them, and
 // loads that need no registers (cp.async).
-constexpr uint32_t kSide = 128, kSlabBlocks = 8, kMaxCtas = 8;
+constexpr uint32_t kSide = 128, kSlabBlocks = 8, kMaxCtas = 16, kPortableCtas = 8;
 constexpr uint32_t kBlockBytes = kSide * 128;   // half a square
 constexpr uint32_t kSquareBytes = 2 * kBlockBytes;
 constexpr uint32_t kSlabUnit = 64 * kSide * 2;  // bytes of X for 64 of the longer side
@@ -814,13 +816,17 @@ __global__ void __launch_bounds__(kSmallThreads) k_ortho_small(const __grid_cons
         for (uint32_t i = rank * kSmallThreads + tid; i < sums; i += p.ctas * kSmallThreads) {
             const uint32_t r = i / quads, c4 = i - r * quads;
             const uint32_t at = partial + r * 512 + ((c4 ^ (r & 7)) << 4);
-            float4 y[kMaxCtas], s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
+            for (uint32_t q0 = 0; q0 < p.ctas; q0 += 4) {
+                float4 y[4];
 #pragma unroll
-            for (uint32_t q = 0; q < kMaxCtas; ++q)   // all on their way before the first is added
-                y[q] = q < p.ctas ? ld_cluster(cluster_addr(at, q)) : s;
+                for (uint32_t q = 0; q < 4; ++q)   // all on their way before the first is added
+                    y[q] = q0 + q < p.ctas ? ld_cluster(cluster_addr(at, q0 + q)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-            for (uint32_t q = 0; q < kMaxCtas; ++q) {
-                s.x += y[q].x; s.y += y[q].y; s.z += y[q].z; s.w += y[q].w;
+                for (uint32_t q = 0; q < 4; ++q) {
+                    s.x += y[q].x; s.y += y[q].y; s.z += y[q].z; s.w += y[q].w;
+                }
             }
             const uint32_t lo = narrow2<kFp16>(s.x * f, s.y * f), hi = narrow2<kFp16>(s.z * f, s.w * f);
             const uint32_t to = sq0 + (c4 >> 4) * kBlockBytes + piece128(r, (c4 & 15) >> 1) + 8 * (c4 & 1);
@@ -1012,6 +1018,39 @@ cudaError_t pairs(int* out) {
     return cudaSuccess;
 }
 
+// Clusters of kMaxCtas CTAs of k_ortho_small that can be resident at once on the current device (none on one whose SMs
+// do not come in groups that large).
+template <int DT>
+cudaError_t large_clusters(size_t smem, int* out) {
+    static std::mutex mu;
+    static int known[64] = {};   // and one
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lock(mu);
+    if (!known[dev]) {
+        if ((e = cudaFuncSetAttribute(k_ortho_small<DT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
+            return e;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(kMaxCtas);
+        cfg.blockDim = dim3(kSmallThreads);
+        cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = kMaxCtas;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if ((e = cudaOccupancyMaxActiveClusters(&n, k_ortho_small<DT>, &cfg)) != cudaSuccess) return e;
+        known[dev] = n + 1;
+    }
+    *out = known[dev] - 1;
+    return cudaSuccess;
+}
+
 constexpr float kDefaultCoeffs[3] = {3.4445f, -4.7750f, 2.0315f};
 
 }  // namespace
@@ -1060,7 +1099,21 @@ int zero_orthogonalize(int dtype, int batch, uint64_t rows, uint64_t cols, const
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
 
     cudaError_t e;
+    constexpr size_t most_small = 1024 + 3 * kSquareBytes + kSlabBlocks * kSlabUnit;
+    uint32_t max_ctas = 0;   // of k_ortho_small for a matrix; none: too large for it
     if (side <= kSide && span <= kMaxCtas * kSlabBlocks * 64) {
+        const bool fp16 = dtype == ZERO_FP16;
+        if ((e = fp16 ? allow_smem<k_ortho_small<kFp16>>(most_small) : allow_smem<k_ortho_small<kBf16>>(most_small)) != cudaSuccess)
+            return cuda_refuse(e, "zero_orthogonalize");
+        max_ctas = span <= kPortableCtas * kSlabBlocks * 64 ? kPortableCtas : 0;
+        if (span > kPortableCtas * 4 * 64) {
+            int room = 0;
+            if ((e = fp16 ? large_clusters<kFp16>(most_small, &room) : large_clusters<kBf16>(most_small, &room)) != cudaSuccess)
+                return cuda_refuse(e, "zero_orthogonalize");
+            if (max_ctas == 0 ? room > 0 : nb <= static_cast<uint32_t>(room)) max_ctas = kMaxCtas;
+        }
+    }
+    if (max_ctas) {
         SmallArgs m = {};
         for (int i = 0; i < batch; ++i) {
             if (!src[i] || !aligned(src[i], 2)) return refuse(ZERO_EINVAL, "src[i] is NULL or not 2-byte aligned");
@@ -1073,11 +1126,15 @@ int zero_orthogonalize(int dtype, int batch, uint64_t rows, uint64_t cols, const
         m.side = static_cast<uint32_t>(side);
         m.span = static_cast<uint32_t>(span);
         const uint32_t blocks = (m.span + 63) / 64;
-        // 4 blocks a CTA (256 values) as long as there are SMs for that, else as many as fit
+        // One CTA where it holds all: it sums nothing over a cluster (128 x 512 35 us, in two CTAs 39; 128 x 320 29, 36;
+        // only a narrow side gains from more, 24 x 500 31 against 33).  Else 2 blocks of 64 a CTA on an empty GPU (2 x
+        // 609 x 39 32 us, with 4 37; 23 x 1519 31, 33), where clusters of that many find room side by side (16 x 64 x
+        // 1000 took 61 so, with 4 32); then 4 as long as there are SMs, else as many as fit (16 x 64 x 1000 38 with 8).
         int sms = 0;
         if ((e = sm_count(&sms)) != cudaSuccess) return cuda_refuse(e, "zero_orthogonalize");
-        m.ctas = (blocks + 3) / 4;
-        if (m.ctas > kMaxCtas) m.ctas = kMaxCtas;
+        const uint32_t halves = (blocks + 1) / 2 < max_ctas ? (blocks + 1) / 2 : max_ctas;
+        m.ctas = blocks <= kSlabBlocks ? 1 : 2 * halves * nb <= static_cast<uint32_t>(sms) ? halves : (blocks + 3) / 4;
+        if (m.ctas > max_ctas) m.ctas = max_ctas;
         while (m.ctas > 1 && m.ctas * nb > static_cast<uint32_t>(sms) && (m.ctas - 1) * kSlabBlocks >= blocks) --m.ctas;
         m.per = (blocks + m.ctas - 1) / m.ctas;
         if (tall) m.per += m.per & 1;            // 128 rows at a time
@@ -1087,15 +1144,9 @@ int zero_orthogonalize(int dtype, int batch, uint64_t rows, uint64_t cols, const
         m.scale = scale;
         for (int i = 0; i < 3 * steps; ++i) m.coeffs[i] = coeffs ? coeffs[i] : kDefaultCoeffs[i % 3];
         const size_t smem = 1024 + 3 * kSquareBytes + static_cast<size_t>(m.per) * kSlabUnit;
-        constexpr size_t most = 1024 + 3 * kSquareBytes + kSlabBlocks * kSlabUnit;
         const dim3 grid(m.ctas * nb);
-        if (dtype == ZERO_FP16) {
-            if ((e = allow_smem<k_ortho_small<kFp16>>(most)) == cudaSuccess)
-                e = launch_pdl(k_ortho_small<kFp16>, grid, kSmallThreads, smem, m.ctas, s, m);
-        } else {
-            if ((e = allow_smem<k_ortho_small<kBf16>>(most)) == cudaSuccess)
-                e = launch_pdl(k_ortho_small<kBf16>, grid, kSmallThreads, smem, m.ctas, s, m);
-        }
+        e = dtype == ZERO_FP16 ? launch_pdl(k_ortho_small<kFp16>, grid, kSmallThreads, smem, m.ctas, s, m)
+                               : launch_pdl(k_ortho_small<kBf16>, grid, kSmallThreads, smem, m.ctas, s, m);
         return e == cudaSuccess ? ZERO_OK : cuda_refuse(e, "zero_orthogonalize");
     }
 
@@ -1227,7 +1278,10 @@ int zero_orthogonalize(int dtype, int batch, uint64_t rows, uint64_t cols, const
     if ((e = allow_smem<k_ortho_products>(kProductSmem)) != cudaSuccess || (e = pairs(&resident)) != cudaSuccess)
         return cuda_refuse(e, "zero_orthogonalize");
     const uint64_t tiles = static_cast<uint64_t>(most) * nb;
-    const unsigned grid = 2u * static_cast<unsigned>(tiles < static_cast<uint64_t>(resident) ? tiles : resident);
+    // Every pair, also where no phase has a tile for each: consecutive phases then run on different pairs, and a tile
+    // finds its pair at rest (9 x 303 x 374: 133 us against 141 with a pair a tile, 3 x 477 x 650: 149 against 159).
+    // A single tile stays where it is (235 x 142: 101.5 against 104.9).
+    const unsigned grid = 2u * static_cast<unsigned>(tiles > 1 ? resident : 1);
     e = launch_together(k_ortho_products, dim3(grid), kProductThreads, kProductSmem, 2, s, p);
     if (e != cudaSuccess) return cuda_refuse(e, "products");
     return ZERO_OK;
