@@ -70,6 +70,24 @@ def test_long_thin_matrices(batch, rows, cols, dtype):
     assert torch.equal(got, ortho(g.cuda()))
 
 
+@pytest.mark.parametrize("rows,cols", [(90, 1537), (1537, 90), (33, 512), (511, 128), (5001, 24), (24, 8190), (7, 3)])
+@pytest.mark.parametrize("offset,pad", [(0, 1), (1, 0), (3, 5), (5, 8), (7, 2), (8, 8)])
+def test_thin_matrices_at_any_alignment(rows, cols, offset, pad):
+    """The result does not depend on where rows start, and nothing beside them is written."""
+    ld = cols + pad
+    g = gradient(rows, cols, rows + 7 * cols).to(torch.bfloat16).cuda()
+    want = ortho(g)[0]
+    src = torch.full((offset + rows * ld + 64,), float("nan"), dtype=torch.bfloat16, device="cuda")
+    dst = torch.full((offset + rows * ld + 64,), 7.0, dtype=torch.bfloat16, device="cuda")
+    view = (rows, cols), (ld, 1), offset
+    src.as_strided(*view).copy_(g[0])
+    Z.zero_orthogonalize(Z.ZERO_BF16, rows, cols, [src[offset:]], [dst[offset:]], workspace(1, rows, cols), ld_src=ld,
+                         ld_dst=ld)
+    assert torch.equal(dst.as_strided(*view), want)
+    dst.as_strided(*view).fill_(7.0)
+    assert bool((dst == 7.0).all())
+
+
 @pytest.mark.parametrize("batch", [1, 5, 128])
 def test_batches_are_independent(batch):
     g = gradient(72, 104, batch, batch=batch).bfloat16().cuda()

@@ -580,8 +580,8 @@ __global__ void __launch_bounds__(kProductThreads) k_ortho_products(const __grid
 // products of five steps take about a microsecond each this way; through
 // global memory they took five.
 // Bound by that chain and by the copies in and out, on few SMs.  Five steps of
-// bf16: 96 x 160 23 us, 23 x 1519 33, 128 x 4096 51, 100 x 8192 59, 100
-// matrices of 48 x 300 31, 60 of 100 x 2000 97.
+// bf16: 96 x 160 23 us, 23 x 1519 30, 128 x 4096 51, 100 x 8192 59, 100
+// matrices of 48 x 300 27, 60 of 100 x 2000 97.
 //
 // X lies as the caller has it, in blocks of 64 columns whose rows are 128
 // bytes.  That one layout serves both products: of a wide matrix the blocks
@@ -617,9 +617,6 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
 }
 __device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t x, uint32_t y) {
     asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(x), "r"(y) : "memory");
-}
-__device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t x) {
-    asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr), "h"(static_cast<uint16_t>(x)) : "memory");
 }
 // 16 bytes into shared memory, the last 16 - `bytes` of them zeros.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {
@@ -669,7 +666,7 @@ __global__ void __launch_bounds__(kSmallThreads) k_ortho_small(const __grid_cons
     auto place = [&](uint32_t r, uint32_t c) {
         return x + (c >> 6) * block_bytes + piece128(r, (c & 63) >> 3) + 2 * (c & 7);
     };
-    const uint32_t eights = (cols + 7) / 8, strips = (cols + 31) / 32;
+    const uint32_t eights = (cols + 7) / 8;
     {
         const unsigned short* src = static_cast<const unsigned short*>(p.src[b]) + (tall ? first * p.ld_src : first);
         if ((reinterpret_cast<uintptr_t>(src) & 15) == 0 && p.ld_src % 8 == 0) {
@@ -679,19 +676,24 @@ __global__ void __launch_bounds__(kSmallThreads) k_ortho_small(const __grid_cons
                 copy16(place(r, c), src + r * p.ld_src + c, 2 * min(8u, cols - c));
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
-        } else {   // value by value, a warp's 32 next to one another
+        } else {   // the aligned pieces that cover 8 values, for two eights at a time (3 x 7777 x 113: 83 us, by value 90)
+            const unsigned short* from = static_cast<const unsigned short*>(p.src[b]);
+            const int64_t total = static_cast<int64_t>(((tall ? p.span : p.side) - 1) * p.ld_src + (tall ? p.side : p.span));
+            const uint64_t start = tall ? first * p.ld_src : first;
 #pragma unroll 1
-            for (uint32_t i0 = warp; i0 < rows * strips; i0 += 8 * (kSmallThreads / 32)) {
-                uint32_t v[8];   // on their way together
+            for (uint32_t i0 = tid; i0 < rows * eights; i0 += 2 * kSmallThreads) {
+                uint32_t w[2][4];
 #pragma unroll
-                for (uint32_t k = 0; k < 8; ++k) {
-                    const uint32_t i = i0 + k * (kSmallThreads / 32), r = i / strips, c = (i - r * strips) * 32 + lane;
-                    v[k] = r < rows && c < cols ? __ldg(src + r * p.ld_src + c) : 0u;
+                for (uint32_t k = 0; k < 2; ++k) {
+                    const uint32_t i = i0 + k * kSmallThreads, r = i / eights, c = (i - r * eights) * 8;
+                    if (r < rows) load8(from, static_cast<int64_t>(start + r * p.ld_src + c), total, w[k]);
                 }
 #pragma unroll
-                for (uint32_t k = 0; k < 8; ++k) {
-                    const uint32_t i = i0 + k * (kSmallThreads / 32), r = i / strips, c = (i - r * strips) * 32 + lane;
-                    if (r < rows && c < cols) st_shared16(place(r, c), v[k]);
+                for (uint32_t k = 0; k < 2; ++k) {
+                    const uint32_t i = i0 + k * kSmallThreads, r = i / eights, c = (i - r * eights) * 8;
+                    if (r >= rows) continue;
+                    clear_from(w[k], static_cast<int>(cols - c));
+                    st_shared(place(r, c), w[k][0], w[k][1], w[k][2], w[k][3]);
                 }
             }
         }
@@ -936,11 +938,29 @@ __global__ void __launch_bounds__(kSmallThreads) k_ortho_small(const __grid_cons
                         if (c + e < cols) out[e] = static_cast<unsigned short>(w[e >> 1] >> (16 * (e & 1)));
                 }
             }
-        } else {
-#pragma unroll 4
-            for (uint32_t i = warp; i < rows * strips; i += kSmallThreads / 32) {
-                const uint32_t r = i / strips, c = (i - r * strips) * 32 + lane;
-                if (c < cols) dst[r * p.ld_dst + c] = ld_shared16(place(r, c));
+        } else {   // aligned pieces of a row, of which the first and the last may be cut (73 us, by value 83)
+            const uint32_t pieces = (cols + 14) / 8;
+#pragma unroll 1
+            for (uint32_t i = tid; i < rows * pieces; i += kSmallThreads) {
+                const uint32_t r = i / pieces;
+                unsigned short* row_out = dst + r * p.ld_dst;
+                const uint32_t m = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row_out) >> 1) & 7u;
+                const int c = static_cast<int>((i - r * pieces) * 8 - m);   // the piece's first column
+                if (c >= static_cast<int>(cols)) continue;
+                // the two eights that it lies in; the second only as far as the row goes
+                const uint4 hi = ld_shared(place(r, min(static_cast<uint32_t>(c + 7), cols - 1) & ~7u));
+                const uint4 lo = c < 0 ? hi : ld_shared(place(r, static_cast<uint32_t>(c) & ~7u));
+                const uint32_t lw[4] = {lo.x, lo.y, lo.z, lo.w}, hw[4] = {hi.x, hi.y, hi.z, hi.w};
+                uint32_t w[4];
+                shift_halves(lw, hw, (8 - m) & 7, w);
+                if (c >= 0 && c + 8 <= static_cast<int>(cols)) {
+                    *reinterpret_cast<uint4*>(row_out + c) = make_uint4(w[0], w[1], w[2], w[3]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (c + e >= 0 && c + e < static_cast<int>(cols))
+                            row_out[c + e] = static_cast<unsigned short>(w[e >> 1] >> (16 * (e & 1)));
+                }
             }
         }
     }
@@ -1127,8 +1147,8 @@ int zero_orthogonalize(int dtype, int batch, uint64_t rows, uint64_t cols, const
         m.span = static_cast<uint32_t>(span);
         const uint32_t blocks = (m.span + 63) / 64;
         // One CTA where it holds all: it sums nothing over a cluster (128 x 512 35 us, in two CTAs 39; 128 x 320 29, 36;
-        // only a narrow side gains from more, 24 x 500 31 against 33).  Else 2 blocks of 64 a CTA on an empty GPU (2 x
-        // 609 x 39 32 us, with 4 37; 23 x 1519 31, 33), where clusters of that many find room side by side (16 x 64 x
+        // only a narrow side gains from more, 24 x 500 by 2 us).  Else 2 blocks of 64 a CTA on an empty GPU (2 x
+        // 609 x 39 32 us, with 4 37; 23 x 1519 by 2 us), where clusters of that many find room side by side (16 x 64 x
         // 1000 took 61 so, with 4 32); then 4 as long as there are SMs, else as many as fit (16 x 64 x 1000 38 with 8).
         int sms = 0;
         if ((e = sm_count(&sms)) != cudaSuccess) return cuda_refuse(e, "zero_orthogonalize");
