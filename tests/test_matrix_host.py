@@ -27,6 +27,14 @@ def test_sizes(Z):
     assert Z.zero_orthogonalize_workspace_bytes(0, 4, 4) == 0 and Z.zero_orthogonalize_workspace_bytes(1, 0, 4) == 0
 
 
+@pytest.mark.parametrize("rows,cols", [(20, 30), (30, 9000), (300, 200)])
+@pytest.mark.parametrize("src,dst", [(None, 256), (257, 256), (256, None), (256, 3)])
+def test_matrices_are_checked_before_any_cuda_call(Z, rows, cols, src, dst):
+    with pytest.raises(Z.ZeroError) as e:
+        Z.zero_orthogonalize(1, rows, cols, [256, src], [256, dst], None, stream=0)
+    assert e.value.code == 1 and "2-byte aligned" in str(e.value)
+
+
 def test_refusals_come_before_any_cuda_call(Z):
     for call in (lambda: Z.zero_orthogonalize(7, 4, 4, [], [], None, stream=0),
                  lambda: Z.zero_orthogonalize(0, 4, 4, [16], [16], None, steps=0, stream=0),

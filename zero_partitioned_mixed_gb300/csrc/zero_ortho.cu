@@ -1106,6 +1106,10 @@ int zero_orthogonalize(int dtype, int batch, uint64_t rows, uint64_t cols, const
     if (ld_src < cols || ld_dst < cols) return refuse(ZERO_EINVAL, "ld_src and ld_dst must be at least cols");
     if (ld_src > (1ull << 40) || ld_dst > (1ull << 40)) return refuse(ZERO_EINVAL, "ld_src or ld_dst too large");
     if (!src || !dst) return refuse(ZERO_EINVAL, "src or dst is NULL");
+    for (int i = 0; i < batch; ++i) {
+        if (!src[i] || !aligned(src[i], 2)) return refuse(ZERO_EINVAL, "src[i] is NULL or not 2-byte aligned");
+        if (!dst[i] || !aligned(dst[i], 2)) return refuse(ZERO_EINVAL, "dst[i] is NULL or not 2-byte aligned");
+    }
     const Scratch z = scratch_of(static_cast<uint64_t>(batch), rows, cols);
     if (!workspace || !aligned(workspace, 256)) return refuse(ZERO_EINVAL, "workspace is NULL or not 256-byte aligned");
     if (workspace_bytes < z.bytes)
@@ -1136,8 +1140,6 @@ int zero_orthogonalize(int dtype, int batch, uint64_t rows, uint64_t cols, const
     if (max_ctas) {
         SmallArgs m = {};
         for (int i = 0; i < batch; ++i) {
-            if (!src[i] || !aligned(src[i], 2)) return refuse(ZERO_EINVAL, "src[i] is NULL or not 2-byte aligned");
-            if (!dst[i] || !aligned(dst[i], 2)) return refuse(ZERO_EINVAL, "dst[i] is NULL or not 2-byte aligned");
             m.src[i] = src[i];
             m.dst[i] = dst[i];
         }
@@ -1175,8 +1177,6 @@ int zero_orthogonalize(int dtype, int batch, uint64_t rows, uint64_t cols, const
     std::memset(&p, 0, sizeof(p));
     p.dst_vec = ld_dst % 8 == 0;
     for (int i = 0; i < batch; ++i) {
-        if (!src[i] || !aligned(src[i], 2)) return refuse(ZERO_EINVAL, "src[i] is NULL or not 2-byte aligned");
-        if (!dst[i] || !aligned(dst[i], 2)) return refuse(ZERO_EINVAL, "dst[i] is NULL or not 2-byte aligned");
         q.src[i] = src[i];
         p.dst[i] = dst[i];
         p.dst_vec &= aligned(dst[i], 16);
