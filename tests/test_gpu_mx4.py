@@ -279,3 +279,18 @@ def test_refusals():
     with pytest.raises(Z.ZeroError):
         Mx4Matrix.of(h.view(64, 64).t())
     torch.cuda.synchronize()
+
+
+def test_rows_that_share_memory_are_refused():
+    # the gradient of y.sum(0) among them: one row for all, so its storage is shorter than its shape
+    dy, x, w = torch.zeros(64).bfloat16().cuda().expand(100, 64), matrix(100, 96, "bf16", 1).cuda(), matrix(64, 96, "bf16", 2).cuda()
+    q, w_t = Mx4Matrix.of(x), Mx4Matrix.of(w, transpose=True)
+    one = torch.zeros(64, dtype=torch.bfloat16, device="cuda")
+    for call in (lambda: Mx4Matrix.of(dy), lambda: Mx4Matrix.of(dy, transpose=True), lambda: mx4_linear_backward(dy, x, w_t),
+                 lambda: mx4_product(q, Mx4Matrix.of(w), out=one.expand(100, 64))):
+        with pytest.raises(Z.ZeroError) as e:
+            call()
+        assert e.value.code == 1 and "contiguous rows" in str(e.value)
+    dx, dw = mx4_linear_backward(dy.contiguous(), x, w_t)
+    assert dx.shape == x.shape and dw.shape == w.shape
+    torch.cuda.synchronize()

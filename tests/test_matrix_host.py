@@ -74,3 +74,23 @@ def test_mx4_reference_by_hand():
     assert mx4_pack(codes)[0, :3].tolist() == [7 | 14 << 4, 6 | 4 << 4, 0 | 10 << 4]
     t = mx4_tile(np.arange(1, 131, dtype=np.uint8)[:, None])
     assert t.size == 1024 and t[0] == 1 and t[16] == 2 and t[4] == 33 and t[512] == 129
+
+
+@pytest.mark.parametrize("t", [torch.zeros(64).expand(100, 64), torch.zeros(100, 1).expand(100, 64),
+                               torch.zeros(200).as_strided((100, 64), (1, 1)), torch.zeros(1).expand(7, 1)],
+                         ids=["one row for all", "one column for all", "overlapping rows", "one value for all"])
+def test_rows_that_share_memory_are_refused(Z, t):
+    # a row stride below the width: the rows do not lie one after the other, as the calls read and write them
+    from zero_partitioned_mixed_gb300 import mx4
+    with pytest.raises(Z.ZeroError) as e:
+        mx4._rows(t)
+    assert e.value.code == 1 and "contiguous rows" in str(e.value)
+
+
+def test_leading_dimensions_of_ordinary_tensors(Z):
+    from zero_partitioned_mixed_gb300 import mx4
+    room = torch.zeros(4096)
+    for shape, stride, ld in (((5, 7), (7, 1), 7), ((5, 7), (9, 1), 9), ((1, 7), (0, 1), 7), ((1, 7), (3, 1), 7),
+                              ((5, 1), (1, 1), 1), ((5, 1), (4, 3), 4), ((0, 7), (0, 1), 7), ((5, 0), (0, 1), 0),
+                              ((5, 0), (1, 1), 1)):
+        assert mx4._rows(room.as_strided(shape, stride)) == ld, (shape, stride)

@@ -24,10 +24,12 @@ def _dtype(t: torch.Tensor) -> int:
 
 
 def _rows(t: torch.Tensor) -> int:
-    """The leading dimension of a 2-D tensor whose rows are contiguous."""
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise B.ZeroError(1, "expected a 2-D tensor with contiguous rows")
-    return max(t.stride(0), t.shape[1]) if t.shape[0] > 1 else t.shape[1]
+    """The leading dimension of a 2-D tensor whose rows are contiguous and do not
+    share memory (an expanded tensor's do: make it contiguous first)."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+        raise B.ZeroError(1, f"expected a 2-D tensor with contiguous rows, got the shape {tuple(t.shape)} "
+                             f"with the strides {t.stride()}")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
 class Mx4Matrix:
