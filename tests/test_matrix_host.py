@@ -94,3 +94,14 @@ def test_leading_dimensions_of_ordinary_tensors(Z):
                               ((5, 1), (1, 1), 1), ((5, 1), (4, 3), 4), ((0, 7), (0, 1), 7), ((5, 0), (0, 1), 0),
                               ((5, 0), (1, 1), 1)):
         assert mx4._rows(room.as_strided(shape, stride)) == ld, (shape, stride)
+
+
+def test_tensors_in_host_memory_are_refused(Z):
+    from zero_partitioned_mixed_gb300 import mx4
+    x, m = torch.zeros(4, 32, dtype=torch.bfloat16), mx4.Mx4Matrix(4, 32, device="cpu")
+    for call in (lambda: mx4.Mx4Matrix.of(x), lambda: mx4.Mx4Matrix.of(x, transpose=True), lambda: m.fill(x), m.values,
+                 lambda: mx4.mx4_product(m, m), lambda: mx4.mx4_product(m, m, out=torch.zeros(4, 4, dtype=torch.bfloat16)),
+                 lambda: mx4.mx4_linear(x, m), lambda: mx4.mx4_linear_backward(x, x, m)):
+        with pytest.raises(Z.ZeroError) as e:
+            call()
+        assert e.value.code == 1 and "GPU" in str(e.value)

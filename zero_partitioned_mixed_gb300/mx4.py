@@ -23,6 +23,12 @@ def _dtype(t: torch.Tensor) -> int:
     return _ZDT[t.dtype]
 
 
+def _same_gpu(*tensors: torch.Tensor) -> None:
+    for t in tensors:
+        if not t.is_cuda or t.device != tensors[0].device:
+            raise B.ZeroError(1, f"expected tensors on one GPU, got {[str(x.device) for x in tensors]}")
+
+
 def _rows(t: torch.Tensor) -> int:
     """The leading dimension of a 2-D tensor whose rows are contiguous and do not
     share memory (an expanded tensor's do: make it contiguous first)."""
@@ -50,10 +56,12 @@ class Mx4Matrix:
         r, c = src.shape
         if ((c, r) if transpose else (r, c)) != (self.rows, self.cols):
             raise B.ZeroError(1, f"expected a matrix for {self.rows} x {self.cols}, got {tuple(src.shape)}")
+        _same_gpu(src, self.codes, self.scales)
         B.zero_mx4_quantize(_dtype(src), r, c, src, self.codes, self.scales, ld=_rows(src), transpose=transpose)
         return self
 
     def values(self, dtype=torch.bfloat16) -> torch.Tensor:
+        _same_gpu(self.codes, self.scales)
         out = torch.empty((self.rows, self.cols), dtype=dtype, device=self.codes.device)
         B.zero_mx4_dequantize(_dtype(out), self.rows, self.cols, self.codes, self.scales, out)
         return out
@@ -67,6 +75,7 @@ def mx4_product(a: Mx4Matrix, b: Mx4Matrix, dtype=torch.bfloat16, out: Optional[
         out = torch.empty((a.rows, b.rows), dtype=dtype, device=a.codes.device)
     elif tuple(out.shape) != (a.rows, b.rows):
         raise B.ZeroError(1, f"out must be {a.rows} x {b.rows}")
+    _same_gpu(out, a.codes, a.scales, b.codes, b.scales)
     B.zero_mx4_matmul(_dtype(out), a.rows, b.rows, a.cols, a.codes, a.scales, b.codes, b.scales, out, ld=_rows(out))
     return out
 
