@@ -55,3 +55,22 @@ def test_tensor_memory_is_allocated_before_the_next_kernel_may_start():
                 assert alloc.start() < enter, f"{name}: {m.group(1)}"
                 assert "__syncthreads();" in body[alloc.start():enter], f"{name}: {m.group(1)}"
     assert found >= 3
+
+
+def test_no_block_with_tensor_memory_waits_for_blocks_that_may_wait_for_it():
+    # Two clusters of different streams on the same two SMs: each has allocated on one of them and its second block
+    # waits there behind the other's first.  Neither ends if a block keeps its tensor memory while it waits for its
+    # cluster.  So a kernel frees it before it waits, or asks for so much shared memory that no other block with
+    # tensor memory fits beside its own (the sizes are compared by static_assert).
+    src = _sources()
+    waiting = set()
+    for name, t in src.items():
+        for m in re.finditer(r"__global__ void[^{;]*?\b(k_\w+)\([^{;]*\)\s*\{(.*?)\n\}\n", t, re.S):
+            body = m.group(2)
+            alloc, free = (re.search(rf"\btmem_{w}(?:_pair)?\(", body) for w in ("alloc", "free"))
+            if alloc and any(alloc.start() < s.start() < free.start() for s in re.finditer(r"\bcluster_sync\(\)", body)):
+                waiting.add(m.group(1))
+    assert waiting == {"k_ortho_small", "k_ortho_products"}
+    assert re.search(r"if \(m\.ctas > 1 && smem < kAloneSmem\) smem = kAloneSmem;", src["zero_ortho.cu"])
+    assert "static_assert(kProductSmem >= kAloneSmem" in src["zero_ortho.cu"]
+    assert len(re.findall(r"static_assert\([^;]*>= kLeastTmemSmem", src["zero_mx4.cu"])) == 2

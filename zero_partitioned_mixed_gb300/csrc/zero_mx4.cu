@@ -342,6 +342,7 @@ struct MxTile {
     static constexpr uint32_t kSet = 8 * MT + 16;     // columns of a set: 4 for 128 rows and 128 values of k
     static constexpr size_t kSmem = 1024 + kStages * kStage + kMxOutWarps * 2 * kMxOut;
     static_assert(2 * kMxN + 4 * kSet <= 512, "tensor memory");
+    static_assert(kSmem >= kLeastTmemSmem, "see tmem_alloc");
 };
 
 // A scale tile (32 lines of 16 bytes in shared memory) into 4 columns of
@@ -558,6 +559,7 @@ struct Narrow {
     static constexpr size_t kSmem = 1024 + kNarrowStages * kStage;
     static constexpr uint32_t kTmem = 128;   // the accumulator and four sets of scales
     static_assert(NT + 4 * 16 <= kTmem, "tensor memory");
+    static_assert(kSmem >= kLeastTmemSmem, "see tmem_alloc");
     static_assert(kNarrowStages * kStage >= NT * 512, "the partial sums take the ring's place");
 };
 
@@ -656,11 +658,11 @@ k_mx4_narrow(const __grid_constant__ CUtensorMap map_b, const __grid_constant__ 
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (p.split > 1) cluster_sync();
-    if (warp == 1) {
+    if (warp == 1) {   // before the wait for the cluster: see tmem_alloc
         tc_fence_after();
         tmem_free(tmem, L::kTmem);
     }
+    if (p.split > 1) cluster_sync();
     // this CTA's share of the rows, four at a time, for all columns
     const uint32_t rows = 128 / p.split, fours = rows / 4;   // split is a power of two, at most 8
     const uint32_t first = tile * 128 + rank * rows;
@@ -691,7 +693,6 @@ k_mx4_narrow(const __grid_constant__ CUtensorMap map_b, const __grid_constant__ 
 
 // -------------------------------------------------------------------- host
 constexpr uint64_t kMaxSide = 1ull << 30;
-constexpr size_t kSmemPerSm = 228 * 1024;   // each CTA takes 1 KiB more than it asks for
 
 uint64_t mx_pitch(uint64_t cols) { return up(cols, kMxBlock) / 2; }
 

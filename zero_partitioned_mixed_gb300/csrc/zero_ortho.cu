@@ -275,6 +275,7 @@ constexpr uint32_t kOperandBytes = kHalf * kBlockK * 2, kStageBytes = 2 * kOpera
 // A warp's output buffers: 32 x 32 values twice, and twice their mirror image.
 constexpr uint32_t kOutBytes = 32 * 32 * 2, kWarpBytes = 4 * kOutBytes;
 constexpr size_t kProductSmem = 1024 + kStages * kStageBytes + kOutWarps * kWarpBytes;
+static_assert(kProductSmem >= kAloneSmem, "see tmem_alloc");
 constexpr uint32_t kDonePerTile = 2 * kOutWarps;   // the warps of 2 CTAs
 
 // The tiles of one CTA pair, in order.
@@ -1124,6 +1125,7 @@ int zero_orthogonalize(int dtype, int batch, uint64_t rows, uint64_t cols, const
 
     cudaError_t e;
     constexpr size_t most_small = 1024 + 3 * kSquareBytes + kSlabBlocks * kSlabUnit;
+    static_assert(most_small >= kAloneSmem, "the limit that is set covers every launch");
     uint32_t max_ctas = 0;   // of k_ortho_small for a matrix; none: too large for it
     if (side <= kSide && span <= kMaxCtas * kSlabBlocks * 64) {
         const bool fp16 = dtype == ZERO_FP16;
@@ -1165,7 +1167,8 @@ int zero_orthogonalize(int dtype, int batch, uint64_t rows, uint64_t cols, const
         m.steps = steps;
         m.scale = scale;
         for (int i = 0; i < 3 * steps; ++i) m.coeffs[i] = coeffs ? coeffs[i] : kDefaultCoeffs[i % 3];
-        const size_t smem = 1024 + 3 * kSquareBytes + static_cast<size_t>(m.per) * kSlabUnit;
+        size_t smem = 1024 + 3 * kSquareBytes + static_cast<size_t>(m.per) * kSlabUnit;
+        if (m.ctas > 1 && smem < kAloneSmem) smem = kAloneSmem;   // its blocks wait for one another: see tmem_alloc
         const dim3 grid(m.ctas * nb);
         e = dtype == ZERO_FP16 ? launch_pdl(k_ortho_small<kFp16>, grid, kSmallThreads, smem, m.ctas, s, m)
                                : launch_pdl(k_ortho_small<kBf16>, grid, kSmallThreads, smem, m.ctas, s, m);

@@ -252,6 +252,19 @@ __device__ __forceinline__ void count_done(uint32_t* counter) {
 // barrier in between: the next kernel's blocks come only after every block of
 // this one has passed pdl_enter(), so they cannot hold tensor memory that a
 // block of this kernel still waits for while they themselves wait for it.
+//
+// That orders the kernels of one stream.  Between streams: an allocation has
+// no time limit, nor has a cluster's barrier, so a block must not keep its
+// tensor memory while it waits for another block, unless nothing that also
+// allocates can be on its SM.  With two clusters of different kernels on the
+// same two SMs, each could hold one and wait for the other, for ever.
+// k_mx4_narrow frees before it waits for its cluster; the clusters of
+// zero_ortho.cu ask for kAloneSmem of shared memory or more, which leaves no
+// room on an SM for a block with kLeastTmemSmem, the least that a kernel here
+// with tensor memory asks for.
+constexpr size_t kSmemPerSm = 228 * 1024;   // each block takes 1 KiB more than it asks for
+constexpr size_t kLeastTmemSmem = 60 * 1024, kAloneSmem = 168 * 1024;
+static_assert(kAloneSmem + kLeastTmemSmem + 2 * 1024 > kSmemPerSm, "a block beside one of kAloneSmem");
 __device__ __forceinline__ void tmem_alloc(uint32_t smem_slot, uint32_t cols) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_slot), "r"(cols)
                  : "memory");
