@@ -74,3 +74,21 @@ def test_no_block_with_tensor_memory_waits_for_blocks_that_may_wait_for_it():
     assert re.search(r"if \(m\.ctas > 1 && smem < kAloneSmem\) smem = kAloneSmem;", src["zero_ortho.cu"])
     assert "static_assert(kProductSmem >= kAloneSmem" in src["zero_ortho.cu"]
     assert len(re.findall(r"static_assert\([^;]*>= kLeastTmemSmem", src["zero_mx4.cu"])) == 2
+
+
+def test_a_block_asks_whether_a_wait_gave_up_after_its_barrier():
+    # asked before it, the answer may come too early: another warp's wait can give up later, and the block would leave
+    # (and free its tensor memory) with copies or products in flight
+    found = 0
+    for name, t in _sources().items():
+        for m in re.finditer(r"__global__ void[^{;]*?\b(k_\w+)\([^{;]*\)\s*\{(.*?)\n\}\n", t, re.S):
+            body = m.group(2)
+            if "s_quit" not in body:
+                continue
+            found += 1
+            free = re.search(r"\btmem_free(?:_pair)?\(", body).start()
+            settle = body.rfind("settle(quit);", 0, free)
+            barrier = body.rfind("__syncthreads();", 0, settle)
+            assert 0 <= barrier < settle, f"{name}: {m.group(1)}"
+            assert "bar_wait(" not in body[barrier:settle] and "finish()" not in body[barrier:settle], f"{name}: {m.group(1)}"
+    assert found == 4

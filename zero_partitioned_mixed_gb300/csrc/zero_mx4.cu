@@ -530,6 +530,7 @@ k_mx4_product(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
     __syncwarp();
     tc_fence_before();
     __syncthreads();
+    settle(quit);
     if (warp == 1) {
         tc_fence_after();
         tmem_free(tmem, 512);
@@ -651,13 +652,9 @@ k_mx4_narrow(const __grid_constant__ CUtensorMap map_b, const __grid_constant__ 
         }
     }
     __syncwarp();
-    if (*quit && threadIdx.x == 0) {   // copies in flight land within microseconds: leave them a millisecond
-        const uint64_t t0 = now_ns();
-        while (now_ns() - t0 < 1000000ull) {}
-    }
-    __syncwarp();
     tc_fence_before();
     __syncthreads();
+    settle(quit);
     if (warp == 1) {   // before the wait for the cluster: see tmem_alloc
         tc_fence_after();
         tmem_free(tmem, L::kTmem);

@@ -554,13 +554,9 @@ __global__ void __launch_bounds__(kProductThreads) k_ortho_products(const __grid
         if (lane == 0) store_wait<0>();
     }
     __syncwarp();
-    if (*quit && threadIdx.x == 0) {   // copies in flight land within microseconds: leave them a millisecond
-        const uint64_t t0 = now_ns();
-        while (now_ns() - t0 < 1000000ull) {}
-    }
-    __syncwarp();
     tc_fence_before();
     __syncthreads();
+    settle(quit);
     cluster_sync();
     if (warp == 1) {
         tc_fence_after();
@@ -965,12 +961,9 @@ __global__ void __launch_bounds__(kSmallThreads) k_ortho_small(const __grid_cons
             }
         }
     }
-    if (*quit && tid == 0) {   // a wait gave up: products may still be running
-        const uint64_t t0 = now_ns();
-        while (now_ns() - t0 < 1000000ull) {}
-    }
     tc_fence_before();
     __syncthreads();
+    settle(quit);
     if (p.ctas > 1) cluster_sync();   // nobody reads this CTA's shared memory any more
     if (warp == 0) {
         tc_fence_after();

@@ -160,6 +160,16 @@ __device__ __forceinline__ void bar_drain(uint32_t bar, uint32_t parity) {
     const uint64_t t0 = now_ns();
     while (!bar_test(bar, parity) && now_ns() - t0 < kGiveUpNs) {}
 }
+// In every thread, after a barrier of the block behind which nobody waits any
+// more: when a wait gave up, copies and products may still be in flight.  They
+// land within microseconds and are left a millisecond, before the block frees
+// its tensor memory or leaves.
+__device__ __forceinline__ void settle(volatile int* quit) {
+    if (!*quit) return;
+    const uint64_t t0 = now_ns();
+    while (now_ns() - t0 < 1000000ull) {}
+    __syncwarp();
+}
 
 // ------------------------------------------------------------------ copies
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
