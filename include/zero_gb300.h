@@ -450,7 +450,7 @@ ZERO_API int zero_step_noalloc(uint64_t psi, int n_ranks, int stage, int dtype, 
  * A step over matrices that lie back to back in flat buffers of `count`
  * elements is three calls on one stream:
  *   1. zero_muon_momentum   gradients of all ranks -> momentum, update
- *   2. zero_orthogonalize   once for each shape among the matrices
+ *   2. zero_muon_orthogonalize  once for each shape among the matrices
  *   3. zero_muon_apply      orthogonalised update -> master, all replicas
  * They take no handle, allocate nothing, can be captured into a CUDA graph
  * (after one call of each outside a capture, which loads the kernels) and
@@ -462,16 +462,21 @@ typedef struct {
     int32_t nesterov;      /* 1: update = g + momentum * m', 0: m' */
 } zero_muon_hyper_t;
 
-/* DEVICE memory of the caller's, 8-byte aligned; set by zero_muon_set_state. */
+/* DEVICE memory of the caller's, 8-byte aligned; set by zero_muon_set_state.
+ * `pending` holds the reasons to skip the step that is under way: */
+#define ZERO_MUON_NONFINITE 1   /* zero_muon_momentum saw a non-finite averaged gradient */
+#define ZERO_MUON_GAVE_UP 2     /* a bounded wait inside zero_muon_orthogonalize gave up */
 typedef struct {
     float loss_scale;      /* halved (floor 1.0) after a step whose gradients overflowed */
     int32_t slot;          /* live slot (0/1) of the momentum */
-    int32_t pending;       /* zero_muon_momentum saw a non-finite averaged gradient */
+    int32_t pending;       /* ZERO_MUON_* bits */
     int32_t overflow;      /* last finished step was skipped */
     int32_t applied;       /* last finished step updated the state */
     uint32_t ticket;       /* 0 between calls */
     int64_t steps_applied, steps_skipped;
-    int64_t reserved[3];
+    int32_t aborted;       /* last finished step was skipped for ZERO_MUON_GAVE_UP */
+    int32_t reserved0;
+    int64_t reserved[2];
 } zero_muon_state_t;
 
 /* Set the state: before the first step, or to resume.  Stream-ordered.  The
@@ -503,9 +508,10 @@ ZERO_API int zero_muon_momentum(int dtype, int n_ranks, uint64_t count, const vo
 /*
  * zero_muon_apply -- master = (1 - lr * weight_decay) * master - lr * ortho,
  * every replica = the 16-bit rounding of it; then the step is finished in
- * the state (the momentum's new slot becomes live).  After an overflow
- * master and replicas keep their values, the loss scale halves and the
- * momentum's live slot stays.
+ * the state (the momentum's new slot becomes live).  When `pending` holds a
+ * reason to skip it, master and replicas keep their values and the
+ * momentum's live slot stays; the loss scale halves for a non-finite
+ * gradient and is kept for a wait that gave up, which sets `aborted`.
  *   dtype   zero_dtype_t of the replicas
  *   ortho   count bf16 values;  master: count floats
  *   params  host array of n_ranks device pointers, count elements each
@@ -552,6 +558,15 @@ ZERO_API int zero_orthogonalize(int dtype, int batch, uint64_t rows, uint64_t co
                                 uint64_t ld_src, void* const* dst, uint64_t ld_dst, int steps, const float* coeffs,
                                 float scale, void* workspace, uint64_t workspace_bytes, void* stream);
 
+/* zero_orthogonalize for the matrices of a step: a wait inside its kernels
+ * that gives up leaves an incomplete result, which is noted in the step's
+ * state (ZERO_MUON_GAVE_UP), so that zero_muon_apply does not apply it.
+ * Errors: EINVAL, ECUDA. */
+ZERO_API int zero_muon_orthogonalize(int dtype, int batch, uint64_t rows, uint64_t cols, const void* const* src,
+                                     uint64_t ld_src, void* const* dst, uint64_t ld_dst, int steps,
+                                     const float* coeffs, float scale, void* workspace, uint64_t workspace_bytes,
+                                     zero_muon_state_t* state, void* stream);
+
 /* Bytes of zero_orthogonalize's workspace (a host query); 0 for sizes that it refuses or that are empty. */
 ZERO_API uint64_t zero_orthogonalize_workspace_bytes(int batch, uint64_t rows, uint64_t cols);
 
@@ -597,9 +612,11 @@ ZERO_API int zero_mx4_dequantize(int dtype, uint64_t rows, uint64_t cols, const 
 ZERO_API int zero_mx4_matmul(int dtype, uint64_t m, uint64_t n, uint64_t k, const void* a_codes, const void* a_scales,
                              const void* b_codes, const void* b_scales, void* out16, uint64_t ld, void* stream);
 
-/* Whether a bounded wait inside a kernel of zero_orthogonalize or
- * zero_mx4_matmul has given up on this device since the last call: ZERO_OK or
- * ZERO_ETIMEOUT (that kernel's output is incomplete).  Synchronises the stream. */
+/* Whether a bounded wait inside a kernel of zero_orthogonalize (or
+ * zero_muon_orthogonalize) or zero_mx4_matmul has given up on this device
+ * since the last call: ZERO_OK or ZERO_ETIMEOUT (that kernel's output is
+ * incomplete).  Synchronises the stream.  The answer is the device's, for
+ * all streams and callers together, and the first to ask gets it. */
 ZERO_API int zero_matrix_status(void* stream);
 
 /* Last error message of this handle (or of the last failed init when h is

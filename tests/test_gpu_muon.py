@@ -450,3 +450,35 @@ def test_refusals():
     refused("ZERO_MAX_SIDE", ns, 0, (1 << 18) + 1, 16, [h], [h], ws)
     assert Z.zero_orthogonalize_workspace_bytes(1, (1 << 18) + 1, 16) == 0
     torch.cuda.synchronize()
+
+
+# ------------------------------------------- an orthogonalisation that could not finish
+@pytest.mark.parametrize("pending,scale", [(2, 512.0), (3, 256.0), (1, 256.0)])
+def test_what_a_wait_that_gave_up_left_is_not_applied(pending, scale):
+    """The word that such a wait sets (2) and a non-finite gradient's (1), written by the host."""
+    buf = MuonBuffers(SHAPES, 2, "bf16", loss_scale=512.0)
+    hyp = Z.muon_hyper(lr=0.1)
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    for t in (buf.grads, buf.params, buf.master):
+        t.copy_(torch.randn(t.shape, generator=gen, device="cuda"))
+    buf.step(hyp)
+    first = buf.status()
+    assert first["applied"] == 1 and first["aborted"] == 0
+    before = [t.clone() for t in (buf.master, buf.params, buf.live_momentum(first["slot"]))]
+    Z.zero_muon_momentum(Z.ZERO_BF16, buf.count, list(buf.grads), buf.momentum, buf.update, hyp, buf.state)
+    buf.state[2] |= pending
+    buf.ortho.fill_(7.0)
+    Z.zero_muon_apply(Z.ZERO_BF16, buf.count, buf.ortho, buf.master, list(buf.params), hyp, buf.state)
+    s = Z.zero_muon_get_state(buf.state)
+    assert torch.equal(buf.master, before[0]) and torch.equal(buf.params, before[1])
+    assert s["slot"] == first["slot"] and torch.equal(buf.live_momentum(s["slot"]), before[2])
+    assert (s["overflow"], s["applied"], s["steps_applied"], s["steps_skipped"]) == (1, 0, 1, 1)
+    assert (s["aborted"], s["loss_scale"], s["pending"]) == (pending >> 1, scale, 0)
+    if s["aborted"]:
+        with pytest.raises(Z.ZeroError) as e:
+            buf.status()
+        assert e.value.code == 4
+    buf.step(hyp)
+    s = buf.status()
+    assert (s["applied"], s["aborted"], s["steps_applied"]) == (1, 0, 2)
+    assert not torch.equal(buf.master, before[0])

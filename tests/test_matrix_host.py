@@ -105,3 +105,10 @@ def test_tensors_in_host_memory_are_refused(Z):
         with pytest.raises(Z.ZeroError) as e:
             call()
         assert e.value.code == 1 and "GPU" in str(e.value)
+
+
+@pytest.mark.parametrize("state", [260, 257])
+def test_a_step_s_orthogonalisation_checks_its_state(Z, state):
+    with pytest.raises(Z.ZeroError) as e:
+        Z.zero_orthogonalize(1, 20, 30, [256], [256], None, stream=0, state=state)
+    assert e.value.code == 1 and "state" in str(e.value)

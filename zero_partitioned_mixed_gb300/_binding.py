@@ -26,7 +26,7 @@ EXPORTS = (
     "zero_gather_bucket_q8", "zero_reduce_scatter_bucket_q", "zero_debug_hold_staged",
     "zero_noalloc_scratch_bytes", "zero_set_persistent", "zero_reduce_scatter_gather_bucket",
     "zero_muon_set_state", "zero_muon_get_state", "zero_muon_momentum", "zero_muon_apply",
-    "zero_orthogonalize", "zero_orthogonalize_workspace_bytes", "zero_mx4_codes_bytes", "zero_mx4_scales_bytes",
+    "zero_orthogonalize", "zero_muon_orthogonalize", "zero_orthogonalize_workspace_bytes", "zero_mx4_codes_bytes", "zero_mx4_scales_bytes",
     "zero_mx4_quantize", "zero_mx4_dequantize", "zero_mx4_matmul", "zero_matrix_status",
 )
 ZERO_Q_BLOCK = 256
@@ -67,7 +67,8 @@ class MuonHyper(C.Structure):
 class MuonState(C.Structure):
     _fields_ = [("loss_scale", C.c_float), ("slot", C.c_int32), ("pending", C.c_int32), ("overflow", C.c_int32),
                 ("applied", C.c_int32), ("ticket", C.c_uint32), ("steps_applied", C.c_int64),
-                ("steps_skipped", C.c_int64), ("reserved", C.c_int64 * 3)]
+                ("steps_skipped", C.c_int64), ("aborted", C.c_int32), ("reserved0", C.c_int32),
+                ("reserved", C.c_int64 * 2)]
 
 
 _lib = None
@@ -126,6 +127,7 @@ def load_library():
     lib.zero_muon_apply.argtypes = [I32, I32, U64, P, P, C.POINTER(P), C.POINTER(MuonHyper), P, P]
     lib.zero_orthogonalize.argtypes = [I32, I32, U64, U64, C.POINTER(P), U64, C.POINTER(P), U64, I32,
                                        C.POINTER(C.c_float), C.c_float, P, U64, P]
+    lib.zero_muon_orthogonalize.argtypes = lib.zero_orthogonalize.argtypes[:-1] + [P, P]
     lib.zero_mx4_quantize.argtypes = [I32, U64, U64, P, U64, I32, P, P, P]
     lib.zero_mx4_dequantize.argtypes = [I32, U64, U64, P, P, P, U64, P]
     lib.zero_mx4_matmul.argtypes = [I32, U64, U64, U64, P, P, P, P, P, U64, P]
@@ -356,7 +358,7 @@ def zero_muon_set_state(state, loss_scale: float = 1.0, steps_applied: int = 0, 
 def zero_muon_get_state(state, stream=None) -> dict:
     out = MuonState()
     _check(load_library().zero_muon_get_state(_ptr(state), _stream(stream), C.byref(out)), None)
-    return {f: getattr(out, f) for f, _ in MuonState._fields_ if f not in ("reserved", "ticket")}
+    return {f: getattr(out, f) for f, _ in MuonState._fields_ if f not in ("reserved", "reserved0", "ticket")}
 
 
 def zero_muon_momentum(dtype: int, count: int, grads, momentum, update, hyp: MuonHyper, state, stream=None):
@@ -378,10 +380,13 @@ def zero_orthogonalize_workspace_bytes(batch: int, rows: int, cols: int) -> int:
 
 
 def zero_orthogonalize(dtype: int, rows: int, cols: int, src, dst, workspace, ld_src: Optional[int] = None,
-                       ld_dst: Optional[int] = None, steps: int = 5, coeffs=None, scale: float = 1.0, stream=None):
+                       ld_dst: Optional[int] = None, steps: int = 5, coeffs=None, scale: float = 1.0, stream=None,
+                       state=None):
     """src, dst: one matrix each per entry (lists of tensors, or their
     pointer_array); workspace: a device tensor.  coeffs: one (a, b, c) for
-    every step, or `steps` of them; None takes the library's."""
+    every step, or `steps` of them; None takes the library's.  state: that of
+    the step which the matrices are part of (zero_muon_orthogonalize): a wait
+    that gives up is noted there, and zero_muon_apply skips the step."""
     if len(src) != len(dst):
         raise ZeroError(1, "src and dst must have the same length")
     arr = None
@@ -392,11 +397,13 @@ def zero_orthogonalize(dtype: int, rows: int, cols: int, src, dst, workspace, ld
         if len(flat) != 3 * steps:
             raise ZeroError(1, "coeffs must be one (a, b, c), or one for each step")
         arr = (C.c_float * max(1, len(flat)))(*flat)
-    rc = load_library().zero_orthogonalize(dtype, len(src), rows, cols, _ptr_array(src),
-                                           cols if ld_src is None else ld_src, _ptr_array(dst),
-                                           cols if ld_dst is None else ld_dst, steps, arr, scale, _ptr(workspace),
-                                           workspace.numel() * workspace.element_size() if workspace is not None else 0,
-                                           _stream(stream))
+    args = (dtype, len(src), rows, cols, _ptr_array(src), cols if ld_src is None else ld_src, _ptr_array(dst),
+            cols if ld_dst is None else ld_dst, steps, arr, scale, _ptr(workspace),
+            workspace.numel() * workspace.element_size() if workspace is not None else 0)
+    if state is None:
+        rc = load_library().zero_orthogonalize(*args, _stream(stream))
+    else:
+        rc = load_library().zero_muon_orthogonalize(*args, _ptr(state), _stream(stream))
     _check(rc, None)
 
 

@@ -19,7 +19,8 @@
 // Whether a gradient overflowed is known only when all were read, but the
 // momentum is written on the way.  It therefore has two slots: the new
 // momentum goes to the slot that is not live, and zero_muon_apply makes that
-// slot the live one or, after an overflow, leaves everything as it was.
+// slot the live one or, after an overflow, leaves everything as it was.  The
+// same holds where the orthogonalisation between them could not finish.
 
 #include <cmath>
 #include <cstdint>
@@ -52,7 +53,7 @@ struct MuonArgs {
 
 struct MuonPro {
     float den, inv;
-    int use_div, slot, skip;
+    int use_div, slot, skip;   // skip: the state's `pending`
 };
 
 // The unscale factor N * scale and the live slot, read once per block.
@@ -66,7 +67,7 @@ __device__ __forceinline__ void muon_prologue(const MuonArgs& a, MuonPro& pro) {
         pro.use_div = pow2 ? 0 : 1;
         pro.inv = pow2 ? __fdiv_rn(1.0f, den) : 0.0f;
         pro.slot = a.state->slot & 1;
-        pro.skip = a.state->pending != 0;
+        pro.skip = a.state->pending;
     }
     __syncthreads();
 }
@@ -127,7 +128,7 @@ __global__ void __launch_bounds__(kThreads) k_muon_momentum(const __grid_constan
     // the last, partial vector: one element a thread of the last block
     if (IO::W > 1 && blockIdx.x == gridDim.x - 1 && threadIdx.x < rest)
         bad |= momentum_at<DT, Io1>(a, pro, nvec * IO::W + threadIdx.x);
-    if (bad) atomicOr(reinterpret_cast<int*>(&a.state->pending), 1);
+    if (bad) atomicOr(reinterpret_cast<int*>(&a.state->pending), ZERO_MUON_NONFINITE);
 }
 
 template <int DT, class IO>
@@ -147,7 +148,8 @@ __device__ __forceinline__ void apply_at(const MuonArgs& a, uint64_t i) {
 }
 
 // The last block to finish turns the step's outcome into the state: applied
-// (the momentum's new slot becomes live) or skipped (the loss scale halves).
+// (the momentum's new slot becomes live) or skipped (the loss scale halves if
+// a gradient was the reason).
 template <int DT, class IO>
 __global__ void __launch_bounds__(kThreads) k_muon_apply(const __grid_constant__ MuonArgs a) {
     pdl_enter();
@@ -170,10 +172,11 @@ __global__ void __launch_bounds__(kThreads) k_muon_apply(const __grid_constant__
         if (atomicAdd(&a.state->ticket, 1u) == gridDim.x - 1) {
             zero_muon_state_t* st = a.state;
             st->ticket = 0u;
-            st->overflow = pro.skip;
-            st->applied = !pro.skip;
+            st->overflow = pro.skip != 0;
+            st->applied = pro.skip == 0;
+            st->aborted = (pro.skip & ZERO_MUON_GAVE_UP) != 0;
             if (pro.skip) {
-                st->loss_scale = fmaxf(__fmul_rn(st->loss_scale, 0.5f), 1.0f);
+                if (pro.skip & ZERO_MUON_NONFINITE) st->loss_scale = fmaxf(__fmul_rn(st->loss_scale, 0.5f), 1.0f);
                 st->steps_skipped += 1;
             } else {
                 st->slot = pro.slot ^ 1;

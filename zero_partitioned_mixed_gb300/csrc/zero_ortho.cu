@@ -46,6 +46,13 @@ namespace zg {
 namespace {
 
 constexpr int kMaxMatrices = ZERO_MAX_MATRICES;
+
+// After settle(): the step that the matrices are part of learns of a wait that
+// gave up, before its zero_muon_apply runs.  `pending`: of its state, or NULL.
+__device__ __forceinline__ void note_gave_up(volatile int* quit, int32_t* pending) {
+    if (*quit && pending && threadIdx.x == 0) atomicOr(pending, ZERO_MUON_GAVE_UP);
+}
+
 constexpr int kMaxPhases = 3 * ZERO_MAX_NS_STEPS + 3;
 
 // Storage scales (all powers of two): entries of X and A are at most a
@@ -255,6 +262,7 @@ struct ProductArgs {
     uint64_t dst_ld;
     const float* g0;           // [batch]
     uint32_t* done;            // [batch][kMaxPhases] finished epilogues, zero at the start
+    int32_t* pending;          // of the step's state, or NULL
     int32_t dst_vec;           // every row of dst starts on 16 bytes
     uint32_t n_phases, batch;
 };
@@ -557,6 +565,7 @@ __global__ void __launch_bounds__(kProductThreads) k_ortho_products(const __grid
     tc_fence_before();
     __syncthreads();
     settle(quit);
+    note_gave_up(quit, p.pending);
     cluster_sync();
     if (warp == 1) {
         tc_fence_after();
@@ -603,6 +612,7 @@ struct SmallArgs {
     uint32_t side, span;     // the shorter and the longer side
     uint32_t ctas, per;      // CTAs a matrix, 64s of the longer side a CTA
     int32_t tall, steps;
+    int32_t* pending;        // of the step's state, or NULL
     float scale;
     float coeffs[3 * ZERO_MAX_NS_STEPS];
 };
@@ -964,6 +974,7 @@ __global__ void __launch_bounds__(kSmallThreads) k_ortho_small(const __grid_cons
     tc_fence_before();
     __syncthreads();
     settle(quit);
+    note_gave_up(quit, p.pending);
     if (p.ctas > 1) cluster_sync();   // nobody reads this CTA's shared memory any more
     if (warp == 0) {
         tc_fence_after();
@@ -1067,25 +1078,10 @@ cudaError_t large_clusters(size_t smem, int* out) {
 
 constexpr float kDefaultCoeffs[3] = {3.4445f, -4.7750f, 2.0315f};
 
-}  // namespace
-
-cudaError_t ortho_gave_up(cudaStream_t s, int32_t* out) { return read_gave_up(s, out); }
-
-}  // namespace zg
-
-using namespace zg;
-
-extern "C" {
-
-uint64_t zero_orthogonalize_workspace_bytes(int batch, uint64_t rows, uint64_t cols) {
-    if (batch < 1 || batch > ZERO_MAX_MATRICES || rows < 1 || cols < 1 || rows > ZERO_MAX_SIDE || cols > ZERO_MAX_SIDE)
-        return 0;
-    return scratch_of(static_cast<uint64_t>(batch), rows, cols).bytes;
-}
-
-int zero_orthogonalize(int dtype, int batch, uint64_t rows, uint64_t cols, const void* const* src, uint64_t ld_src,
-                       void* const* dst, uint64_t ld_dst, int steps, const float* coeffs, float scale, void* workspace,
-                       uint64_t workspace_bytes, void* stream) {
+// Both calls; `pending` is the word of a step's state that learns of a wait that gave up, or NULL.
+int orthogonalize(int dtype, int batch, uint64_t rows, uint64_t cols, const void* const* src, uint64_t ld_src,
+                  void* const* dst, uint64_t ld_dst, int steps, const float* coeffs, float scale, void* workspace,
+                  uint64_t workspace_bytes, int32_t* pending, void* stream) {
     nvtxRangePushA("zero_orthogonalize");
     struct Pop { ~Pop() { nvtxRangePop(); } } pop;
     if (dtype != ZERO_FP16 && dtype != ZERO_BF16) return refuse(ZERO_EINVAL, "dtype must be fp16 or bf16");
@@ -1159,6 +1155,7 @@ int zero_orthogonalize(int dtype, int batch, uint64_t rows, uint64_t cols, const
         m.tall = tall;
         m.steps = steps;
         m.scale = scale;
+        m.pending = pending;
         for (int i = 0; i < 3 * steps; ++i) m.coeffs[i] = coeffs ? coeffs[i] : kDefaultCoeffs[i % 3];
         size_t smem = 1024 + 3 * kSquareBytes + static_cast<size_t>(m.per) * kSlabUnit;
         if (m.ctas > 1 && smem < kAloneSmem) smem = kAloneSmem;   // its blocks wait for one another: see tmem_alloc
@@ -1214,6 +1211,7 @@ int zero_orthogonalize(int dtype, int batch, uint64_t rows, uint64_t cols, const
     }
     p.g0 = q.g0;
     p.done = q.done;
+    p.pending = pending;
     p.batch = nb;
     uint32_t most = 0;   // tiles of the largest phase
 
@@ -1301,6 +1299,37 @@ int zero_orthogonalize(int dtype, int batch, uint64_t rows, uint64_t cols, const
     e = launch_together(k_ortho_products, dim3(grid), kProductThreads, kProductSmem, 2, s, p);
     if (e != cudaSuccess) return cuda_refuse(e, "products");
     return ZERO_OK;
+}
+
+}  // namespace
+
+cudaError_t ortho_gave_up(cudaStream_t s, int32_t* out) { return read_gave_up(s, out); }
+
+}  // namespace zg
+
+using namespace zg;
+
+extern "C" {
+
+uint64_t zero_orthogonalize_workspace_bytes(int batch, uint64_t rows, uint64_t cols) {
+    if (batch < 1 || batch > ZERO_MAX_MATRICES || rows < 1 || cols < 1 || rows > ZERO_MAX_SIDE || cols > ZERO_MAX_SIDE)
+        return 0;
+    return scratch_of(static_cast<uint64_t>(batch), rows, cols).bytes;
+}
+
+int zero_orthogonalize(int dtype, int batch, uint64_t rows, uint64_t cols, const void* const* src, uint64_t ld_src,
+                       void* const* dst, uint64_t ld_dst, int steps, const float* coeffs, float scale, void* workspace,
+                       uint64_t workspace_bytes, void* stream) {
+    return orthogonalize(dtype, batch, rows, cols, src, ld_src, dst, ld_dst, steps, coeffs, scale, workspace,
+                         workspace_bytes, nullptr, stream);
+}
+
+int zero_muon_orthogonalize(int dtype, int batch, uint64_t rows, uint64_t cols, const void* const* src, uint64_t ld_src,
+                            void* const* dst, uint64_t ld_dst, int steps, const float* coeffs, float scale,
+                            void* workspace, uint64_t workspace_bytes, zero_muon_state_t* state, void* stream) {
+    if (!state || !aligned(state, 8)) return refuse(ZERO_EINVAL, "state is NULL or not 8-byte aligned");
+    return orthogonalize(dtype, batch, rows, cols, src, ld_src, dst, ld_dst, steps, coeffs, scale, workspace,
+                         workspace_bytes, &state->pending, stream);
 }
 
 }  // extern "C"

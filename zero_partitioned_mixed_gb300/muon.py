@@ -85,7 +85,7 @@ class MuonBuffers:
         B.zero_muon_momentum(dt, self.count, self._grad_rows, self.momentum, self.update, hyp, self.state, stream)
         for r, c, src, dst in self._calls:
             B.zero_orthogonalize(B.ZERO_BF16, r, c, src, dst, self.workspace, steps=steps, coeffs=coeffs,
-                                 scale=float(scale(r, c)), stream=stream)
+                                 scale=float(scale(r, c)), stream=stream, state=self.state)
         B.zero_muon_apply(dt, self.count, self.ortho, self.master, self._param_rows, hyp, self.state, stream)
 
     def quantize(self, i: int, transpose: bool = False, rank: int = 0) -> Mx4Matrix:
@@ -94,6 +94,11 @@ class MuonBuffers:
         return Mx4Matrix.of(self.matrix(i, self.params[rank]), transpose)
 
     def status(self, stream=None) -> dict:
-        """The state after the last step; raises when a kernel's bounded wait gave up."""
+        """The state after the last step; raises when a kernel's bounded wait gave up (a step in whose
+        orthogonalisation that happened was skipped)."""
         B.zero_matrix_status(stream)
-        return B.zero_muon_get_state(self.state, stream)
+        s = B.zero_muon_get_state(self.state, stream)
+        if s["aborted"]:
+            raise B.ZeroError(B.ZERO_ETIMEOUT, "a bounded wait of the last step's orthogonalisation gave up: "
+                                               "the step was skipped")
+        return s
