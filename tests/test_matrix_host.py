@@ -112,3 +112,18 @@ def test_a_step_s_orthogonalisation_checks_its_state(Z, state):
     with pytest.raises(Z.ZeroError) as e:
         Z.zero_orthogonalize(1, 20, 30, [256], [256], None, stream=0, state=state)
     assert e.value.code == 1 and "state" in str(e.value)
+
+
+def test_shared_memory_that_is_read_in_wider_pieces_is_aligned_for_them():
+    import pathlib
+    import re
+    csrc = pathlib.Path(__file__).resolve().parents[1] / "zero_partitioned_mixed_gb300" / "csrc"
+    found = 0
+    for path in sorted(csrc.glob("*.cu*")):
+        t = path.read_text()
+        for align, name in re.findall(r"__shared__ (__align__\(\d+\) )?(?:uint8_t|unsigned char|uint16_t|__half) (\w+)\[", t):
+            casts = re.findall(rf"reinterpret_cast<(?:const )?(uint\d_t|uint32_t|uint64_t|uint2|uint4|float4) ?\*>\([^;]*?\b{name}\b", t)
+            if casts:
+                found += 1
+                assert align, f"{path.name}: {name} is read as {casts[0]}"
+    assert found >= 1

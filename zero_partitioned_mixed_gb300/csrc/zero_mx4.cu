@@ -148,7 +148,7 @@ template <int DT>
 __global__ void __launch_bounds__(kThreads) k_mx4_columns(const __grid_constant__ MxArgs a) {
     pdl_enter();
     __shared__ __align__(16) uint4 s_codes[128][5];   // 5: neighbouring columns start in other banks
-    __shared__ uint8_t s_scale[128][4];
+    __shared__ __align__(4) uint8_t s_scale[128][4];   // a row is read as one word
     const int lane = threadIdx.x & 31, b = (threadIdx.x >> 5) & 3;
     const int c = (threadIdx.x >> 7) * 64 + 2 * lane;
     const uint64_t col0 = static_cast<uint64_t>(blockIdx.x) * 128, row0 = static_cast<uint64_t>(blockIdx.y) * 128;
