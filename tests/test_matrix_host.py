@@ -127,3 +127,16 @@ def test_shared_memory_that_is_read_in_wider_pieces_is_aligned_for_them():
                 found += 1
                 assert align, f"{path.name}: {name} is read as {casts[0]}"
     assert found >= 1
+
+
+def test_a_linear_layer_refuses_to_drop_its_input_s_gradient(Z):
+    # the call makes no autograd graph: without a word, whatever made x would train on no gradient
+    from zero_partitioned_mixed_gb300 import mx4
+    x, w = torch.zeros(4, 32, dtype=torch.bfloat16, requires_grad=True), mx4.Mx4Matrix(8, 32, device="cpu")
+    with pytest.raises(Z.ZeroError) as e:
+        mx4.mx4_linear(x, w)
+    assert e.value.code == 1 and "mx4_linear_backward" in str(e.value)
+    for quiet in (lambda: mx4.mx4_linear(x.detach(), w), torch.no_grad()(lambda: mx4.mx4_linear(x, w))):
+        with pytest.raises(Z.ZeroError) as e:
+            quiet()
+        assert "GPU" in str(e.value)      # as far as a host tensor gets

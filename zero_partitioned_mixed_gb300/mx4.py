@@ -83,7 +83,12 @@ def mx4_product(a: Mx4Matrix, b: Mx4Matrix, dtype=torch.bfloat16, out: Optional[
 def mx4_linear(x: torch.Tensor, w: Mx4Matrix, out: Optional[torch.Tensor] = None,
                scratch: Optional[Mx4Matrix] = None) -> torch.Tensor:
     """y = x w^T: x [tokens, inner] in 16 bits is quantised, w [outer, inner] is kept in 4.
-    scratch: a Mx4Matrix of x's size to reuse from call to call."""
+    scratch: a Mx4Matrix of x's size to reuse from call to call.
+    The call records no autograd graph (mx4_linear_backward gives the gradients),
+    so an x whose gradient autograd is to find is refused."""
+    if x.requires_grad and torch.is_grad_enabled():
+        raise B.ZeroError(1, "mx4_linear records no autograd graph: pass x.detach() (or call it under torch.no_grad()) "
+                             "and take the gradients from mx4_linear_backward")
     q = scratch.fill(x) if scratch is not None else Mx4Matrix.of(x)
     return mx4_product(q, w, x.dtype, out)
 
