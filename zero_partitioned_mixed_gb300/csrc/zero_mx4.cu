@@ -519,7 +519,7 @@ k_mx4_product(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
                                   narrow2<DT>(v[8 * j + 2], v[8 * j + 3]), narrow2<DT>(v[8 * j + 4], v[8 * j + 5]),
                                   narrow2<DT>(v[8 * j + 6], v[8 * j + 7]));
                     __syncwarp();
-                    write_rows<32>(static_cast<unsigned short*>(p.out), p.ld, p.vec, p.m, p.n, row0, col0 + c, buf);
+                    write_rows(static_cast<unsigned short*>(p.out), p.ld, p.vec, p.m, p.n, row0, col0 + c, buf);
                 }
                 tc_fence_before();
                 __syncwarp();

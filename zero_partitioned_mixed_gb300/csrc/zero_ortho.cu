@@ -534,7 +534,7 @@ __global__ void __launch_bounds__(kProductThreads) k_ortho_products(const __grid
                 }
                 if (final) {
                     __syncwarp();
-                    write_rows<32>(static_cast<unsigned short*>(p.dst[w.b]), p.dst_ld, p.dst_vec, f.rows, f.cols, row0,
+                    write_rows(static_cast<unsigned short*>(p.dst[w.b]), p.dst_ld, p.dst_vec, f.rows, f.cols, row0,
                                    col0 + 32 * c, buf);
                 } else {
                     proxy_fence_shared();

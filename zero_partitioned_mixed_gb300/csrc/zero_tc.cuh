@@ -39,8 +39,7 @@ inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
     return fn;
 }
 
-// A [batch][rows][cols] array of `elem`-byte values (1, 2 or 4)
-// with `pitch` values between rows, read in boxes of box_cols x box_rows in
+// A [batch][rows][cols] array of `elem`-byte values (1 or 2) with `pitch` values between rows, read in boxes of box_cols x box_rows in
 // the 128-byte swizzle (or another); what lies outside the array reads as zero.
 inline cudaError_t make_map(CUtensorMap* map, int elem, const void* base, uint64_t cols, uint64_t rows, uint64_t batch,
                             uint64_t pitch, uint64_t matrix_stride, uint32_t box_cols, uint32_t box_rows,
@@ -51,9 +50,7 @@ inline cudaError_t make_map(CUtensorMap* map, int elem, const void* base, uint64
     const cuuint64_t strides[2] = {pitch * static_cast<uint64_t>(elem), matrix_stride * static_cast<uint64_t>(elem)};
     const cuuint32_t box[3] = {box_cols, box_rows, box_batch};
     const cuuint32_t step[3] = {1, 1, 1};
-    const CUresult r = encode(map, elem == 4   ? CU_TENSOR_MAP_DATA_TYPE_UINT32
-                                   : elem == 2 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
-                                               : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3,
+    const CUresult r = encode(map, elem == 2 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3,
                               const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
                               swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -107,17 +104,6 @@ __device__ __forceinline__ bool elect_one() {
     uint32_t p;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
     return p != 0;
-}
-// Whether the phase is complete, without waiting (bar_test may suspend the
-// thread for a while).
-__device__ __forceinline__ bool bar_peek(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
 }
 // A place in a ring of N stages: its index, and the parity of its barriers'
 // phase in this round.
@@ -402,21 +388,19 @@ __device__ __forceinline__ uint16_t ld_shared16(uint32_t addr) {
     return x;
 }
 
-// 32 rows x W columns (64 or 32) of 16-bit values in a warp's buffer, swizzled
-// for rows of that width, into rows row0... and columns col0... of a row-major
-// rows x cols matrix: 16 bytes a lane where every row starts on 16 bytes
-// (`vec`), value by value elsewhere.
-template <uint32_t W>
+// 32 rows x 32 columns of 16-bit values in a warp's buffer (piece64) into rows
+// row0... and columns col0... of a row-major rows x cols matrix: 16 bytes a
+// lane where every row starts on 16 bytes (`vec`), value by value elsewhere.
 __device__ __forceinline__ void write_rows(unsigned short* dst, uint64_t ld, bool vec, uint32_t rows, uint32_t cols,
                                            uint32_t row0, uint32_t col0, uint32_t buf) {
     const uint32_t lane = threadIdx.x & 31;
     if (vec) {
 #pragma unroll
-        for (uint32_t i = lane; i < 4 * W; i += 32) {
-            const uint32_t r = i / (W / 8), j = i % (W / 8), col = col0 + 8 * j;
+        for (uint32_t i = lane; i < 4 * 32; i += 32) {
+            const uint32_t r = i / 4, j = i % 4, col = col0 + 8 * j;
             if (row0 + r >= rows || col >= cols) continue;
             unsigned short* out = dst + static_cast<uint64_t>(row0 + r) * ld + col;
-            const uint4 x = ld_shared(buf + (W == 64 ? piece128(r, j) : piece64(r, j)));
+            const uint4 x = ld_shared(buf + piece64(r, j));
             if (col + 8 <= cols) {
                 *reinterpret_cast<uint4*>(out) = x;
             } else {
@@ -428,11 +412,11 @@ __device__ __forceinline__ void write_rows(unsigned short* dst, uint64_t ld, boo
         }
     } else {
 #pragma unroll 4
-        for (uint32_t i = lane; i < 32 * W; i += 32) {
-            const uint32_t r = i / W, e = i % W;
+        for (uint32_t i = lane; i < 32 * 32; i += 32) {
+            const uint32_t r = i / 32, e = i % 32;
             if (row0 + r < rows && col0 + e < cols)
                 dst[static_cast<uint64_t>(row0 + r) * ld + col0 + e] =
-                    ld_shared16(buf + (W == 64 ? piece128(r, e >> 3) : piece64(r, e >> 3)) + 2 * (e & 7));
+                    ld_shared16(buf + piece64(r, e >> 3) + 2 * (e & 7));
         }
     }
 }
