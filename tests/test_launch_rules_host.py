@@ -92,3 +92,15 @@ def test_a_block_asks_whether_a_wait_gave_up_after_its_barrier():
             assert 0 <= barrier < settle, f"{name}: {m.group(1)}"
             assert "bar_wait(" not in body[barrier:settle] and "finish()" not in body[barrier:settle], f"{name}: {m.group(1)}"
     assert found == 4
+
+
+def test_waits_for_tensor_memory_loads_name_the_loaded_registers():
+    # the registers of tcgen05.ld are filled only after tcgen05.wait::ld: a wait that does not name them lets the
+    # compiler copy them before it
+    t = _sources()["zero_tc.cuh"]
+    loads = re.findall(r"void (\w+)\((?:uint32_t \w+, )?(?:uint32_t|float) \(&\w+\)\[(\d+)\]\) \{(.*?)\n\}\n", t, re.S)
+    waits = [(name, int(n), body) for name, n, body in loads if "tcgen05.wait::ld" in body]
+    assert sum(t.count(w) for w in ["tcgen05.wait::ld"]) == len(waits) == 2
+    for name, n, body in waits:
+        named = set(re.findall(r'"\+r"\(r\[(\d+)\]\)', body))
+        assert named == {str(i) for i in range(n)}, name
