@@ -619,6 +619,20 @@ ZERO_API int zero_mx4_matmul(int dtype, uint64_t m, uint64_t n, uint64_t k, cons
  * all streams and callers together, and the first to ask gets it. */
 ZERO_API int zero_matrix_status(void* stream);
 
+/*
+ * zero_debug_hold_matrix -- test hook for the failure path of the matrix
+ * kernels.  In the next zero_orthogonalize, zero_muon_orthogonalize or
+ * zero_mx4_matmul of the process that launches a kernel with bounded waits
+ * (one-shot), block 0 stops issuing its copies at its stage `stage` (stages
+ * counted from 0 over its tiles); in the orthogonalisation of short sides it
+ * leaves out the signal that its product `stage` is done.  The waits for
+ * them run out (about 2 s).  No access leaves its buffers and every wait
+ * ends.  The call's output is incomplete, and zero_matrix_status returns
+ * ZERO_ETIMEOUT once.  stage < 0 clears a pending hold; one past block 0's
+ * last has no effect.  Returns ZERO_OK.
+ */
+ZERO_API int zero_debug_hold_matrix(int64_t stage);
+
 /* Last error message of this handle (or of the last failed init when h is
  * NULL).  The string is owned by the library and valid until the next call. */
 ZERO_API const char* zero_last_error(zero_handle_t h);

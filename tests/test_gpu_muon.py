@@ -482,3 +482,70 @@ def test_what_a_wait_that_gave_up_left_is_not_applied(pending, scale):
     s = buf.status()
     assert (s["applied"], s["aborted"], s["steps_applied"]) == (1, 0, 2)
     assert not torch.equal(buf.master, before[0])
+
+
+HELD = [(1, 64, 96), (1, 96, 64), (1, 100, 2000), (2, 1500, 40), (1, 60, 6000), (3, 300, 180), (2, 180, 700)]
+
+
+@pytest.mark.parametrize("batch,rows,cols", HELD)
+@pytest.mark.parametrize("stage", [0, 2])
+def test_a_wait_that_runs_out_ends_the_call_and_is_reported(batch, rows, cols, stage):
+    """Both kernels, in one block and in clusters: block 0 stops feeding the tensor cores on purpose."""
+    g = gradient(rows, cols, rows + cols, batch=batch).bfloat16().cuda()
+    want = ortho(g)
+    ws = workspace(batch, rows, cols)
+    room = torch.full((batch, rows * cols + 512), 7.0, dtype=torch.bfloat16, device="cuda")
+    dst = [t[256:256 + rows * cols].view(rows, cols) for t in room]
+    Z._binding.zero_debug_hold_matrix(stage)
+    Z.zero_orthogonalize(Z.ZERO_BF16, rows, cols, list(g), dst, ws)
+    with pytest.raises(Z.ZeroError) as e:
+        Z.zero_matrix_status()
+    assert e.value.code == 4 and "zero_orthogonalize" in str(e.value)
+    for _ in range(2):
+        Z.zero_orthogonalize(Z.ZERO_BF16, rows, cols, list(g), dst, ws)
+    Z.zero_matrix_status()
+    for d, w in zip(dst, want):
+        assert torch.equal(d, w)
+        d.fill_(7.0)
+    assert bool((room == 7.0).all())
+
+
+@pytest.mark.parametrize("shape", [(48, 80), (90, 1100), (300, 180)])
+def test_a_step_whose_orthogonalisation_gave_up_is_skipped(shape):
+    hyp = Z.muon_hyper(lr=0.05, weight_decay=0.1)
+    bufs = [MuonBuffers([shape, (33, 65)], 2, "fp16", loss_scale=128.0) for _ in range(2)]
+    gen = torch.Generator().manual_seed(5)
+    w = [0.02 * torch.randn(s, generator=gen) for s in bufs[0].shapes]
+    for b in bufs:
+        for i in range(2):
+            b.matrix(i, b.master).copy_(w[i])
+        b.params.copy_(b.master.half())
+
+    def gradients(step):
+        for b in bufs:
+            for k in range(2):
+                for i, (r, c) in enumerate(b.shapes):
+                    b.matrix(i, b.grads[k]).copy_(128 * gradient(r, c, 40 * step + 10 * k + i)[0])
+
+    gradients(0)
+    for b in bufs:
+        b.step(hyp)
+    a, b = bufs
+    a.status()
+    before = [t.clone() for t in (b.master, b.params)]
+    Z._binding.zero_debug_hold_matrix(1)      # the first matrix of the next step
+    b.step(hyp)
+    s = Z.zero_muon_get_state(b.state)
+    assert (s["applied"], s["overflow"], s["aborted"], s["steps_applied"], s["loss_scale"]) == (0, 1, 1, 1, 128.0)
+    assert torch.equal(b.master, before[0]) and torch.equal(b.params, before[1])
+    for _ in range(2):                        # the device's word, then the step's own
+        with pytest.raises(Z.ZeroError) as e:
+            b.status()
+        assert e.value.code == 4
+    gradients(1)
+    for c in bufs:                            # as if the skipped step had not been
+        c.step(hyp)
+    assert torch.equal(a.master, b.master) and torch.equal(a.params, b.params)
+    sa, sb = a.status(), b.status()
+    assert torch.equal(a.live_momentum(sa["slot"]), b.live_momentum(sb["slot"]))
+    assert sb["steps_skipped"] == 1 and sa["steps_applied"] == sb["steps_applied"] == 2

@@ -294,3 +294,24 @@ def test_rows_that_share_memory_are_refused():
     dx, dw = mx4_linear_backward(dy.contiguous(), x, w_t)
     assert dx.shape == x.shape and dw.shape == w.shape
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 300, 4096), (20, 129, 300), (32, 200, 5000), (100, 600, 1300), (2100, 4000, 520)])
+@pytest.mark.parametrize("stage", [0, 1])
+def test_a_wait_that_runs_out_ends_the_call_and_is_reported(m, n, k, stage):
+    """All forms of the product: block 0 stops copying its operands on purpose."""
+    qx, qw = Mx4Matrix.of(matrix(m, k, "bf16", 1).cuda()), Mx4Matrix.of(matrix(n, k, "bf16", 2).cuda())
+    want = mx4_product(qx, qw)
+    room = torch.full((m * n + 512,), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = room[256:256 + m * n].view(m, n)
+    Z._binding.zero_debug_hold_matrix(stage)
+    mx4_product(qx, qw, out=out)
+    with pytest.raises(Z.ZeroError) as e:
+        Z.zero_matrix_status()
+    assert e.value.code == 4 and "zero_mx4_matmul" in str(e.value)
+    for _ in range(2):
+        mx4_product(qx, qw, out=out)
+    Z.zero_matrix_status()
+    assert torch.equal(out, want)
+    out.fill_(7.0)
+    assert bool((room == 7.0).all())

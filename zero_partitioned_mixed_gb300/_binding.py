@@ -27,7 +27,7 @@ EXPORTS = (
     "zero_noalloc_scratch_bytes", "zero_set_persistent", "zero_reduce_scatter_gather_bucket",
     "zero_muon_set_state", "zero_muon_get_state", "zero_muon_momentum", "zero_muon_apply",
     "zero_orthogonalize", "zero_muon_orthogonalize", "zero_orthogonalize_workspace_bytes", "zero_mx4_codes_bytes", "zero_mx4_scales_bytes",
-    "zero_mx4_quantize", "zero_mx4_dequantize", "zero_mx4_matmul", "zero_matrix_status",
+    "zero_mx4_quantize", "zero_mx4_dequantize", "zero_mx4_matmul", "zero_matrix_status", "zero_debug_hold_matrix",
 )
 ZERO_Q_BLOCK = 256
 ZERO_MX_BLOCK = 32
@@ -132,6 +132,7 @@ def load_library():
     lib.zero_mx4_dequantize.argtypes = [I32, U64, U64, P, P, P, U64, P]
     lib.zero_mx4_matmul.argtypes = [I32, U64, U64, U64, P, P, P, P, P, U64, P]
     lib.zero_matrix_status.argtypes = [P]
+    lib.zero_debug_hold_matrix.argtypes = [C.c_int64]
     lib.zero_orthogonalize_workspace_bytes.argtypes = [I32, U64, U64]
     lib.zero_mx4_codes_bytes.argtypes = lib.zero_mx4_scales_bytes.argtypes = [U64, U64]
     sizes = ("zero_orthogonalize_workspace_bytes", "zero_mx4_codes_bytes", "zero_mx4_scales_bytes")
@@ -436,6 +437,10 @@ def zero_mx4_matmul(dtype: int, m: int, n: int, k: int, a_codes, a_scales, b_cod
 def zero_matrix_status(stream=None) -> None:
     """Raises ZeroError (ZERO_ETIMEOUT) when a matrix kernel's bounded wait gave up since the last call."""
     _check(load_library().zero_matrix_status(_stream(stream)), None)
+
+
+def zero_debug_hold_matrix(stage: int) -> None:
+    _check(load_library().zero_debug_hold_matrix(int(stage)), None)
 
 
 def zero_last_error(h) -> str:

@@ -24,4 +24,9 @@ inline bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uint
 inline uint64_t up(uint64_t x, uint64_t to) { return (x + to - 1) / to * to; }
 
 }  // namespace
+
+// The stage at which block 0 of the next matrix kernel holds, counted from 1,
+// or 0; takes it (zero_debug_hold_matrix).
+uint32_t take_matrix_hold();
+
 }  // namespace zg

@@ -16,6 +16,7 @@
 // 4 (r / 32) + b.  That is what the tensor cores take: a tile is copied into
 // tensor memory as it stands.  The tiles' unused bytes are 0.
 
+#include <atomic>
 #include <cstdint>
 #include <string>
 
@@ -329,6 +330,7 @@ struct MxProductArgs {
     void* out;
     uint64_t ld;
     int vec;                 // rows of out start on 16 bytes
+    uint32_t hold;           // zero_debug_hold_matrix, or 0
 };
 
 constexpr int kMxN = 192, kMxK = 256;   // a stage's values of k are 128 bytes of a row
@@ -419,7 +421,8 @@ k_mx4_product(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
             mx_tile(p, t, tm, tn);
             const int ra = static_cast<int>(tm * T::kRows), rb = static_cast<int>(tn * kMxN);
             for (uint32_t kb = 0; kb < nk; ++kb, r.next(), ++fills) {
-                if (!bar_wait(empty + 8 * r.s, r.parity ^ 1, quit, kForSpace)) {   // passes at once in the first round
+                if (!bar_wait(empty + 8 * r.s, r.parity ^ 1, quit, kForSpace) ||   // passes at once in the first round
+                    (blockIdx.x == 0 && fills + 1 == p.hold)) {
                     ok = false;
                     break;
                 }
@@ -551,6 +554,7 @@ struct MxNarrowArgs {
     uint32_t split;             // CTAs a cluster
     void* out;
     uint64_t ld;
+    uint32_t hold;              // zero_debug_hold_matrix, or 0
 };
 
 constexpr int kNarrowThreads = 192, kNarrowStages = 3;
@@ -598,7 +602,7 @@ k_mx4_narrow(const __grid_constant__ CUtensorMap map_b, const __grid_constant__ 
         Ring<kNarrowStages> r;
         uint32_t kb = k0;
         for (; kb < k1; ++kb, r.next()) {
-            if (!bar_wait(empty + 8 * r.s, r.parity ^ 1, quit, kForSpace)) break;
+            if (!bar_wait(empty + 8 * r.s, r.parity ^ 1, quit, kForSpace) || (blockIdx.x == 0 && kb + 1 == p.hold)) break;
             const uint32_t bar = full + 8 * r.s, st = ring + r.s * L::kStage;
             bar_expect(bar, L::kStage);
             copy_box(st, &map_b, static_cast<int>(kb * 128), static_cast<int>(tile * 128), 0, bar);
@@ -734,6 +738,7 @@ cudaError_t narrow_of(int dtype, uint64_t m, uint64_t n, uint64_t k, const void*
     p.n = static_cast<uint32_t>(n);
     p.tiles_k = static_cast<uint32_t>(up(k, 128) / 128);
     p.stages = static_cast<uint32_t>(up(k, kMxK) / kMxK);
+    p.hold = take_matrix_hold();
     p.out = out;
     p.ld = ld;
     const uint64_t tiles = up(n, 128) / 128;
@@ -750,6 +755,9 @@ cudaError_t narrow_of(int dtype, uint64_t m, uint64_t n, uint64_t k, const void*
 }
 
 }  // namespace
+
+static std::atomic<uint32_t> g_matrix_hold{0};
+uint32_t take_matrix_hold() { return g_matrix_hold.exchange(0); }
 
 cudaError_t mx4_gave_up(cudaStream_t s, int32_t* out) { return read_gave_up(s, out); }
 cudaError_t ortho_gave_up(cudaStream_t s, int32_t* out);   // zero_ortho.cu
@@ -870,6 +878,7 @@ int zero_mx4_matmul(int dtype, uint64_t m, uint64_t n, uint64_t k, const void* a
     p.out = out16;
     p.ld = ld;
     p.vec = aligned(out16, 16) && ld % 8 == 0;
+    p.hold = take_matrix_hold();
     CUtensorMap ma, mb, sa, sb;
     if ((e = mx_maps(&ma, &sa, a_codes, a_scales, m, k, static_cast<uint32_t>(rows), tall ? 2 : 1)) != cudaSuccess ||
         (e = mx_maps(&mb, &sb, b_codes, b_scales, n, k, kMxN, 2)) != cudaSuccess)
@@ -888,6 +897,11 @@ int zero_mx4_matmul(int dtype, uint64_t m, uint64_t n, uint64_t k, const void* a
             e = launch_pdl(fp16 ? k_mx4_product<kFp16, 1> : k_mx4_product<kBf16, 1>, grid, kMxThreads, smem, 1, s, ma, mb, sa, sb, p);
     }
     return e == cudaSuccess ? ZERO_OK : cuda_refuse(e, "zero_mx4_matmul");
+}
+
+int zero_debug_hold_matrix(int64_t stage) {
+    g_matrix_hold = stage < 0 || stage >= 0xFFFFFFFFll ? 0u : static_cast<uint32_t>(stage) + 1u;
+    return ZERO_OK;
 }
 
 int zero_matrix_status(void* stream) {

@@ -265,6 +265,7 @@ struct ProductArgs {
     int32_t* pending;          // of the step's state, or NULL
     int32_t dst_vec;           // every row of dst starts on 16 bytes
     uint32_t n_phases, batch;
+    uint32_t hold;             // zero_debug_hold_matrix, or 0
 };
 
 // A pair of CTAs computes 256 x 256 tiles: a stage of 64 steps of the
@@ -365,6 +366,7 @@ __global__ void __launch_bounds__(kProductThreads) k_ortho_products(const __grid
     if (warp == 0 && elect_one()) {
         const uint32_t leader_full = cluster_addr(full, 0);
         Ring<kStages> r;
+        uint32_t fills = 0;
         bool ok = true;
         Walk w(p);
         for (bool more = w.find(); more && ok; more = w.next()) {
@@ -377,7 +379,8 @@ __global__ void __launch_bounds__(kProductThreads) k_ortho_products(const __grid
             const int rb = static_cast<int>(w.tn * kTile + rank * kHalf), z = static_cast<int>(w.b);
             const bool a_mn = f.a_mn, b_mn = f.b_mn;
             for (uint32_t kb = 0; kb < nk; ++kb, r.next()) {
-                if (!bar_wait(empty + 8 * r.s, r.parity ^ 1, quit, kForSpace)) {   // passes at once in the first round
+                if (!bar_wait(empty + 8 * r.s, r.parity ^ 1, quit, kForSpace) ||   // passes at once in the first round
+                    (blockIdx.x == 0 && ++fills == p.hold)) {
                     ok = false;
                     break;
                 }
@@ -612,6 +615,7 @@ struct SmallArgs {
     uint32_t side, span;     // the shorter and the longer side
     uint32_t ctas, per;      // CTAs a matrix, 64s of the longer side a CTA
     int32_t tall, steps;
+    uint32_t hold;           // zero_debug_hold_matrix, or 0
     int32_t* pending;        // of the step's state, or NULL
     float scale;
     float coeffs[3 * ZERO_MAX_NS_STEPS];
@@ -750,6 +754,10 @@ __global__ void __launch_bounds__(kSmallThreads) k_ortho_small(const __grid_cons
         __syncthreads();
         tc_fence_after();
     };
+    uint32_t signals = 0;
+    auto signal = [&]() {   // from the thread that issued the products
+        if (blockIdx.x != 0 || ++signals != p.hold) tc_commit(bar);
+    };
     auto finish = [&]() {
         bar_wait(bar, parity, quit);
         parity ^= 1;
@@ -805,7 +813,7 @@ __global__ void __launch_bounds__(kSmallThreads) k_ortho_small(const __grid_cons
                 const uint64_t d = d0 + (tall ? k * (2048 >> 4) : (k >> 2) * (kBlockBytes >> 4) + (k & 3) * 2);
                 mma_f16(tmem, d, d, idesc, k > 0);
             }
-            tc_commit(bar);
+            signal();
         }
         finish();
         if (p.ctas == 1) return;
@@ -863,7 +871,7 @@ __global__ void __launch_bounds__(kSmallThreads) k_ortho_small(const __grid_cons
                         mma_f16(tmem + n0 * 64, square, dx + n0 * (kBlockBytes >> 4) + k * (2048 >> 4), idesc, k > 0);
                 }
             }
-            tc_commit(bar);
+            signal();
         }
         finish();
 #pragma unroll 1
@@ -912,7 +920,7 @@ __global__ void __launch_bounds__(kSmallThreads) k_ortho_small(const __grid_cons
                         const uint32_t at = (s >> 2) * (kBlockBytes >> 4) + (s & 3) * 2;
                         mma_f16(tmem, da + at, dc + at, kIdesc128, s > 0);
                     }
-                    tc_commit(bar);
+                    signal();
                 }
                 finish();
             }
@@ -1155,6 +1163,7 @@ int orthogonalize(int dtype, int batch, uint64_t rows, uint64_t cols, const void
         m.tall = tall;
         m.steps = steps;
         m.scale = scale;
+        m.hold = take_matrix_hold();
         m.pending = pending;
         for (int i = 0; i < 3 * steps; ++i) m.coeffs[i] = coeffs ? coeffs[i] : kDefaultCoeffs[i % 3];
         size_t smem = 1024 + 3 * kSquareBytes + static_cast<size_t>(m.per) * kSlabUnit;
@@ -1211,6 +1220,7 @@ int orthogonalize(int dtype, int batch, uint64_t rows, uint64_t cols, const void
     }
     p.g0 = q.g0;
     p.done = q.done;
+    p.hold = take_matrix_hold();
     p.pending = pending;
     p.batch = nb;
     uint32_t most = 0;   // tiles of the largest phase
