@@ -549,3 +549,78 @@ def test_a_step_whose_orthogonalisation_gave_up_is_skipped(shape):
     sa, sb = a.status(), b.status()
     assert torch.equal(a.live_momentum(sa["slot"]), b.live_momentum(sb["slot"]))
     assert sb["steps_skipped"] == 1 and sa["steps_applied"] == sb["steps_applied"] == 2
+
+
+# ------------------- shorter sides above 128: the products through global memory, at what the tests above hold at small sizes
+# Bounds as above; the 64-bit model of the rounding points gives 1.7e-3 to 1.9e-3 for the step counts here and 9.8e-3
+# for the matrices of rank one.
+@pytest.mark.parametrize("batch", [1, 5, 128])
+def test_large_batches_are_independent(batch):
+    g = gradient(172, 204, batch, batch=batch).bfloat16().cuda()
+    got = ortho(g)
+    for i in {0, batch // 2, batch - 1}:
+        assert torch.equal(got[i:i + 1], ortho(g[i:i + 1].clone()))
+
+
+@pytest.mark.parametrize("steps", [1, 2, 3, 8, 32])
+@pytest.mark.parametrize("rows,cols", [(150, 290), (290, 150), (260, 520)])
+def test_large_steps_coefficients_and_scale(steps, rows, cols):
+    g = gradient(rows, cols, steps).bfloat16()
+    coeffs = [DEFAULT, (3.0, -3.2, 1.2), (1.875, -1.25, 0.375), (1.5, -0.5, 0.0)]
+    coeffs = (coeffs * 8)[:steps]
+    got = ortho(g.cuda(), steps=steps, coeffs=coeffs, scale=-0.37)
+    assert rel(got[0], newton_schulz(g[0].double(), steps, coeffs, -0.37)) <= 5e-3
+
+
+@pytest.mark.parametrize("dtype,factor", [("bf16", 2.0 ** 100), ("bf16", 2.0 ** 67), ("bf16", 2.0 ** -100),
+                                          ("bf16", 2.0 ** -60), ("fp16", 2.0 ** 13)])
+def test_scale_of_a_large_input_does_not_matter(dtype, factor):
+    g = (1e3 * gradient(180, 212, 5)).to(TD[dtype]).cuda()
+    far = (g.double() * factor).to(TD[dtype])
+    assert torch.equal(far.double(), g.double() * factor)
+    assert torch.equal(ortho(far), ortho(g))
+
+
+@pytest.mark.parametrize("rows,cols", [(170, 290), (290, 170)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_zero_infinity_and_nan_stay_in_their_large_matrix(rows, cols, dtype):
+    g = (100 * gradient(rows, cols, 3, batch=6)).to(TD[dtype]).cuda()
+    clean = ortho(g.clone())
+    g[1] = 0
+    g[2, rows - 1, cols - 1] = float("inf")
+    g[3, 0, 0] = float("nan")
+    g[4, rows // 2, 7] = -float("inf")
+    got = ortho(g)
+    assert torch.equal(got[0], clean[0]) and torch.equal(got[5], clean[5])
+    assert not got[1].any()
+    assert all(torch.isnan(got[i]).all() for i in (2, 3, 4))
+
+
+@pytest.mark.parametrize("rows,cols", [(160, 300), (300, 160)])
+def test_large_rank_one_and_zero_rows(rows, cols):
+    u, v = (torch.randn(*s, generator=torch.Generator().manual_seed(k)) for s, k in (((rows, 1), 1), ((1, cols), 2)))
+    g = (u @ v)[None].bfloat16()
+    g[0, 7] = 0
+    got = ortho(g.cuda())
+    assert not got[0, 7].any()
+    assert rel(got[0], newton_schulz(g[0].double())) <= 2.5e-2
+
+
+@pytest.mark.parametrize("rows,cols", [(165, 297), (297, 165)])
+@pytest.mark.parametrize("offset,pad", [(0, 7), (1, 0), (3, 34), (8, 3), (0, 23)])
+def test_large_strides_alignment_and_guard_bands(rows, cols, offset, pad):
+    ld, batch = cols + pad, 3
+    g = gradient(rows, cols, 11, batch=batch).bfloat16().cuda()
+    want = ortho(g)
+    room = offset + rows * ld + 64
+    src = torch.full((batch, room), float("nan"), dtype=torch.bfloat16, device="cuda")
+    dst = torch.full((batch, room), 5.0, dtype=torch.bfloat16, device="cuda")
+    view = lambda t, i: t[i, offset:offset + rows * ld].view(rows, ld)[:, :cols]   # noqa: E731
+    for i in range(batch):
+        view(src, i).copy_(g[i])
+    Z.zero_orthogonalize(Z.ZERO_BF16, rows, cols, [view(src, i) for i in range(batch)],
+                         [view(dst, i) for i in range(batch)], workspace(batch, rows, cols), ld_src=ld, ld_dst=ld)
+    for i in range(batch):
+        assert torch.equal(view(dst, i), want[i])
+        view(dst, i).fill_(5.0)
+    assert bool((dst == 5.0).all())
