@@ -623,13 +623,13 @@ ZERO_API int zero_matrix_status(void* stream);
  * zero_debug_hold_matrix -- test hook for the failure path of the matrix
  * kernels.  In the next zero_orthogonalize, zero_muon_orthogonalize or
  * zero_mx4_matmul of the process that launches a kernel with bounded waits
- * (one-shot), block 0 stops issuing its copies at its stage `stage` (stages
- * counted from 0 over its tiles); in the orthogonalisation of short sides it
- * leaves out the signal that its product `stage` is done.  The waits for
- * them run out (about 2 s).  No access leaves its buffers and every wait
- * ends.  The call's output is incomplete, and zero_matrix_status returns
- * ZERO_ETIMEOUT once.  stage < 0 clears a pending hold; one past block 0's
- * last has no effect.  Returns ZERO_OK.
+ * (one-shot), the barrier for stage `stage` of block 0's ring expects an
+ * arrival that never comes (in the orthogonalisation of short sides every
+ * block's barrier for its products, whatever the stage), so that the waits for it
+ * run out (about 2 s).  No access leaves its buffers and every wait ends.
+ * The call's output is incomplete, and zero_matrix_status returns
+ * ZERO_ETIMEOUT once.  stage < 0 clears a pending hold; one that block 0
+ * does not use has no effect.  Returns ZERO_OK.
  */
 ZERO_API int zero_debug_hold_matrix(int64_t stage);
 

@@ -25,8 +25,8 @@ inline uint64_t up(uint64_t x, uint64_t to) { return (x + to - 1) / to * to; }
 
 }  // namespace
 
-// The stage at which block 0 of the next matrix kernel holds, counted from 1,
-// or 0; takes it (zero_debug_hold_matrix).
+// The ring stage whose barrier block 0 of the next matrix kernel is to wait for
+// in vain, counted from 1, or 0; takes it (zero_debug_hold_matrix).
 uint32_t take_matrix_hold();
 
 }  // namespace zg

@@ -395,7 +395,8 @@ k_mx4_product(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
                    last = freed + 16;
     if (threadIdx.x == 0) {
         s_quit = 0;
-        for (uint32_t i = 0; i < 2 * kStages + 2; ++i) bar_init(full + 8 * i, 1);
+        const uint32_t held = blockIdx.x == 0 ? p.hold : 0;
+        for (uint32_t i = 0; i < 2 * kStages + 2; ++i) bar_init(full + 8 * i, i < kStages && i + 1 == held ? 2 : 1);
         for (uint32_t i = 0; i < 2; ++i) bar_init(freed + 8 * i, kMxOutWarps);
         bar_init(last, 1);
         bar_init_fence();
@@ -421,8 +422,7 @@ k_mx4_product(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
             mx_tile(p, t, tm, tn);
             const int ra = static_cast<int>(tm * T::kRows), rb = static_cast<int>(tn * kMxN);
             for (uint32_t kb = 0; kb < nk; ++kb, r.next(), ++fills) {
-                if (!bar_wait(empty + 8 * r.s, r.parity ^ 1, quit, kForSpace) ||   // passes at once in the first round
-                    (blockIdx.x == 0 && fills + 1 == p.hold)) {
+                if (!bar_wait(empty + 8 * r.s, r.parity ^ 1, quit, kForSpace)) {   // passes at once in the first round
                     ok = false;
                     break;
                 }
@@ -435,9 +435,11 @@ k_mx4_product(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
                 copy_box(ss + T::kScaleA, &map_sb, 0, static_cast<int>(8 * kb), rb >> 7, bar);
             }
         }
-        if (!ok)   // the block must not leave with copies in flight
+        if (!ok) {   // the block must not leave with copies in flight
+            const uint64_t t0 = now_ns();
             for (uint32_t i = fills > kStages ? fills - kStages : 0; i < fills; ++i)
-                bar_drain(full + 8 * (i % kStages), (i / kStages) & 1);
+                bar_drain(full + 8 * (i % kStages), (i / kStages) & 1, t0);
+        }
     } else if (warp == 1 && elect_one()) {
         // e2m1 operands, power-of-two scales, 128 x 192
         constexpr uint32_t idesc =
@@ -493,7 +495,7 @@ k_mx4_product(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
         }
         if (*quit) {   // tensor memory must not be freed under a product
             tc_commit(last);
-            bar_drain(last, 0);
+            bar_drain(last, 0, now_ns());
         }
     } else if (warp >= 2) {
         const uint32_t quarter = warp & 3, part = (warp - 2) >> 2;   // 32 rows, 96 columns
@@ -586,7 +588,8 @@ k_mx4_narrow(const __grid_constant__ CUtensorMap map_b, const __grid_constant__ 
     const uint32_t k0 = rank * p.stages / p.split, k1 = (rank + 1) * p.stages / p.split;
     if (threadIdx.x == 0) {
         s_quit = 0;
-        for (int i = 0; i < 2 * kNarrowStages + 1; ++i) bar_init(full + 8 * i, 1);
+        const int held = blockIdx.x == 0 ? static_cast<int>(p.hold) : 0;
+        for (int i = 0; i < 2 * kNarrowStages + 1; ++i) bar_init(full + 8 * i, i < kNarrowStages && i + 1 == held ? 2 : 1);
         bar_init_fence();
         prefetch_map(&map_b);
         prefetch_map(&map_a);
@@ -602,7 +605,7 @@ k_mx4_narrow(const __grid_constant__ CUtensorMap map_b, const __grid_constant__ 
         Ring<kNarrowStages> r;
         uint32_t kb = k0;
         for (; kb < k1; ++kb, r.next()) {
-            if (!bar_wait(empty + 8 * r.s, r.parity ^ 1, quit, kForSpace) || (blockIdx.x == 0 && kb + 1 == p.hold)) break;
+            if (!bar_wait(empty + 8 * r.s, r.parity ^ 1, quit, kForSpace)) break;
             const uint32_t bar = full + 8 * r.s, st = ring + r.s * L::kStage;
             bar_expect(bar, L::kStage);
             copy_box(st, &map_b, static_cast<int>(kb * 128), static_cast<int>(tile * 128), 0, bar);
@@ -639,7 +642,7 @@ k_mx4_narrow(const __grid_constant__ CUtensorMap map_b, const __grid_constant__ 
             tc_commit(empty + 8 * r.s);
         }
         tc_commit(done);
-        if (!ok) bar_drain(done, 0);
+        if (!ok) bar_drain(done, 0, now_ns());
     } else if (warp >= 2) {
         // partial sums [column][128 rows] where the ring was
         const bool ok = bar_wait(done, 0, quit);
@@ -900,7 +903,7 @@ int zero_mx4_matmul(int dtype, uint64_t m, uint64_t n, uint64_t k, const void* a
 }
 
 int zero_debug_hold_matrix(int64_t stage) {
-    g_matrix_hold = stage < 0 || stage >= 0xFFFFFFFFll ? 0u : static_cast<uint32_t>(stage) + 1u;
+    g_matrix_hold = stage < 0 || stage >= 0x7FFFFFFF ? 0u : static_cast<uint32_t>(stage) + 1u;
     return ZERO_OK;
 }
 

@@ -339,8 +339,9 @@ __global__ void __launch_bounds__(kProductThreads) k_ortho_products(const __grid
                    lin0 = freed + 16;
     if (threadIdx.x == 0) {
         s_quit = 0;
+        const int held = blockIdx.x == 0 ? static_cast<int>(p.hold) : 0;
         for (int i = 0; i < kStages; ++i) {
-            bar_init(full + 8 * i, 1);
+            bar_init(full + 8 * i, i + 1 == held ? 2 : 1);
             bar_init(empty + 8 * i, 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -366,7 +367,6 @@ __global__ void __launch_bounds__(kProductThreads) k_ortho_products(const __grid
     if (warp == 0 && elect_one()) {
         const uint32_t leader_full = cluster_addr(full, 0);
         Ring<kStages> r;
-        uint32_t fills = 0;
         bool ok = true;
         Walk w(p);
         for (bool more = w.find(); more && ok; more = w.next()) {
@@ -379,8 +379,7 @@ __global__ void __launch_bounds__(kProductThreads) k_ortho_products(const __grid
             const int rb = static_cast<int>(w.tn * kTile + rank * kHalf), z = static_cast<int>(w.b);
             const bool a_mn = f.a_mn, b_mn = f.b_mn;
             for (uint32_t kb = 0; kb < nk; ++kb, r.next()) {
-                if (!bar_wait(empty + 8 * r.s, r.parity ^ 1, quit, kForSpace) ||   // passes at once in the first round
-                    (blockIdx.x == 0 && ++fills == p.hold)) {
+                if (!bar_wait(empty + 8 * r.s, r.parity ^ 1, quit, kForSpace)) {   // passes at once in the first round
                     ok = false;
                     break;
                 }
@@ -433,7 +432,7 @@ __global__ void __launch_bounds__(kProductThreads) k_ortho_products(const __grid
         }
         if (*quit) {   // tensor memory must not be freed under a product
             tc_commit_pair(smem_u32(&s_last));
-            bar_drain(smem_u32(&s_last), 0);
+            bar_drain(smem_u32(&s_last), 0, now_ns());
         }
     } else if (warp >= 2) {
         const uint32_t quarter = warp & 3;   // the lanes of tensor memory that this warp can read
@@ -615,7 +614,7 @@ struct SmallArgs {
     uint32_t side, span;     // the shorter and the longer side
     uint32_t ctas, per;      // CTAs a matrix, 64s of the longer side a CTA
     int32_t tall, steps;
-    uint32_t hold;           // zero_debug_hold_matrix, or 0
+    uint32_t arrivals;       // that a product's end takes: 1, or with zero_debug_hold_matrix one more, which never comes
     int32_t* pending;        // of the step's state, or NULL
     float scale;
     float coeffs[3 * ZERO_MAX_NS_STEPS];
@@ -657,7 +656,7 @@ __global__ void __launch_bounds__(kSmallThreads) k_ortho_small(const __grid_cons
     const uint32_t bar = smem_u32(&s_bar);
     if (tid == 0) {
         s_quit = 0;
-        bar_init(bar, 1);
+        bar_init(bar, p.arrivals);
         bar_init_fence();
     }
     if (warp == 0) tmem_alloc(smem_u32(&s_tmem), 512);
@@ -754,10 +753,6 @@ __global__ void __launch_bounds__(kSmallThreads) k_ortho_small(const __grid_cons
         __syncthreads();
         tc_fence_after();
     };
-    uint32_t signals = 0;
-    auto signal = [&]() {   // from the thread that issued the products
-        if (blockIdx.x != 0 || ++signals != p.hold) tc_commit(bar);
-    };
     auto finish = [&]() {
         bar_wait(bar, parity, quit);
         parity ^= 1;
@@ -813,7 +808,7 @@ __global__ void __launch_bounds__(kSmallThreads) k_ortho_small(const __grid_cons
                 const uint64_t d = d0 + (tall ? k * (2048 >> 4) : (k >> 2) * (kBlockBytes >> 4) + (k & 3) * 2);
                 mma_f16(tmem, d, d, idesc, k > 0);
             }
-            signal();
+            tc_commit(bar);
         }
         finish();
         if (p.ctas == 1) return;
@@ -871,7 +866,7 @@ __global__ void __launch_bounds__(kSmallThreads) k_ortho_small(const __grid_cons
                         mma_f16(tmem + n0 * 64, square, dx + n0 * (kBlockBytes >> 4) + k * (2048 >> 4), idesc, k > 0);
                 }
             }
-            signal();
+            tc_commit(bar);
         }
         finish();
 #pragma unroll 1
@@ -920,7 +915,7 @@ __global__ void __launch_bounds__(kSmallThreads) k_ortho_small(const __grid_cons
                         const uint32_t at = (s >> 2) * (kBlockBytes >> 4) + (s & 3) * 2;
                         mma_f16(tmem, da + at, dc + at, kIdesc128, s > 0);
                     }
-                    signal();
+                    tc_commit(bar);
                 }
                 finish();
             }
@@ -1163,7 +1158,7 @@ int orthogonalize(int dtype, int batch, uint64_t rows, uint64_t cols, const void
         m.tall = tall;
         m.steps = steps;
         m.scale = scale;
-        m.hold = take_matrix_hold();
+        m.arrivals = take_matrix_hold() ? 2 : 1;
         m.pending = pending;
         for (int i = 0; i < 3 * steps; ++i) m.coeffs[i] = coeffs ? coeffs[i] : kDefaultCoeffs[i % 3];
         size_t smem = 1024 + 3 * kSquareBytes + static_cast<size_t>(m.per) * kSlabUnit;

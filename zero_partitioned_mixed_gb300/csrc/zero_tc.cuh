@@ -140,10 +140,9 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile
         }
     }
 }
-// The same without regard to `quit`: for the copies and products that a
-// block still has in flight when it gives up.
-__device__ __forceinline__ void bar_drain(uint32_t bar, uint32_t parity) {
-    const uint64_t t0 = now_ns();
+// The same without regard to `quit`, until kGiveUpNs after t0: for the copies
+// and products that a block still has in flight when it gives up.
+__device__ __forceinline__ void bar_drain(uint32_t bar, uint32_t parity, uint64_t t0) {
     while (!bar_test(bar, parity) && now_ns() - t0 < kGiveUpNs) {}
 }
 // In every thread, after a barrier of the block behind which nobody waits any
