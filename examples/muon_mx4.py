@@ -1,8 +1,8 @@
 """Two linear layers trained on N simulated ranks with orthogonalised momentum,
-their weights exchanged and multiplied in microscaled 4 bits.
+their weights multiplied in microscaled 4 bits.
 
-Every step, every rank multiplies its own tokens with the gathered 4-bit
-weights (forward and backward), and the ranks' 16-bit gradients go through
+Every step, every rank multiplies its own tokens with the 4-bit weights
+(forward and backward), and the ranks' 16-bit gradients go through
 one Muon step: average, momentum, Newton-Schulz, update of the fp32 master
 and of every rank's replica, from which the weights are quantised again.
 

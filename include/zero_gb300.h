@@ -545,8 +545,10 @@ ZERO_API int zero_muon_apply(int dtype, int n_ranks, uint64_t count, const void*
  * accumulate in fp32.  The coefficients must keep the singular values of
  * every X below 3 and those of a I + b A + c A^2 (and of the first two
  * steps' product of it) below 500, or fp16 overflows and the result is not
- * finite.  Against 64 bits the result is off by about 2e-3 of its 2-norm,
- * most of it the rounding to bf16; more where the shorter side is below 16.
+ * finite (the calls do not check that).  Against 64 bits the result is off
+ * by about 2e-3 of its 2-norm, most of it the rounding to bf16 (1.7e-3); by
+ * up to 3.3e-3 where the shorter side is 16 to 48, and below 16 by 2e-3 to
+ * 5e-3 in the mean and up to 2e-2 for single matrices.
  * For a shorter side above 128 (or a longer one above 8192) the products run
  * as one cooperative launch that takes the whole GPU.
  * Errors: EINVAL, ECUDA; see zero_matrix_status for a wait that gave up.
@@ -571,10 +573,11 @@ ZERO_API int zero_muon_orthogonalize(int dtype, int batch, uint64_t rows, uint64
 ZERO_API uint64_t zero_orthogonalize_workspace_bytes(int batch, uint64_t rows, uint64_t cols);
 
 /*
- * Microscaled 4-bit floats (the OCP MX format with e2m1 elements): an
- * exchange in a quarter of 16 bits whose codes the tensor cores multiply as
- * they are, next to the zero-point formats of zero_quantize_blocks, which
- * must be dequantized first.
+ * Microscaled 4-bit floats (the OCP MX format with e2m1 elements): a form of
+ * a quarter of 16 bits whose codes the tensor cores multiply as they are, next
+ * to the zero-point formats of zero_quantize_blocks, which must be dequantized
+ * first.  These calls quantize, read back and multiply; none moves codes
+ * between ranks, as zero_gather_bucket_q8 does for INT8.
  * A block is ZERO_MX_BLOCK consecutive values of a row.  Its scale is
  * 2^(floor(log2(largest magnitude)) - 2), not below 2^-127, one byte with a
  * bias of 127; a value's code is x / scale rounded to the nearest of +-{0,

@@ -8,8 +8,8 @@
 //
 // Both are bound by HBM: 2N + 10 and 10 + 2N bytes an element, every byte
 // touched once.  Measured: the 84,934,656 elements of GPT-2 small's hidden
-// matrices on 8 ranks take the momentum 307 us (7.2 TB/s, mostly reads), a
-// Llama-7B layer's 202,375,168 on 8 ranks take apply 789 us (6.7 TB/s); a
+// matrices on 8 ranks take the momentum 308 us (7.2 TB/s, mostly reads), a
+// Llama-7B layer's 202,375,168 on 8 ranks take apply 780 us (6.7 TB/s); a
 // plain copy moves 6.8 TB/s.  A thread moves 8 elements (256-bit fp32 accesses where the
 // buffers allow), with the loads of up to 8 ranks in flight together, as
 // the AdamW step's kernels do.  The grid is not persistent: a block handles

@@ -72,9 +72,9 @@ __device__ __forceinline__ uint32_t codes8(const float (&x)[8]) {
 // rows' loads in flight together.  They are bound by the instructions they
 // issue as much as by HBM, so a piece that lies inside the matrix and starts
 // on 16 bytes takes a path without any of the edges' cases (`INSIDE`): for
-// 11008 x 4096 bf16 21 us to quantise (5.4 TB/s) and 23 us to read back (4.9
-// TB/s) against 28 and 28 with one path for all.  Rows at odd strides: 9.8
-// and 9.0 us for 2047 x 5003 against 6.8 and 7.3 for 2048 x 5000.
+// 11008 x 4096 bf16 20 us to quantise (5.7 TB/s) and 23 us to read back (5.0
+// TB/s) against 28 and 28 with one path for all.  Rows at odd strides: 8.2
+// and 7.8 us for 2047 x 5003 against 7.4 and 5.9 for 2048 x 5000.
 constexpr int kMxRows = 4;
 
 template <int DT, bool INSIDE>
@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kThreads) k_mx4_rows(const __grid_constant__ M
 // Along the columns: the codes are those of the transpose.  A block takes
 // 128 rows (a scale tile's four blocks) of 128 columns, a thread 32 values
 // of two neighbouring columns; the codes go through shared memory so that a
-// row of them leaves as 64 neighbouring bytes.  11008 x 4096: 19.5 us (5.9
+// row of them leaves as 64 neighbouring bytes.  11008 x 4096: 18.6 us (6.1
 // TB/s; one column a thread and codes straight from registers took 33).
 template <int DT>
 __global__ void __launch_bounds__(kThreads) k_mx4_columns(const __grid_constant__ MxArgs a) {
@@ -543,9 +543,9 @@ k_mx4_product(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
 }
 
 // ------------------------------------------------- product with few rows
-// Up to 32 rows of A (a token, a handful): bound by reading B once, 6.4 us for
-// a row against 4096 x 11008 (3.7 TB/s; above 32 rows the tiles of 128 are
-// faster, 8.5 us up to 256 rows).  B's rows are the tensor cores' 128 rows and A's the columns (NT of
+// Up to 32 rows of A (a token, a handful): bound by reading B once, 5.7 us for
+// a row against 4096 x 11008 (4.2 TB/s) and 6.6 for 32 (above 32 rows the tiles
+// of 128 are faster: 8.0 us for 33 rows, 9.8 for 256).  B's rows are the tensor cores' 128 rows and A's the columns (NT of
 // them), a CTA takes 128 of B's rows over a share of k, and the CTAs of a
 // cluster add up their shares through shared memory, in order of rank.  The
 // shares are chosen so that about two CTAs an SM have their copies in flight

@@ -13,7 +13,11 @@
 // p(A_1) B, and X_2 = Q X_0.  Against 64 bits a result before its rounding to
 // bf16 is off by 1.0e-3 to 1.9e-3 (2-norm; gradients of low rank over noise,
 // 64 x 64 to 768 x 2048), about what that rounding costs (1.7e-3); rounding
-// every X gives up to 3.2e-3, and bf16 throughout 1e-2 to 2.5e-2.
+// every X gives up to 3.2e-3, and bf16 throughout 1e-2 to 2.5e-2.  That is the
+// price against intermediates of 32 bits, which would leave the 1.7e-3 alone:
+// with the rounding, measured on 6 to 24 matrices a size, 1.9e-3 to 2.2e-3 for
+// shorter sides from 64 up, up to 3.3e-3 for 16 to 48, and below 16, where few
+// values average, 2e-3 to 5e-3 in the mean and single matrices up to 2e-2.
 //
 // Work.  All products but the last of a step are symmetric: only tiles on or
 // below the diagonal are computed, and each is written twice.  With the
@@ -24,7 +28,7 @@
 // is multiplied from the right, a wide one the other way around.
 //
 // Two kernels by size.  A shorter side of at most 128 (and a longer one of at
-// most 8192) stays on chip: k_ortho_small, one launch, 23 us for 96 x 160.
+// most 8192) stays on chip: k_ortho_small, one launch, 21 us for 96 x 160.
 // Anything else goes through global memory (in practice L2): two streams that
 // scale and pack G, then k_ortho_products, all products in one cooperative
 // launch.  Measured with five steps: 12 x 768 x 768 186 us, 6 x 1531 x 1003
@@ -588,8 +592,8 @@ __global__ void __launch_bounds__(kProductThreads) k_ortho_products(const __grid
 // products of five steps take about a microsecond each this way; through
 // global memory they took five.
 // Bound by that chain and by the copies in and out, on few SMs.  Five steps of
-// bf16: 96 x 160 23 us, 23 x 1519 30, 128 x 4096 51, 100 x 8192 59, 100
-// matrices of 48 x 300 27, 60 of 100 x 2000 97.
+// bf16: 96 x 160 21 us, 23 x 1519 28, 128 x 4096 49, 100 x 8192 58, 100
+// matrices of 48 x 300 26, 60 of 100 x 2000 97.
 //
 // X lies as the caller has it, in blocks of 64 columns whose rows are 128
 // bytes.  That one layout serves both products: of a wide matrix the blocks

@@ -58,7 +58,12 @@ inline cudaError_t make_map(CUtensorMap* map, int elem, const void* base, uint64
 }
 
 // ---------------------------------------------------------------- barriers
-constexpr uint64_t kGiveUpNs = 2000000000ull;   // every wait ends within about 2 s
+// Waits for an mbarrier or a counter end by themselves after this time.  What
+// has no limit: allocating tensor memory (see tmem_alloc), a cluster's barrier
+// (its blocks run together, and between two barriers each has only waits of
+// the first kind), and the waits for a block's own copies and loads, which
+// the hardware completes.
+constexpr uint64_t kGiveUpNs = 2000000000ull;
 
 // What the first thread whose bounded wait gave up was waiting for (WaitFor);
 // read and cleared by the host's status call.

@@ -89,8 +89,8 @@ class MuonBuffers:
         B.zero_muon_apply(dt, self.count, self.ortho, self.master, self._param_rows, hyp, self.state, stream)
 
     def quantize(self, i: int, transpose: bool = False, rank: int = 0) -> Mx4Matrix:
-        """Matrix i of a rank's replica in microscaled 4 bits: what the others receive in a 4-bit gather,
-        ready to multiply with.  transpose: along its columns, as the backward pass takes it."""
+        """Matrix i of a rank's replica in microscaled 4 bits, ready to multiply with.
+        transpose: along its columns, as the backward pass takes it."""
         return Mx4Matrix.of(self.matrix(i, self.params[rank]), transpose)
 
     def status(self, stream=None) -> dict:

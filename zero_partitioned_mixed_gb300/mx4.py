@@ -1,7 +1,7 @@
 """Matrices in microscaled 4-bit floats, and linear layers on them.
 
-A rank that gathers its parameters in 4 bits multiplies with the codes as
-they arrive; the three products of a layer's training step are one call on
+A rank that holds its parameters in 4 bits multiplies with the codes as they
+are; the three products of a layer's training step are one call on
 operands quantised along the dimension that is summed over.  Everything here
 runs on torch's current stream, where the tensors it makes belong.
 """
