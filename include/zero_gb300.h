@@ -615,8 +615,27 @@ ZERO_API int zero_mx4_dequantize(int dtype, uint64_t rows, uint64_t cols, const 
 ZERO_API int zero_mx4_matmul(int dtype, uint64_t m, uint64_t n, uint64_t k, const void* a_codes, const void* a_scales,
                              const void* b_codes, const void* b_scales, void* out16, uint64_t ld, void* stream);
 
+/*
+ * Microscaled 8-bit floats: the same format with e4m3 elements, for linear
+ * layers that 4 bits are too coarse for.  A block's scale is
+ * 2^(floor(log2(largest magnitude)) - 8), not below 2^-127; a value's code is
+ * x / scale rounded to the nearest e4m3 value (3 bits after the leading one,
+ * down to 2^-9), ties to the even code, those above 448 to 448.  Blocks with
+ * an infinity or a NaN, the scales' layout, alignment, transposition and
+ * products are as for 4 bits; codes are one a byte, rows of ceil(cols/32)*32
+ * bytes with zeros after cols.  Both operands of a product have 8 bits.
+ */
+ZERO_API uint64_t zero_mx8_codes_bytes(uint64_t rows, uint64_t cols);
+ZERO_API uint64_t zero_mx8_scales_bytes(uint64_t rows, uint64_t cols);
+ZERO_API int zero_mx8_quantize(int dtype, uint64_t rows, uint64_t cols, const void* src16, uint64_t ld, int transpose,
+                               void* codes, void* scales, void* stream);
+ZERO_API int zero_mx8_dequantize(int dtype, uint64_t rows, uint64_t cols, const void* codes, const void* scales,
+                                 void* out16, uint64_t ld, void* stream);
+ZERO_API int zero_mx8_matmul(int dtype, uint64_t m, uint64_t n, uint64_t k, const void* a_codes, const void* a_scales,
+                             const void* b_codes, const void* b_scales, void* out16, uint64_t ld, void* stream);
+
 /* Whether a bounded wait inside a kernel of zero_orthogonalize (or
- * zero_muon_orthogonalize) or zero_mx4_matmul has given up on this device
+ * zero_muon_orthogonalize), zero_mx4_matmul or zero_mx8_matmul has given up on this device
  * since the last call: ZERO_OK or ZERO_ETIMEOUT (that kernel's output is
  * incomplete).  Synchronises the stream.  The answer is the device's, for
  * all streams and callers together, and the first to ask gets it. */
@@ -624,8 +643,8 @@ ZERO_API int zero_matrix_status(void* stream);
 
 /*
  * zero_debug_hold_matrix -- test hook for the failure path of the matrix
- * kernels.  In the next zero_orthogonalize, zero_muon_orthogonalize or
- * zero_mx4_matmul of the process that launches a kernel with bounded waits
+ * kernels.  In the next zero_orthogonalize, zero_muon_orthogonalize,
+ * zero_mx4_matmul or zero_mx8_matmul of the process that launches a kernel with bounded waits
  * (one-shot), the barrier for stage `stage` of block 0's ring expects an
  * arrival that never comes (in the orthogonalisation of short sides every
  * block's barrier for its products, whatever the stage), so that the waits for it
@@ -635,6 +654,119 @@ ZERO_API int zero_matrix_status(void* stream);
  * does not use has no effect.  Returns ZERO_OK.
  */
 ZERO_API int zero_debug_hold_matrix(int64_t stage);
+
+/*
+ * The residual stream of a training step: what lies between its linear
+ * layers.  Like the matrix calls these take no handle, allocate nothing and
+ * can be captured into a CUDA graph (after one call of each outside a
+ * capture).  Matrices are row-major with `ld` elements between rows, 2-byte
+ * aligned (faster when rows start on 16 bytes); rows may not share memory.
+ * Results are rounded once to 16 bits and repeat bit for bit.  An empty
+ * matrix is an empty call.  A workspace's contents need not be kept between
+ * calls; calls that share one (replays of captured ones too) must run in
+ * order.  Errors: EINVAL, ECUDA (zero_last_error(NULL)).
+ */
+
+/*
+ * Dropout by a counter-based generator: the numbers are a function of seed,
+ * stream and place, so no mask is stored and the backward pass makes the same
+ * call.  Each element gets 16 bits of Philox4x32-10 (Salmon et al., "Parallel
+ * random numbers: as easy as 1, 2, 3", SC 2011):
+ *   key      seed, low word first
+ *   counter  its low 64 bits row * ceil(cols / 8) + floor(col / 8), its high
+ *            64 bits the stream, offset + (step ? *step : 0)
+ *   bits     of column c: word (c mod 8) / 2, its low half for an even c
+ * With k = p * 65536 rounded to the nearest whole number (at most 65535), an
+ * element is 0 where its bits are below k, whatever it was, and else its
+ * value times 65536 / (65536 - k).  Give every layer and step a stream of its
+ * own.
+ */
+typedef struct {
+    double p;                /* share to drop, in [0, 1) */
+    uint64_t seed, offset;
+    const uint64_t* step;    /* DEVICE memory, 8-byte aligned, or NULL: read when the kernel runs, so that
+                                replays of a captured graph can be given other numbers */
+} zero_dropout_t;
+
+/* out16 = dropout(src16), rows x cols; dropout NULL copies.  out16 may be
+ * src16 when the leading dimensions agree; they may not overlap otherwise. */
+ZERO_API int zero_dropout(int dtype, uint64_t rows, uint64_t cols, const void* src16, uint64_t ld_src, void* out16,
+                          uint64_t ld_out, const zero_dropout_t* dropout, void* stream);
+
+/*
+ * zero_rms_norm -- the stream with a branch added to it, and its
+ * root-mean-square norm:
+ *   h = round16(residual + dropout(x))
+ *   y = h / sqrt(mean over the row of h^2 + eps) * weight
+ *   residual16  or NULL (0);  dropout: or NULL (none)
+ *   weight16    cols values
+ *   h16         h, or NULL
+ *   out16       y in 16 bits, or NULL
+ *   bits        4 or 8: y in that microscaled format, into codes and scales
+ *               (one rounding, from fp32; zero_mx4_matmul and zero_mx8_matmul
+ *               read them), or 0
+ * Something must be written.  The statistics are those of h as it is stored,
+ * in fp32; a row whose sum of squares overflows fp32 gives zeros.  h16 may be
+ * x16 or residual16, and out16 x16 or residual16 (not both the same one),
+ * where the leading dimensions agree; nothing may overlap otherwise.
+ * cols <= ZERO_MAX_NORM_COLS, rows <= 2^30.
+ */
+#define ZERO_MAX_NORM_COLS 16384
+ZERO_API int zero_rms_norm(int dtype, uint64_t rows, uint64_t cols, const void* x16, uint64_t ld_x, const void* residual16,
+                           uint64_t ld_residual, const void* weight16, float eps, const zero_dropout_t* dropout, void* h16,
+                           uint64_t ld_h, void* out16, uint64_t ld_out, int bits, void* codes, void* scales, void* stream);
+
+/*
+ * zero_rms_norm_backward -- with g = dy * weight and r = 1 / sqrt(mean(h^2) + eps):
+ *   dh = r * (g - h * r^2 * mean(g * h)) + dh_in      the residual's gradient
+ *   dx = dropout(dh)                                  the branch's
+ *   dweight = sum over the rows of dy * h * r
+ *   dy16        gradient of y;  h16: the forward call's h
+ *   dh_in16     gradient of h from elsewhere (the stream goes on past the norm), or NULL (0)
+ *   dx16        or NULL;  dweight16: cols values, or NULL
+ *   dropout     the forward call's, or NULL
+ *   workspace   for dweight16 (else NULL): 16-byte aligned, at least
+ *               zero_rms_norm_backward_workspace_bytes(rows, cols) bytes
+ * Any gradient of y through its 4 or 8 bits is that of the 16-bit y.  dh16 and
+ * dx16 may each be dy16 or dh_in16 (not both the same one) where the leading
+ * dimensions agree; nothing may overlap otherwise.  rows = 0 gives a dweight
+ * of zeros.
+ */
+ZERO_API int zero_rms_norm_backward(int dtype, uint64_t rows, uint64_t cols, const void* dy16, uint64_t ld_dy, const void* h16,
+                                    uint64_t ld_h, const void* weight16, float eps, const void* dh_in16, uint64_t ld_in,
+                                    void* dh16, uint64_t ld_dh, const zero_dropout_t* dropout, void* dx16, uint64_t ld_dx,
+                                    void* dweight16, void* workspace, uint64_t workspace_bytes, void* stream);
+
+/* Bytes of that workspace (a host query); 0 for sizes that the call refuses or that are empty. */
+ZERO_API uint64_t zero_rms_norm_backward_workspace_bytes(uint64_t rows, uint64_t cols);
+
+/*
+ * zero_embedding -- out16[t] = scale * table16[ids[t]], tokens x dim from a
+ * vocab x dim table.  ids: device array of id_bytes (4 or 8) each, signed; one
+ * outside [0, vocab) is padding and gives a row of zeros.
+ * vocab 1..2^31, dim <= 2^20, tokens <= 2^31.
+ */
+ZERO_API int zero_embedding(int dtype, uint64_t vocab, uint64_t dim, const void* table16, uint64_t ld_table, uint64_t tokens,
+                            const void* ids, int id_bytes, float scale, void* out16, uint64_t ld_out, void* stream);
+
+/*
+ * zero_embedding_backward -- dtable16[v] = scale * (sum of dout16[t] over the
+ * tokens t with ids[t] = v), every row of the table (0 where no token names
+ * it); with accumulate != 0 what the rows held is added before the rounding
+ * (rows that no token names keep their values), as a table that is also the
+ * output layer's weight needs.  Sums are fp32, in the order of the tokens;
+ * padding adds nothing.
+ *   workspace   256-byte aligned, at least
+ *               zero_embedding_backward_workspace_bytes(vocab, dim, tokens) bytes
+ * tokens = 0 gives zeros.
+ */
+ZERO_API int zero_embedding_backward(int dtype, uint64_t vocab, uint64_t dim, const void* dout16, uint64_t ld_dout,
+                                     uint64_t tokens, const void* ids, int id_bytes, float scale, int accumulate,
+                                     void* dtable16, uint64_t ld_dtable, void* workspace, uint64_t workspace_bytes,
+                                     void* stream);
+
+/* Bytes of that workspace (a host query); 0 for sizes that the call refuses or that are empty. */
+ZERO_API uint64_t zero_embedding_backward_workspace_bytes(uint64_t vocab, uint64_t dim, uint64_t tokens);
 
 /* Last error message of this handle (or of the last failed init when h is
  * NULL).  The string is owned by the library and valid until the next call. */

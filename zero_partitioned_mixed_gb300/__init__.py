@@ -21,4 +21,7 @@ from ._binding import (  # noqa: F401
     muon_hyper, zero_muon_set_state, zero_muon_get_state, zero_muon_momentum, zero_muon_apply, zero_orthogonalize,
     zero_orthogonalize_workspace_bytes, zero_mx4_codes_bytes, zero_mx4_scales_bytes, zero_mx4_quantize,
     zero_mx4_dequantize, zero_mx4_matmul, zero_matrix_status, ZERO_MX_BLOCK, ZERO_MAX_MATRICES,
+    zero_mx8_codes_bytes, zero_mx8_scales_bytes, zero_mx8_quantize, zero_mx8_dequantize, zero_mx8_matmul,
+    dropout_spec, zero_dropout, zero_rms_norm, zero_rms_norm_backward, zero_rms_norm_backward_workspace_bytes,
+    zero_embedding, zero_embedding_backward, zero_embedding_backward_workspace_bytes, ZERO_MAX_NORM_COLS,
 )

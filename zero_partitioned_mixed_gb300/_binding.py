@@ -28,10 +28,14 @@ EXPORTS = (
     "zero_muon_set_state", "zero_muon_get_state", "zero_muon_momentum", "zero_muon_apply",
     "zero_orthogonalize", "zero_muon_orthogonalize", "zero_orthogonalize_workspace_bytes", "zero_mx4_codes_bytes", "zero_mx4_scales_bytes",
     "zero_mx4_quantize", "zero_mx4_dequantize", "zero_mx4_matmul", "zero_matrix_status", "zero_debug_hold_matrix",
+    "zero_mx8_codes_bytes", "zero_mx8_scales_bytes", "zero_mx8_quantize", "zero_mx8_dequantize", "zero_mx8_matmul",
+    "zero_dropout", "zero_rms_norm", "zero_rms_norm_backward", "zero_rms_norm_backward_workspace_bytes",
+    "zero_embedding", "zero_embedding_backward", "zero_embedding_backward_workspace_bytes",
 )
 ZERO_Q_BLOCK = 256
 ZERO_MX_BLOCK = 32
 ZERO_MAX_MATRICES = 128
+ZERO_MAX_NORM_COLS = 16384
 
 
 class ZeroError(RuntimeError):
@@ -69,6 +73,10 @@ class MuonState(C.Structure):
                 ("applied", C.c_int32), ("ticket", C.c_uint32), ("steps_applied", C.c_int64),
                 ("steps_skipped", C.c_int64), ("aborted", C.c_int32), ("reserved0", C.c_int32),
                 ("reserved", C.c_int64 * 2)]
+
+
+class Dropout(C.Structure):
+    _fields_ = [("p", C.c_double), ("seed", C.c_uint64), ("offset", C.c_uint64), ("step", C.c_void_p)]
 
 
 _lib = None
@@ -135,7 +143,18 @@ def load_library():
     lib.zero_debug_hold_matrix.argtypes = [C.c_int64]
     lib.zero_orthogonalize_workspace_bytes.argtypes = [I32, U64, U64]
     lib.zero_mx4_codes_bytes.argtypes = lib.zero_mx4_scales_bytes.argtypes = [U64, U64]
-    sizes = ("zero_orthogonalize_workspace_bytes", "zero_mx4_codes_bytes", "zero_mx4_scales_bytes")
+    for name in ("quantize", "dequantize", "matmul", "codes_bytes", "scales_bytes"):
+        getattr(lib, "zero_mx8_" + name).argtypes = getattr(lib, "zero_mx4_" + name).argtypes
+    D, F = C.POINTER(Dropout), C.c_float
+    lib.zero_dropout.argtypes = [I32, U64, U64, P, U64, P, U64, D, P]
+    lib.zero_rms_norm.argtypes = [I32, U64, U64, P, U64, P, U64, P, F, D, P, U64, P, U64, I32, P, P, P]
+    lib.zero_rms_norm_backward.argtypes = [I32, U64, U64, P, U64, P, U64, P, F, P, U64, P, U64, D, P, U64, P, P, U64, P]
+    lib.zero_rms_norm_backward_workspace_bytes.argtypes = [U64, U64]
+    lib.zero_embedding.argtypes = [I32, U64, U64, P, U64, U64, P, I32, F, P, U64, P]
+    lib.zero_embedding_backward.argtypes = [I32, U64, U64, P, U64, U64, P, I32, F, I32, P, U64, P, U64, P]
+    lib.zero_embedding_backward_workspace_bytes.argtypes = [U64, U64, U64]
+    sizes = ("zero_orthogonalize_workspace_bytes", "zero_mx4_codes_bytes", "zero_mx4_scales_bytes", "zero_mx8_codes_bytes",
+             "zero_mx8_scales_bytes", "zero_rms_norm_backward_workspace_bytes", "zero_embedding_backward_workspace_bytes")
     for name in sizes:
         getattr(lib, name).restype = U64
     for name in EXPORTS:
@@ -432,6 +451,110 @@ def zero_mx4_matmul(dtype: int, m: int, n: int, k: int, a_codes, a_scales, b_cod
                     ld: Optional[int] = None, stream=None):
     _check(load_library().zero_mx4_matmul(dtype, m, n, k, _ptr(a_codes), _ptr(a_scales), _ptr(b_codes), _ptr(b_scales),
                                           _ptr(out16), n if ld is None else ld, _stream(stream)), None)
+
+
+# ---------------------------------------------- microscaled 8-bit floats
+def zero_mx8_codes_bytes(rows: int, cols: int) -> int:
+    return int(load_library().zero_mx8_codes_bytes(rows, cols))
+
+
+def zero_mx8_scales_bytes(rows: int, cols: int) -> int:
+    return int(load_library().zero_mx8_scales_bytes(rows, cols))
+
+
+def zero_mx8_quantize(dtype: int, rows: int, cols: int, src16, codes, scales, ld: Optional[int] = None,
+                      transpose: bool = False, stream=None):
+    _check(load_library().zero_mx8_quantize(dtype, rows, cols, _ptr(src16), cols if ld is None else ld,
+                                            1 if transpose else 0, _ptr(codes), _ptr(scales), _stream(stream)), None)
+
+
+def zero_mx8_dequantize(dtype: int, rows: int, cols: int, codes, scales, out16, ld: Optional[int] = None, stream=None):
+    _check(load_library().zero_mx8_dequantize(dtype, rows, cols, _ptr(codes), _ptr(scales), _ptr(out16),
+                                              cols if ld is None else ld, _stream(stream)), None)
+
+
+def zero_mx8_matmul(dtype: int, m: int, n: int, k: int, a_codes, a_scales, b_codes, b_scales, out16,
+                    ld: Optional[int] = None, stream=None):
+    _check(load_library().zero_mx8_matmul(dtype, m, n, k, _ptr(a_codes), _ptr(a_scales), _ptr(b_codes), _ptr(b_scales),
+                                          _ptr(out16), n if ld is None else ld, _stream(stream)), None)
+
+
+# --------------------------------------------------- the residual stream
+def dropout_spec(p: float, seed: int, offset: int = 0, step=None) -> Dropout:
+    """The dropout of one layer and step: share p, the generator's seed and its stream offset (+ *step: a device
+    tensor of one int64, read when the kernel runs).  The tensor must stay alive while the spec is in use."""
+    spec = Dropout(p, seed & 0xFFFFFFFFFFFFFFFF, offset & 0xFFFFFFFFFFFFFFFF, _ptr(step))
+    spec.tensor = step
+    return spec
+
+
+def _spec(dropout):
+    return None if dropout is None else C.byref(dropout)
+
+
+def _bytes_of(t) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def zero_dropout(dtype: int, rows: int, cols: int, src16, out16, dropout: Optional[Dropout], ld_src: Optional[int] = None,
+                 ld_out: Optional[int] = None, stream=None):
+    _check(load_library().zero_dropout(dtype, rows, cols, _ptr(src16), cols if ld_src is None else ld_src, _ptr(out16),
+                                       cols if ld_out is None else ld_out, _spec(dropout), _stream(stream)), None)
+
+
+def zero_rms_norm(dtype: int, rows: int, cols: int, x16, weight16, eps: float, residual16=None, h16=None, out16=None,
+                  bits: int = 0, codes=None, scales=None, dropout: Optional[Dropout] = None, ld_x: Optional[int] = None,
+                  ld_residual: Optional[int] = None, ld_h: Optional[int] = None, ld_out: Optional[int] = None, stream=None):
+    _check(load_library().zero_rms_norm(
+        dtype, rows, cols, _ptr(x16), cols if ld_x is None else ld_x, _ptr(residual16),
+        cols if ld_residual is None else ld_residual, _ptr(weight16), eps, _spec(dropout), _ptr(h16),
+        cols if ld_h is None else ld_h, _ptr(out16), cols if ld_out is None else ld_out, bits, _ptr(codes), _ptr(scales),
+        _stream(stream)), None)
+
+
+def zero_rms_norm_backward_workspace_bytes(rows: int, cols: int) -> int:
+    return int(load_library().zero_rms_norm_backward_workspace_bytes(rows, cols))
+
+
+def zero_rms_norm_backward(dtype: int, rows: int, cols: int, dy16, h16, weight16, eps: float, dh16, workspace=None,
+                           dh_in16=None, dx16=None, dweight16=None, dropout: Optional[Dropout] = None,
+                           ld_dy: Optional[int] = None, ld_h: Optional[int] = None, ld_in: Optional[int] = None,
+                           ld_dh: Optional[int] = None, ld_dx: Optional[int] = None, stream=None):
+    """workspace: a device tensor (needed for dweight16)."""
+    _check(load_library().zero_rms_norm_backward(
+        dtype, rows, cols, _ptr(dy16), cols if ld_dy is None else ld_dy, _ptr(h16), cols if ld_h is None else ld_h,
+        _ptr(weight16), eps, _ptr(dh_in16), cols if ld_in is None else ld_in, _ptr(dh16), cols if ld_dh is None else ld_dh,
+        _spec(dropout), _ptr(dx16), cols if ld_dx is None else ld_dx, _ptr(dweight16), _ptr(workspace), _bytes_of(workspace),
+        _stream(stream)), None)
+
+
+def zero_embedding(dtype: int, vocab: int, dim: int, table16, tokens: int, ids, out16, scale: float = 1.0,
+                   ld_table: Optional[int] = None, ld_out: Optional[int] = None, stream=None):
+    """ids: a device tensor of int32 or int64."""
+    _check(load_library().zero_embedding(dtype, vocab, dim, _ptr(table16), dim if ld_table is None else ld_table, tokens,
+                                         _ptr(ids), _id_bytes(ids), scale, _ptr(out16), dim if ld_out is None else ld_out,
+                                         _stream(stream)), None)
+
+
+def _id_bytes(ids) -> int:
+    """4 or 8; 0, which the calls refuse, for a tensor of anything but int32 or int64."""
+    if ids is None or isinstance(ids, int):   # an address: 64-bit ids
+        return 8
+    return {"torch.int32": 4, "torch.int64": 8}.get(str(ids.dtype), 0)
+
+
+def zero_embedding_backward_workspace_bytes(vocab: int, dim: int, tokens: int) -> int:
+    return int(load_library().zero_embedding_backward_workspace_bytes(vocab, dim, tokens))
+
+
+def zero_embedding_backward(dtype: int, vocab: int, dim: int, dout16, tokens: int, ids, dtable16, workspace,
+                            scale: float = 1.0, accumulate: bool = False, ld_dout: Optional[int] = None,
+                            ld_dtable: Optional[int] = None, stream=None):
+    """ids: a device tensor of int32 or int64; workspace: a device tensor."""
+    _check(load_library().zero_embedding_backward(
+        dtype, vocab, dim, _ptr(dout16), dim if ld_dout is None else ld_dout, tokens, _ptr(ids), _id_bytes(ids), scale,
+        1 if accumulate else 0, _ptr(dtable16), dim if ld_dtable is None else ld_dtable, _ptr(workspace),
+        _bytes_of(workspace), _stream(stream)), None)
 
 
 def zero_matrix_status(stream=None) -> None:

@@ -26,10 +26,10 @@ LIB_NAME = "libzero_gb300.so"
 LIB_PATH = os.path.join(BUILD_DIR, LIB_NAME)
 
 SOURCES = ["zero_kernels.cu", "zero_quant.cu", "zero_tma.cu", "zero_api.cpp", "zero_noalloc.cu",
-           "zero_muon.cu", "zero_ortho.cu", "zero_mx4.cu"]
+           "zero_muon.cu", "zero_ortho.cu", "zero_mx4.cu", "zero_embed.cu", "zero_norm.cu"]
 HEADERS = [os.path.join(INCLUDE, "zero_gb300.h"), os.path.join(CSRC, "zero_internal.h"),
            os.path.join(CSRC, "zero_device.cuh"), os.path.join(CSRC, "zero_host.h"), os.path.join(CSRC, "zero_tc.cuh"),
-           os.path.join(CSRC, "zero_rows.cuh")]
+           os.path.join(CSRC, "zero_rows.cuh"), os.path.join(CSRC, "zero_mx.cuh"), os.path.join(CSRC, "zero_philox.cuh")]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 

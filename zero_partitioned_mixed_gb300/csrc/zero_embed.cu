@@ -1,0 +1,501 @@
+// The embedding of a training step: rows of a 16-bit table by token, and the
+// table's gradient.
+//
+//   out[t] = s E[id_t];   dE[v] = s (sum over t with id_t = v of dy[t])
+//
+// Both move rows and are bound by HBM, the gradient mostly by writing the
+// table: every row of it, most of them zeros.  Its sums are made without
+// atomics on values, so that they do not depend on an order of arrival:
+//
+//   sort   the tokens by id, stably, by one cluster of 8 CTAs (radix digits
+//          of up to 8 bits; its CTAs see each other's counts through their
+//          shared memory and wait for each other at the cluster's barrier
+//          only).  The launch's other CTAs fill the table with zeros
+//          meanwhile, which takes longer for tables of real sizes.
+//   sum    a warp takes 256 columns of kPiece consecutive sorted tokens, in
+//          fp32.  A run of one id that lies inside its piece is finished and
+//          written; one that crosses into other pieces leaves partial sums.
+//   join   the warp of the piece in which such a run begins adds them in order.
+//
+// An id outside the table is padding: zeros forward, no gradient.
+
+#include <cmath>
+#include <cstdint>
+#include <string>
+
+#include <nvtx3/nvToolsExt.h>
+
+#include "zero_gb300.h"
+#include "zero_host.h"
+#include "zero_rows.cuh"
+
+namespace zg {
+namespace {
+
+struct EmbedArgs {
+    const unsigned short* table;
+    unsigned short* out;
+    const void* ids;
+    uint64_t vocab, dim, tokens, ld_table, ld_out;
+    uint64_t segments;   // of 256 columns
+    float scale;
+    int wide_ids;        // 8 bytes each, else 4
+};
+
+// The id of token t, or vocab for one outside the table.
+__device__ __forceinline__ uint32_t id_at(const void* ids, int wide, uint64_t t, uint64_t vocab) {
+    const int64_t id = wide ? static_cast<const int64_t*>(ids)[t] : static_cast<const int32_t*>(ids)[t];
+    return id >= 0 && static_cast<uint64_t>(id) < vocab ? static_cast<uint32_t>(id) : static_cast<uint32_t>(vocab);
+}
+
+// A warp takes 256 columns of kEmbedTokens tokens, 8 a lane, all loads in
+// flight together.
+constexpr int kEmbedTokens = 4;
+
+template <int DT, bool ALIGNED>
+__global__ void __launch_bounds__(kThreads) k_embedding(const __grid_constant__ EmbedArgs a) {
+    pdl_enter();
+    const uint64_t item = static_cast<uint64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+    const uint64_t quad = item / a.segments, t0 = quad * kEmbedTokens;
+    if (t0 >= a.tokens) return;
+    const uint64_t c = (item - quad * a.segments) * 256 + 8 * (threadIdx.x & 31);
+    const int valid = values_left(a.dim, c);
+    const uint64_t total = (a.vocab - 1) * a.ld_table + a.dim;
+    uint32_t w[kEmbedTokens][4];
+#pragma unroll
+    for (int i = 0; i < kEmbedTokens; ++i) {
+        w[i][0] = w[i][1] = w[i][2] = w[i][3] = 0u;
+        if (t0 + i >= a.tokens) continue;
+        const uint32_t id = id_at(a.ids, a.wide_ids, t0 + i, a.vocab);
+        if (id < a.vocab) read8<ALIGNED>(a.table, id * a.ld_table + c, valid, total, w[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kEmbedTokens; ++i) {
+        if (t0 + i >= a.tokens) continue;
+        float v[8];
+        widen8<DT>(w[i], v);
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) mul2(v[e], v[e + 1], a.scale);
+        uint32_t q[4];
+        narrow8<DT>(v, q);
+        store8<ALIGNED>(a.out + (t0 + i) * a.ld_out, c, valid, q);
+    }
+}
+
+// -------------------------------------------------------------------- sort
+constexpr uint32_t kSortCtas = 8, kSortThreads = 1024, kDigits = 256;
+
+struct SortArgs {
+    const void* ids;
+    uint64_t vocab, tokens;
+    int wide_ids;
+    uint32_t passes, digit_bits;
+    uint32_t *key[2], *index[2];   // the sorted ones end in [(passes - 1) & 1]
+    // what the other CTAs fill with zeros, as rows
+    unsigned short* zero;
+    uint64_t zero_rows, zero_cols, zero_ld, zero_total;   // total: from the first row's start to the last one's end
+};
+
+__device__ __forceinline__ uint32_t cta_of_cluster() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void wait_for_cluster() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t load_of_cta(const uint32_t* shared, uint32_t cta) {
+    uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(shared)), there, x;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(at), "r"(cta));
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(there) : "memory");
+    return x;
+}
+// What other CTAs of the cluster wrote comes from L2, not from this SM's L1.
+__device__ __forceinline__ uint32_t load_l2(const uint32_t* p) {
+    uint32_t x;
+    asm volatile("ld.global.cg.u32 %0, [%1];" : "=r"(x) : "l"(p) : "memory");
+    return x;
+}
+
+__device__ void fill_zeros(const SortArgs& a, uint64_t warp, uint64_t warps) {
+    const uint32_t lane = threadIdx.x & 31;
+    for (uint64_t r = warp; r < a.zero_rows; r += warps) {
+        unsigned short* row = a.zero + r * a.zero_ld;
+        const uint64_t left = a.zero_total - r * a.zero_ld, cols = left < a.zero_cols ? left : a.zero_cols;
+        uint64_t head = (16 - (reinterpret_cast<uintptr_t>(row) & 15)) / 2 % 8;
+        if (head > cols) head = cols;
+        const uint64_t pieces = (cols - head) / 8;
+        if (lane < head) row[lane] = 0;
+        for (uint64_t i = lane; i < pieces; i += 32) reinterpret_cast<uint4*>(row + head)[i] = make_uint4(0u, 0u, 0u, 0u);
+        const uint64_t done = head + 8 * pieces;
+        if (lane < cols - done) row[done + lane] = 0;
+    }
+}
+
+__global__ void __launch_bounds__(kSortThreads) k_embedding_sort(const __grid_constant__ SortArgs a) {
+    pdl_enter();
+    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (blockIdx.x >= kSortCtas) {
+        fill_zeros(a, static_cast<uint64_t>(blockIdx.x - kSortCtas) * 32 + warp,
+                   static_cast<uint64_t>(gridDim.x - kSortCtas) * 32);
+        return;
+    }
+    __shared__ uint32_t s_count[kDigits];                    // this CTA's keys of each digit
+    __shared__ uint32_t s_base[kDigits];                     // where its next key of a digit goes
+    __shared__ uint32_t s_tile[kDigits];                     // the same at the tile's start
+    __shared__ unsigned short s_warp[kSortThreads / 32][kDigits];   // a tile's keys of each digit, by warp
+    __shared__ uint32_t s_scan[kDigits / 32];
+    const uint32_t me = cta_of_cluster();
+    const uint64_t share = (a.tokens + kSortCtas - 1) / kSortCtas, first = me * share;
+    const uint64_t end = first >= a.tokens ? first : first + share < a.tokens ? first + share : a.tokens;
+    for (uint32_t pass = 0; pass < a.passes; ++pass) {
+        const uint32_t shift = pass * a.digit_bits, mask = (1u << a.digit_bits) - 1;
+        const uint32_t* from = a.key[(pass & 1) ^ 1];
+        const uint32_t* from_index = a.index[(pass & 1) ^ 1];
+        uint32_t *to = a.key[pass & 1], *to_index = a.index[pass & 1];
+        auto key_of = [&](uint64_t i) { return pass == 0 ? id_at(a.ids, a.wide_ids, i, a.vocab) : load_l2(from + i); };
+        if (threadIdx.x < kDigits) s_count[threadIdx.x] = 0;
+        __syncthreads();
+        for (uint64_t i = first + threadIdx.x; i < end; i += kSortThreads) atomicAdd(&s_count[(key_of(i) >> shift) & mask], 1u);
+        wait_for_cluster();
+        // keys of smaller digits anywhere, and of the same digit in the CTAs before
+        if (threadIdx.x < kDigits) {
+            uint32_t before = 0, all = 0;
+#pragma unroll
+            for (uint32_t q = 0; q < kSortCtas; ++q) {
+                const uint32_t n = load_of_cta(&s_count[threadIdx.x], q);
+                before += q < me ? n : 0u;
+                all += n;
+            }
+            uint32_t sum = all;   // inclusive scan over the digits
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+                if (lane >= static_cast<uint32_t>(d)) sum += x;
+            }
+            if (lane == 31) s_scan[warp] = sum;
+            s_base[threadIdx.x] = before + sum - all;
+        }
+        __syncthreads();
+        if (threadIdx.x < kDigits) {
+            uint32_t x = 0;
+            for (uint32_t q = 0; q < warp; ++q) x += s_scan[q];
+            s_base[threadIdx.x] += x;
+        }
+        for (uint64_t tile = first; tile < end; tile += kSortThreads) {
+            for (uint32_t i = threadIdx.x; i < sizeof(s_warp) / 4; i += kSortThreads) reinterpret_cast<uint32_t*>(s_warp)[i] = 0u;
+            __syncthreads();
+            const uint64_t i = tile + threadIdx.x;
+            const bool here = i < end;
+            const uint32_t key = here ? key_of(i) : 0u, digit = here ? (key >> shift) & mask : kDigits;
+            const uint32_t index = !here ? 0u : pass == 0 ? static_cast<uint32_t>(i) : load_l2(from_index + i);
+            // the keys of the same digit in the lanes before
+            const uint32_t same = __match_any_sync(0xFFFFFFFFu, digit);
+            const uint32_t rank = __popc(same & ((1u << lane) - 1));
+            if (here && rank == 0) s_warp[warp][digit] = static_cast<unsigned short>(__popc(same));
+            __syncthreads();
+            if (threadIdx.x < kDigits) {   // in the warps before; the tile's keys move the base on
+                uint32_t x = s_base[threadIdx.x];
+                const uint32_t x0 = x;
+#pragma unroll
+                for (uint32_t w = 0; w < kSortThreads / 32; ++w) {
+                    const uint32_t n = s_warp[w][threadIdx.x];
+                    s_warp[w][threadIdx.x] = static_cast<unsigned short>(x - x0);
+                    x += n;
+                }
+                s_tile[threadIdx.x] = x0;
+                s_base[threadIdx.x] = x;
+            }
+            __syncthreads();
+            if (here) {
+                const uint32_t at = s_tile[digit] + s_warp[warp][digit] + rank;
+                to[at] = key;
+                to_index[at] = index;
+            }
+            __syncthreads();
+        }
+        wait_for_cluster();
+    }
+}
+
+// -------------------------------------------------------------- sum and join
+struct SumArgs {
+    const unsigned short* grad;
+    unsigned short* table;
+    const uint32_t *key, *index;   // sorted tokens
+    float* partial;                // [pieces][2][8 * across]: of the run that enters a piece, of the one that leaves it
+    uint64_t vocab, dim, tokens, ld_grad, ld_table;
+    uint64_t segments, pieces, width;   // width = 8 * ceil(dim / 8)
+    float scale;
+    int add;                       // to what the table holds
+};
+constexpr uint32_t kPiece = 16, kSumLoads = 8;
+
+template <int DT, bool ALIGNED>
+__device__ __forceinline__ void write_sum(const SumArgs& a, uint32_t id, uint64_t c, int valid, float (&s)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) mul2(s[e], s[e + 1], a.scale);
+    unsigned short* row = a.table + id * a.ld_table;
+    if (a.add) {
+        uint32_t w[4];
+        read8<ALIGNED>(a.table, id * a.ld_table + c, valid, (a.vocab - 1) * a.ld_table + a.dim, w);
+        float v[8];
+        widen8<DT>(w, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[e] = __fadd_rn(v[e], s[e]);
+    }
+    uint32_t q[4];
+    narrow8<DT>(s, q);
+    store8<ALIGNED>(row, c, valid, q);
+}
+__device__ __forceinline__ float* partial_at(const SumArgs& a, uint64_t piece, int leaves, uint64_t c) {
+    return a.partial + (2 * piece + leaves) * a.width + c;
+}
+
+template <int DT, bool ALIGNED>
+__global__ void __launch_bounds__(kThreads) k_embedding_sum(const __grid_constant__ SumArgs a) {
+    pdl_enter();
+    const uint64_t item = static_cast<uint64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+    const uint64_t piece = item / a.segments;
+    if (piece >= a.pieces) return;
+    const uint32_t lane = threadIdx.x & 31;
+    const uint64_t c = (item - piece * a.segments) * 256 + 8 * lane, first = piece * kPiece;
+    const int valid = values_left(a.dim, c);
+    const uint64_t total = (a.tokens - 1) * a.ld_grad + a.dim;
+    const uint32_t none = static_cast<uint32_t>(a.vocab);   // padding, sorted behind all ids
+    // lane i: the piece's token i; lanes 30 and 31 the neighbours' ids
+    const uint64_t mine = lane == 30 ? first - 1 : lane == 31 ? first + kPiece : first + lane;
+    const bool there = lane == 30 ? first > 0 : mine < a.tokens && (lane == 31 || lane < kPiece);
+    const uint32_t key = there ? load_l2(a.key + mine) : none;
+    const uint32_t index = there && lane < kPiece ? load_l2(a.index + mine) : 0u;
+    const uint32_t before = __shfl_sync(0xFFFFFFFFu, key, 30), after = __shfl_sync(0xFFFFFFFFu, key, 31);
+    const uint32_t count = __popc(__ballot_sync(0xFFFFFFFFu, lane < kPiece && key != none));
+    if (count == 0) return;
+    float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    uint32_t id = __shfl_sync(0xFFFFFFFFu, key, 0);
+    bool enters = first > 0 && id == before;   // the run began in an earlier piece
+#pragma unroll 1
+    for (uint32_t i0 = 0; i0 < count; i0 += kSumLoads) {
+        uint32_t w[kSumLoads][4];
+#pragma unroll
+        for (uint32_t i = 0; i < kSumLoads; ++i) {
+            const uint64_t t = __shfl_sync(0xFFFFFFFFu, index, i0 + i);
+            w[i][0] = w[i][1] = w[i][2] = w[i][3] = 0u;
+            if (i0 + i < count) read8<ALIGNED>(a.grad, t * a.ld_grad + c, valid, total, w[i]);
+        }
+#pragma unroll
+        for (uint32_t i = 0; i < kSumLoads; ++i) {
+            const uint32_t next = __shfl_sync(0xFFFFFFFFu, key, i0 + i);
+            if (i0 + i >= count) continue;
+            if (next != id) {   // the run is complete here
+                if (enters) {
+                    if (valid > 0) {
+                        float4* to = reinterpret_cast<float4*>(partial_at(a, piece, 0, c));
+                        to[0] = make_float4(s[0], s[1], s[2], s[3]);
+                        to[1] = make_float4(s[4], s[5], s[6], s[7]);
+                    }
+                } else {
+                    write_sum<DT, ALIGNED>(a, id, c, valid, s);
+                }
+                id = next;
+                enters = false;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s[e] = 0.0f;
+            }
+            float v[8];
+            widen8<DT>(w[i], v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[e] = __fadd_rn(s[e], v[e]);
+        }
+    }
+    if (enters || (count == kPiece && id == after)) {
+        if (valid > 0) {
+            float4* to = reinterpret_cast<float4*>(partial_at(a, piece, enters ? 0 : 1, c));
+            to[0] = make_float4(s[0], s[1], s[2], s[3]);
+            to[1] = make_float4(s[4], s[5], s[6], s[7]);
+        }
+    } else {
+        write_sum<DT, ALIGNED>(a, id, c, valid, s);
+    }
+}
+
+// A warp for each piece and 256 columns; it has work where a run begins in
+// the piece and goes on in the next one.
+template <int DT, bool ALIGNED>
+__global__ void __launch_bounds__(kThreads) k_embedding_join(const __grid_constant__ SumArgs a) {
+    pdl_enter();
+    const uint64_t item = static_cast<uint64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+    const uint64_t piece = item / a.segments;
+    if (piece + 1 >= a.pieces) return;
+    const uint64_t first = piece * kPiece;
+    const uint32_t id = load_l2(a.key + first + kPiece - 1);
+    if (id >= a.vocab || load_l2(a.key + first + kPiece) != id) return;
+    if (first > 0 && load_l2(a.key + first - 1) == id) return;   // sorted: the whole piece is of a run that began earlier
+    const uint32_t lane = threadIdx.x & 31;
+    const uint64_t c = (item - piece * a.segments) * 256 + 8 * lane;
+    const int valid = values_left(a.dim, c);
+    // the pieces after this one that the run enters
+    uint64_t last = piece + 1;
+    for (;;) {
+        const uint64_t q = last + 1 + lane;
+        const uint32_t in = __ballot_sync(0xFFFFFFFFu, q < a.pieces && load_l2(a.key + q * kPiece) == id);
+        const uint32_t run = in == 0xFFFFFFFFu ? 32u : __ffs(~in) - 1;
+        last += run;
+        if (run < 32u) break;
+    }
+    if (valid <= 0) return;
+    float s[8];
+    auto add = [&](const float* p, bool start) {
+        const float4 x = *reinterpret_cast<const float4*>(p), y = *reinterpret_cast<const float4*>(p + 4);
+        const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[e] = start ? v[e] : __fadd_rn(s[e], v[e]);
+    };
+    add(partial_at(a, piece, 1, c), true);
+#pragma unroll 4
+    for (uint64_t q = piece + 1; q <= last; ++q) add(partial_at(a, q, 0, c), false);
+    write_sum<DT, ALIGNED>(a, id, c, valid, s);
+}
+
+// -------------------------------------------------------------------- host
+constexpr uint64_t kMaxTokens = 1ull << 31, kMaxVocab = 1ull << 31, kMaxDim = 1ull << 20, kMaxLd = 1ull << 40;
+
+int check_embedding(int dtype, uint64_t vocab, uint64_t dim, uint64_t tokens, const void* ids, int id_bytes, float scale) {
+    if (dtype != ZERO_FP16 && dtype != ZERO_BF16) return refuse(ZERO_EINVAL, "dtype must be fp16 or bf16");
+    if (vocab < 1 || vocab > kMaxVocab) return refuse(ZERO_EINVAL, "vocab must be in 1..2^31");
+    if (dim > kMaxDim) return refuse(ZERO_EINVAL, "dim is more than 2^20");
+    if (tokens > kMaxTokens) return refuse(ZERO_EINVAL, "more than 2^31 tokens");
+    if (id_bytes != 4 && id_bytes != 8) return refuse(ZERO_EINVAL, "id_bytes must be 4 or 8");
+    if (!std::isfinite(scale)) return refuse(ZERO_EINVAL, "scale must be finite");
+    if (tokens && dim && (!ids || !aligned(ids, static_cast<uintptr_t>(id_bytes))))
+        return refuse(ZERO_EINVAL, "ids is NULL or not aligned to its elements");
+    return ZERO_OK;
+}
+int check_rows(const char* name, const void* at, uint64_t ld, uint64_t dim) {
+    if (!at || !aligned(at, 2)) return refuse(ZERO_EINVAL, std::string(name) + " is NULL or not 2-byte aligned");
+    if (ld < dim || ld > kMaxLd)
+        return refuse(ZERO_EINVAL, "ld of " + std::string(name) + " must be at least dim (and at most 2^40)");
+    return ZERO_OK;
+}
+constexpr uint64_t kZeroCtas = 304, kZeroCols = 4096;   // two an SM; values a warp fills at a time
+uint64_t sort_bytes(uint64_t tokens) { return up(tokens * 4, 256); }   // one of four arrays
+uint64_t pieces_of(uint64_t tokens) { return (tokens + kPiece - 1) / kPiece; }
+
+}  // namespace
+}  // namespace zg
+
+using namespace zg;
+
+extern "C" {
+
+int zero_embedding(int dtype, uint64_t vocab, uint64_t dim, const void* table16, uint64_t ld_table, uint64_t tokens,
+                   const void* ids, int id_bytes, float scale, void* out16, uint64_t ld_out, void* stream) {
+    nvtxRangePushA("zero_embedding");
+    struct Pop { ~Pop() { nvtxRangePop(); } } pop;
+    if (const int rc = check_embedding(dtype, vocab, dim, tokens, ids, id_bytes, scale)) return rc;
+    if (tokens == 0 || dim == 0) return ZERO_OK;
+    if (const int rc = check_rows("table16", table16, ld_table, dim)) return rc;
+    if (const int rc = check_rows("out16", out16, ld_out, dim)) return rc;
+    EmbedArgs a = {};
+    a.table = static_cast<const unsigned short*>(table16);
+    a.out = static_cast<unsigned short*>(out16);
+    a.ids = ids;
+    a.vocab = vocab;
+    a.dim = dim;
+    a.tokens = tokens;
+    a.ld_table = ld_table;
+    a.ld_out = ld_out;
+    a.segments = up(dim, 256) / 256;
+    a.scale = scale;
+    a.wide_ids = id_bytes == 8;
+    const uint64_t items = up(tokens, kEmbedTokens) / kEmbedTokens * a.segments, blocks = up(items, kThreads / 32) / (kThreads / 32);
+    if (blocks > 0x7FFFFFFFull) return refuse(ZERO_EINVAL, "tokens and dim are too large together");
+    const bool fp16 = dtype == ZERO_FP16;
+    const bool whole = aligned(table16, 16) && ld_table % 8 == 0 && aligned(out16, 16) && ld_out % 8 == 0;
+    const cudaError_t e = launch_pdl(whole ? (fp16 ? k_embedding<kFp16, true> : k_embedding<kBf16, true>)
+                                           : (fp16 ? k_embedding<kFp16, false> : k_embedding<kBf16, false>),
+                                     dim3(static_cast<unsigned>(blocks)), kThreads, 0, 1, static_cast<cudaStream_t>(stream), a);
+    return e == cudaSuccess ? ZERO_OK : cuda_refuse(e, "zero_embedding");
+}
+
+uint64_t zero_embedding_backward_workspace_bytes(uint64_t vocab, uint64_t dim, uint64_t tokens) {
+    if (vocab < 1 || vocab > kMaxVocab || dim == 0 || dim > kMaxDim || tokens == 0 || tokens > kMaxTokens) return 0;
+    return 4 * sort_bytes(tokens) + pieces_of(tokens) * 2 * up(dim, 8) * sizeof(float);
+}
+
+int zero_embedding_backward(int dtype, uint64_t vocab, uint64_t dim, const void* dout16, uint64_t ld_dout, uint64_t tokens,
+                            const void* ids, int id_bytes, float scale, int accumulate, void* dtable16, uint64_t ld_dtable,
+                            void* workspace, uint64_t workspace_bytes, void* stream) {
+    nvtxRangePushA("zero_embedding_backward");
+    struct Pop { ~Pop() { nvtxRangePop(); } } pop;
+    if (const int rc = check_embedding(dtype, vocab, dim, tokens, ids, id_bytes, scale)) return rc;
+    if (dim == 0) return ZERO_OK;
+    if (const int rc = check_rows("dtable16", dtable16, ld_dtable, dim)) return rc;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (tokens == 0) {   // empty sums
+        e = accumulate ? cudaSuccess : cudaMemset2DAsync(dtable16, ld_dtable * 2, 0, dim * 2, vocab, s);
+        return e == cudaSuccess ? ZERO_OK : cuda_refuse(e, "zero_embedding_backward");
+    }
+    if (const int rc = check_rows("dout16", dout16, ld_dout, dim)) return rc;
+    if (!workspace || !aligned(workspace, 256)) return refuse(ZERO_EINVAL, "workspace is NULL or not 256-byte aligned");
+    if (workspace_bytes < zero_embedding_backward_workspace_bytes(vocab, dim, tokens))
+        return refuse(ZERO_EINVAL, "workspace is smaller than zero_embedding_backward_workspace_bytes()");
+    unsigned char* at = static_cast<unsigned char*>(workspace);
+    SortArgs o = {};
+    o.ids = ids;
+    o.vocab = vocab;
+    o.tokens = tokens;
+    o.wide_ids = id_bytes == 8;
+    uint32_t bits = 1;
+    while (vocab >> bits) ++bits;   // of the ids and of vocab itself, which stands for padding
+    o.passes = (bits + 7) / 8;
+    o.digit_bits = (bits + o.passes - 1) / o.passes;
+    for (int i = 0; i < 2; ++i, at += 2 * sort_bytes(tokens)) {
+        o.key[i] = reinterpret_cast<uint32_t*>(at);
+        o.index[i] = reinterpret_cast<uint32_t*>(at + sort_bytes(tokens));
+    }
+    uint64_t others = 0;
+    if (!accumulate) {
+        o.zero = static_cast<unsigned short*>(dtable16);
+        o.zero_total = (vocab - 1) * ld_dtable + dim;
+        o.zero_cols = ld_dtable == dim ? kZeroCols : dim;   // rows without gaps are one range, cut where it suits
+        o.zero_ld = ld_dtable == dim ? kZeroCols : ld_dtable;
+        o.zero_rows = ld_dtable == dim ? up(o.zero_total, kZeroCols) / kZeroCols : vocab;
+        others = up(o.zero_rows, kSortThreads / 32) / (kSortThreads / 32);
+        if (others > kZeroCtas) others = kZeroCtas;
+    }
+    if ((e = launch_pdl(k_embedding_sort, dim3(static_cast<unsigned>(kSortCtas + up(others, kSortCtas))), kSortThreads, 0,
+                        kSortCtas, s, o)) != cudaSuccess)
+        return cuda_refuse(e, "zero_embedding_backward");
+    SumArgs a = {};
+    a.grad = static_cast<const unsigned short*>(dout16);
+    a.table = static_cast<unsigned short*>(dtable16);
+    a.key = o.key[(o.passes - 1) & 1];
+    a.index = o.index[(o.passes - 1) & 1];
+    a.partial = reinterpret_cast<float*>(at);
+    a.vocab = vocab;
+    a.dim = dim;
+    a.tokens = tokens;
+    a.ld_grad = ld_dout;
+    a.ld_table = ld_dtable;
+    a.segments = up(dim, 256) / 256;
+    a.pieces = pieces_of(tokens);
+    a.width = up(dim, 8);
+    a.scale = scale;
+    a.add = accumulate != 0;
+    const dim3 grid(static_cast<unsigned>(up(a.pieces * a.segments, kThreads / 32) / (kThreads / 32)));
+    const bool fp16 = dtype == ZERO_FP16;
+    const bool whole = aligned(dout16, 16) && ld_dout % 8 == 0 && aligned(dtable16, 16) && ld_dtable % 8 == 0;
+    e = launch_pdl(whole ? (fp16 ? k_embedding_sum<kFp16, true> : k_embedding_sum<kBf16, true>)
+                         : (fp16 ? k_embedding_sum<kFp16, false> : k_embedding_sum<kBf16, false>),
+                   grid, kThreads, 0, 1, s, a);
+    if (e == cudaSuccess && a.pieces > 1)
+        e = launch_pdl(whole ? (fp16 ? k_embedding_join<kFp16, true> : k_embedding_join<kBf16, true>)
+                             : (fp16 ? k_embedding_join<kFp16, false> : k_embedding_join<kBf16, false>),
+                       grid, kThreads, 0, 1, s, a);
+    return e == cudaSuccess ? ZERO_OK : cuda_refuse(e, "zero_embedding_backward");
+}
+
+}  // extern "C"

@@ -1,20 +1,7 @@
-// Microscaled 4-bit floats (the OCP MX format with e2m1 elements): quantising
+// Microscaled floats of 4 and 8 bits (zero_mx.cuh has the formats): quantising
 // a matrix along its rows or its columns, reading it back, and the product of
-// two such matrices on the block-scaled tensor cores.
-//
-// A block is 32 consecutive values of a row.  With E the exponent of the
-// block's largest magnitude, its scale is 2^(E - 2) (2 is e2m1's largest
-// exponent), stored as a byte with a bias of 127 and never below 2^-127; a
-// value's code is x / scale rounded to the nearest of 0, 0.5, 1, 1.5, 2, 3,
-// 4, 6 (ties to the even code), larger ones becoming 6.  The division is a
-// multiplication by a power of two and exact.  A block that holds an
-// infinity or a NaN gets the scale 255, which stands for NaN, and codes of 0.
-//
-// Layout.  Codes: row by row, two a byte, the even one low, every row filled
-// with zeros to whole blocks.  Scales: tiles of 128 rows x 4 blocks, 512
-// bytes each, row-major over the matrix; in a tile, byte 16 (r mod 32) +
-// 4 (r / 32) + b.  That is what the tensor cores take: a tile is copied into
-// tensor memory as it stands.  The tiles' unused bytes are 0.
+// two such matrices on the block-scaled tensor cores.  One source for both
+// widths (BITS); the figures here are of 4 bits where nothing else is said.
 
 #include <atomic>
 #include <cstdint>
@@ -23,13 +10,11 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "zero_gb300.h"
-#include "zero_rows.cuh"
+#include "zero_mx.cuh"
 #include "zero_tc.cuh"
 
 namespace zg {
 namespace {
-
-constexpr int kMxBlock = ZERO_MX_BLOCK;
 
 struct MxArgs {
     const void* src;
@@ -41,33 +26,6 @@ struct MxArgs {
     uint64_t tiles_k;          // scale tiles along a row of codes
 };
 
-__device__ __forceinline__ uint64_t scale_at(uint64_t row, uint64_t block, uint64_t tiles_k) {
-    return ((row >> 7) * tiles_k + (block >> 2)) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4 + (block & 3);
-}
-
-// The scale byte of a block from the bits of its largest magnitude.
-__device__ __forceinline__ uint32_t scale_byte(float top) {
-    const uint32_t e = __float_as_uint(top) >> 23;   // 255: infinity or NaN
-    return e == 255u ? 255u : e > 2u ? e - 2u : 0u;
-}
-// 1 / scale; 0 for a NaN block, whose codes are 0.
-__device__ __forceinline__ float scale_inverse(uint32_t byte) {
-    return byte == 255u ? 0.0f : __uint_as_float((254u - byte) << 23);
-}
-// 8 values as codes, the first in the lowest 4 bits.
-__device__ __forceinline__ uint32_t codes8(const float (&x)[8]) {
-    uint32_t r;
-    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
-        "mov.b32 %0, {a, b, c, d};\n\t}"
-        : "=r"(r)
-        : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
-    return r;
-}
-
 // The row kernels: a warp takes kMxRows rows by 256 columns, 8 a lane, all
 // rows' loads in flight together.  They are bound by the instructions they
 // issue as much as by HBM, so a piece that lies inside the matrix and starts
@@ -77,7 +35,7 @@ __device__ __forceinline__ uint32_t codes8(const float (&x)[8]) {
 // and 7.8 us for 2047 x 5003 against 7.4 and 5.9 for 2048 x 5000.
 constexpr int kMxRows = 4;
 
-template <int DT, bool INSIDE>
+template <int BITS, int DT, bool INSIDE>
 __device__ __forceinline__ void rows_piece(const MxArgs& a, uint64_t row0, uint64_t segment) {
     const int lane = threadIdx.x & 31;
     const uint64_t c = segment * 256 + 8 * lane;
@@ -103,7 +61,7 @@ __device__ __forceinline__ void rows_piece(const MxArgs& a, uint64_t row0, uint6
             }
         }
     }
-    uint8_t* codes = a.codes + row0 * a.pitch + (c >> 1);
+    uint8_t* codes = a.codes + row0 * a.pitch + c * BITS / 8;
     // kMxRows rows of a scale tile follow each other at 16 bytes
     uint8_t* scales = a.scales + scale_at(row0, c >> 5, a.tiles_k);
 #pragma unroll
@@ -111,7 +69,7 @@ __device__ __forceinline__ void rows_piece(const MxArgs& a, uint64_t row0, uint6
         uint32_t top = top_pattern(raw[r]);
         top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));   // four lanes share a block
         top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-        const uint32_t byte = scale_byte(widen<DT>(top));
+        const uint32_t byte = scale_byte<BITS>(widen<DT>(top));
         const float inv = scale_inverse(byte);
         float v[8];
 #pragma unroll
@@ -119,8 +77,10 @@ __device__ __forceinline__ void rows_piece(const MxArgs& a, uint64_t row0, uint6
             widen2<DT>(raw[r][e], v[2 * e], v[2 * e + 1]);
             mul2(v[2 * e], v[2 * e + 1], inv);
         }
-        const uint32_t q = byte == 255u ? 0u : codes8(v);
-        if (INSIDE || (row0 + r < a.rows && (c >> 1) < a.pitch)) __stcs(reinterpret_cast<uint32_t*>(codes), q);
+        typename MxElement<BITS>::Eight q;
+        codes8(v, q);
+        if (byte == 255u) no_codes(q);
+        if (INSIDE || (row0 + r < a.rows && c * BITS / 8 < a.pitch)) __stcs(reinterpret_cast<decltype(q)*>(codes), q);
         // the four blocks of a scale tile's row in one word
         uint32_t word = byte | __shfl_down_sync(0xFFFFFFFFu, byte, 4) << 8;
         word |= __shfl_down_sync(0xFFFFFFFFu, word, 8) << 16;
@@ -130,13 +90,13 @@ __device__ __forceinline__ void rows_piece(const MxArgs& a, uint64_t row0, uint6
 
 // Along the rows; those that only fill the last scale tiles are walked too,
 // for their zeros.  ALIGNED: every row of the matrix starts on 16 bytes.
-template <int DT, bool ALIGNED>
-__global__ void __launch_bounds__(kThreads) k_mx4_rows(const __grid_constant__ MxArgs a) {
+template <int BITS, int DT, bool ALIGNED>
+__global__ void __launch_bounds__(kThreads) k_mx_rows(const __grid_constant__ MxArgs a) {
     pdl_enter();
     const uint64_t row0 = (static_cast<uint64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5)) * kMxRows;
     for (uint64_t segment = blockIdx.y; segment < (a.tiles_k + 1) / 2; segment += gridDim.y) {
-        if (ALIGNED && row0 + kMxRows <= a.rows && (segment + 1) * 256 <= a.cols) rows_piece<DT, true>(a, row0, segment);
-        else rows_piece<DT, false>(a, row0, segment);
+        if (ALIGNED && row0 + kMxRows <= a.rows && (segment + 1) * 256 <= a.cols) rows_piece<BITS, DT, true>(a, row0, segment);
+        else rows_piece<BITS, DT, false>(a, row0, segment);
     }
 }
 
@@ -145,10 +105,11 @@ __global__ void __launch_bounds__(kThreads) k_mx4_rows(const __grid_constant__ M
 // of two neighbouring columns; the codes go through shared memory so that a
 // row of them leaves as 64 neighbouring bytes.  11008 x 4096: 18.6 us (6.1
 // TB/s; one column a thread and codes straight from registers took 33).
-template <int DT>
-__global__ void __launch_bounds__(kThreads) k_mx4_columns(const __grid_constant__ MxArgs a) {
+template <int BITS, int DT>
+__global__ void __launch_bounds__(kThreads) k_mx_columns(const __grid_constant__ MxArgs a) {
     pdl_enter();
-    __shared__ __align__(16) uint4 s_codes[128][5];   // 5: neighbouring columns start in other banks
+    constexpr int kPieces = BITS / 4;   // 16-byte pieces of a column's 32 codes
+    __shared__ __align__(16) uint4 s_codes[128][4 * kPieces + 1];   // + 1: neighbouring columns start in other banks
     __shared__ __align__(4) uint8_t s_scale[128][4];   // a row is read as one word
     const int lane = threadIdx.x & 31, b = (threadIdx.x >> 5) & 3;
     const int c = (threadIdx.x >> 7) * 64 + 2 * lane;
@@ -179,9 +140,9 @@ __global__ void __launch_bounds__(kThreads) k_mx4_columns(const __grid_constant_
     for (int e = 0; e < 32; ++e) tops = __vmaxu2(tops, raw[e] & 0x7FFF7FFFu);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const uint32_t byte = scale_byte(widen<DT>((tops >> (16 * h)) & 0xFFFFu));
+        const uint32_t byte = scale_byte<BITS>(widen<DT>((tops >> (16 * h)) & 0xFFFFu));
         const float inv = scale_inverse(byte);
-        uint32_t q[4];
+        typename MxElement<BITS>::Eight q[4];
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
             float x[8];
@@ -191,16 +152,22 @@ __global__ void __launch_bounds__(kThreads) k_mx4_columns(const __grid_constant_
                 x[e + 1] = widen<DT>((raw[8 * g + e + 1] >> (16 * h)) & 0xFFFFu);
                 mul2(x[e], x[e + 1], inv);
             }
-            q[g] = byte == 255u ? 0u : codes8(x);
+            codes8(x, q[g]);
+            if (byte == 255u) no_codes(q[g]);
         }
-        s_codes[c + h][b] = make_uint4(q[0], q[1], q[2], q[3]);
+        if constexpr (BITS == 4) {
+            s_codes[c + h][b] = make_uint4(q[0], q[1], q[2], q[3]);
+        } else {
+            s_codes[c + h][2 * b] = make_uint4(q[0].x, q[0].y, q[1].x, q[1].y);
+            s_codes[c + h][2 * b + 1] = make_uint4(q[2].x, q[2].y, q[3].x, q[3].y);
+        }
         s_scale[c + h][b] = static_cast<uint8_t>(byte);
     }
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const int cc = (threadIdx.x >> 2) + 64 * k, bb = threadIdx.x & 3;
-        const uint64_t out = col0 + cc, at = (row0 + 32 * bb) / 2;
+    for (int k = 0; k < 2 * kPieces; ++k) {
+        const int cc = threadIdx.x / (4 * kPieces) + 64 / kPieces * k, bb = threadIdx.x & (4 * kPieces - 1);
+        const uint64_t out = col0 + cc, at = row0 * BITS / 8 + 16 * bb;
         if (out < a.cols && at < a.pitch) *reinterpret_cast<uint4*>(a.codes + out * a.pitch + at) = s_codes[cc][bb];
     }
     if (threadIdx.x < 128)   // the grid covers whole scale tiles
@@ -208,27 +175,18 @@ __global__ void __launch_bounds__(kThreads) k_mx4_columns(const __grid_constant_
             *reinterpret_cast<const uint32_t*>(s_scale[threadIdx.x]);
 }
 
-// What a scale byte stands for: 2^(byte - 127), the smallest a subnormal number.
-__device__ __forceinline__ float scale_value(uint32_t byte) {
-    return byte == 255u ? NAN : __uint_as_float(byte == 0u ? 0x00400000u : byte << 23);
-}
-// Two codes (the low 8 bits of q) as fp32.
-__device__ __forceinline__ void decode2(uint32_t q, float& lo, float& hi) {
-    uint32_t h;
-    asm("{\n\t.reg .b8 b, x, y, z;\n\tmov.b32 {b, x, y, z}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}" : "=r"(h) : "r"(q));
-    widen2<kFp16>(h, lo, hi);
-}
-
 // Rows that start on 16 bytes, 256 columns of them inside the matrix.
-template <int DT>
+template <int BITS, int DT>
 __device__ __forceinline__ void values_inside(const MxArgs& a, uint64_t row0, uint64_t segment) {
     const uint64_t c = segment * 256 + 8 * (threadIdx.x & 31);
-    const uint8_t* codes = a.codes + row0 * a.pitch + (c >> 1);
+    using Eight = typename MxElement<BITS>::Eight;
+    const uint8_t* codes = a.codes + row0 * a.pitch + c * BITS / 8;
     const uint8_t* scales = a.scales + scale_at(row0, c >> 5, a.tiles_k);
-    uint32_t q[kMxRows], byte[kMxRows];
+    Eight q[kMxRows];
+    uint32_t byte[kMxRows];
 #pragma unroll
     for (int r = 0; r < kMxRows; ++r, codes += a.pitch) {
-        q[r] = __ldcs(reinterpret_cast<const uint32_t*>(codes));
+        q[r] = __ldcs(reinterpret_cast<const Eight*>(codes));
         byte[r] = __ldg(scales + 16 * r);
     }
     unsigned short* dst = static_cast<unsigned short*>(a.dst) + row0 * a.ld + c;
@@ -239,7 +197,7 @@ __device__ __forceinline__ void values_inside(const MxArgs& a, uint64_t row0, ui
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             float lo, hi;
-            decode2(q[r] >> (8 * e), lo, hi);
+            decode2(q[r], e, lo, hi);
             mul2(lo, hi, scale);
             out[e] = narrow2<DT>(lo, hi);
         }
@@ -251,16 +209,18 @@ __device__ __forceinline__ void values_inside(const MxArgs& a, uint64_t row0, ui
 // row starts between two boundaries (not ALIGNED), the piece begins m values
 // before a word of 8 codes does, and its first m values are the last ones of
 // the word before, which may belong to another block.
-template <int DT, bool ALIGNED>
+template <int BITS, int DT, bool ALIGNED>
 __device__ __forceinline__ void values_any(const MxArgs& a, uint64_t row0, uint64_t segment) {
     const int64_t word = static_cast<int64_t>(segment) * 32 + (threadIdx.x & 31);   // along the row of codes
-    const int64_t words = static_cast<int64_t>(a.pitch / 4), cols = static_cast<int64_t>(a.cols);
+    using Eight = typename MxElement<BITS>::Eight;
+    const int64_t words = static_cast<int64_t>(a.pitch / sizeof(Eight)), cols = static_cast<int64_t>(a.cols);
     // words past the row's ends stand for nothing that is written: any will do
     const int64_t here = min(word, words - 1), there = max(min(word - 1, words - 1), static_cast<int64_t>(0));
-    const uint32_t* codes = reinterpret_cast<const uint32_t*>(a.codes + row0 * a.pitch);
+    const Eight* codes = reinterpret_cast<const Eight*>(a.codes + row0 * a.pitch);
     const uint8_t* scales = a.scales + scale_at(row0, here >> 2, a.tiles_k);
     const uint8_t* scales_before = a.scales + scale_at(row0, there >> 2, a.tiles_k);
-    uint32_t q[kMxRows], before[kMxRows], byte[kMxRows], byte_before[kMxRows];
+    Eight q[kMxRows], before[kMxRows];
+    uint32_t byte[kMxRows], byte_before[kMxRows];
 #pragma unroll
     for (int r = 0; r < kMxRows; ++r, codes += words) {
         if (row0 + r >= a.rows) break;
@@ -277,12 +237,12 @@ __device__ __forceinline__ void values_any(const MxArgs& a, uint64_t row0, uint6
         if (row0 + r >= a.rows) break;
         const int m = ALIGNED ? 0 : static_cast<int>((reinterpret_cast<uintptr_t>(row) >> 1) & 7);
         const float scale = scale_value(byte[r]), scale_before = ALIGNED ? 0.0f : scale_value(byte_before[r]);
-        const uint32_t eight = m == 0 ? q[r] : __funnelshift_r(before[r], q[r], 4 * (8 - m));
+        const Eight eight = m == 0 ? q[r] : codes_before(before[r], q[r], m);
         uint32_t out[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             float lo, hi;
-            decode2(eight >> (8 * e), lo, hi);
+            decode2(eight, e, lo, hi);
             lo = __fmul_rn(lo, 2 * e < m ? scale_before : scale);
             hi = __fmul_rn(hi, 2 * e + 1 < m ? scale_before : scale);
             out[e] = narrow2<DT>(lo, hi);
@@ -300,15 +260,15 @@ __device__ __forceinline__ void values_any(const MxArgs& a, uint64_t row0, uint6
 
 // Codes and scales back to 16 bits.  ALIGNED: every row of the matrix starts
 // on 16 bytes.
-template <int DT, bool ALIGNED>
-__global__ void __launch_bounds__(kThreads) k_mx4_values(const __grid_constant__ MxArgs a) {
+template <int BITS, int DT, bool ALIGNED>
+__global__ void __launch_bounds__(kThreads) k_mx_values(const __grid_constant__ MxArgs a) {
     pdl_enter();
     const uint64_t row0 = (static_cast<uint64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5)) * kMxRows;
     if (row0 >= a.rows) return;
     // the pieces of a row that starts between boundaries may be one more than its words
     for (uint64_t segment = blockIdx.y; segment < (a.cols + (ALIGNED ? 0 : 7) + 255) / 256; segment += gridDim.y) {
-        if (ALIGNED && row0 + kMxRows <= a.rows && (segment + 1) * 256 <= a.cols) values_inside<DT>(a, row0, segment);
-        else values_any<DT, ALIGNED>(a, row0, segment);
+        if (ALIGNED && row0 + kMxRows <= a.rows && (segment + 1) * 256 <= a.cols) values_inside<BITS, DT>(a, row0, segment);
+        else values_any<BITS, DT, ALIGNED>(a, row0, segment);
     }
 }
 
@@ -333,15 +293,27 @@ struct MxProductArgs {
     uint32_t hold;           // zero_debug_hold_matrix, or 0
 };
 
-constexpr int kMxN = 192, kMxK = 256;   // a stage's values of k are 128 bytes of a row
+constexpr int kMxN = 192;
 constexpr int kMxOutWarps = 8, kMxThreads = 64 + 32 * kMxOutWarps;
 constexpr uint32_t kMxOut = 32 * 32 * 2;   // a warp's output buffer, two each
-template <int MT>
+// A stage's values of k are 128 bytes of a row: 256 of 4 bits or 128 of 8, so
+// two scale tiles along k or one.  Its 128 bytes are four products of 32 bytes
+// in either width, and 8-bit ones run at half the rate: a stage moves and
+// takes as much time as one of 4 bits and covers half of its k.
+template <int BITS>
+struct MxStage {
+    static constexpr uint32_t kK = 1024 / BITS;       // values of k
+    static constexpr uint32_t kTiles = kK / 128;      // scale tiles along k
+    static constexpr uint32_t kSteps = 4 / kTiles;    // products for each of them
+};
+template <int BITS, int MT>
 struct MxTile {
-    static constexpr uint32_t kRows = 128 * MT, kA = kRows * 128, kB = kMxN * 128, kScaleA = 1024 * MT, kScaleB = 2048;
+    static constexpr uint32_t kTiles = MxStage<BITS>::kTiles;
+    static constexpr uint32_t kRows = 128 * MT, kA = kRows * 128, kB = kMxN * 128, kScaleA = 512 * kTiles * MT,
+                              kScaleB = 1024 * kTiles;
     static constexpr uint32_t kStage = kA + kB + kScaleA + kScaleB;
     static constexpr int kStages = MT == 2 ? 3 : 4;   // at most the sets of scales: a set is free once its stage is
-    static constexpr uint32_t kSet = 8 * MT + 16;     // columns of a set: 4 for 128 rows and 128 values of k
+    static constexpr uint32_t kSet = kTiles * (4 * MT + 8);   // columns of a set: 4 for 128 rows and 128 values of k
     static constexpr size_t kSmem = 1024 + kStages * kStage + kMxOutWarps * 2 * kMxOut;
     static_assert(2 * kMxN + 4 * kSet <= 512, "tensor memory");
     static_assert(kSmem >= kLeastTmemSmem, "see tmem_alloc");
@@ -358,13 +330,30 @@ __device__ __forceinline__ uint64_t scale_desc(uint32_t smem) {
 __device__ __forceinline__ void tc_copy_scales(uint32_t tmem, uint64_t d) {
     asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(d) : "memory");
 }
-__device__ __forceinline__ void mma_mx4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
-                                        bool accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
-        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(static_cast<uint32_t>(accumulate))
-        : "memory");
+// One product of 32 bytes of k.  Step j of a scale tile's takes its scales
+// from byte j * kTiles of the tile's words on (two of them for 64 4-bit
+// values), which the instruction's descriptor says.
+template <int BITS>
+__device__ __forceinline__ void mma_mx(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
+                                       bool accumulate) {
+    if constexpr (BITS == 4)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+            ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(static_cast<uint32_t>(accumulate))
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+            ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(static_cast<uint32_t>(accumulate))
+            : "memory");
+}
+// The instruction's descriptor: element types (e2m1 is 1 in the one kind, e4m3
+// 0 in the other), power-of-two scales, 128 x n.
+template <int BITS>
+__device__ constexpr uint32_t mx_idesc(uint32_t n) {
+    return (BITS == 4 ? (1u << 7) | (1u << 10) : 0u) | ((n >> 3) << 17) | (1u << 23) | (8u << 24);
 }
 
 // Tile t in bands of kBand tiles down, band after band: the tiles in flight
@@ -377,13 +366,13 @@ __device__ __forceinline__ void mx_tile(const MxProductArgs& p, uint32_t t, uint
     tm = band * kBand + in - tn * high;
 }
 
-template <int DT, int MT>
+template <int BITS, int DT, int MT>
 __global__ void __launch_bounds__(kMxThreads)
-k_mx4_product(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-              const __grid_constant__ CUtensorMap map_sa, const __grid_constant__ CUtensorMap map_sb,
-              const __grid_constant__ MxProductArgs p) {
-    using T = MxTile<MT>;
-    constexpr uint32_t kStages = T::kStages;
+k_mx_product(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+             const __grid_constant__ CUtensorMap map_sa, const __grid_constant__ CUtensorMap map_sb,
+             const __grid_constant__ MxProductArgs p) {
+    using T = MxTile<BITS, MT>;
+    constexpr uint32_t kStages = T::kStages, kTiles = T::kTiles, kSteps = MxStage<BITS>::kSteps;
     extern __shared__ unsigned char smem_raw[];
     __shared__ __align__(8) uint64_t bars[2 * kStages + 5];
     __shared__ uint32_t s_tmem;
@@ -411,7 +400,7 @@ k_mx4_product(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
     tc_fence_after();
     const uint32_t tmem = s_tmem;
     pdl_enter();
-    const uint32_t nk = (p.k + kMxK - 1) / kMxK;
+    const uint32_t nk = (p.k + MxStage<BITS>::kK - 1) / MxStage<BITS>::kK;
 
     if (warp == 0 && elect_one()) {
         Ring<kStages> r;
@@ -431,8 +420,8 @@ k_mx4_product(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
                 bar_expect(bar, T::kStage);
                 copy_box(st, &map_a, static_cast<int>(kb * 128), ra, 0, bar);
                 copy_box(st + T::kA, &map_b, static_cast<int>(kb * 128), rb, 0, bar);
-                copy_box(ss, &map_sa, 0, static_cast<int>(8 * kb), ra >> 7, bar);
-                copy_box(ss + T::kScaleA, &map_sb, 0, static_cast<int>(8 * kb), rb >> 7, bar);
+                copy_box(ss, &map_sa, 0, static_cast<int>(4 * kTiles * kb), ra >> 7, bar);
+                copy_box(ss + T::kScaleA, &map_sb, 0, static_cast<int>(4 * kTiles * kb), rb >> 7, bar);
             }
         }
         if (!ok) {   // the block must not leave with copies in flight
@@ -441,9 +430,7 @@ k_mx4_product(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
                 bar_drain(full + 8 * (i % kStages), (i / kStages) & 1, t0);
         }
     } else if (warp == 1 && elect_one()) {
-        // e2m1 operands, power-of-two scales, 128 x 192
-        constexpr uint32_t idesc =
-            (1u << 7) | (1u << 10) | (static_cast<uint32_t>(kMxN >> 3) << 17) | (1u << 23) | (8u << 24);
+        constexpr uint32_t idesc = mx_idesc<BITS>(kMxN);
         const uint64_t desc0 = operand_desc(ring, 0), scales0 = scale_desc(ring + T::kA + T::kB);
         Ring<kStages> r;
         uint32_t it = 0, n = 0;   // stages, and accumulators begun
@@ -460,14 +447,15 @@ k_mx4_product(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
                 tc_fence_after();
                 const uint64_t da = desc0 + r.s * (T::kStage >> 4), db = da + (T::kA >> 4);
                 const uint64_t ss = scales0 + r.s * (T::kStage >> 4);
-                const uint32_t sf = tmem + 2 * kMxN + (it & 3) * T::kSet, sfb = sf + 8 * MT;
+                const uint32_t sf = tmem + 2 * kMxN + (it & 3) * T::kSet, sfb = sf + 4 * kTiles * MT;
 #pragma unroll
-                for (uint32_t h = 0; h < 2; ++h) {   // per 128 values of k
+                for (uint32_t h = 0; h < kTiles; ++h) {   // per 128 values of k
 #pragma unroll
-                    for (uint32_t i = 0; i < MT; ++i) tc_copy_scales(sf + 8 * i + 4 * h, ss + (1024 >> 4) * i + (512 >> 4) * h);
+                    for (uint32_t i = 0; i < MT; ++i)
+                        tc_copy_scales(sf + 4 * (kTiles * i + h), ss + (512 >> 4) * (kTiles * i + h));
 #pragma unroll
                     for (uint32_t i = 0; i < 2; ++i)
-                        tc_copy_scales(sfb + 8 * h + 4 * i, ss + (T::kScaleA >> 4) + (1024 >> 4) * i + (512 >> 4) * h);
+                        tc_copy_scales(sfb + 8 * h + 4 * i, ss + (T::kScaleA >> 4) + (512 >> 4) * (kTiles * i + h));
                 }
 #pragma unroll
                 for (uint32_t i = 0; i < MT; ++i) {
@@ -480,13 +468,13 @@ k_mx4_product(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
                         tc_fence_after();
                     }
 #pragma unroll
-                    for (uint32_t h = 0; h < 2; ++h) {
-                        if (2 * kb + h >= p.tiles_k) break;
+                    for (uint32_t h = 0; h < kTiles; ++h) {
+                        if (kTiles * kb + h >= p.tiles_k) break;
 #pragma unroll
-                        for (uint32_t j = 0; j < 2; ++j)
-                            mma_mx4(d, da + (16384 >> 4) * i + (2 * h + j) * 2, db + (2 * h + j) * 2,
-                                    idesc | (2 * j << 4) | (2 * j << 29), sf + 8 * i + 4 * h, sfb + 8 * h + odd,
-                                    kb > 0 || h > 0 || j > 0);
+                        for (uint32_t j = 0; j < kSteps; ++j)
+                            mma_mx<BITS>(d, da + (16384 >> 4) * i + (kSteps * h + j) * 2, db + (kSteps * h + j) * 2,
+                                         idesc | (kTiles * j << 4) | (kTiles * j << 29), sf + 4 * (kTiles * i + h),
+                                         sfb + 8 * h + odd, kb > 0 || h > 0 || j > 0);
                     }
                     if (kb + 1 == nk) tc_commit(done + 8 * acc);
                 }
@@ -552,7 +540,7 @@ k_mx4_product(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
 // from the start.
 struct MxNarrowArgs {
     uint32_t m, n;
-    uint32_t tiles_k, stages;   // scale tiles along k; stages of 256 values
+    uint32_t tiles_k, stages;   // scale tiles along k; stages of 128 bytes
     uint32_t split;             // CTAs a cluster
     void* out;
     uint64_t ld;
@@ -560,22 +548,25 @@ struct MxNarrowArgs {
 };
 
 constexpr int kNarrowThreads = 192, kNarrowStages = 3;
-template <int NT>
+template <int BITS, int NT>
 struct Narrow {
-    static constexpr uint32_t kB = 128 * 128, kA = NT * 128, kStage = kB + kA + 2048;   // and 1 KiB of scales each
-    static constexpr size_t kSmem = 1024 + kNarrowStages * kStage;
+    static constexpr uint32_t kTiles = MxStage<BITS>::kTiles;
+    static constexpr uint32_t kB = 128 * 128, kA = NT * 128, kScale = 512 * kTiles, kStage = kB + kA + 2 * kScale;
+    static constexpr size_t kRing = 1024 + kNarrowStages * kStage;
+    static constexpr size_t kSmem = kRing < kLeastTmemSmem ? kLeastTmemSmem : kRing;
     static constexpr uint32_t kTmem = 128;   // the accumulator and four sets of scales
     static_assert(NT + 4 * 16 <= kTmem, "tensor memory");
     static_assert(kSmem >= kLeastTmemSmem, "see tmem_alloc");
     static_assert(kNarrowStages * kStage >= NT * 512, "the partial sums take the ring's place");
 };
 
-template <int DT, int NT>
+template <int BITS, int DT, int NT>
 __global__ void __launch_bounds__(kNarrowThreads)
-k_mx4_narrow(const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_a,
-             const __grid_constant__ CUtensorMap map_sb, const __grid_constant__ CUtensorMap map_sa,
-             const __grid_constant__ MxNarrowArgs p) {
-    using L = Narrow<NT>;
+k_mx_narrow(const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_a,
+            const __grid_constant__ CUtensorMap map_sb, const __grid_constant__ CUtensorMap map_sa,
+            const __grid_constant__ MxNarrowArgs p) {
+    using L = Narrow<BITS, NT>;
+    constexpr uint32_t kTiles = L::kTiles, kSteps = MxStage<BITS>::kSteps;
     extern __shared__ unsigned char smem_raw[];
     __shared__ __align__(8) uint64_t bars[2 * kNarrowStages + 1];
     __shared__ uint32_t s_tmem;
@@ -610,11 +601,11 @@ k_mx4_narrow(const __grid_constant__ CUtensorMap map_b, const __grid_constant__ 
             bar_expect(bar, L::kStage);
             copy_box(st, &map_b, static_cast<int>(kb * 128), static_cast<int>(tile * 128), 0, bar);
             copy_box(st + L::kB, &map_a, static_cast<int>(kb * 128), 0, 0, bar);
-            copy_box(st + L::kB + L::kA, &map_sb, 0, static_cast<int>(8 * kb), static_cast<int>(tile), bar);
-            copy_box(st + L::kB + L::kA + 1024, &map_sa, 0, static_cast<int>(8 * kb), 0, bar);
+            copy_box(st + L::kB + L::kA, &map_sb, 0, static_cast<int>(4 * kTiles * kb), static_cast<int>(tile), bar);
+            copy_box(st + L::kB + L::kA + L::kScale, &map_sa, 0, static_cast<int>(4 * kTiles * kb), 0, bar);
         }
     } else if (warp == 1 && elect_one()) {
-        constexpr uint32_t idesc = (1u << 7) | (1u << 10) | (static_cast<uint32_t>(NT >> 3) << 17) | (1u << 23) | (8u << 24);
+        constexpr uint32_t idesc = mx_idesc<BITS>(NT);
         const uint64_t desc0 = operand_desc(ring, 0), scales0 = scale_desc(ring + L::kB + L::kA);
         Ring<kNarrowStages> r;
         bool ok = true;
@@ -627,17 +618,18 @@ k_mx4_narrow(const __grid_constant__ CUtensorMap map_b, const __grid_constant__ 
             const uint64_t db = desc0 + r.s * (L::kStage >> 4), da = db + (L::kB >> 4), ss = scales0 + r.s * (L::kStage >> 4);
             const uint32_t sf = tmem + NT + ((kb - k0) & 3) * 16;
 #pragma unroll
-            for (uint32_t h = 0; h < 2; ++h) {
+            for (uint32_t h = 0; h < kTiles; ++h) {
                 tc_copy_scales(sf + 4 * h, ss + (512 >> 4) * h);
-                tc_copy_scales(sf + 8 + 4 * h, ss + (1024 >> 4) + (512 >> 4) * h);
+                tc_copy_scales(sf + 8 + 4 * h, ss + (L::kScale >> 4) + (512 >> 4) * h);
             }
 #pragma unroll
-            for (uint32_t h = 0; h < 2; ++h) {
-                if (2 * kb + h >= p.tiles_k) break;
+            for (uint32_t h = 0; h < kTiles; ++h) {
+                if (kTiles * kb + h >= p.tiles_k) break;
 #pragma unroll
-                for (uint32_t j = 0; j < 2; ++j)
-                    mma_mx4(tmem, db + (2 * h + j) * 2, da + (2 * h + j) * 2, idesc | (2 * j << 4) | (2 * j << 29),
-                                sf + 4 * h, sf + 8 + 4 * h, kb > k0 || h > 0 || j > 0);
+                for (uint32_t j = 0; j < kSteps; ++j)
+                    mma_mx<BITS>(tmem, db + (kSteps * h + j) * 2, da + (kSteps * h + j) * 2,
+                                 idesc | (kTiles * j << 4) | (kTiles * j << 29), sf + 4 * h, sf + 8 + 4 * h,
+                                 kb > k0 || h > 0 || j > 0);
             }
             tc_commit(empty + 8 * r.s);
         }
@@ -698,7 +690,7 @@ k_mx4_narrow(const __grid_constant__ CUtensorMap map_b, const __grid_constant__ 
 // -------------------------------------------------------------------- host
 constexpr uint64_t kMaxSide = 1ull << 30;
 
-uint64_t mx_pitch(uint64_t cols) { return up(cols, kMxBlock) / 2; }
+uint64_t mx_pitch(int bits, uint64_t cols) { return up(cols, kMxBlock) * bits / 8; }
 
 // Checks shared by the calls on one matrix; (rows, cols) are those of the codes.
 int mx_check(int dtype, uint64_t rows, uint64_t cols, const void* codes, const void* scales) {
@@ -717,71 +709,63 @@ dim3 row_grid(uint64_t rows, uint64_t cols) {
 }
 
 // The map of a matrix of codes in boxes of `box_rows` rows, and of its scale
-// tiles in boxes of 1 KiB (two tiles along k) by `box_tiles`.
+// tiles in boxes of a stage's tiles along k by `box_tiles`.
+template <int BITS>
 cudaError_t mx_maps(CUtensorMap* codes_map, CUtensorMap* scales_map, const void* codes, const void* scales, uint64_t rows,
                     uint64_t k, uint32_t box_rows, uint32_t box_tiles) {
-    const uint64_t pitch = mx_pitch(k), lines = up(k, 128) / 128 * 4;   // lines of 128 bytes in a row of scale tiles
+    const uint64_t pitch = mx_pitch(BITS, k), lines = up(k, 128) / 128 * 4;   // lines of 128 bytes in a row of scale tiles
     const cudaError_t e = make_map(codes_map, 1, codes, pitch, rows, 1, pitch, rows * pitch, 128, box_rows);
     return e != cudaSuccess ? e
-                            : make_map(scales_map, 1, scales, 128, lines, up(rows, 128) / 128, 128, lines * 128, 128, 8,
-                                       CU_TENSOR_MAP_SWIZZLE_NONE, box_tiles);
+                            : make_map(scales_map, 1, scales, 128, lines, up(rows, 128) / 128, 128, lines * 128, 128,
+                                       4 * MxStage<BITS>::kTiles, CU_TENSOR_MAP_SWIZZLE_NONE, box_tiles);
 }
 
-template <int NT>
-cudaError_t narrow_of(int dtype, uint64_t m, uint64_t n, uint64_t k, const void* a_codes, const void* a_scales,
-                      const void* b_codes, const void* b_scales, void* out, uint64_t ld, cudaStream_t s) {
+template <int BITS, int DT, int NT>
+cudaError_t narrow_of(uint64_t m, uint64_t n, uint64_t k, const void* a_codes, const void* a_scales, const void* b_codes,
+                      const void* b_scales, void* out, uint64_t ld, cudaStream_t s) {
+    using L = Narrow<BITS, NT>;
     CUtensorMap ma, mb, sa, sb;
     int sms = 0;
     cudaError_t e;
-    if ((e = sm_count(&sms)) != cudaSuccess || (e = mx_maps(&ma, &sa, a_codes, a_scales, m, k, NT, 1)) != cudaSuccess ||
-        (e = mx_maps(&mb, &sb, b_codes, b_scales, n, k, 128, 1)) != cudaSuccess)
+    if ((e = sm_count(&sms)) != cudaSuccess ||
+        (e = mx_maps<BITS>(&ma, &sa, a_codes, a_scales, m, k, NT, 1)) != cudaSuccess ||
+        (e = mx_maps<BITS>(&mb, &sb, b_codes, b_scales, n, k, 128, 1)) != cudaSuccess ||
+        (e = allow_smem<k_mx_narrow<BITS, DT, NT>>(L::kSmem)) != cudaSuccess)
         return e;
     MxNarrowArgs p = {};
     p.m = static_cast<uint32_t>(m);
     p.n = static_cast<uint32_t>(n);
     p.tiles_k = static_cast<uint32_t>(up(k, 128) / 128);
-    p.stages = static_cast<uint32_t>(up(k, kMxK) / kMxK);
+    p.stages = static_cast<uint32_t>(up(k, MxStage<BITS>::kK) / MxStage<BITS>::kK);
     p.hold = take_matrix_hold();
     p.out = out;
     p.ld = ld;
     const uint64_t tiles = up(n, 128) / 128;
     // shares of k: up to 8, as long as all CTAs are resident at once (by their shared memory) and a share keeps two stages
-    const uint64_t resident = static_cast<uint64_t>(sms) * (kSmemPerSm / (Narrow<NT>::kSmem + 1024));
+    const uint64_t resident = static_cast<uint64_t>(sms) * (kSmemPerSm / (L::kSmem + 1024));
     for (p.split = 1; p.split < 8 && 2 * tiles * p.split <= resident && p.stages >= 4 * p.split;) p.split *= 2;
-    const dim3 grid(static_cast<unsigned>(tiles * p.split));
-    if (dtype == ZERO_FP16) {
-        if ((e = allow_smem<k_mx4_narrow<kFp16, NT>>(Narrow<NT>::kSmem)) != cudaSuccess) return e;
-        return launch_pdl(k_mx4_narrow<kFp16, NT>, grid, kNarrowThreads, Narrow<NT>::kSmem, p.split, s, mb, ma, sb, sa, p);
-    }
-    if ((e = allow_smem<k_mx4_narrow<kBf16, NT>>(Narrow<NT>::kSmem)) != cudaSuccess) return e;
-    return launch_pdl(k_mx4_narrow<kBf16, NT>, grid, kNarrowThreads, Narrow<NT>::kSmem, p.split, s, mb, ma, sb, sa, p);
+    return launch_pdl(k_mx_narrow<BITS, DT, NT>, dim3(static_cast<unsigned>(tiles * p.split)), kNarrowThreads, L::kSmem,
+                      p.split, s, mb, ma, sb, sa, p);
 }
 
-}  // namespace
-
-static std::atomic<uint32_t> g_matrix_hold{0};
-uint32_t take_matrix_hold() { return g_matrix_hold.exchange(0); }
-
-cudaError_t mx4_gave_up(cudaStream_t s, int32_t* out) { return read_gave_up(s, out); }
-cudaError_t ortho_gave_up(cudaStream_t s, int32_t* out);   // zero_ortho.cu
-
-}  // namespace zg
-
-using namespace zg;
-
-extern "C" {
-
-uint64_t zero_mx4_codes_bytes(uint64_t rows, uint64_t cols) {
-    return rows > kMaxSide || cols > kMaxSide ? 0 : rows * mx_pitch(cols);
+template <int BITS, int DT, int MT>
+cudaError_t product_of(const MxProductArgs& p, uint64_t m, uint64_t n, uint64_t k, const void* a_codes,
+                       const void* a_scales, const void* b_codes, const void* b_scales, int sms, cudaStream_t s) {
+    using T = MxTile<BITS, MT>;
+    CUtensorMap ma, mb, sa, sb;
+    cudaError_t e;
+    if ((e = mx_maps<BITS>(&ma, &sa, a_codes, a_scales, m, k, T::kRows, MT)) != cudaSuccess ||
+        (e = mx_maps<BITS>(&mb, &sb, b_codes, b_scales, n, k, kMxN, 2)) != cudaSuccess ||
+        (e = allow_smem<k_mx_product<BITS, DT, MT>>(T::kSmem)) != cudaSuccess)
+        return e;
+    const dim3 grid(static_cast<unsigned>(p.total < static_cast<uint32_t>(sms) ? p.total : sms));
+    return launch_pdl(k_mx_product<BITS, DT, MT>, grid, kMxThreads, T::kSmem, 1, s, ma, mb, sa, sb, p);
 }
 
-uint64_t zero_mx4_scales_bytes(uint64_t rows, uint64_t cols) {
-    return rows > kMaxSide || cols > kMaxSide ? 0 : up(rows, 128) / 128 * (up(cols, 128) / 128) * 512;
-}
-
-int zero_mx4_quantize(int dtype, uint64_t rows, uint64_t cols, const void* src16, uint64_t ld, int transpose,
-                      void* codes, void* scales, void* stream) {
-    nvtxRangePushA("zero_mx4_quantize");
+template <int BITS>
+int mx_quantize(const char* name, int dtype, uint64_t rows, uint64_t cols, const void* src16, uint64_t ld, int transpose,
+                void* codes, void* scales, void* stream) {
+    nvtxRangePushA(name);
     struct Pop { ~Pop() { nvtxRangePop(); } } pop;
     if (const int rc = mx_check(dtype, rows, cols, codes, scales)) return rc;
     if (rows == 0 || cols == 0) return ZERO_OK;
@@ -797,27 +781,28 @@ int zero_mx4_quantize(int dtype, uint64_t rows, uint64_t cols, const void* src16
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (transpose) {
-        a.pitch = mx_pitch(rows);
+        a.pitch = mx_pitch(BITS, rows);
         a.tiles_k = up(rows, 128) / 128;
         if (a.tiles_k > 65535) return refuse(ZERO_EINVAL, "a transposed matrix has at most 65535 * 128 rows");
         const dim3 grid(static_cast<unsigned>(up(cols, 128) / 128), static_cast<unsigned>(a.tiles_k));
-        e = dtype == ZERO_FP16 ? launch_pdl(k_mx4_columns<kFp16>, grid, kThreads, 0, 1, s, a)
-                               : launch_pdl(k_mx4_columns<kBf16>, grid, kThreads, 0, 1, s, a);
+        e = launch_pdl(dtype == ZERO_FP16 ? k_mx_columns<BITS, kFp16> : k_mx_columns<BITS, kBf16>, grid, kThreads, 0, 1, s, a);
     } else {
-        a.pitch = mx_pitch(cols);
+        a.pitch = mx_pitch(BITS, cols);
         a.tiles_k = up(cols, 128) / 128;
         const dim3 grid = row_grid(up(rows, 128), cols);
         const bool fp16 = dtype == ZERO_FP16;
-        e = launch_pdl(aligned(src16, 16) && ld % 8 == 0 ? (fp16 ? k_mx4_rows<kFp16, true> : k_mx4_rows<kBf16, true>)
-                                                         : (fp16 ? k_mx4_rows<kFp16, false> : k_mx4_rows<kBf16, false>),
+        e = launch_pdl(aligned(src16, 16) && ld % 8 == 0
+                           ? (fp16 ? k_mx_rows<BITS, kFp16, true> : k_mx_rows<BITS, kBf16, true>)
+                           : (fp16 ? k_mx_rows<BITS, kFp16, false> : k_mx_rows<BITS, kBf16, false>),
                        grid, kThreads, 0, 1, s, a);
     }
-    return e == cudaSuccess ? ZERO_OK : cuda_refuse(e, "zero_mx4_quantize");
+    return e == cudaSuccess ? ZERO_OK : cuda_refuse(e, name);
 }
 
-int zero_mx4_dequantize(int dtype, uint64_t rows, uint64_t cols, const void* codes, const void* scales, void* out16,
-                        uint64_t ld, void* stream) {
-    nvtxRangePushA("zero_mx4_dequantize");
+template <int BITS>
+int mx_dequantize(const char* name, int dtype, uint64_t rows, uint64_t cols, const void* codes, const void* scales,
+                  void* out16, uint64_t ld, void* stream) {
+    nvtxRangePushA(name);
     struct Pop { ~Pop() { nvtxRangePop(); } } pop;
     if (const int rc = mx_check(dtype, rows, cols, codes, scales)) return rc;
     if (rows == 0 || cols == 0) return ZERO_OK;
@@ -830,21 +815,21 @@ int zero_mx4_dequantize(int dtype, uint64_t rows, uint64_t cols, const void* cod
     a.rows = rows;
     a.cols = cols;
     a.ld = ld;
-    a.pitch = mx_pitch(cols);
+    a.pitch = mx_pitch(BITS, cols);
     a.tiles_k = up(cols, 128) / 128;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool fp16 = dtype == ZERO_FP16, whole = aligned(out16, 16) && ld % 8 == 0;
     const dim3 grid = row_grid(rows, cols + (whole ? 0 : 7));
-    const cudaError_t e =
-        launch_pdl(whole ? (fp16 ? k_mx4_values<kFp16, true> : k_mx4_values<kBf16, true>)
-                                                     : (fp16 ? k_mx4_values<kFp16, false> : k_mx4_values<kBf16, false>),
-                   grid, kThreads, 0, 1, s, a);
-    return e == cudaSuccess ? ZERO_OK : cuda_refuse(e, "zero_mx4_dequantize");
+    const cudaError_t e = launch_pdl(whole ? (fp16 ? k_mx_values<BITS, kFp16, true> : k_mx_values<BITS, kBf16, true>)
+                                           : (fp16 ? k_mx_values<BITS, kFp16, false> : k_mx_values<BITS, kBf16, false>),
+                                     grid, kThreads, 0, 1, s, a);
+    return e == cudaSuccess ? ZERO_OK : cuda_refuse(e, name);
 }
 
-int zero_mx4_matmul(int dtype, uint64_t m, uint64_t n, uint64_t k, const void* a_codes, const void* a_scales,
-                    const void* b_codes, const void* b_scales, void* out16, uint64_t ld, void* stream) {
-    nvtxRangePushA("zero_mx4_matmul");
+template <int BITS>
+int mx_matmul(const char* name, int dtype, uint64_t m, uint64_t n, uint64_t k, const void* a_codes, const void* a_scales,
+              const void* b_codes, const void* b_scales, void* out16, uint64_t ld, void* stream) {
+    nvtxRangePushA(name);
     struct Pop { ~Pop() { nvtxRangePop(); } } pop;
     if (const int rc = mx_check(dtype, m, k, a_codes, a_scales)) return rc;
     if (const int rc = mx_check(dtype, n, k, b_codes, b_scales)) return rc;
@@ -852,18 +837,20 @@ int zero_mx4_matmul(int dtype, uint64_t m, uint64_t n, uint64_t k, const void* a
     if (!out16 || !aligned(out16, 2)) return refuse(ZERO_EINVAL, "out16 is NULL or not 2-byte aligned");
     if (ld < n || ld > (1ull << 40)) return refuse(ZERO_EINVAL, "ld must be at least n (and at most 2^40)");
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool fp16 = dtype == ZERO_FP16;
     cudaError_t e;
     if (k == 0) {   // an empty sum
         e = cudaMemset2DAsync(out16, ld * 2, 0, n * 2, m, s);
-        return e == cudaSuccess ? ZERO_OK : cuda_refuse(e, "zero_mx4_matmul");
+        return e == cudaSuccess ? ZERO_OK : cuda_refuse(e, name);
     }
     if (m <= 32) {
-        e = m <= 16 ? narrow_of<16>(dtype, m, n, k, a_codes, a_scales, b_codes, b_scales, out16, ld, s)
-                    : narrow_of<32>(dtype, m, n, k, a_codes, a_scales, b_codes, b_scales, out16, ld, s);
-        return e == cudaSuccess ? ZERO_OK : cuda_refuse(e, "zero_mx4_matmul");
+        const auto of = m <= 16 ? (fp16 ? narrow_of<BITS, kFp16, 16> : narrow_of<BITS, kBf16, 16>)
+                                : (fp16 ? narrow_of<BITS, kFp16, 32> : narrow_of<BITS, kBf16, 32>);
+        e = of(m, n, k, a_codes, a_scales, b_codes, b_scales, out16, ld, s);
+        return e == cudaSuccess ? ZERO_OK : cuda_refuse(e, name);
     }
     int sms = 0;
-    if ((e = sm_count(&sms)) != cudaSuccess) return cuda_refuse(e, "zero_mx4_matmul");
+    if ((e = sm_count(&sms)) != cudaSuccess) return cuda_refuse(e, name);
     // 256 rows a tile are cheaper a row (1224 cycles a stage against 863 for 128) unless they leave SMs idle
     const uint64_t across = up(n, kMxN) / kMxN;
     auto rounds = [&](uint64_t rows) { return (up(m, rows) / rows * across + sms - 1) / sms; };
@@ -882,24 +869,70 @@ int zero_mx4_matmul(int dtype, uint64_t m, uint64_t n, uint64_t k, const void* a
     p.ld = ld;
     p.vec = aligned(out16, 16) && ld % 8 == 0;
     p.hold = take_matrix_hold();
-    CUtensorMap ma, mb, sa, sb;
-    if ((e = mx_maps(&ma, &sa, a_codes, a_scales, m, k, static_cast<uint32_t>(rows), tall ? 2 : 1)) != cudaSuccess ||
-        (e = mx_maps(&mb, &sb, b_codes, b_scales, n, k, kMxN, 2)) != cudaSuccess)
-        return cuda_refuse(e, "tensor map");
-    const dim3 grid(static_cast<unsigned>(tiles < static_cast<uint64_t>(sms) ? tiles : sms));
-    const bool fp16 = dtype == ZERO_FP16;
-    if (tall) {
-        constexpr size_t smem = MxTile<2>::kSmem;
-        if ((e = allow_smem<k_mx4_product<kFp16, 2>>(smem)) == cudaSuccess &&
-            (e = allow_smem<k_mx4_product<kBf16, 2>>(smem)) == cudaSuccess)
-            e = launch_pdl(fp16 ? k_mx4_product<kFp16, 2> : k_mx4_product<kBf16, 2>, grid, kMxThreads, smem, 1, s, ma, mb, sa, sb, p);
-    } else {
-        constexpr size_t smem = MxTile<1>::kSmem;
-        if ((e = allow_smem<k_mx4_product<kFp16, 1>>(smem)) == cudaSuccess &&
-            (e = allow_smem<k_mx4_product<kBf16, 1>>(smem)) == cudaSuccess)
-            e = launch_pdl(fp16 ? k_mx4_product<kFp16, 1> : k_mx4_product<kBf16, 1>, grid, kMxThreads, smem, 1, s, ma, mb, sa, sb, p);
-    }
-    return e == cudaSuccess ? ZERO_OK : cuda_refuse(e, "zero_mx4_matmul");
+    const auto of = tall ? (fp16 ? product_of<BITS, kFp16, 2> : product_of<BITS, kBf16, 2>)
+                         : (fp16 ? product_of<BITS, kFp16, 1> : product_of<BITS, kBf16, 1>);
+    e = of(p, m, n, k, a_codes, a_scales, b_codes, b_scales, sms, s);
+    return e == cudaSuccess ? ZERO_OK : cuda_refuse(e, name);
+}
+
+}  // namespace
+
+static std::atomic<uint32_t> g_matrix_hold{0};
+uint32_t take_matrix_hold() { return g_matrix_hold.exchange(0); }
+
+cudaError_t mx4_gave_up(cudaStream_t s, int32_t* out) { return read_gave_up(s, out); }
+cudaError_t ortho_gave_up(cudaStream_t s, int32_t* out);   // zero_ortho.cu
+
+}  // namespace zg
+
+using namespace zg;
+
+extern "C" {
+
+uint64_t zero_mx4_codes_bytes(uint64_t rows, uint64_t cols) {
+    return rows > kMaxSide || cols > kMaxSide ? 0 : rows * mx_pitch(4, cols);
+}
+
+uint64_t zero_mx4_scales_bytes(uint64_t rows, uint64_t cols) {
+    return rows > kMaxSide || cols > kMaxSide ? 0 : up(rows, 128) / 128 * (up(cols, 128) / 128) * 512;
+}
+
+int zero_mx4_quantize(int dtype, uint64_t rows, uint64_t cols, const void* src16, uint64_t ld, int transpose,
+                      void* codes, void* scales, void* stream) {
+    return mx_quantize<4>("zero_mx4_quantize", dtype, rows, cols, src16, ld, transpose, codes, scales, stream);
+}
+
+int zero_mx4_dequantize(int dtype, uint64_t rows, uint64_t cols, const void* codes, const void* scales, void* out16,
+                        uint64_t ld, void* stream) {
+    return mx_dequantize<4>("zero_mx4_dequantize", dtype, rows, cols, codes, scales, out16, ld, stream);
+}
+
+int zero_mx4_matmul(int dtype, uint64_t m, uint64_t n, uint64_t k, const void* a_codes, const void* a_scales,
+                    const void* b_codes, const void* b_scales, void* out16, uint64_t ld, void* stream) {
+    return mx_matmul<4>("zero_mx4_matmul", dtype, m, n, k, a_codes, a_scales, b_codes, b_scales, out16, ld, stream);
+}
+
+uint64_t zero_mx8_codes_bytes(uint64_t rows, uint64_t cols) {
+    return rows > kMaxSide || cols > kMaxSide ? 0 : rows * mx_pitch(8, cols);
+}
+
+uint64_t zero_mx8_scales_bytes(uint64_t rows, uint64_t cols) {
+    return rows > kMaxSide || cols > kMaxSide ? 0 : up(rows, 128) / 128 * (up(cols, 128) / 128) * 512;
+}
+
+int zero_mx8_quantize(int dtype, uint64_t rows, uint64_t cols, const void* src16, uint64_t ld, int transpose,
+                      void* codes, void* scales, void* stream) {
+    return mx_quantize<8>("zero_mx8_quantize", dtype, rows, cols, src16, ld, transpose, codes, scales, stream);
+}
+
+int zero_mx8_dequantize(int dtype, uint64_t rows, uint64_t cols, const void* codes, const void* scales, void* out16,
+                        uint64_t ld, void* stream) {
+    return mx_dequantize<8>("zero_mx8_dequantize", dtype, rows, cols, codes, scales, out16, ld, stream);
+}
+
+int zero_mx8_matmul(int dtype, uint64_t m, uint64_t n, uint64_t k, const void* a_codes, const void* a_scales,
+                    const void* b_codes, const void* b_scales, void* out16, uint64_t ld, void* stream) {
+    return mx_matmul<8>("zero_mx8_matmul", dtype, m, n, k, a_codes, a_scales, b_codes, b_scales, out16, ld, stream);
 }
 
 int zero_debug_hold_matrix(int64_t stage) {
@@ -917,7 +950,7 @@ int zero_matrix_status(void* stream) {
         const char* what[] = {"", "space", "data", "products", "inputs"};
         const int32_t w = a ? a : b;
         return refuse(ZERO_ETIMEOUT, std::string("a bounded wait inside a kernel of ") +
-                                         (a ? "zero_orthogonalize" : "zero_mx4_matmul") + " gave up, for " +
+                                         (a ? "zero_orthogonalize" : "zero_mx4_matmul or zero_mx8_matmul") + " gave up, for " +
                                          what[w >= 1 && w <= 4 ? w : 0] + ": its output is incomplete");
     }
     return ZERO_OK;

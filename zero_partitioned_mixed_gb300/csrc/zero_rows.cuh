@@ -113,5 +113,60 @@ __device__ __forceinline__ void mul2(float& a, float& b, float by) {
     asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
 }
 
+// 8 values of a row from column c on, `valid` of them inside it, into a row
+// that may start anywhere.
+template <bool ALIGNED>
+__device__ __forceinline__ void store8(unsigned short* row, uint64_t c, int valid, const uint32_t (&w)[4]) {
+    if (ALIGNED && valid == 8) {
+        __stcs(reinterpret_cast<uint4*>(row + c), make_uint4(w[0], w[1], w[2], w[3]));
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e < valid) row[c + e] = static_cast<unsigned short>(w[e >> 1] >> (16 * (e & 1)));
+    }
+}
+// A read near a row's or the matrix's end: rare, so one copy of its code.
+__device__ __noinline__ uint4 read8_edge(const unsigned short* base, uint64_t at, int valid) {
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (e < valid) w[e >> 1] |= static_cast<uint32_t>(__ldcs(base + at + e)) << (16 * (e & 1));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// The same read, with zeros for what is outside; total: values from `base` to
+// the matrix's end.  A row that starts between two 16-byte boundaries (not
+// ALIGNED) is read as the two aligned pieces around the 8 values.
+template <bool ALIGNED>
+__device__ __forceinline__ void read8(const unsigned short* base, uint64_t at, int valid, uint64_t total, uint32_t (&w)[4]) {
+    if (ALIGNED ? valid == 8 : valid == 8 && at >= 8 && at + 16 <= total) {
+        const uint32_t m = ALIGNED ? 0u : static_cast<uint32_t>((reinterpret_cast<uintptr_t>(base) >> 1) + at) & 7u;
+        const uint4* from = reinterpret_cast<const uint4*>(base + at - m);
+        const uint4 x = ALIGNED ? __ldcs(from) : *from;
+        const uint32_t own[4] = {x.x, x.y, x.z, x.w};
+        if (m == 0) {
+            w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+        } else {   // the second piece is the next lane's first: the cache serves it
+            const uint4 y = from[1];
+            const uint32_t next[4] = {y.x, y.y, y.z, y.w};
+            shift_halves(own, next, m, w);
+        }
+    } else if (valid > 0) {
+        const uint4 x = read8_edge(base, at, valid);
+        w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+    } else {
+        w[0] = w[1] = w[2] = w[3] = 0u;
+    }
+}
+template <int DT>
+__device__ __forceinline__ void widen8(const uint32_t (&w)[4], float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) widen2<DT>(w[i], v[2 * i], v[2 * i + 1]);
+}
+template <int DT>
+__device__ __forceinline__ void narrow8(const float (&v)[8], uint32_t (&w)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = narrow2<DT>(v[2 * i], v[2 * i + 1]);
+}
+
 }  // namespace
 }  // namespace zg

@@ -16,7 +16,8 @@ from typing import Dict, List, Optional, Sequence, Tuple
 import torch
 
 from . import _binding as B
-from .mx4 import Mx4Matrix
+from .mx4 import Mx4Matrix, MxMatrix
+from .mx8 import Mx8Matrix
 from .synth import torch_dtype
 
 _ZDT = {"fp16": B.ZERO_FP16, "bf16": B.ZERO_BF16}
@@ -88,10 +89,12 @@ class MuonBuffers:
                                  scale=float(scale(r, c)), stream=stream, state=self.state)
         B.zero_muon_apply(dt, self.count, self.ortho, self.master, self._param_rows, hyp, self.state, stream)
 
-    def quantize(self, i: int, transpose: bool = False, rank: int = 0) -> Mx4Matrix:
-        """Matrix i of a rank's replica in microscaled 4 bits, ready to multiply with.
+    def quantize(self, i: int, transpose: bool = False, rank: int = 0, bits: int = 4) -> MxMatrix:
+        """Matrix i of a rank's replica in microscaled 4 (or 8) bits, ready to multiply with.
         transpose: along its columns, as the backward pass takes it."""
-        return Mx4Matrix.of(self.matrix(i, self.params[rank]), transpose)
+        if bits not in (4, 8):
+            raise B.ZeroError(1, f"bits must be 4 or 8, got {bits}")
+        return (Mx4Matrix if bits == 4 else Mx8Matrix).of(self.matrix(i, self.params[rank]), transpose)
 
     def status(self, stream=None) -> dict:
         """The state after the last step; raises when a kernel's bounded wait gave up (a step in whose

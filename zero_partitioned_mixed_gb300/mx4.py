@@ -1,4 +1,4 @@
-"""Matrices in microscaled 4-bit floats, and linear layers on them.
+"""Matrices in microscaled 4-bit floats, and linear layers on them (mx8.py has those in 8 bits).
 
 A rank that holds its parameters in 4 bits multiplies with the codes as they
 are; the three products of a layer's training step are one call on
@@ -38,46 +38,63 @@ def _rows(t: torch.Tensor) -> int:
     return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
-class Mx4Matrix:
-    """Codes and scales of a rows x cols matrix, in the library's layout."""
+class MxMatrix:
+    """Codes and scales of a rows x cols matrix, in the library's layout; Mx4Matrix and mx8.Mx8Matrix say in which width."""
+
+    bits = 0
 
     def __init__(self, rows: int, cols: int, device="cuda"):
         self.rows, self.cols = rows, cols
-        self.codes = torch.empty(max(16, B.zero_mx4_codes_bytes(rows, cols)), dtype=torch.uint8, device=device)
-        self.scales = torch.empty(max(16, B.zero_mx4_scales_bytes(rows, cols)), dtype=torch.uint8, device=device)
+        self.codes = torch.empty(max(16, self._codes_bytes(rows, cols)), dtype=torch.uint8, device=device)
+        self.scales = torch.empty(max(16, self._scales_bytes(rows, cols)), dtype=torch.uint8, device=device)
 
     @classmethod
-    def of(cls, src: torch.Tensor, transpose: bool = False) -> "Mx4Matrix":
+    def of(cls, src: torch.Tensor, transpose: bool = False) -> "MxMatrix":
         r, c = src.shape
         return cls(*((c, r) if transpose else (r, c)), device=src.device).fill(src, transpose)
 
-    def fill(self, src: torch.Tensor, transpose: bool = False) -> "Mx4Matrix":
+    def fill(self, src: torch.Tensor, transpose: bool = False) -> "MxMatrix":
         """Quantise src along its rows, or along its columns (then self holds its transpose)."""
         r, c = src.shape
         if ((c, r) if transpose else (r, c)) != (self.rows, self.cols):
             raise B.ZeroError(1, f"expected a matrix for {self.rows} x {self.cols}, got {tuple(src.shape)}")
         _same_gpu(src, self.codes, self.scales)
-        B.zero_mx4_quantize(_dtype(src), r, c, src, self.codes, self.scales, ld=_rows(src), transpose=transpose)
+        self._quantize(_dtype(src), r, c, src, self.codes, self.scales, ld=_rows(src), transpose=transpose)
         return self
 
     def values(self, dtype=torch.bfloat16) -> torch.Tensor:
         _same_gpu(self.codes, self.scales)
         out = torch.empty((self.rows, self.cols), dtype=dtype, device=self.codes.device)
-        B.zero_mx4_dequantize(_dtype(out), self.rows, self.cols, self.codes, self.scales, out)
+        self._dequantize(_dtype(out), self.rows, self.cols, self.codes, self.scales, out)
         return out
+
+    @classmethod
+    def product(cls, a: "MxMatrix", b: "MxMatrix", dtype=torch.bfloat16, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """a b^T, both quantised along the dimension that is summed over."""
+        for m in (a, b):
+            if not isinstance(m, cls):
+                raise B.ZeroError(1, f"expected a {cls.__name__}, got a {type(m).__name__}")
+        if a.cols != b.cols:
+            raise B.ZeroError(1, f"the operands have {a.cols} and {b.cols} columns")
+        if out is None:
+            out = torch.empty((a.rows, b.rows), dtype=dtype, device=a.codes.device)
+        elif tuple(out.shape) != (a.rows, b.rows):
+            raise B.ZeroError(1, f"out must be {a.rows} x {b.rows}")
+        _same_gpu(out, a.codes, a.scales, b.codes, b.scales)
+        cls._matmul(_dtype(out), a.rows, b.rows, a.cols, a.codes, a.scales, b.codes, b.scales, out, ld=_rows(out))
+        return out
+
+
+class Mx4Matrix(MxMatrix):
+    bits = 4
+    _codes_bytes, _scales_bytes = staticmethod(B.zero_mx4_codes_bytes), staticmethod(B.zero_mx4_scales_bytes)
+    _quantize, _dequantize = staticmethod(B.zero_mx4_quantize), staticmethod(B.zero_mx4_dequantize)
+    _matmul = staticmethod(B.zero_mx4_matmul)
 
 
 def mx4_product(a: Mx4Matrix, b: Mx4Matrix, dtype=torch.bfloat16, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """a b^T, both quantised along the dimension that is summed over."""
-    if a.cols != b.cols:
-        raise B.ZeroError(1, f"the operands have {a.cols} and {b.cols} columns")
-    if out is None:
-        out = torch.empty((a.rows, b.rows), dtype=dtype, device=a.codes.device)
-    elif tuple(out.shape) != (a.rows, b.rows):
-        raise B.ZeroError(1, f"out must be {a.rows} x {b.rows}")
-    _same_gpu(out, a.codes, a.scales, b.codes, b.scales)
-    B.zero_mx4_matmul(_dtype(out), a.rows, b.rows, a.cols, a.codes, a.scales, b.codes, b.scales, out, ld=_rows(out))
-    return out
+    return Mx4Matrix.product(a, b, dtype, out)
 
 
 def mx4_linear(x: torch.Tensor, w: Mx4Matrix, out: Optional[torch.Tensor] = None,
