@@ -26,8 +26,8 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "zero_gb300.h"
-#include "zero_host.h"
 #include "zero_rows.cuh"
+#include "zero_tc.cuh"
 
 namespace zg {
 namespace {
@@ -74,8 +74,7 @@ __global__ void __launch_bounds__(kThreads) k_embedding(const __grid_constant__ 
         if (t0 + i >= a.tokens) continue;
         float v[8];
         widen8<DT>(w[i], v);
-#pragma unroll
-        for (int e = 0; e < 8; e += 2) mul2(v[e], v[e + 1], a.scale);
+        mul8(v, a.scale);
         uint32_t q[4];
         narrow8<DT>(v, q);
         store8<ALIGNED>(a.out + (t0 + i) * a.ld_out, c, valid, q);
@@ -91,24 +90,14 @@ struct SortArgs {
     int wide_ids;
     uint32_t passes, digit_bits;
     uint32_t *key[2], *index[2];   // the sorted ones end in [(passes - 1) & 1]
-    // what the other CTAs fill with zeros, as rows
+    // what the other CTAs fill with zeros: rows, or one range
     unsigned short* zero;
-    uint64_t zero_rows, zero_cols, zero_ld, zero_total;   // total: from the first row's start to the last one's end
+    uint64_t zero_rows, zero_cols, zero_ld;
 };
 
-__device__ __forceinline__ uint32_t cta_of_cluster() {
-    uint32_t r;
-    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void wait_for_cluster() {
-    __syncwarp();
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 __device__ __forceinline__ uint32_t load_of_cta(const uint32_t* shared, uint32_t cta) {
-    uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(shared)), there, x;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(at), "r"(cta));
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(there) : "memory");
+    uint32_t x;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(cluster_addr(smem_u32(shared), cta)) : "memory");
     return x;
 }
 // What other CTAs of the cluster wrote comes from L2, not from this SM's L1.
@@ -118,27 +107,53 @@ __device__ __forceinline__ uint32_t load_l2(const uint32_t* p) {
     return x;
 }
 
-__device__ void fill_zeros(const SortArgs& a, uint64_t warp, uint64_t warps) {
-    const uint32_t lane = threadIdx.x & 31;
-    for (uint64_t r = warp; r < a.zero_rows; r += warps) {
+constexpr uint32_t kZeroBytes = 16384;
+
+// By CTA `cta` of `ctas`.  Rows without gaps are one range, which a thread a
+// CTA fills by bulk copies of `zeros` (77 MB in 12 us; 16-byte stores of all
+// threads took 18); rows with gaps a warp each.
+__device__ void fill_zeros(const SortArgs& a, uint4 (&zeros)[kZeroBytes / 16], uint32_t cta, uint32_t ctas) {
+    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (a.zero_rows == 1) {
+        for (uint32_t i = threadIdx.x; i < kZeroBytes / 16; i += kSortThreads) zeros[i] = make_uint4(0u, 0u, 0u, 0u);
+        proxy_fence_shared();
+        __syncthreads();
+        uint64_t head = (16 - (reinterpret_cast<uintptr_t>(a.zero) & 15)) / 2 % 8;
+        if (head > a.zero_cols) head = a.zero_cols;
+        const uint64_t body = (a.zero_cols - head) / 8 * 16, done = head + body / 2;   // bytes of whole pieces
+        if (warp == 1 && cta == 0) {
+            if (lane < head) a.zero[lane] = 0;
+            if (lane < a.zero_cols - done) a.zero[done + lane] = 0;
+        }
+        if (threadIdx.x != 0) return;
+        unsigned char* to = reinterpret_cast<unsigned char*>(a.zero + head);
+        for (uint64_t at = static_cast<uint64_t>(cta) * kZeroBytes; at < body; at += static_cast<uint64_t>(ctas) * kZeroBytes) {
+            const uint32_t n = body - at < kZeroBytes ? static_cast<uint32_t>(body - at) : kZeroBytes;
+            asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;"
+                         ::"l"(to + at), "r"(smem_u32(zeros)), "r"(n)
+                         : "memory");
+        }
+        store_commit();
+        store_wait<0>();
+        return;
+    }
+    for (uint64_t r = static_cast<uint64_t>(cta) * 32 + warp; r < a.zero_rows; r += static_cast<uint64_t>(ctas) * 32) {
         unsigned short* row = a.zero + r * a.zero_ld;
-        const uint64_t left = a.zero_total - r * a.zero_ld, cols = left < a.zero_cols ? left : a.zero_cols;
         uint64_t head = (16 - (reinterpret_cast<uintptr_t>(row) & 15)) / 2 % 8;
-        if (head > cols) head = cols;
-        const uint64_t pieces = (cols - head) / 8;
+        if (head > a.zero_cols) head = a.zero_cols;
+        const uint64_t pieces = (a.zero_cols - head) / 8, done = head + 8 * pieces;
         if (lane < head) row[lane] = 0;
         for (uint64_t i = lane; i < pieces; i += 32) reinterpret_cast<uint4*>(row + head)[i] = make_uint4(0u, 0u, 0u, 0u);
-        const uint64_t done = head + 8 * pieces;
-        if (lane < cols - done) row[done + lane] = 0;
+        if (lane < a.zero_cols - done) row[done + lane] = 0;
     }
 }
 
 __global__ void __launch_bounds__(kSortThreads) k_embedding_sort(const __grid_constant__ SortArgs a) {
     pdl_enter();
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    __shared__ __align__(128) uint4 s_zeros[kZeroBytes / 16];
     if (blockIdx.x >= kSortCtas) {
-        fill_zeros(a, static_cast<uint64_t>(blockIdx.x - kSortCtas) * 32 + warp,
-                   static_cast<uint64_t>(gridDim.x - kSortCtas) * 32);
+        fill_zeros(a, s_zeros, blockIdx.x - kSortCtas, gridDim.x - kSortCtas);
         return;
     }
     __shared__ uint32_t s_count[kDigits];                    // this CTA's keys of each digit
@@ -146,7 +161,7 @@ __global__ void __launch_bounds__(kSortThreads) k_embedding_sort(const __grid_co
     __shared__ uint32_t s_tile[kDigits];                     // the same at the tile's start
     __shared__ unsigned short s_warp[kSortThreads / 32][kDigits];   // a tile's keys of each digit, by warp
     __shared__ uint32_t s_scan[kDigits / 32];
-    const uint32_t me = cta_of_cluster();
+    const uint32_t me = cluster_rank();
     const uint64_t share = (a.tokens + kSortCtas - 1) / kSortCtas, first = me * share;
     const uint64_t end = first >= a.tokens ? first : first + share < a.tokens ? first + share : a.tokens;
     for (uint32_t pass = 0; pass < a.passes; ++pass) {
@@ -158,7 +173,7 @@ __global__ void __launch_bounds__(kSortThreads) k_embedding_sort(const __grid_co
         if (threadIdx.x < kDigits) s_count[threadIdx.x] = 0;
         __syncthreads();
         for (uint64_t i = first + threadIdx.x; i < end; i += kSortThreads) atomicAdd(&s_count[(key_of(i) >> shift) & mask], 1u);
-        wait_for_cluster();
+        cluster_sync();
         // keys of smaller digits anywhere, and of the same digit in the CTAs before
         if (threadIdx.x < kDigits) {
             uint32_t before = 0, all = 0;
@@ -215,7 +230,7 @@ __global__ void __launch_bounds__(kSortThreads) k_embedding_sort(const __grid_co
             }
             __syncthreads();
         }
-        wait_for_cluster();
+        cluster_sync();
     }
 }
 
@@ -230,20 +245,18 @@ struct SumArgs {
     float scale;
     int add;                       // to what the table holds
 };
-constexpr uint32_t kPiece = 16, kSumLoads = 8;
+constexpr uint32_t kPiece = 16;
 
 template <int DT, bool ALIGNED>
 __device__ __forceinline__ void write_sum(const SumArgs& a, uint32_t id, uint64_t c, int valid, float (&s)[8]) {
-#pragma unroll
-    for (int e = 0; e < 8; e += 2) mul2(s[e], s[e + 1], a.scale);
+    mul8(s, a.scale);
     unsigned short* row = a.table + id * a.ld_table;
     if (a.add) {
         uint32_t w[4];
         read8<ALIGNED>(a.table, id * a.ld_table + c, valid, (a.vocab - 1) * a.ld_table + a.dim, w);
         float v[8];
         widen8<DT>(w, v);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s[e] = __fadd_rn(v[e], s[e]);
+        add8(s, v);
     }
     uint32_t q[4];
     narrow8<DT>(s, q);
@@ -251,6 +264,14 @@ __device__ __forceinline__ void write_sum(const SumArgs& a, uint32_t id, uint64_
 }
 __device__ __forceinline__ float* partial_at(const SumArgs& a, uint64_t piece, int leaves, uint64_t c) {
     return a.partial + (2 * piece + leaves) * a.width + c;
+}
+
+__device__ __forceinline__ void write_partial(const SumArgs& a, uint64_t piece, int leaves, uint64_t c, int valid,
+                                              const float (&s)[8]) {
+    if (valid <= 0) return;
+    float4* to = reinterpret_cast<float4*>(partial_at(a, piece, leaves, c));
+    to[0] = make_float4(s[0], s[1], s[2], s[3]);
+    to[1] = make_float4(s[4], s[5], s[6], s[7]);
 }
 
 template <int DT, bool ALIGNED>
@@ -275,87 +296,112 @@ __global__ void __launch_bounds__(kThreads) k_embedding_sum(const __grid_constan
     float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
     uint32_t id = __shfl_sync(0xFFFFFFFFu, key, 0);
     bool enters = first > 0 && id == before;   // the run began in an earlier piece
-#pragma unroll 1
-    for (uint32_t i0 = 0; i0 < count; i0 += kSumLoads) {
-        uint32_t w[kSumLoads][4];
+    uint32_t w[kPiece][4];
 #pragma unroll
-        for (uint32_t i = 0; i < kSumLoads; ++i) {
-            const uint64_t t = __shfl_sync(0xFFFFFFFFu, index, i0 + i);
-            w[i][0] = w[i][1] = w[i][2] = w[i][3] = 0u;
-            if (i0 + i < count) read8<ALIGNED>(a.grad, t * a.ld_grad + c, valid, total, w[i]);
-        }
-#pragma unroll
-        for (uint32_t i = 0; i < kSumLoads; ++i) {
-            const uint32_t next = __shfl_sync(0xFFFFFFFFu, key, i0 + i);
-            if (i0 + i >= count) continue;
-            if (next != id) {   // the run is complete here
-                if (enters) {
-                    if (valid > 0) {
-                        float4* to = reinterpret_cast<float4*>(partial_at(a, piece, 0, c));
-                        to[0] = make_float4(s[0], s[1], s[2], s[3]);
-                        to[1] = make_float4(s[4], s[5], s[6], s[7]);
-                    }
-                } else {
-                    write_sum<DT, ALIGNED>(a, id, c, valid, s);
-                }
-                id = next;
-                enters = false;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) s[e] = 0.0f;
-            }
-            float v[8];
-            widen8<DT>(w[i], v);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) s[e] = __fadd_rn(s[e], v[e]);
-        }
+    for (uint32_t i = 0; i < kPiece; ++i) {
+        const uint64_t t = __shfl_sync(0xFFFFFFFFu, index, i);
+        read8<ALIGNED>(a.grad, t * a.ld_grad + c, i < count ? valid : 0, total, w[i]);
     }
-    if (enters || (count == kPiece && id == after)) {
-        if (valid > 0) {
-            float4* to = reinterpret_cast<float4*>(partial_at(a, piece, enters ? 0 : 1, c));
-            to[0] = make_float4(s[0], s[1], s[2], s[3]);
-            to[1] = make_float4(s[4], s[5], s[6], s[7]);
+#pragma unroll
+    for (uint32_t i = 0; i < kPiece; ++i) {
+        const uint32_t next = __shfl_sync(0xFFFFFFFFu, key, i);
+        if (i >= count) break;
+        if (next != id) {   // the run is complete here
+            if (enters) write_partial(a, piece, 0, c, valid, s);
+            else write_sum<DT, ALIGNED>(a, id, c, valid, s);
+            id = next;
+            enters = false;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[e] = 0.0f;
         }
-    } else {
-        write_sum<DT, ALIGNED>(a, id, c, valid, s);
+        float v[8];
+        widen8<DT>(w[i], v);
+        add8(s, v);
     }
+    if (enters || (count == kPiece && id == after)) write_partial(a, piece, enters ? 0 : 1, c, valid, s);
+    else write_sum<DT, ALIGNED>(a, id, c, valid, s);
 }
 
-// A warp for each piece and 256 columns; it has work where a run begins in
-// the piece and goes on in the next one.
+// A block looks at kJoinPieces pieces, a warp each, for a run that begins in
+// the piece and goes on in the next one, and adds its partial sums of 256
+// columns.  A warp adds a run over up to kShortRun pieces by itself; the
+// block's warps share the others (the frequent tokens of a language model's
+// batch cover some ten pieces each), every eighth piece a warp, and add their
+// sums in order.
+constexpr uint32_t kJoinPieces = kThreads / 32, kShortRun = 8;
+
 template <int DT, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads) k_embedding_join(const __grid_constant__ SumArgs a) {
     pdl_enter();
-    const uint64_t item = static_cast<uint64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-    const uint64_t piece = item / a.segments;
-    if (piece + 1 >= a.pieces) return;
-    const uint64_t first = piece * kPiece;
-    const uint32_t id = load_l2(a.key + first + kPiece - 1);
-    if (id >= a.vocab || load_l2(a.key + first + kPiece) != id) return;
-    if (first > 0 && load_l2(a.key + first - 1) == id) return;   // sorted: the whole piece is of a run that began earlier
-    const uint32_t lane = threadIdx.x & 31;
-    const uint64_t c = (item - piece * a.segments) * 256 + 8 * lane;
+    __shared__ uint32_t s_id[kJoinPieces], s_run[kJoinPieces];   // a long run that begins in the warp's piece, or none (0)
+    __shared__ __align__(16) float s_sum[kJoinPieces][256];
+    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint64_t group = blockIdx.x / a.segments, piece = group * kJoinPieces + warp;
+    const uint64_t c = (blockIdx.x - group * a.segments) * 256 + 8 * lane;
     const int valid = values_left(a.dim, c);
-    // the pieces after this one that the run enters
-    uint64_t last = piece + 1;
-    for (;;) {
-        const uint64_t q = last + 1 + lane;
-        const uint32_t in = __ballot_sync(0xFFFFFFFFu, q < a.pieces && load_l2(a.key + q * kPiece) == id);
-        const uint32_t run = in == 0xFFFFFFFFu ? 32u : __ffs(~in) - 1;
-        last += run;
-        if (run < 32u) break;
-    }
-    if (valid <= 0) return;
-    float s[8];
-    auto add = [&](const float* p, bool start) {
-        const float4 x = *reinterpret_cast<const float4*>(p), y = *reinterpret_cast<const float4*>(p + 4);
+    auto add = [&](float (&s)[8], uint64_t p, int leaves) {
+        const float4* at = reinterpret_cast<const float4*>(partial_at(a, p, leaves, c));
+        const float4 x = at[0], y = at[1];
         const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s[e] = start ? v[e] : __fadd_rn(s[e], v[e]);
+        add8(s, v);
     };
-    add(partial_at(a, piece, 1, c), true);
+    uint32_t id = 0, run = 0;   // the pieces after this one that the run enters
+    const uint64_t first = piece * kPiece;
+    if (piece + 1 < a.pieces) {
+        id = load_l2(a.key + first + kPiece - 1);
+        // a run that fills the whole piece (the ids are sorted) may have begun earlier
+        const bool begins = id < a.vocab && load_l2(a.key + first + kPiece) == id &&
+                            !(first > 0 && load_l2(a.key + first - 1) == id);
+        for (bool more = begins; more;) {
+            const uint64_t q = piece + 1 + run + lane;
+            const uint32_t in = __ballot_sync(0xFFFFFFFFu, q < a.pieces && load_l2(a.key + q * kPiece) == id);
+            const uint32_t n = in == 0xFFFFFFFFu ? 32u : __ffs(~in) - 1;
+            run += n;
+            more = n == 32u;
+        }
+    }
+    float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    if (lane == 0) {
+        s_id[warp] = id;
+        s_run[warp] = run > kShortRun ? run : 0;
+    }
+    if (run > 0 && run <= kShortRun) {
+        if (valid > 0) {
+            add(s, piece, 1);
+#pragma unroll
+            for (uint32_t i = 0; i < kShortRun; ++i)
+                if (i < run) add(s, piece + 1 + i, 0);
+        }
+        write_sum<DT, ALIGNED>(a, id, c, valid, s);
+    }
+    __syncthreads();
+    for (uint32_t k = 0; k < kJoinPieces; ++k) {
+        const uint32_t pieces = s_run[k];
+        if (pieces == 0) continue;   // the same for all
+        const uint64_t from = group * kJoinPieces + k;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[e] = 0.0f;
+        if (valid > 0) {
+            if (warp == 0) add(s, from, 1);
 #pragma unroll 4
-    for (uint64_t q = piece + 1; q <= last; ++q) add(partial_at(a, q, 0, c), false);
-    write_sum<DT, ALIGNED>(a, id, c, valid, s);
+            for (uint32_t i = warp; i < pieces; i += kJoinPieces) add(s, from + 1 + i, 0);
+        }
+        float4* mine = reinterpret_cast<float4*>(&s_sum[warp][8 * lane]);
+        mine[0] = make_float4(s[0], s[1], s[2], s[3]);
+        mine[1] = make_float4(s[4], s[5], s[6], s[7]);
+        __syncthreads();
+        if (warp == 0) {
+#pragma unroll
+            for (uint32_t w = 1; w < kJoinPieces; ++w) {
+                float v[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = s_sum[w][8 * lane + e];
+                add8(s, v);
+            }
+            write_sum<DT, ALIGNED>(a, s_id[k], c, valid, s);
+        }
+        __syncthreads();
+    }
 }
 
 // -------------------------------------------------------------------- host
@@ -378,7 +424,7 @@ int check_rows(const char* name, const void* at, uint64_t ld, uint64_t dim) {
         return refuse(ZERO_EINVAL, "ld of " + std::string(name) + " must be at least dim (and at most 2^40)");
     return ZERO_OK;
 }
-constexpr uint64_t kZeroCtas = 304, kZeroCols = 4096;   // two an SM; values a warp fills at a time
+constexpr uint64_t kZeroCtas = 304;   // two an SM
 uint64_t sort_bytes(uint64_t tokens) { return up(tokens * 4, 256); }   // one of four arrays
 uint64_t pieces_of(uint64_t tokens) { return (tokens + kPiece - 1) / kPiece; }
 
@@ -412,7 +458,7 @@ int zero_embedding(int dtype, uint64_t vocab, uint64_t dim, const void* table16,
     const uint64_t items = up(tokens, kEmbedTokens) / kEmbedTokens * a.segments, blocks = up(items, kThreads / 32) / (kThreads / 32);
     if (blocks > 0x7FFFFFFFull) return refuse(ZERO_EINVAL, "tokens and dim are too large together");
     const bool fp16 = dtype == ZERO_FP16;
-    const bool whole = aligned(table16, 16) && ld_table % 8 == 0 && aligned(out16, 16) && ld_out % 8 == 0;
+    const bool whole = dim % 8 == 0 && aligned(table16, 16) && ld_table % 8 == 0 && aligned(out16, 16) && ld_out % 8 == 0;
     const cudaError_t e = launch_pdl(whole ? (fp16 ? k_embedding<kFp16, true> : k_embedding<kBf16, true>)
                                            : (fp16 ? k_embedding<kFp16, false> : k_embedding<kBf16, false>),
                                      dim3(static_cast<unsigned>(blocks)), kThreads, 0, 1, static_cast<cudaStream_t>(stream), a);
@@ -459,11 +505,11 @@ int zero_embedding_backward(int dtype, uint64_t vocab, uint64_t dim, const void*
     uint64_t others = 0;
     if (!accumulate) {
         o.zero = static_cast<unsigned short*>(dtable16);
-        o.zero_total = (vocab - 1) * ld_dtable + dim;
-        o.zero_cols = ld_dtable == dim ? kZeroCols : dim;   // rows without gaps are one range, cut where it suits
-        o.zero_ld = ld_dtable == dim ? kZeroCols : ld_dtable;
-        o.zero_rows = ld_dtable == dim ? up(o.zero_total, kZeroCols) / kZeroCols : vocab;
-        others = up(o.zero_rows, kSortThreads / 32) / (kSortThreads / 32);
+        const bool range = ld_dtable == dim;
+        o.zero_rows = range ? 1 : vocab;
+        o.zero_cols = range ? vocab * dim : dim;
+        o.zero_ld = ld_dtable;
+        others = range ? up(2 * o.zero_cols, kZeroBytes) / kZeroBytes : up(vocab, 32) / 32;
         if (others > kZeroCtas) others = kZeroCtas;
     }
     if ((e = launch_pdl(k_embedding_sort, dim3(static_cast<unsigned>(kSortCtas + up(others, kSortCtas))), kSortThreads, 0,
@@ -487,14 +533,15 @@ int zero_embedding_backward(int dtype, uint64_t vocab, uint64_t dim, const void*
     a.add = accumulate != 0;
     const dim3 grid(static_cast<unsigned>(up(a.pieces * a.segments, kThreads / 32) / (kThreads / 32)));
     const bool fp16 = dtype == ZERO_FP16;
-    const bool whole = aligned(dout16, 16) && ld_dout % 8 == 0 && aligned(dtable16, 16) && ld_dtable % 8 == 0;
+    const bool whole = dim % 8 == 0 && aligned(dout16, 16) && ld_dout % 8 == 0 && aligned(dtable16, 16) && ld_dtable % 8 == 0;
     e = launch_pdl(whole ? (fp16 ? k_embedding_sum<kFp16, true> : k_embedding_sum<kBf16, true>)
                          : (fp16 ? k_embedding_sum<kFp16, false> : k_embedding_sum<kBf16, false>),
                    grid, kThreads, 0, 1, s, a);
+    const dim3 joins(static_cast<unsigned>(up(a.pieces, kJoinPieces) / kJoinPieces * a.segments));
     if (e == cudaSuccess && a.pieces > 1)
         e = launch_pdl(whole ? (fp16 ? k_embedding_join<kFp16, true> : k_embedding_join<kBf16, true>)
                              : (fp16 ? k_embedding_join<kFp16, false> : k_embedding_join<kBf16, false>),
-                       grid, kThreads, 0, 1, s, a);
+                       joins, kThreads, 0, 1, s, a);
     return e == cudaSuccess ? ZERO_OK : cuda_refuse(e, "zero_embedding_backward");
 }
 

@@ -36,13 +36,20 @@ namespace {
 template <bool ALIGNED>
 __device__ __forceinline__ void read_weight(const unsigned short* weight, uint64_t c, int valid, uint64_t cols,
                                             uint32_t (&w)[4]) {
-    if (ALIGNED && valid == 8) {
-        const uint4 x = *reinterpret_cast<const uint4*>(weight + c);
+    if (ALIGNED) {
+        const uint4 x = valid > 0 ? *reinterpret_cast<const uint4*>(weight + c) : make_uint4(0u, 0u, 0u, 0u);
         w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
     } else {
         read8<false>(weight, c, valid, cols, w);
     }
 }
+// How many of a thread's 8 columns from group v on lie inside the row.
+template <bool ALIGNED>
+__device__ __forceinline__ int inside(uint32_t v, uint32_t cols) {
+    const int left = static_cast<int>(cols) - static_cast<int>(8 * v);
+    return ALIGNED ? (left > 0 ? 8 : 0) : left > 8 ? 8 : left;
+}
+
 // ----------------------------------------------------------------- dropout
 struct DropoutArgs {
     const unsigned short* src;
@@ -53,8 +60,9 @@ struct DropoutArgs {
 };
 constexpr int kDropVecs = 4;
 
-// A thread takes kDropVecs groups, their loads in flight together.
-template <int DT, bool ALIGNED>
+// A thread takes kDropVecs groups, their loads in flight together.  ONE_ROW:
+// a group's number is its place (rows without gaps, of whole eights).
+template <int DT, bool ALIGNED, bool ONE_ROW>
 __global__ void __launch_bounds__(kThreads) k_dropout(const __grid_constant__ DropoutArgs a) {
     pdl_enter();
     const uint64_t stream = drop_stream(a.drop), first = static_cast<uint64_t>(blockIdx.x) * kDropVecs * kThreads + threadIdx.x;
@@ -65,17 +73,16 @@ __global__ void __launch_bounds__(kThreads) k_dropout(const __grid_constant__ Dr
     for (int i = 0; i < kDropVecs; ++i) {
         const uint64_t g = first + static_cast<uint64_t>(i) * kThreads;
         // one division of 32 bits where that is enough
-        row[i] = a.groups <= 0xFFFFFFFFull ? static_cast<uint32_t>(g) / static_cast<uint32_t>(a.across) : g / a.across;
+        row[i] = ONE_ROW ? 0ull : a.groups <= 0xFFFFFFFFull ? static_cast<uint32_t>(g) / static_cast<uint32_t>(a.across) : g / a.across;
         c[i] = 8 * (g - row[i] * a.across);
-        valid[i] = g < a.groups ? values_left(a.cols, c[i]) : 0;
+        valid[i] = g >= a.groups ? 0 : ALIGNED ? 8 : values_left(a.cols, c[i]);
         read8<ALIGNED>(a.src, row[i] * a.ld_src + c[i], valid[i], (a.rows - 1) * a.ld_src + a.cols, w[i]);
     }
 #pragma unroll
     for (int i = 0; i < kDropVecs; ++i) {
-        if (valid[i] <= 0) continue;
         float v[8];
         widen8<DT>(w[i], v);
-        if (a.drop.below) drop8(a.drop, row[i] * a.across + (c[i] >> 3), stream, v);
+        if (a.drop.below) drop8(a.drop, first + static_cast<uint64_t>(i) * kThreads, stream, v);
         uint32_t q[4];
         narrow8<DT>(v, q);
         store8<ALIGNED>(a.dst + row[i] * a.ld_dst, c[i], valid[i], q);
@@ -119,34 +126,41 @@ __device__ __forceinline__ float rsqrt_of(float sum, uint64_t cols, float eps) {
     return __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(sum, static_cast<float>(cols)), eps)));
 }
 
+// The larger magnitude; NaN where there is one.
+__device__ __forceinline__ float larger(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
+    return r;
+}
 // One warp's 256 values of a row: 8 a lane, y, to codes and scale words.
-// `c`: the lane's first column.
+// v: the lane's group of 8 columns, `valid` of them inside the row.
 template <int BITS>
-__device__ __forceinline__ void write_codes(const NormArgs& a, uint64_t row, uint64_t c, float (&y)[8]) {
-    uint32_t top = 0u;
+__device__ __forceinline__ void write_codes(const NormArgs& a, uint64_t row, uint32_t v, int valid, float (&y)[8]) {
+    if (valid < 8) {   // 0 / 0 in a row of zeros, or NaN times 0, stays inside the row
 #pragma unroll
-    for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(y[e]) & 0x7FFFFFFFu);   // infinity and NaN above every number
+        for (int e = 0; e < 8; ++e) y[e] = e < valid ? y[e] : 0.0f;
+    }
+    // (bits of magnitudes are ordered like these, infinity and NaN above every number)
+    uint32_t top = __float_as_uint(larger(larger(larger(y[0], y[1]), larger(y[2], y[3])),
+                                          larger(larger(y[4], y[5]), larger(y[6], y[7]))));
     top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));   // four lanes share a block
     top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
     const uint32_t byte = scale_byte<BITS>(__uint_as_float(top));
-    const float inv = scale_inverse(byte);
-#pragma unroll
-    for (int e = 0; e < 8; e += 2) mul2(y[e], y[e + 1], inv);
+    mul8(y, scale_inverse(byte));
     typename MxElement<BITS>::Eight q;
     codes8(y, q);
     if (byte == 255u) no_codes(q);
-    if (c * BITS / 8 < a.pitch) *reinterpret_cast<decltype(q)*>(a.codes + row * a.pitch + c * BITS / 8) = q;
+    if (v * BITS < a.pitch) *reinterpret_cast<decltype(q)*>(a.codes + row * a.pitch + v * BITS) = q;
     // the four blocks of a scale tile's row in one word
-    const int lane = threadIdx.x & 31;
     uint32_t word = byte | __shfl_down_sync(0xFFFFFFFFu, byte, 4) << 8;
     word |= __shfl_down_sync(0xFFFFFFFFu, word, 8) << 16;
-    if ((lane & 15) == 0 && (c >> 7) < a.tiles_k)
-        *reinterpret_cast<uint32_t*>(a.scales + scale_at(row, c >> 5, a.tiles_k)) = word;
+    if ((v & 15) == 0 && (v >> 4) < a.tiles_k)
+        *reinterpret_cast<uint32_t*>(a.scales + scale_at(row, v >> 2, a.tiles_k)) = word;
 }
 
 // V groups of 8 columns a thread, those of a row in steps of its threads.
 // BITS: of the codes, or 0.  ALIGNED: every row of every matrix starts on 16
-// bytes.
+// bytes and is whole eights.
 template <int BITS, int DT, int V, bool ALIGNED>
 __global__ void __launch_bounds__(1024) k_rms_norm(const __grid_constant__ NormArgs a) {
     pdl_enter();
@@ -159,66 +173,67 @@ __global__ void __launch_bounds__(1024) k_rms_norm(const __grid_constant__ NormA
                 *reinterpret_cast<uint32_t*>(a.scales + scale_at(row, 4 * k, a.tiles_k)) = 0u;
         return;
     }
+    const uint32_t cols = static_cast<uint32_t>(a.cols);
     uint32_t h[V][4];
-    const uint64_t total_x = (a.rows - 1) * a.ld_x + a.cols;
+    const uint64_t at_x = row * a.ld_x, total_x = (a.rows - 1) * a.ld_x + a.cols;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        const uint64_t c = 8ull * (j * threads + t);
-        read8<ALIGNED>(a.x, row * a.ld_x + c, values_left(a.cols, c), total_x, h[j]);
+        const uint32_t v = j * threads + t;
+        read8<ALIGNED>(a.x, at_x + 8 * v, inside<ALIGNED>(v, cols), total_x, h[j]);
     }
     if (a.residual || a.drop.below) {
-        const uint64_t stream = drop_stream(a.drop), total_r = (a.rows - 1) * a.ld_residual + a.cols;
         uint32_t r[V][4];
         if (a.residual) {
+            const uint64_t at_r = row * a.ld_residual, total_r = (a.rows - 1) * a.ld_residual + a.cols;
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const uint64_t c = 8ull * (j * threads + t);
-                read8<ALIGNED>(a.residual, row * a.ld_residual + c, values_left(a.cols, c), total_r, r[j]);
+                const uint32_t v = j * threads + t;
+                read8<ALIGNED>(a.residual, at_r + 8 * v, inside<ALIGNED>(v, cols), total_r, r[j]);
             }
         }
+        const uint64_t stream = drop_stream(a.drop), group = row * a.across + t;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            float v[8];
-            widen8<DT>(h[j], v);
-            if (a.drop.below) drop8(a.drop, row * a.across + j * threads + t, stream, v);
+            float y[8];
+            widen8<DT>(h[j], y);
+            if (a.drop.below) drop8(a.drop, group + j * threads, stream, y);
             if (a.residual) {
                 float s[8];
                 widen8<DT>(r[j], s);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = __fadd_rn(v[e], s[e]);
+                add8(y, s);
             }
-            narrow8<DT>(v, h[j]);
+            narrow8<DT>(y, h[j]);
         }
     }
-    float sum[1] = {0.0f};
+    float sums[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        const uint64_t c = 8ull * (j * threads + t);
-        if (a.h) store8<ALIGNED>(a.h + row * a.ld_h, c, values_left(a.cols, c), h[j]);
-        float v[8];
-        widen8<DT>(h[j], v);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sum[0] = fmaf(v[e], v[e], sum[0]);
+        const uint32_t v = j * threads + t;
+        if (a.h) store8<ALIGNED>(a.h + row * a.ld_h, 8 * v, inside<ALIGNED>(v, cols), h[j]);
+        float y[8];
+        widen8<DT>(h[j], y);
+        dot8(y, y, sums);
     }
+    float sum[1] = {sums[0] + sums[1]};
     row_sums<1>(sum, a.by_warp, s_sum);
     const float r = rsqrt_of(sum[0], a.cols, a.eps);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        const uint64_t c = 8ull * (j * threads + t);
-        const int valid = values_left(a.cols, c);
+        const uint32_t v = j * threads + t;
+        const int valid = inside<ALIGNED>(v, cols);
         uint32_t w[4];
-        read_weight<ALIGNED>(a.weight, c, valid, a.cols, w);
+        read_weight<ALIGNED>(a.weight, 8 * v, valid, a.cols, w);
         float y[8], f[8];
         widen8<DT>(h[j], y);
         widen8<DT>(w, f);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = e < valid ? __fmul_rn(__fmul_rn(y[e], r), f[e]) : 0.0f;
+        mul8(y, r);
+        mul8(y, f);
         if (a.out) {
             uint32_t q[4];
             narrow8<DT>(y, q);
-            store8<ALIGNED>(a.out + row * a.ld_out, c, valid, q);
+            store8<ALIGNED>(a.out + row * a.ld_out, 8 * v, valid, q);
         }
-        if constexpr (BITS != 0) write_codes<BITS>(a, row, c, y);
+        if constexpr (BITS != 0) write_codes<BITS>(a, row, v, valid, y);
     }
 }
 
@@ -248,74 +263,98 @@ __global__ void __launch_bounds__(512) k_rms_norm_backward(const __grid_constant
     const uint64_t stream = drop_stream(a.drop);
     const uint64_t total_y = (a.rows - 1) * a.ld_dy + a.cols, total_h = (a.rows - 1) * a.ld_h + a.cols,
                    total_i = (a.rows - 1) * a.ld_in + a.cols;
+    const uint32_t cols = static_cast<uint32_t>(a.cols);
+    constexpr bool kAhead = V <= 2;   // registers for two rows
     float dw[V][8];
     uint32_t h[V][4], dy[V][4], in[V][4];
 #pragma unroll
     for (int j = 0; j < V; ++j)
 #pragma unroll
         for (int e = 0; e < 8; ++e) dw[j][e] = 0.0f;
-    auto load = [&](uint64_t row) {
+    auto load = [&](uint64_t row, uint32_t (&h)[V][4], uint32_t (&dy)[V][4], uint32_t (&in)[V][4]) {
+        const uint64_t at_h = row * a.ld_h, at_y = row * a.ld_dy, at_i = row * a.ld_in;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const uint64_t c = 8ull * (j * threads + t);
-            const int valid = values_left(a.cols, c);
-            read8<ALIGNED>(a.h, row * a.ld_h + c, valid, total_h, h[j]);
-            read8<ALIGNED>(a.dy, row * a.ld_dy + c, valid, total_y, dy[j]);
-            if (a.dh_in) read8<ALIGNED>(a.dh_in, row * a.ld_in + c, valid, total_i, in[j]);
+            const uint32_t v = j * threads + t;
+            const int valid = inside<ALIGNED>(v, cols);
+            read8<ALIGNED>(a.h, at_h + 8 * v, valid, total_h, h[j]);
+            read8<ALIGNED>(a.dy, at_y + 8 * v, valid, total_y, dy[j]);
+            if (a.dh_in) read8<ALIGNED>(a.dh_in, at_i + 8 * v, valid, total_i, in[j]);
         }
     };
     uint64_t row = static_cast<uint64_t>(blockIdx.x) * slots + slot;
-    if (row < a.rows) load(row);
+    if (row < a.rows) load(row, h, dy, in);
     for (int flip = 0; row < a.rows; row += step, flip ^= 1) {   // uniform over a row's threads
-        float sums[2] = {0.0f, 0.0f};
+        float ss[2] = {0.0f, 0.0f}, sg[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const uint64_t c = 8ull * (j * threads + t);
+            const uint32_t v = j * threads + t;
             uint32_t w[4];
-            read_weight<ALIGNED>(a.weight, c, values_left(a.cols, c), a.cols, w);
+            read_weight<ALIGNED>(a.weight, 8 * v, inside<ALIGNED>(v, cols), a.cols, w);
             float x[8], y[8], f[8];
             widen8<DT>(h[j], x);
             widen8<DT>(dy[j], y);
             widen8<DT>(w, f);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                sums[0] = fmaf(x[e], x[e], sums[0]);
-                sums[1] = fmaf(__fmul_rn(y[e], f[e]), x[e], sums[1]);
-            }
+            mul8(y, f);
+            dot8(x, x, ss);
+            dot8(y, x, sg);
         }
+        constexpr int N = kAhead ? V : 1;
+        uint32_t h2[N][4], dy2[N][4], in2[N][4];
+        const bool more = row + step < a.rows;
+        if constexpr (kAhead) {
+            if (more) load(row + step, h2, dy2, in2);
+        }
+        float sums[2] = {ss[0] + ss[1], sg[0] + sg[1]};
         row_sums<2>(sums, a.by_warp, s_sum[flip]);
         const float r = rsqrt_of(sums[0], a.cols, a.eps);
         const float k = __fmul_rn(__fmul_rn(r, r), __fdiv_rn(sums[1], static_cast<float>(a.cols)));
+        const uint64_t group = row * a.across + t;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const uint64_t c = 8ull * (j * threads + t);
-            const int valid = values_left(a.cols, c);
+            const uint32_t v = j * threads + t;
+            const int valid = inside<ALIGNED>(v, cols);
             uint32_t w[4];
-            read_weight<ALIGNED>(a.weight, c, valid, a.cols, w);
+            read_weight<ALIGNED>(a.weight, 8 * v, valid, a.cols, w);
             float x[8], y[8], f[8];
             widen8<DT>(h[j], x);
             widen8<DT>(dy[j], y);
             widen8<DT>(w, f);
+            mul8(f, y);          // g
+            float u[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                dw[j][e] = fmaf(y[e], __fmul_rn(x[e], r), dw[j][e]);
-                y[e] = __fmul_rn(r, fmaf(-x[e], k, __fmul_rn(y[e], f[e])));
-            }
+            for (int e = 0; e < 8; ++e) u[e] = -k;
+            fma8(x, u, f);       // g - h k
+            mul8(f, r);
+            mul8(x, r);
+            fma8(y, x, dw[j]);
             if (a.dh_in) {
                 widen8<DT>(in[j], x);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = __fadd_rn(y[e], x[e]);
+                add8(f, x);
             }
             uint32_t q[4];
-            narrow8<DT>(y, q);
-            store8<ALIGNED>(a.dh + row * a.ld_dh, c, valid, q);
+            narrow8<DT>(f, q);
+            store8<ALIGNED>(a.dh + row * a.ld_dh, 8 * v, valid, q);
             if (a.dx) {
-                if (a.drop.below) drop8(a.drop, row * a.across + j * threads + t, stream, y);
-                narrow8<DT>(y, q);
-                store8<ALIGNED>(a.dx + row * a.ld_dx, c, valid, q);
+                if (a.drop.below) drop8(a.drop, group + j * threads, stream, f);
+                narrow8<DT>(f, q);
+                store8<ALIGNED>(a.dx + row * a.ld_dx, 8 * v, valid, q);
             }
         }
-        if (row + step < a.rows) load(row + step);
+        if constexpr (kAhead) {
+            if (more) {
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        h[j][i] = h2[j][i];
+                        dy[j][i] = dy2[j][i];
+                        in[j][i] = in2[j][i];
+                    }
+            }
+        } else if (more) {
+            load(row + step, h, dy, in);
+        }
     }
     if (!a.partial) return;
     float* out = a.partial + static_cast<uint64_t>(blockIdx.x) * 8 * a.across;
@@ -380,8 +419,9 @@ struct Matrix {
     uint64_t ld;
     bool needed;
 };
-// Refusals of the matrices of a call; whether all rows start on 16 bytes.
+// Refusals of the matrices of a call; whether all rows start on 16 bytes and are whole eights.
 int check_matrices(const Matrix* m, int count, uint64_t cols, bool& whole) {
+    whole = cols % 8 == 0;
     for (int i = 0; i < count; ++i) {
         if (!m[i].at) {
             if (m[i].needed) return refuse(ZERO_EINVAL, std::string(m[i].name) + " is NULL");
@@ -489,8 +529,9 @@ int zero_dropout(int dtype, uint64_t rows, uint64_t cols, const void* src16, uin
     const uint64_t blocks = (a.groups + kDropVecs * kThreads - 1) / (kDropVecs * kThreads);
     if (blocks > 0x7FFFFFFFull) return refuse(ZERO_EINVAL, "rows and cols are too large together");
     const bool fp16 = dtype == ZERO_FP16;
-    const cudaError_t e = launch_pdl(whole ? (fp16 ? k_dropout<kFp16, true> : k_dropout<kBf16, true>)
-                                           : (fp16 ? k_dropout<kFp16, false> : k_dropout<kBf16, false>),
+    const cudaError_t e = launch_pdl(whole && rows == 1 ? (fp16 ? k_dropout<kFp16, true, true> : k_dropout<kBf16, true, true>)
+                                     : whole            ? (fp16 ? k_dropout<kFp16, true, false> : k_dropout<kBf16, true, false>)
+                                                        : (fp16 ? k_dropout<kFp16, false, false> : k_dropout<kBf16, false, false>),
                                      dim3(static_cast<unsigned>(blocks)), kThreads, 0, 1, static_cast<cudaStream_t>(stream), a);
     return e == cudaSuccess ? ZERO_OK : cuda_refuse(e, "zero_dropout");
 }

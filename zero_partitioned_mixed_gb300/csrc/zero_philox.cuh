@@ -16,8 +16,8 @@
 // as it was.
 #pragma once
 
-#include "zero_device.cuh"
 #include "zero_host.h"
+#include "zero_rows.cuh"
 
 namespace zg {
 namespace {
@@ -72,10 +72,11 @@ __device__ __forceinline__ uint4 philox(const DropArgs& a, uint64_t group, uint6
 __device__ __forceinline__ void drop8(const DropArgs& a, uint64_t group, uint64_t stream, float (&v)[8]) {
     const uint4 w = philox(a, group, stream);
     const uint32_t r[4] = {w.x, w.y, w.z, w.w};
+    mul8(v, a.factor);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        v[2 * i] = (r[i] << 16) < a.below ? 0.0f : __fmul_rn(v[2 * i], a.factor);
-        v[2 * i + 1] = r[i] < a.below ? 0.0f : __fmul_rn(v[2 * i + 1], a.factor);
+        v[2 * i] = (r[i] << 16) < a.below ? 0.0f : v[2 * i];
+        v[2 * i + 1] = r[i] < a.below ? 0.0f : v[2 * i + 1];
     }
 }
 

@@ -112,18 +112,100 @@ __device__ __forceinline__ void mul2(float& a, float& b, float by) {
     asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(x) : "l"(y));
     asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
 }
+// Eight at a time, in pairs: one instruction for two values, each rounded as
+// by itself.
+__device__ __forceinline__ unsigned long long pair(float a, float b) {
+    unsigned long long x;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a), "f"(b));
+    return x;
+}
+__device__ __forceinline__ void unpair(unsigned long long x, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ void mul8(float (&a)[8], float by) {
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) mul2(a[e], a[e + 1], by);
+}
+__device__ __forceinline__ void mul8(float (&a)[8], const float (&b)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+        unsigned long long x;
+        asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(x) : "l"(pair(a[e], a[e + 1])), "l"(pair(b[e], b[e + 1])));
+        unpair(x, a[e], a[e + 1]);
+    }
+}
+__device__ __forceinline__ void add8(float (&a)[8], const float (&b)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+        unsigned long long x;
+        asm("add.rn.f32x2 %0, %1, %2;" : "=l"(x) : "l"(pair(a[e], a[e + 1])), "l"(pair(b[e], b[e + 1])));
+        unpair(x, a[e], a[e + 1]);
+    }
+}
+// a b + c, rounded once.
+__device__ __forceinline__ void fma8(const float (&a)[8], const float (&b)[8], float (&c)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+        unsigned long long x;
+        asm("fma.rn.f32x2 %0, %1, %2, %3;"
+            : "=l"(x)
+            : "l"(pair(a[e], a[e + 1])), "l"(pair(b[e], b[e + 1])), "l"(pair(c[e], c[e + 1])));
+        unpair(x, c[e], c[e + 1]);
+    }
+}
+// The sum over the eight of a b, into two running sums.
+__device__ __forceinline__ void dot8(const float (&a)[8], const float (&b)[8], float (&s)[2]) {
+    unsigned long long x = pair(s[0], s[1]);
+#pragma unroll
+    for (int e = 0; e < 8; e += 2)
+        asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(x) : "l"(pair(a[e], a[e + 1])), "l"(pair(b[e], b[e + 1])));
+    unpair(x, s[0], s[1]);
+}
 
-// 8 values of a row from column c on, `valid` of them inside it, into a row
-// that may start anywhere.
+// Values `from` to `to` - 1 of the eight at `at`: rare, so one copy of its code.
+__device__ __noinline__ void store_some(unsigned short* at, uint4 x, int from, int to) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (e >= from && e < to) at[e] = static_cast<unsigned short>(w[e >> 1] >> (16 * (e & 1)));
+}
+// 8 values of a row from column c on, `valid` of them inside it, by all lanes
+// of a warp together.  ALIGNED: rows start on 16 bytes and are whole eights.
+// Else the lanes have consecutive eights (of one row, or c = 0 where another
+// one begins): a lane that starts between two boundaries writes the aligned
+// piece with the last values of the lane before and its own first ones, and
+// what has no such neighbour is written value by value.  2047 x 1003 fp16
+// through dropout: 4.0 us against 8.3 with every value by itself.
 template <bool ALIGNED>
 __device__ __forceinline__ void store8(unsigned short* row, uint64_t c, int valid, const uint32_t (&w)[4]) {
-    if (ALIGNED && valid == 8) {
-        __stcs(reinterpret_cast<uint4*>(row + c), make_uint4(w[0], w[1], w[2], w[3]));
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (e < valid) row[c + e] = static_cast<unsigned short>(w[e >> 1] >> (16 * (e & 1)));
+    if (ALIGNED) {
+        if (valid > 0) __stcs(reinterpret_cast<uint4*>(row + c), make_uint4(w[0], w[1], w[2], w[3]));
+        return;
     }
+    const uint32_t lane = threadIdx.x & 31;
+    uint32_t before[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) before[i] = __shfl_up_sync(0xFFFFFFFFu, w[i], 1);
+    const int next = __shfl_down_sync(0xFFFFFFFFu, c == 0 ? 0 : valid, 1);
+    if (valid <= 0) return;
+    unsigned short* at = row + c;
+    const int m = static_cast<int>((reinterpret_cast<uintptr_t>(at) >> 1) & 7), own = 8 - m;   // own: up to the boundary
+    int from = 0, to = valid;
+    if (m == 0) {
+        if (valid == 8) {
+            *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+            return;
+        }
+    } else {
+        if (lane > 0 && c > 0 && valid >= own) {
+            uint32_t q[4];
+            shift_halves(before, w, static_cast<uint32_t>(own), q);
+            *reinterpret_cast<uint4*>(at - m) = make_uint4(q[0], q[1], q[2], q[3]);
+            from = own;
+        }
+        if (lane < 31 && next >= own) to = own;
+    }
+    if (from < to) store_some(at, make_uint4(w[0], w[1], w[2], w[3]), from, to);
 }
 // A read near a row's or the matrix's end: rare, so one copy of its code.
 __device__ __noinline__ uint4 read8_edge(const unsigned short* base, uint64_t at, int valid) {
@@ -134,27 +216,28 @@ __device__ __noinline__ uint4 read8_edge(const unsigned short* base, uint64_t at
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 // The same read, with zeros for what is outside; total: values from `base` to
-// the matrix's end.  A row that starts between two 16-byte boundaries (not
-// ALIGNED) is read as the two aligned pieces around the 8 values.
+// the matrix's end.  A row that starts between two 16-byte boundaries is read
+// as the two aligned pieces around the 8 values.
 template <bool ALIGNED>
 __device__ __forceinline__ void read8(const unsigned short* base, uint64_t at, int valid, uint64_t total, uint32_t (&w)[4]) {
-    if (ALIGNED ? valid == 8 : valid == 8 && at >= 8 && at + 16 <= total) {
-        const uint32_t m = ALIGNED ? 0u : static_cast<uint32_t>((reinterpret_cast<uintptr_t>(base) >> 1) + at) & 7u;
+    w[0] = w[1] = w[2] = w[3] = 0u;
+    if (valid <= 0) return;
+    if (ALIGNED) {
+        const uint4 x = __ldcs(reinterpret_cast<const uint4*>(base + at));
+        w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+    } else if (valid == 8 && at >= 8 && at + 16 <= total) {
+        const uint32_t m = static_cast<uint32_t>((reinterpret_cast<uintptr_t>(base) >> 1) + at) & 7u;
         const uint4* from = reinterpret_cast<const uint4*>(base + at - m);
-        const uint4 x = ALIGNED ? __ldcs(from) : *from;
-        const uint32_t own[4] = {x.x, x.y, x.z, x.w};
-        if (m == 0) {
-            w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
-        } else {   // the second piece is the next lane's first: the cache serves it
+        const uint4 x = *from;
+        w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+        if (m != 0) {   // the second piece is the next lane's first: the cache serves it
             const uint4 y = from[1];
-            const uint32_t next[4] = {y.x, y.y, y.z, y.w};
+            const uint32_t own[4] = {x.x, x.y, x.z, x.w}, next[4] = {y.x, y.y, y.z, y.w};
             shift_halves(own, next, m, w);
         }
-    } else if (valid > 0) {
+    } else {
         const uint4 x = read8_edge(base, at, valid);
         w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
-    } else {
-        w[0] = w[1] = w[2] = w[3] = 0u;
     }
 }
 template <int DT>
