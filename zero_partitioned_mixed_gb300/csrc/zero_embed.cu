@@ -58,26 +58,29 @@ __global__ void __launch_bounds__(kThreads) k_embedding(const __grid_constant__ 
     const uint64_t item = static_cast<uint64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
     const uint64_t quad = item / a.segments, t0 = quad * kEmbedTokens;
     if (t0 >= a.tokens) return;
-    const uint64_t c = (item - quad * a.segments) * 256 + 8 * (threadIdx.x & 31);
-    const int valid = values_left(a.dim, c);
-    const uint64_t total = (a.vocab - 1) * a.ld_table + a.dim;
-    uint32_t w[kEmbedTokens][4];
+    const uint32_t v = static_cast<uint32_t>(item - quad * a.segments) * 32 + (threadIdx.x & 31);
+    const int left = values_left(a.dim, 8ull * v);
+    RowIn<ALIGNED> in[kEmbedTokens];
+    int valid[kEmbedTokens];
+    Fetched<ALIGNED> f[kEmbedTokens];
 #pragma unroll
     for (int i = 0; i < kEmbedTokens; ++i) {
-        w[i][0] = w[i][1] = w[i][2] = w[i][3] = 0u;
-        if (t0 + i >= a.tokens) continue;
-        const uint32_t id = id_at(a.ids, a.wide_ids, t0 + i, a.vocab);
-        if (id < a.vocab) read8<ALIGNED>(a.table, id * a.ld_table + c, valid, total, w[i]);
+        const uint32_t id = t0 + i < a.tokens ? id_at(a.ids, a.wide_ids, t0 + i, a.vocab) : 0xFFFFFFFFu;
+        valid[i] = id < a.vocab ? left : 0;
+        in[i] = row_in<ALIGNED>(a.table, id < a.vocab ? id : 0u, a.ld_table, a.vocab, a.dim);
     }
 #pragma unroll
+    for (int i = 0; i < kEmbedTokens; ++i) fetch8(in[i], v, valid[i], f[i]);
+#pragma unroll
     for (int i = 0; i < kEmbedTokens; ++i) {
         if (t0 + i >= a.tokens) continue;
-        float v[8];
-        widen8<DT>(w[i], v);
-        mul8(v, a.scale);
-        uint32_t q[4];
-        narrow8<DT>(v, q);
-        store8<ALIGNED>(a.out + (t0 + i) * a.ld_out, c, valid, q);
+        uint32_t w[4], q[4];
+        finish8(in[i], v, valid[i], f[i], w);
+        float x[8];
+        widen8<DT>(w, x);
+        mul8(x, a.scale);
+        narrow8<DT>(x, q);
+        store8<ALIGNED>(a.out + (t0 + i) * a.ld_out, v, left, q);
     }
 }
 
@@ -245,22 +248,20 @@ struct SumArgs {
     float scale;
     int add;                       // to what the table holds
 };
-constexpr uint32_t kPiece = 16;
+constexpr uint32_t kPiece = 8;
 
 template <int DT, bool ALIGNED>
-__device__ __forceinline__ void write_sum(const SumArgs& a, uint32_t id, uint64_t c, int valid, float (&s)[8]) {
+__device__ __forceinline__ void write_sum(const SumArgs& a, uint32_t id, uint32_t v, int valid, float (&s)[8]) {
     mul8(s, a.scale);
-    unsigned short* row = a.table + id * a.ld_table;
+    uint32_t w[4];
     if (a.add) {
-        uint32_t w[4];
-        read8<ALIGNED>(a.table, id * a.ld_table + c, valid, (a.vocab - 1) * a.ld_table + a.dim, w);
-        float v[8];
-        widen8<DT>(w, v);
-        add8(s, v);
+        read8<ALIGNED>(row_in<ALIGNED>(a.table, id, a.ld_table, a.vocab, a.dim), v, valid, w);
+        float x[8];
+        widen8<DT>(w, x);
+        add8(s, x);
     }
-    uint32_t q[4];
-    narrow8<DT>(s, q);
-    store8<ALIGNED>(row, c, valid, q);
+    narrow8<DT>(s, w);
+    store8<ALIGNED>(a.table + id * a.ld_table, v, valid, w);
 }
 __device__ __forceinline__ float* partial_at(const SumArgs& a, uint64_t piece, int leaves, uint64_t c) {
     return a.partial + (2 * piece + leaves) * a.width + c;
@@ -281,9 +282,9 @@ __global__ void __launch_bounds__(kThreads) k_embedding_sum(const __grid_constan
     const uint64_t piece = item / a.segments;
     if (piece >= a.pieces) return;
     const uint32_t lane = threadIdx.x & 31;
-    const uint64_t c = (item - piece * a.segments) * 256 + 8 * lane, first = piece * kPiece;
+    const uint32_t v = static_cast<uint32_t>(item - piece * a.segments) * 32 + lane;
+    const uint64_t c = 8ull * v, first = piece * kPiece;
     const int valid = values_left(a.dim, c);
-    const uint64_t total = (a.tokens - 1) * a.ld_grad + a.dim;
     const uint32_t none = static_cast<uint32_t>(a.vocab);   // padding, sorted behind all ids
     // lane i: the piece's token i; lanes 30 and 31 the neighbours' ids
     const uint64_t mine = lane == 30 ? first - 1 : lane == 31 ? first + kPiece : first + lane;
@@ -296,30 +297,36 @@ __global__ void __launch_bounds__(kThreads) k_embedding_sum(const __grid_constan
     float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
     uint32_t id = __shfl_sync(0xFFFFFFFFu, key, 0);
     bool enters = first > 0 && id == before;   // the run began in an earlier piece
-    uint32_t w[kPiece][4];
+    constexpr uint32_t kLoads = 8;   // in flight
+    Fetched<ALIGNED> f[kLoads];
+    auto row_of = [&](uint32_t i) {
+        return row_in<ALIGNED>(a.grad, __shfl_sync(0xFFFFFFFFu, index, i), a.ld_grad, a.tokens, a.dim);
+    };
 #pragma unroll
     for (uint32_t i = 0; i < kPiece; ++i) {
-        const uint64_t t = __shfl_sync(0xFFFFFFFFu, index, i);
-        read8<ALIGNED>(a.grad, t * a.ld_grad + c, i < count ? valid : 0, total, w[i]);
-    }
+        if (i % kLoads == 0) {
 #pragma unroll
-    for (uint32_t i = 0; i < kPiece; ++i) {
+            for (uint32_t k = 0; k < kLoads; ++k) fetch8(row_of(i + k), v, i + k < count ? valid : 0, f[k]);
+        }
         const uint32_t next = __shfl_sync(0xFFFFFFFFu, key, i);
+        const RowIn<ALIGNED> in = row_of(i);
         if (i >= count) break;
+        uint32_t w[4];
+        finish8(in, v, valid, f[i % kLoads], w);
         if (next != id) {   // the run is complete here
             if (enters) write_partial(a, piece, 0, c, valid, s);
-            else write_sum<DT, ALIGNED>(a, id, c, valid, s);
+            else write_sum<DT, ALIGNED>(a, id, v, valid, s);
             id = next;
             enters = false;
 #pragma unroll
             for (int e = 0; e < 8; ++e) s[e] = 0.0f;
         }
-        float v[8];
-        widen8<DT>(w[i], v);
-        add8(s, v);
+        float x[8];
+        widen8<DT>(w, x);
+        add8(s, x);
     }
     if (enters || (count == kPiece && id == after)) write_partial(a, piece, enters ? 0 : 1, c, valid, s);
-    else write_sum<DT, ALIGNED>(a, id, c, valid, s);
+    else write_sum<DT, ALIGNED>(a, id, v, valid, s);
 }
 
 // A block looks at kJoinPieces pieces, a warp each, for a run that begins in
@@ -337,13 +344,14 @@ __global__ void __launch_bounds__(kThreads) k_embedding_join(const __grid_consta
     __shared__ __align__(16) float s_sum[kJoinPieces][256];
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint64_t group = blockIdx.x / a.segments, piece = group * kJoinPieces + warp;
-    const uint64_t c = (blockIdx.x - group * a.segments) * 256 + 8 * lane;
+    const uint32_t v = static_cast<uint32_t>(blockIdx.x - group * a.segments) * 32 + lane;
+    const uint64_t c = 8ull * v;
     const int valid = values_left(a.dim, c);
     auto add = [&](float (&s)[8], uint64_t p, int leaves) {
         const float4* at = reinterpret_cast<const float4*>(partial_at(a, p, leaves, c));
         const float4 x = at[0], y = at[1];
-        const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-        add8(s, v);
+        const float z[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+        add8(s, z);
     };
     uint32_t id = 0, run = 0;   // the pieces after this one that the run enters
     const uint64_t first = piece * kPiece;
@@ -372,7 +380,7 @@ __global__ void __launch_bounds__(kThreads) k_embedding_join(const __grid_consta
             for (uint32_t i = 0; i < kShortRun; ++i)
                 if (i < run) add(s, piece + 1 + i, 0);
         }
-        write_sum<DT, ALIGNED>(a, id, c, valid, s);
+        write_sum<DT, ALIGNED>(a, id, v, valid, s);
     }
     __syncthreads();
     for (uint32_t k = 0; k < kJoinPieces; ++k) {
@@ -393,12 +401,12 @@ __global__ void __launch_bounds__(kThreads) k_embedding_join(const __grid_consta
         if (warp == 0) {
 #pragma unroll
             for (uint32_t w = 1; w < kJoinPieces; ++w) {
-                float v[8];
+                float x[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = s_sum[w][8 * lane + e];
-                add8(s, v);
+                for (int e = 0; e < 8; ++e) x[e] = s_sum[w][8 * lane + e];
+                add8(s, x);
             }
-            write_sum<DT, ALIGNED>(a, s_id[k], c, valid, s);
+            write_sum<DT, ALIGNED>(a, s_id[k], v, valid, s);
         }
         __syncthreads();
     }
@@ -488,6 +496,9 @@ int zero_embedding_backward(int dtype, uint64_t vocab, uint64_t dim, const void*
     if (!workspace || !aligned(workspace, 256)) return refuse(ZERO_EINVAL, "workspace is NULL or not 256-byte aligned");
     if (workspace_bytes < zero_embedding_backward_workspace_bytes(vocab, dim, tokens))
         return refuse(ZERO_EINVAL, "workspace is smaller than zero_embedding_backward_workspace_bytes()");
+    const uint64_t segments = up(dim, 256) / 256;
+    if (up(pieces_of(tokens), kThreads / 32) / (kThreads / 32) * segments > 0x7FFFFFFFull)
+        return refuse(ZERO_EINVAL, "tokens and dim are too large together");
     unsigned char* at = static_cast<unsigned char*>(workspace);
     SortArgs o = {};
     o.ids = ids;
@@ -526,7 +537,7 @@ int zero_embedding_backward(int dtype, uint64_t vocab, uint64_t dim, const void*
     a.tokens = tokens;
     a.ld_grad = ld_dout;
     a.ld_table = ld_dtable;
-    a.segments = up(dim, 256) / 256;
+    a.segments = segments;
     a.pieces = pieces_of(tokens);
     a.width = up(dim, 8);
     a.scale = scale;

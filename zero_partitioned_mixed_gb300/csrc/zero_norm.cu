@@ -27,6 +27,7 @@
 #include "zero_gb300.h"
 #include "zero_host.h"
 #include "zero_mx.cuh"
+#include "zero_tc.cuh"
 #include "zero_philox.cuh"
 
 namespace zg {
@@ -34,13 +35,12 @@ namespace {
 
 // 8 weights: every row reads them again, from the caches.
 template <bool ALIGNED>
-__device__ __forceinline__ void read_weight(const unsigned short* weight, uint64_t c, int valid, uint64_t cols,
-                                            uint32_t (&w)[4]) {
-    if (ALIGNED) {
-        const uint4 x = valid > 0 ? *reinterpret_cast<const uint4*>(weight + c) : make_uint4(0u, 0u, 0u, 0u);
+__device__ __forceinline__ void read_weight(const RowIn<ALIGNED>& r, uint32_t v, int valid, uint32_t (&w)[4]) {
+    if constexpr (ALIGNED) {
+        const uint4 x = valid > 0 ? r.first[v] : make_uint4(0u, 0u, 0u, 0u);
         w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
     } else {
-        read8<false>(weight, c, valid, cols, w);
+        read8<false>(r, v, valid, w);
     }
 }
 // How many of a thread's 8 columns from group v on lie inside the row.
@@ -55,37 +55,69 @@ struct DropoutArgs {
     const unsigned short* src;
     unsigned short* dst;
     uint64_t rows, cols, ld_src, ld_dst;
-    uint64_t across, groups;   // groups of 8 columns in a row, and in all
+    uint64_t across;           // groups of 8 columns in a row
+    uint64_t segments, items;  // of 256 columns in a row, and in all
     DropArgs drop;
 };
 constexpr int kDropVecs = 4;
 
-// A thread takes kDropVecs groups, their loads in flight together.  ONE_ROW:
-// a group's number is its place (rows without gaps, of whole eights).
-template <int DT, bool ALIGNED, bool ONE_ROW>
+template <int DT, bool ALIGNED>
+__device__ __forceinline__ void drop_one(const DropoutArgs& a, unsigned short* row, uint32_t v, int valid, uint64_t group,
+                                         uint64_t stream, const uint32_t (&w)[4]) {
+    float x[8];
+    widen8<DT>(w, x);
+    if (a.drop.below) drop8(a.drop, group, stream, x);
+    uint32_t q[4];
+    narrow8<DT>(x, q);
+    store8<ALIGNED>(row, v, valid, q);
+}
+
+// Rows without gaps, of whole eights: a group's number is its place.  A thread
+// takes kDropVecs groups, their loads in flight together.  HBM and the
+// generator's products about even: 8192 x 4096 bf16 in 21.4 us (6.3 TB/s).
+template <int DT>
 __global__ void __launch_bounds__(kThreads) k_dropout(const __grid_constant__ DropoutArgs a) {
     pdl_enter();
     const uint64_t stream = drop_stream(a.drop), first = static_cast<uint64_t>(blockIdx.x) * kDropVecs * kThreads + threadIdx.x;
-    uint32_t w[kDropVecs][4];
-    uint64_t row[kDropVecs], c[kDropVecs];
-    int valid[kDropVecs];
+    Fetched<true> f[kDropVecs];
 #pragma unroll
     for (int i = 0; i < kDropVecs; ++i) {
         const uint64_t g = first + static_cast<uint64_t>(i) * kThreads;
-        // one division of 32 bits where that is enough
-        row[i] = ONE_ROW ? 0ull : a.groups <= 0xFFFFFFFFull ? static_cast<uint32_t>(g) / static_cast<uint32_t>(a.across) : g / a.across;
-        c[i] = 8 * (g - row[i] * a.across);
-        valid[i] = g >= a.groups ? 0 : ALIGNED ? 8 : values_left(a.cols, c[i]);
-        read8<ALIGNED>(a.src, row[i] * a.ld_src + c[i], valid[i], (a.rows - 1) * a.ld_src + a.cols, w[i]);
+        fetch8(RowIn<true>{reinterpret_cast<const uint4*>(a.src) + g}, 0, g < a.across ? 8 : 0, f[i]);
     }
 #pragma unroll
     for (int i = 0; i < kDropVecs; ++i) {
-        float v[8];
-        widen8<DT>(w[i], v);
-        if (a.drop.below) drop8(a.drop, first + static_cast<uint64_t>(i) * kThreads, stream, v);
-        uint32_t q[4];
-        narrow8<DT>(v, q);
-        store8<ALIGNED>(a.dst + row[i] * a.ld_dst, c[i], valid[i], q);
+        const uint64_t g = first + static_cast<uint64_t>(i) * kThreads;
+        const uint32_t w[4] = {f[i].x.x, f[i].x.y, f[i].x.z, f[i].x.w};
+        drop_one<DT, true>(a, a.dst + 8 * g, 0, g < a.across ? 8 : 0, g, stream, w);
+    }
+}
+
+// Any rows: a warp takes kDropVecs pieces of 256 columns, row after row.
+template <int DT, bool ALIGNED>
+__global__ void __launch_bounds__(kThreads) k_dropout_rows(const __grid_constant__ DropoutArgs a) {
+    pdl_enter();
+    const uint64_t stream = drop_stream(a.drop);
+    const uint64_t item = (static_cast<uint64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5)) * kDropVecs;
+    Fetched<ALIGNED> f[kDropVecs];
+    uint64_t row[kDropVecs];
+    uint32_t v[kDropVecs];
+    int valid[kDropVecs];
+    RowIn<ALIGNED> in[kDropVecs];
+#pragma unroll
+    for (int i = 0; i < kDropVecs; ++i) {
+        const uint64_t at = item + i < a.items ? item + i : a.items - 1;
+        row[i] = a.items <= 0xFFFFFFFFull ? static_cast<uint32_t>(at) / static_cast<uint32_t>(a.segments) : at / a.segments;
+        v[i] = static_cast<uint32_t>(at - row[i] * a.segments) * 32 + (threadIdx.x & 31);
+        valid[i] = item + i < a.items ? values_left(a.cols, 8ull * v[i]) : 0;
+        in[i] = row_in<ALIGNED>(a.src, row[i], a.ld_src, a.rows, a.cols);
+        fetch8(in[i], v[i], valid[i], f[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kDropVecs; ++i) {
+        uint32_t w[4];
+        finish8(in[i], v[i], valid[i], f[i], w);
+        drop_one<DT, ALIGNED>(a, a.dst + row[i] * a.ld_dst, v[i], valid[i], row[i] * a.across + v[i], stream, w);
     }
 }
 
@@ -162,7 +194,7 @@ __device__ __forceinline__ void write_codes(const NormArgs& a, uint64_t row, uin
 // BITS: of the codes, or 0.  ALIGNED: every row of every matrix starts on 16
 // bytes and is whole eights.
 template <int BITS, int DT, int V, bool ALIGNED>
-__global__ void __launch_bounds__(1024) k_rms_norm(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(V == 4 ? 512 : 1024, V == 4 && ALIGNED ? 2 : 1) k_rms_norm(const __grid_constant__ NormArgs a) {
     pdl_enter();
     __shared__ float s_sum[1][32];
     const uint32_t threads = a.by_warp ? 32u : blockDim.x, t = a.by_warp ? threadIdx.x & 31u : threadIdx.x;
@@ -174,32 +206,30 @@ __global__ void __launch_bounds__(1024) k_rms_norm(const __grid_constant__ NormA
         return;
     }
     const uint32_t cols = static_cast<uint32_t>(a.cols);
+    Fetched<ALIGNED> x[V], res[V];
     uint32_t h[V][4];
-    const uint64_t at_x = row * a.ld_x, total_x = (a.rows - 1) * a.ld_x + a.cols;
+    const RowIn<ALIGNED> in_x = row_in<ALIGNED>(a.x, row, a.ld_x, a.rows, a.cols);
+    const RowIn<ALIGNED> in_res = row_in<ALIGNED>(a.residual, row, a.ld_residual, a.rows, a.cols);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         const uint32_t v = j * threads + t;
-        read8<ALIGNED>(a.x, at_x + 8 * v, inside<ALIGNED>(v, cols), total_x, h[j]);
+        fetch8(in_x, v, inside<ALIGNED>(v, cols), x[j]);
+        if (a.residual) fetch8(in_res, v, inside<ALIGNED>(v, cols), res[j]);
     }
-    if (a.residual || a.drop.below) {
-        uint32_t r[V][4];
-        if (a.residual) {
-            const uint64_t at_r = row * a.ld_residual, total_r = (a.rows - 1) * a.ld_residual + a.cols;
+    const uint64_t stream = drop_stream(a.drop), group = row * a.across + t;
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const uint32_t v = j * threads + t;
-                read8<ALIGNED>(a.residual, at_r + 8 * v, inside<ALIGNED>(v, cols), total_r, r[j]);
-            }
-        }
-        const uint64_t stream = drop_stream(a.drop), group = row * a.across + t;
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
+    for (int j = 0; j < V; ++j) {
+        const uint32_t v = j * threads + t;
+        finish8(in_x, v, inside<ALIGNED>(v, cols), x[j], h[j]);
+        if (a.residual || a.drop.below) {
             float y[8];
             widen8<DT>(h[j], y);
             if (a.drop.below) drop8(a.drop, group + j * threads, stream, y);
             if (a.residual) {
+                uint32_t q[4];
+                finish8(in_res, v, inside<ALIGNED>(v, cols), res[j], q);
                 float s[8];
-                widen8<DT>(r[j], s);
+                widen8<DT>(q, s);
                 add8(y, s);
             }
             narrow8<DT>(y, h[j]);
@@ -209,7 +239,7 @@ __global__ void __launch_bounds__(1024) k_rms_norm(const __grid_constant__ NormA
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         const uint32_t v = j * threads + t;
-        if (a.h) store8<ALIGNED>(a.h + row * a.ld_h, 8 * v, inside<ALIGNED>(v, cols), h[j]);
+        if (a.h) store8<ALIGNED>(a.h + row * a.ld_h, v, inside<ALIGNED>(v, cols), h[j]);
         float y[8];
         widen8<DT>(h[j], y);
         dot8(y, y, sums);
@@ -217,12 +247,13 @@ __global__ void __launch_bounds__(1024) k_rms_norm(const __grid_constant__ NormA
     float sum[1] = {sums[0] + sums[1]};
     row_sums<1>(sum, a.by_warp, s_sum);
     const float r = rsqrt_of(sum[0], a.cols, a.eps);
+    const RowIn<ALIGNED> in_w = row_in<ALIGNED>(a.weight, 0, 0, 1, a.cols);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         const uint32_t v = j * threads + t;
         const int valid = inside<ALIGNED>(v, cols);
         uint32_t w[4];
-        read_weight<ALIGNED>(a.weight, 8 * v, valid, a.cols, w);
+        read_weight<ALIGNED>(in_w, v, valid, w);
         float y[8], f[8];
         widen8<DT>(h[j], y);
         widen8<DT>(w, f);
@@ -231,7 +262,7 @@ __global__ void __launch_bounds__(1024) k_rms_norm(const __grid_constant__ NormA
         if (a.out) {
             uint32_t q[4];
             narrow8<DT>(y, q);
-            store8<ALIGNED>(a.out + row * a.ld_out, 8 * v, valid, q);
+            store8<ALIGNED>(a.out + row * a.ld_out, v, valid, q);
         }
         if constexpr (BITS != 0) write_codes<BITS>(a, row, v, valid, y);
     }
@@ -249,61 +280,122 @@ struct NormGradArgs {
     DropArgs drop;
 };
 
+// 16 bytes into shared memory.
+__device__ __forceinline__ void copy16(uint4* to, const uint4* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                 ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(to))), "l"(from)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {   // all but the last N groups
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+constexpr int kGradStages = 2;
+constexpr size_t grad_ring(size_t v, size_t threads) {   // bytes: a slot more a warp, see below
+    return size_t{3} * kGradStages * (v * threads + threads / 32) * sizeof(uint4);
+}
+constexpr size_t kMostGradSmem = grad_ring(4, 512);
+
 // A block takes rows blockIdx.x, + gridDim.x, ... (by_warp: one a warp at a
 // time), and keeps its share of dw in registers over all of them.  The next
-// row's loads are in flight while this one's sums are formed.
+// row is on its way to shared memory while this one is worked on: 62 us for
+// 8192 x 4096 bf16 with dropout (5.4 TB/s) against 70 with the next row in
+// registers and 94 without.  Rows that start between two 16-byte boundaries
+// are copied as the aligned pieces that cover them; a thread then needs two
+// neighbouring pieces, of which another thread copied the second.
 template <int DT, int V, bool ALIGNED>
 __global__ void __launch_bounds__(512) k_rms_norm_backward(const __grid_constant__ NormGradArgs a) {
     pdl_enter();
     __shared__ float s_sum[2][2][32];
-    extern __shared__ __align__(16) float s_dw[];   // by_warp: [warps][8 * across]
+    // [row's slots][stage][h, dy, dh_in][width]; at the end, by_warp: [warps][8 * across] floats
+    extern __shared__ __align__(16) uint4 s_rows[];
     const uint32_t threads = a.by_warp ? 32u : blockDim.x, t = a.by_warp ? threadIdx.x & 31u : threadIdx.x;
     const uint32_t slots = a.by_warp ? blockDim.x >> 5 : 1u, slot = a.by_warp ? threadIdx.x >> 5 : 0u;
     const uint64_t step = static_cast<uint64_t>(gridDim.x) * slots;
     const uint64_t stream = drop_stream(a.drop);
-    const uint64_t total_y = (a.rows - 1) * a.ld_dy + a.cols, total_h = (a.rows - 1) * a.ld_h + a.cols,
-                   total_i = (a.rows - 1) * a.ld_in + a.cols;
     const uint32_t cols = static_cast<uint32_t>(a.cols);
-    constexpr bool kAhead = V <= 2;   // registers for two rows
     float dw[V][8];
-    uint32_t h[V][4], dy[V][4], in[V][4];
+    uint32_t w[V][4];
+    // a row's slots: one for each group, and one for the piece behind the last
+    const uint32_t width = V * threads + 1, each = 3 * kGradStages * width;
+    uint4* const mine = s_rows + (a.by_warp ? slot * each : 0u);
+    auto place = [&](uint32_t stage, int which, uint32_t v) -> uint4& { return mine[(stage * 3 + which) * width + v]; };
+    const RowIn<ALIGNED> in_w = row_in<ALIGNED>(a.weight, 0, 0, 1, a.cols);
 #pragma unroll
-    for (int j = 0; j < V; ++j)
+    for (int j = 0; j < V; ++j) {
+        const uint32_t v = j * threads + t;
+        const int valid = inside<ALIGNED>(v, cols);
+        read_weight<ALIGNED>(in_w, v, valid, w[j]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) dw[j][e] = 0.0f;
-    auto load = [&](uint64_t row, uint32_t (&h)[V][4], uint32_t (&dy)[V][4], uint32_t (&in)[V][4]) {
-        const uint64_t at_h = row * a.ld_h, at_y = row * a.ld_dy, at_i = row * a.ld_in;
+        if (ALIGNED && valid <= 0) {   // never copied to
+#pragma unroll
+            for (int i = 0; i < 3 * kGradStages; ++i) place(i / 3, i % 3, v) = make_uint4(0u, 0u, 0u, 0u);
+        }
+    }
+    uint64_t row = static_cast<uint64_t>(blockIdx.x) * slots + slot;
+    auto copy_row = [&](const RowIn<ALIGNED>& r, uint32_t stage, int which) {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const uint32_t v = j * threads + t;
             const int valid = inside<ALIGNED>(v, cols);
-            read8<ALIGNED>(a.h, at_h + 8 * v, valid, total_h, h[j]);
-            read8<ALIGNED>(a.dy, at_y + 8 * v, valid, total_y, dy[j]);
-            if (a.dh_in) read8<ALIGNED>(a.dh_in, at_i + 8 * v, valid, total_i, in[j]);
+            if (valid <= 0) continue;
+            if constexpr (ALIGNED) {
+                copy16(&place(stage, which, v), r.first + v);
+            } else {
+                if (r.m == 8u) {   // the first row or the last one
+                    place(stage, which, v) = read_some(r.row + 8ull * v, valid);
+                } else {
+                    copy16(&place(stage, which, v), r.first + v);
+                    if (v + 1 == a.across && valid > 8 - static_cast<int>(r.m)) copy16(&place(stage, which, v + 1), r.first + v + 1);
+                }
+            }
         }
     };
-    uint64_t row = static_cast<uint64_t>(blockIdx.x) * slots + slot;
-    if (row < a.rows) load(row, h, dy, in);
-    for (int flip = 0; row < a.rows; row += step, flip ^= 1) {   // uniform over a row's threads
+    auto start = [&](uint64_t row, uint32_t stage) {
+        if (row < a.rows) {
+            copy_row(row_in<ALIGNED>(a.h, row, a.ld_h, a.rows, a.cols), stage, 0);
+            copy_row(row_in<ALIGNED>(a.dy, row, a.ld_dy, a.rows, a.cols), stage, 1);
+            if (a.dh_in) copy_row(row_in<ALIGNED>(a.dh_in, row, a.ld_in, a.rows, a.cols), stage, 2);
+        }
+        copy_commit();
+    };
+    start(row, 0);
+    for (uint32_t flip = 0; row < a.rows; row += step, flip ^= 1) {   // uniform over a row's threads; flip: the stage too
+        if (ALIGNED) {
+            start(row + step, flip ^ 1);
+            copy_wait<1>();
+        } else {
+            copy_wait<0>();
+            if (a.by_warp) __syncwarp();   // the others' copies are there, and what they read of the row before is read
+            else __syncthreads();
+            start(row + step, flip ^ 1);
+        }
+        RowIn<ALIGNED> in[3] = {row_in<ALIGNED>(a.h, row, a.ld_h, a.rows, a.cols), row_in<ALIGNED>(a.dy, row, a.ld_dy, a.rows, a.cols),
+                                row_in<ALIGNED>(a.dh_in, row, a.ld_in, a.rows, a.cols)};
+        auto values = [&](int which, int j, float (&x)[8]) {
+            const uint32_t v = j * threads + t;
+            const uint4 p = place(flip, which, v);
+            uint32_t q[4] = {p.x, p.y, p.z, p.w};
+            if constexpr (!ALIGNED) {
+                const uint4 n = place(flip, which, v + 1);
+                const uint32_t own[4] = {p.x, p.y, p.z, p.w}, next[4] = {n.x, n.y, n.z, n.w};
+                shift_halves(own, next, in[which].m & 7u, q);
+                clear_from(q, inside<false>(v, cols));
+            }
+            widen8<DT>(q, x);
+        };
         float ss[2] = {0.0f, 0.0f}, sg[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const uint32_t v = j * threads + t;
-            uint32_t w[4];
-            read_weight<ALIGNED>(a.weight, 8 * v, inside<ALIGNED>(v, cols), a.cols, w);
             float x[8], y[8], f[8];
-            widen8<DT>(h[j], x);
-            widen8<DT>(dy[j], y);
-            widen8<DT>(w, f);
+            values(0, j, x);
+            values(1, j, y);
+            widen8<DT>(w[j], f);
             mul8(y, f);
             dot8(x, x, ss);
             dot8(y, x, sg);
-        }
-        constexpr int N = kAhead ? V : 1;
-        uint32_t h2[N][4], dy2[N][4], in2[N][4];
-        const bool more = row + step < a.rows;
-        if constexpr (kAhead) {
-            if (more) load(row + step, h2, dy2, in2);
         }
         float sums[2] = {ss[0] + ss[1], sg[0] + sg[1]};
         row_sums<2>(sums, a.by_warp, s_sum[flip]);
@@ -314,12 +406,10 @@ __global__ void __launch_bounds__(512) k_rms_norm_backward(const __grid_constant
         for (int j = 0; j < V; ++j) {
             const uint32_t v = j * threads + t;
             const int valid = inside<ALIGNED>(v, cols);
-            uint32_t w[4];
-            read_weight<ALIGNED>(a.weight, 8 * v, valid, a.cols, w);
             float x[8], y[8], f[8];
-            widen8<DT>(h[j], x);
-            widen8<DT>(dy[j], y);
-            widen8<DT>(w, f);
+            values(0, j, x);
+            values(1, j, y);
+            widen8<DT>(w[j], f);
             mul8(f, y);          // g
             float u[8];
 #pragma unroll
@@ -329,33 +419,20 @@ __global__ void __launch_bounds__(512) k_rms_norm_backward(const __grid_constant
             mul8(x, r);
             fma8(y, x, dw[j]);
             if (a.dh_in) {
-                widen8<DT>(in[j], x);
+                values(2, j, x);
                 add8(f, x);
             }
             uint32_t q[4];
             narrow8<DT>(f, q);
-            store8<ALIGNED>(a.dh + row * a.ld_dh, 8 * v, valid, q);
+            store8<ALIGNED>(a.dh + row * a.ld_dh, v, valid, q);
             if (a.dx) {
                 if (a.drop.below) drop8(a.drop, group + j * threads, stream, f);
                 narrow8<DT>(f, q);
-                store8<ALIGNED>(a.dx + row * a.ld_dx, 8 * v, valid, q);
+                store8<ALIGNED>(a.dx + row * a.ld_dx, v, valid, q);
             }
-        }
-        if constexpr (kAhead) {
-            if (more) {
-#pragma unroll
-                for (int j = 0; j < V; ++j)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        h[j][i] = h2[j][i];
-                        dy[j][i] = dy2[j][i];
-                        in[j][i] = in2[j][i];
-                    }
-            }
-        } else if (more) {
-            load(row + step, h, dy, in);
         }
     }
+    copy_wait<0>();
     if (!a.partial) return;
     float* out = a.partial + static_cast<uint64_t>(blockIdx.x) * 8 * a.across;
     if (!a.by_warp) {
@@ -369,20 +446,22 @@ __global__ void __launch_bounds__(512) k_rms_norm_backward(const __grid_constant
         }
         return;
     }
-    // the warps' shares, added in their order
-    const uint32_t width = static_cast<uint32_t>(8 * a.across);
+    // the warps' shares, added in their order, where the rows were
+    __syncthreads();
+    float* const s_dw = reinterpret_cast<float*>(s_rows);
+    const uint32_t values = static_cast<uint32_t>(8 * a.across);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         const uint32_t v = j * threads + t;
         if (v >= a.across) continue;
-        float4* to = reinterpret_cast<float4*>(s_dw + slot * width + 8 * v);
+        float4* to = reinterpret_cast<float4*>(s_dw + slot * values + 8 * v);
         to[0] = make_float4(dw[j][0], dw[j][1], dw[j][2], dw[j][3]);
         to[1] = make_float4(dw[j][4], dw[j][5], dw[j][6], dw[j][7]);
     }
     __syncthreads();
-    for (uint32_t c = threadIdx.x; c < width; c += blockDim.x) {
+    for (uint32_t c = threadIdx.x; c < values; c += blockDim.x) {
         float s = 0.0f;
-        for (uint32_t i = 0; i < slots; ++i) s += s_dw[i * width + c];
+        for (uint32_t i = 0; i < slots; ++i) s += s_dw[i * values + c];
         out[c] = s;
     }
 }
@@ -453,6 +532,12 @@ cudaError_t launch_norm(const NormArgs& a, int v, bool whole, unsigned blocks, u
 }
 template <int DT, int V>
 cudaError_t launch_norm_grad(const NormGradArgs& a, bool whole, unsigned blocks, unsigned threads, size_t smem, cudaStream_t s) {
+    const size_t ring = grad_ring(V, threads);
+    if (ring > smem) smem = ring;
+    cudaError_t e;
+    if ((e = allow_smem<k_rms_norm_backward<DT, V, true>>(kMostGradSmem)) != cudaSuccess ||
+        (e = allow_smem<k_rms_norm_backward<DT, V, false>>(kMostGradSmem)) != cudaSuccess)
+        return e;
     return launch_pdl(whole ? k_rms_norm_backward<DT, V, true> : k_rms_norm_backward<DT, V, false>, dim3(blocks), threads, smem,
                       1, s, a);
 }
@@ -471,9 +556,9 @@ struct RowShape {
     unsigned threads;   // of a block
     unsigned rows;      // of a block at a time
 };
-RowShape row_shape(uint64_t groups, unsigned least_v, unsigned most) {
+RowShape row_shape(uint64_t groups, unsigned warp_groups, unsigned least_v, unsigned most) {
     RowShape r;
-    if (groups <= 128) {
+    if (groups <= warp_groups) {
         r.by_warp = 1;
         r.v = groups <= 32 ? 1 : groups <= 64 ? 2 : 4;
         r.threads = kThreads;
@@ -488,7 +573,7 @@ RowShape row_shape(uint64_t groups, unsigned least_v, unsigned most) {
     return r;
 }
 constexpr unsigned kGradBlocks = 304;   // two an SM
-RowShape grad_shape(uint64_t cols) { return row_shape((cols + 7) / 8, 2, 512); }
+RowShape grad_shape(uint64_t cols) { return row_shape((cols + 7) / 8, 128, 2, 512); }
 uint64_t grad_blocks(uint64_t rows, const RowShape& r) {
     const uint64_t b = (rows + r.rows - 1) / r.rows;
     return b < kGradBlocks ? b : kGradBlocks;
@@ -524,14 +609,16 @@ int zero_dropout(int dtype, uint64_t rows, uint64_t cols, const void* src16, uin
     a.ld_src = ld_src;
     a.ld_dst = ld_out;
     a.across = (cols + 7) / 8;
+    a.segments = (cols + 255) / 256;
     if (a.across > (1ull << 40) / rows) return refuse(ZERO_EINVAL, "rows and cols are too large together");
-    a.groups = rows * a.across;
-    const uint64_t blocks = (a.groups + kDropVecs * kThreads - 1) / (kDropVecs * kThreads);
+    a.items = rows * a.segments;
+    const bool one = whole && rows == 1, fp16 = dtype == ZERO_FP16;
+    const uint64_t per = one ? kDropVecs * kThreads : kDropVecs * kThreads / 32;
+    const uint64_t blocks = ((one ? a.across : a.items) + per - 1) / per;
     if (blocks > 0x7FFFFFFFull) return refuse(ZERO_EINVAL, "rows and cols are too large together");
-    const bool fp16 = dtype == ZERO_FP16;
-    const cudaError_t e = launch_pdl(whole && rows == 1 ? (fp16 ? k_dropout<kFp16, true, true> : k_dropout<kBf16, true, true>)
-                                     : whole            ? (fp16 ? k_dropout<kFp16, true, false> : k_dropout<kBf16, true, false>)
-                                                        : (fp16 ? k_dropout<kFp16, false, false> : k_dropout<kBf16, false, false>),
+    const cudaError_t e = launch_pdl(one     ? (fp16 ? k_dropout<kFp16> : k_dropout<kBf16>)
+                                     : whole ? (fp16 ? k_dropout_rows<kFp16, true> : k_dropout_rows<kBf16, true>)
+                                             : (fp16 ? k_dropout_rows<kFp16, false> : k_dropout_rows<kBf16, false>),
                                      dim3(static_cast<unsigned>(blocks)), kThreads, 0, 1, static_cast<cudaStream_t>(stream), a);
     return e == cudaSuccess ? ZERO_OK : cuda_refuse(e, "zero_dropout");
 }
@@ -574,7 +661,7 @@ int zero_rms_norm(int dtype, uint64_t rows, uint64_t cols, const void* x16, uint
     a.pitch = up(cols, kMxBlock) * bits / 8;
     a.tiles_k = bits ? up(cols, 128) / 128 : 0;
     a.eps = eps;
-    const RowShape r = row_shape(bits ? 16 * a.tiles_k : a.across, 1, 1024);
+    const RowShape r = row_shape(bits ? 16 * a.tiles_k : a.across, 128, 1, 1024);
     a.by_warp = r.by_warp;
     const uint64_t all = bits ? up(rows, 128) : rows;
     const unsigned blocks = static_cast<unsigned>((all + r.rows - 1) / r.rows);

@@ -162,82 +162,143 @@ __device__ __forceinline__ void dot8(const float (&a)[8], const float (&b)[8], f
     unpair(x, s[0], s[1]);
 }
 
-// Values `from` to `to` - 1 of the eight at `at`: rare, so one copy of its code.
+// Rows of 16-bit matrices, eight values a lane: lane l of a warp has the row's
+// group v of 8 consecutive values, lane l + 1 group v + 1.  ALIGNED: every row
+// starts on 16 bytes and is whole eights.  Else a row that starts m values
+// behind a 16-byte boundary is read as the two aligned pieces around a group
+// and put together by shifts, and written in aligned pieces, each with the
+// last m values of the lane before.
+__device__ __noinline__ uint4 read_some(const unsigned short* at, int count) {
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (e < count) w[e >> 1] |= static_cast<uint32_t>(__ldcs(at + e)) << (16 * (e & 1));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// Values `from` to `to` - 1 of eight.
 __device__ __noinline__ void store_some(unsigned short* at, uint4 x, int from, int to) {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
     for (int e = 0; e < 8; ++e)
         if (e >= from && e < to) at[e] = static_cast<unsigned short>(w[e >> 1] >> (16 * (e & 1)));
 }
-// 8 values of a row from column c on, `valid` of them inside it, by all lanes
-// of a warp together.  ALIGNED: rows start on 16 bytes and are whole eights.
-// Else the lanes have consecutive eights (of one row, or c = 0 where another
-// one begins): a lane that starts between two boundaries writes the aligned
-// piece with the last values of the lane before and its own first ones, and
-// what has no such neighbour is written value by value.  2047 x 1003 fp16
-// through dropout: 4.0 us against 8.3 with every value by itself.
+
 template <bool ALIGNED>
-__device__ __forceinline__ void store8(unsigned short* row, uint64_t c, int valid, const uint32_t (&w)[4]) {
-    if (ALIGNED) {
-        if (valid > 0) __stcs(reinterpret_cast<uint4*>(row + c), make_uint4(w[0], w[1], w[2], w[3]));
-        return;
-    }
-    const uint32_t lane = threadIdx.x & 31;
-    uint32_t before[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) before[i] = __shfl_up_sync(0xFFFFFFFFu, w[i], 1);
-    const int next = __shfl_down_sync(0xFFFFFFFFu, c == 0 ? 0 : valid, 1);
-    if (valid <= 0) return;
-    unsigned short* at = row + c;
-    const int m = static_cast<int>((reinterpret_cast<uintptr_t>(at) >> 1) & 7), own = 8 - m;   // own: up to the boundary
-    int from = 0, to = valid;
-    if (m == 0) {
-        if (valid == 8) {
-            *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
-            return;
-        }
+struct RowIn;
+template <>
+struct RowIn<true> {
+    const uint4* first;
+};
+template <>
+struct RowIn<false> {
+    const uint4* first;          // the piece with the row's first value
+    const unsigned short* row;
+    uint32_t m;                  // values before that one in it; 8: pieces would leave the matrix, read value by value
+};
+// Row `row` of a rows x cols matrix.
+template <bool ALIGNED>
+__device__ __forceinline__ RowIn<ALIGNED> row_in(const unsigned short* base, uint64_t row, uint64_t ld, uint64_t rows, uint64_t cols) {
+    const unsigned short* at = base + row * ld;
+    if constexpr (ALIGNED) {
+        return {reinterpret_cast<const uint4*>(at)};
     } else {
-        if (lane > 0 && c > 0 && valid >= own) {
-            uint32_t q[4];
+        const uintptr_t a = reinterpret_cast<uintptr_t>(at), first = a & ~static_cast<uintptr_t>(15);
+        const uint32_t m = static_cast<uint32_t>(a - first) >> 1;
+        const bool in = first >= reinterpret_cast<uintptr_t>(base) &&
+                        first + 16 * ((m + cols + 7) / 8) <= reinterpret_cast<uintptr_t>(base + (rows - 1) * ld + cols);
+        return {reinterpret_cast<const uint4*>(first), at, in ? m : 8u};
+    }
+}
+
+// A read in two steps, so that a thread's loads are all in flight before the
+// first one's values are looked at (putting them together takes branches).
+template <bool ALIGNED>
+struct Fetched {
+    uint4 x;
+};
+template <>
+struct Fetched<false> {
+    uint4 x, y;
+};
+// Group v, `valid` (at most 8) of whose values are inside the row.
+__device__ __forceinline__ void fetch8(const RowIn<true>& r, uint32_t v, int valid, Fetched<true>& f) {
+    f.x = make_uint4(0u, 0u, 0u, 0u);
+    if (valid > 0) f.x = __ldcs(r.first + v);
+}
+__device__ __forceinline__ void fetch8(const RowIn<false>& r, uint32_t v, int valid, Fetched<false>& f) {
+    f.x = f.y = make_uint4(0u, 0u, 0u, 0u);
+    if (r.m < 8u && valid > 0) f.x = r.first[v];
+    if (r.m < 8u && valid > 8 - static_cast<int>(r.m)) f.y = r.first[v + 1];   // the next lane's first: the cache serves it
+}
+__device__ __forceinline__ void finish8(const RowIn<true>&, uint32_t, int, const Fetched<true>& f, uint32_t (&w)[4]) {
+    w[0] = f.x.x; w[1] = f.x.y; w[2] = f.x.z; w[3] = f.x.w;
+}
+__device__ __forceinline__ void finish8(const RowIn<false>& r, uint32_t v, int valid, const Fetched<false>& f, uint32_t (&w)[4]) {
+    if (r.m < 8u) {
+        const uint32_t own[4] = {f.x.x, f.x.y, f.x.z, f.x.w}, next[4] = {f.y.x, f.y.y, f.y.z, f.y.w};
+        shift_halves(own, next, r.m, w);
+        clear_from(w, valid);
+    } else {
+        const uint4 x = valid > 0 ? read_some(r.row + 8ull * v, valid) : make_uint4(0u, 0u, 0u, 0u);
+        w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+    }
+}
+template <bool ALIGNED>
+__device__ __forceinline__ void read8(const RowIn<ALIGNED>& r, uint32_t v, int valid, uint32_t (&w)[4]) {
+    Fetched<ALIGNED> f;
+    fetch8(r, v, valid, f);
+    finish8(r, v, valid, f, w);
+}
+
+// The first m, and the last 8 - m, halves of an aligned piece; m in 1..7.
+__device__ __forceinline__ void store_low(uint4* piece, const uint32_t (&q)[4], uint32_t m) {
+    if (m & 4) *reinterpret_cast<uint2*>(piece) = make_uint2(q[0], q[1]);
+    if (m & 2) reinterpret_cast<uint32_t*>(piece)[m & 4 ? 2 : 0] = m & 4 ? q[2] : q[0];
+    if (m & 1) reinterpret_cast<unsigned short*>(piece)[m - 1] =
+        static_cast<unsigned short>(m == 1 ? q[0] : m == 3 ? q[1] : m == 5 ? q[2] : q[3]);
+}
+__device__ __forceinline__ void store_high(uint4* piece, const uint32_t (&q)[4], uint32_t m) {
+    const uint32_t k = (m + 1) >> 1;   // whole words from the k-th on
+    if (m & 1) reinterpret_cast<unsigned short*>(piece)[m] =
+        static_cast<unsigned short>((m == 1 ? q[0] : m == 3 ? q[1] : m == 5 ? q[2] : q[3]) >> 16);
+    if (k & 1) reinterpret_cast<uint32_t*>(piece)[k] = k == 1 ? q[1] : q[3];
+    if (k <= 2) reinterpret_cast<uint2*>(piece)[1] = make_uint2(q[2], q[3]);
+}
+// Group v into a row, by all lanes of a warp together.  The piece between two
+// warps is written by lane 0 of either: its own values, and those of this
+// warp's lane 31, which come round to it.  What ends the row is written value
+// by value.  4001 x 5003 bf16 through the norm and into 8 bits takes XXX us,
+// against 91 with every value of lanes 0 and 31 by itself.
+template <bool ALIGNED>
+__device__ __forceinline__ void store8(unsigned short* row, uint32_t v, int valid, const uint32_t (&w)[4]) {
+    if constexpr (ALIGNED) {
+        if (valid > 0) __stcs(reinterpret_cast<uint4*>(row) + v, make_uint4(w[0], w[1], w[2], w[3]));
+    } else {
+        const uint32_t lane = threadIdx.x & 31;
+        unsigned short* at = row + 8ull * v;
+        const uint32_t m = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row) >> 1) & 7u;   // the same in all lanes
+        const int own = 8 - static_cast<int>(m);   // values up to the boundary
+        int from = 0, to = 0;                      // values to be written by themselves
+        if (m == 0u) {
+            if (valid == 8) *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+            else to = valid;
+        } else {
+            uint32_t before[4], q[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) before[i] = __shfl_sync(0xFFFFFFFFu, w[i], (lane + 31) & 31);
+            const int next = __shfl_sync(0xFFFFFFFFu, valid, (lane + 1) & 31), last = __shfl_sync(0xFFFFFFFFu, valid, 31);
             shift_halves(before, w, static_cast<uint32_t>(own), q);
-            *reinterpret_cast<uint4*>(at - m) = make_uint4(q[0], q[1], q[2], q[3]);
-            from = own;
+            uint4* piece = reinterpret_cast<uint4*>(at - m);
+            if (lane > 0) {
+                if (valid >= own) *piece = make_uint4(q[0], q[1], q[2], q[3]);
+            } else {
+                if (valid >= own) store_high(piece, q, m);
+                if (last == 8) store_low(piece + 32, q, m);
+            }
+            if (valid < own) to = valid;
+            else if (valid > own && (lane == 31 ? valid < 8 : next < own)) from = own, to = valid;
         }
-        if (lane < 31 && next >= own) to = own;
-    }
-    if (from < to) store_some(at, make_uint4(w[0], w[1], w[2], w[3]), from, to);
-}
-// A read near a row's or the matrix's end: rare, so one copy of its code.
-__device__ __noinline__ uint4 read8_edge(const unsigned short* base, uint64_t at, int valid) {
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        if (e < valid) w[e >> 1] |= static_cast<uint32_t>(__ldcs(base + at + e)) << (16 * (e & 1));
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-// The same read, with zeros for what is outside; total: values from `base` to
-// the matrix's end.  A row that starts between two 16-byte boundaries is read
-// as the two aligned pieces around the 8 values.
-template <bool ALIGNED>
-__device__ __forceinline__ void read8(const unsigned short* base, uint64_t at, int valid, uint64_t total, uint32_t (&w)[4]) {
-    w[0] = w[1] = w[2] = w[3] = 0u;
-    if (valid <= 0) return;
-    if (ALIGNED) {
-        const uint4 x = __ldcs(reinterpret_cast<const uint4*>(base + at));
-        w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
-    } else if (valid == 8 && at >= 8 && at + 16 <= total) {
-        const uint32_t m = static_cast<uint32_t>((reinterpret_cast<uintptr_t>(base) >> 1) + at) & 7u;
-        const uint4* from = reinterpret_cast<const uint4*>(base + at - m);
-        const uint4 x = *from;
-        w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
-        if (m != 0) {   // the second piece is the next lane's first: the cache serves it
-            const uint4 y = from[1];
-            const uint32_t own[4] = {x.x, x.y, x.z, x.w}, next[4] = {y.x, y.y, y.z, y.w};
-            shift_halves(own, next, m, w);
-        }
-    } else {
-        const uint4 x = read8_edge(base, at, valid);
-        w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+        if (from < to) store_some(at, make_uint4(w[0], w[1], w[2], w[3]), from, to);
     }
 }
 template <int DT>
