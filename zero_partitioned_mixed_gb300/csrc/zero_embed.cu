@@ -80,12 +80,12 @@ __global__ void __launch_bounds__(kThreads) k_embedding(const __grid_constant__ 
         widen8<DT>(w, x);
         mul8(x, a.scale);
         narrow8<DT>(x, q);
-        store8<ALIGNED>(a.out + (t0 + i) * a.ld_out, v, left, q);
+        RowOut<ALIGNED>(a.out + (t0 + i) * a.ld_out).template put<true, true>(v, left, values_left(a.dim, 8ull * (v + 1)), q);
     }
 }
 
 // -------------------------------------------------------------------- sort
-constexpr uint32_t kSortCtas = 8, kSortThreads = 1024, kDigits = 256;
+constexpr uint32_t kSortCtas = 8, kSortThreads = 1024, kDigits = 256, kMostPer = 4;
 
 struct SortArgs {
     const void* ids;
@@ -153,86 +153,136 @@ __device__ void fill_zeros(const SortArgs& a, uint4 (&zeros)[kZeroBytes / 16], u
 
 __global__ void __launch_bounds__(kSortThreads) k_embedding_sort(const __grid_constant__ SortArgs a) {
     pdl_enter();
+    constexpr uint32_t kWarps = kSortThreads / 32;
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     __shared__ __align__(128) uint4 s_zeros[kZeroBytes / 16];
     if (blockIdx.x >= kSortCtas) {
         fill_zeros(a, s_zeros, blockIdx.x - kSortCtas, gridDim.x - kSortCtas);
         return;
     }
-    __shared__ uint32_t s_count[kDigits];                    // this CTA's keys of each digit
-    __shared__ uint32_t s_base[kDigits];                     // where its next key of a digit goes
-    __shared__ uint32_t s_tile[kDigits];                     // the same at the tile's start
-    __shared__ unsigned short s_warp[kSortThreads / 32][kDigits];   // a tile's keys of each digit, by warp
+    // a tile's keys of each digit, by warp; then those in the warps before
+    unsigned short (*const s_warp)[kDigits] = reinterpret_cast<unsigned short (*)[kDigits]>(s_zeros);
+    static_assert(sizeof(s_zeros) == kWarps * kDigits * sizeof(unsigned short) && kDigits * 4 == kSortThreads, "one place");
+    __shared__ uint32_t s_count[kDigits];   // this CTA's keys of each digit
+    __shared__ uint32_t s_base[kDigits];    // where the tile's first key of a digit goes
+    __shared__ uint32_t s_total[kDigits];   // the tile's keys of each digit
     __shared__ uint32_t s_scan[kDigits / 32];
     const uint32_t me = cluster_rank();
     const uint64_t share = (a.tokens + kSortCtas - 1) / kSortCtas, first = me * share;
     const uint64_t end = first >= a.tokens ? first : first + share < a.tokens ? first + share : a.tokens;
+    // keys a thread has of a tile; a warp's are consecutive, 32 at a time
+    const uint32_t per = share > 2 * kSortThreads ? kMostPer : share > kSortThreads ? 2 : 1, tile_keys = per * kSortThreads;
+    const uint32_t digits = 1u << a.digit_bits;
     for (uint32_t pass = 0; pass < a.passes; ++pass) {
-        const uint32_t shift = pass * a.digit_bits, mask = (1u << a.digit_bits) - 1;
+        const uint32_t shift = pass * a.digit_bits;
         const uint32_t* from = a.key[(pass & 1) ^ 1];
         const uint32_t* from_index = a.index[(pass & 1) ^ 1];
         uint32_t *to = a.key[pass & 1], *to_index = a.index[pass & 1];
         auto key_of = [&](uint64_t i) { return pass == 0 ? id_at(a.ids, a.wide_ids, i, a.vocab) : load_l2(from + i); };
-        if (threadIdx.x < kDigits) s_count[threadIdx.x] = 0;
-        __syncthreads();
-        for (uint64_t i = first + threadIdx.x; i < end; i += kSortThreads) atomicAdd(&s_count[(key_of(i) >> shift) & mask], 1u);
-        cluster_sync();
-        // keys of smaller digits anywhere, and of the same digit in the CTAs before
-        if (threadIdx.x < kDigits) {
-            uint32_t before = 0, all = 0;
-#pragma unroll
-            for (uint32_t q = 0; q < kSortCtas; ++q) {
-                const uint32_t n = load_of_cta(&s_count[threadIdx.x], q);
-                before += q < me ? n : 0u;
-                all += n;
-            }
-            uint32_t sum = all;   // inclusive scan over the digits
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, sum, d);
-                if (lane >= static_cast<uint32_t>(d)) sum += x;
-            }
-            if (lane == 31) s_scan[warp] = sum;
-            s_base[threadIdx.x] = before + sum - all;
-        }
-        __syncthreads();
-        if (threadIdx.x < kDigits) {
-            uint32_t x = 0;
-            for (uint32_t q = 0; q < warp; ++q) x += s_scan[q];
-            s_base[threadIdx.x] += x;
-        }
-        for (uint64_t tile = first; tile < end; tile += kSortThreads) {
-            for (uint32_t i = threadIdx.x; i < sizeof(s_warp) / 4; i += kSortThreads) reinterpret_cast<uint32_t*>(s_warp)[i] = 0u;
+        const bool one_tile = share <= tile_keys;   // then the tile's counts are the CTA's
+        if (!one_tile) {
+            if (threadIdx.x < kDigits) s_count[threadIdx.x] = 0;
             __syncthreads();
-            const uint64_t i = tile + threadIdx.x;
-            const bool here = i < end;
-            const uint32_t key = here ? key_of(i) : 0u, digit = here ? (key >> shift) & mask : kDigits;
-            const uint32_t index = !here ? 0u : pass == 0 ? static_cast<uint32_t>(i) : load_l2(from_index + i);
-            // the keys of the same digit in the lanes before
-            const uint32_t same = __match_any_sync(0xFFFFFFFFu, digit);
-            const uint32_t rank = __popc(same & ((1u << lane) - 1));
-            if (here && rank == 0) s_warp[warp][digit] = static_cast<unsigned short>(__popc(same));
-            __syncthreads();
-            if (threadIdx.x < kDigits) {   // in the warps before; the tile's keys move the base on
-                uint32_t x = s_base[threadIdx.x];
-                const uint32_t x0 = x;
+#pragma unroll 4
+            for (uint64_t i = first + threadIdx.x; i < end; i += kSortThreads)
+                atomicAdd(&s_count[(key_of(i) >> shift) & (digits - 1)], 1u);
+        }
+        uint64_t tile = first;
+        bool placed = false;   // s_base is set
+        do {
+            uint32_t key[kMostPer], index[kMostPer], rank[kMostPer];
+            const uint64_t mine = tile + warp * (32 * per) + lane;
 #pragma unroll
-                for (uint32_t w = 0; w < kSortThreads / 32; ++w) {
-                    const uint32_t n = s_warp[w][threadIdx.x];
-                    s_warp[w][threadIdx.x] = static_cast<unsigned short>(x - x0);
-                    x += n;
+            for (uint32_t k = 0; k < kMostPer; ++k) {
+                const uint64_t i = mine + 32 * k;
+                if (k >= per || i >= end) continue;
+                key[k] = key_of(i);
+                index[k] = pass == 0 ? static_cast<uint32_t>(i) : load_l2(from_index + i);
+            }
+            s_zeros[threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
+            __syncthreads();
+#pragma unroll
+            for (uint32_t k = 0; k < kMostPer; ++k) {   // the keys of the same digit before this one in the warp
+                if (k >= per) break;
+                const bool here = mine + 32 * k < end;
+                const uint32_t digit = here ? (key[k] >> shift) & (digits - 1) : kDigits;
+                const uint32_t same = __match_any_sync(0xFFFFFFFFu, digit), ahead = __popc(same & ((1u << lane) - 1));
+                const uint32_t so_far = here ? s_warp[warp][digit] : 0u;
+                rank[k] = so_far + ahead;
+                __syncwarp();
+                if (here && ahead == 0) s_warp[warp][digit] = static_cast<unsigned short>(so_far + __popc(same));
+                __syncwarp();
+            }
+            __syncthreads();
+            {   // four threads a digit, 8 warps each
+                constexpr uint32_t kEach = kWarps / 4;
+                const uint32_t digit = threadIdx.x >> 2, part = threadIdx.x & 3;
+                uint32_t n[kEach], sum = 0;
+#pragma unroll
+                for (uint32_t q = 0; q < kEach; ++q) n[q] = s_warp[part * kEach + q][digit];
+#pragma unroll
+                for (uint32_t q = 0; q < kEach; ++q) {
+                    const uint32_t x = n[q];
+                    n[q] = sum;
+                    sum += x;
                 }
-                s_tile[threadIdx.x] = x0;
-                s_base[threadIdx.x] = x;
+                uint32_t before = sum;
+#pragma unroll
+                for (int d = 1; d < 4; d <<= 1) {
+                    const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, before, d);
+                    if (part >= static_cast<uint32_t>(d)) before += x;
+                }
+                if (part == 3) {
+                    s_total[digit] = before;
+                    if (one_tile) s_count[digit] = before;
+                }
+                before -= sum;
+#pragma unroll
+                for (uint32_t q = 0; q < kEach; ++q)
+                    s_warp[part * kEach + q][digit] = static_cast<unsigned short>(n[q] + before);
+            }
+            if (!placed) {   // the CTAs' counts are complete
+                cluster_sync();
+                // keys of smaller digits anywhere, and of the same digit in the CTAs before
+                uint32_t base = 0;
+                if (threadIdx.x < kDigits) {
+                    uint32_t all = 0;
+#pragma unroll
+                    for (uint32_t q = 0; q < kSortCtas; ++q) {
+                        const uint32_t n = load_of_cta(&s_count[threadIdx.x], q);
+                        base += q < me ? n : 0u;
+                        all += n;
+                    }
+                    uint32_t sum = all;   // inclusive scan over the digits
+#pragma unroll
+                    for (int d = 1; d < 32; d <<= 1) {
+                        const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+                        if (lane >= static_cast<uint32_t>(d)) sum += x;
+                    }
+                    if (lane == 31) s_scan[warp] = sum;
+                    base += sum - all;
+                }
+                __syncthreads();
+                if (threadIdx.x < kDigits) {
+                    for (uint32_t q = 0; q < warp; ++q) base += s_scan[q];
+                    s_base[threadIdx.x] = base;
+                }
+                placed = true;
             }
             __syncthreads();
-            if (here) {
-                const uint32_t at = s_tile[digit] + s_warp[warp][digit] + rank;
-                to[at] = key;
-                to_index[at] = index;
+#pragma unroll
+            for (uint32_t k = 0; k < kMostPer; ++k) {
+                if (k >= per || mine + 32 * k >= end) continue;
+                const uint32_t digit = (key[k] >> shift) & (digits - 1);
+                const uint32_t at = s_base[digit] + s_warp[warp][digit] + rank[k];
+                to[at] = key[k];
+                to_index[at] = index[k];
             }
+            tile += tile_keys;
+            if (one_tile || tile >= end) break;
             __syncthreads();
-        }
+            if (threadIdx.x < kDigits) s_base[threadIdx.x] += s_total[threadIdx.x];
+        } while (true);
         cluster_sync();
     }
 }
@@ -250,6 +300,7 @@ struct SumArgs {
 };
 constexpr uint32_t kPiece = 8;
 
+// By all lanes of a warp: a sum, times the factor, into its row of the table.
 template <int DT, bool ALIGNED>
 __device__ __forceinline__ void write_sum(const SumArgs& a, uint32_t id, uint32_t v, int valid, float (&s)[8]) {
     mul8(s, a.scale);
@@ -261,7 +312,7 @@ __device__ __forceinline__ void write_sum(const SumArgs& a, uint32_t id, uint32_
         add8(s, x);
     }
     narrow8<DT>(s, w);
-    store8<ALIGNED>(a.table + id * a.ld_table, v, valid, w);
+    RowOut<ALIGNED>(a.table + id * a.ld_table).template put<true, true>(v, valid, values_left(a.dim, 8ull * (v + 1)), w);
 }
 __device__ __forceinline__ float* partial_at(const SumArgs& a, uint64_t piece, int leaves, uint64_t c) {
     return a.partial + (2 * piece + leaves) * a.width + c;
@@ -276,7 +327,7 @@ __device__ __forceinline__ void write_partial(const SumArgs& a, uint64_t piece, 
 }
 
 template <int DT, bool ALIGNED>
-__global__ void __launch_bounds__(kThreads) k_embedding_sum(const __grid_constant__ SumArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) k_embedding_sum(const __grid_constant__ SumArgs a) {
     pdl_enter();
     const uint64_t item = static_cast<uint64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
     const uint64_t piece = item / a.segments;
@@ -356,16 +407,27 @@ __global__ void __launch_bounds__(kThreads) k_embedding_join(const __grid_consta
     uint32_t id = 0, run = 0;   // the pieces after this one that the run enters
     const uint64_t first = piece * kPiece;
     if (piece + 1 < a.pieces) {
+        const uint32_t none = static_cast<uint32_t>(a.vocab);
         id = load_l2(a.key + first + kPiece - 1);
+        const uint32_t before = first > 0 ? load_l2(a.key + first - 1) : none;
+        const uint64_t q = piece + 1 + lane, rest = a.pieces - piece - 1;
+        const uint32_t next = q < a.pieces ? load_l2(a.key + q * kPiece) : none;
         // a run that fills the whole piece (the ids are sorted) may have begun earlier
-        const bool begins = id < a.vocab && load_l2(a.key + first + kPiece) == id &&
-                            !(first > 0 && load_l2(a.key + first - 1) == id);
-        for (bool more = begins; more;) {
-            const uint64_t q = piece + 1 + run + lane;
-            const uint32_t in = __ballot_sync(0xFFFFFFFFu, q < a.pieces && load_l2(a.key + q * kPiece) == id);
-            const uint32_t n = in == 0xFFFFFFFFu ? 32u : __ffs(~in) - 1;
-            run += n;
-            more = n == 32u;
+        if (id < none && before != id) {
+            const uint32_t in = __ballot_sync(0xFFFFFFFFu, next == id);
+            run = in == 0xFFFFFFFFu ? 32u : __ffs(~in) - 1;
+            if (run == 32u) {   // a long one: its end is in (low, high]; 32 places of that at a time
+                uint64_t low = 31, high = rest;
+                while (high - low > 1) {
+                    const uint64_t step = (high - low + 31) / 32, at = low + (lane + 1) * step;
+                    const uint32_t still = __ballot_sync(0xFFFFFFFFu, at < high && load_l2(a.key + (piece + 1 + at) * kPiece) == id);
+                    const uint32_t n = still == 0xFFFFFFFFu ? 32u : __ffs(~still) - 1;   // sorted: the first n are in the run
+                    const uint64_t to = low + (n + 1) * step;
+                    low += n * step;
+                    high = to < high ? to : high;
+                }
+                run = static_cast<uint32_t>(high);
+            }
         }
     }
     float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
@@ -391,7 +453,7 @@ __global__ void __launch_bounds__(kThreads) k_embedding_join(const __grid_consta
         for (int e = 0; e < 8; ++e) s[e] = 0.0f;
         if (valid > 0) {
             if (warp == 0) add(s, from, 1);
-#pragma unroll 4
+#pragma unroll 8
             for (uint32_t i = warp; i < pieces; i += kJoinPieces) add(s, from + 1 + i, 0);
         }
         float4* mine = reinterpret_cast<float4*>(&s_sum[warp][8 * lane]);

@@ -50,75 +50,85 @@ __device__ __forceinline__ int inside(uint32_t v, uint32_t cols) {
     return ALIGNED ? (left > 0 ? 8 : 0) : left > 8 ? 8 : left;
 }
 
+// f(0), f(1), ... f(N - 1), the number known to the compiler.
+template <int N, typename F, int... I>
+__device__ __forceinline__ void each(F&& f, std::integer_sequence<int, I...>) {
+    (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void each(F&& f) {
+    each<N>(f, std::make_integer_sequence<int, N>{});
+}
+
 // ----------------------------------------------------------------- dropout
 struct DropoutArgs {
     const unsigned short* src;
     unsigned short* dst;
     uint64_t rows, cols, ld_src, ld_dst;
     uint64_t across;           // groups of 8 columns in a row
-    uint64_t segments, items;  // of 256 columns in a row, and in all
+    uint64_t segments, items;  // of kDropVecs * 256 columns in a row, and in all
     DropArgs drop;
 };
 constexpr int kDropVecs = 4;
 
-template <int DT, bool ALIGNED>
-__device__ __forceinline__ void drop_one(const DropoutArgs& a, unsigned short* row, uint32_t v, int valid, uint64_t group,
-                                         uint64_t stream, const uint32_t (&w)[4]) {
+template <int DT>
+__device__ __forceinline__ void drop_one(const DropoutArgs& a, uint64_t group, uint64_t stream, const uint32_t (&w)[4],
+                                         uint32_t (&q)[4]) {
     float x[8];
     widen8<DT>(w, x);
     if (a.drop.below) drop8(a.drop, group, stream, x);
-    uint32_t q[4];
     narrow8<DT>(x, q);
-    store8<ALIGNED>(row, v, valid, q);
 }
 
 // Rows without gaps, of whole eights: a group's number is its place.  A thread
 // takes kDropVecs groups, their loads in flight together.  HBM and the
-// generator's products about even: 8192 x 4096 bf16 in 21.4 us (6.3 TB/s).
+// generator's products about even: 8192 x 4096 bf16 in 21 us (6.4 TB/s).
 template <int DT>
 __global__ void __launch_bounds__(kThreads) k_dropout(const __grid_constant__ DropoutArgs a) {
     pdl_enter();
     const uint64_t stream = drop_stream(a.drop), first = static_cast<uint64_t>(blockIdx.x) * kDropVecs * kThreads + threadIdx.x;
-    Fetched<true> f[kDropVecs];
+    const uint4* src = reinterpret_cast<const uint4*>(a.src);
+    uint4 x[kDropVecs];
 #pragma unroll
     for (int i = 0; i < kDropVecs; ++i) {
         const uint64_t g = first + static_cast<uint64_t>(i) * kThreads;
-        fetch8(RowIn<true>{reinterpret_cast<const uint4*>(a.src) + g}, 0, g < a.across ? 8 : 0, f[i]);
+        if (g < a.across) x[i] = __ldcs(src + g);
     }
 #pragma unroll
     for (int i = 0; i < kDropVecs; ++i) {
         const uint64_t g = first + static_cast<uint64_t>(i) * kThreads;
-        const uint32_t w[4] = {f[i].x.x, f[i].x.y, f[i].x.z, f[i].x.w};
-        drop_one<DT, true>(a, a.dst + 8 * g, 0, g < a.across ? 8 : 0, g, stream, w);
+        if (g >= a.across) continue;
+        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        uint32_t q[4];
+        drop_one<DT>(a, g, stream, w, q);
+        __stcs(reinterpret_cast<uint4*>(a.dst) + g, make_uint4(q[0], q[1], q[2], q[3]));
     }
 }
 
-// Any rows: a warp takes kDropVecs pieces of 256 columns, row after row.
+// Any rows: a warp takes up to kDropVecs times 256 columns of a row.
 template <int DT, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads) k_dropout_rows(const __grid_constant__ DropoutArgs a) {
     pdl_enter();
     const uint64_t stream = drop_stream(a.drop);
-    const uint64_t item = (static_cast<uint64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5)) * kDropVecs;
+    const uint64_t item = static_cast<uint64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+    if (item >= a.items) return;
+    const uint64_t row = item / a.segments;
+    const uint32_t v0 = static_cast<uint32_t>(item - row * a.segments) * (kDropVecs * 32) + (threadIdx.x & 31);
+    const RowIn<ALIGNED> in = row_in<ALIGNED>(a.src, row, a.ld_src, a.rows, a.cols);
+    RowOut<ALIGNED> out(a.dst + row * a.ld_dst);
     Fetched<ALIGNED> f[kDropVecs];
-    uint64_t row[kDropVecs];
-    uint32_t v[kDropVecs];
-    int valid[kDropVecs];
-    RowIn<ALIGNED> in[kDropVecs];
+    auto valid = [&](uint32_t v) { return values_left(a.cols, 8ull * v); };
 #pragma unroll
-    for (int i = 0; i < kDropVecs; ++i) {
-        const uint64_t at = item + i < a.items ? item + i : a.items - 1;
-        row[i] = a.items <= 0xFFFFFFFFull ? static_cast<uint32_t>(at) / static_cast<uint32_t>(a.segments) : at / a.segments;
-        v[i] = static_cast<uint32_t>(at - row[i] * a.segments) * 32 + (threadIdx.x & 31);
-        valid[i] = item + i < a.items ? values_left(a.cols, 8ull * v[i]) : 0;
-        in[i] = row_in<ALIGNED>(a.src, row[i], a.ld_src, a.rows, a.cols);
-        fetch8(in[i], v[i], valid[i], f[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < kDropVecs; ++i) {
-        uint32_t w[4];
-        finish8(in[i], v[i], valid[i], f[i], w);
-        drop_one<DT, ALIGNED>(a, a.dst + row[i] * a.ld_dst, v[i], valid[i], row[i] * a.across + v[i], stream, w);
-    }
+    for (int i = 0; i < kDropVecs; ++i) fetch8(in, v0 + 32 * i, valid(v0 + 32 * i), f[i]);
+    each<kDropVecs>([&](auto step) {
+        constexpr int i = decltype(step)::value;
+        const uint32_t v = v0 + 32 * i;
+        if (8ull * (v & ~31u) >= a.cols) return;   // the same in all lanes
+        uint32_t w[4], q[4];
+        finish8(in, v, valid(v), f[i], w);
+        drop_one<DT>(a, row * a.across + v, stream, w, q);
+        out.template put<i == 0, i + 1 == kDropVecs>(v, valid(v), valid(v + 1), q);
+    });
 }
 
 // -------------------------------------------------------------------- norm
@@ -130,28 +140,39 @@ struct NormArgs {
     uint64_t pitch, tiles_k;   // of the codes; 0 tiles without them
     uint64_t across;           // groups of 8 columns in a row
     float eps;
-    int by_warp;               // a row a warp; else a row a block
+    uint32_t row_threads;      // of a row; a block has several rows where these are few
     DropArgs drop;
 };
 
+// The threads of a row: whole warps, and a block has 256 threads or one row.
+struct RowThreads {
+    uint32_t threads, slot, t;   // of a row; which row of the block; which of the row's threads
+    __device__ __forceinline__ explicit RowThreads(uint32_t n) : threads(n), slot(threadIdx.x / n), t(threadIdx.x - slot * n) {}
+    // All threads of the row have come here; each row of a block has a barrier of its own.
+    __device__ __forceinline__ void sync() const {
+        if (threads == 32) __syncwarp();
+        else if (threads == blockDim.x) __syncthreads();
+        else asm volatile("barrier.sync %0, %1;" ::"r"(slot + 1), "r"(threads) : "memory");
+    }
+};
 // N sums over the threads of a row, in all of them.
 template <int N>
-__device__ __forceinline__ void row_sums(float (&s)[N], bool by_warp, float (*shared)[32]) {
+__device__ __forceinline__ void row_sums(float (&s)[N], const RowThreads& row, float (*shared)[32]) {
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1)
 #pragma unroll
         for (int k = 0; k < N; ++k) s[k] += __shfl_xor_sync(0xFFFFFFFFu, s[k], d);
-    if (by_warp) return;
-    const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    if (row.threads == 32) return;
+    const uint32_t first = (row.slot * row.threads) >> 5, warps = row.threads >> 5;
     if ((threadIdx.x & 31) == 0) {
 #pragma unroll
-        for (int k = 0; k < N; ++k) shared[k][warp] = s[k];
+        for (int k = 0; k < N; ++k) shared[k][threadIdx.x >> 5] = s[k];
     }
-    __syncthreads();
+    row.sync();
 #pragma unroll
     for (int k = 0; k < N; ++k) {
         s[k] = 0.0f;
-        for (int i = 0; i < warps; ++i) s[k] += shared[k][i];
+        for (uint32_t i = 0; i < warps; ++i) s[k] += shared[k][first + i];
     }
 }
 __device__ __forceinline__ float rsqrt_of(float sum, uint64_t cols, float eps) {
@@ -197,34 +218,35 @@ template <int BITS, int DT, int V, bool ALIGNED>
 __global__ void __launch_bounds__(V == 4 ? 512 : 1024, V == 4 && ALIGNED ? 2 : 1) k_rms_norm(const __grid_constant__ NormArgs a) {
     pdl_enter();
     __shared__ float s_sum[1][32];
-    const uint32_t threads = a.by_warp ? 32u : blockDim.x, t = a.by_warp ? threadIdx.x & 31u : threadIdx.x;
-    const uint64_t row = a.by_warp ? static_cast<uint64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
+    const RowThreads team(a.row_threads);
+    const uint32_t threads = team.threads, t = team.t;
+    const uint64_t row = static_cast<uint64_t>(blockIdx.x) * (blockDim.x / threads) + team.slot;
     if (row >= a.rows) {   // uniform over a row's threads; the unused rows of the last scale tiles
         if (BITS != 0 && row < (a.rows + 127) / 128 * 128)
             for (uint64_t k = t; k < a.tiles_k; k += threads)
                 *reinterpret_cast<uint32_t*>(a.scales + scale_at(row, 4 * k, a.tiles_k)) = 0u;
         return;
     }
-    const uint32_t cols = static_cast<uint32_t>(a.cols);
+    const uint32_t cols = static_cast<uint32_t>(a.cols), v0 = (t >> 5) * (32 * V) + (t & 31);
     Fetched<ALIGNED> x[V], res[V];
     uint32_t h[V][4];
     const RowIn<ALIGNED> in_x = row_in<ALIGNED>(a.x, row, a.ld_x, a.rows, a.cols);
     const RowIn<ALIGNED> in_res = row_in<ALIGNED>(a.residual, row, a.ld_residual, a.rows, a.cols);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        const uint32_t v = j * threads + t;
+        const uint32_t v = v0 + 32 * j;
         fetch8(in_x, v, inside<ALIGNED>(v, cols), x[j]);
         if (a.residual) fetch8(in_res, v, inside<ALIGNED>(v, cols), res[j]);
     }
-    const uint64_t stream = drop_stream(a.drop), group = row * a.across + t;
+    const uint64_t stream = drop_stream(a.drop), group = row * a.across;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        const uint32_t v = j * threads + t;
+        const uint32_t v = v0 + 32 * j;
         finish8(in_x, v, inside<ALIGNED>(v, cols), x[j], h[j]);
         if (a.residual || a.drop.below) {
             float y[8];
             widen8<DT>(h[j], y);
-            if (a.drop.below) drop8(a.drop, group + j * threads, stream, y);
+            if (a.drop.below) drop8(a.drop, group + v, stream, y);
             if (a.residual) {
                 uint32_t q[4];
                 finish8(in_res, v, inside<ALIGNED>(v, cols), res[j], q);
@@ -236,21 +258,22 @@ __global__ void __launch_bounds__(V == 4 ? 512 : 1024, V == 4 && ALIGNED ? 2 : 1
         }
     }
     float sums[2] = {0.0f, 0.0f};
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        const uint32_t v = j * threads + t;
-        if (a.h) store8<ALIGNED>(a.h + row * a.ld_h, v, inside<ALIGNED>(v, cols), h[j]);
+    RowOut<ALIGNED> out_h(a.h + row * a.ld_h), out_y(a.out + row * a.ld_out);
+    each<V>([&](auto step) {
+        constexpr int j = decltype(step)::value;
+        const uint32_t v = v0 + 32 * j;
+        if (a.h) out_h.template put<j == 0, j + 1 == V>(v, inside<ALIGNED>(v, cols), inside<ALIGNED>(v + 1, cols), h[j]);
         float y[8];
         widen8<DT>(h[j], y);
         dot8(y, y, sums);
-    }
+    });
     float sum[1] = {sums[0] + sums[1]};
-    row_sums<1>(sum, a.by_warp, s_sum);
+    row_sums<1>(sum, team, s_sum);
     const float r = rsqrt_of(sum[0], a.cols, a.eps);
     const RowIn<ALIGNED> in_w = row_in<ALIGNED>(a.weight, 0, 0, 1, a.cols);
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        const uint32_t v = j * threads + t;
+    each<V>([&](auto step) {
+        constexpr int j = decltype(step)::value;
+        const uint32_t v = v0 + 32 * j;
         const int valid = inside<ALIGNED>(v, cols);
         uint32_t w[4];
         read_weight<ALIGNED>(in_w, v, valid, w);
@@ -262,10 +285,10 @@ __global__ void __launch_bounds__(V == 4 ? 512 : 1024, V == 4 && ALIGNED ? 2 : 1
         if (a.out) {
             uint32_t q[4];
             narrow8<DT>(y, q);
-            store8<ALIGNED>(a.out + row * a.ld_out, v, valid, q);
+            out_y.template put<j == 0, j + 1 == V>(v, valid, inside<ALIGNED>(v + 1, cols), q);
         }
         if constexpr (BITS != 0) write_codes<BITS>(a, row, v, valid, y);
-    }
+    });
 }
 
 // ---------------------------------------------------------- norm, backward
@@ -276,7 +299,7 @@ struct NormGradArgs {
     uint64_t rows, cols, ld_dy, ld_h, ld_in, ld_dh, ld_dx;
     uint64_t across;
     float eps;
-    int by_warp;
+    uint32_t row_threads;
     DropArgs drop;
 };
 
@@ -292,39 +315,39 @@ __device__ __forceinline__ void copy_wait() {   // all but the last N groups
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 constexpr int kGradStages = 2;
-constexpr size_t grad_ring(size_t v, size_t threads) {   // bytes: a slot more a warp, see below
-    return size_t{3} * kGradStages * (v * threads + threads / 32) * sizeof(uint4);
+constexpr size_t grad_ring(size_t v, size_t row_threads, size_t rows) {   // bytes; a slot more a row, see below
+    return 3 * kGradStages * rows * (v * row_threads + 1) * sizeof(uint4);
 }
-constexpr size_t kMostGradSmem = grad_ring(4, 512);
+constexpr size_t kMostGradSmem = grad_ring(4, 512, 1);
+static_assert(kMostGradSmem >= grad_ring(2, 64, 4) && kMostGradSmem >= grad_ring(4, 32, 8), "shared memory");
 
-// A block takes rows blockIdx.x, + gridDim.x, ... (by_warp: one a warp at a
-// time), and keeps its share of dw in registers over all of them.  The next
+// A block takes its rows blockIdx.x, + gridDim.x, ..., and keeps its share of dw in registers over all of them.  The next
 // row is on its way to shared memory while this one is worked on: 62 us for
 // 8192 x 4096 bf16 with dropout (5.4 TB/s) against 70 with the next row in
 // registers and 94 without.  Rows that start between two 16-byte boundaries
 // are copied as the aligned pieces that cover them; a thread then needs two
 // neighbouring pieces, of which another thread copied the second.
 template <int DT, int V, bool ALIGNED>
-__global__ void __launch_bounds__(512) k_rms_norm_backward(const __grid_constant__ NormGradArgs a) {
+__global__ void __maxnreg__(V == 4 || ALIGNED ? 128 : 96) k_rms_norm_backward(const __grid_constant__ NormGradArgs a) {
     pdl_enter();
     __shared__ float s_sum[2][2][32];
-    // [row's slots][stage][h, dy, dh_in][width]; at the end, by_warp: [warps][8 * across] floats
+    // [row of the block][stage][h, dy, dh_in][width]; at the end, with several rows: [row][8 * across] floats
     extern __shared__ __align__(16) uint4 s_rows[];
-    const uint32_t threads = a.by_warp ? 32u : blockDim.x, t = a.by_warp ? threadIdx.x & 31u : threadIdx.x;
-    const uint32_t slots = a.by_warp ? blockDim.x >> 5 : 1u, slot = a.by_warp ? threadIdx.x >> 5 : 0u;
+    const RowThreads team(a.row_threads);
+    const uint32_t threads = team.threads, t = team.t, slot = team.slot, slots = blockDim.x / threads;
     const uint64_t step = static_cast<uint64_t>(gridDim.x) * slots;
     const uint64_t stream = drop_stream(a.drop);
-    const uint32_t cols = static_cast<uint32_t>(a.cols);
+    const uint32_t cols = static_cast<uint32_t>(a.cols), v0 = (t >> 5) * (32 * V) + (t & 31);
     float dw[V][8];
     uint32_t w[V][4];
     // a row's slots: one for each group, and one for the piece behind the last
-    const uint32_t width = V * threads + 1, each = 3 * kGradStages * width;
-    uint4* const mine = s_rows + (a.by_warp ? slot * each : 0u);
+    const uint32_t width = V * threads + 1, room = 3 * kGradStages * width;
+    uint4* const mine = s_rows + slot * room;
     auto place = [&](uint32_t stage, int which, uint32_t v) -> uint4& { return mine[(stage * 3 + which) * width + v]; };
     const RowIn<ALIGNED> in_w = row_in<ALIGNED>(a.weight, 0, 0, 1, a.cols);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        const uint32_t v = j * threads + t;
+        const uint32_t v = v0 + 32 * j;
         const int valid = inside<ALIGNED>(v, cols);
         read_weight<ALIGNED>(in_w, v, valid, w[j]);
 #pragma unroll
@@ -338,7 +361,7 @@ __global__ void __launch_bounds__(512) k_rms_norm_backward(const __grid_constant
     auto copy_row = [&](const RowIn<ALIGNED>& r, uint32_t stage, int which) {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const uint32_t v = j * threads + t;
+            const uint32_t v = v0 + 32 * j;
             const int valid = inside<ALIGNED>(v, cols);
             if (valid <= 0) continue;
             if constexpr (ALIGNED) {
@@ -368,47 +391,66 @@ __global__ void __launch_bounds__(512) k_rms_norm_backward(const __grid_constant
             copy_wait<1>();
         } else {
             copy_wait<0>();
-            if (a.by_warp) __syncwarp();   // the others' copies are there, and what they read of the row before is read
-            else __syncthreads();
+            team.sync();   // the others' copies are there, and what they read of the row before is read
             start(row + step, flip ^ 1);
         }
-        RowIn<ALIGNED> in[3] = {row_in<ALIGNED>(a.h, row, a.ld_h, a.rows, a.cols), row_in<ALIGNED>(a.dy, row, a.ld_dy, a.rows, a.cols),
-                                row_in<ALIGNED>(a.dh_in, row, a.ld_in, a.rows, a.cols)};
-        auto values = [&](int which, int j, float (&x)[8]) {
-            const uint32_t v = j * threads + t;
+        auto values = [&](int which, int j, const unsigned short* base, uint64_t ld, uint32_t (&q)[4]) {
+            const uint32_t v = v0 + 32 * j;
             const uint4 p = place(flip, which, v);
-            uint32_t q[4] = {p.x, p.y, p.z, p.w};
+            q[0] = p.x; q[1] = p.y; q[2] = p.z; q[3] = p.w;
             if constexpr (!ALIGNED) {
                 const uint4 n = place(flip, which, v + 1);
                 const uint32_t own[4] = {p.x, p.y, p.z, p.w}, next[4] = {n.x, n.y, n.z, n.w};
-                shift_halves(own, next, in[which].m & 7u, q);
-                clear_from(q, inside<false>(v, cols));
+                shift_halves(own, next, row_in<false>(base, row, ld, a.rows, a.cols).m & 7u, q);
+                const int valid = inside<false>(v, cols);
+                if (valid < 8) clear_tail(q, valid);
             }
-            widen8<DT>(q, x);
         };
+        // what had to be put together is kept for the second pass, where there are registers for it
+        constexpr bool kHold = !ALIGNED && V <= 2;
+        uint32_t held[kHold ? V : 1][2][4];
         float ss[2] = {0.0f, 0.0f}, sg[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int j = 0; j < V; ++j) {
+            uint32_t p[4], q[4];
+            values(0, j, a.h, a.ld_h, p);
+            values(1, j, a.dy, a.ld_dy, q);
+            if constexpr (kHold) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    held[j][0][i] = p[i];
+                    held[j][1][i] = q[i];
+                }
+            }
             float x[8], y[8], f[8];
-            values(0, j, x);
-            values(1, j, y);
+            widen8<DT>(p, x);
+            widen8<DT>(q, y);
             widen8<DT>(w[j], f);
             mul8(y, f);
             dot8(x, x, ss);
             dot8(y, x, sg);
         }
         float sums[2] = {ss[0] + ss[1], sg[0] + sg[1]};
-        row_sums<2>(sums, a.by_warp, s_sum[flip]);
+        row_sums<2>(sums, team, s_sum[flip]);
         const float r = rsqrt_of(sums[0], a.cols, a.eps);
         const float k = __fmul_rn(__fmul_rn(r, r), __fdiv_rn(sums[1], static_cast<float>(a.cols)));
-        const uint64_t group = row * a.across + t;
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const uint32_t v = j * threads + t;
-            const int valid = inside<ALIGNED>(v, cols);
+        const uint64_t group = row * a.across;
+        RowOut<ALIGNED> out_h(a.dh + row * a.ld_dh), out_x(a.dx + row * a.ld_dx);
+        each<V>([&](auto number) {
+            constexpr int j = decltype(number)::value;
+            const uint32_t v = v0 + 32 * j;
+            const int valid = inside<ALIGNED>(v, cols), next = inside<ALIGNED>(v + 1, cols);
+            uint32_t q[4];
             float x[8], y[8], f[8];
-            values(0, j, x);
-            values(1, j, y);
+            if constexpr (kHold) {
+                widen8<DT>(held[j][0], x);
+                widen8<DT>(held[j][1], y);
+            } else {
+                values(0, j, a.h, a.ld_h, q);
+                widen8<DT>(q, x);
+                values(1, j, a.dy, a.ld_dy, q);
+                widen8<DT>(q, y);
+            }
             widen8<DT>(w[j], f);
             mul8(f, y);          // g
             float u[8];
@@ -419,26 +461,26 @@ __global__ void __launch_bounds__(512) k_rms_norm_backward(const __grid_constant
             mul8(x, r);
             fma8(y, x, dw[j]);
             if (a.dh_in) {
-                values(2, j, x);
+                values(2, j, a.dh_in, a.ld_in, q);
+                widen8<DT>(q, x);
                 add8(f, x);
             }
-            uint32_t q[4];
             narrow8<DT>(f, q);
-            store8<ALIGNED>(a.dh + row * a.ld_dh, v, valid, q);
+            out_h.template put<j == 0, j + 1 == V>(v, valid, next, q);
             if (a.dx) {
-                if (a.drop.below) drop8(a.drop, group + j * threads, stream, f);
+                if (a.drop.below) drop8(a.drop, group + v, stream, f);
                 narrow8<DT>(f, q);
-                store8<ALIGNED>(a.dx + row * a.ld_dx, v, valid, q);
+                out_x.template put<j == 0, j + 1 == V>(v, valid, next, q);
             }
-        }
+        });
     }
     copy_wait<0>();
     if (!a.partial) return;
     float* out = a.partial + static_cast<uint64_t>(blockIdx.x) * 8 * a.across;
-    if (!a.by_warp) {
+    if (slots == 1) {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const uint64_t v = j * threads + t;
+            const uint32_t v = v0 + 32 * j;
             if (v >= a.across) continue;
             float4* to = reinterpret_cast<float4*>(out + 8 * v);
             to[0] = make_float4(dw[j][0], dw[j][1], dw[j][2], dw[j][3]);
@@ -446,13 +488,13 @@ __global__ void __launch_bounds__(512) k_rms_norm_backward(const __grid_constant
         }
         return;
     }
-    // the warps' shares, added in their order, where the rows were
+    // the rows' shares, added in their order, where the rows were
     __syncthreads();
     float* const s_dw = reinterpret_cast<float*>(s_rows);
     const uint32_t values = static_cast<uint32_t>(8 * a.across);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        const uint32_t v = j * threads + t;
+        const uint32_t v = v0 + 32 * j;
         if (v >= a.across) continue;
         float4* to = reinterpret_cast<float4*>(s_dw + slot * values + 8 * v);
         to[0] = make_float4(dw[j][0], dw[j][1], dw[j][2], dw[j][3]);
@@ -477,7 +519,7 @@ __global__ void __launch_bounds__(1024) k_norm_dweight(const float* partial, uin
     const uint64_t c = static_cast<uint64_t>(blockIdx.x) * 32 + lane;
     float sum = 0.0f;
     if (c < cols) {
-#pragma unroll 4
+#pragma unroll 10
         for (uint64_t p = warp; p < parts; p += 32) sum += partial[p * width + c];
     }
     s[warp][lane] = sum;
@@ -532,7 +574,7 @@ cudaError_t launch_norm(const NormArgs& a, int v, bool whole, unsigned blocks, u
 }
 template <int DT, int V>
 cudaError_t launch_norm_grad(const NormGradArgs& a, bool whole, unsigned blocks, unsigned threads, size_t smem, cudaStream_t s) {
-    const size_t ring = grad_ring(V, threads);
+    const size_t ring = grad_ring(V, a.row_threads, threads / a.row_threads);
     if (ring > smem) smem = ring;
     cudaError_t e;
     if ((e = allow_smem<k_rms_norm_backward<DT, V, true>>(kMostGradSmem)) != cudaSuccess ||
@@ -549,31 +591,40 @@ cudaError_t launch_norm_grad(const NormGradArgs& a, int v, bool whole, unsigned 
                     : launch_norm_grad<DT, 4>(a, whole, blocks, threads, smem, s);
 }
 
-// How a row of `groups` eights lies over threads: a warp up to 128 of them,
-// else a block of `most` threads or fewer with `v` eights each.
+// How a row of `groups` eights lies over threads: `v` eights each, as near to
+// `most_v` (a power of two) as leaves no more than three tenths of the threads'
+// places empty, and more where the threads would be over `most`.  (Fewer eights
+// a thread cost more than some empty places: 8192 x 768 forward 17 us at 4 of
+// which a quarter is empty, 22 at 1 of which none is; backward 18 and 27.)
 struct RowShape {
-    int v, by_warp;
-    unsigned threads;   // of a block
-    unsigned rows;      // of a block at a time
+    int v;
+    unsigned row_threads, rows;   // rows: of a block at a time
 };
-RowShape row_shape(uint64_t groups, unsigned warp_groups, unsigned least_v, unsigned most) {
-    RowShape r;
-    if (groups <= warp_groups) {
-        r.by_warp = 1;
-        r.v = groups <= 32 ? 1 : groups <= 64 ? 2 : 4;
-        r.threads = kThreads;
-        r.rows = kThreads / 32;
-        return r;
+RowShape row_shape(uint64_t groups, int most_v, unsigned most) {
+    auto of = [&](int v) {
+        const unsigned n = static_cast<unsigned>(up((groups + v - 1) / v, 32));
+        return RowShape{v, n, n < kThreads ? kThreads / n : 1u};
+    };
+    RowShape r = of(most_v);
+    for (int v = most_v; v >= 1; v /= 2) {
+        const RowShape s = of(v);
+        if (s.row_threads > most) break;
+        const auto places = [](const RowShape& x) { return static_cast<uint64_t>(x.v) * x.row_threads; };
+        if (places(s) < places(r) || r.row_threads > most) r = s;
+        if (10 * groups >= 7 * places(r)) break;
     }
-    r.by_warp = 0;
-    r.v = static_cast<int>(least_v);
-    while (groups > static_cast<uint64_t>(r.v) * most) r.v *= 2;
-    r.threads = static_cast<unsigned>(up((groups + r.v - 1) / r.v, 32));
-    r.rows = 1;
+    while (r.row_threads > most) r = of(2 * r.v);
     return r;
 }
+// Few rows finish sooner with more threads each; many are cheaper a row with
+// fewer: 64 x 4096 with dropout into 8 bits 4.2, 4.4 and 5.3 us at 1, 2 and 4
+// eights a thread, 608 x 4096 9.6, 8.2 and 9.5, 8192 x 4096 76, 68 and 61.
+RowShape norm_shape(uint64_t rows, uint64_t groups) {
+    const int v = rows >= 1216 ? 4 : rows >= 304 ? 2 : 1;
+    return row_shape(groups, v, v == 4 ? 512 : 1024);
+}
 constexpr unsigned kGradBlocks = 304;   // two an SM
-RowShape grad_shape(uint64_t cols) { return row_shape((cols + 7) / 8, 128, 2, 512); }
+RowShape grad_shape(uint64_t cols) { return row_shape((cols + 7) / 8, cols <= 1024 ? 4 : 2, 512); }
 uint64_t grad_blocks(uint64_t rows, const RowShape& r) {
     const uint64_t b = (rows + r.rows - 1) / r.rows;
     return b < kGradBlocks ? b : kGradBlocks;
@@ -609,11 +660,11 @@ int zero_dropout(int dtype, uint64_t rows, uint64_t cols, const void* src16, uin
     a.ld_src = ld_src;
     a.ld_dst = ld_out;
     a.across = (cols + 7) / 8;
-    a.segments = (cols + 255) / 256;
+    a.segments = (cols + kDropVecs * 256 - 1) / (kDropVecs * 256);
     if (a.across > (1ull << 40) / rows) return refuse(ZERO_EINVAL, "rows and cols are too large together");
     a.items = rows * a.segments;
     const bool one = whole && rows == 1, fp16 = dtype == ZERO_FP16;
-    const uint64_t per = one ? kDropVecs * kThreads : kDropVecs * kThreads / 32;
+    const uint64_t per = one ? kDropVecs * kThreads : kThreads / 32;
     const uint64_t blocks = ((one ? a.across : a.items) + per - 1) / per;
     if (blocks > 0x7FFFFFFFull) return refuse(ZERO_EINVAL, "rows and cols are too large together");
     const cudaError_t e = launch_pdl(one     ? (fp16 ? k_dropout<kFp16> : k_dropout<kBf16>)
@@ -661,8 +712,8 @@ int zero_rms_norm(int dtype, uint64_t rows, uint64_t cols, const void* x16, uint
     a.pitch = up(cols, kMxBlock) * bits / 8;
     a.tiles_k = bits ? up(cols, 128) / 128 : 0;
     a.eps = eps;
-    const RowShape r = row_shape(bits ? 16 * a.tiles_k : a.across, 128, 1, 1024);
-    a.by_warp = r.by_warp;
+    const RowShape r = norm_shape(rows, bits ? 16 * a.tiles_k : a.across);
+    a.row_threads = r.row_threads;
     const uint64_t all = bits ? up(rows, 128) : rows;
     const unsigned blocks = static_cast<unsigned>((all + r.rows - 1) / r.rows);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -670,7 +721,7 @@ int zero_rms_norm(int dtype, uint64_t rows, uint64_t cols, const void* x16, uint
     const auto of = bits == 0   ? (fp16 ? launch_norm<0, kFp16> : launch_norm<0, kBf16>)
                     : bits == 4 ? (fp16 ? launch_norm<4, kFp16> : launch_norm<4, kBf16>)
                                 : (fp16 ? launch_norm<8, kFp16> : launch_norm<8, kBf16>);
-    const cudaError_t e = of(a, r.v, whole, blocks, r.threads, s);
+    const cudaError_t e = of(a, r.v, whole, blocks, r.rows * r.row_threads, s);
     return e == cudaSuccess ? ZERO_OK : cuda_refuse(e, "zero_rms_norm");
 }
 
@@ -725,11 +776,11 @@ int zero_rms_norm_backward(int dtype, uint64_t rows, uint64_t cols, const void* 
     a.ld_dx = ld_dx;
     a.across = (cols + 7) / 8;
     a.eps = eps;
-    a.by_warp = r.by_warp;
-    const size_t smem = r.by_warp && dweight16 ? r.rows * 8 * a.across * sizeof(float) : 0;   // 32 KiB at most
+    a.row_threads = r.row_threads;
+    const size_t smem = r.rows > 1 && dweight16 ? r.rows * 8 * a.across * sizeof(float) : 0;   // less than the rows' own
     const bool fp16 = dtype == ZERO_FP16;
-    e = fp16 ? launch_norm_grad<kFp16>(a, r.v, whole, blocks, r.threads, smem, s)
-             : launch_norm_grad<kBf16>(a, r.v, whole, blocks, r.threads, smem, s);
+    e = fp16 ? launch_norm_grad<kFp16>(a, r.v, whole, blocks, r.rows * r.row_threads, smem, s)
+             : launch_norm_grad<kBf16>(a, r.v, whole, blocks, r.rows * r.row_threads, smem, s);
     if (e == cudaSuccess && dweight16)
         e = launch_pdl(fp16 ? k_norm_dweight<kFp16> : k_norm_dweight<kBf16>, dim3(static_cast<unsigned>((cols + 31) / 32)), 1024, 0,
                        1, s, static_cast<const float*>(a.partial), static_cast<uint64_t>(blocks), 8 * a.across, cols,

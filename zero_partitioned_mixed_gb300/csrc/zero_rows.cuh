@@ -23,7 +23,7 @@ __device__ __forceinline__ void shift_halves(const uint32_t (&lo)[4], const uint
         for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) out[i] = m & 1 ? __funnelshift_r(w[i], w[i + 1], 16) : w[i];
+    for (int i = 0; i < 4; ++i) out[i] = __funnelshift_r(w[i], w[i + 1], 16 * (m & 1));
 }
 
 // The aligned piece whose first value is `at` (which may lie before the
@@ -183,6 +183,17 @@ __device__ __noinline__ void store_some(unsigned short* at, uint4 x, int from, i
         if (e >= from && e < to) at[e] = static_cast<unsigned short>(w[e >> 1] >> (16 * (e & 1)));
 }
 
+// Zeros from value `valid` on: rare too.
+__device__ __noinline__ uint4 without_tail(uint4 x, int valid) {
+    uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    clear_from(w, valid);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void clear_tail(uint32_t (&w)[4], int valid) {
+    const uint4 x = without_tail(make_uint4(w[0], w[1], w[2], w[3]), valid);
+    w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+}
+
 template <bool ALIGNED>
 struct RowIn;
 template <>
@@ -237,7 +248,7 @@ __device__ __forceinline__ void finish8(const RowIn<false>& r, uint32_t v, int v
     if (r.m < 8u) {
         const uint32_t own[4] = {f.x.x, f.x.y, f.x.z, f.x.w}, next[4] = {f.y.x, f.y.y, f.y.z, f.y.w};
         shift_halves(own, next, r.m, w);
-        clear_from(w, valid);
+        if (valid < 8) clear_tail(w, valid);
     } else {
         const uint4 x = valid > 0 ? read_some(r.row + 8ull * v, valid) : make_uint4(0u, 0u, 0u, 0u);
         w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
@@ -264,19 +275,35 @@ __device__ __forceinline__ void store_high(uint4* piece, const uint32_t (&q)[4],
     if (k & 1) reinterpret_cast<uint32_t*>(piece)[k] = k == 1 ? q[1] : q[3];
     if (k <= 2) reinterpret_cast<uint2*>(piece)[1] = make_uint2(q[2], q[3]);
 }
-// Group v into a row, by all lanes of a warp together.  The piece between two
-// warps is written by lane 0 of either: its own values, and those of this
-// warp's lane 31, which come round to it.  What ends the row is written value
-// by value.  4001 x 5003 bf16 through the norm and into 8 bits takes XXX us,
-// against 91 with every value of lanes 0 and 31 by itself.
+// A row's groups written by all lanes of a warp together, 32 consecutive ones
+// at a time and these one after the other (put), and at the end what is left
+// between this warp and the next (finish).  Not ALIGNED: a lane writes the
+// aligned piece with the last values of the lane before it, lane 0 with those
+// that lane 31 had the last time; the piece between two warps is written by
+// lane 0 of either; what ends the row is written value by value.
 template <bool ALIGNED>
-__device__ __forceinline__ void store8(unsigned short* row, uint32_t v, int valid, const uint32_t (&w)[4]) {
-    if constexpr (ALIGNED) {
-        if (valid > 0) __stcs(reinterpret_cast<uint4*>(row) + v, make_uint4(w[0], w[1], w[2], w[3]));
-    } else {
+struct RowOut;
+template <>
+struct RowOut<true> {
+    uint4* row;
+    __device__ __forceinline__ explicit RowOut(unsigned short* at) : row(reinterpret_cast<uint4*>(at)) {}
+    // `next`: how many values of group v + 1 are inside the row
+    template <bool FIRST, bool LAST>
+    __device__ __forceinline__ void put(uint32_t v, int valid, int, const uint32_t (&w)[4]) {
+        if (valid > 0) __stcs(row + v, make_uint4(w[0], w[1], w[2], w[3]));
+    }
+};
+template <>
+struct RowOut<false> {
+    unsigned short* row;
+    uint32_t m;          // values between the row's first piece's start and the row: the same in all lanes
+    uint32_t carry[4];   // lane 0: what lane 31 had
+    __device__ __forceinline__ explicit RowOut(unsigned short* at)
+        : row(at), m(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(at) >> 1) & 7u), carry{0u, 0u, 0u, 0u} {}
+    template <bool FIRST, bool LAST>
+    __device__ __forceinline__ void put(uint32_t v, int valid, int next, const uint32_t (&w)[4]) {
         const uint32_t lane = threadIdx.x & 31;
         unsigned short* at = row + 8ull * v;
-        const uint32_t m = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row) >> 1) & 7u;   // the same in all lanes
         const int own = 8 - static_cast<int>(m);   // values up to the boundary
         int from = 0, to = 0;                      // values to be written by themselves
         if (m == 0u) {
@@ -285,22 +312,28 @@ __device__ __forceinline__ void store8(unsigned short* row, uint32_t v, int vali
         } else {
             uint32_t before[4], q[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) before[i] = __shfl_sync(0xFFFFFFFFu, w[i], (lane + 31) & 31);
-            const int next = __shfl_sync(0xFFFFFFFFu, valid, (lane + 1) & 31), last = __shfl_sync(0xFFFFFFFFu, valid, 31);
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t round = __shfl_sync(0xFFFFFFFFu, w[i], (lane + 31) & 31);
+                before[i] = lane == 0 ? carry[i] : round;
+                carry[i] = round;
+            }
             shift_halves(before, w, static_cast<uint32_t>(own), q);
             uint4* piece = reinterpret_cast<uint4*>(at - m);
-            if (lane > 0) {
-                if (valid >= own) *piece = make_uint4(q[0], q[1], q[2], q[3]);
-            } else {
-                if (valid >= own) store_high(piece, q, m);
-                if (last == 8) store_low(piece + 32, q, m);
+            if (valid >= own) {
+                if (FIRST && lane == 0) store_high(piece, q, m);
+                else *piece = make_uint4(q[0], q[1], q[2], q[3]);
             }
             if (valid < own) to = valid;
-            else if (valid > own && (lane == 31 ? valid < 8 : next < own)) from = own, to = valid;
+            else if (valid > own && (LAST && lane == 31 ? valid < 8 : next < own)) from = own, to = valid;
+            if (LAST && __shfl_sync(0xFFFFFFFFu, valid, 31) == 8 && lane == 0) {
+                const uint32_t none[4] = {0u, 0u, 0u, 0u};
+                shift_halves(carry, none, static_cast<uint32_t>(own), q);
+                store_low(piece + 32, q, m);
+            }
         }
         if (from < to) store_some(at, make_uint4(w[0], w[1], w[2], w[3]), from, to);
     }
-}
+};
 template <int DT>
 __device__ __forceinline__ void widen8(const uint32_t (&w)[4], float (&v)[8]) {
 #pragma unroll
