@@ -9,8 +9,8 @@
 //
 //   sort   the tokens by id, stably, by one cluster of 8 CTAs (radix digits
 //          of up to 8 bits; its CTAs see each other's counts through their
-//          shared memory and wait for each other at the cluster's barrier
-//          only).  The launch's other CTAs fill the table with zeros
+//          shared memory, hand each other up to 16384 keys the same way, and
+//          wait for each other at the cluster's barrier only).  The launch's other CTAs fill the table with zeros
 //          meanwhile, which takes longer for tables of real sizes.
 //   sum    a warp takes 256 columns of kPiece consecutive sorted tokens, in
 //          fp32.  A run of one id that lies inside its piece is finished and
@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kThreads) k_embedding(const __grid_constant__ 
 }
 
 // -------------------------------------------------------------------- sort
-constexpr uint32_t kSortCtas = 8, kSortThreads = 1024, kDigits = 256, kMostPer = 4;
+constexpr uint32_t kSortCtas = 8, kSortThreads = 1024, kDigits = 256, kMostPer = 4, kHere = 2048;
 
 struct SortArgs {
     const void* ids;
@@ -102,6 +102,14 @@ __device__ __forceinline__ uint32_t load_of_cta(const uint32_t* shared, uint32_t
     uint32_t x;
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(cluster_addr(smem_u32(shared), cta)) : "memory");
     return x;
+}
+__device__ __forceinline__ void store_to_cta(uint2* shared, uint32_t cta, uint2 x) {
+    asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(cluster_addr(smem_u32(shared), cta)), "r"(x.x), "r"(x.y) : "memory");
+}
+// The cluster's barrier without waiting for this CTA's writes to global memory.
+__device__ __forceinline__ void cluster_leave() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // What other CTAs of the cluster wrote comes from L2, not from this SM's L1.
 __device__ __forceinline__ uint32_t load_l2(const uint32_t* p) {
@@ -163,6 +171,8 @@ __global__ void __launch_bounds__(kSortThreads) k_embedding_sort(const __grid_co
     // a tile's keys of each digit, by warp; then those in the warps before
     unsigned short (*const s_warp)[kDigits] = reinterpret_cast<unsigned short (*)[kDigits]>(s_zeros);
     static_assert(sizeof(s_zeros) == kWarps * kDigits * sizeof(unsigned short) && kDigits * 4 == kSortThreads, "one place");
+    __shared__ uint2 s_next[kHere];         // the next pass's keys and indexes, where the CTAs can hold them
+    __shared__ uint32_t s_part[4][kDigits]; // a quarter of the warps' keys of each digit
     __shared__ uint32_t s_count[kDigits];   // this CTA's keys of each digit
     __shared__ uint32_t s_base[kDigits];    // where the tile's first key of a digit goes
     __shared__ uint32_t s_total[kDigits];   // the tile's keys of each digit
@@ -180,6 +190,8 @@ __global__ void __launch_bounds__(kSortThreads) k_embedding_sort(const __grid_co
         uint32_t *to = a.key[pass & 1], *to_index = a.index[pass & 1];
         auto key_of = [&](uint64_t i) { return pass == 0 ? id_at(a.ids, a.wide_ids, i, a.vocab) : load_l2(from + i); };
         const bool one_tile = share <= tile_keys;   // then the tile's counts are the CTA's
+        const bool here = share <= kHere;           // a place goes to the CTA whose keys it is among in the next pass
+        const bool last = pass + 1 == a.passes;
         if (!one_tile) {
             if (threadIdx.x < kDigits) s_count[threadIdx.x] = 0;
             __syncthreads();
@@ -196,27 +208,33 @@ __global__ void __launch_bounds__(kSortThreads) k_embedding_sort(const __grid_co
             for (uint32_t k = 0; k < kMostPer; ++k) {
                 const uint64_t i = mine + 32 * k;
                 if (k >= per || i >= end) continue;
-                key[k] = key_of(i);
-                index[k] = pass == 0 ? static_cast<uint32_t>(i) : load_l2(from_index + i);
+                if (pass == 0 || !here) {
+                    key[k] = key_of(i);
+                    index[k] = pass == 0 ? static_cast<uint32_t>(i) : load_l2(from_index + i);
+                } else {
+                    const uint2 x = s_next[i - first];
+                    key[k] = x.x;
+                    index[k] = x.y;
+                }
             }
             s_zeros[threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
             __syncthreads();
 #pragma unroll
             for (uint32_t k = 0; k < kMostPer; ++k) {   // the keys of the same digit before this one in the warp
                 if (k >= per) break;
-                const bool here = mine + 32 * k < end;
-                const uint32_t digit = here ? (key[k] >> shift) & (digits - 1) : kDigits;
+                const bool some = mine + 32 * k < end;
+                const uint32_t digit = some ? (key[k] >> shift) & (digits - 1) : kDigits;
                 const uint32_t same = __match_any_sync(0xFFFFFFFFu, digit), ahead = __popc(same & ((1u << lane) - 1));
-                const uint32_t so_far = here ? s_warp[warp][digit] : 0u;
+                const uint32_t so_far = some ? s_warp[warp][digit] : 0u;
                 rank[k] = so_far + ahead;
                 __syncwarp();
-                if (here && ahead == 0) s_warp[warp][digit] = static_cast<unsigned short>(so_far + __popc(same));
+                if (some && ahead == 0) s_warp[warp][digit] = static_cast<unsigned short>(so_far + __popc(same));
                 __syncwarp();
             }
             __syncthreads();
             {   // four threads a digit, 8 warps each
                 constexpr uint32_t kEach = kWarps / 4;
-                const uint32_t digit = threadIdx.x >> 2, part = threadIdx.x & 3;
+                const uint32_t digit = threadIdx.x & (kDigits - 1), part = threadIdx.x / kDigits;
                 uint32_t n[kEach], sum = 0;
 #pragma unroll
                 for (uint32_t q = 0; q < kEach; ++q) n[q] = s_warp[part * kEach + q][digit];
@@ -226,17 +244,14 @@ __global__ void __launch_bounds__(kSortThreads) k_embedding_sort(const __grid_co
                     n[q] = sum;
                     sum += x;
                 }
-                uint32_t before = sum;
-#pragma unroll
-                for (int d = 1; d < 4; d <<= 1) {
-                    const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, before, d);
-                    if (part >= static_cast<uint32_t>(d)) before += x;
-                }
+                s_part[part][digit] = sum;
+                __syncthreads();
+                uint32_t before = 0;
+                for (uint32_t q = 0; q < part; ++q) before += s_part[q][digit];
                 if (part == 3) {
-                    s_total[digit] = before;
-                    if (one_tile) s_count[digit] = before;
+                    s_total[digit] = before + sum;
+                    if (one_tile) s_count[digit] = before + sum;
                 }
-                before -= sum;
 #pragma unroll
                 for (uint32_t q = 0; q < kEach; ++q)
                     s_warp[part * kEach + q][digit] = static_cast<unsigned short>(n[q] + before);
@@ -275,15 +290,21 @@ __global__ void __launch_bounds__(kSortThreads) k_embedding_sort(const __grid_co
                 if (k >= per || mine + 32 * k >= end) continue;
                 const uint32_t digit = (key[k] >> shift) & (digits - 1);
                 const uint32_t at = s_base[digit] + s_warp[warp][digit] + rank[k];
-                to[at] = key[k];
-                to_index[at] = index[k];
+                if (here && !last) {
+                    const uint32_t cta = at / static_cast<uint32_t>(share);
+                    store_to_cta(&s_next[at - cta * static_cast<uint32_t>(share)], cta, make_uint2(key[k], index[k]));
+                } else {
+                    to[at] = key[k];
+                    to_index[at] = index[k];
+                }
             }
             tile += tile_keys;
             if (one_tile || tile >= end) break;
             __syncthreads();
             if (threadIdx.x < kDigits) s_base[threadIdx.x] += s_total[threadIdx.x];
         } while (true);
-        cluster_sync();
+        if (last) cluster_leave();   // the other CTAs have read its counts
+        else cluster_sync();
     }
 }
 
@@ -329,6 +350,7 @@ __device__ __forceinline__ void write_partial(const SumArgs& a, uint64_t piece, 
 template <int DT, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads, 3) k_embedding_sum(const __grid_constant__ SumArgs a) {
     pdl_enter();
+    __shared__ uint4 s_rows[kThreads / 32][kPiece * 32];
     const uint64_t item = static_cast<uint64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
     const uint64_t piece = item / a.segments;
     if (piece >= a.pieces) return;
@@ -345,39 +367,45 @@ __global__ void __launch_bounds__(kThreads, 3) k_embedding_sum(const __grid_cons
     const uint32_t before = __shfl_sync(0xFFFFFFFFu, key, 30), after = __shfl_sync(0xFFFFFFFFu, key, 31);
     const uint32_t count = __popc(__ballot_sync(0xFFFFFFFFu, lane < kPiece && key != none));
     if (count == 0) return;
+    // all rows in flight together; then one after the other in a loop, through
+    // shared memory, of which every lane reads what it wrote: a short loop's
+    // instructions are there sooner than those of eight copies
+    uint4* rows = s_rows[threadIdx.x >> 5] + lane;
+    {
+        RowIn<ALIGNED> in[kPiece];
+        Fetched<ALIGNED> f[kPiece];
+#pragma unroll
+        for (uint32_t i = 0; i < kPiece; ++i) {
+            in[i] = row_in<ALIGNED>(a.grad, __shfl_sync(0xFFFFFFFFu, index, i), a.ld_grad, a.tokens, a.dim);
+            fetch8(in[i], v, i < count ? valid : 0, f[i]);
+        }
+#pragma unroll
+        for (uint32_t i = 0; i < kPiece; ++i) {
+            uint32_t w[4];
+            finish8(in[i], v, i < count ? valid : 0, f[i], w);
+            rows[32 * i] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
     float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
     uint32_t id = __shfl_sync(0xFFFFFFFFu, key, 0);
     bool enters = first > 0 && id == before;   // the run began in an earlier piece
-    constexpr uint32_t kLoads = 8;   // in flight
-    Fetched<ALIGNED> f[kLoads];
-    auto row_of = [&](uint32_t i) {
-        return row_in<ALIGNED>(a.grad, __shfl_sync(0xFFFFFFFFu, index, i), a.ld_grad, a.tokens, a.dim);
-    };
+#pragma unroll 1
+    for (uint32_t i = 0; i < count; ++i) {
+        const uint4 x = rows[32 * i];
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        float y[8];
+        widen8<DT>(w, y);
+        add8(s, y);
+        const uint32_t next = i + 1 < count ? __shfl_sync(0xFFFFFFFFu, key, i + 1) : count == kPiece ? after : none;
+        if (next == id && i + 1 < count) continue;
+        // the run is complete here, or leaves the piece
+        if (enters || next == id) write_partial(a, piece, enters ? 0 : 1, c, valid, s);
+        else write_sum<DT, ALIGNED>(a, id, v, valid, s);
+        id = next;
+        enters = false;
 #pragma unroll
-    for (uint32_t i = 0; i < kPiece; ++i) {
-        if (i % kLoads == 0) {
-#pragma unroll
-            for (uint32_t k = 0; k < kLoads; ++k) fetch8(row_of(i + k), v, i + k < count ? valid : 0, f[k]);
-        }
-        const uint32_t next = __shfl_sync(0xFFFFFFFFu, key, i);
-        const RowIn<ALIGNED> in = row_of(i);
-        if (i >= count) break;
-        uint32_t w[4];
-        finish8(in, v, valid, f[i % kLoads], w);
-        if (next != id) {   // the run is complete here
-            if (enters) write_partial(a, piece, 0, c, valid, s);
-            else write_sum<DT, ALIGNED>(a, id, v, valid, s);
-            id = next;
-            enters = false;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) s[e] = 0.0f;
-        }
-        float x[8];
-        widen8<DT>(w, x);
-        add8(s, x);
+        for (int e = 0; e < 8; ++e) s[e] = 0.0f;
     }
-    if (enters || (count == kPiece && id == after)) write_partial(a, piece, enters ? 0 : 1, c, valid, s);
-    else write_sum<DT, ALIGNED>(a, id, v, valid, s);
 }
 
 // A block looks at kJoinPieces pieces, a warp each, for a run that begins in
