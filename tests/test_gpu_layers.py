@@ -120,6 +120,66 @@ def test_dropout_past_32_bits():
     assert torch.equal(got.cpu() != 0, kept(rows, cols, 0.5, 9, 0)[0])
 
 
+# --------------------------------------------------- rows at any alignment
+WIDTHS = list(range(1, 42)) + [63, 64, 65, 121, 127, 128, 129] + list(range(247, 266)) + [300, 503, 511, 512, 513, 520, 777, 1017, 1025]
+
+
+@pytest.mark.parametrize("offset", range(8))
+def test_rows_of_every_alignment_and_width(offset):
+    """Copies through every way of reading and writing a row: its first and last pieces, the ends of warps, and
+    nothing beside it."""
+    spec = Z.dropout_spec(0.0, 1)
+    for cols in WIDTHS:
+        gap = (cols * 5 + offset) % 8                   # rows of one matrix at several alignments
+        x = torch.randint(-2 ** 15, 2 ** 15, (5, cols), generator=gen(cols), dtype=torch.int16)
+        x = torch.where((x & 0x7C00) == 0x7C00, x & 0x3FFF, x).view(torch.float16)       # any number
+        src, src_room = strided(x, offset, gap)
+        dst, room = strided(torch.zeros_like(x), (3 * offset + 1) % 8, gap)
+        L.dropout(src, spec, out=dst)
+        assert torch.equal(dst.cpu().view(torch.int16), x.view(torch.int16)) and untouched(dst, room), cols
+        ids = torch.tensor([4, 0, 3, -1, 1], device="cuda")
+        L.embedding(ids, src, out=dst)
+        want = x[ids.cpu().clamp(min=0)].clone()
+        want[3] = 0
+        assert torch.equal(dst.cpu().view(torch.int16), want.view(torch.int16)) and untouched(dst, room), cols
+        back = torch.tensor([2, 0, 4, 1, 3], device="cuda")       # each row from one token
+        L.embedding_backward(src, back, dst)
+        assert torch.equal(dst[back].cpu(), x) and untouched(dst, room), cols
+        assert untouched(src, src_room)
+
+
+@pytest.mark.parametrize("rows", [3, 310, 1220])
+def test_norm_rows_of_every_alignment_and_width(rows):
+    # (threads have one, two and four groups of a row)
+    w = torch.ones(2100, dtype=torch.float16, device="cuda")
+    for k, cols in enumerate(WIDTHS + [1400, 2049]):
+        offset, gap = k % 8, (k * 3) % 8
+        x = torch.randint(-9, 10, (rows, cols), generator=gen(cols)).half()
+        src, _ = strided(x, offset, gap)
+        h, h_room = strided(torch.zeros_like(x), (offset * 5 + 2) % 8, gap)
+        y, y_room = strided(torch.zeros_like(x), (offset + 3) % 8, gap)
+        Z.zero_rms_norm(0, rows, cols, src, w, 1e-5, src, h, y, ld_x=cols + gap, ld_residual=cols + gap, ld_h=cols + gap,
+                        ld_out=cols + gap)
+        assert torch.equal(h.cpu(), 2 * x), cols
+        want, _ = norm64(2 * x, w[:cols].cpu(), 1e-5)
+        assert within(y, want, half_step(want, torch.float16) + NORM * want.abs()), cols
+        assert untouched(h, h_room) and untouched(y, y_room), cols
+        if rows > 400:
+            continue
+        dy = torch.randint(-3, 4, (rows, cols), generator=gen(cols + 1)).half()
+        g, _ = strided(dy, (offset + 6) % 8, gap)
+        dh, dh_room = strided(torch.zeros_like(x), (offset * 3 + 1) % 8, gap)
+        dw = torch.full((cols + 16,), 5.0, dtype=torch.float16, device="cuda")
+        room = torch.empty(Z.zero_rms_norm_backward_workspace_bytes(rows, cols), dtype=torch.uint8, device="cuda")
+        ld = cols + gap
+        Z.zero_rms_norm_backward(0, rows, cols, g, src, w, 1e-5, dh, room, dweight16=dw[8:], ld_dy=ld, ld_h=ld, ld_dh=ld)
+        want, want_w, size, w_size = norm_grad64(dy, x, w[:cols].cpu(), 1e-5)
+        assert within(dh, want, half_step(want, torch.float16) + GRAD * size), cols
+        adds = rows / 100 + 8 + 10 + 32 + 36
+        assert within(dw[8:8 + cols], want_w, half_step(want_w, torch.float16) + adds * U * w_size), cols
+        assert untouched(dh, dh_room) and bool((dw[:8] == 5).all()) and bool((dw[8 + cols:] == 5).all()), cols
+
+
 # -------------------------------------------------------------------- norm
 SIZES = [(1, 1), (1, 8), (2, 31), (3, 256), (9, 257), (5, 768), (131, 100), (4, 1003), (3, 1024), (2, 1025), (3, 4096),
          (2, 8200), (2, 16384), (257, 40)]

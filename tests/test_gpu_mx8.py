@@ -269,6 +269,21 @@ def test_many_passes_in_a_row():
     assert all(torch.equal(o, want) for o in outs) and all(torch.equal(o, want_few) for o in outs_few)
 
 
+def test_matrices_of_an_optimizer_s_replicas():
+    from zero_partitioned_mixed_gb300.muon import MuonBuffers
+    buf = MuonBuffers([(40, 70), (33, 128)], 2, "bf16")
+    x = matrix(33, 128, "bf16", 1)
+    buf.matrix(1, buf.params[1]).copy_(x)
+    for transpose in (False, True):
+        q = buf.quantize(1, transpose, rank=1, bits=8)
+        assert isinstance(q, Mx8Matrix)
+        check_encoding(q, x.t().contiguous() if transpose else x)
+        assert torch.equal(buf.quantize(1, transpose, 1).codes, Mx4Matrix.of(x.cuda(), transpose).codes)
+    with pytest.raises(Z.ZeroError) as e:
+        buf.quantize(0, bits=16)
+    assert e.value.code == 1 and "bits" in str(e.value)
+
+
 def test_refusals():
     z = torch.zeros(4096, dtype=torch.uint8, device="cuda")
     h = torch.zeros(4096, dtype=torch.bfloat16, device="cuda")

@@ -88,20 +88,19 @@ __global__ void __launch_bounds__(kThreads) k_dropout(const __grid_constant__ Dr
     pdl_enter();
     const uint64_t stream = drop_stream(a.drop), first = static_cast<uint64_t>(blockIdx.x) * kDropVecs * kThreads + threadIdx.x;
     const uint4* src = reinterpret_cast<const uint4*>(a.src);
-    uint4 x[kDropVecs];
+    Fetched<true> f[kDropVecs];
 #pragma unroll
     for (int i = 0; i < kDropVecs; ++i) {
         const uint64_t g = first + static_cast<uint64_t>(i) * kThreads;
-        if (g < a.across) x[i] = __ldcs(src + g);
+        fetch8(RowIn<true>{src + g}, 0, g < a.across ? 8 : 0, f[i]);
     }
 #pragma unroll
     for (int i = 0; i < kDropVecs; ++i) {
         const uint64_t g = first + static_cast<uint64_t>(i) * kThreads;
-        if (g >= a.across) continue;
-        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        const uint32_t w[4] = {f[i].x.x, f[i].x.y, f[i].x.z, f[i].x.w};
         uint32_t q[4];
         drop_one<DT>(a, g, stream, w, q);
-        __stcs(reinterpret_cast<uint4*>(a.dst) + g, make_uint4(q[0], q[1], q[2], q[3]));
+        if (g < a.across) __stcs(reinterpret_cast<uint4*>(a.dst) + g, make_uint4(q[0], q[1], q[2], q[3]));
     }
 }
 
