@@ -689,7 +689,9 @@ typedef struct {
 } zero_dropout_t;
 
 /* out16 = dropout(src16), rows x cols; dropout NULL copies.  out16 may be
- * src16 when the leading dimensions agree; they may not overlap otherwise. */
+ * src16 when the leading dimensions agree; they may not overlap otherwise.
+ * rows <= 2^30; cols <= 2^34, or 2^40 values in all without gaps, aligned and
+ * in whole eights. */
 ZERO_API int zero_dropout(int dtype, uint64_t rows, uint64_t cols, const void* src16, uint64_t ld_src, void* out16,
                           uint64_t ld_out, const zero_dropout_t* dropout, void* stream);
 
@@ -755,7 +757,7 @@ ZERO_API int zero_embedding(int dtype, uint64_t vocab, uint64_t dim, const void*
  * it); with accumulate != 0 what the rows held is added before the rounding
  * (rows that no token names keep their values), as a table that is also the
  * output layer's weight needs.  Sums are fp32, in the order of the tokens;
- * padding adds nothing.
+ * padding adds nothing.  Nothing may overlap.
  *   workspace   256-byte aligned, at least
  *               zero_embedding_backward_workspace_bytes(vocab, dim, tokens) bytes
  * tokens = 0 gives zeros.

@@ -540,7 +540,8 @@ def _id_bytes(ids) -> int:
     """4 or 8; 0, which the calls refuse, for a tensor of anything but int32 or int64."""
     if ids is None or isinstance(ids, int):   # an address: 64-bit ids
         return 8
-    return {"torch.int32": 4, "torch.int64": 8}.get(str(ids.dtype), 0)
+    import torch
+    return 8 if ids.dtype is torch.int64 else 4 if ids.dtype is torch.int32 else 0
 
 
 def zero_embedding_backward_workspace_bytes(vocab: int, dim: int, tokens: int) -> int:

@@ -663,6 +663,7 @@ int zero_dropout(int dtype, uint64_t rows, uint64_t cols, const void* src16, uin
     if (a.across > (1ull << 40) / rows) return refuse(ZERO_EINVAL, "rows and cols are too large together");
     a.items = rows * a.segments;
     const bool one = whole && rows == 1, fp16 = dtype == ZERO_FP16;
+    if (!one && cols > (1ull << 34)) return refuse(ZERO_EINVAL, "rows of more than 2^34 values must be aligned and without gaps");
     const uint64_t per = one ? kDropVecs * kThreads : kThreads / 32;
     const uint64_t blocks = ((one ? a.across : a.items) + per - 1) / per;
     if (blocks > 0x7FFFFFFFull) return refuse(ZERO_EINVAL, "rows and cols are too large together");

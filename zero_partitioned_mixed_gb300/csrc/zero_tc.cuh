@@ -258,7 +258,7 @@ __device__ __forceinline__ void count_done(uint32_t* counter) {
 // tensor memory while it waits for another block, unless nothing that also
 // allocates can be on its SM.  With two clusters of different kernels on the
 // same two SMs, each could hold one and wait for the other, for ever.
-// k_mx4_narrow frees before it waits for its cluster; the clusters of
+// k_mx_narrow frees before it waits for its cluster; the clusters of
 // zero_ortho.cu ask for kAloneSmem of shared memory or more, which leaves no
 // room on an SM for a block with kLeastTmemSmem, the least that a kernel here
 // with tensor memory asks for.

@@ -10,13 +10,12 @@ tensors' device, where the tensors it makes belong.
 
 from __future__ import annotations
 
-import contextlib
 from typing import NamedTuple, Optional, Tuple
 
 import torch
 
 from . import _binding as B
-from .mx4 import Mx4Matrix, MxMatrix, _dtype, _rows, _same_gpu
+from .mx4 import Mx4Matrix, MxMatrix, _at, _dtype, _rows, _same_gpu
 from .mx8 import Mx8Matrix
 
 
@@ -31,11 +30,6 @@ def _plain(name: str, *tensors: Optional[torch.Tensor]) -> None:
     if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
         raise B.ZeroError(1, f"{name} records no autograd graph: pass detached tensors (or call it under torch.no_grad()) "
                              f"and take the gradients from the backward call")
-
-
-def _at(t: torch.Tensor):
-    """The tensor's device as the current one, for the call and for its stream."""
-    return contextlib.nullcontext() if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
 
 
 def _matrix(t: torch.Tensor) -> torch.Tensor:

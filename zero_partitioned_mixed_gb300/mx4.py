@@ -3,11 +3,13 @@
 A rank that holds its parameters in 4 bits multiplies with the codes as they
 are; the three products of a layer's training step are one call on
 operands quantised along the dimension that is summed over.  Everything here
-runs on torch's current stream, where the tensors it makes belong.
+runs on torch's current stream of the tensors' device, where the tensors it
+makes belong.
 """
 
 from __future__ import annotations
 
+import contextlib
 from typing import Optional, Tuple
 
 import torch
@@ -27,6 +29,11 @@ def _same_gpu(*tensors: torch.Tensor) -> None:
     for t in tensors:
         if not t.is_cuda or t.device != tensors[0].device:
             raise B.ZeroError(1, f"expected tensors on one GPU, got {[str(x.device) for x in tensors]}")
+
+
+def _at(t: torch.Tensor):
+    """The tensor's device as the current one, for a call and for its stream."""
+    return contextlib.nullcontext() if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
 
 
 def _rows(t: torch.Tensor) -> int:
@@ -59,13 +66,15 @@ class MxMatrix:
         if ((c, r) if transpose else (r, c)) != (self.rows, self.cols):
             raise B.ZeroError(1, f"expected a matrix for {self.rows} x {self.cols}, got {tuple(src.shape)}")
         _same_gpu(src, self.codes, self.scales)
-        self._quantize(_dtype(src), r, c, src, self.codes, self.scales, ld=_rows(src), transpose=transpose)
+        with _at(src):
+            self._quantize(_dtype(src), r, c, src, self.codes, self.scales, ld=_rows(src), transpose=transpose)
         return self
 
     def values(self, dtype=torch.bfloat16) -> torch.Tensor:
         _same_gpu(self.codes, self.scales)
         out = torch.empty((self.rows, self.cols), dtype=dtype, device=self.codes.device)
-        self._dequantize(_dtype(out), self.rows, self.cols, self.codes, self.scales, out)
+        with _at(out):
+            self._dequantize(_dtype(out), self.rows, self.cols, self.codes, self.scales, out)
         return out
 
     @classmethod
@@ -81,7 +90,8 @@ class MxMatrix:
         elif tuple(out.shape) != (a.rows, b.rows):
             raise B.ZeroError(1, f"out must be {a.rows} x {b.rows}")
         _same_gpu(out, a.codes, a.scales, b.codes, b.scales)
-        cls._matmul(_dtype(out), a.rows, b.rows, a.cols, a.codes, a.scales, b.codes, b.scales, out, ld=_rows(out))
+        with _at(out):
+            cls._matmul(_dtype(out), a.rows, b.rows, a.cols, a.codes, a.scales, b.codes, b.scales, out, ld=_rows(out))
         return out
 
 

@@ -2,8 +2,8 @@
 
 The same calls as mx4.py's, for layers that 4 bits are too coarse for.  The
 norm of layers.py writes its result in these codes, so that the product after
-it reads them as they are.  Everything here runs on torch's current stream,
-where the tensors it makes belong.
+it reads them as they are.  Everything here runs on torch's current stream of
+the tensors' device, where the tensors it makes belong.
 """
 
 from __future__ import annotations
