@@ -58,29 +58,24 @@ __global__ void __launch_bounds__(kThreads) k_embedding(const __grid_constant__ 
     const uint64_t item = static_cast<uint64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
     const uint64_t quad = item / a.segments, t0 = quad * kEmbedTokens;
     if (t0 >= a.tokens) return;
-    const uint32_t v = static_cast<uint32_t>(item - quad * a.segments) * 32 + (threadIdx.x & 31);
-    const int left = values_left(a.dim, 8ull * v);
-    RowIn<ALIGNED> in[kEmbedTokens];
-    int valid[kEmbedTokens];
-    Fetched<ALIGNED> f[kEmbedTokens];
+    const uint64_t c = (item - quad * a.segments) * 256;
+    const int left = columns_left(a.dim, c);
+    Loaded<ALIGNED> f[kEmbedTokens];
+    uint32_t id[kEmbedTokens];
+#pragma unroll
+    for (int i = 0; i < kEmbedTokens; ++i) id[i] = t0 + i < a.tokens ? id_at(a.ids, a.wide_ids, t0 + i, a.vocab) : 0xFFFFFFFFu;
+#pragma unroll
+    for (int i = 0; i < kEmbedTokens; ++i)
+        load_eight(a.table + (id[i] < a.vocab ? id[i] * a.ld_table + c : 0u), id[i] < a.vocab ? left : 0, f[i]);
 #pragma unroll
     for (int i = 0; i < kEmbedTokens; ++i) {
-        const uint32_t id = t0 + i < a.tokens ? id_at(a.ids, a.wide_ids, t0 + i, a.vocab) : 0xFFFFFFFFu;
-        valid[i] = id < a.vocab ? left : 0;
-        in[i] = row_in<ALIGNED>(a.table, id < a.vocab ? id : 0u, a.ld_table, a.vocab, a.dim);
-    }
-#pragma unroll
-    for (int i = 0; i < kEmbedTokens; ++i) fetch8(in[i], v, valid[i], f[i]);
-#pragma unroll
-    for (int i = 0; i < kEmbedTokens; ++i) {
-        if (t0 + i >= a.tokens) continue;
-        uint32_t w[4], q[4];
-        finish8(in[i], v, valid[i], f[i], w);
+        if (t0 + i >= a.tokens) break;
         float x[8];
-        widen8<DT>(w, x);
+        widen_eight<DT>(f[i], x);
         mul8(x, a.scale);
+        uint32_t q[4];
         narrow8<DT>(x, q);
-        RowOut<ALIGNED>(a.out + (t0 + i) * a.ld_out).template put<true, true>(v, left, values_left(a.dim, 8ull * (v + 1)), q);
+        store_eight<ALIGNED>(a.out + (t0 + i) * a.ld_out + c, left, q);
     }
 }
 
@@ -321,43 +316,78 @@ struct SumArgs {
 };
 constexpr uint32_t kPiece = 8;
 
-// By all lanes of a warp: a sum, times the factor, into its row of the table.
+// A warp's 256 columns from c on, `left` of them inside the row: a sum, times
+// the factor, into its row of the table.
 template <int DT, bool ALIGNED>
-__device__ __forceinline__ void write_sum(const SumArgs& a, uint32_t id, uint32_t v, int valid, float (&s)[8]) {
+__device__ __forceinline__ void write_sum(const SumArgs& a, uint32_t id, uint64_t c, int left, float (&s)[8]) {
+    unsigned short* at = a.table + id * a.ld_table + c;
     mul8(s, a.scale);
-    uint32_t w[4];
     if (a.add) {
-        read8<ALIGNED>(row_in<ALIGNED>(a.table, id, a.ld_table, a.vocab, a.dim), v, valid, w);
+        Loaded<ALIGNED> r;
+        load_eight(at, left, r);
         float x[8];
-        widen8<DT>(w, x);
+        widen_eight<DT>(r, x);
         add8(s, x);
     }
-    narrow8<DT>(s, w);
-    RowOut<ALIGNED>(a.table + id * a.ld_table).template put<true, true>(v, valid, values_left(a.dim, 8ull * (v + 1)), w);
+    uint32_t q[4];
+    narrow8<DT>(s, q);
+    store_eight<ALIGNED>(at, left, q);
 }
 __device__ __forceinline__ float* partial_at(const SumArgs& a, uint64_t piece, int leaves, uint64_t c) {
     return a.partial + (2 * piece + leaves) * a.width + c;
 }
-
-__device__ __forceinline__ void write_partial(const SumArgs& a, uint64_t piece, int leaves, uint64_t c, int valid,
-                                              const float (&s)[8]) {
-    if (valid <= 0) return;
-    float4* to = reinterpret_cast<float4*>(partial_at(a, piece, leaves, c));
-    to[0] = make_float4(s[0], s[1], s[2], s[3]);
-    to[1] = make_float4(s[4], s[5], s[6], s[7]);
+// A warp's 256 values in shared memory.
+__device__ __forceinline__ void put_shared(uint4* at, const Loaded<true>& r) { at[threadIdx.x & 31] = r.x; }
+__device__ __forceinline__ void get_shared(const uint4* at, Loaded<true>& r) { r.x = at[threadIdx.x & 31]; }
+__device__ __forceinline__ void put_shared(uint4* at, const Loaded<false>& r) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) reinterpret_cast<unsigned short*>(at)[column_of<false>(e)] = r.x[e];
+}
+__device__ __forceinline__ void get_shared(const uint4* at, Loaded<false>& r) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) r.x[e] = reinterpret_cast<const unsigned short*>(at)[column_of<false>(e)];
+}
+template <bool ALIGNED>
+__device__ __forceinline__ void write_partial(float* at, int left, const float (&s)[8]) {
+    if constexpr (ALIGNED) {
+        if (static_cast<int>(column_of<true>(0)) >= left) return;
+        float4* to = reinterpret_cast<float4*>(at + column_of<true>(0));
+        to[0] = make_float4(s[0], s[1], s[2], s[3]);
+        to[1] = make_float4(s[4], s[5], s[6], s[7]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (static_cast<int>(column_of<false>(e)) < left) at[column_of<false>(e)] = s[e];
+    }
+}
+template <bool ALIGNED>
+__device__ __forceinline__ void add_partial(const float* at, int left, float (&s)[8]) {
+    float x[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    if constexpr (ALIGNED) {
+        if (static_cast<int>(column_of<true>(0)) < left) {
+            const float4* from = reinterpret_cast<const float4*>(at + column_of<true>(0));
+            const float4 y = from[0], z = from[1];
+            x[0] = y.x; x[1] = y.y; x[2] = y.z; x[3] = y.w;
+            x[4] = z.x; x[5] = z.y; x[6] = z.z; x[7] = z.w;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (static_cast<int>(column_of<false>(e)) < left) x[e] = at[column_of<false>(e)];
+    }
+    add8(s, x);
 }
 
 template <int DT, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads, 3) k_embedding_sum(const __grid_constant__ SumArgs a) {
     pdl_enter();
-    __shared__ uint4 s_rows[kThreads / 32][kPiece * 32];
+    __shared__ uint4 s_rows[kThreads / 32][kPiece][32];   // 256 values each
     const uint64_t item = static_cast<uint64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
     const uint64_t piece = item / a.segments;
     if (piece >= a.pieces) return;
     const uint32_t lane = threadIdx.x & 31;
-    const uint32_t v = static_cast<uint32_t>(item - piece * a.segments) * 32 + lane;
-    const uint64_t c = 8ull * v, first = piece * kPiece;
-    const int valid = values_left(a.dim, c);
+    const uint64_t c = (item - piece * a.segments) * 256, first = piece * kPiece;
+    const int left = columns_left(a.dim, c);
     const uint32_t none = static_cast<uint32_t>(a.vocab);   // padding, sorted behind all ids
     // lane i: the piece's token i; lanes 30 and 31 the neighbours' ids
     const uint64_t mine = lane == 30 ? first - 1 : lane == 31 ? first + kPiece : first + lane;
@@ -370,37 +400,30 @@ __global__ void __launch_bounds__(kThreads, 3) k_embedding_sum(const __grid_cons
     // all rows in flight together; then one after the other in a loop, through
     // shared memory, of which every lane reads what it wrote: a short loop's
     // instructions are there sooner than those of eight copies
-    uint4* rows = s_rows[threadIdx.x >> 5] + lane;
+    uint4 (*const rows)[32] = s_rows[threadIdx.x >> 5];
     {
-        RowIn<ALIGNED> in[kPiece];
-        Fetched<ALIGNED> f[kPiece];
+        Loaded<ALIGNED> f[kPiece];
 #pragma unroll
-        for (uint32_t i = 0; i < kPiece; ++i) {
-            in[i] = row_in<ALIGNED>(a.grad, __shfl_sync(0xFFFFFFFFu, index, i), a.ld_grad, a.tokens, a.dim);
-            fetch8(in[i], v, i < count ? valid : 0, f[i]);
-        }
+        for (uint32_t i = 0; i < kPiece; ++i)
+            load_eight(a.grad + __shfl_sync(0xFFFFFFFFu, index, i) * a.ld_grad + c, i < count ? left : 0, f[i]);
 #pragma unroll
-        for (uint32_t i = 0; i < kPiece; ++i) {
-            uint32_t w[4];
-            finish8(in[i], v, i < count ? valid : 0, f[i], w);
-            rows[32 * i] = make_uint4(w[0], w[1], w[2], w[3]);
-        }
+        for (uint32_t i = 0; i < kPiece; ++i) put_shared(rows[i], f[i]);
     }
     float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
     uint32_t id = __shfl_sync(0xFFFFFFFFu, key, 0);
     bool enters = first > 0 && id == before;   // the run began in an earlier piece
 #pragma unroll 1
     for (uint32_t i = 0; i < count; ++i) {
-        const uint4 x = rows[32 * i];
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
         float y[8];
-        widen8<DT>(w, y);
+        Loaded<ALIGNED> x;
+        get_shared(rows[i], x);
+        widen_eight<DT>(x, y);
         add8(s, y);
         const uint32_t next = i + 1 < count ? __shfl_sync(0xFFFFFFFFu, key, i + 1) : count == kPiece ? after : none;
         if (next == id && i + 1 < count) continue;
         // the run is complete here, or leaves the piece
-        if (enters || next == id) write_partial(a, piece, enters ? 0 : 1, c, valid, s);
-        else write_sum<DT, ALIGNED>(a, id, v, valid, s);
+        if (enters || next == id) write_partial<ALIGNED>(partial_at(a, piece, enters ? 0 : 1, c), left, s);
+        else write_sum<DT, ALIGNED>(a, id, c, left, s);
         id = next;
         enters = false;
 #pragma unroll
@@ -423,15 +446,9 @@ __global__ void __launch_bounds__(kThreads) k_embedding_join(const __grid_consta
     __shared__ __align__(16) float s_sum[kJoinPieces][256];
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint64_t group = blockIdx.x / a.segments, piece = group * kJoinPieces + warp;
-    const uint32_t v = static_cast<uint32_t>(blockIdx.x - group * a.segments) * 32 + lane;
-    const uint64_t c = 8ull * v;
-    const int valid = values_left(a.dim, c);
-    auto add = [&](float (&s)[8], uint64_t p, int leaves) {
-        const float4* at = reinterpret_cast<const float4*>(partial_at(a, p, leaves, c));
-        const float4 x = at[0], y = at[1];
-        const float z[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-        add8(s, z);
-    };
+    const uint64_t c = (blockIdx.x - group * a.segments) * 256;
+    const int left = columns_left(a.dim, c);
+    auto add = [&](float (&s)[8], uint64_t p, int leaves) { add_partial<ALIGNED>(partial_at(a, p, leaves, c), left, s); };
     uint32_t id = 0, run = 0;   // the pieces after this one that the run enters
     const uint64_t first = piece * kPiece;
     if (piece + 1 < a.pieces) {
@@ -464,13 +481,11 @@ __global__ void __launch_bounds__(kThreads) k_embedding_join(const __grid_consta
         s_run[warp] = run > kShortRun ? run : 0;
     }
     if (run > 0 && run <= kShortRun) {
-        if (valid > 0) {
-            add(s, piece, 1);
+        add(s, piece, 1);
 #pragma unroll
-            for (uint32_t i = 0; i < kShortRun; ++i)
-                if (i < run) add(s, piece + 1 + i, 0);
-        }
-        write_sum<DT, ALIGNED>(a, id, v, valid, s);
+        for (uint32_t i = 0; i < kShortRun; ++i)
+            if (i < run) add(s, piece + 1 + i, 0);
+        write_sum<DT, ALIGNED>(a, id, c, left, s);
     }
     __syncthreads();
     for (uint32_t k = 0; k < kJoinPieces; ++k) {
@@ -479,24 +494,21 @@ __global__ void __launch_bounds__(kThreads) k_embedding_join(const __grid_consta
         const uint64_t from = group * kJoinPieces + k;
 #pragma unroll
         for (int e = 0; e < 8; ++e) s[e] = 0.0f;
-        if (valid > 0) {
-            if (warp == 0) add(s, from, 1);
+        if (warp == 0) add(s, from, 1);
 #pragma unroll 8
-            for (uint32_t i = warp; i < pieces; i += kJoinPieces) add(s, from + 1 + i, 0);
-        }
-        float4* mine = reinterpret_cast<float4*>(&s_sum[warp][8 * lane]);
-        mine[0] = make_float4(s[0], s[1], s[2], s[3]);
-        mine[1] = make_float4(s[4], s[5], s[6], s[7]);
+        for (uint32_t i = warp; i < pieces; i += kJoinPieces) add(s, from + 1 + i, 0);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s_sum[warp][32 * e + lane] = s[e];
         __syncthreads();
         if (warp == 0) {
 #pragma unroll
             for (uint32_t w = 1; w < kJoinPieces; ++w) {
                 float x[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = s_sum[w][8 * lane + e];
+                for (int e = 0; e < 8; ++e) x[e] = s_sum[w][32 * e + lane];
                 add8(s, x);
             }
-            write_sum<DT, ALIGNED>(a, s_id[k], v, valid, s);
+            write_sum<DT, ALIGNED>(a, s_id[k], c, left, s);
         }
         __syncthreads();
     }

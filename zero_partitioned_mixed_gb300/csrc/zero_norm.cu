@@ -33,31 +33,20 @@
 namespace zg {
 namespace {
 
-// 8 weights: every row reads them again, from the caches.
-template <bool ALIGNED>
-__device__ __forceinline__ void read_weight(const RowIn<ALIGNED>& r, uint32_t v, int valid, uint32_t (&w)[4]) {
+// The weights of 256 columns: every row reads them again, from the caches.
+template <int DT, bool ALIGNED>
+__device__ __forceinline__ void read_weight(const unsigned short* at, int left, float (&f)[8]) {
     if constexpr (ALIGNED) {
-        const uint4 x = valid > 0 ? r.first[v] : make_uint4(0u, 0u, 0u, 0u);
-        w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+        Loaded<true> r{make_uint4(0u, 0u, 0u, 0u)};
+        if (static_cast<int>(column_of<true>(0)) < left) r.x = reinterpret_cast<const uint4*>(at)[threadIdx.x & 31];
+        widen_eight<DT>(r, f);
     } else {
-        read8<false>(r, v, valid, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint32_t c = column_of<false>(e);
+            f[e] = static_cast<int>(c) < left ? widen<DT>(at[c]) : 0.0f;
+        }
     }
-}
-// How many of a thread's 8 columns from group v on lie inside the row.
-template <bool ALIGNED>
-__device__ __forceinline__ int inside(uint32_t v, uint32_t cols) {
-    const int left = static_cast<int>(cols) - static_cast<int>(8 * v);
-    return ALIGNED ? (left > 0 ? 8 : 0) : left > 8 ? 8 : left;
-}
-
-// f(0), f(1), ... f(N - 1), the number known to the compiler.
-template <int N, typename F, int... I>
-__device__ __forceinline__ void each(F&& f, std::integer_sequence<int, I...>) {
-    (f(std::integral_constant<int, I>{}), ...);
-}
-template <int N, typename F>
-__device__ __forceinline__ void each(F&& f) {
-    each<N>(f, std::make_integer_sequence<int, N>{});
 }
 
 // ----------------------------------------------------------------- dropout
@@ -71,15 +60,6 @@ struct DropoutArgs {
 };
 constexpr int kDropVecs = 4;
 
-template <int DT>
-__device__ __forceinline__ void drop_one(const DropoutArgs& a, uint64_t group, uint64_t stream, const uint32_t (&w)[4],
-                                         uint32_t (&q)[4]) {
-    float x[8];
-    widen8<DT>(w, x);
-    if (a.drop.below) drop8(a.drop, group, stream, x);
-    narrow8<DT>(x, q);
-}
-
 // Rows without gaps, of whole eights: a group's number is its place.  A thread
 // takes kDropVecs groups, their loads in flight together.  HBM and the
 // generator's products about even: 8192 x 4096 bf16 in 21 us (6.4 TB/s).
@@ -88,18 +68,21 @@ __global__ void __launch_bounds__(kThreads) k_dropout(const __grid_constant__ Dr
     pdl_enter();
     const uint64_t stream = drop_stream(a.drop), first = static_cast<uint64_t>(blockIdx.x) * kDropVecs * kThreads + threadIdx.x;
     const uint4* src = reinterpret_cast<const uint4*>(a.src);
-    Fetched<true> f[kDropVecs];
+    Loaded<true> f[kDropVecs];
 #pragma unroll
     for (int i = 0; i < kDropVecs; ++i) {
         const uint64_t g = first + static_cast<uint64_t>(i) * kThreads;
-        fetch8(RowIn<true>{src + g}, 0, g < a.across ? 8 : 0, f[i]);
+        f[i].x = make_uint4(0u, 0u, 0u, 0u);
+        if (g < a.across) f[i].x = __ldcs(src + g);
     }
 #pragma unroll
     for (int i = 0; i < kDropVecs; ++i) {
         const uint64_t g = first + static_cast<uint64_t>(i) * kThreads;
-        const uint32_t w[4] = {f[i].x.x, f[i].x.y, f[i].x.z, f[i].x.w};
+        float x[8];
+        widen_eight<DT>(f[i], x);
+        if (a.drop.below) drop_eight<true>(a.drop, g, stream, x);
         uint32_t q[4];
-        drop_one<DT>(a, g, stream, w, q);
+        narrow8<DT>(x, q);
         if (g < a.across) __stcs(reinterpret_cast<uint4*>(a.dst) + g, make_uint4(q[0], q[1], q[2], q[3]));
     }
 }
@@ -111,23 +94,24 @@ __global__ void __launch_bounds__(kThreads) k_dropout_rows(const __grid_constant
     const uint64_t stream = drop_stream(a.drop);
     const uint64_t item = static_cast<uint64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
     if (item >= a.items) return;
-    const uint64_t row = item / a.segments;
-    const uint32_t v0 = static_cast<uint32_t>(item - row * a.segments) * (kDropVecs * 32) + (threadIdx.x & 31);
-    const RowIn<ALIGNED> in = row_in<ALIGNED>(a.src, row, a.ld_src, a.rows, a.cols);
-    RowOut<ALIGNED> out(a.dst + row * a.ld_dst);
-    Fetched<ALIGNED> f[kDropVecs];
-    auto valid = [&](uint32_t v) { return values_left(a.cols, 8ull * v); };
+    const uint64_t row = item / a.segments, c0 = (item - row * a.segments) * (kDropVecs * 256);
+    const unsigned short* src = a.src + row * a.ld_src + c0;
+    unsigned short* dst = a.dst + row * a.ld_dst + c0;
+    const uint64_t group = row * a.across + c0 / 8 + (threadIdx.x & 31);
+    Loaded<ALIGNED> f[kDropVecs];
 #pragma unroll
-    for (int i = 0; i < kDropVecs; ++i) fetch8(in, v0 + 32 * i, valid(v0 + 32 * i), f[i]);
-    each<kDropVecs>([&](auto step) {
-        constexpr int i = decltype(step)::value;
-        const uint32_t v = v0 + 32 * i;
-        if (8ull * (v & ~31u) >= a.cols) return;   // the same in all lanes
-        uint32_t w[4], q[4];
-        finish8(in, v, valid(v), f[i], w);
-        drop_one<DT>(a, row * a.across + v, stream, w, q);
-        out.template put<i == 0, i + 1 == kDropVecs>(v, valid(v), valid(v + 1), q);
-    });
+    for (int i = 0; i < kDropVecs; ++i) load_eight(src + 256 * i, columns_left(a.cols, c0 + 256 * i), f[i]);
+#pragma unroll
+    for (int i = 0; i < kDropVecs; ++i) {
+        const int left = columns_left(a.cols, c0 + 256 * i);
+        if (left == 0) break;   // the same in all lanes
+        float x[8];
+        widen_eight<DT>(f[i], x);
+        if (a.drop.below) drop_eight<ALIGNED>(a.drop, group + 32 * i, stream, x);
+        uint32_t q[4];
+        narrow8<DT>(x, q);
+        store_eight<ALIGNED>(dst + 256 * i, left, q);
+    }
 }
 
 // -------------------------------------------------------------------- norm
@@ -184,110 +168,120 @@ __device__ __forceinline__ float larger(float a, float b) {
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
     return r;
 }
-// One warp's 256 values of a row: 8 a lane, y, to codes and scale words.
-// v: the lane's group of 8 columns, `valid` of them inside the row.
-template <int BITS>
-__device__ __forceinline__ void write_codes(const NormArgs& a, uint64_t row, uint32_t v, int valid, float (&y)[8]) {
-    if (valid < 8) {   // 0 / 0 in a row of zeros, or NaN times 0, stays inside the row
+// A warp's 256 columns of a row from c0 on, y, `left` of them inside it, to
+// codes and scale words.
+template <int BITS, bool ALIGNED>
+__device__ __forceinline__ void write_codes(const NormArgs& a, uint64_t row, uint32_t c0, int left, float (&y)[8]) {
+    if (left < 256) {   // 0 / 0 in a row of zeros, or NaN times 0, stays inside the row
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = e < valid ? y[e] : 0.0f;
+        for (int e = 0; e < 8; ++e) y[e] = static_cast<int>(column_of<ALIGNED>(e)) < left ? y[e] : 0.0f;
     }
-    // (bits of magnitudes are ordered like these, infinity and NaN above every number)
-    uint32_t top = __float_as_uint(larger(larger(larger(y[0], y[1]), larger(y[2], y[3])),
-                                          larger(larger(y[4], y[5]), larger(y[6], y[7]))));
-    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));   // four lanes share a block
-    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-    const uint32_t byte = scale_byte<BITS>(__uint_as_float(top));
-    mul8(y, scale_inverse(byte));
-    typename MxElement<BITS>::Eight q;
-    codes8(y, q);
-    if (byte == 255u) no_codes(q);
-    if (v * BITS < a.pitch) *reinterpret_cast<decltype(q)*>(a.codes + row * a.pitch + v * BITS) = q;
-    // the four blocks of a scale tile's row in one word
-    uint32_t word = byte | __shfl_down_sync(0xFFFFFFFFu, byte, 4) << 8;
-    word |= __shfl_down_sync(0xFFFFFFFFu, word, 8) << 16;
-    if ((v & 15) == 0 && (v >> 4) < a.tiles_k)
-        *reinterpret_cast<uint32_t*>(a.scales + scale_at(row, v >> 2, a.tiles_k)) = word;
+    const uint32_t lane = threadIdx.x & 31;
+    uint8_t* codes = a.codes + row * a.pitch;
+    if constexpr (ALIGNED) {
+        const uint32_t v = c0 / 8 + lane;
+        // (bits of magnitudes are ordered like these, infinity and NaN above every number)
+        uint32_t top = __float_as_uint(larger(larger(larger(y[0], y[1]), larger(y[2], y[3])),
+                                              larger(larger(y[4], y[5]), larger(y[6], y[7]))));
+        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));   // four lanes share a block
+        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+        const uint32_t byte = scale_byte<BITS>(__uint_as_float(top));
+        mul8(y, scale_inverse(byte));
+        typename MxElement<BITS>::Eight q;
+        codes8(y, q);
+        if (byte == 255u) no_codes(q);
+        if (v * BITS < a.pitch) *reinterpret_cast<decltype(q)*>(codes + v * BITS) = q;
+        // the four blocks of a scale tile's row in one word
+        uint32_t word = byte | __shfl_down_sync(0xFFFFFFFFu, byte, 4) << 8;
+        word |= __shfl_down_sync(0xFFFFFFFFu, word, 8) << 16;
+        if ((v & 15) == 0 && (v >> 4) < a.tiles_k)
+            *reinterpret_cast<uint32_t*>(a.scales + scale_at(row, v >> 2, a.tiles_k)) = word;
+    } else {   // a block is one value of each lane
+        uint32_t words[2] = {0u, 0u};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(y[e]) & 0x7FFFFFFFu);
+            const uint32_t byte = scale_byte<BITS>(__uint_as_float(top));
+            words[e >> 2] |= byte << (8 * (e & 3));
+            y[e] = __fmul_rn(y[e], scale_inverse(byte));
+            const bool none = byte == 255u;
+            const uint32_t c = c0 + 32 * e + lane;
+            if constexpr (BITS == 8) {
+                if (c < a.pitch) codes[c] = none ? 0 : static_cast<uint8_t>(codes4_e4m3(y[e], 0.0f, 0.0f, 0.0f));
+            } else {
+                const float next = __shfl_down_sync(0xFFFFFFFFu, y[e], 1);
+                const float two[8] = {y[e], next, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+                uint32_t q;
+                codes8(two, q);
+                if ((lane & 1) == 0 && c / 2 < a.pitch) codes[c / 2] = none ? 0 : static_cast<uint8_t>(q);
+            }
+        }
+        if (lane < 2 && (c0 >> 7) + lane < a.tiles_k)
+            *reinterpret_cast<uint32_t*>(a.scales + scale_at(row, (c0 >> 5) + 4 * lane, a.tiles_k)) = lane == 0 ? words[0] : words[1];
+    }
 }
 
-// V groups of 8 columns a thread, those of a row in steps of its threads.
-// BITS: of the codes, or 0.  ALIGNED: every row of every matrix starts on 16
-// bytes and is whole eights.
+// V times 256 columns a warp, one after the other.  BITS: of the codes, or 0.
 template <int BITS, int DT, int V, bool ALIGNED>
 __global__ void __launch_bounds__(V == 4 ? 512 : 1024, V == 4 && ALIGNED ? 2 : 1) k_rms_norm(const __grid_constant__ NormArgs a) {
     pdl_enter();
     __shared__ float s_sum[1][32];
     const RowThreads team(a.row_threads);
-    const uint32_t threads = team.threads, t = team.t;
-    const uint64_t row = static_cast<uint64_t>(blockIdx.x) * (blockDim.x / threads) + team.slot;
+    const uint64_t row = static_cast<uint64_t>(blockIdx.x) * (blockDim.x / team.threads) + team.slot;
     if (row >= a.rows) {   // uniform over a row's threads; the unused rows of the last scale tiles
         if (BITS != 0 && row < (a.rows + 127) / 128 * 128)
-            for (uint64_t k = t; k < a.tiles_k; k += threads)
+            for (uint64_t k = team.t; k < a.tiles_k; k += team.threads)
                 *reinterpret_cast<uint32_t*>(a.scales + scale_at(row, 4 * k, a.tiles_k)) = 0u;
         return;
     }
-    const uint32_t cols = static_cast<uint32_t>(a.cols), v0 = (t >> 5) * (32 * V) + (t & 31);
-    Fetched<ALIGNED> x[V], res[V];
+    const uint32_t c0 = (team.t >> 5) * (256 * V);   // the warp's first column
+    const int cols = static_cast<int>(a.cols) - static_cast<int>(c0);
+    auto left = [&](int j) { return cols - 256 * j; };   // of the row from the j-th 256 columns on
+    Loaded<ALIGNED> x[V], res[V];
     uint32_t h[V][4];
-    const RowIn<ALIGNED> in_x = row_in<ALIGNED>(a.x, row, a.ld_x, a.rows, a.cols);
-    const RowIn<ALIGNED> in_res = row_in<ALIGNED>(a.residual, row, a.ld_residual, a.rows, a.cols);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        const uint32_t v = v0 + 32 * j;
-        fetch8(in_x, v, inside<ALIGNED>(v, cols), x[j]);
-        if (a.residual) fetch8(in_res, v, inside<ALIGNED>(v, cols), res[j]);
+        load_eight(a.x + row * a.ld_x + c0 + 256 * j, left(j), x[j]);
+        if (a.residual) load_eight(a.residual + row * a.ld_residual + c0 + 256 * j, left(j), res[j]);
     }
-    const uint64_t stream = drop_stream(a.drop), group = row * a.across;
+    const uint64_t stream = drop_stream(a.drop), group = row * a.across + c0 / 8 + (threadIdx.x & 31);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        const uint32_t v = v0 + 32 * j;
-        finish8(in_x, v, inside<ALIGNED>(v, cols), x[j], h[j]);
-        if (a.residual || a.drop.below) {
-            float y[8];
-            widen8<DT>(h[j], y);
-            if (a.drop.below) drop8(a.drop, group + v, stream, y);
-            if (a.residual) {
-                uint32_t q[4];
-                finish8(in_res, v, inside<ALIGNED>(v, cols), res[j], q);
-                float s[8];
-                widen8<DT>(q, s);
-                add8(y, s);
-            }
-            narrow8<DT>(y, h[j]);
+        float y[8];
+        widen_eight<DT>(x[j], y);
+        if (a.drop.below) drop_eight<ALIGNED>(a.drop, group + 32 * j, stream, y);
+        if (a.residual) {
+            float s[8];
+            widen_eight<DT>(res[j], s);
+            add8(y, s);
         }
+        narrow8<DT>(y, h[j]);   // (the values as they were where nothing was added or dropped)
     }
     float sums[2] = {0.0f, 0.0f};
-    RowOut<ALIGNED> out_h(a.h + row * a.ld_h), out_y(a.out + row * a.ld_out);
-    each<V>([&](auto step) {
-        constexpr int j = decltype(step)::value;
-        const uint32_t v = v0 + 32 * j;
-        if (a.h) out_h.template put<j == 0, j + 1 == V>(v, inside<ALIGNED>(v, cols), inside<ALIGNED>(v + 1, cols), h[j]);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        if (a.h) store_eight<ALIGNED>(a.h + row * a.ld_h + c0 + 256 * j, left(j), h[j]);
         float y[8];
         widen8<DT>(h[j], y);
         dot8(y, y, sums);
-    });
+    }
     float sum[1] = {sums[0] + sums[1]};
     row_sums<1>(sum, team, s_sum);
     const float r = rsqrt_of(sum[0], a.cols, a.eps);
-    const RowIn<ALIGNED> in_w = row_in<ALIGNED>(a.weight, 0, 0, 1, a.cols);
-    each<V>([&](auto step) {
-        constexpr int j = decltype(step)::value;
-        const uint32_t v = v0 + 32 * j;
-        const int valid = inside<ALIGNED>(v, cols);
-        uint32_t w[4];
-        read_weight<ALIGNED>(in_w, v, valid, w);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
         float y[8], f[8];
         widen8<DT>(h[j], y);
-        widen8<DT>(w, f);
+        read_weight<DT, ALIGNED>(a.weight + c0 + 256 * j, left(j), f);
         mul8(y, r);
         mul8(y, f);
         if (a.out) {
             uint32_t q[4];
             narrow8<DT>(y, q);
-            out_y.template put<j == 0, j + 1 == V>(v, valid, inside<ALIGNED>(v + 1, cols), q);
+            store_eight<ALIGNED>(a.out + row * a.ld_out + c0 + 256 * j, left(j), q);
         }
-        if constexpr (BITS != 0) write_codes<BITS>(a, row, v, valid, y);
-    });
+        if constexpr (BITS != 0) write_codes<BITS, ALIGNED>(a, row, c0 + 256 * j, left(j), y);
+    }
 }
 
 // ---------------------------------------------------------- norm, backward
@@ -320,12 +314,17 @@ constexpr size_t grad_ring(size_t v, size_t row_threads, size_t rows) {   // byt
 constexpr size_t kMostGradSmem = grad_ring(4, 512, 1);
 static_assert(kMostGradSmem >= grad_ring(2, 64, 4) && kMostGradSmem >= grad_ring(4, 32, 8), "shared memory");
 
-// A block takes its rows blockIdx.x, + gridDim.x, ..., and keeps its share of dw in registers over all of them.  The next
-// row is on its way to shared memory while this one is worked on: 62 us for
-// 8192 x 4096 bf16 with dropout (5.4 TB/s) against 70 with the next row in
-// registers and 94 without.  Rows that start between two 16-byte boundaries
-// are copied as the aligned pieces that cover them; a thread then needs two
-// neighbouring pieces, of which another thread copied the second.
+// How many values behind a 16-byte boundary a row starts.
+__device__ __forceinline__ uint32_t behind(const unsigned short* row) {
+    return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row) >> 1) & 7u;
+}
+
+// A block takes its rows blockIdx.x, + gridDim.x, ..., and keeps its share of
+// dw in registers over all of them.  The next row is on its way to shared
+// memory while this one is worked on: 62 us for 8192 x 4096 bf16 with dropout
+// (5.4 TB/s) against 70 with the next row in registers and 94 without.  Rows
+// that start between two 16-byte boundaries are copied as the aligned pieces
+// that cover them, and read from there as column_of says.
 template <int DT, int V, bool ALIGNED>
 __global__ void __maxnreg__(V == 4 || ALIGNED ? 128 : 96) k_rms_norm_backward(const __grid_constant__ NormGradArgs a) {
     pdl_enter();
@@ -333,59 +332,66 @@ __global__ void __maxnreg__(V == 4 || ALIGNED ? 128 : 96) k_rms_norm_backward(co
     // [row of the block][stage][h, dy, dh_in][width]; at the end, with several rows: [row][8 * across] floats
     extern __shared__ __align__(16) uint4 s_rows[];
     const RowThreads team(a.row_threads);
-    const uint32_t threads = team.threads, t = team.t, slot = team.slot, slots = blockDim.x / threads;
+    const uint32_t slots = blockDim.x / team.threads, lane = threadIdx.x & 31;
     const uint64_t step = static_cast<uint64_t>(gridDim.x) * slots;
     const uint64_t stream = drop_stream(a.drop);
-    const uint32_t cols = static_cast<uint32_t>(a.cols), v0 = (t >> 5) * (32 * V) + (t & 31);
+    const uint32_t c0 = (team.t >> 5) * (256 * V), v0 = c0 / 8 + lane;   // the warp's first column, the lane's first piece
+    const int cols = static_cast<int>(a.cols) - static_cast<int>(c0);
+    auto left = [&](int j) { return cols - 256 * j; };   // of the row from the j-th 256 columns on
     float dw[V][8];
-    uint32_t w[V][4];
-    // a row's slots: one for each group, and one for the piece behind the last
-    const uint32_t width = V * threads + 1, room = 3 * kGradStages * width;
-    uint4* const mine = s_rows + slot * room;
+    Loaded<ALIGNED> w[V];
+    // a row's slots: one for each eight columns, and one for the piece behind the last
+    const uint32_t width = V * team.threads + 1, room = 3 * kGradStages * width;
+    uint4* const mine = s_rows + team.slot * room;
     auto place = [&](uint32_t stage, int which, uint32_t v) -> uint4& { return mine[(stage * 3 + which) * width + v]; };
-    const RowIn<ALIGNED> in_w = row_in<ALIGNED>(a.weight, 0, 0, 1, a.cols);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        const uint32_t v = v0 + 32 * j;
-        const int valid = inside<ALIGNED>(v, cols);
-        read_weight<ALIGNED>(in_w, v, valid, w[j]);
+        load_eight(a.weight + c0 + 256 * j, left(j), w[j]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) dw[j][e] = 0.0f;
-        if (ALIGNED && valid <= 0) {   // never copied to
+        if (ALIGNED && v0 + 32 * j >= a.across) {   // never copied to
 #pragma unroll
-            for (int i = 0; i < 3 * kGradStages; ++i) place(i / 3, i % 3, v) = make_uint4(0u, 0u, 0u, 0u);
+            for (int i = 0; i < 3 * kGradStages; ++i) place(i / 3, i % 3, v0 + 32 * j) = make_uint4(0u, 0u, 0u, 0u);
         }
     }
-    uint64_t row = static_cast<uint64_t>(blockIdx.x) * slots + slot;
-    auto copy_row = [&](const RowIn<ALIGNED>& r, uint32_t stage, int which) {
+    uint64_t row = static_cast<uint64_t>(blockIdx.x) * slots + team.slot;
+    auto copy_row = [&](const unsigned short* base, uint64_t ld, uint64_t row, uint32_t stage, int which) {
+        if constexpr (ALIGNED) {
+            const uint4* at = reinterpret_cast<const uint4*>(base + row * ld);
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const uint32_t v = v0 + 32 * j;
-            const int valid = inside<ALIGNED>(v, cols);
-            if (valid <= 0) continue;
-            if constexpr (ALIGNED) {
-                copy16(&place(stage, which, v), r.first + v);
-            } else {
-                if (r.m == 8u) {   // the first row or the last one
-                    place(stage, which, v) = read_some(r.row + 8ull * v, valid);
+            for (int j = 0; j < V; ++j)
+                if (v0 + 32 * j < a.across) copy16(&place(stage, which, v0 + 32 * j), at + v0 + 32 * j);
+        } else {
+            const unsigned short* at = base + row * ld;
+            const uint32_t m = behind(at), pieces = (m + static_cast<uint32_t>(a.cols) + 7) / 8;
+            const uint4* from = reinterpret_cast<const uint4*>(at - m);
+            // what is outside the matrix is not touched: the first row's first piece and the last row's last one may begin
+            // or end there
+            const uint4* low = reinterpret_cast<const uint4*>(base);
+            const unsigned short* high = base + (a.rows - 1) * ld + a.cols;
+            for (uint32_t v = team.t; v < pieces; v += team.threads) {
+                if (from + v >= low && reinterpret_cast<const unsigned short*>(from + v + 1) <= high) {
+                    copy16(&place(stage, which, v), from + v);
                 } else {
-                    copy16(&place(stage, which, v), r.first + v);
-                    if (v + 1 == a.across && valid > 8 - static_cast<int>(r.m)) copy16(&place(stage, which, v + 1), r.first + v + 1);
+                    unsigned short* to = reinterpret_cast<unsigned short*>(&place(stage, which, v));
+#pragma unroll
+                    for (uint32_t e = 0; e < 8; ++e)
+                        if (8 * v + e >= m && 8 * v + e < m + a.cols) to[e] = at[8 * v + e - m];
                 }
             }
         }
     };
     auto start = [&](uint64_t row, uint32_t stage) {
         if (row < a.rows) {
-            copy_row(row_in<ALIGNED>(a.h, row, a.ld_h, a.rows, a.cols), stage, 0);
-            copy_row(row_in<ALIGNED>(a.dy, row, a.ld_dy, a.rows, a.cols), stage, 1);
-            if (a.dh_in) copy_row(row_in<ALIGNED>(a.dh_in, row, a.ld_in, a.rows, a.cols), stage, 2);
+            copy_row(a.h, a.ld_h, row, stage, 0);
+            copy_row(a.dy, a.ld_dy, row, stage, 1);
+            if (a.dh_in) copy_row(a.dh_in, a.ld_in, row, stage, 2);
         }
         copy_commit();
     };
     start(row, 0);
     for (uint32_t flip = 0; row < a.rows; row += step, flip ^= 1) {   // uniform over a row's threads; flip: the stage too
-        if (ALIGNED) {
+        if (ALIGNED) {   // a thread reads what it copied
             start(row + step, flip ^ 1);
             copy_wait<1>();
         } else {
@@ -393,38 +399,32 @@ __global__ void __maxnreg__(V == 4 || ALIGNED ? 128 : 96) k_rms_norm_backward(co
             team.sync();   // the others' copies are there, and what they read of the row before is read
             start(row + step, flip ^ 1);
         }
-        auto values = [&](int which, int j, const unsigned short* base, uint64_t ld, uint32_t (&q)[4]) {
-            const uint32_t v = v0 + 32 * j;
-            const uint4 p = place(flip, which, v);
-            q[0] = p.x; q[1] = p.y; q[2] = p.z; q[3] = p.w;
-            if constexpr (!ALIGNED) {
-                const uint4 n = place(flip, which, v + 1);
-                const uint32_t own[4] = {p.x, p.y, p.z, p.w}, next[4] = {n.x, n.y, n.z, n.w};
-                shift_halves(own, next, row_in<false>(base, row, ld, a.rows, a.cols).m & 7u, q);
-                const int valid = inside<false>(v, cols);
-                if (valid < 8) clear_tail(q, valid);
+        // where the row's columns begin in its slots
+        const uint32_t m[3] = {ALIGNED ? 0u : behind(a.h + row * a.ld_h), ALIGNED ? 0u : behind(a.dy + row * a.ld_dy),
+                               ALIGNED ? 0u : behind(a.dh_in + row * a.ld_in)};
+        auto values = [&](int which, int j, float (&x)[8]) {
+            if constexpr (ALIGNED) {
+                widen_eight<DT>(Loaded<true>{place(flip, which, v0 + 32 * j)}, x);
+            } else {
+                const unsigned short* from =
+                    reinterpret_cast<const unsigned short*>(&place(flip, which, 0)) + m[which] + c0 + 256 * j + lane;
+                if (left(j) >= 256) {   // the same in all lanes
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = widen<DT>(from[32 * e]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        x[e] = static_cast<int>(column_of<false>(e)) < left(j) ? widen<DT>(from[32 * e]) : 0.0f;
+                }
             }
         };
-        // what had to be put together is kept for the second pass, where there are registers for it
-        constexpr bool kHold = !ALIGNED && V <= 2;
-        uint32_t held[kHold ? V : 1][2][4];
         float ss[2] = {0.0f, 0.0f}, sg[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            uint32_t p[4], q[4];
-            values(0, j, a.h, a.ld_h, p);
-            values(1, j, a.dy, a.ld_dy, q);
-            if constexpr (kHold) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    held[j][0][i] = p[i];
-                    held[j][1][i] = q[i];
-                }
-            }
             float x[8], y[8], f[8];
-            widen8<DT>(p, x);
-            widen8<DT>(q, y);
-            widen8<DT>(w[j], f);
+            values(0, j, x);
+            values(1, j, y);
+            widen_eight<DT>(w[j], f);
             mul8(y, f);
             dot8(x, x, ss);
             dot8(y, x, sg);
@@ -433,24 +433,14 @@ __global__ void __maxnreg__(V == 4 || ALIGNED ? 128 : 96) k_rms_norm_backward(co
         row_sums<2>(sums, team, s_sum[flip]);
         const float r = rsqrt_of(sums[0], a.cols, a.eps);
         const float k = __fmul_rn(__fmul_rn(r, r), __fdiv_rn(sums[1], static_cast<float>(a.cols)));
-        const uint64_t group = row * a.across;
-        RowOut<ALIGNED> out_h(a.dh + row * a.ld_dh), out_x(a.dx + row * a.ld_dx);
-        each<V>([&](auto number) {
-            constexpr int j = decltype(number)::value;
-            const uint32_t v = v0 + 32 * j;
-            const int valid = inside<ALIGNED>(v, cols), next = inside<ALIGNED>(v + 1, cols);
+        const uint64_t group = row * a.across + v0;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
             uint32_t q[4];
             float x[8], y[8], f[8];
-            if constexpr (kHold) {
-                widen8<DT>(held[j][0], x);
-                widen8<DT>(held[j][1], y);
-            } else {
-                values(0, j, a.h, a.ld_h, q);
-                widen8<DT>(q, x);
-                values(1, j, a.dy, a.ld_dy, q);
-                widen8<DT>(q, y);
-            }
-            widen8<DT>(w[j], f);
+            values(0, j, x);
+            values(1, j, y);
+            widen_eight<DT>(w[j], f);
             mul8(f, y);          // g
             float u[8];
 #pragma unroll
@@ -460,45 +450,41 @@ __global__ void __maxnreg__(V == 4 || ALIGNED ? 128 : 96) k_rms_norm_backward(co
             mul8(x, r);
             fma8(y, x, dw[j]);
             if (a.dh_in) {
-                values(2, j, a.dh_in, a.ld_in, q);
-                widen8<DT>(q, x);
+                values(2, j, x);
                 add8(f, x);
             }
             narrow8<DT>(f, q);
-            out_h.template put<j == 0, j + 1 == V>(v, valid, next, q);
+            store_eight<ALIGNED>(a.dh + row * a.ld_dh + c0 + 256 * j, left(j), q);
             if (a.dx) {
-                if (a.drop.below) drop8(a.drop, group + v, stream, f);
+                if (a.drop.below) drop_eight<ALIGNED>(a.drop, group + 32 * j, stream, f);
                 narrow8<DT>(f, q);
-                out_x.template put<j == 0, j + 1 == V>(v, valid, next, q);
+                store_eight<ALIGNED>(a.dx + row * a.ld_dx + c0 + 256 * j, left(j), q);
             }
-        });
+        }
     }
     copy_wait<0>();
     if (!a.partial) return;
     float* out = a.partial + static_cast<uint64_t>(blockIdx.x) * 8 * a.across;
-    if (slots == 1) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const uint32_t v = v0 + 32 * j;
-            if (v >= a.across) continue;
-            float4* to = reinterpret_cast<float4*>(out + 8 * v);
-            to[0] = make_float4(dw[j][0], dw[j][1], dw[j][2], dw[j][3]);
-            to[1] = make_float4(dw[j][4], dw[j][5], dw[j][6], dw[j][7]);
-        }
-        return;
-    }
-    // the rows' shares, added in their order, where the rows were
-    __syncthreads();
-    float* const s_dw = reinterpret_cast<float*>(s_rows);
     const uint32_t values = static_cast<uint32_t>(8 * a.across);
+    float* const s_dw = reinterpret_cast<float*>(s_rows);
+    if (slots > 1) __syncthreads();   // the rows are done with; their shares of dw take their place
+    float* to = slots > 1 ? s_dw + team.slot * values : out;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        const uint32_t v = v0 + 32 * j;
-        if (v >= a.across) continue;
-        float4* to = reinterpret_cast<float4*>(s_dw + slot * values + 8 * v);
-        to[0] = make_float4(dw[j][0], dw[j][1], dw[j][2], dw[j][3]);
-        to[1] = make_float4(dw[j][4], dw[j][5], dw[j][6], dw[j][7]);
+        if constexpr (ALIGNED) {
+            if (v0 + 32 * j >= a.across) continue;
+            float4* at = reinterpret_cast<float4*>(to + 8 * (v0 + 32 * j));
+            at[0] = make_float4(dw[j][0], dw[j][1], dw[j][2], dw[j][3]);
+            at[1] = make_float4(dw[j][4], dw[j][5], dw[j][6], dw[j][7]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t c = c0 + 256 * j + column_of<false>(e);
+                if (c < values) to[c] = dw[j][e];
+            }
+        }
     }
+    if (slots == 1) return;
     __syncthreads();
     for (uint32_t c = threadIdx.x; c < values; c += blockDim.x) {
         float s = 0.0f;
@@ -618,8 +604,8 @@ RowShape row_shape(uint64_t groups, int most_v, unsigned most) {
 // Few rows finish sooner with more threads each; many are cheaper a row with
 // fewer: 64 x 4096 with dropout into 8 bits 4.2, 4.4 and 5.3 us at 1, 2 and 4
 // eights a thread, 608 x 4096 9.6, 8.2 and 9.5, 8192 x 4096 76, 68 and 61.
-RowShape norm_shape(uint64_t rows, uint64_t groups) {
-    const int v = rows >= 1216 ? 4 : rows >= 304 ? 2 : 1;
+RowShape norm_shape(uint64_t rows, uint64_t groups, bool whole) {
+    const int v = !whole ? (rows >= 1216 ? 2 : 1) : rows >= 1216 ? 4 : rows >= 304 ? 2 : 1;
     return row_shape(groups, v, v == 4 ? 512 : 1024);
 }
 constexpr unsigned kGradBlocks = 304;   // two an SM
@@ -712,7 +698,7 @@ int zero_rms_norm(int dtype, uint64_t rows, uint64_t cols, const void* x16, uint
     a.pitch = up(cols, kMxBlock) * bits / 8;
     a.tiles_k = bits ? up(cols, 128) / 128 : 0;
     a.eps = eps;
-    const RowShape r = norm_shape(rows, bits ? 16 * a.tiles_k : a.across);
+    const RowShape r = norm_shape(rows, bits ? 16 * a.tiles_k : a.across, whole);
     a.row_threads = r.row_threads;
     const uint64_t all = bits ? up(rows, 128) : rows;
     const unsigned blocks = static_cast<unsigned>((all + r.rows - 1) / r.rows);

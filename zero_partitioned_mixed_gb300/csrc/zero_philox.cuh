@@ -67,16 +67,33 @@ __device__ __forceinline__ uint4 philox(const DropArgs& a, uint64_t group, uint6
     return make_uint4(x0, x1, x2, x3);
 }
 
-// The dropout of a group's 8 values: a kept one times the factor, rounded
-// once; a dropped one is 0, whatever it was.
-__device__ __forceinline__ void drop8(const DropArgs& a, uint64_t group, uint64_t stream, float (&v)[8]) {
+// The dropout of a lane's eight values: a kept one times the factor, rounded
+// once; a dropped one is 0, whatever it was.  By all lanes of a warp together;
+// group: the lane's, of the 32 groups of a warp's 256 columns.  Where the lane
+// has other columns than its group's (column_of), the groups' decisions are
+// handed round.
+template <bool ALIGNED>
+__device__ __forceinline__ void drop_eight(const DropArgs& a, uint64_t group, uint64_t stream, float (&v)[8]) {
     const uint4 w = philox(a, group, stream);
     const uint32_t r[4] = {w.x, w.y, w.z, w.w};
     mul8(v, a.factor);
+    if constexpr (ALIGNED) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = (r[i] << 16) < a.below ? 0.0f : v[2 * i];
-        v[2 * i + 1] = r[i] < a.below ? 0.0f : v[2 * i + 1];
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = (r[i] << 16) < a.below ? 0.0f : v[2 * i];
+            v[2 * i + 1] = r[i] < a.below ? 0.0f : v[2 * i + 1];
+        }
+    } else {
+        uint32_t dropped = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            dropped |= (r[i] << 16) < a.below ? 1u << (2 * i) : 0u;
+            dropped |= r[i] < a.below ? 2u << (2 * i) : 0u;
+        }
+        const uint32_t lane = threadIdx.x & 31, bit = 1u << (lane & 7);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] = __shfl_sync(0xFFFFFFFFu, dropped, 4 * e + (lane >> 3)) & bit ? 0.0f : v[e];
     }
 }
 

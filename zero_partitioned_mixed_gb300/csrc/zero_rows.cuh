@@ -162,178 +162,79 @@ __device__ __forceinline__ void dot8(const float (&a)[8], const float (&b)[8], f
     unpair(x, s[0], s[1]);
 }
 
-// Rows of 16-bit matrices, eight values a lane: lane l of a warp has the row's
-// group v of 8 consecutive values, lane l + 1 group v + 1.  ALIGNED: every row
-// starts on 16 bytes and is whole eights.  Else a row that starts m values
-// behind a 16-byte boundary is read as the two aligned pieces around a group
-// and put together by shifts, and written in aligned pieces, each with the
-// last m values of the lane before.
-__device__ __noinline__ uint4 read_some(const unsigned short* at, int count) {
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        if (e < count) w[e >> 1] |= static_cast<uint32_t>(__ldcs(at + e)) << (16 * (e & 1));
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-// Values `from` to `to` - 1 of eight.
-__device__ __noinline__ void store_some(unsigned short* at, uint4 x, int from, int to) {
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        if (e >= from && e < to) at[e] = static_cast<unsigned short>(w[e >> 1] >> (16 * (e & 1)));
-}
-
-// Zeros from value `valid` on: rare too.
-__device__ __noinline__ uint4 without_tail(uint4 x, int valid) {
-    uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    clear_from(w, valid);
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-__device__ __forceinline__ void clear_tail(uint32_t (&w)[4], int valid) {
-    const uint4 x = without_tail(make_uint4(w[0], w[1], w[2], w[3]), valid);
-    w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
-}
-
+// 256 columns of a row of 16-bit values at a time, by a warp, eight a lane.
+// ALIGNED, where every row starts on 16 bytes and is whole eights: lane l has
+// columns 8 l to 8 l + 7.  Else it has columns l, l + 32, ..., l + 224, so that
+// every access of the warp is 64 neighbouring bytes wherever the row starts,
+// nothing has to be shifted together, and nothing beside the row is touched:
+// @@ODD@@
 template <bool ALIGNED>
-struct RowIn;
+__device__ __forceinline__ uint32_t column_of(int e) {
+    const uint32_t lane = threadIdx.x & 31;
+    return ALIGNED ? 8 * lane + e : 32 * e + lane;
+}
+template <bool ALIGNED>
+struct Loaded;
 template <>
-struct RowIn<true> {
-    const uint4* first;
-};
-template <>
-struct RowIn<false> {
-    const uint4* first;          // the piece with the row's first value
-    const unsigned short* row;
-    uint32_t m;                  // values before that one in it; 8: pieces would leave the matrix, read value by value
-};
-// Row `row` of a rows x cols matrix.
-template <bool ALIGNED>
-__device__ __forceinline__ RowIn<ALIGNED> row_in(const unsigned short* base, uint64_t row, uint64_t ld, uint64_t rows, uint64_t cols) {
-    const unsigned short* at = base + row * ld;
-    if constexpr (ALIGNED) {
-        return {reinterpret_cast<const uint4*>(at)};
-    } else {
-        const uintptr_t a = reinterpret_cast<uintptr_t>(at), first = a & ~static_cast<uintptr_t>(15);
-        const uint32_t m = static_cast<uint32_t>(a - first) >> 1;
-        const bool in = first >= reinterpret_cast<uintptr_t>(base) &&
-                        first + 16 * ((m + cols + 7) / 8) <= reinterpret_cast<uintptr_t>(base + (rows - 1) * ld + cols);
-        return {reinterpret_cast<const uint4*>(first), at, in ? m : 8u};
-    }
-}
-
-// A read in two steps, so that a thread's loads are all in flight before the
-// first one's values are looked at (putting them together takes branches).
-template <bool ALIGNED>
-struct Fetched {
+struct Loaded<true> {
     uint4 x;
 };
 template <>
-struct Fetched<false> {
-    uint4 x, y;
+struct Loaded<false> {
+    unsigned short x[8];
 };
-// Group v, `valid` (at most 8) of whose values are inside the row.
-__device__ __forceinline__ void fetch8(const RowIn<true>& r, uint32_t v, int valid, Fetched<true>& f) {
-    f.x = make_uint4(0u, 0u, 0u, 0u);
-    if (valid > 0) f.x = __ldcs(r.first + v);
+// at: the first of the 256 columns, `left` of which (any number) are inside
+// the row; zeros for the others.
+__device__ __forceinline__ void load_eight(const unsigned short* at, int left, Loaded<true>& r) {
+    r.x = make_uint4(0u, 0u, 0u, 0u);
+    if (static_cast<int>(column_of<true>(0)) < left) r.x = __ldcs(reinterpret_cast<const uint4*>(at) + (threadIdx.x & 31));
 }
-__device__ __forceinline__ void fetch8(const RowIn<false>& r, uint32_t v, int valid, Fetched<false>& f) {
-    f.x = f.y = make_uint4(0u, 0u, 0u, 0u);
-    if (r.m < 8u && valid > 0) f.x = r.first[v];
-    if (r.m < 8u && valid > 8 - static_cast<int>(r.m)) f.y = r.first[v + 1];   // the next lane's first: the cache serves it
-}
-__device__ __forceinline__ void finish8(const RowIn<true>&, uint32_t, int, const Fetched<true>& f, uint32_t (&w)[4]) {
-    w[0] = f.x.x; w[1] = f.x.y; w[2] = f.x.z; w[3] = f.x.w;
-}
-__device__ __forceinline__ void finish8(const RowIn<false>& r, uint32_t v, int valid, const Fetched<false>& f, uint32_t (&w)[4]) {
-    if (r.m < 8u) {
-        const uint32_t own[4] = {f.x.x, f.x.y, f.x.z, f.x.w}, next[4] = {f.y.x, f.y.y, f.y.z, f.y.w};
-        shift_halves(own, next, r.m, w);
-        if (valid < 8) clear_tail(w, valid);
-    } else {
-        const uint4 x = valid > 0 ? read_some(r.row + 8ull * v, valid) : make_uint4(0u, 0u, 0u, 0u);
-        w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
-    }
-}
-template <bool ALIGNED>
-__device__ __forceinline__ void read8(const RowIn<ALIGNED>& r, uint32_t v, int valid, uint32_t (&w)[4]) {
-    Fetched<ALIGNED> f;
-    fetch8(r, v, valid, f);
-    finish8(r, v, valid, f, w);
-}
-
-// The first m, and the last 8 - m, halves of an aligned piece; m in 1..7.
-__device__ __forceinline__ void store_low(uint4* piece, const uint32_t (&q)[4], uint32_t m) {
-    if (m & 4) *reinterpret_cast<uint2*>(piece) = make_uint2(q[0], q[1]);
-    if (m & 2) reinterpret_cast<uint32_t*>(piece)[m & 4 ? 2 : 0] = m & 4 ? q[2] : q[0];
-    if (m & 1) reinterpret_cast<unsigned short*>(piece)[m - 1] =
-        static_cast<unsigned short>(m == 1 ? q[0] : m == 3 ? q[1] : m == 5 ? q[2] : q[3]);
-}
-__device__ __forceinline__ void store_high(uint4* piece, const uint32_t (&q)[4], uint32_t m) {
-    const uint32_t k = (m + 1) >> 1;   // whole words from the k-th on
-    if (m & 1) reinterpret_cast<unsigned short*>(piece)[m] =
-        static_cast<unsigned short>((m == 1 ? q[0] : m == 3 ? q[1] : m == 5 ? q[2] : q[3]) >> 16);
-    if (k & 1) reinterpret_cast<uint32_t*>(piece)[k] = k == 1 ? q[1] : q[3];
-    if (k <= 2) reinterpret_cast<uint2*>(piece)[1] = make_uint2(q[2], q[3]);
-}
-// A row's groups written by all lanes of a warp together, 32 consecutive ones
-// at a time and these one after the other (put), and at the end what is left
-// between this warp and the next (finish).  Not ALIGNED: a lane writes the
-// aligned piece with the last values of the lane before it, lane 0 with those
-// that lane 31 had the last time; the piece between two warps is written by
-// lane 0 of either; what ends the row is written value by value.
-template <bool ALIGNED>
-struct RowOut;
-template <>
-struct RowOut<true> {
-    uint4* row;
-    __device__ __forceinline__ explicit RowOut(unsigned short* at) : row(reinterpret_cast<uint4*>(at)) {}
-    // `next`: how many values of group v + 1 are inside the row
-    template <bool FIRST, bool LAST>
-    __device__ __forceinline__ void put(uint32_t v, int valid, int, const uint32_t (&w)[4]) {
-        if (valid > 0) __stcs(row + v, make_uint4(w[0], w[1], w[2], w[3]));
-    }
-};
-template <>
-struct RowOut<false> {
-    unsigned short* row;
-    uint32_t m;          // values between the row's first piece's start and the row: the same in all lanes
-    uint32_t carry[4];   // lane 0: what lane 31 had
-    __device__ __forceinline__ explicit RowOut(unsigned short* at)
-        : row(at), m(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(at) >> 1) & 7u), carry{0u, 0u, 0u, 0u} {}
-    template <bool FIRST, bool LAST>
-    __device__ __forceinline__ void put(uint32_t v, int valid, int next, const uint32_t (&w)[4]) {
-        const uint32_t lane = threadIdx.x & 31;
-        unsigned short* at = row + 8ull * v;
-        const int own = 8 - static_cast<int>(m);   // values up to the boundary
-        int from = 0, to = 0;                      // values to be written by themselves
-        if (m == 0u) {
-            if (valid == 8) *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
-            else to = valid;
-        } else {
-            uint32_t before[4], q[4];
+__device__ __forceinline__ void load_eight(const unsigned short* at, int left, Loaded<false>& r) {
+    at += threadIdx.x & 31;
+    if (left >= 256) {   // the same in all lanes
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t round = __shfl_sync(0xFFFFFFFFu, w[i], (lane + 31) & 31);
-                before[i] = lane == 0 ? carry[i] : round;
-                carry[i] = round;
-            }
-            shift_halves(before, w, static_cast<uint32_t>(own), q);
-            uint4* piece = reinterpret_cast<uint4*>(at - m);
-            if (valid >= own) {
-                if (FIRST && lane == 0) store_high(piece, q, m);
-                else *piece = make_uint4(q[0], q[1], q[2], q[3]);
-            }
-            if (valid < own) to = valid;
-            else if (valid > own && (LAST && lane == 31 ? valid < 8 : next < own)) from = own, to = valid;
-            if (LAST && __shfl_sync(0xFFFFFFFFu, valid, 31) == 8 && lane == 0) {
-                const uint32_t none[4] = {0u, 0u, 0u, 0u};
-                shift_halves(carry, none, static_cast<uint32_t>(own), q);
-                store_low(piece + 32, q, m);
-            }
-        }
-        if (from < to) store_some(at, make_uint4(w[0], w[1], w[2], w[3]), from, to);
+        for (int e = 0; e < 8; ++e) r.x[e] = __ldcs(at + 32 * e);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r.x[e] = static_cast<int>(column_of<false>(e)) < left ? __ldcs(at + 32 * e) : 0;
     }
-};
+}
+template <int DT>
+__device__ __forceinline__ void widen_eight(const Loaded<true>& r, float (&v)[8]) {
+    widen2<DT>(r.x.x, v[0], v[1]);
+    widen2<DT>(r.x.y, v[2], v[3]);
+    widen2<DT>(r.x.z, v[4], v[5]);
+    widen2<DT>(r.x.w, v[6], v[7]);
+}
+template <int DT>
+__device__ __forceinline__ void widen_eight(const Loaded<false>& r, float (&v)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = widen<DT>(r.x[e]);
+}
+// q: the eight in pairs, the first one low.
+template <bool ALIGNED>
+__device__ __forceinline__ void store_eight(unsigned short* at, int left, const uint32_t (&q)[4]) {
+    if constexpr (ALIGNED) {
+        if (static_cast<int>(column_of<true>(0)) < left)
+            __stcs(reinterpret_cast<uint4*>(at) + (threadIdx.x & 31), make_uint4(q[0], q[1], q[2], q[3]));
+    } else {
+        at += threadIdx.x & 31;
+        if (left >= 256) {   // the same in all lanes
+#pragma unroll
+            for (int e = 0; e < 8; ++e) at[32 * e] = static_cast<unsigned short>(q[e >> 1] >> (16 * (e & 1)));
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (static_cast<int>(column_of<false>(e)) < left)
+                    at[32 * e] = static_cast<unsigned short>(q[e >> 1] >> (16 * (e & 1)));
+        }
+    }
+}
+// How many of the 256 columns from `first` on are inside a row of `cols`.
+__device__ __forceinline__ int columns_left(uint64_t cols, uint64_t first) {
+    const int64_t left = static_cast<int64_t>(cols) - static_cast<int64_t>(first);
+    return left > 256 ? 256 : left < 0 ? 0 : static_cast<int>(left);
+}
 template <int DT>
 __device__ __forceinline__ void widen8(const uint32_t (&w)[4], float (&v)[8]) {
 #pragma unroll
