@@ -609,7 +609,9 @@ RowShape norm_shape(uint64_t rows, uint64_t groups, bool whole) {
     return row_shape(groups, v, v == 4 ? 512 : 1024);
 }
 constexpr unsigned kGradBlocks = 304;   // two an SM
-RowShape grad_shape(uint64_t cols) { return row_shape((cols + 7) / 8, cols <= 1024 ? 4 : 2, 512); }
+RowShape grad_shape(uint64_t rows, uint64_t cols) {
+    return row_shape((cols + 7) / 8, rows < kGradBlocks ? 1 : cols <= 1024 ? 4 : 2, 512);
+}
 uint64_t grad_blocks(uint64_t rows, const RowShape& r) {
     const uint64_t b = (rows + r.rows - 1) / r.rows;
     return b < kGradBlocks ? b : kGradBlocks;
@@ -713,7 +715,7 @@ int zero_rms_norm(int dtype, uint64_t rows, uint64_t cols, const void* x16, uint
 
 uint64_t zero_rms_norm_backward_workspace_bytes(uint64_t rows, uint64_t cols) {
     if (rows == 0 || cols == 0 || rows > kMaxRows || cols > ZERO_MAX_NORM_COLS) return 0;
-    return grad_blocks(rows, grad_shape(cols)) * up(cols, 8) * sizeof(float);
+    return grad_blocks(rows, grad_shape(rows, cols)) * up(cols, 8) * sizeof(float);
 }
 
 int zero_rms_norm_backward(int dtype, uint64_t rows, uint64_t cols, const void* dy16, uint64_t ld_dy, const void* h16,
@@ -744,7 +746,7 @@ int zero_rms_norm_backward(int dtype, uint64_t rows, uint64_t cols, const void* 
         if (workspace_bytes < zero_rms_norm_backward_workspace_bytes(rows, cols))
             return refuse(ZERO_EINVAL, "workspace is smaller than zero_rms_norm_backward_workspace_bytes()");
     }
-    const RowShape r = grad_shape(cols);
+    const RowShape r = grad_shape(rows, cols);
     const unsigned blocks = static_cast<unsigned>(grad_blocks(rows, r));
     a.dy = static_cast<const unsigned short*>(dy16);
     a.h = static_cast<const unsigned short*>(h16);
