@@ -10,12 +10,20 @@
 //   sort   the tokens by id, stably, by one cluster of 8 CTAs (radix digits
 //          of up to 8 bits; its CTAs see each other's counts through their
 //          shared memory, hand each other up to 16384 keys the same way, and
-//          wait for each other at the cluster's barrier only).  The launch's other CTAs fill the table with zeros
-//          meanwhile, which takes longer for tables of real sizes.
+//          wait for each other at the cluster's barrier only).  The launch's
+//          other CTAs fill the table with zeros meanwhile, which takes as
+//          long or longer for tables of real sizes.
 //   sum    a warp takes 256 columns of kPiece consecutive sorted tokens, in
 //          fp32.  A run of one id that lies inside its piece is finished and
 //          written; one that crosses into other pieces leaves partial sums.
-//   join   the warp of the piece in which such a run begins adds them in order.
+//   join   the warp of the piece in which such a run begins adds them in
+//          order, or its block where there are many.
+//
+// Up to 512 tokens are not sorted: each looks at all ids (k_embedding_few).
+// 8192 x 768 bf16 into 50257 rows takes 26.5 us, 6007 x 1003 fp16 into 32003
+// 27.2: writing the table at the 6 TB/s that stores alone reach is 12 to 13 of
+// them, the sort hides behind it, and sum and join are chains of dependent
+// reads, 9 us together, that nothing is left to hide.
 //
 // An id outside the table is padding: zeros forward, no gradient.
 
@@ -116,8 +124,8 @@ __device__ __forceinline__ uint32_t load_l2(const uint32_t* p) {
 constexpr uint32_t kZeroBytes = 16384;
 
 // By CTA `cta` of `ctas`.  Rows without gaps are one range, which a thread a
-// CTA fills by bulk copies of `zeros` (77 MB in 12 us; 16-byte stores of all
-// threads took 18); rows with gaps a warp each.
+// CTA fills by bulk copies of `zeros` (77 MB in 12 to 13 us, 16-byte stores of
+// all threads 18); rows with gaps a warp each.
 __device__ void fill_zeros(const SortArgs& a, uint4 (&zeros)[kZeroBytes / 16], uint32_t cta, uint32_t ctas) {
     const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (a.zero_rows == 1) {
@@ -301,6 +309,13 @@ __global__ void __launch_bounds__(kSortThreads) k_embedding_sort(const __grid_co
         if (last) cluster_leave();   // the other CTAs have read its counts
         else cluster_sync();
     }
+}
+
+// The zeros by themselves.
+__global__ void __launch_bounds__(kSortThreads) k_embedding_zeros(const __grid_constant__ SortArgs a) {
+    pdl_enter();
+    __shared__ __align__(128) uint4 s_zeros[kZeroBytes / 16];
+    fill_zeros(a, s_zeros, blockIdx.x, gridDim.x);
 }
 
 // -------------------------------------------------------------- sum and join
@@ -514,6 +529,62 @@ __global__ void __launch_bounds__(kThreads) k_embedding_join(const __grid_consta
     }
 }
 
+// ------------------------------------------------------------ few tokens
+// Up to kFewTokens tokens need no sorting: a warp takes 256 columns of one
+// token, looks at all ids, and leaves where its own occurs before; else it
+// adds up the rows with that id, in order.
+struct FewArgs {
+    SumArgs sum;
+    const void* ids;
+    int wide_ids;
+};
+constexpr uint32_t kFewTokens = 512;
+static_assert(kFewTokens <= 32 * 32, "a word a lane");
+
+template <int DT, bool ALIGNED>
+__global__ void __launch_bounds__(kThreads) k_embedding_few(const __grid_constant__ FewArgs f) {
+    pdl_enter();
+    const SumArgs& a = f.sum;
+    const uint32_t lane = threadIdx.x & 31, tokens = static_cast<uint32_t>(a.tokens);
+    const uint64_t item = static_cast<uint64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+    const uint32_t t = static_cast<uint32_t>(item / a.segments);
+    if (t >= tokens) return;
+    const uint64_t c = (item - t * a.segments) * 256;
+    const int left = columns_left(a.dim, c);
+    const uint32_t id = id_at(f.ids, f.wide_ids, t, a.vocab);
+    uint32_t same = 0;   // lane k: which of the tokens 32 k to 32 k + 31 have this id
+#pragma unroll
+    for (uint32_t k = 0; k < kFewTokens / 32; ++k) {
+        const uint32_t i = 32 * k + lane;
+        const uint32_t word = __ballot_sync(0xFFFFFFFFu, i < tokens && id_at(f.ids, f.wide_ids, i, a.vocab) == id);
+        if (lane == k) same = word;
+    }
+    const uint32_t before = t >= 32 * lane + 32 ? 0xFFFFFFFFu : t > 32 * lane ? (1u << (t - 32 * lane)) - 1 : 0u;
+    if (id >= a.vocab || __any_sync(0xFFFFFFFFu, (same & before) != 0)) return;
+    float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+    for (uint32_t k = t / 32; 32 * k < tokens; ++k) {
+        uint32_t rest = __shfl_sync(0xFFFFFFFFu, same, k);
+#pragma unroll 1
+        while (rest) {   // four rows in flight
+            Loaded<ALIGNED> r[4];
+#pragma unroll
+            for (uint32_t i = 0; i < 4; ++i) {
+                const uint64_t at = 32 * k + (rest ? __ffs(rest) - 1 : 0);
+                load_eight(a.grad + at * a.ld_grad + c, rest ? left : 0, r[i]);
+                rest &= rest - 1;
+            }
+#pragma unroll
+            for (uint32_t i = 0; i < 4; ++i) {
+                float x[8];
+                widen_eight<DT>(r[i], x);
+                add8(s, x);
+            }
+        }
+    }
+    write_sum<DT, ALIGNED>(a, id, c, left, s);
+}
+
 // -------------------------------------------------------------------- host
 constexpr uint64_t kMaxTokens = 1ull << 31, kMaxVocab = 1ull << 31, kMaxDim = 1ull << 20, kMaxLd = 1ull << 40;
 
@@ -625,10 +696,8 @@ int zero_embedding_backward(int dtype, uint64_t vocab, uint64_t dim, const void*
         others = range ? up(2 * o.zero_cols, kZeroBytes) / kZeroBytes : up(vocab, 32) / 32;
         if (others > kZeroCtas) others = kZeroCtas;
     }
-    if ((e = launch_pdl(k_embedding_sort, dim3(static_cast<unsigned>(kSortCtas + up(others, kSortCtas))), kSortThreads, 0,
-                        kSortCtas, s, o)) != cudaSuccess)
-        return cuda_refuse(e, "zero_embedding_backward");
-    SumArgs a = {};
+    FewArgs f = {};
+    SumArgs& a = f.sum;
     a.grad = static_cast<const unsigned short*>(dout16);
     a.table = static_cast<unsigned short*>(dtable16);
     a.key = o.key[(o.passes - 1) & 1];
@@ -644,17 +713,31 @@ int zero_embedding_backward(int dtype, uint64_t vocab, uint64_t dim, const void*
     a.width = up(dim, 8);
     a.scale = scale;
     a.add = accumulate != 0;
-    const dim3 grid(static_cast<unsigned>(up(a.pieces * a.segments, kThreads / 32) / (kThreads / 32)));
     const bool fp16 = dtype == ZERO_FP16;
     const bool whole = dim % 8 == 0 && aligned(dout16, 16) && ld_dout % 8 == 0 && aligned(dtable16, 16) && ld_dtable % 8 == 0;
-    e = launch_pdl(whole ? (fp16 ? k_embedding_sum<kFp16, true> : k_embedding_sum<kBf16, true>)
-                         : (fp16 ? k_embedding_sum<kFp16, false> : k_embedding_sum<kBf16, false>),
-                   grid, kThreads, 0, 1, s, a);
-    const dim3 joins(static_cast<unsigned>(up(a.pieces, kJoinPieces) / kJoinPieces * a.segments));
-    if (e == cudaSuccess && a.pieces > 1)
+    constexpr unsigned kWarps = kThreads / 32;
+    // without sorting: 128 tokens of 768 columns into 50257 rows 13.7 us (19.2 sorted), 512 18.7 (19.9), 768 22.1 (20.4);
+    // with accumulate 3.3 (12.3), 6.9 (13.1), 9.8 (13.8)
+    if (tokens <= kFewTokens) {
+        f.ids = ids;
+        f.wide_ids = o.wide_ids;
+        e = accumulate ? cudaSuccess
+                       : launch_pdl(k_embedding_zeros, dim3(static_cast<unsigned>(others)), kSortThreads, 0, 1, s, o);
+        if (e == cudaSuccess)
+            e = launch_pdl(whole ? (fp16 ? k_embedding_few<kFp16, true> : k_embedding_few<kBf16, true>)
+                                 : (fp16 ? k_embedding_few<kFp16, false> : k_embedding_few<kBf16, false>),
+                           dim3(static_cast<unsigned>((tokens * segments + kWarps - 1) / kWarps)), kThreads, 0, 1, s, f);
+        return e == cudaSuccess ? ZERO_OK : cuda_refuse(e, "zero_embedding_backward");
+    }
+    e = launch_pdl(k_embedding_sort, dim3(static_cast<unsigned>(kSortCtas + up(others, kSortCtas))), kSortThreads, 0, kSortCtas, s, o);
+    if (e == cudaSuccess)
+        e = launch_pdl(whole ? (fp16 ? k_embedding_sum<kFp16, true> : k_embedding_sum<kBf16, true>)
+                             : (fp16 ? k_embedding_sum<kFp16, false> : k_embedding_sum<kBf16, false>),
+                       dim3(static_cast<unsigned>((a.pieces * segments + kWarps - 1) / kWarps)), kThreads, 0, 1, s, a);
+    if (e == cudaSuccess)
         e = launch_pdl(whole ? (fp16 ? k_embedding_join<kFp16, true> : k_embedding_join<kBf16, true>)
                              : (fp16 ? k_embedding_join<kFp16, false> : k_embedding_join<kBf16, false>),
-                       joins, kThreads, 0, 1, s, a);
+                       dim3(static_cast<unsigned>(up(a.pieces, kJoinPieces) / kJoinPieces * segments)), kThreads, 0, 1, s, a);
     return e == cudaSuccess ? ZERO_OK : cuda_refuse(e, "zero_embedding_backward");
 }
 

@@ -608,13 +608,17 @@ RowShape norm_shape(uint64_t rows, uint64_t groups, bool whole) {
     const int v = !whole ? (rows >= 1216 ? 2 : 1) : rows >= 1216 ? 4 : rows >= 304 ? 2 : 1;
     return row_shape(groups, v, v == 4 ? 512 : 1024);
 }
+// Backward: blocks enough that an SM has some 512 threads (a block of 160, of
+// which two an SM left it idle, took 96 us for 6057 x 2187), and few enough
+// that their shares of dw are little beside the rows.
 constexpr unsigned kGradBlocks = 304;   // two an SM
 RowShape grad_shape(uint64_t rows, uint64_t cols) {
     return row_shape((cols + 7) / 8, rows < kGradBlocks ? 1 : cols <= 1024 ? 4 : 2, 512);
 }
 uint64_t grad_blocks(uint64_t rows, const RowShape& r) {
-    const uint64_t b = (rows + r.rows - 1) / r.rows;
-    return b < kGradBlocks ? b : kGradBlocks;
+    const unsigned threads = r.rows * r.row_threads;
+    const uint64_t b = (rows + r.rows - 1) / r.rows, most = kGradBlocks / 2 * (threads <= 160 ? 4 : threads <= 192 ? 3 : 2);
+    return b < most ? b : most;
 }
 
 }  // namespace

@@ -166,8 +166,11 @@ __device__ __forceinline__ void dot8(const float (&a)[8], const float (&b)[8], f
 // ALIGNED, where every row starts on 16 bytes and is whole eights: lane l has
 // columns 8 l to 8 l + 7.  Else it has columns l, l + 32, ..., l + 224, so that
 // every access of the warp is 64 neighbouring bytes wherever the row starts,
-// nothing has to be shifted together, and nothing beside the row is touched:
-// @@ODD@@
+// nothing has to be shifted together, and nothing beside the row is touched.
+// (Aligned 16-byte pieces put together by shifts, the lanes at a warp's ends
+// writing theirs in parts, took 89 us for 4001 x 5003 bf16 through the norm's
+// backward pass against 69 so, 15.8 against 11.4 for 2047 x 1003 fp16 and 4.9
+// against 3.7 through dropout, 25 against 13 for looking up 8001 x 2001.)
 template <bool ALIGNED>
 __device__ __forceinline__ uint32_t column_of(int e) {
     const uint32_t lane = threadIdx.x & 31;
