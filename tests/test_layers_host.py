@@ -146,7 +146,8 @@ def test_tensors_in_host_memory_and_graphs_are_refused(Z):
     g, v = x.clone().requires_grad_(), w.clone().requires_grad_()
     for call in (lambda: L.dropout(g, Z.dropout_spec(0.1, 1)), lambda: L.rms_norm(g, w), lambda: L.rms_norm(x, v),
                  lambda: L.rms_norm(x, w, residual=g), lambda: L.rms_norm_backward(g, x, w), lambda: L.embedding(ids, g),
-                 lambda: L.embedding_backward(g, ids, x), lambda: mx8_linear(g, m)):
+                 lambda: L.embedding_backward(g, ids, x), lambda: mx8_linear(g, m), lambda: L.embedding(ids, x, out=g),
+                 lambda: L.dropout(x, Z.dropout_spec(0.1, 1), out=g)):
         refused(Z, "autograd", call)
         with torch.no_grad():
             refused(Z, "GPU", call)

@@ -32,7 +32,8 @@ struct MxArgs {
 // on 16 bytes takes a path without any of the edges' cases (`INSIDE`): for
 // 11008 x 4096 bf16 20 us to quantise (5.7 TB/s) and 23 us to read back (5.0
 // TB/s) against 28 and 28 with one path for all.  Rows at odd strides: 8.2
-// and 7.8 us for 2047 x 5003 against 7.4 and 5.9 for 2048 x 5000.
+// and 7.8 us for 2047 x 5003 against 7.4 and 5.9 for 2048 x 5000.  In 8 bits:
+// 8192 x 4096 18.3 us to quantise and 16 to read back.
 constexpr int kMxRows = 4;
 
 template <int BITS, int DT, bool INSIDE>
@@ -283,6 +284,8 @@ __global__ void __launch_bounds__(kThreads) k_mx_values(const __grid_constant__ 
 // products run.  192 columns begin in the middle of a scale tile of 128 rows
 // half of the time: two scale tiles cover them either way, and the product
 // starts two columns further on in tensor memory.
+// In 8 bits 8192 x 11008 x 4096 takes 260 us (2.8 PFLOP/s): the same fill a
+// stage, for half of its k.
 struct MxProductArgs {
     uint32_t m, n, k;
     uint32_t tiles_m, tiles_n, total;
@@ -532,7 +535,7 @@ k_mx_product(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
 
 // ------------------------------------------------- product with few rows
 // Up to 32 rows of A (a token, a handful): bound by reading B once, 5.7 us for
-// a row against 4096 x 11008 (4.2 TB/s) and 6.6 for 32 (above 32 rows the tiles
+// a row against 4096 x 11008 (4.2 TB/s; in 8 bits 9.5, 4.9 TB/s) and 6.6 for 32 (above 32 rows the tiles
 // of 128 are faster: 8.0 us for 33 rows, 9.8 for 256).  B's rows are the tensor cores' 128 rows and A's the columns (NT of
 // them), a CTA takes 128 of B's rows over a share of k, and the CTAs of a
 // cluster add up their shares through shared memory, in order of rank.  The

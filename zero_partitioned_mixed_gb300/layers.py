@@ -81,7 +81,7 @@ def _table(name: str, ids: torch.Tensor, table: torch.Tensor) -> torch.Tensor:
 
 def embedding(ids: torch.Tensor, table: torch.Tensor, scale: float = 1.0, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """scale * table[ids], [*ids.shape, dim]; an id outside the table is padding and gives zeros."""
-    _plain("embedding", table)
+    _plain("embedding", table, out)
     _table("table", ids, table)
     vocab, dim = table.shape
     if out is None:
@@ -118,7 +118,7 @@ def embedding_backward(dout: torch.Tensor, ids: torch.Tensor, dtable: torch.Tens
 def dropout(x: torch.Tensor, spec: B.Dropout, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """x with spec's dropout (dropout_spec); the same call on the output's gradient is the backward pass.
     out may be x."""
-    _plain("dropout", x)
+    _plain("dropout", x, out)
     out = torch.empty_like(x, memory_format=torch.contiguous_format) if out is None else out
     _like(x, ("out", out))
     a, o = _matrix(x), _matrix(out)
