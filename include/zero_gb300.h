@@ -708,7 +708,8 @@ ZERO_API int zero_dropout(int dtype, uint64_t rows, uint64_t cols, const void* s
  *               (one rounding, from fp32; zero_mx4_matmul and zero_mx8_matmul
  *               read them), or 0
  * Something must be written.  The statistics are those of h as it is stored,
- * in fp32; a row whose sum of squares overflows fp32 gives zeros.  h16 may be
+ * in fp32, of scaled values where their squares would leave it (with eps = 0 a
+ * row below 2^-127 gives infinities, one of zeros NaN).  h16 may be
  * x16 or residual16, and out16 x16 or residual16 (not both the same one),
  * where the leading dimensions agree; nothing may overlap otherwise.
  * cols <= ZERO_MAX_NORM_COLS, rows <= 2^30.

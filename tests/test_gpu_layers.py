@@ -276,9 +276,30 @@ def test_special_rows_stay_alone():
     assert torch.isnan(got.y[5]).all() and torch.isnan(got.q.values()[5]).all()
     assert torch.isnan(got.y[7, 0]) and not got.y[7, 1:].any()    # infinity times 0
     assert torch.isnan(got.q.values()[7, :32]).all() and not got.q.values()[7, 32:].any()
-    assert not got.y[9].any()                                     # the sum of squares overflows
+    big = norm64(x[9:10], w, 1e-5)[0]                             # the square leaves fp32, and the others are next to nothing
+    assert within(got.y[9:10], big, half_step(big, torch.bfloat16) + NORM * big.abs())
     zero = L.rms_norm(torch.zeros(3, 300, dtype=torch.bfloat16, device="cuda"), w.cuda(), 0.0, bits=8)
     assert torch.isnan(zero.y).all() and torch.isnan(zero.q.values()).all()   # 0 / 0
+
+
+OUTSIDE = [2.0 ** e for e in (0, 66, -70, 56, 100, -100, 120, -30, 60, -80)]
+
+
+@pytest.mark.parametrize("rows,cols", [(10, 1), (10, 8), (10, 300), (11, 1003), (10, 4096), (10, 16384), (310, 260), (1300, 520), (1300, 301)])
+def test_norm_of_rows_whose_squares_leave_fp32(rows, cols):
+    h, dy, w = matrix(rows, cols, "bf16", 1), matrix(rows, cols, "bf16", 2, 0.1), matrix(1, cols, "bf16", 3)[0]
+    h = (h.float() * torch.tensor(OUTSIDE).repeat(rows // 10 + 1)[:rows, None]).bfloat16()
+    for offset, gap in LAYOUTS[:1] + LAYOUTS[3:4]:
+        hs, ys = strided(h, offset, gap)[0], strided(dy, offset, gap)[0]
+        for eps in (0.0, 1e-5):
+            want, _ = norm64(h, w, eps)
+            got = L.rms_norm(hs, w.cuda(), eps, bits=8)
+            assert within(got.y, want, half_step(want, torch.bfloat16) + NORM * want.abs())
+            code = L.rms_norm(hs, w.cuda(), eps, bits=8, wide=False).q
+            assert torch.equal(code.codes, got.q.codes) and torch.equal(code.scales, got.q.scales)
+            tops = want.abs().amax(1)                   # the scale words follow the values
+            assert within(got.q.values().double().cpu().abs().amax(1), tops, tops / 8)
+            check_backward(L.rms_norm_backward(ys, hs, w.cuda(), eps), dy, h, w, eps, None, None, "bf16", rows)
 
 
 # ---------------------------------------------------------- norm, backward
