@@ -158,6 +158,7 @@ def test_shapes_are_refused(Z):
     x = torch.zeros(4, 6, 32).bfloat16()
     refused(Z, "rows", L._matrix, x.transpose(0, 1))
     refused(Z, "one dimension", L._matrix, x[0, 0, 0])
+    refused(Z, "contiguous", L._room, torch.zeros(1, dtype=torch.uint8).expand(4096), 4096, "cpu")
     assert L._matrix(x).shape == (24, 32) and L._matrix(x[0, 0]).shape == (1, 32) and L._matrix(x[:, :0]).shape == (0, 32)
     assert L._matrix(x[..., :0]).shape == (24, 0)
     refused(Z, "weight", L._vector, "weight", torch.zeros(8).bfloat16()[::2], 4, torch.bfloat16)

@@ -67,7 +67,11 @@ def _vector(name: str, v: torch.Tensor, cols: int, dtype) -> torch.Tensor:
 
 
 def _room(workspace: Optional[torch.Tensor], need: int, device) -> torch.Tensor:
-    return torch.empty(max(need, 1), dtype=torch.uint8, device=device) if workspace is None else workspace
+    if workspace is None:
+        return torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+    if not workspace.is_contiguous():
+        raise B.ZeroError(1, "workspace must be contiguous")
+    return workspace
 
 
 # --------------------------------------------------------------- embedding
