@@ -162,3 +162,33 @@ def test_shapes_are_refused(Z):
     assert L._matrix(x).shape == (24, 32) and L._matrix(x[0, 0]).shape == (1, 32) and L._matrix(x[:, :0]).shape == (0, 32)
     assert L._matrix(x[..., :0]).shape == (24, 0)
     refused(Z, "weight", L._vector, "weight", torch.zeros(8).bfloat16()[::2], 4, torch.bfloat16)
+
+
+def test_forward_mode_tangents_are_refused(Z):
+    """No call gives a result without the tangent that its input had; detached tensors pass on to the next check."""
+    from torch.autograd import forward_ad
+    from zero_partitioned_mixed_gb300 import layers as L
+    from zero_partitioned_mixed_gb300.mx4 import Mx4Matrix, mx4_linear, mx4_linear_backward, mx4_product
+    from zero_partitioned_mixed_gb300.mx8 import Mx8Matrix, mx8_linear, mx8_linear_backward, mx8_product
+    x, w, ids = torch.zeros(4, 32).bfloat16(), torch.zeros(32).bfloat16(), torch.zeros(4, dtype=torch.int64)
+    m8, m4, spec = Mx8Matrix(4, 32, device="cpu"), Mx4Matrix(4, 32, device="cpu"), Z.dropout_spec(0.1, 1)
+    with forward_ad.dual_level():
+        d, v = forward_ad.make_dual(x, torch.ones_like(x)), forward_ad.make_dual(w, torch.ones_like(w))
+        o = forward_ad.make_dual(torch.zeros(4, 4).bfloat16(), torch.zeros(4, 4).bfloat16())
+        calls = [lambda d, v, o: L.embedding(ids, d), lambda d, v, o: L.embedding(ids, x, out=d), lambda d, v, o: L.embedding_backward(d, ids, x),
+                 lambda d, v, o: L.embedding_backward(x, ids, d), lambda d, v, o: L.dropout(d, spec), lambda d, v, o: L.dropout(x, spec, out=d),
+                 lambda d, v, o: L.rms_norm(d, w), lambda d, v, o: L.rms_norm(x, v), lambda d, v, o: L.rms_norm(x, w, residual=d),
+                 lambda d, v, o: L.rms_norm_backward(d, x, w), lambda d, v, o: L.rms_norm_backward(x, d, w),
+                 lambda d, v, o: L.rms_norm_backward(x, x, v), lambda d, v, o: L.rms_norm_backward(x, x, w, dh_in=d),
+                 lambda d, v, o: L.rms_norm_backward(x, x, w, dweight=v),
+                 lambda d, v, o: Mx8Matrix.of(d), lambda d, v, o: m8.fill(d), lambda d, v, o: mx8_linear(d, m8), lambda d, v, o: mx8_linear(d, m8, scratch=m8),
+                 lambda d, v, o: mx8_linear(m8, m8, out=o), lambda d, v, o: mx8_product(m8, m8, out=o), lambda d, v, o: mx8_linear_backward(d, x, m8),
+                 lambda d, v, o: Mx4Matrix.of(d, True), lambda d, v, o: mx4_linear(d, m4), lambda d, v, o: mx4_product(m4, m4, out=o),
+                 lambda d, v, o: mx4_linear_backward(d, x, m4)]
+        for call in calls:
+            for mode in (torch.enable_grad, torch.no_grad):
+                with mode():
+                    refused(Z, "tangent", call, d, v, o)
+                    refused(Z, "GPU", call, d.detach(), v.detach(), o.detach())
+    for call in calls:
+        refused(Z, "GPU", call, x, w, torch.zeros(4, 4).bfloat16())

@@ -3,7 +3,7 @@
 Like mx4.py and mx8.py these record no autograd graph: each forward call has
 its backward call beside it, whose weight gradients go straight into a rank's
 16-bit gradient row (a view of it, as MuonBuffers.matrix gives).  Inputs whose
-gradient autograd is to find are refused.  Activations are [..., cols] with
+gradient autograd is to find are refused, and inputs with forward-mode tangents.  Activations are [..., cols] with
 contiguous rows.  Everything here runs on torch's current stream of the
 tensors' device, where the tensors it makes belong.
 """

@@ -13,6 +13,7 @@ import contextlib
 from typing import Optional, Tuple
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _binding as B
 
@@ -26,6 +27,10 @@ def _dtype(t: torch.Tensor) -> int:
 
 
 def _same_gpu(*tensors: torch.Tensor) -> None:
+    # A tangent of forward-mode differentiation lies beside a tensor, whatever requires_grad and the grad mode say; the calls
+    # see the values alone.  There are none outside a dual level, where asking for them (0.6 us a tensor) is left out.
+    if getattr(forward_ad, "_current_level", 0) >= 0 and any(forward_ad.unpack_dual(t).tangent is not None for t in tensors):
+        raise B.ZeroError(1, "a tensor has a forward-mode tangent, which would be lost: pass detached tensors")
     for t in tensors:
         if not t.is_cuda or t.device != tensors[0].device:
             raise B.ZeroError(1, f"expected tensors on one GPU, got {[str(x.device) for x in tensors]}")
@@ -112,7 +117,7 @@ def mx4_linear(x: torch.Tensor, w: Mx4Matrix, out: Optional[torch.Tensor] = None
     """y = x w^T: x [tokens, inner] in 16 bits is quantised, w [outer, inner] is kept in 4.
     scratch: a Mx4Matrix of x's size to reuse from call to call.
     The call records no autograd graph (mx4_linear_backward gives the gradients),
-    so an x whose gradient autograd is to find is refused."""
+    so an x whose gradient autograd is to find is refused, and one with a forward-mode tangent."""
     if x.requires_grad and torch.is_grad_enabled():
         raise B.ZeroError(1, "mx4_linear records no autograd graph: pass x.detach() (or call it under torch.no_grad()) "
                              "and take the gradients from mx4_linear_backward")

@@ -33,7 +33,7 @@ def mx8_linear(x: Union[torch.Tensor, Mx8Matrix], w: Mx8Matrix, out: Optional[to
     """y = x w^T: x [tokens, inner] in 16 bits is quantised (or comes in 8 bits from the norm before it, and y is then
     of `dtype`), w [outer, inner] is kept in 8.  scratch: a Mx8Matrix of x's size to reuse from call to call.
     The call records no autograd graph (mx8_linear_backward gives the gradients),
-    so an x whose gradient autograd is to find is refused."""
+    so an x whose gradient autograd is to find is refused, and one with a forward-mode tangent."""
     if isinstance(x, Mx8Matrix):
         return mx8_product(x, w, dtype, out)
     if x.requires_grad and torch.is_grad_enabled():
