@@ -120,6 +120,17 @@ def test_dropout_past_32_bits():
     assert torch.equal(got.cpu() != 0, kept(rows, cols, 0.5, 9, 0)[0])
 
 
+def test_dropout_of_more_values_than_an_odd_row_may_have():
+    # 2^34 values and more, without gaps, from 2 bytes behind a boundary: its rows are short
+    rows, cols = 2 ** 22 + 3, 4096
+    room = torch.ones(rows * cols + 1, dtype=torch.bfloat16, device="cuda")
+    x = room[1:].view(rows, cols)
+    L.dropout(x, Z.dropout_spec(0.5, 9), out=x)
+    for first in (0, 2 ** 21 - 1, rows - 2):
+        assert torch.equal(x[first:first + 2].cpu() != 0, kept(2, cols, 0.5, 9, 0, first_row=first)[0])
+    assert float(room[0]) == 1.0
+
+
 # --------------------------------------------------- rows at any alignment
 WIDTHS = list(range(1, 42)) + [63, 64, 65, 121, 127, 128, 129] + list(range(247, 266)) + [300, 503, 511, 512, 513, 520, 777, 1017, 1025]
 

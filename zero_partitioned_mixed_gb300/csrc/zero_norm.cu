@@ -564,6 +564,7 @@ __global__ void __launch_bounds__(1024) k_norm_dweight(const float* partial, uin
 
 // -------------------------------------------------------------------- host
 constexpr uint64_t kMaxRows = 1ull << 30, kMaxLd = 1ull << 40;
+constexpr uint64_t kMostOddRow = 1ull << 34;   // columns of dropout's rows that are not whole eights from 16 bytes on, without gaps
 
 struct Matrix {
     const char* name;
@@ -690,7 +691,8 @@ int zero_dropout(int dtype, uint64_t rows, uint64_t cols, const void* src16, uin
     if (rows == 0 || cols == 0) return ZERO_OK;
     const Matrix m[] = {{"src16", src16, ld_src, true}, {"out16", out16, ld_out, true}};
     if (const int rc = check_matrices(m, 2, cols, whole)) return rc;
-    if (cols % 8 == 0 && ld_src == cols && ld_out == cols && rows <= (1ull << 40) / cols) {   // one long row has the same groups
+    // one long row has the same groups; past kMostOddRow only where rows may be that long
+    if (cols % 8 == 0 && ld_src == cols && ld_out == cols && rows <= (whole ? 1ull << 40 : kMostOddRow) / cols) {
         cols *= rows;
         rows = 1;
         ld_src = ld_out = cols;
@@ -705,7 +707,7 @@ int zero_dropout(int dtype, uint64_t rows, uint64_t cols, const void* src16, uin
     if (a.across > (1ull << 40) / rows) return refuse(ZERO_EINVAL, "rows and cols are too large together");
     a.items = rows * a.segments;
     const bool one = whole && rows == 1, fp16 = dtype == ZERO_FP16;
-    if (!one && cols > (1ull << 34)) return refuse(ZERO_EINVAL, "rows of more than 2^34 values must be aligned and without gaps");
+    if (!one && cols > kMostOddRow) return refuse(ZERO_EINVAL, "rows of more than 2^34 values must be aligned and without gaps");
     const uint64_t per = one ? kDropVecs * kThreads : kThreads / 32;
     const uint64_t blocks = ((one ? a.across : a.items) + per - 1) / per;
     if (blocks > 0x7FFFFFFFull) return refuse(ZERO_EINVAL, "rows and cols are too large together");
