@@ -309,16 +309,22 @@ struct MxStage {
     static constexpr uint32_t kTiles = kK / 128;      // scale tiles along k
     static constexpr uint32_t kSteps = 4 / kTiles;    // products for each of them
 };
+// The operands' rows of 128 bytes are swizzled in groups of 8, and the
+// products' descriptors are those of operands that begin with a group: so does
+// every stage (in 8 bits with one accumulator its 41.5 KiB are followed by a gap).
+constexpr uint32_t kSwizzlePeriod = 1024;
+constexpr uint32_t swizzle_periods(uint32_t bytes) { return (bytes + kSwizzlePeriod - 1) / kSwizzlePeriod * kSwizzlePeriod; }
 template <int BITS, int MT>
 struct MxTile {
     static constexpr uint32_t kTiles = MxStage<BITS>::kTiles;
     static constexpr uint32_t kRows = 128 * MT, kA = kRows * 128, kB = kMxN * 128, kScaleA = 512 * kTiles * MT,
                               kScaleB = 1024 * kTiles;
-    static constexpr uint32_t kStage = kA + kB + kScaleA + kScaleB;
+    static constexpr uint32_t kFill = kA + kB + kScaleA + kScaleB, kStage = swizzle_periods(kFill);
     static constexpr int kStages = MT == 2 ? 3 : 4;   // at most the sets of scales: a set is free once its stage is
     static constexpr uint32_t kSet = kTiles * (4 * MT + 8);   // columns of a set: 4 for 128 rows and 128 values of k
     static constexpr size_t kSmem = 1024 + kStages * kStage + kMxOutWarps * 2 * kMxOut;
     static_assert(2 * kMxN + 4 * kSet <= 512, "tensor memory");
+    static_assert(kStage % kSwizzlePeriod == 0 && kA % kSwizzlePeriod == 0, "where A and B begin");
     static_assert(kSmem >= kLeastTmemSmem, "see tmem_alloc");
 };
 
@@ -420,7 +426,7 @@ k_mx_product(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                 }
                 const uint32_t bar = full + 8 * r.s, st = ring + r.s * T::kStage;
                 const uint32_t ss = st + T::kA + T::kB;
-                bar_expect(bar, T::kStage);
+                bar_expect(bar, T::kFill);
                 copy_box(st, &map_a, static_cast<int>(kb * 128), ra, 0, bar);
                 copy_box(st + T::kA, &map_b, static_cast<int>(kb * 128), rb, 0, bar);
                 copy_box(ss, &map_sa, 0, static_cast<int>(4 * kTiles * kb), ra >> 7, bar);
@@ -554,11 +560,13 @@ constexpr int kNarrowThreads = 192, kNarrowStages = 3;
 template <int BITS, int NT>
 struct Narrow {
     static constexpr uint32_t kTiles = MxStage<BITS>::kTiles;
-    static constexpr uint32_t kB = 128 * 128, kA = NT * 128, kScale = 512 * kTiles, kStage = kB + kA + 2 * kScale;
+    static constexpr uint32_t kB = 128 * 128, kA = NT * 128, kScale = 512 * kTiles, kFill = kB + kA + 2 * kScale;
+    static constexpr uint32_t kStage = swizzle_periods(kFill);
     static constexpr size_t kRing = 1024 + kNarrowStages * kStage;
     static constexpr size_t kSmem = kRing < kLeastTmemSmem ? kLeastTmemSmem : kRing;
     static constexpr uint32_t kTmem = 128;   // the accumulator and four sets of scales
     static_assert(NT + 4 * 16 <= kTmem, "tensor memory");
+    static_assert(kStage % kSwizzlePeriod == 0 && kB % kSwizzlePeriod == 0, "where B and A begin");
     static_assert(kSmem >= kLeastTmemSmem, "see tmem_alloc");
     static_assert(kNarrowStages * kStage >= NT * 512, "the partial sums take the ring's place");
 };
@@ -601,7 +609,7 @@ k_mx_narrow(const __grid_constant__ CUtensorMap map_b, const __grid_constant__ C
         for (; kb < k1; ++kb, r.next()) {
             if (!bar_wait(empty + 8 * r.s, r.parity ^ 1, quit, kForSpace)) break;
             const uint32_t bar = full + 8 * r.s, st = ring + r.s * L::kStage;
-            bar_expect(bar, L::kStage);
+            bar_expect(bar, L::kFill);
             copy_box(st, &map_b, static_cast<int>(kb * 128), static_cast<int>(tile * 128), 0, bar);
             copy_box(st + L::kB, &map_a, static_cast<int>(kb * 128), 0, 0, bar);
             copy_box(st + L::kB + L::kA, &map_sb, 0, static_cast<int>(4 * kTiles * kb), static_cast<int>(tile), bar);
