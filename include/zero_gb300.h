@@ -757,8 +757,11 @@ ZERO_API int zero_embedding(int dtype, uint64_t vocab, uint64_t dim, const void*
  * tokens t with ids[t] = v), every row of the table (0 where no token names
  * it); with accumulate != 0 what the rows held is added before the rounding
  * (rows that no token names keep their values), as a table that is also the
- * output layer's weight needs.  Sums are fp32, in the order of the tokens;
- * padding adds nothing.  Nothing may overlap.
+ * output layer's weight needs.  Sums are fp32, in an order that the ids and
+ * the sizes fix: up to 512 tokens, those of every eighth token, then these
+ * eight sums; beyond, within pieces of 8 places of a stable sort by id, then
+ * the pieces' sums (of more than 9 pieces every eighth one's, then these).
+ * Padding adds nothing.  Nothing may overlap.
  *   workspace   256-byte aligned, at least
  *               zero_embedding_backward_workspace_bytes(vocab, dim, tokens) bytes
  * tokens = 0 gives zeros.

@@ -532,56 +532,89 @@ __global__ void __launch_bounds__(kThreads) k_embedding_join(const __grid_consta
 }
 
 // ------------------------------------------------------------ few tokens
-// Up to kFewTokens tokens need no sorting: a warp takes 256 columns of one
-// token, looks at all ids, and leaves where its own occurs before; else it
-// adds up the rows with that id, in order.
+// Up to kFewTokens tokens need no sorting: a block takes 256 columns of one
+// token, looks at all ids, and leaves where the token's own occurs before.
+// Else it adds up the rows with that id: each warp those of every eighth
+// token, in order, then the warps' sums in order.  So a run of one id (a
+// batch whose padding is a row of the table) is read by eight warps, each
+// with as many rows in flight as its registers allow at full occupancy: with
+// accumulate 512 tokens of 768 columns take 4.7 us by Zipf's law and 11.3
+// with one id (sorted: 14.8 and 13.7; one warp a run: 9.4 and 71).  Six rows
+// against four and eight: 512 of one id 28.5 us (32.9, 25.6), 512 x 4096 by
+// Zipf's law with accumulate 14.3 (12.8, 16.1).
 struct FewArgs {
     SumArgs sum;
     const void* ids;
     int wide_ids;
 };
 constexpr uint32_t kFewTokens = 512;
-static_assert(kFewTokens <= 32 * 32, "a word a lane");
 
 template <int DT, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads) k_embedding_few(const __grid_constant__ FewArgs f) {
     pdl_enter();
+    constexpr uint32_t kWarps = kThreads / 32, kLooks = kFewTokens / kThreads, kAhead = ALIGNED ? 6 : 4;
+    static_assert(kFewTokens % kThreads == 0, "a thread looks at kLooks ids");
+    __shared__ uint32_t s_some[kWarps];
+    __shared__ float s_sum[kWarps][256];
     const SumArgs& a = f.sum;
-    const uint32_t lane = threadIdx.x & 31, tokens = static_cast<uint32_t>(a.tokens);
-    const uint64_t item = static_cast<uint64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-    const uint32_t t = static_cast<uint32_t>(item / a.segments);
-    if (t >= tokens) return;
-    const uint64_t c = (item - t * a.segments) * 256;
-    const int left = columns_left(a.dim, c);
-    const uint32_t id = id_at(f.ids, f.wide_ids, t, a.vocab);
-    uint32_t same = 0;   // lane k: which of the tokens 32 k to 32 k + 31 have this id
+    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tokens = static_cast<uint32_t>(a.tokens);
+    const uint32_t segments = static_cast<uint32_t>(a.segments), t = blockIdx.x / segments;
+    const uint32_t none = static_cast<uint32_t>(a.vocab), id = id_at(f.ids, f.wide_ids, t, a.vocab);
+    uint32_t same[kLooks];   // bit l: token kThreads k + kWarps l + warp has this id
+    bool before = false;
 #pragma unroll
-    for (uint32_t k = 0; k < kFewTokens / 32; ++k) {
-        const uint32_t i = 32 * k + lane;
-        const uint32_t word = __ballot_sync(0xFFFFFFFFu, i < tokens && id_at(f.ids, f.wide_ids, i, a.vocab) == id);
-        if (lane == k) same = word;
+    for (uint32_t k = 0; k < kLooks; ++k) {
+        const uint32_t i = kThreads * k + kWarps * lane + warp;
+        const bool is = i < tokens && id_at(f.ids, f.wide_ids, i, a.vocab) == id;
+        same[k] = __ballot_sync(0xFFFFFFFFu, is);
+        before = before || (is && i < t);
     }
-    const uint32_t before = t >= 32 * lane + 32 ? 0xFFFFFFFFu : t > 32 * lane ? (1u << (t - 32 * lane)) - 1 : 0u;
-    if (id >= a.vocab || __any_sync(0xFFFFFFFFu, (same & before) != 0)) return;
+    if (lane == 0) {
+        uint32_t some = 0;
+#pragma unroll
+        for (uint32_t k = 0; k < kLooks; ++k) some |= same[k];
+        s_some[warp] = some;
+    }
+    if (__syncthreads_or(before) || id == none) return;
+    const uint32_t warps = __ballot_sync(0xFFFFFFFFu, lane < kWarps && s_some[lane % kWarps] != 0);   // those that have rows
+    const bool alone = (warps & (warps - 1)) == 0;
+    if (alone && warps != 1u << warp) return;
+    const uint64_t c = static_cast<uint64_t>(blockIdx.x - t * segments) * 256;
+    const int left = columns_left(a.dim, c);
     float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 1
-    for (uint32_t k = t / 32; 32 * k < tokens; ++k) {
-        uint32_t rest = __shfl_sync(0xFFFFFFFFu, same, k);
-#pragma unroll 1
-        while (rest) {   // four rows in flight
-            Loaded<ALIGNED> r[4];
+    for (uint32_t k = 0; k < kLooks; ++k) {
+        uint32_t rest = same[0];
 #pragma unroll
-            for (uint32_t i = 0; i < 4; ++i) {
-                const uint64_t at = 32 * k + (rest ? __ffs(rest) - 1 : 0);
+        for (uint32_t q = 1; q < kLooks; ++q) rest = k == q ? same[q] : rest;
+#pragma unroll 1
+        while (rest) {   // kAhead rows in flight
+            Loaded<ALIGNED> r[kAhead];
+#pragma unroll
+            for (uint32_t i = 0; i < kAhead; ++i) {
+                const uint64_t at = kThreads * k + kWarps * (rest ? __ffs(rest) - 1 : 0) + warp;
                 load_eight(a.grad + at * a.ld_grad + c, rest ? left : 0, r[i]);
                 rest &= rest - 1;
             }
 #pragma unroll
-            for (uint32_t i = 0; i < 4; ++i) {
+            for (uint32_t i = 0; i < kAhead; ++i) {
                 float x[8];
                 widen_eight<DT>(r[i], x);
                 add8(s, x);
             }
+        }
+    }
+    if (!alone) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s_sum[warp][32 * e + lane] = s[e];
+        __syncthreads();
+        if (warp + 1 != __ffs(warps)) return;
+#pragma unroll 1
+        for (uint32_t rest = warps & (warps - 1); rest; rest &= rest - 1) {
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = s_sum[__ffs(rest) - 1][32 * e + lane];
+            add8(s, x);
         }
     }
     write_sum<DT, ALIGNED>(a, id, c, left, s);
@@ -718,8 +751,8 @@ int zero_embedding_backward(int dtype, uint64_t vocab, uint64_t dim, const void*
     const bool fp16 = dtype == ZERO_FP16;
     const bool whole = dim % 8 == 0 && aligned(dout16, 16) && ld_dout % 8 == 0 && aligned(dtable16, 16) && ld_dtable % 8 == 0;
     constexpr unsigned kWarps = kThreads / 32;
-    // without sorting: 128 tokens of 768 columns into 50257 rows 13.7 us (19.2 sorted), 512 18.7 (19.9), 768 22.1 (20.4);
-    // with accumulate 3.3 (12.3), 6.9 (13.1), 9.8 (13.8)
+    // without sorting (by Zipf's law, sorted in brackets): 128 tokens of 768 columns into 50257 rows 15.0 us (19.9), 512 16.7
+    // (20.7), of 4096 into 32000 53.8 (51.4); one id for all of them 17.8 (20.2), 28.5 (22.2), 57.1 (52.9)
     if (tokens <= kFewTokens) {
         f.ids = ids;
         f.wide_ids = o.wide_ids;
@@ -728,7 +761,7 @@ int zero_embedding_backward(int dtype, uint64_t vocab, uint64_t dim, const void*
         if (e == cudaSuccess)
             e = launch_pdl(whole ? (fp16 ? k_embedding_few<kFp16, true> : k_embedding_few<kBf16, true>)
                                  : (fp16 ? k_embedding_few<kFp16, false> : k_embedding_few<kBf16, false>),
-                           dim3(static_cast<unsigned>((tokens * segments + kWarps - 1) / kWarps)), kThreads, 0, 1, s, f);
+                           dim3(static_cast<unsigned>(tokens * segments)), kThreads, 0, 1, s, f);
         return e == cudaSuccess ? ZERO_OK : cuda_refuse(e, "zero_embedding_backward");
     }
     e = launch_pdl(k_embedding_sort, dim3(static_cast<unsigned>(kSortCtas + up(others, kSortCtas))), kSortThreads, 0, kSortCtas, s, o);
