@@ -1,7 +1,9 @@
 """The residual stream's operators on the paths that small calls do not take.
 
-Runs of one id in embedding gradients of up to 512 tokens, which are not
-sorted: rows of one warp, of several, of all.
+Embedding gradients of more than 512 tokens (sorted) over every digit count of
+the sort, rows at every alignment, tables past 32 bits, captured; runs of one
+id that begin and end at every place of their pieces of 8 tokens; and of up to
+512 tokens, which are not sorted: rows of one warp, of several, of all.
 
 Sums of whole numbers below 2048 are exact in fp16 and in any order.  The
 tolerances elsewhere are those of test_gpu_layers.py."""
@@ -11,6 +13,7 @@ import pytest
 import torch
 
 from _layer_ref import half_step, within
+import zero_partitioned_mixed_gb300 as Z
 from zero_partitioned_mixed_gb300 import layers as L
 
 pytestmark = pytest.mark.gpu
@@ -46,6 +49,110 @@ def sums(ids, dy, vocab):
     """The rows' sums in 64 bits, on the GPU."""
     at = torch.where((ids >= 0) & (ids < vocab), ids, vocab)
     return torch.zeros((vocab + 1, dy.shape[1]), dtype=torch.float64, device="cuda").index_add_(0, at, dy.double())[:-1]
+
+
+# -------------------------------------------------- embedding, many tokens
+@pytest.mark.parametrize("tokens", [600, 5000, 20011])
+@pytest.mark.parametrize("vocab", [2 ** 16 - 1, 2 ** 16, 2 ** 24 - 1, 2 ** 24, 2 ** 24 + 5, 2 ** 31 - 1, 2 ** 31])
+def test_sorted_ids_of_every_digit_count(vocab, tokens):
+    ids = torch.randint(0, vocab, (tokens,), generator=gen(tokens))
+    ids[:40] = vocab - 1 - torch.arange(40) % 7
+    ids[40:80] = torch.arange(40) % 5
+    ids[80:130] = torch.tensor([-1, vocab, 2 ** 40, -2 ** 50, 2 ** 32]).repeat(10)       # padding
+    ids[130:200] = (1 << torch.arange(70) % 31) % vocab                                  # one bit each
+    ids = ids[torch.randperm(tokens, generator=gen(1))].cuda()
+    dy = whole((tokens, 1), tokens).cuda()
+    out = torch.full((vocab, 1), 7.0, dtype=torch.float16, device="cuda")
+    L.embedding_backward(dy, ids, out)
+    inside = (ids >= 0) & (ids < vocab)
+    rows, back = torch.unique(ids[inside], return_inverse=True)
+    want = torch.zeros(len(rows), dtype=torch.float64, device="cuda").index_add_(0, back, dy[inside, 0].double())
+    assert torch.equal(out[rows, 0].double(), want)
+    out[rows] = 0.0
+    assert not any(bool(part.any()) for part in out.split(1 << 28))
+
+
+def test_sorted_gradient_of_a_table_past_32_bits():
+    vocab, dim, tokens = 1_100_003, 4000, 700           # 4.4e9 elements
+    ids = (vocab - 1 - torch.randint(0, 90, (tokens,), generator=gen(1))).cuda()
+    ids[::7] = 3
+    dy = whole((tokens, dim), 2).cuda()
+    out = torch.full((vocab, dim), 7.0, dtype=torch.float16, device="cuda")
+    for accumulate in (False, True):
+        L.embedding_backward(dy, ids, out, accumulate=accumulate)
+        rows = torch.unique(ids)
+        at = torch.searchsorted(rows, ids)
+        want = sums(at, dy, len(rows)) * (1 + accumulate)
+        assert torch.equal(out[rows].double(), want)
+    out[rows] = 0.0
+    assert not any(bool(part.any()) for part in out.split(100_000))
+
+
+WIDTHS = list(range(1, 42)) + [63, 64, 65, 121, 127, 128, 129] + list(range(247, 266)) + [300, 503, 511, 512, 513, 520, 777, 1017, 1025]
+
+
+@pytest.mark.parametrize("offset", range(8))
+def test_sorted_gradient_of_rows_of_every_alignment_and_width(offset):
+    vocab, tokens = 97, SORTED + 88
+    for cols in WIDTHS:
+        gap = (cols * 5 + offset) % 8
+        ids = torch.randint(-2, vocab + 2, (tokens,), generator=gen(cols)).cuda()
+        ids[offset * 20:offset * 20 + 150] = 31         # a run that the join adds up by a block
+        dy, _ = strided(whole((tokens, cols), cols).cuda(), offset, gap)
+        held = whole((vocab, cols), cols + 1).cuda()
+        want = sums(ids, dy, vocab)
+        for accumulate in (False, True):
+            out, room = strided(held, (3 * offset + 1) % 8, gap)
+            L.embedding_backward(dy, ids, out, accumulate=accumulate)
+            assert torch.equal(out.double(), want + held.double() if accumulate else want), cols
+            assert untouched(out, room), cols
+
+
+@pytest.mark.parametrize("pieces", [1, 2, 8, 9, 10, 31, 32, 33, 34, 65, 97])
+@pytest.mark.parametrize("dim", [40, 41])
+def test_runs_at_every_place_of_their_pieces(dim, pieces):
+    """A run that covers so many pieces of 8 sorted tokens, from each place of its first to three of its last; other runs
+    before and behind it, and padding up to the sorted form."""
+    for begin in range(8):
+        for end in (1, 5, 8):
+            length = 8 * pieces - begin - (8 - end)
+            if length < 1:
+                continue
+            for behind in (0, 3):
+                ids = torch.cat((torch.arange(begin), torch.full((length,), 20), 21 + torch.arange(behind)))
+                ids = torch.cat((ids, torch.full((max(0, SORTED - len(ids)),), -1)))
+                perm = torch.randperm(len(ids), generator=gen(pieces))
+                ids = ids[perm].cuda()
+                dy = whole((len(ids), dim), length).cuda()
+                out = torch.full((30, dim), 9.0, dtype=torch.float16, device="cuda")
+                L.embedding_backward(dy, ids, out)
+                assert torch.equal(out.double(), sums(ids, dy, 30)), (begin, end, behind)
+
+
+def test_captured_sorted_gradients():
+    """Two graphs that share a workspace and run in order; the replays sort the ids that are there then."""
+    vocab, dim, tokens = 3000, 264, 4100
+    ids, dy = torch.zeros(tokens, dtype=torch.int64, device="cuda"), torch.zeros((tokens, dim), dtype=torch.float16, device="cuda")
+    room = torch.empty(Z.zero_embedding_backward_workspace_bytes(vocab, dim, tokens), dtype=torch.uint8, device="cuda")
+    outs = [torch.empty((vocab, dim), dtype=torch.float16, device="cuda") for _ in range(2)]
+    L.embedding_backward(dy, ids, outs[0], workspace=room)
+    torch.cuda.synchronize()
+    graphs = [torch.cuda.CUDAGraph() for _ in outs]
+    for graph, out, scale in zip(graphs, outs, (1.0, 2.0)):
+        with torch.cuda.graph(graph):
+            L.embedding_backward(dy, ids, out, scale, workspace=room)
+            L.embedding_backward(dy, ids, out, scale, True, room)
+    for k in range(4):
+        new = torch.randint(-5, vocab + 5, (tokens,), generator=gen(k))
+        new[k * 100:k * 100 + 90 * k] = 77 + k
+        ids.copy_(new)
+        dy.copy_(whole((tokens, dim), k, 1))
+        for _ in range(3):
+            for graph in graphs:
+                graph.replay()
+        torch.cuda.synchronize()
+        want = sums(ids, dy, vocab)
+        assert torch.equal(outs[0].double(), 2 * want) and torch.equal(outs[1].double(), 4 * want)
 
 
 # --------------------------------------------------- embedding, few tokens
