@@ -3,23 +3,27 @@
 Embedding gradients of more than 512 tokens (sorted) over every digit count of
 the sort, rows at every alignment, tables past 32 bits, captured; runs of one
 id that begin and end at every place of their pieces of 8 tokens; and of up to
-512 tokens, which are not sorted: rows of one warp, of several, of all.
+512 tokens, which are not sorted: rows of one warp, of several, of all.  The
+norm's backward pass with several rows for each row of threads, so that its
+ring of copies, its sums and its share of the weight's gradient go round.
 
 Sums of whole numbers below 2048 are exact in fp16 and in any order.  The
-tolerances elsewhere are those of test_gpu_layers.py."""
+tolerances elsewhere are those of test_gpu_layers.py, the one of the weight's
+gradient with the blocks that there are: the workspace has a row of fp32 for
+each."""
 
 import numpy as np
 import pytest
 import torch
 
-from _layer_ref import half_step, within
+from _layer_ref import half_step, kept, norm_grad64, within
 import zero_partitioned_mixed_gb300 as Z
 from zero_partitioned_mixed_gb300 import layers as L
 
 pytestmark = pytest.mark.gpu
 TD = {"fp16": torch.float16, "bf16": torch.bfloat16}
 DTYPES = ["bf16", "fp16"]
-U = 2.0 ** -24
+U, GRAD = 2.0 ** -24, 2.0 ** -16
 SORTED = 513     # tokens from which the gradient sorts them
 
 
@@ -153,6 +157,63 @@ def test_captured_sorted_gradients():
         torch.cuda.synchronize()
         want = sums(ids, dy, vocab)
         assert torch.equal(outs[0].double(), 2 * want) and torch.equal(outs[1].double(), 4 * want)
+
+
+# ------------------------------------------------------ norm, backward pass
+def mask(rows, cols, p, seed, stream):
+    """_layer_ref.kept for many rows: the generator in numpy's 64-bit whole numbers."""
+    low, groups = np.uint64(0xFFFFFFFF), (cols + 7) // 8
+    n = np.arange(rows * groups, dtype=np.uint64)
+    c = [n & low, n >> np.uint64(32), np.full_like(n, stream & 0xFFFFFFFF), np.full_like(n, stream >> 32)]
+    k = [seed & 0xFFFFFFFF, seed >> 32]
+    for _ in range(10):
+        a, b = np.uint64(0xD2511F53) * c[0], np.uint64(0xCD9E8D57) * c[2]
+        c = [(b >> np.uint64(32)) ^ c[1] ^ np.uint64(k[0]), b & low, (a >> np.uint64(32)) ^ c[3] ^ np.uint64(k[1]), a & low]
+        k = [k[0] + 0x9E3779B9 & 0xFFFFFFFF, k[1] + 0xBB67AE85 & 0xFFFFFFFF]
+    halves = np.stack([w >> np.uint64(16 * h) & np.uint64(0xFFFF) for w in c for h in (0, 1)], 1).reshape(rows, groups * 8)
+    drop = round(p * 65536)
+    return torch.from_numpy(halves[:, :cols] >= drop), float(np.float32(65536 / (65536 - drop)))
+
+
+#: Rows, columns, and how many rows a block has at a time: every row of threads takes three to five rows.
+LOOPS = [(8000, 96, 8), (8000, 99, 8), (7400, 776, 8), (7400, 777, 8), (4000, 520, 2), (4000, 523, 2), (2000, 2184, 1),
+         (2000, 2187, 1), (1000, 4096, 1), (1000, 5003, 1), (1000, 9000, 1), (1000, 9001, 1), (950, 16384, 1), (950, 16001, 1)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,cols,slots", LOOPS)
+def test_norm_backward_of_several_rows_a_thread(rows, cols, slots, dtype):
+    g = gen(rows + cols)
+    h = torch.randn((rows, cols), generator=g) * torch.exp(0.5 * torch.randn((rows, 1), generator=g))
+    if dtype == "bf16":   # some rows' squares leave fp32, on either side
+        h *= torch.tensor([1.0, 1.0, 2.0 ** 70, 1.0, 2.0 ** -70, 1.0, 2.0 ** 100]).repeat(rows // 7 + 1)[:rows, None]
+    h, w = h.to(TD[dtype]), torch.randn(cols, generator=g).to(TD[dtype])
+    dy, d = ((0.1 * torch.randn((rows, cols), generator=g)).to(TD[dtype]) for _ in range(2))
+    blocks = Z.zero_rms_norm_backward_workspace_bytes(rows, cols) // (4 * 8 * ((cols + 7) // 8))
+    assert rows > 3 * blocks * slots
+    keep, factor = mask(rows, cols, 0.1, 3, 4)
+    small = kept(3, cols, 0.1, 3, 4)
+    assert torch.equal(keep[:3], small[0]) and factor == small[1]
+    dh, dw, size, dw_size = norm_grad64(dy, h, w, 1e-5, d)
+    dx = torch.where(keep, dh * factor, torch.zeros((), dtype=torch.float64))
+    # additions to dw: a thread's rows, a block's rows of threads, a warp's shares, 32 warps; and r's roundings
+    adds = -(-rows // (blocks * slots)) + slots + -(-blocks // 32) + 32 + 36
+    spec = Z.dropout_spec(0.1, 3, 4)
+    for offset, gap in ((0, 0), (3, 5)):
+        hs, ys, ds = (strided(t.cuda(), offset, gap)[0] for t in (h, dy, d))
+        got = L.rms_norm_backward(ys, hs, w.cuda(), 1e-5, ds, spec)
+        assert within(got[0], dh, half_step(dh, TD[dtype]) + GRAD * size)
+        assert within(got[1], dx, half_step(dx, TD[dtype]) + factor * (GRAD + U) * size)
+        assert within(got[2], dw, half_step(dw, TD[dtype]) + adds * U * dw_size)
+        for _ in range(3):
+            again = L.rms_norm_backward(ys, hs, w.cuda(), 1e-5, ds, spec)
+            assert all(torch.equal(a, b) for a, b in zip(got, again))
+        # in place: the stream's gradient where the incoming one was, the branch's where the output's was
+        ld, room = cols + gap, torch.empty(Z.zero_rms_norm_backward_workspace_bytes(rows, cols), dtype=torch.uint8, device="cuda")
+        dweight = torch.empty_like(w, device="cuda")
+        Z.zero_rms_norm_backward({"fp16": 0, "bf16": 1}[dtype], rows, cols, ys, hs, w.cuda(), 1e-5, ds, room, ds, ys, dweight, spec,
+                                 ld, ld, ld, ld, ld)
+        assert torch.equal(ds, got[0]) and torch.equal(ys, got[1]) and torch.equal(dweight, got[2])
 
 
 # --------------------------------------------------- embedding, few tokens
