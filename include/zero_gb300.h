@@ -660,7 +660,9 @@ ZERO_API int zero_debug_hold_matrix(int64_t stage);
  * layers.  Like the matrix calls these take no handle, allocate nothing and
  * can be captured into a CUDA graph (after one call of each outside a
  * capture).  Matrices are row-major with `ld` elements between rows, 2-byte
- * aligned (faster when rows start on 16 bytes); rows may not share memory.
+ * aligned; rows may not share memory.  Calls are faster, up to twice, when the
+ * rows of all their matrices start on 16 bytes and are whole eights, and
+ * weight16 starts on 16 bytes too.
  * Results are rounded once to 16 bits and repeat bit for bit.  An empty
  * matrix is an empty call.  A workspace's contents need not be kept between
  * calls; calls that share one (replays of captured ones too) must run in

@@ -11,8 +11,11 @@
 //          of up to 8 bits; its CTAs see each other's counts through their
 //          shared memory, hand each other up to 16384 keys the same way, and
 //          wait for each other at the cluster's barrier only).  The launch's
-//          other CTAs fill the table with zeros meanwhile, which takes as
-//          long or longer for tables of real sizes.
+//          other CTAs fill the table with zeros meanwhile, which takes about
+//          as long for some 8000 tokens and a table of a real size (both
+//          together 14.6 us of which the 77 MB of zeros are 12 to 13).
+//          Past 16384 tokens the keys go through global memory, and the sort
+//          is what takes long.
 //   sum    a warp takes 256 columns of kPiece consecutive sorted tokens, in
 //          fp32.  A run of one id that lies inside its piece is finished and
 //          written; one that crosses into other pieces leaves partial sums.
@@ -20,10 +23,12 @@
 //          order, or its block where there are many.
 //
 // Up to 512 tokens are not sorted: each looks at all ids (k_embedding_few).
-// 8192 x 768 bf16 into 50257 rows takes 26.5 us, 6007 x 1003 fp16 into 32003
-// 27.2: writing the table at the 6 TB/s that stores alone reach is 12 to 13 of
-// them, the sort hides behind it, and sum and join are chains of dependent
-// reads, 12 us together, that nothing is left to hide.  (Partial sums added by
+// 8192 x 768 bf16 into 50257 rows takes 26.6 us, 6007 x 1003 fp16 into 32003
+// 27.3: writing the table at the 6 TB/s that stores alone reach is 12 to 13 of
+// them, all of the sort but some 2 hides behind it, and sum and join are
+// chains of dependent reads, 12 us together, that nothing is left to hide.
+// 65536 x 768 takes 88 to 91, 16384 x 4096 into 32000 92; with accumulate
+// 8192 x 768 24, 65536 x 768 96.  (Partial sums added by
 // the last warp of their run to come, with counters and fences in place of the
 // join's launch: 27.4 and 32.2 us.)
 //

@@ -105,7 +105,8 @@ __global__ void __launch_bounds__(kThreads) k_mx_rows(const __grid_constant__ Mx
 // 128 rows (a scale tile's four blocks) of 128 columns, a thread 32 values
 // of two neighbouring columns; the codes go through shared memory so that a
 // row of them leaves as 64 neighbouring bytes.  11008 x 4096: 18.6 us (6.1
-// TB/s; one column a thread and codes straight from registers took 33).
+// TB/s; one column a thread and codes straight from registers took 33).  In 8
+// bits 8192 x 4096 takes 16.9 us (6.0 TB/s), 8192 x 11008 41.
 template <int BITS, int DT>
 __global__ void __launch_bounds__(kThreads) k_mx_columns(const __grid_constant__ MxArgs a) {
     pdl_enter();
@@ -284,8 +285,8 @@ __global__ void __launch_bounds__(kThreads) k_mx_values(const __grid_constant__ 
 // products run.  192 columns begin in the middle of a scale tile of 128 rows
 // half of the time: two scale tiles cover them either way, and the product
 // starts two columns further on in tensor memory.
-// In 8 bits 8192 x 11008 x 4096 takes 260 us (2.8 PFLOP/s): the same fill a
-// stage, for half of its k.
+// In 8 bits 8192 x 11008 x 4096 takes 257 to 270 us (2.7 to 2.9 PFLOP/s): the
+// same fill a stage, for half of its k.
 struct MxProductArgs {
     uint32_t m, n, k;
     uint32_t tiles_m, tiles_n, total;
@@ -862,7 +863,10 @@ int mx_matmul(const char* name, int dtype, uint64_t m, uint64_t n, uint64_t k, c
     }
     int sms = 0;
     if ((e = sm_count(&sms)) != cudaSuccess) return cuda_refuse(e, name);
-    // 256 rows a tile are cheaper a row (1224 cycles a stage against 863 for 128) unless they leave SMs idle
+    // 256 rows a tile are cheaper a row (1224 cycles a stage against 863 for 128) unless they leave SMs idle.  The same rule in
+    // 8 bits, with 256 and 128 rows a tile: 256 x 11008 x 4096 23.4 and 17.2 us, 1000 x 4096 x 11008 50.9 and 59.5, 8192 x
+    // 11008 x 4096 257 and 277; where the two are near it takes the slower one at times (700 x 11008 x 4096 41.9 and 36.5,
+    // 2048 x 4096 x 4096 41.1 and 34.5).  With few tiles most SMs have nothing: 33 to 256 x 4096 x 11008 take 32 to 33 us.
     const uint64_t across = up(n, kMxN) / kMxN;
     auto rounds = [&](uint64_t rows) { return (up(m, rows) / rows * across + sms - 1) / sms; };
     const bool tall = rounds(256) * 1224 <= rounds(128) * 863;

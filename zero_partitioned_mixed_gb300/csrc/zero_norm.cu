@@ -232,7 +232,10 @@ __device__ __forceinline__ void write_codes(const NormArgs& a, uint64_t row, uin
 
 // V times 256 columns a warp, one after the other.  BITS: of the codes, or 0.
 // 8192 x 4096 bf16 with residual and dropout into 16 and 8 bits: 50 us for 303
-// MB (6.1 TB/s, issue slots 70 % taken).
+// MB (6.1 TB/s, issue slots 70 % taken); into 16 and 4 bits 50, into 16 alone
+// 41, into 8 or 4 alone 46; 87 and (16 alone) 59 where one of the matrices or
+// the weight does not start on 16 bytes, for then every value is an access of
+// its own.
 template <int BITS, int DT, int V, bool ALIGNED>
 __global__ void __launch_bounds__(V == 4 ? 512 : 1024, V == 4 ? 2 : 1) k_rms_norm(const __grid_constant__ NormArgs a) {
     pdl_enter();
@@ -346,10 +349,11 @@ __device__ __forceinline__ uint32_t behind(const unsigned short* row) {
 
 // A block takes its rows blockIdx.x, + gridDim.x, ..., and keeps its share of
 // dw in registers over all of them.  The next row is on its way to shared
-// memory while this one is worked on: 62 us for 8192 x 4096 bf16 with dropout
-// (5.4 TB/s) against 70 with the next row in registers and 94 without.  Rows
+// memory while this one is worked on: 63 us for 8192 x 4096 bf16 with dropout
+// (5.3 TB/s) against 70 with the next row in registers and 94 without.  Rows
 // that start between two 16-byte boundaries are copied as the aligned pieces
-// that cover them, and read from there as column_of says.
+// that cover them, and read from there as column_of says, two bytes at a time:
+// 110 us for the same size where only the weight lies at an odd address.
 template <int DT, int V, bool ALIGNED>
 __global__ void __maxnreg__(V == 4 || ALIGNED ? 128 : 96) k_rms_norm_backward(const __grid_constant__ NormGradArgs a) {
     pdl_enter();
@@ -655,14 +659,22 @@ RowShape row_shape(uint64_t groups, int most_v, unsigned most) {
 // eights a thread, 608 x 4096 9.6, 8.2 and 9.5, 8192 x 4096 76, 68 and 61 (all
 // with the codes read back again).  Rows at odd strides hold a register a value
 // and stop at 2: 4001 x 5003 84 us, 87 at 1 and 92 at 4, when that was chosen,
-// and 76 now.
+// and 76 now.  Without the reading back, at 1, 2 and 4: 400 x 768 2.6, 3.1 and
+// 3.9, 608 x 2048 3.7, 4.1 and 5.2, 1300 x 768 4.5, 4.9 and 4.7, 1300 x 2048
+// 7.6, 6.4 and 8.1, 8192 x 768 17.7, 15.0 and 13.3, 8192 x 2048 39.6, 29.7 and
+// 26.7: beside a limit the rule is up to a quarter off.
 RowShape norm_shape(uint64_t rows, uint64_t groups, bool whole) {
     const int v = !whole ? (rows >= 1216 ? 2 : 1) : rows >= 1216 ? 4 : rows >= 304 ? 2 : 1;
     return row_shape(groups, v, v == 4 ? 512 : 1024);
 }
 // Backward: blocks enough that an SM has some 512 threads (a block of 160, of
 // which two an SM left it idle, took 96 us for 6057 x 2187), and few enough
-// that their shares of dw are little beside the rows.
+// that their shares of dw are little beside the rows.  At 1, 2 and 4 eights a
+// thread: 8192 x 768 20.9, 20.4 and 17.3 us, 8192 x 1024 25.6, 21.1 and 18.8,
+// 8001 x 1003 50, 35 and 30, 8192 x 2048 44, 36.3 and 36.8, 8192 x 4096 97,
+// 63.6 and 65.6, 6057 x 2187 66, 54 and 83.  Between them the rule is not the
+// best everywhere: 8192 x 1536 takes 39 with 2 and 31 with 4, 8192 x 3000 71
+// and 60, 8192 x 8192 138 and 114.
 constexpr unsigned kGradBlocks = 304;   // two an SM
 RowShape grad_shape(uint64_t rows, uint64_t cols) {
     return row_shape((cols + 7) / 8, rows < kGradBlocks ? 1 : cols <= 1024 ? 4 : 2, 512);

@@ -1,8 +1,11 @@
 """What lies between a layer's linear products: embedding, dropout, and the norm with the residual's addition.
 
 Like mx4.py and mx8.py these record no autograd graph: each forward call has
-its backward call beside it, whose weight gradients go straight into a rank's
-16-bit gradient row (a view of it, as MuonBuffers.matrix gives).  Inputs whose
+its backward call beside it.  The table's and the norm's weight gradients go
+straight into a rank's 16-bit gradient row (a view of it, as MuonBuffers.matrix
+gives), the table's also on top of what is there; the linear layers' calls
+return theirs, to be copied.  A norm's weight that does not start on 16 bytes
+costs its calls up to twice the time.  Inputs whose
 gradient autograd is to find are refused, and inputs with forward-mode tangents.  Activations are [..., cols] with
 contiguous rows.  Everything here runs on torch's current stream of the
 tensors' device, where the tensors it makes belong.

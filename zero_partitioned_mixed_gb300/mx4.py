@@ -128,7 +128,8 @@ def mx4_linear(x: torch.Tensor, w: Mx4Matrix, out: Optional[torch.Tensor] = None
 def mx4_linear_backward(dy: torch.Tensor, x: torch.Tensor, w_t: Mx4Matrix) -> Tuple[torch.Tensor, torch.Tensor]:
     """(dx, dw) of y = x w^T, with the rounding of the operands passed through:
     dx = dy w and dw = dy^T x, each from operands quantised along the summed
-    dimension.  w_t: w quantised along its columns (Mx4Matrix.of(w, transpose=True))."""
+    dimension.  w_t: w quantised along its columns (Mx4Matrix.of(w, transpose=True)).
+    Both are new matrices, constants to autograd whatever dy and x require."""
     dx = mx4_product(Mx4Matrix.of(dy), w_t, dy.dtype)
     dw = mx4_product(Mx4Matrix.of(dy, True), Mx4Matrix.of(x, True), dy.dtype)
     return dx, dw
